@@ -254,8 +254,7 @@ def _own(s):
     if op == "embed_grad":
         return handle.grad(s["tokens"], s["dout"], s["dtable"], accumulate=s["add"])
     if op == "clip":
-        norm = handle.norm(s["grads"])
-        return norm, handle.clip(s["grads"], s["max_norm"])
+        return handle.norm_and_clip(s["grads"], s["max_norm"])
     s["t"] += 1
     handle.step(s["grads"], LR, BETA1, BETA2, EPS, s["t"], max_norm=s["max_norm"])
     return handle.grad_norm, handle.master, handle.m, handle.v, handle.p16
