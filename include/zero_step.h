@@ -33,6 +33,12 @@
  * (zero_step_dp_replicas); and ZeRO-2 with the optimizer on the host CPU
  * (zero_offload_*).
  *
+ * It also holds the operators that stand next to the step in a language
+ * model's training: the global gradient norm and clipping (zero_grad_norm,
+ * zero_grad_clip, zero_step_clipped), the embedding lookup and its gradient
+ * (zero_embedding, zero_embedding_grad), and the cross entropy over a large
+ * vocabulary with its gradients (zero_lm_loss, zero_lm_loss_grad).
+ *
  * Layout.  n real parameters are split into units (one unit for data
  * parallel, ZeRO-1 and ZeRO-2; the caller's units, e.g. one per transformer
  * layer, for ZeRO-3).  Unit u holds unit_sizes[u] parameters padded with
@@ -90,6 +96,7 @@ extern "C" {
 /* ---- 16-bit formats ---------------------------------------------------- */
 #define ZERO_FP16       0
 #define ZERO_BF16       1
+#define ZERO_FP32       2   /* zero_grad_norm and zero_grad_clip only            */
 
 /* ---- accounting kinds --------------------------------------------------- */
 #define ZERO_RESIDENT   0
@@ -659,6 +666,160 @@ int zero_offload_destroy(zero_offload* ctx);
  */
 int zero_adam_host(int64_t n, const float* grad, float* master, float* m, float* v, void* out16, int work_dtype,
                    double lr, double beta1, double beta2, double eps, int64_t t, int W, int threads);
+
+/* ---- the global gradient norm and clipping --------------------------------- */
+
+/* Bytes of the workspace zero_grad_norm needs, whatever its list holds. */
+int64_t zero_grad_norm_workspace_bytes(void);
+
+/*
+ * The global norm of the mean gradient over many tensors:
+ *   g = (G_0 + ... + G_{W-1}) / W for each element (ranks in order, fp32),
+ *   norm = sqrt(sum of g^2 over every element of every tensor).
+ *   W          ranks, 1..ZERO_MAX_RANKS (1: the tensors' own norm).
+ *   n_tensors, numels  the tensors' element counts (0 is allowed; an empty
+ *              list has norm 0).
+ *   dtype      ZERO_FP16, ZERO_BF16 or ZERO_FP32, of every tensor.
+ *   grads      host array of W * n_tensors device pointers, rank after rank:
+ *              grads[w * n_tensors + t].  Aligned to their element; tensors
+ *              whose pointers are all aligned to 8 elements are read faster.
+ *   norm       one fp32 value of device memory (the result).
+ *   workspace  device, 256-byte aligned, at least
+ *              zero_grad_norm_workspace_bytes() bytes, zero before its first
+ *              use; the calls leave it ready for the next one.  Calls that
+ *              may overlap on the GPU need a workspace each.
+ *   stream     cudaStream_t (NULL: the legacy default stream).
+ * Squares are summed in fp32 within a thread and in fp64 beyond, in an order
+ * that depends on the sizes alone.  A NaN or an infinity anywhere makes the
+ * norm NaN or infinite, as does a sum of squares beyond fp32's range.
+ * Enqueues and returns.  ZERO_E_ARG / ZERO_E_ALIGN / ZERO_E_CUDA.
+ */
+int zero_grad_norm(int W, int64_t n_tensors, const int64_t* numels, int dtype, const void* const* grads, float* norm,
+                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * The clipped mean gradient: out = g * min(1, max_norm / (norm + 1e-6)),
+ * computed in fp32 and rounded once to `dtype`.  Arguments as for
+ * zero_grad_norm; `norm` is read on the device when the work runs (as
+ * zero_grad_norm left it; any positive value serves), max_norm is a positive
+ * finite fp32 value, and out is a host array of n_tensors device pointers.
+ * out[t] may be one of the tensor's own gradient pointers (in place), and must
+ * not overlap the gradients otherwise.  With a norm that is not finite nothing
+ * is scaled: out is g.
+ */
+int zero_grad_clip(int W, int64_t n_tensors, const int64_t* numels, int dtype, const void* const* grads,
+                   const float* norm, double max_norm, void* const* out, void* stream);
+
+/* Device bytes of the workspace zero_step_clipped needs for this context: the
+ * fp32 mean gradient (4 n_pad) and the norm's partial sums. */
+int64_t zero_step_clipped_workspace_bytes(const zero_ctx* ctx);
+
+/*
+ * zero_step with the mean gradient clipped by its global norm: Adam runs on
+ * g * min(1, max_norm / (norm + 1e-6)).  One pass over the W gradient vectors
+ * leaves g, in fp32, in the workspace and the norm in *norm; the update reads
+ * g from there.  Arguments as for zero_step, and
+ *   max_norm   a positive finite fp32 value.
+ *   norm       one fp32 value of device memory: the norm before clipping.
+ *   workspace  device, 256-byte aligned, zero_step_clipped_workspace_bytes
+ *              bytes, zero before its first use; used by this context alone.
+ * A norm that is not finite (an overflow in fp16 gradients) leaves master, m,
+ * v and the working copy as they were; the step counter advances all the
+ * same, and *norm says so.  ZeRO-3 with a unit hook: the backward pass gathers
+ * each unit and calls the hook without updating it; the norm and the updates
+ * follow, so that gradients which the hook's work makes are complete.  Clipped
+ * steps run as ordinary launches under zero_set_graph.  Where the norm is
+ * below max_norm the result is that of zero_step, bit for bit.
+ */
+int zero_step_clipped(zero_ctx* ctx, int scheme, int W, int64_t n, const void* const* grads, double lr, double beta1,
+                      double beta2, double eps, int64_t t, double max_norm, float* norm, void* workspace,
+                      int64_t workspace_bytes);
+
+/* ---- the embedding -------------------------------------------------------------- */
+
+/*
+ * Embedding lookup with scaling: row i of out is scale * table[ids[i]], the
+ * product in fp32, rounded once; 0 for an id outside [0, vocab) (padding).
+ *   tokens     ids, 0..2^24.
+ *   vocab, width  rows of the table (1..2^24) and values of a row (a multiple
+ *              of 8, 8..65536).
+ *   dtype      ZERO_FP16 or ZERO_BF16, of table and out (e.g. the step's
+ *              working copy).
+ *   ids        device, int32 (id_bytes 4) or int64 (id_bytes 8).
+ *   table_stride, out_stride  elements from one row to the next: at least
+ *              width, a multiple of 8; rows start on 16-byte boundaries.
+ *   scale      finite in fp32.
+ * Enqueues one kernel on `stream` (NULL: legacy default) and returns.
+ */
+int zero_embedding(int64_t tokens, int64_t vocab, int64_t width, int dtype, const void* ids, int id_bytes,
+                   const void* table, int64_t table_stride, double scale, void* out, int64_t out_stride, void* stream);
+
+/* Device bytes of the workspace zero_embedding_grad needs for up to `tokens` ids. */
+int64_t zero_embedding_workspace_bytes(int64_t tokens, int64_t width);
+
+/*
+ * The table's gradient: dtable[v] = scale * sum of dout[i] over the i with
+ * ids[i] = v, summed in fp32 in the order of i and rounded once.  With
+ * accumulate = 0 every row of dtable is written (0 where no id names it);
+ * with 1 the sum is added, in fp32, to the rows that ids name, and the others
+ * are left alone (a tied table: on top of zero_lm_loss_grad's).  Ids outside
+ * [0, vocab) contribute nothing, whatever their dout rows hold.  The same
+ * inputs give the same bits every time.  Other arguments as for
+ * zero_embedding; workspace is device memory, 256-byte aligned, of at least
+ * zero_embedding_workspace_bytes(tokens, width) bytes, with any contents.
+ */
+int zero_embedding_grad(int64_t tokens, int64_t vocab, int64_t width, int dtype, const void* ids, int id_bytes,
+                        const void* dout, int64_t dout_stride, double scale, void* dtable, int64_t dtable_stride,
+                        int accumulate, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---- cross entropy over a large vocabulary ------------------------------------------ */
+
+/* Device bytes of the workspace that zero_lm_loss (with_grad = 0) or both it
+ * and zero_lm_loss_grad (1) need for up to `tokens` tokens. */
+int64_t zero_lm_workspace_bytes(int64_t tokens, int64_t vocab, int64_t width, int with_grad);
+
+/*
+ * Softmax cross entropy of a language model's head: with the logits
+ * l = hidden table^T (tokens x vocab, never stored),
+ *   lse[i]  = log sum_v exp l[i, v],   loss[i] = lse[i] - l[i, targets[i]],
+ * loss 0 where the target is outside [0, vocab) (a token that is not trained
+ * on; its lse is written all the same).
+ *   tokens     0..2^24; vocab 1..2^24; width a multiple of 8, 8..65536.
+ *   dtype      ZERO_FP16 or ZERO_BF16, of hidden and table.
+ *   hidden, table  device, rows of `width` values; strides in elements (at
+ *              least width, a multiple of 8); rows start on 16-byte boundaries.
+ *   targets    device, int32 (id_bytes 4) or int64 (8).
+ *   loss, lse  device, `tokens` fp32 values each.
+ *   workspace  device, 256-byte aligned, any contents.
+ * Products are accumulated, and the sums of exponentials kept, in fp32.
+ * Enqueues on `stream` (NULL: legacy default) and returns.
+ */
+int zero_lm_loss(int64_t tokens, int64_t vocab, int64_t width, int dtype, const void* hidden, int64_t hidden_stride,
+                 const void* table, int64_t table_stride, const void* targets, int id_bytes, float* loss, float* lse,
+                 void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * The gradients of scale * (sum of loss): with D = exp(l - lse) - onehot(target)
+ * (rows of tokens without target: 0, whatever their hidden vectors hold),
+ *   dhidden = scale D table,   dtable = scale D^T hidden (+ dtable).
+ * The logits are formed again, piece by piece of the vocabulary, from lse as
+ * zero_lm_loss wrote it.  D is rounded to `dtype` for the two products, their
+ * sums are fp32, and each gradient is rounded once.
+ *   scale      finite in fp32: 1 / tokens for a mean, times a loss scale in fp16.
+ *   accumulate 1 adds to dtable (in fp32, rounded once), 0 overwrites all of it.
+ * Other arguments as above; dhidden and dtable like hidden and table.
+ */
+int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, int dtype, const void* hidden,
+                      int64_t hidden_stride, const void* table, int64_t table_stride, const void* targets, int id_bytes,
+                      const float* lse, double scale, void* dhidden, int64_t dhidden_stride, void* dtable,
+                      int64_t dtable_stride, int accumulate, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Wait for `stream` and report the LM kernels' bounded device waits (each
+ * about a second): ZERO_E_STATE if any gave up on the current device since
+ * the last call, so that what it belonged to is incomplete; else ZERO_OK.
+ */
+int zero_lm_status(void* stream);
 
 /* Message for the calling thread's last error ("" if none). */
 const char* zero_last_error(void);

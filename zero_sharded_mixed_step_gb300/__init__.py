@@ -15,6 +15,7 @@ places theta0 in the padded layout and creates the context.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -25,7 +26,7 @@ LIB_PATH = os.path.join(_HERE, "libzero_gb300.so")
 ZERO_OK, ZERO_E_ARG, ZERO_E_ALIGN, ZERO_E_CUDA, ZERO_E_RANK, ZERO_E_TIMEOUT, ZERO_E_STATE = 0, -1, -2, -3, -4, -5, -6
 ZERO_E_NOMEM = -7
 ZERO_SCHEME_DP, ZERO_SCHEME_Z1, ZERO_SCHEME_Z2, ZERO_SCHEME_Z3 = 0, 1, 2, 3
-ZERO_FP16, ZERO_BF16 = 0, 1
+ZERO_FP16, ZERO_BF16, ZERO_FP32 = 0, 1, 2
 ZERO_RESIDENT, ZERO_PEAK = 0, 1
 ZERO_VARIANT_AUTO, ZERO_VARIANT_VECTOR, ZERO_VARIANT_BULK = 0, 1, 2
 (ZERO_STAT_COMM_BYTES, ZERO_STAT_LAUNCHES, ZERO_STAT_GATHERS, ZERO_STAT_SCATTERS, ZERO_STAT_LIVE_ELEMS,
@@ -84,6 +85,18 @@ SIGNATURES = {
     "zero_step_z3_static": (_I, [_I, _L, _LP, _I, _I, _P, _P, _P, _PP, _PP, _D, _D, _D, _D, _L, HOOK, _P, _P]),
     "zero_step_dp_replicas": (_I, [_I, _L, _I, _I, _PP, _PP, _PP, _PP, _PP, _D, _D, _D, _D, _L, _P]),
     "zero_dp_replicas_mismatches": (_I, [_I, _L, _PP, _PP, _PP, _PP, _P, _P]),
+    "zero_grad_norm_workspace_bytes": (_L, []),
+    "zero_grad_norm": (_I, [_I, _L, _P, _I, _P, _P, _P, _L, _P]),
+    "zero_grad_clip": (_I, [_I, _L, _P, _I, _P, _P, _D, _P, _P]),
+    "zero_step_clipped_workspace_bytes": (_L, [_P]),
+    "zero_step_clipped": (_I, [_P, _I, _I, _L, _PP, _D, _D, _D, _D, _L, _D, _P, _P, _L]),
+    "zero_embedding": (_I, [_L, _L, _L, _I, _P, _I, _P, _L, _D, _P, _L, _P]),
+    "zero_embedding_workspace_bytes": (_L, [_L, _L]),
+    "zero_embedding_grad": (_I, [_L, _L, _L, _I, _P, _I, _P, _L, _D, _P, _L, _I, _P, _L, _P]),
+    "zero_lm_workspace_bytes": (_L, [_L, _L, _L, _I]),
+    "zero_lm_loss": (_I, [_L, _L, _L, _I, _P, _L, _P, _L, _P, _I, _P, _P, _P, _L, _P]),
+    "zero_lm_loss_grad": (_I, [_L, _L, _L, _I, _P, _L, _P, _L, _P, _I, _P, _D, _P, _L, _P, _L, _I, _P, _L, _P]),
+    "zero_lm_status": (_I, [_P]),
     "zero_last_error": (ctypes.c_char_p, []),
 }
 
@@ -132,6 +145,11 @@ def _ptr(x):
             raise ValueError("a tensor passed to the library must be contiguous")
         return x.data_ptr()
     return int(x)
+
+
+def _addr(x):
+    """The address of a tensor whose rows the caller describes by a stride."""
+    return x.data_ptr() if hasattr(x, "data_ptr") else x
 
 
 def _stream(s):
@@ -400,6 +418,84 @@ def zero_dp_replicas_mismatches(W, n, master, m, v, p16, mismatches, stream=None
         _stream(stream)))
 
 
+def _u64_array(values):
+    """The values as a C array of 64-bit words and its address."""
+    a = array.array("Q", values)
+    return a, a.buffer_info()[0]
+
+
+def zero_grad_norm_workspace_bytes() -> int:
+    return lib().zero_grad_norm_workspace_bytes()
+
+
+def zero_grad_norm(W, numels, dtype, grads, norm, workspace, workspace_bytes, stream=None) -> None:
+    """grads: W * len(numels) device pointers or tensors, rank after rank."""
+    sizes, sizes_at = _u64_array(numels)
+    ptrs, ptrs_at = _u64_array([_ptr(g) or 0 for g in grads])
+    _check("zero_grad_norm", lib().zero_grad_norm(W, len(sizes), sizes_at, dtype, ptrs_at, _ptr(norm),
+                                                  _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def zero_grad_clip(W, numels, dtype, grads, norm, max_norm, out, stream=None) -> None:
+    sizes, sizes_at = _u64_array(numels)
+    ptrs, ptrs_at = _u64_array([_ptr(g) or 0 for g in grads])
+    outs, outs_at = _u64_array([_ptr(o) or 0 for o in out])
+    _check("zero_grad_clip", lib().zero_grad_clip(W, len(sizes), sizes_at, dtype, ptrs_at, _ptr(norm), max_norm,
+                                                  outs_at, _stream(stream)))
+
+
+def zero_step_clipped_workspace_bytes(ctx) -> int:
+    return _check("zero_step_clipped_workspace_bytes", lib().zero_step_clipped_workspace_bytes(ctx))
+
+
+def zero_step_clipped(ctx, scheme, W, n, grads, lr, beta1, beta2, eps, t, max_norm, norm, workspace,
+                      workspace_bytes) -> None:
+    _check("zero_step_clipped", lib().zero_step_clipped(ctx, scheme, W, n, _ptr_array(grads), lr, beta1, beta2, eps, t,
+                                                        max_norm, _ptr(norm), _ptr(workspace), workspace_bytes))
+
+
+def zero_embedding(tokens, vocab, width, dtype, ids, id_bytes, table, table_stride, scale, out, out_stride,
+                   stream=None) -> None:
+    _check("zero_embedding", lib().zero_embedding(tokens, vocab, width, dtype, _addr(ids), id_bytes, _addr(table),
+                                                  table_stride, scale, _addr(out), out_stride, _stream(stream)))
+
+
+def zero_embedding_workspace_bytes(tokens: int, width: int) -> int:
+    return _check("zero_embedding_workspace_bytes", lib().zero_embedding_workspace_bytes(tokens, width))
+
+
+def zero_embedding_grad(tokens, vocab, width, dtype, ids, id_bytes, dout, dout_stride, scale, dtable, dtable_stride,
+                        accumulate, workspace, workspace_bytes, stream=None) -> None:
+    _check("zero_embedding_grad", lib().zero_embedding_grad(
+        tokens, vocab, width, dtype, _addr(ids), id_bytes, _addr(dout), dout_stride, scale, _addr(dtable),
+        dtable_stride, 1 if accumulate else 0, _addr(workspace), workspace_bytes, _stream(stream)))
+
+
+def zero_lm_workspace_bytes(tokens: int, vocab: int, width: int, with_grad: bool = True) -> int:
+    return _check("zero_lm_workspace_bytes", lib().zero_lm_workspace_bytes(tokens, vocab, width, 1 if with_grad else 0))
+
+
+def zero_lm_loss(tokens, vocab, width, dtype, hidden, hidden_stride, table, table_stride, targets, id_bytes, loss, lse,
+                 workspace, workspace_bytes, stream=None) -> None:
+    _check("zero_lm_loss", lib().zero_lm_loss(
+        tokens, vocab, width, dtype, _addr(hidden), hidden_stride, _addr(table), table_stride, _addr(targets),
+        id_bytes, _addr(loss), _addr(lse), _addr(workspace), workspace_bytes, _stream(stream)))
+
+
+def zero_lm_loss_grad(tokens, vocab, width, dtype, hidden, hidden_stride, table, table_stride, targets, id_bytes, lse,
+                      scale, dhidden, dhidden_stride, dtable, dtable_stride, accumulate, workspace, workspace_bytes,
+                      stream=None) -> None:
+    _check("zero_lm_loss_grad", lib().zero_lm_loss_grad(
+        tokens, vocab, width, dtype, _addr(hidden), hidden_stride, _addr(table), table_stride, _addr(targets),
+        id_bytes, _addr(lse), scale, _addr(dhidden), dhidden_stride, _addr(dtable), dtable_stride,
+        1 if accumulate else 0, _addr(workspace), workspace_bytes, _stream(stream)))
+
+
+def zero_lm_status(stream=None) -> None:
+    """Wait for the stream; raises ZeroError if a bounded device wait of the LM kernels gave up."""
+    _check("zero_lm_status", lib().zero_lm_status(_stream(stream)))
+
+
 # ---- convenience owners ---------------------------------------------------------
 
 _DT = {"fp16": ZERO_FP16, "bf16": ZERO_BF16, ZERO_FP16: ZERO_FP16, ZERO_BF16: ZERO_BF16}
@@ -447,6 +543,8 @@ class ZeroStep:
         self.ctx = zero_init(self.scheme, self.W, self.n, self.unit_sizes, self.gdt, self.wdt, self.master,
                              self.m, self.v, self.p16, self.shard16, self.unit_bufs, self.stream, gather_stream)
         self._hook = None
+        self.grad_norm = None      # fp32 scalar on the device: the last clipped step's norm
+        self._clip_space = None
         zero_refresh_working_copy(self.ctx)
         self.grads = self.new_grad_buffers() if with_grad_buffers else None
 
@@ -480,8 +578,20 @@ class ZeroStep:
                 out[o + r * s:o + (r + 1) * s].copy_(self.shard16[r][o16:o16 + s])
         return out
 
-    def step(self, grads, lr, beta1, beta2, eps, t):
-        zero_step(self.ctx, self.scheme, self.W, self.n, grads, lr, beta1, beta2, eps, t)
+    def step(self, grads, lr, beta1, beta2, eps, t, max_norm=None):
+        """One step; with ``max_norm`` the mean gradient is clipped by its global
+        norm, which ``grad_norm`` holds afterwards (on the device, in stream
+        order).  The first clipped step allocates the workspace for it."""
+        if max_norm is None:
+            zero_step(self.ctx, self.scheme, self.W, self.n, grads, lr, beta1, beta2, eps, t)
+            return
+        if self._clip_space is None:
+            nbytes = zero_step_clipped_workspace_bytes(self.ctx)
+            with _on(self.stream):
+                self._clip_space = self._alloc(nbytes, self.torch.uint8)
+                self.grad_norm = self._alloc(1, self.torch.float32)
+        zero_step_clipped(self.ctx, self.scheme, self.W, self.n, grads, lr, beta1, beta2, eps, t, max_norm,
+                          self.grad_norm, self._clip_space, self._clip_space.numel())
 
     def set_unit_hook(self, fn):
         self._hook = zero_set_unit_hook(self.ctx, fn)
@@ -650,3 +760,232 @@ class ZeroOffload:
             self.close()
         except Exception:
             pass
+
+
+# ---- operators of a language model around the step ----------------------------------
+
+def _on(stream):
+    """Allocate in the order of ``stream`` (None: the current one)."""
+    import contextlib
+
+    import torch
+    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
+
+
+def _rows(x, what, rows, width, dtype):
+    """(address, row stride) of a matrix of 16-bit rows; raises ValueError where it is none."""
+    if x.dim() != 2 or x.dtype != dtype or x.shape[1] != width or (rows is not None and x.shape[0] != rows) or \
+            not x.is_cuda or (width > 1 and x.stride(1) != 1):
+        raise ValueError(f"{what} must be a CUDA tensor of {'any number of' if rows is None else rows} rows of {width} "
+                         f"adjacent {dtype} values, not {x.dtype} {tuple(x.shape)} with strides {x.stride()}")
+    return x.data_ptr(), (x.stride(0) if x.shape[0] > 1 else width)
+
+
+def _ids(x, what):
+    """(address, bytes per id) of a contiguous vector of ids."""
+    size = x.element_size()
+    if size < 4 or x.is_floating_point() or x.is_complex() or not x.is_contiguous() or not x.is_cuda:
+        raise ValueError(f"{what} must be a contiguous CUDA tensor of int32 or int64 ids, not {x.dtype}")
+    return x.data_ptr(), size
+
+
+class _Owner:
+    """What the owners below share: the format, the workspace, the stream."""
+
+    def _setup(self, dtype, device, stream, alloc):
+        import torch
+        self.torch = torch
+        self.dtype = _DT[dtype]
+        self.torch_dtype = {ZERO_FP16: torch.float16, ZERO_BF16: torch.bfloat16}[self.dtype]
+        self.device = torch.device(device)
+        self.stream = stream
+        self._alloc = alloc or (lambda numel, dt: torch.zeros(numel, dtype=dt, device=self.device))
+
+    def _workspace(self, nbytes):
+        with _on(self.stream):
+            self.workspace = self._alloc(max(256, nbytes), self.torch.uint8)
+        self.workspace_bytes = self.workspace.numel()
+        self._ws = self.workspace.data_ptr()
+
+    def _raw_stream(self):
+        s = self.stream if self.stream is not None else self.torch.cuda.current_stream(self.device)
+        return s.cuda_stream or None
+
+    def _empty(self, shape, dtype):
+        if self.stream is None:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        with _on(self.stream):
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _check_tokens(self, count):
+        if count > self.max_tokens:
+            raise ValueError(f"{count} tokens: this owner was made for up to {self.max_tokens}")
+
+
+class LmLoss(_Owner):
+    """Cross entropy of a head of ``vocab`` rows of ``width`` values, and its
+    gradients, for up to ``max_tokens`` tokens a call (zero_lm_loss,
+    zero_lm_loss_grad).  The owner holds the workspace: calls that may overlap
+    on the GPU need an owner each.  Work goes to ``stream``, or to the stream
+    that is current at the call."""
+
+    def __init__(self, vocab, width, dtype="fp16", max_tokens=8192, with_grad=True, device="cuda", stream=None,
+                 alloc=None):
+        self._setup(dtype, device, stream, alloc)
+        self.vocab, self.width, self.max_tokens = int(vocab), int(width), int(max_tokens)
+        self.with_grad = bool(with_grad)
+        self._workspace(zero_lm_workspace_bytes(self.max_tokens, self.vocab, self.width, self.with_grad))
+
+    def loss(self, hidden, table, targets, loss=None, lse=None):
+        """(loss, lse) of each token, fp32; loss is 0 where the target lies outside the vocabulary."""
+        tokens = targets.numel()
+        self._check_tokens(tokens)
+        h, hs = _rows(hidden, "hidden", tokens, self.width, self.torch_dtype)
+        t, ts = _rows(table, "table", self.vocab, self.width, self.torch_dtype)
+        ids, id_bytes = _ids(targets, "targets")
+        loss = self._vector(loss, tokens)
+        lse = self._vector(lse, tokens)
+        zero_lm_loss(tokens, self.vocab, self.width, self.dtype, h, hs, t, ts, ids, id_bytes, loss.data_ptr(),
+                     lse.data_ptr(), self._ws, self.workspace_bytes, self._raw_stream())
+        return loss, lse
+
+    def grad(self, hidden, table, targets, lse, scale, dhidden=None, dtable=None, accumulate=False):
+        """(dhidden, dtable) of scale * loss.sum(); with ``accumulate`` added onto the given dtable."""
+        if not self.with_grad:
+            raise ValueError("this owner was made without room for the gradient (with_grad=False)")
+        if accumulate and dtable is None:
+            raise ValueError("accumulate needs the dtable to add to")
+        tokens = targets.numel()
+        self._check_tokens(tokens)
+        h, hs = _rows(hidden, "hidden", tokens, self.width, self.torch_dtype)
+        t, ts = _rows(table, "table", self.vocab, self.width, self.torch_dtype)
+        ids, id_bytes = _ids(targets, "targets")
+        lse = self._vector(lse, tokens)
+        if dhidden is None:
+            dhidden = self._empty((tokens, self.width), self.torch_dtype)
+        if dtable is None:
+            dtable = self._empty((self.vocab, self.width), self.torch_dtype)
+        dh, dhs = _rows(dhidden, "dhidden", tokens, self.width, self.torch_dtype)
+        dt, dts = _rows(dtable, "dtable", self.vocab, self.width, self.torch_dtype)
+        zero_lm_loss_grad(tokens, self.vocab, self.width, self.dtype, h, hs, t, ts, ids, id_bytes, lse.data_ptr(),
+                          scale, dh, dhs, dt, dts, accumulate, self._ws, self.workspace_bytes, self._raw_stream())
+        return dhidden, dtable
+
+    def _vector(self, x, tokens):
+        if x is None:
+            return self._empty(tokens, self.torch.float32)
+        if x.dtype != self.torch.float32 or x.numel() != tokens or not x.is_contiguous() or not x.is_cuda:
+            raise ValueError(f"loss and lse must be contiguous CUDA tensors of {tokens} fp32 values")
+        return x
+
+    def status(self):
+        """Wait for the work enqueued so far; raises ZeroError if a device wait gave up."""
+        zero_lm_status(self._raw_stream())
+
+
+class Embedding(_Owner):
+    """Lookup in a table of ``vocab`` rows of ``width`` values, times ``scale``,
+    and the table's gradient (zero_embedding, zero_embedding_grad), for up to
+    ``max_tokens`` ids a call.  Workspace and stream as for :class:`LmLoss`."""
+
+    def __init__(self, vocab, width, dtype="fp16", max_tokens=8192, scale=1.0, device="cuda", stream=None, alloc=None):
+        self._setup(dtype, device, stream, alloc)
+        self.vocab, self.width, self.max_tokens = int(vocab), int(width), int(max_tokens)
+        self.scale = float(scale)
+        self._workspace(zero_embedding_workspace_bytes(self.max_tokens, self.width))
+
+    def forward(self, tokens, table, out=None):
+        """scale * table[tokens], one row per id (0 for an id outside the table)."""
+        count = tokens.numel()
+        t, ts = _rows(table, "table", self.vocab, self.width, self.torch_dtype)
+        ids, id_bytes = _ids(tokens, "tokens")
+        if out is None:
+            out = self._empty((count, self.width), self.torch_dtype)
+        o, os_ = _rows(out, "out", count, self.width, self.torch_dtype)
+        zero_embedding(count, self.vocab, self.width, self.dtype, ids, id_bytes, t, ts, self.scale, o, os_,
+                       self._raw_stream())
+        return out
+
+    def grad(self, tokens, dout, dtable=None, accumulate=False):
+        """The table's gradient, written to (or, with ``accumulate``, added onto) dtable."""
+        if accumulate and dtable is None:
+            raise ValueError("accumulate needs the dtable to add to")
+        count = tokens.numel()
+        self._check_tokens(count)
+        ids, id_bytes = _ids(tokens, "tokens")
+        d, ds = _rows(dout, "dout", count, self.width, self.torch_dtype)
+        if dtable is None:
+            dtable = self._empty((self.vocab, self.width), self.torch_dtype)
+        t, ts = _rows(dtable, "dtable", self.vocab, self.width, self.torch_dtype)
+        zero_embedding_grad(count, self.vocab, self.width, self.dtype, ids, id_bytes, d, ds, self.scale, t, ts,
+                            accumulate, self._ws, self.workspace_bytes, self._raw_stream())
+        return dtable
+
+
+class GradClip(_Owner):
+    """The global norm of the mean gradient of W ranks over tensors of the given
+    element counts, and the clipped mean gradient as one flat vector, tensor
+    after tensor (zero_grad_norm, zero_grad_clip).  ``grads`` is a list of W
+    lists of tensors; dtype "fp16", "bf16" or "fp32"."""
+
+    def __init__(self, numels, W=1, dtype="fp16", device="cuda", stream=None, alloc=None):
+        import torch
+        fp32 = dtype in ("fp32", ZERO_FP32)
+        self._setup("fp16" if fp32 else dtype, device, stream, alloc)
+        if fp32:
+            self.dtype, self.torch_dtype = ZERO_FP32, torch.float32
+        self.W = int(W)
+        self.numels = [int(k) for k in numels]
+        self.n = sum(self.numels)
+        self._sizes, self._sizes_at = _u64_array(self.numels)
+        self._expected = self.numels * self.W
+        self._item = _itemsize(self.torch_dtype)
+        offsets, at = [], 0
+        for k in self.numels:
+            offsets.append(at * self._item)
+            at += k
+        self._offsets = offsets
+        self._workspace(zero_grad_norm_workspace_bytes())
+
+    def _pointers(self, grads):
+        T = self.torch.Tensor
+        flat = [g for rank in grads for g in rank]
+        if len(grads) != self.W or list(map(T.numel, flat)) != self._expected:
+            raise ValueError(f"grads must be {self.W} lists of tensors of the owner's sizes")
+        if any(g.dtype != self.torch_dtype for g in flat) or not all(map(T.is_contiguous, flat)):
+            raise ValueError(f"gradients must be contiguous and {self.torch_dtype}")
+        return _u64_array(map(T.data_ptr, flat))
+
+    def _norm(self, ptrs_at, stream):
+        norm = self._empty(1, self.torch.float32)
+        _check("zero_grad_norm", lib().zero_grad_norm(self.W, len(self.numels), self._sizes_at, self.dtype, ptrs_at,
+                                                      norm.data_ptr(), self._ws, self.workspace_bytes, stream))
+        return norm
+
+    def _clip(self, ptrs_at, norm, max_norm, out, stream):
+        if out is None:
+            out = self._empty(self.n, self.torch_dtype)
+        if out.numel() != self.n or out.dtype != self.torch_dtype or not out.is_contiguous():
+            raise ValueError(f"out must be {self.n} contiguous values of {self.torch_dtype}")
+        base = out.data_ptr()
+        outs, outs_at = _u64_array([base + o for o in self._offsets])
+        _check("zero_grad_clip", lib().zero_grad_clip(self.W, len(self.numels), self._sizes_at, self.dtype, ptrs_at,
+                                                      norm.data_ptr(), max_norm, outs_at, stream))
+        return out
+
+    def norm(self, grads):
+        """The norm, one fp32 value on the device."""
+        ptrs, at = self._pointers(grads)
+        return self._norm(at, self._raw_stream())
+
+    def clip(self, grads, norm, max_norm, out=None):
+        """The flat mean gradient times min(1, max_norm / (norm + 1e-6))."""
+        ptrs, at = self._pointers(grads)
+        return self._clip(at, norm, max_norm, out, self._raw_stream())
+
+    def norm_and_clip(self, grads, max_norm, out=None):
+        """(norm, flat clipped mean gradient)."""
+        ptrs, at = self._pointers(grads)
+        stream = self._raw_stream()
+        norm = self._norm(at, stream)
+        return norm, self._clip(at, norm, max_norm, out, stream)

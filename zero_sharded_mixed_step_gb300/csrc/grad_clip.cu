@@ -1,0 +1,543 @@
+// The global gradient norm over many tensors, and clipping by it.
+//
+//   g_e  = (G_0[e] + ... + G_{W-1}[e]) / W        (ranks in order, fp32)
+//   norm = sqrt(sum over every tensor's elements e of g_e^2)
+//   coef = min(1, max_norm / (norm + 1e-6))
+//
+// zero_grad_norm computes norm, zero_grad_clip writes round(coef g), and
+// zero_step_clipped runs the step on coef g: its first pass reads the W
+// gradient vectors once, keeps g in fp32 and sums the squares, its second
+// runs Adam on coef g.  Reading the fp32 mean back costs 8 bytes an element
+// (written and read) where reading the W gradients again would cost 2 W.
+//
+// Squares are summed in fp32 by each thread and in fp64 from there on: within
+// a block, and over the blocks in their order by the last block to finish, so
+// the norm does not depend on the order in which blocks run.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "step_math.cuh"
+#include "zero_context.h"
+#include "zero_internal.h"
+#include "zero_step.h"
+
+namespace zero {
+namespace {
+
+using namespace dev;
+using host::ceil_div;
+using host::fail;
+
+constexpr int kThreads = 256;
+constexpr int kMaxBlocks = 1024;           // partial sums of one launch
+constexpr double kClipEps = 1e-6;
+
+// Workspace: the number of blocks that have finished (0 between calls), then
+// a partial sum of squares for each block.
+struct NormSpace {
+  unsigned int* done;
+  double* part;
+};
+constexpr int64_t kNormBytes = 256 + kMaxBlocks * 8;
+
+NormSpace norm_space(void* ws) {
+  return {static_cast<unsigned int*>(ws), reinterpret_cast<double*>(static_cast<char*>(ws) + 256)};
+}
+
+// ---- element types -------------------------------------------------------------
+
+// 8 consecutive elements of T as floats; aligned: the address allows the wide load.
+template <typename T>
+struct Eight {
+  static __device__ __forceinline__ void load(const T* p, float (&f)[8]) { Fmt<T>::unpack8(ld_16B(p), f); }
+  static __device__ __forceinline__ void store(T* p, const float (&f)[8]) { st_16B(p, Fmt<T>::pack8(f)); }
+  static __device__ __forceinline__ float load1(const T* p) { return Fmt<T>::load1(p, 0); }
+  static __device__ __forceinline__ void store1(T* p, float x) { Fmt<T>::store1(p, 0, x); }
+};
+
+template <>
+struct Eight<float> {
+  static __device__ __forceinline__ void load(const float* p, float (&f)[8]) { ld_32B(p, f); }
+  static __device__ __forceinline__ void store(float* p, const float (&f)[8]) { st_32B(p, f); }
+  static __device__ __forceinline__ float load1(const float* p) { return *p; }
+  static __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+};
+
+// ---- sums over the blocks ---------------------------------------------------------
+
+// Adds the block's sum of squares to its slot; the last block of the launch
+// adds all the slots [0, blocks) in order and, with `norm`, writes the root.
+__device__ __forceinline__ void finish_sum(float mine, const NormSpace& ws, unsigned int first, unsigned int blocks,
+                                           float* norm) {
+  __shared__ double warp_sum[kThreads / 32];
+  __shared__ bool last;
+  double s = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+    for (int k = 0; k < kThreads / 32; ++k) t += warp_sum[k];
+    ws.part[first + blockIdx.x] = t;
+    __threadfence();
+    last = norm != nullptr && atomicAdd(ws.done, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double t = 0.0;
+  for (unsigned int k = threadIdx.x; k < blocks; k += kThreads) t += __ldcg(ws.part + k);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = t;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double all = 0.0;
+    for (int k = 0; k < kThreads / 32; ++k) all += warp_sum[k];
+    *norm = static_cast<float>(sqrt(all));
+    *ws.done = 0;
+  }
+}
+
+__device__ __forceinline__ float clip_coef(float norm, float max_norm) {
+  return fminf(1.f, __fdiv_rn(max_norm, __fadd_rn(norm, static_cast<float>(kClipEps))));
+}
+
+// ---- many tensors ------------------------------------------------------------------
+//
+// The tensors' sizes and addresses travel as the kernel's parameters, so a
+// call needs no copy to the device; a list that does not fit one launch takes
+// several.  Work is cut into chunks of kChunk elements of one tensor.
+
+constexpr int kChunk = 8192;
+constexpr int kTableBytes = 28 * 1024;     // a launch's parameters may hold 32,764 bytes
+
+struct Table {
+  int tensors, W;
+  unsigned int chunks;
+  int want_out;
+  // follows: chunk_start[tensors + 1], then per tensor its element count,
+  // W gradient addresses and, with want_out, an output address
+  alignas(8) unsigned char data[kTableBytes];
+
+  __host__ __device__ int64_t words() const { return 1 + W + want_out; }
+  __host__ __device__ const unsigned int* starts() const { return reinterpret_cast<const unsigned int*>(data); }
+  __host__ __device__ const int64_t* row(int t) const {
+    return reinterpret_cast<const int64_t*>(data + (tensors + 2) / 2 * 8) + t * words();
+  }
+};
+
+// The mean over the ranks of 8 elements, or of one.
+template <typename T>
+__device__ __forceinline__ void mean8(const int64_t* ranks, int64_t i, int W, bool pow2, float inv_w, float (&g)[8]) {
+  Eight<T>::load(reinterpret_cast<const T*>(ranks[0]) + i, g);
+  for (int w = 1; w < W; ++w) {
+    float f[8];
+    Eight<T>::load(reinterpret_cast<const T*>(ranks[w]) + i, f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] = __fadd_rn(g[k], f[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) g[k] = rank_mean(g[k], W, inv_w, pow2);
+}
+
+template <typename T>
+__device__ __forceinline__ float mean1(const int64_t* ranks, int64_t i, int W, bool pow2, float inv_w) {
+  float g = Eight<T>::load1(reinterpret_cast<const T*>(ranks[0]) + i);
+  for (int w = 1; w < W; ++w) g = __fadd_rn(g, Eight<T>::load1(reinterpret_cast<const T*>(ranks[w]) + i));
+  return rank_mean(g, W, inv_w, pow2);
+}
+
+template <typename T, bool CLIP>
+__global__ void __launch_bounds__(kThreads) tensors_pass(const __grid_constant__ Table t, NormSpace ws,
+                                                         unsigned int first, unsigned int blocks, float* norm,
+                                                         float max_norm) {
+  const int W = t.W;
+  const bool pow2 = (W & (W - 1)) == 0;
+  const float inv_w = 1.f / W;
+  float coef = 1.f;
+  if (CLIP) {
+    const float n = *norm;
+    coef = isfinite(n) ? clip_coef(n, max_norm) : 1.f;
+  }
+  float squares = 0.f;
+  for (unsigned int chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
+    // the last tensor that starts at or before this chunk
+    int lo = 0, hi = t.tensors - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (t.starts()[mid] <= chunk) lo = mid;
+      else hi = mid - 1;
+    }
+    const int64_t* row = t.row(lo);
+    const int64_t numel = row[0], begin = static_cast<int64_t>(chunk - t.starts()[lo]) * kChunk;
+    const int64_t end = min(numel, begin + kChunk);
+    const int64_t* ranks = row + 1;
+    int64_t bits = 0;
+    for (int w = 0; w < W + CLIP; ++w) bits |= ranks[w];
+    T* out = CLIP ? reinterpret_cast<T*>(ranks[W]) : nullptr;
+    const bool wide = (bits & (8 * sizeof(T) - 1)) == 0;
+    const int64_t vec_end = wide ? begin + (end - begin) / 8 * 8 : begin;
+    for (int64_t i = begin + threadIdx.x * 8; i < vec_end; i += kThreads * 8) {
+      float g[8];
+      mean8<T>(ranks, i, W, pow2, inv_w, g);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (CLIP) g[k] *= coef;
+        else squares = fmaf(g[k], g[k], squares);
+      }
+      if (CLIP) Eight<T>::store(out + i, g);
+    }
+    for (int64_t i = vec_end + threadIdx.x; i < end; i += kThreads) {
+      const float g = mean1<T>(ranks, i, W, pow2, inv_w);
+      if (CLIP) Eight<T>::store1(out + i, g * coef);
+      else squares = fmaf(g, g, squares);
+    }
+  }
+  if (!CLIP) finish_sum(squares, ws, first, blocks, norm);
+}
+
+// ---- the step's two passes --------------------------------------------------------------
+
+struct MeanNormArgs {
+  int W;
+  const void* grads[kMaxRanks];
+  int64_t n;
+  float* mean;
+  float inv_w;
+  NormSpace ws;
+  float* norm;
+};
+
+template <typename GT, int WC>
+__global__ void __launch_bounds__(kThreads) mean_norm_pass(const __grid_constant__ MeanNormArgs a) {
+  const int W = WC > 0 ? WC : a.W;
+  const bool pow2 = (W & (W - 1)) == 0;
+  float squares = 0.f;
+  const int64_t groups = a.n >> 3;
+  for (int64_t gi = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; gi < groups;
+       gi += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int64_t i = gi << 3;
+    float sum[8];
+    if constexpr (WC > 0) {
+      uint4 raw[WC];
+#pragma unroll
+      for (int w = 0; w < WC; ++w) raw[w] = ld_16B(static_cast<const GT*>(a.grads[w]) + i);
+      Fmt<GT>::unpack8(raw[0], sum);
+#pragma unroll
+      for (int w = 1; w < WC; ++w) {
+        float f[8];
+        Fmt<GT>::unpack8(raw[w], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[k] = __fadd_rn(sum[k], f[k]);
+      }
+    } else {
+      Fmt<GT>::unpack8(ld_16B(static_cast<const GT*>(a.grads[0]) + i), sum);
+#pragma unroll 4
+      for (int w = 1; w < W; ++w) {
+        float f[8];
+        Fmt<GT>::unpack8(ld_16B(static_cast<const GT*>(a.grads[w]) + i), f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[k] = __fadd_rn(sum[k], f[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      sum[k] = rank_mean(sum[k], W, a.inv_w, pow2);
+      squares = fmaf(sum[k], sum[k], squares);
+    }
+    st_32B(a.mean + i, sum);
+  }
+  if (blockIdx.x == 0) {
+    for (int64_t e = (groups << 3) + threadIdx.x; e < a.n; e += kThreads) {
+      float g = Fmt<GT>::load1(a.grads[0], e);
+      for (int w = 1; w < W; ++w) g = __fadd_rn(g, Fmt<GT>::load1(a.grads[w], e));
+      g = rank_mean(g, W, a.inv_w, pow2);
+      a.mean[e] = g;
+      squares = fmaf(g, g, squares);
+    }
+  }
+  finish_sum(squares, a.ws, 0, gridDim.x, a.norm);
+}
+
+struct ClippedArgs {
+  const float* mean;
+  float* master;
+  float* m;
+  float* v;
+  Seg segs[kMaxSegs];
+  AdamCoef coef;
+  const float* norm;
+  float max_norm;
+};
+
+// Adam on coef * mean over a segment; the ZeRO-3 gather of its old 16-bit
+// values (pre_out) as in the fused step.  A norm that is not finite leaves
+// the state as it was.
+template <typename OT>
+__global__ void __launch_bounds__(kThreads) clipped_update(const __grid_constant__ ClippedArgs a) {
+  const Seg& seg = a.segs[blockIdx.y];
+  const float norm = *a.norm;
+  const bool update = isfinite(norm);
+  const float coef = update ? clip_coef(norm, a.max_norm) : 0.f;
+  OT* out = static_cast<OT*>(seg.out);
+  OT* pre = static_cast<OT*>(seg.pre_out);
+  if (!update && !pre) return;
+  const int64_t lo = seg.lo, hi = seg.lo + seg.len;
+  const int64_t g0 = (lo + 7) >> 3, g1 = hi >> 3;
+  const bool out_vec = ((reinterpret_cast<uintptr_t>(out) - static_cast<uintptr_t>(lo) * 2u) & 15u) == 0;
+  const bool pre_vec = out_vec && ((reinterpret_cast<uintptr_t>(pre) - static_cast<uintptr_t>(lo) * 2u) & 15u) == 0;
+  auto one = [&](int64_t e) {
+    const int64_t j = e - lo;
+    if (pre) pre[j] = out[j];
+    if (!update) return;
+    float th = a.master[e], m = a.m[e], v = a.v[e];
+    adam_element(__fmul_rn(a.mean[e], coef), th, m, v, a.coef);
+    a.master[e] = th;
+    a.m[e] = m;
+    a.v[e] = v;
+    Fmt<OT>::store1(out, j, th);
+  };
+  for (int64_t g = g0 + static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; g < g1;
+       g += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int64_t i = g << 3, j = i - lo;
+    if (pre) {
+      if (pre_vec) {
+        st_16B(pre + j, ld_16B(out + j));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) pre[j + k] = out[j + k];
+      }
+    }
+    if (!update) continue;
+    float x[8], th[8], m[8], v[8];
+    ld_32B(a.mean + i, x);
+    ld_32B(a.master + i, th);
+    ld_32B(a.m + i, m);
+    ld_32B(a.v + i, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) adam_element(__fmul_rn(x[k], coef), th[k], m[k], v[k], a.coef);
+    st_32B(a.master + i, th);
+    st_32B(a.m + i, m);
+    st_32B(a.v + i, v);
+    if (out_vec) {
+      st_16B(out + j, Fmt<OT>::pack8(th));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) Fmt<OT>::store1(out, j + k, th[k]);
+    }
+  }
+  if (blockIdx.x == 0) {
+    const int64_t head = g0 < g1 ? g0 << 3 : hi, tail = g0 < g1 ? g1 << 3 : hi;
+    for (int64_t e = lo + threadIdx.x; e < head; e += kThreads) one(e);
+    for (int64_t e = tail + threadIdx.x; e < hi; e += kThreads) one(e);
+  }
+}
+
+using MeanNormFn = void (*)(const MeanNormArgs);
+
+template <typename GT>
+MeanNormFn pick_mean_norm(int W) {
+  switch (W) {
+    case 1: return mean_norm_pass<GT, 1>;
+    case 2: return mean_norm_pass<GT, 2>;
+    case 4: return mean_norm_pass<GT, 4>;
+    case 8: return mean_norm_pass<GT, 8>;
+    case 16: return mean_norm_pass<GT, 16>;
+    default: return mean_norm_pass<GT, 0>;
+  }
+}
+
+// ---- host -------------------------------------------------------------------------------
+
+int check_tensors(int W, int64_t n_tensors, const int64_t* numels, int dtype, const void* const* grads,
+                  void* const* out) {
+  if (W < 1 || W > kMaxRanks) return fail(ZERO_E_ARG, "W=%d outside [1, %d]", W, kMaxRanks);
+  if (n_tensors < 0 || n_tensors > (int64_t(1) << 24)) return fail(ZERO_E_ARG, "%lld tensors", (long long)n_tensors);
+  if (dtype != ZERO_FP16 && dtype != ZERO_BF16 && dtype != ZERO_FP32)
+    return fail(ZERO_E_ARG, "the gradients' format must be ZERO_FP16, ZERO_BF16 or ZERO_FP32");
+  if (n_tensors > 0 && (numels == nullptr || grads == nullptr)) return fail(ZERO_E_ARG, "numels and grads are required");
+  const uintptr_t size = dtype == ZERO_FP32 ? 4 : 2;
+  for (int64_t t = 0; t < n_tensors; ++t) {
+    if (numels[t] < 0 || numels[t] > (int64_t(1) << 46))
+      return fail(ZERO_E_ARG, "tensor %lld has %lld elements", (long long)t, (long long)numels[t]);
+    if (numels[t] == 0) continue;
+    for (int w = 0; w <= W; ++w) {
+      if (w == W && out == nullptr) break;
+      const void* p = w < W ? grads[w * n_tensors + t] : out[t];
+      if (p == nullptr) return fail(ZERO_E_ARG, "tensor %lld: a pointer is NULL", (long long)t);
+      if (reinterpret_cast<uintptr_t>(p) % size) return fail(ZERO_E_ALIGN, "tensor %lld is not aligned to its elements", (long long)t);
+    }
+  }
+  return ZERO_OK;
+}
+
+// Fill launches from the list and call `launch(table, last)` for each.
+template <typename F>
+int for_tables(int W, int64_t n_tensors, const int64_t* numels, const void* const* grads, void* const* out, F launch) {
+  static thread_local Table t;
+  static thread_local int64_t pick[kTableBytes / 16];   // the tensors of one launch
+  const int64_t words = 1 + W + (out ? 1 : 0);
+  const int64_t most = (kTableBytes - 16) / (8 * words + 4);
+  int64_t k = 0;
+  do {
+    int64_t chunks = 0;
+    int count = 0;
+    while (k < n_tensors && count < most) {
+      const int64_t c = ceil_div(numels[k], kChunk);
+      if (c > INT32_MAX) return fail(ZERO_E_ARG, "tensor %lld has too many elements", (long long)k);
+      if (count > 0 && chunks + c > INT32_MAX) break;
+      if (c > 0) {
+        pick[count++] = k;
+        chunks += c;
+      }
+      ++k;
+    }
+    t.tensors = count;
+    t.W = W;
+    t.want_out = out ? 1 : 0;
+    t.chunks = static_cast<unsigned int>(chunks);
+    unsigned int* starts = const_cast<unsigned int*>(t.starts());
+    unsigned int at = 0;
+    for (int j = 0; j < t.tensors; ++j) {
+      starts[j] = at;
+      at += static_cast<unsigned int>(ceil_div(numels[pick[j]], kChunk));
+      int64_t* row = const_cast<int64_t*>(t.row(j));
+      row[0] = numels[pick[j]];
+      for (int w = 0; w < W; ++w) row[1 + w] = reinterpret_cast<int64_t>(grads[w * n_tensors + pick[j]]);
+      if (out) row[1 + W] = reinterpret_cast<int64_t>(out[pick[j]]);
+    }
+    starts[t.tensors] = at;
+    const int rc = launch(t, k >= n_tensors);
+    if (rc) return rc;
+  } while (k < n_tensors);
+  return ZERO_OK;
+}
+
+unsigned pass_blocks(int64_t chunks, int64_t most) {
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>({chunks, static_cast<int64_t>(sm_count()) * 4, most})));
+}
+
+int check_norm_args(const float* norm, const void* workspace, int64_t workspace_bytes) {
+  if (norm == nullptr) return fail(ZERO_E_ARG, "norm is NULL");
+  if (reinterpret_cast<uintptr_t>(norm) % 4) return fail(ZERO_E_ALIGN, "norm must be 4-byte aligned");
+  if (workspace == nullptr) return fail(ZERO_E_ARG, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(ZERO_E_ALIGN, "workspace must be 256-byte aligned");
+  if (workspace_bytes < kNormBytes)
+    return fail(ZERO_E_ARG, "workspace of %lld bytes: %lld are needed", (long long)workspace_bytes, (long long)kNormBytes);
+  return ZERO_OK;
+}
+
+template <bool CLIP>
+void launch_tensors(const Table& t, int dtype, unsigned blocks, const NormSpace& ws, unsigned first, float* norm,
+                    float max_norm, cudaStream_t s) {
+  const unsigned all = first + blocks;
+  if (dtype == ZERO_FP16) tensors_pass<__half, CLIP><<<blocks, kThreads, 0, s>>>(t, ws, first, all, norm, max_norm);
+  else if (dtype == ZERO_BF16)
+    tensors_pass<__nv_bfloat16, CLIP><<<blocks, kThreads, 0, s>>>(t, ws, first, all, norm, max_norm);
+  else tensors_pass<float, CLIP><<<blocks, kThreads, 0, s>>>(t, ws, first, all, norm, max_norm);
+}
+
+}  // namespace
+
+int64_t clip_workspace_bytes(int64_t n_pad) { return kNormBytes + host::round_up(n_pad * 4, 256); }
+
+float* clip_mean(void* workspace) { return reinterpret_cast<float*>(static_cast<char*>(workspace) + kNormBytes); }
+
+cudaError_t launch_mean_norm(int W, int grad_dtype, const void* const* grads, int64_t n_pad, void* workspace,
+                             float* norm, cudaStream_t stream, int64_t* launches) {
+  MeanNormArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.W = W;
+  for (int w = 0; w < W; ++w) a.grads[w] = grads[w];
+  a.n = n_pad;
+  a.mean = clip_mean(workspace);
+  a.inv_w = static_cast<float>(1.0 / W);
+  a.ws = norm_space(workspace);
+  a.norm = norm;
+  const MeanNormFn fn = grad_dtype == kF16 ? pick_mean_norm<__half>(W) : pick_mean_norm<__nv_bfloat16>(W);
+  fn<<<pass_blocks(n_pad / 8 / kThreads + 1, kMaxBlocks), kThreads, 0, stream>>>(a);
+  ++*launches;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_clipped_update(const FusedLaunch& f, const float* mean, const float* norm, float max_norm,
+                                  cudaStream_t stream, int64_t* launches) {
+  if (f.nseg <= 0) return cudaSuccess;
+  ClippedArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.mean = mean;
+  a.master = f.master;
+  a.m = f.m;
+  a.v = f.v;
+  int64_t longest = 0;
+  for (int s = 0; s < f.nseg; ++s) {
+    a.segs[s] = f.segs[s];
+    longest = std::max(longest, f.segs[s].len);
+  }
+  a.coef = f.coef;
+  a.norm = norm;
+  a.max_norm = max_norm;
+  const int64_t per_seg = ceil_div(static_cast<int64_t>(sm_count()) * 2, f.nseg);
+  const int64_t bx = std::max<int64_t>(1, std::min<int64_t>(per_seg, longest / 8 / kThreads + 1));
+  const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>(f.nseg));
+  if (f.work_dtype == kF16) clipped_update<__half><<<grid, kThreads, 0, stream>>>(a);
+  else clipped_update<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
+  ++*launches;
+  return cudaGetLastError();
+}
+
+}  // namespace zero
+
+using namespace zero;
+
+extern "C" int64_t zero_grad_norm_workspace_bytes(void) { return kNormBytes; }
+
+extern "C" int zero_grad_norm(int W, int64_t n_tensors, const int64_t* numels, int dtype, const void* const* grads,
+                              float* norm, void* workspace, int64_t workspace_bytes, void* stream) {
+  int rc = check_tensors(W, n_tensors, numels, dtype, grads, nullptr);
+  if (rc || (rc = check_norm_args(norm, workspace, workspace_bytes))) return rc;
+  const NormSpace ws = norm_space(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // every launch leaves its blocks' sums in slots of its own; the last one adds them up
+  const int64_t words = 1 + W, most = (kTableBytes - 16) / (8 * words + 4);
+  const int64_t launches = std::max<int64_t>(1, ceil_div(n_tensors, most));
+  if (launches > kMaxBlocks) return fail(ZERO_E_ARG, "too many tensors (%lld)", (long long)n_tensors);
+  unsigned first = 0;
+  return for_tables(W, n_tensors, numels, grads, nullptr, [&](const Table& t, bool last) -> int {
+    const unsigned blocks = pass_blocks(t.chunks, kMaxBlocks / launches);
+    if (first + blocks > kMaxBlocks) return fail(ZERO_E_ARG, "too many elements");
+    launch_tensors<false>(t, dtype, blocks, ws, first, last ? norm : nullptr, 0.f, s);
+    first += blocks;
+    ZERO_CUDA(cudaGetLastError());
+    return ZERO_OK;
+  });
+}
+
+extern "C" int zero_grad_clip(int W, int64_t n_tensors, const int64_t* numels, int dtype, const void* const* grads,
+                              const float* norm, double max_norm, void* const* out, void* stream) {
+  if (n_tensors > 0 && out == nullptr) return fail(ZERO_E_ARG, "out is NULL");
+  int rc = check_tensors(W, n_tensors, numels, dtype, grads, out);
+  if (rc) return rc;
+  if (norm == nullptr) return fail(ZERO_E_ARG, "norm is NULL");
+  if (reinterpret_cast<uintptr_t>(norm) % 4) return fail(ZERO_E_ALIGN, "norm must be 4-byte aligned");
+  const float limit = static_cast<float>(max_norm);
+  if (!(limit > 0) || !std::isfinite(limit)) return fail(ZERO_E_ARG, "max_norm %g is not a positive finite fp32 value", max_norm);
+  if (n_tensors == 0) return ZERO_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return for_tables(W, n_tensors, numels, grads, out, [&](const Table& t, bool) -> int {
+    if (t.tensors == 0) return ZERO_OK;
+    launch_tensors<true>(t, dtype, pass_blocks(t.chunks, INT32_MAX), NormSpace{nullptr, nullptr}, 0,
+                         const_cast<float*>(norm), limit, s);
+    ZERO_CUDA(cudaGetLastError());
+    return ZERO_OK;
+  });
+}

@@ -177,7 +177,7 @@ int launch_update(zero_ctx* c, int64_t u, const void* const* grads, const zero::
   a.v = c->v;
   a.coef = coef;
   a.variant = c->variant;
-  if (c->stall_pending) {
+  if (c->stall_pending && c->clip == nullptr) {   // the clipped update has no device-side waits
     a.inject_stall = 1;
     a.stall_tile = c->stall_tile;
     c->stall_pending = false;
@@ -210,9 +210,15 @@ int launch_update(zero_ctx* c, int64_t u, const void* const* grads, const zero::
   Bracket br{c, ZERO_KERNEL_FUSED, stream};
   int rc = br.open();
   if (rc) return rc;
-  cudaError_t e = zero::launch_fused_step(a, stream, &c->launches);
-  if (e != cudaSuccess) return cuda_fail(e, "fused reduce-scatter/Adam/recast launch");
-  c->last_variant = zero::last_fused_variant();
+  if (c->clip) {
+    const cudaError_t e = zero::launch_clipped_update(a, zero::clip_mean(c->clip->workspace), c->clip->norm,
+                                                      c->clip->max_norm, stream, &c->launches);
+    if (e != cudaSuccess) return cuda_fail(e, "clipped update launch");
+  } else {
+    const cudaError_t e = zero::launch_fused_step(a, stream, &c->launches);
+    if (e != cudaSuccess) return cuda_fail(e, "fused reduce-scatter/Adam/recast launch");
+    c->last_variant = zero::last_fused_variant();
+  }
   touch(c, stream);
   return br.close();
 }
@@ -298,6 +304,15 @@ int poison_unit(zero_ctx* c, int64_t u, void* buf, cudaStream_t s) {
   return ZERO_OK;
 }
 
+// The mean and norm pass of a clipped step, on the update stream.
+int launch_norm(zero_ctx* c, const void* const* grads) {
+  const cudaError_t e = zero::launch_mean_norm(c->W, c->gdt, grads, c->L.n_pad, c->clip->workspace, c->clip->norm,
+                                               c->su, &c->launches);
+  if (e != cudaSuccess) return cuda_fail(e, "gradient norm launch");
+  touch(c, c->su);
+  return ZERO_OK;
+}
+
 // ZeRO-3 step: forward gathers in unit order, backward gathers in reverse
 // order each followed by the unit's update, two gather buffers in turn.  The
 // gather of the next unit (stream G) waits only for the buffer it reuses to
@@ -313,6 +328,11 @@ int poison_unit(zero_ctx* c, int64_t u, void* buf, cudaStream_t s) {
 // each buffer), and each backward gather is done by its unit's update pass.
 // A unit counts as live from its gather until its buffer is taken by a later
 // gather (or the step ends): at most two units are live.
+// A clipped step needs the norm of every unit's gradient before the first
+// update.  Without a hook the norm pass simply comes first.  With one, the
+// hook's work on the gathered units may still be making the gradients, so the
+// backward pass gathers and calls the hook without updating, and the norm and
+// all the updates follow it.
 int run_zero3_step(zero_ctx* c, const void* const* grads, const zero::AdamCoef& coef) {
   int rc = ensure_cuda(c);
   if (rc) return rc;
@@ -327,6 +347,8 @@ int run_zero3_step(zero_ctx* c, const void* const* grads, const zero::AdamCoef& 
   bool used[2] = {false, false};
   int64_t held[2] = {0, 0};
   int64_t seq = 0;
+  const bool defer = c->clip != nullptr && c->hook != nullptr;
+  if (c->clip && !defer && (rc = launch_norm(c, grads))) return rc;
   // the stream of the fused backward pass (without a hook): su, or the
   // second chain of a captured step (see below)
   cudaStream_t s_upd = su;
@@ -357,7 +379,7 @@ int run_zero3_step(zero_ctx* c, const void* const* grads, const zero::AdamCoef& 
       ZERO_CUDA(cudaStreamWaitEvent(su, c->ev_gathered[b], 0));
     }
     if (c->hook) c->hook(c->hook_user, phase, u, buf, static_cast<void*>(su));
-    if (phase == 1) {
+    if (phase == 1 && !defer) {
       r = launch_update(c, u, grads, coef, su);
       if (r) return r;
       count_scatter(c, u);
@@ -441,6 +463,13 @@ int run_zero3_step(zero_ctx* c, const void* const* grads, const zero::AdamCoef& 
     ZERO_CUDA(cudaStreamWaitEvent(su, c->ev_join, 0));
   }
   if (rc) return rc;
+  if (defer) {
+    if ((rc = launch_norm(c, grads))) return rc;
+    for (int64_t u = U - 1; u >= 0; --u) {
+      if ((rc = launch_update(c, u, grads, coef, su))) return rc;
+      count_scatter(c, u);
+    }
+  }
   c->live_elems -= held[0] + held[1];
   return ZERO_OK;
 }
@@ -463,11 +492,11 @@ void drop_graph(zero_ctx* c) {
 }
 
 // Whether this step may run from the graph: anything that adds or changes
-// work (a hook, timing brackets, poisoning, an injected stall) runs the
-// ordinary launches instead.
+// work (a hook, timing brackets, poisoning, an injected stall, clipping) runs
+// the ordinary launches instead.
 bool graph_applies(const zero_ctx* c) {
   return c->graph_on && c->scheme == ZERO_SCHEME_Z3 && c->hook == nullptr && !c->timing && c->debug == 0 &&
-         !c->stall_pending;
+         !c->stall_pending && c->clip == nullptr;
 }
 
 // Capture one step's launches into c->graph (nothing runs) and remember what
@@ -554,6 +583,47 @@ int replay_zero3(zero_ctx* c, const void* const* grads, const zero::AdamCoef& co
   c->gathers += c->graph_gathers;
   c->scatters += c->graph_scatters;
   touch(c, c->su);
+  return ZERO_OK;
+}
+
+// One step, clipped or (clip == nullptr) not.
+int run_step(zero_ctx* c, int scheme, int W, int64_t n, const void* const* grads, double lr, double beta1,
+             double beta2, double eps, int64_t t, const Clip* clip) {
+  if (c == nullptr) return fail(ZERO_E_ARG, "ctx is NULL");
+  if (scheme != c->scheme || W != c->W || n != c->L.n)
+    return fail(ZERO_E_ARG, "scheme/W/n (%d/%d/%lld) differ from the context's (%d/%d/%lld)", scheme, W,
+                (long long)n, c->scheme, c->W, (long long)c->L.n);
+  int rc = check_hyper(lr, beta1, beta2, eps, t);
+  if (rc) return rc;
+  if (t != c->t + 1)
+    return fail(ZERO_E_STATE, "step counter %lld does not follow %lld", (long long)t, (long long)c->t);
+  if ((rc = check_no_open_bucket_step(c))) return rc;
+  if ((rc = check_grads(c, grads)) || (rc = check_ranks_up(c))) return rc;
+  for (size_t u = 0; u < c->live.size(); ++u)
+    if (c->live[u]) return fail(ZERO_E_STATE, "unit %zu is still gathered by the caller", u);
+  const zero::AdamCoef coef = make_coef(lr, beta1, beta2, eps, t, W);
+  Range range("zero_step %lld", static_cast<long long>(t));
+  struct Clipping {
+    zero_ctx* c;
+    ~Clipping() { c->clip = nullptr; }
+  } clipping{c};
+  c->clip = clip;
+  if (c->scheme != ZERO_SCHEME_Z3) {
+    if (clip && (rc = launch_norm(c, grads))) return rc;
+    rc = launch_update(c, 0, grads, coef, c->su);
+    if (rc) return rc;
+    // all-reduce (DP) or reduce-scatter + all-gather (Z1/Z2): two collectives
+    count_scatter(c, 0);
+    c->gathers += 1;
+    c->comm += ring_bytes(c->W, c->L.shard[0]);
+  } else if (graph_applies(c)) {
+    if (!c->graph_exec && (rc = capture_zero3(c, grads, coef))) return rc;
+    if ((rc = replay_zero3(c, grads, coef))) return rc;
+  } else {
+    rc = run_zero3_step(c, grads, coef);
+    if (rc) return rc;
+  }
+  c->t = t;
   return ZERO_OK;
 }
 
@@ -757,36 +827,29 @@ int zero_refresh_working_copy(zero_ctx* c) {
 
 int zero_step(zero_ctx* c, int scheme, int W, int64_t n, const void* const* grads, double lr, double beta1,
               double beta2, double eps, int64_t t) {
+  return run_step(c, scheme, W, n, grads, lr, beta1, beta2, eps, t, nullptr);
+}
+
+int64_t zero_step_clipped_workspace_bytes(const zero_ctx* c) {
   if (c == nullptr) return fail(ZERO_E_ARG, "ctx is NULL");
-  if (scheme != c->scheme || W != c->W || n != c->L.n)
-    return fail(ZERO_E_ARG, "scheme/W/n (%d/%d/%lld) differ from the context's (%d/%d/%lld)", scheme, W,
-                (long long)n, c->scheme, c->W, (long long)c->L.n);
-  int rc = check_hyper(lr, beta1, beta2, eps, t);
-  if (rc) return rc;
-  if (t != c->t + 1)
-    return fail(ZERO_E_STATE, "step counter %lld does not follow %lld", (long long)t, (long long)c->t);
-  if ((rc = check_no_open_bucket_step(c))) return rc;
-  if ((rc = check_grads(c, grads)) || (rc = check_ranks_up(c))) return rc;
-  for (size_t u = 0; u < c->live.size(); ++u)
-    if (c->live[u]) return fail(ZERO_E_STATE, "unit %zu is still gathered by the caller", u);
-  const zero::AdamCoef coef = make_coef(lr, beta1, beta2, eps, t, W);
-  Range range("zero_step %lld", static_cast<long long>(t));
-  if (c->scheme != ZERO_SCHEME_Z3) {
-    rc = launch_update(c, 0, grads, coef, c->su);
-    if (rc) return rc;
-    // all-reduce (DP) or reduce-scatter + all-gather (Z1/Z2): two collectives
-    count_scatter(c, 0);
-    c->gathers += 1;
-    c->comm += ring_bytes(c->W, c->L.shard[0]);
-  } else if (graph_applies(c)) {
-    if (!c->graph_exec && (rc = capture_zero3(c, grads, coef))) return rc;
-    if ((rc = replay_zero3(c, grads, coef))) return rc;
-  } else {
-    rc = run_zero3_step(c, grads, coef);
-    if (rc) return rc;
-  }
-  c->t = t;
-  return ZERO_OK;
+  return zero::clip_workspace_bytes(c->L.n_pad);
+}
+
+int zero_step_clipped(zero_ctx* c, int scheme, int W, int64_t n, const void* const* grads, double lr, double beta1,
+                      double beta2, double eps, int64_t t, double max_norm, float* norm, void* workspace,
+                      int64_t workspace_bytes) {
+  if (c == nullptr) return fail(ZERO_E_ARG, "ctx is NULL");
+  const float limit = static_cast<float>(max_norm);
+  if (!(limit > 0) || !std::isfinite(limit))
+    return fail(ZERO_E_ARG, "max_norm %g is not a positive finite fp32 value", max_norm);
+  if (norm == nullptr || workspace == nullptr) return fail(ZERO_E_ARG, "norm and workspace are required");
+  if (reinterpret_cast<uintptr_t>(norm) % 4) return fail(ZERO_E_ALIGN, "norm must be 4-byte aligned");
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(ZERO_E_ALIGN, "workspace must be 256-byte aligned");
+  if (workspace_bytes < zero::clip_workspace_bytes(c->L.n_pad))
+    return fail(ZERO_E_ARG, "workspace of %lld bytes: %lld are needed", (long long)workspace_bytes,
+                (long long)zero::clip_workspace_bytes(c->L.n_pad));
+  const Clip clip = {workspace, norm, limit};
+  return run_step(c, scheme, W, n, grads, lr, beta1, beta2, eps, t, &clip);
 }
 
 int zero_set_unit_hook(zero_ctx* c, zero_unit_hook fn, void* user) {

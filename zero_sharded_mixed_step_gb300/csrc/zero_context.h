@@ -58,6 +58,13 @@ struct Layout {
   int64_t n = 0, n_pad = 0, shard_total = 0, unit_max = 0;
 };
 
+// The clipping of the step that is running (zero_step_clipped).
+struct Clip {
+  void* workspace;
+  float* norm;
+  float max_norm;
+};
+
 int make_layout(int W, int64_t n_units, const int64_t* sizes, Layout* L);
 
 // Bytes one rank sends in one ring reduce-scatter or all-gather of a unit
@@ -102,6 +109,7 @@ struct zero_ctx {
   bool err_slot_ready = false; // cleared on the device (at the first fused launch)
   int64_t dev_err_seen = 0;    // count at the last zero_sync
   int last_variant = 0;
+  const zero::host::Clip* clip = nullptr;   // set while a clipped step is being enqueued
   // a step being done bucket by bucket: the ranges covered so far (lo -> hi)
   int debug = 0;
   std::vector<void*> live_buf;          // where the caller gathered each live unit
