@@ -31,7 +31,7 @@ SOURCES = ["zero_api.cpp", "host_step.cpp", "bucket_step.cpp", "fused_step.cu", 
 # which would keep the loop from being vectorised.
 EXTRA_FLAGS = {"offload.cpp": ["-Xcompiler", "-ffp-contract=off", "-Xcompiler", "-fno-math-errno"]}
 HEADERS = [os.path.join(CSRC, "zero_internal.h"), os.path.join(CSRC, "zero_context.h"), os.path.join(CSRC, "step_math.cuh"),
-           os.path.join(CSRC, "umma.cuh"),
+           os.path.join(CSRC, "umma.cuh"), os.path.join(CSRC, "launch.cuh"),
            os.path.join(INCLUDE, "zero_step.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

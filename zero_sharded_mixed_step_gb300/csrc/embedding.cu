@@ -16,6 +16,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "launch.cuh"
 #include "step_math.cuh"
 #include "zero_context.h"
 #include "zero_internal.h"
@@ -36,27 +37,49 @@ __device__ __forceinline__ int load_id(const void* ids, int id_bytes, int64_t i,
 }
 
 // ---- the lookup -----------------------------------------------------------------
+//
+// A CTA takes some consecutive tokens whose ids it reads first, and then the
+// 16-byte words of their rows: each thread issues kLookupBatch loads before
+// the first store, so that the rows' latencies overlap.
 
 constexpr int kLookupThreads = 256;
+constexpr int kLookupBatch = 8;
+constexpr int kLookupRows = 256;      // most tokens of a CTA
 
 template <typename T>
 __global__ void __launch_bounds__(kLookupThreads) embed_lookup(const void* ids, int id_bytes, int tokens, int vocab,
-                                                               int width8, const T* table, int64_t table_stride,
-                                                               float scale, T* out, int64_t out_stride) {
-  const int64_t total = static_cast<int64_t>(tokens) * width8;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * kLookupThreads + threadIdx.x; e < total;
-       e += static_cast<int64_t>(gridDim.x) * kLookupThreads) {
-    const int64_t row = e / width8, c = (e - row * width8) * 8;
-    const int id = load_id(ids, id_bytes, row, vocab);
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (id < vocab) {
-      float f[8];
-      Fmt<T>::unpack8(dev::ld_16B(table + id * table_stride + c), f);
+                                                               int width8, unsigned int inv_width8, int rows,
+                                                               const T* table, int64_t table_stride, float scale, T* out,
+                                                               int64_t out_stride) {
+  __shared__ int id[kLookupRows];
+  const int first = blockIdx.x * rows, count = min(rows, tokens - first);
+  for (int r = threadIdx.x; r < count; r += kLookupThreads) id[r] = load_id(ids, id_bytes, first + r, vocab);
+  __syncthreads();
+  const int words = count * width8;
+  for (int j0 = threadIdx.x; j0 < words; j0 += kLookupThreads * kLookupBatch) {
+    uint4 x[kLookupBatch];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] *= scale;
-      x = Fmt<T>::pack8(f);
+    for (int u = 0; u < kLookupBatch; ++u) {
+      const int j = j0 + u * kLookupThreads;
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (j < words) {
+        // j / width8: exact, as j and width8 stay below 2^14 (see the host side)
+        const int r = width8 == 1 ? j : static_cast<int>(__umulhi(j, inv_width8));
+        if (id[r] < vocab) x[u] = dev::ld_16B(table + id[r] * table_stride + (j - r * width8) * 8);
+      }
     }
-    dev::st_16B(out + row * out_stride + c, x);
+#pragma unroll
+    for (int u = 0; u < kLookupBatch; ++u) {
+      const int j = j0 + u * kLookupThreads;
+      if (j < words) {
+        const int r = width8 == 1 ? j : static_cast<int>(__umulhi(j, inv_width8));
+        float f[8];
+        Fmt<T>::unpack8(x[u], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] *= scale;
+        dev::st_16B(out + (first + r) * out_stride + (j - r * width8) * 8, Fmt<T>::pack8(f));
+      }
+    }
   }
 }
 
@@ -73,20 +96,35 @@ constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kRadix = 256;
+constexpr int kSortBatch = 8;      // groups of 32 pairs whose loads a warp has in flight
 
 struct SortArgs {
   const void* ids;
   int id_bytes, tokens, vocab;
   int passes, bits;            // digits of `bits` bits (at most 8)
-  int* keys[2];                // after the last pass the sorted pairs are in [passes & 1]
-  int* vals[2];
+  int2* pairs[2];              // (id, position); sorted in pairs[passes & 1] after the last pass
+  int* runs;                   // a counter to set to 0 (RunArgs)
   char* fill;                  // rows to set to 0 (NULL: none)
   int64_t fill_stride;         // bytes
   int64_t fill_rows, row16;    // rows, and 16-byte words of a row
+  int64_t fill_words;          // of all the rows (the last one may be short)
 };
 
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The lanes whose `bits`-bit digit equals this lane's, one vote for each bit
+// (the match instruction takes time with every different value: it made a
+// pass over 32 unequal digits cost 2,500 cycles).  Lanes without a pair match
+// nobody's.
+__device__ __forceinline__ unsigned same_digit(int digit, bool real, int bits) {
+  unsigned same = __ballot_sync(0xffffffffu, real);
+  for (int b = 0; b < bits; ++b) {
+    const unsigned one = __ballot_sync(0xffffffffu, (digit >> b) & 1);
+    same &= (digit >> b) & 1 ? one : ~one;
+  }
+  return real ? same : 0u;
 }
 
 __device__ __forceinline__ int peer_load(const int* p, uint32_t rank) {
@@ -98,13 +136,14 @@ __device__ __forceinline__ int peer_load(const int* p, uint32_t rank) {
 }
 
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1) embed_sort(const SortArgs a) {
+  allow_next();
+  await_previous();
   const int tid = threadIdx.x;
   if (blockIdx.x >= kSortCtas) {
-    const int64_t total = a.fill_rows * a.row16;
-    for (int64_t e = static_cast<int64_t>(blockIdx.x - kSortCtas) * kSortThreads + tid; e < total;
-         e += static_cast<int64_t>(gridDim.x - kSortCtas) * kSortThreads) {
-      const int64_t row = e / a.row16;
-      dev::st_16B(a.fill + row * a.fill_stride + (e - row * a.row16) * 16, make_uint4(0, 0, 0, 0));
+    for (int64_t row = blockIdx.x - kSortCtas; row < a.fill_rows; row += gridDim.x - kSortCtas) {
+      char* p = a.fill + row * a.fill_stride;
+      const int64_t words = min(a.row16, a.fill_words - row * a.row16);
+      for (int64_t c = tid; c < words; c += kSortThreads) dev::st_16B(p + c * 16, make_uint4(0, 0, 0, 0));
     }
     return;
   }
@@ -120,22 +159,35 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
   const int g0 = static_cast<int>(static_cast<int64_t>(groups) * w / warps);
   const int g1 = static_cast<int>(static_cast<int64_t>(groups) * (w + 1) / warps);
   const int mask = (1 << a.bits) - 1;
+  if (blockIdx.x == 0 && tid == 0) *a.runs = 0;
   for (int p = 0; p < a.passes; ++p) {
     const int shift = p * a.bits;
-    const int* keys = a.keys[p & 1];
-    const int* vals = a.vals[p & 1];
-    int* keys_out = a.keys[(p & 1) ^ 1];
-    int* vals_out = a.vals[(p & 1) ^ 1];
-    auto key_at = [&](int i) { return p == 0 ? load_id(a.ids, a.id_bytes, i, a.vocab) : __ldcg(keys + i); };
+    const int2* in = a.pairs[p & 1];
+    int2* out = a.pairs[(p & 1) ^ 1];
+    // the pair at i; (-1, i) past the end
+    auto pair_at = [&](int i) {
+      if (i >= a.tokens) return make_int2(-1, i);
+      return p == 0 ? make_int2(load_id(a.ids, a.id_bytes, i, a.vocab), i) : __ldcg(in + i);
+    };
     for (int d = lane; d < kRadix; d += 32) count[warp][d] = 0;
     __syncwarp();
-    for (int g = g0; g < g1; ++g) {
-      const int i = g * 32 + lane;
-      if (i < a.tokens) atomicAdd(&count[warp][(key_at(i) >> shift) & mask], 1);
+    for (int g = g0; g < g1; g += kSortBatch) {
+      int2 x[kSortBatch];
+#pragma unroll
+      for (int u = 0; u < kSortBatch; ++u) x[u] = g + u < g1 ? pair_at((g + u) * 32 + lane) : make_int2(-1, 0);
+#pragma unroll
+      for (int u = 0; u < kSortBatch; ++u) {
+        if (g + u >= g1) break;
+        const int d = (x[u].x >> shift) & mask;
+        const unsigned same = same_digit(d, x[u].x >= 0, a.bits);
+        if (same && (same & ((1u << lane) - 1)) == 0) count[warp][d] += __popc(same);
+        __syncwarp();
+      }
     }
     __syncthreads();
     if (tid < kRadix) {
       int sum = 0;
+#pragma unroll
       for (int k = 0; k < kSortWarps; ++k) {
         const int c = count[k][tid];
         count[k][tid] = sum;
@@ -170,22 +222,23 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     __syncthreads();
     for (int d = lane; d < kRadix; d += 32) count[warp][d] += digit_base[d];
     __syncwarp();
-    for (int g = g0; g < g1; ++g) {
-      const int i = g * 32 + lane;
-      const bool in = i < a.tokens;
-      const int key = in ? key_at(i) : 0;
-      // the lanes past the end form a group of their own
-      const int d = in ? (key >> shift) & mask : kRadix;
-      const unsigned same = __match_any_sync(0xffffffffu, d);
-      const int ahead = __popc(same & ((1u << lane) - 1));
-      int at = 0;
-      if (in) at = count[warp][d] + ahead;
-      __syncwarp();
-      if (in && ahead == 0) count[warp][d] += __popc(same);
-      __syncwarp();
-      if (in) {
-        __stcg(keys_out + at, key);
-        __stcg(vals_out + at, p == 0 ? i : __ldcg(vals + i));
+    for (int g = g0; g < g1; g += kSortBatch) {
+      int2 x[kSortBatch];
+#pragma unroll
+      for (int u = 0; u < kSortBatch; ++u) x[u] = g + u < g1 ? pair_at((g + u) * 32 + lane) : make_int2(-1, 0);
+#pragma unroll
+      for (int u = 0; u < kSortBatch; ++u) {
+        if (g + u >= g1) break;
+        const bool real = x[u].x >= 0;
+        const int d = (x[u].x >> shift) & mask;
+        const unsigned same = same_digit(d, real, a.bits);
+        const int ahead = __popc(same & ((1u << lane) - 1));
+        int at = 0;
+        if (real) at = count[warp][d] + ahead;
+        __syncwarp();
+        if (real && ahead == 0) count[warp][d] += __popc(same);
+        __syncwarp();
+        if (real) __stcg(out + at, x[u]);
       }
     }
     // the pairs of this pass, and everyone's reads of cta_count, before the next pass
@@ -195,48 +248,54 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
 
 // ---- summing the runs ---------------------------------------------------------------
 //
-// One CTA per chunk of kChunk sorted pairs, a thread per 8 columns.  Runs that
-// lie inside the chunk are written at once; the part of a run that goes on
-// from the chunk before (head) or into the chunk after (tail) is left in
-// workspace in fp32, and embed_join adds those parts in order.
+// One CTA per chunk of sorted pairs, a thread per 8 columns.  Runs that lie
+// inside the chunk are written at once; the part of a run that goes on from
+// the chunk before (head) or into the chunk after (tail) is left in workspace
+// in fp32, the run is noted, and embed_join adds its parts in order.
 
-constexpr int kMaxChunk = 64;
+constexpr int kMinChunk = 8, kMaxChunk = 64;
+constexpr int kRunBatch = 8;          // rows whose loads a thread has in flight
 
 struct RunArgs {
-  const int* keys;
-  const int* vals;
+  const int2* pairs;
   int tokens, vocab, width8, chunk, chunks;
   const void* dout;
   int64_t dout_stride;
   void* dtable;
   int64_t dtable_stride;
   float* parts;                // [chunk][head, tail][width]
+  int* runs;                   // how many runs go past their chunk, and after it the chunks where they begin
   float scale;
-  int add;
 };
 
-template <typename T>
-__device__ __forceinline__ void write_row(const RunArgs& a, int id, int64_t c, float (&sum)[8]) {
-  if (id >= a.vocab) return;   // pairs without a row of the table
-  T* out = static_cast<T*>(a.dtable) + id * a.dtable_stride + c;
-  float old[8];
-  if (a.add) Fmt<T>::unpack8(dev::ld_16B(out), old);
+// scale * sum (+ the old row) to a row of the table's gradient.
+template <typename T, bool ADD>
+__device__ __forceinline__ void write_row(const RunArgs& a, int id, int64_t c, float (&sum)[8], const uint4& old) {
+  float f[8];
+  if (ADD) Fmt<T>::unpack8(old, f);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) sum[k] = a.add ? fmaf(sum[k], a.scale, old[k]) : sum[k] * a.scale;
-  dev::st_16B(out, Fmt<T>::pack8(sum));
+  for (int k = 0; k < 8; ++k) sum[k] = ADD ? fmaf(sum[k], a.scale, f[k]) : sum[k] * a.scale;
+  dev::st_16B(static_cast<T*>(a.dtable) + id * a.dtable_stride + c, Fmt<T>::pack8(sum));
 }
 
-template <typename T>
+template <typename T, bool ADD>
 __global__ void __launch_bounds__(256) embed_runs(const RunArgs a) {
+  allow_next();
+  await_previous();
   __shared__ int key[kMaxChunk + 2];   // the chunk's, with one before and one after (-1: none)
   __shared__ int val[kMaxChunk];
   const int first = blockIdx.x * a.chunk, count = min(a.chunk, a.tokens - first);
   for (int k = threadIdx.x; k < count + 2; k += blockDim.x) {
     const int i = first + k - 1;
-    key[k] = i >= 0 && i < a.tokens ? a.keys[i] : -1;
-    if (k >= 1 && k <= count) val[k - 1] = a.vals[i];
+    const int2 x = i >= 0 && i < a.tokens ? a.pairs[i] : make_int2(-1, 0);
+    key[k] = x.x;
+    if (k >= 1 && k <= count) val[k - 1] = x.y;
   }
   __syncthreads();
+  const int last_key = key[count];
+  // begins here and goes on: the last key continues, and its run did not come from before
+  if (threadIdx.x == 0 && last_key < a.vocab && key[count + 1] == last_key && key[0] != last_key)
+    a.runs[1 + atomicAdd(a.runs, 1)] = blockIdx.x;
   const T* dout = static_cast<const T*>(a.dout);
   const int64_t width = static_cast<int64_t>(a.width8) * 8;
   float* head = a.parts + static_cast<int64_t>(blockIdx.x) * 2 * width;
@@ -246,25 +305,31 @@ __global__ void __launch_bounds__(256) embed_runs(const RunArgs a) {
     bool from_before = key[1] == key[0];   // the run that is being summed began in an earlier chunk
 #pragma unroll
     for (int q = 0; q < 8; ++q) sum[q] = 0.f;
-    for (int k0 = 0; k0 < count; k0 += 8) {
-      uint4 x[8];
+    for (int k0 = 0; k0 < count; k0 += kRunBatch) {
+      uint4 x[kRunBatch], old[ADD ? kRunBatch : 1];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k0 + k < count && key[k0 + k + 1] < a.vocab) x[k] = dev::ld_16B(dout + val[k0 + k] * a.dout_stride + c);
-        else x[k] = make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < kRunBatch; ++k) {
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (ADD) old[k] = x[k];
+        if (k0 + k < count && key[k0 + k + 1] < a.vocab) {
+          x[k] = dev::ld_16B(dout + val[k0 + k] * a.dout_stride + c);
+          if (ADD && key[k0 + k + 2] != key[k0 + k + 1])
+            old[k] = dev::ld_16B(static_cast<const T*>(a.dtable) + key[k0 + k + 1] * a.dtable_stride + c);
+        }
+      }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < kRunBatch; ++k) {
         if (k0 + k >= count) break;
         float f[8];
         Fmt<T>::unpack8(x[k], f);
 #pragma unroll
         for (int q = 0; q < 8; ++q) sum[q] += f[q];
         const int id = key[k0 + k + 1];
-        const bool last = k0 + k == count - 1;
-        if (last || key[k0 + k + 2] != id) {
+        const bool goes_on = key[k0 + k + 2] == id;
+        if (k0 + k == count - 1 || !goes_on) {
           if (from_before) dev::st_32B(head + c, sum);
-          else if (last && key[k0 + k + 2] == id) dev::st_32B(head + width + c, sum);
-          else write_row<T>(a, id, c, sum);
+          else if (goes_on) dev::st_32B(head + width + c, sum);
+          else if (id < a.vocab) write_row<T, ADD>(a, id, c, sum, old[ADD ? k : 0]);
           from_before = false;
 #pragma unroll
           for (int q = 0; q < 8; ++q) sum[q] = 0.f;
@@ -274,33 +339,72 @@ __global__ void __launch_bounds__(256) embed_runs(const RunArgs a) {
   }
 }
 
-// The runs that begin in chunk blockIdx.x and go on past its end.
-template <typename T>
-__global__ void __launch_bounds__(256) embed_join(const RunArgs a) {
-  const int b = blockIdx.x, end = (b + 1) * a.chunk;
-  if (end >= a.tokens) return;
-  const int id = a.keys[end - 1];
-  if (id >= a.vocab || a.keys[end] != id) return;
-  if (b > 0 && a.keys[b * a.chunk - 1] == id) return;   // began earlier
+// The runs that go past the chunk they begin in.  An item is one run and 256
+// columns; kJoinSlices groups of 32 threads each add a stretch of the run's
+// parts, and the first adds the stretches, in order.
+constexpr int kJoinSlices = 8;
+constexpr int kJoinThreads = 32 * kJoinSlices;
+
+template <typename T, bool ADD>
+__global__ void __launch_bounds__(kJoinThreads) embed_join(const RunArgs a) {
+  allow_next();
+  await_previous();
+  __shared__ float stretch[kJoinSlices][32][9];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int blocks = (a.width8 + 31) / 32, items = a.runs[0] * blocks;
   const int64_t width = static_cast<int64_t>(a.width8) * 8;
-  for (int c8 = threadIdx.x; c8 < a.width8; c8 += blockDim.x) {
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int b = a.runs[1 + item / blocks], c8 = item % blocks * 32 + lane;
     const int64_t c = static_cast<int64_t>(c8) * 8;
-    float sum[8];
-    dev::ld_32B(a.parts + (2 * static_cast<int64_t>(b) + 1) * width + c, sum);
-    for (int j = b + 1; j < a.chunks && a.keys[j * a.chunk] == id; ++j) {
-      float x[8];
-      dev::ld_32B(a.parts + 2 * static_cast<int64_t>(j) * width + c, x);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) sum[q] += x[q];
+    const int id = a.pairs[(b + 1) * a.chunk - 1].x;
+    // how many chunks after b the run reaches into: those that begin with its id
+    int more = 0;
+    for (;;) {
+      const int64_t at = (static_cast<int64_t>(b) + 1 + more + threadIdx.x) * a.chunk;
+      const int n = __syncthreads_count(at < a.tokens && a.pairs[at].x == id);
+      more += n;
+      if (n < kJoinThreads) break;
     }
-    write_row<T>(a, id, c, sum);
+    // parts 0..more: the tail of b, then the heads of the chunks after it
+    const int p0 = (more + 1) * slice / kJoinSlices, p1 = (more + 1) * (slice + 1) / kJoinSlices;
+    float sum[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum[q] = 0.f;
+    if (c8 < a.width8) {
+#pragma unroll 8
+      for (int p = p0; p < p1; ++p) {
+        float x[8];
+        dev::ld_32B(a.parts + (2 * (static_cast<int64_t>(b) + p) + (p == 0 ? 1 : 0)) * width + c, x);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum[q] += x[q];
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) stretch[slice][lane][q] = sum[q];
+    __syncthreads();
+    if (slice == 0 && c8 < a.width8) {
+      uint4 old = make_uint4(0, 0, 0, 0);
+      if (ADD) old = dev::ld_16B(static_cast<const T*>(a.dtable) + id * a.dtable_stride + c);
+      for (int k = 1; k < kJoinSlices; ++k)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum[q] += stretch[k][lane][q];
+      write_row<T, ADD>(a, id, c, sum, old);
+    }
+    __syncthreads();
   }
 }
 
 // ---- host -----------------------------------------------------------------------------
 
 constexpr int64_t kMaxTokens = int64_t(1) << 24, kMaxVocab = int64_t(1) << 24, kMaxWidth = int64_t(1) << 16;
-constexpr int kChunk = 16;
+
+// Sorted pairs per chunk: 600 to 1200 chunks where the tokens allow it (4 to 8
+// CTAs for each SM), a power of two.
+int chunk_of(int64_t tokens) {
+  int c = kMinChunk;
+  while (c < kMaxChunk && tokens / (2 * c) >= 608) c *= 2;
+  return c;
+}
 
 int check_ids(int64_t tokens, int64_t vocab, int64_t width, int dtype, const void* ids, int id_bytes) {
   if (tokens < 0 || tokens > kMaxTokens) return fail(ZERO_E_ARG, "tokens=%lld outside [0, 2^24]", (long long)tokens);
@@ -327,32 +431,42 @@ int check_scale(double scale) {
   return ZERO_OK;
 }
 
-int64_t pairs_bytes(int64_t tokens) { return round_up(tokens * 4, 256); }
+int64_t pairs_bytes(int64_t tokens) { return round_up(tokens * 8, 256); }
+
+// Most chunks that any count up to `tokens` is cut into.
+int64_t most_chunks(int64_t tokens) {
+  return std::min(ceil_div(tokens, kMinChunk), std::max<int64_t>(1217, ceil_div(tokens, kMaxChunk)));
+}
+
+int64_t runs_bytes(int64_t tokens) { return round_up((most_chunks(tokens) + 1) * 4, 256); }
 
 int64_t space(int64_t tokens, int64_t width) {
-  return std::max<int64_t>(256, 4 * pairs_bytes(tokens) + round_up(ceil_div(tokens, kChunk) * 2 * width * 4, 256));
+  return std::max<int64_t>(256, 2 * pairs_bytes(tokens) + runs_bytes(tokens) + round_up(most_chunks(tokens) * 2 * width * 4, 256));
 }
 
 template <typename T>
 int lookup(int64_t tokens, int64_t vocab, int64_t width, const void* ids, int id_bytes, const void* table,
            int64_t table_stride, float scale, void* out, int64_t out_stride, cudaStream_t s) {
-  const int64_t items = tokens * (width / 8);
-  const int64_t blocks = std::min<int64_t>(ceil_div(items, kLookupThreads), static_cast<int64_t>(sm_count()) * 8);
-  embed_lookup<T><<<static_cast<unsigned>(blocks), kLookupThreads, 0, s>>>(
-      ids, id_bytes, static_cast<int>(tokens), static_cast<int>(vocab), static_cast<int>(width / 8),
-      static_cast<const T*>(table), table_stride, scale, static_cast<T*>(out), out_stride);
+  const int64_t width8 = width / 8;
+  // one batch of every thread per CTA, and fewer rows while there are SMs without work
+  const int64_t full = std::max<int64_t>(1, kLookupThreads * kLookupBatch / width8);
+  const int64_t rows = std::max<int64_t>(1, std::min<int64_t>({full, kLookupRows, ceil_div(tokens, 2 * sm_count())}));
+  const unsigned inv = width8 == 1 ? 0 : static_cast<unsigned>((uint64_t(1) << 32) / width8 + 1);
+  embed_lookup<T><<<static_cast<unsigned>(ceil_div(tokens, rows)), kLookupThreads, 0, s>>>(
+      ids, id_bytes, static_cast<int>(tokens), static_cast<int>(vocab), static_cast<int>(width8), inv,
+      static_cast<int>(rows), static_cast<const T*>(table), table_stride, scale, static_cast<T*>(out), out_stride);
   ZERO_CUDA(cudaGetLastError());
   return ZERO_OK;
 }
 
-template <typename T>
+template <typename T, bool ADD>
 int sum_runs(const RunArgs& a, cudaStream_t s) {
   const int threads = static_cast<int>(std::min<int64_t>(256, round_up(a.width8, 32)));
-  embed_runs<T><<<a.chunks, threads, 0, s>>>(a);
-  ZERO_CUDA(cudaGetLastError());
+  ZERO_CUDA(launch_chained(embed_runs<T, ADD>, dim3(a.chunks), threads, 0, s, a));
   if (a.chunks > 1) {
-    embed_join<T><<<a.chunks - 1, threads, 0, s>>>(a);
-    ZERO_CUDA(cudaGetLastError());
+    const int64_t most = static_cast<int64_t>(a.chunks - 1) * ceil_div(a.width8, 32);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(8 * sm_count(), most)));
+    ZERO_CUDA(launch_chained(embed_join<T, ADD>, grid, kJoinThreads, 0, s, a));
   }
   return ZERO_OK;
 }
@@ -413,35 +527,40 @@ extern "C" int zero_embedding_grad(int64_t tokens, int64_t vocab, int64_t width,
   while ((int64_t(1) << key_bits) <= vocab) ++key_bits;
   sa.passes = (key_bits + 7) / 8;
   sa.bits = (key_bits + sa.passes - 1) / sa.passes;
-  for (int k = 0; k < 2; ++k) {
-    sa.keys[k] = reinterpret_cast<int*>(ws + k * pb);
-    sa.vals[k] = reinterpret_cast<int*>(ws + (2 + k) * pb);
-  }
+  for (int k = 0; k < 2; ++k) sa.pairs[k] = reinterpret_cast<int2*>(ws + k * pb);
+  sa.runs = reinterpret_cast<int*>(ws + 2 * pb);
   unsigned grid = kSortCtas;
   if (!accumulate) {
     sa.fill = static_cast<char*>(dtable);
-    sa.fill_stride = dtable_stride * 2;
-    sa.fill_rows = vocab;
-    sa.row16 = width / 8;
-    const int64_t want = ceil_div(ceil_div(vocab * sa.row16, kSortThreads), kSortCtas);
-    grid += kSortCtas * static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(sm_count() / kSortCtas - 1, want)));
+    if (dtable_stride == width) {   // one stretch, in rows of 64 KB
+      sa.fill_words = vocab * (width / 8);
+      sa.row16 = 4096;
+      sa.fill_rows = ceil_div(sa.fill_words, sa.row16);
+      sa.fill_stride = sa.row16 * 16;
+    } else {
+      sa.row16 = width / 8;
+      sa.fill_rows = vocab;
+      sa.fill_words = vocab * sa.row16;
+      sa.fill_stride = dtable_stride * 2;
+    }
+    const int64_t clusters = std::min<int64_t>(sm_count() / kSortCtas - 1, ceil_div(sa.fill_rows, kSortCtas));
+    grid += kSortCtas * static_cast<unsigned>(std::max<int64_t>(1, clusters));
   }
-  embed_sort<<<grid, kSortThreads, 0, s>>>(sa);
-  ZERO_CUDA(cudaGetLastError());
+  ZERO_CUDA(launch_chained(embed_sort, dim3(grid), kSortThreads, 0, s, sa));
   RunArgs ra{};
-  ra.keys = sa.keys[sa.passes & 1];
-  ra.vals = sa.vals[sa.passes & 1];
+  ra.pairs = sa.pairs[sa.passes & 1];
   ra.tokens = sa.tokens;
   ra.vocab = sa.vocab;
   ra.width8 = static_cast<int>(width / 8);
-  ra.chunk = kChunk;
-  ra.chunks = static_cast<int>(ceil_div(tokens, kChunk));
+  ra.chunk = chunk_of(tokens);
+  ra.chunks = static_cast<int>(ceil_div(tokens, ra.chunk));
   ra.dout = dout;
   ra.dout_stride = dout_stride;
   ra.dtable = dtable;
   ra.dtable_stride = dtable_stride;
-  ra.parts = reinterpret_cast<float*>(ws + 4 * pb);
+  ra.runs = sa.runs;
+  ra.parts = reinterpret_cast<float*>(ws + 2 * pb + runs_bytes(tokens));
   ra.scale = static_cast<float>(scale);
-  ra.add = accumulate != 0;
-  return dtype == ZERO_FP16 ? sum_runs<__half>(ra, s) : sum_runs<__nv_bfloat16>(ra, s);
+  if (accumulate) return dtype == ZERO_FP16 ? sum_runs<__half, true>(ra, s) : sum_runs<__nv_bfloat16, true>(ra, s);
+  return dtype == ZERO_FP16 ? sum_runs<__half, false>(ra, s) : sum_runs<__nv_bfloat16, false>(ra, s);
 }

@@ -22,6 +22,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "launch.cuh"
 #include "step_math.cuh"
 #include "zero_context.h"
 #include "zero_internal.h"
@@ -52,10 +53,12 @@ NormSpace norm_space(void* ws) {
 
 // ---- element types -------------------------------------------------------------
 
-// 8 consecutive elements of T as floats; aligned: the address allows the wide load.
+// 8 consecutive elements of T, read and written in one access, as floats.
 template <typename T>
 struct Eight {
-  static __device__ __forceinline__ void load(const T* p, float (&f)[8]) { Fmt<T>::unpack8(ld_16B(p), f); }
+  using Raw = uint4;
+  static __device__ __forceinline__ Raw raw(const T* p) { return ld_16B(p); }
+  static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[8]) { Fmt<T>::unpack8(r, f); }
   static __device__ __forceinline__ void store(T* p, const float (&f)[8]) { st_16B(p, Fmt<T>::pack8(f)); }
   static __device__ __forceinline__ float load1(const T* p) { return Fmt<T>::load1(p, 0); }
   static __device__ __forceinline__ void store1(T* p, float x) { Fmt<T>::store1(p, 0, x); }
@@ -63,7 +66,18 @@ struct Eight {
 
 template <>
 struct Eight<float> {
-  static __device__ __forceinline__ void load(const float* p, float (&f)[8]) { ld_32B(p, f); }
+  struct Raw {
+    float f[8];
+  };
+  static __device__ __forceinline__ Raw raw(const float* p) {
+    Raw r;
+    ld_32B(p, r.f);
+    return r;
+  }
+  static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = r.f[k];
+  }
   static __device__ __forceinline__ void store(float* p, const float (&f)[8]) { st_32B(p, f); }
   static __device__ __forceinline__ float load1(const float* p) { return *p; }
   static __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
@@ -135,41 +149,96 @@ struct Table {
   }
 };
 
-// The mean over the ranks of 8 elements, or of one.
-template <typename T>
-__device__ __forceinline__ void mean8(const int64_t* ranks, int64_t i, int W, bool pow2, float inv_w, float (&g)[8]) {
-  Eight<T>::load(reinterpret_cast<const T*>(ranks[0]) + i, g);
-  for (int w = 1; w < W; ++w) {
-    float f[8];
-    Eight<T>::load(reinterpret_cast<const T*>(ranks[w]) + i, f);
+// 8 elements of every rank at element i, summed in rank order in fp32.  WC > 0:
+// W known at compile time, all its loads in flight at once; WC == 0: any W,
+// 8 ranks at a time.  `rank` gives rank w's vector.
+template <typename T, int WC, typename F>
+__device__ __forceinline__ void sum_ranks8(F rank, int64_t i, int W, float (&sum)[8]) {
+  constexpr int kAtOnce = WC > 0 ? WC : 8;
+  for (int w0 = 0; w0 < (WC > 0 ? 1 : W); w0 += kAtOnce) {
+    typename Eight<T>::Raw raw[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) g[k] = __fadd_rn(g[k], f[k]);
+    for (int w = 0; w < kAtOnce; ++w)
+      if (WC > 0 || w0 + w < W) raw[w] = Eight<T>::raw(rank(w0 + w) + i);
+#pragma unroll
+    for (int w = 0; w < kAtOnce; ++w) {
+      if (WC == 0 && w0 + w >= W) break;
+      float f[8];
+      Eight<T>::unpack(raw[w], f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] = w0 + w == 0 ? f[k] : __fadd_rn(sum[k], f[k]);
+    }
   }
-#pragma unroll
-  for (int k = 0; k < 8; ++k) g[k] = rank_mean(g[k], W, inv_w, pow2);
 }
 
-template <typename T>
-__device__ __forceinline__ float mean1(const int64_t* ranks, int64_t i, int W, bool pow2, float inv_w) {
-  float g = Eight<T>::load1(reinterpret_cast<const T*>(ranks[0]) + i);
-  for (int w = 1; w < W; ++w) g = __fadd_rn(g, Eight<T>::load1(reinterpret_cast<const T*>(ranks[w]) + i));
+template <typename T, typename F>
+__device__ __forceinline__ float mean1(F rank, int64_t i, int W, bool pow2, float inv_w) {
+  float g = Eight<T>::load1(rank(0) + i);
+  for (int w = 1; w < W; ++w) g = __fadd_rn(g, Eight<T>::load1(rank(w) + i));
   return rank_mean(g, W, inv_w, pow2);
 }
 
-template <typename T, bool CLIP>
+// The warp's 32 x 8 values v, lane after lane, to out, which lies `shift`
+// elements (1..7) before a boundary of 8: every lane but the last stores one
+// whole group made of its own tail and the next lane's head; the first
+// lane's head and the last lane's tail go element by element.
+template <typename T>
+__device__ __forceinline__ void store_shifted(T* out, int shift, const float (&v)[8], int lane) {
+  float x[16];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    x[k] = v[k];
+    x[8 + k] = __shfl_down_sync(0xffffffffu, v[k], 1);
+  }
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+      if (k < shift) Eight<T>::store1(out + k, v[k]);
+  }
+  if (lane == 31) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k)
+      if (k >= shift) Eight<T>::store1(out + k, v[k]);
+  }
+  // x moved down by `shift` places, one bit of it at a time
+#pragma unroll
+  for (int bit = 1; bit < 8; bit *= 2) {
+    if (shift & bit) {
+#pragma unroll
+      for (int k = 0; k + bit < 16; ++k) x[k] = x[k + bit];
+    }
+  }
+  if (lane < 31) {
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = x[k];
+    Eight<T>::store(out + shift, y);
+  }
+}
+
+// One pass over a table's tensors: the sum of squares of the mean (CLIP
+// false), or the clipped mean (CLIP true).  Tensors whose W gradients lie
+// alike relative to a group of 8 elements are read a group at a time; the
+// output may lie anywhere.  The clipping pass walks the chunks backwards:
+// what the norm's pass read last is what L2 still holds.
+template <typename T, int WC, bool CLIP>
 __global__ void __launch_bounds__(kThreads) tensors_pass(const __grid_constant__ Table t, NormSpace ws,
                                                          unsigned int first, unsigned int blocks, float* norm,
                                                          float max_norm) {
-  const int W = t.W;
+  allow_next();
+  await_previous();
+  const int W = WC > 0 ? WC : t.W;
   const bool pow2 = (W & (W - 1)) == 0;
   const float inv_w = 1.f / W;
+  const int lane = threadIdx.x & 31;
   float coef = 1.f;
   if (CLIP) {
     const float n = *norm;
     coef = isfinite(n) ? clip_coef(n, max_norm) : 1.f;
   }
   float squares = 0.f;
-  for (unsigned int chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
+  for (unsigned int at = blockIdx.x; at < t.chunks; at += gridDim.x) {
+    const unsigned int chunk = CLIP ? t.chunks - 1 - at : at;
     // the last tensor that starts at or before this chunk
     int lo = 0, hi = t.tensors - 1;
     while (lo < hi) {
@@ -180,27 +249,46 @@ __global__ void __launch_bounds__(kThreads) tensors_pass(const __grid_constant__
     const int64_t* row = t.row(lo);
     const int64_t numel = row[0], begin = static_cast<int64_t>(chunk - t.starts()[lo]) * kChunk;
     const int64_t end = min(numel, begin + kChunk);
-    const int64_t* ranks = row + 1;
-    int64_t bits = 0;
-    for (int w = 0; w < W + CLIP; ++w) bits |= ranks[w];
-    T* out = CLIP ? reinterpret_cast<T*>(ranks[W]) : nullptr;
-    const bool wide = (bits & (8 * sizeof(T) - 1)) == 0;
-    const int64_t vec_end = wide ? begin + (end - begin) / 8 * 8 : begin;
-    for (int64_t i = begin + threadIdx.x * 8; i < vec_end; i += kThreads * 8) {
+    auto rank = [&](int w) { return reinterpret_cast<const T*>(row[1 + w]); };
+    T* out = CLIP ? reinterpret_cast<T*>(row[1 + W]) : nullptr;
+    // elements from a pointer to the next boundary of 8 elements
+    auto to_boundary = [](int64_t p) { return static_cast<int>((-p & (8 * static_cast<int64_t>(sizeof(T)) - 1)) / sizeof(T)); };
+    const int head = to_boundary(row[1]);
+    bool alike = true;
+    for (int w = 1; w < W; ++w) alike = alike && to_boundary(row[1 + w]) == head;
+    int64_t v0 = min(begin + head, end), v1 = v0;       // [v0, v1): whole groups of 8
+    if (alike) v1 = v0 + (end - v0) / 8 * 8;
+    const int shift = CLIP ? to_boundary(row[1 + W] + v0 * static_cast<int64_t>(sizeof(T))) : 0;
+    // whole warps of groups, then the groups left over
+    const int64_t vw = v0 + (v1 - v0) / 256 * 256;
+    for (int64_t i = v0 + threadIdx.x * 8; i < v1; i += kThreads * 8) {
       float g[8];
-      mean8<T>(ranks, i, W, pow2, inv_w, g);
+      sum_ranks8<T, WC>(rank, i, W, g);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
+        g[k] = rank_mean(g[k], W, inv_w, pow2);
         if (CLIP) g[k] *= coef;
         else squares = fmaf(g[k], g[k], squares);
       }
-      if (CLIP) Eight<T>::store(out + i, g);
+      if (CLIP) {
+        if (shift == 0) {
+          Eight<T>::store(out + i, g);
+        } else if (i - lane * 8 < vw) {
+          store_shifted<T>(out + i, shift, g, lane);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) Eight<T>::store1(out + i + k, g[k]);
+        }
+      }
     }
-    for (int64_t i = vec_end + threadIdx.x; i < end; i += kThreads) {
-      const float g = mean1<T>(ranks, i, W, pow2, inv_w);
+    // what is left: the head (or everything, where the gradients lie unlike) and the tail
+    auto one = [&](int64_t i) {
+      const float g = mean1<T>(rank, i, W, pow2, inv_w);
       if (CLIP) Eight<T>::store1(out + i, g * coef);
       else squares = fmaf(g, g, squares);
-    }
+    };
+    for (int64_t i = begin + threadIdx.x; i < v0; i += kThreads) one(i);
+    for (int64_t i = v1 + threadIdx.x; i < end; i += kThreads) one(i);
   }
   if (!CLIP) finish_sum(squares, ws, first, blocks, norm);
 }
@@ -219,36 +307,18 @@ struct MeanNormArgs {
 
 template <typename GT, int WC>
 __global__ void __launch_bounds__(kThreads) mean_norm_pass(const __grid_constant__ MeanNormArgs a) {
+  allow_next();
+  await_previous();
   const int W = WC > 0 ? WC : a.W;
   const bool pow2 = (W & (W - 1)) == 0;
+  auto rank = [&](int w) { return static_cast<const GT*>(a.grads[w]); };
   float squares = 0.f;
   const int64_t groups = a.n >> 3;
   for (int64_t gi = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; gi < groups;
        gi += static_cast<int64_t>(gridDim.x) * kThreads) {
     const int64_t i = gi << 3;
     float sum[8];
-    if constexpr (WC > 0) {
-      uint4 raw[WC];
-#pragma unroll
-      for (int w = 0; w < WC; ++w) raw[w] = ld_16B(static_cast<const GT*>(a.grads[w]) + i);
-      Fmt<GT>::unpack8(raw[0], sum);
-#pragma unroll
-      for (int w = 1; w < WC; ++w) {
-        float f[8];
-        Fmt<GT>::unpack8(raw[w], f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum[k] = __fadd_rn(sum[k], f[k]);
-      }
-    } else {
-      Fmt<GT>::unpack8(ld_16B(static_cast<const GT*>(a.grads[0]) + i), sum);
-#pragma unroll 4
-      for (int w = 1; w < W; ++w) {
-        float f[8];
-        Fmt<GT>::unpack8(ld_16B(static_cast<const GT*>(a.grads[w]) + i), f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum[k] = __fadd_rn(sum[k], f[k]);
-      }
-    }
+    sum_ranks8<GT, WC>(rank, i, W, sum);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       sum[k] = rank_mean(sum[k], W, a.inv_w, pow2);
@@ -258,9 +328,7 @@ __global__ void __launch_bounds__(kThreads) mean_norm_pass(const __grid_constant
   }
   if (blockIdx.x == 0) {
     for (int64_t e = (groups << 3) + threadIdx.x; e < a.n; e += kThreads) {
-      float g = Fmt<GT>::load1(a.grads[0], e);
-      for (int w = 1; w < W; ++w) g = __fadd_rn(g, Fmt<GT>::load1(a.grads[w], e));
-      g = rank_mean(g, W, a.inv_w, pow2);
+      const float g = mean1<GT>(rank, e, W, pow2, a.inv_w);
       a.mean[e] = g;
       squares = fmaf(g, g, squares);
     }
@@ -284,6 +352,8 @@ struct ClippedArgs {
 // the state as it was.
 template <typename OT>
 __global__ void __launch_bounds__(kThreads) clipped_update(const __grid_constant__ ClippedArgs a) {
+  allow_next();
+  await_previous();
   const Seg& seg = a.segs[blockIdx.y];
   const float norm = *a.norm;
   const bool update = isfinite(norm);
@@ -436,14 +506,23 @@ int check_norm_args(const float* norm, const void* workspace, int64_t workspace_
   return ZERO_OK;
 }
 
+using TensorsFn = void (*)(const Table, NormSpace, unsigned int, unsigned int, float*, float);
+
+template <typename T, bool CLIP>
+TensorsFn pick_tensors_w(int W) {
+  switch (W) {
+    case 1: return tensors_pass<T, 1, CLIP>;
+    case 2: return tensors_pass<T, 2, CLIP>;
+    case 4: return tensors_pass<T, 4, CLIP>;
+    case 8: return tensors_pass<T, 8, CLIP>;
+    default: return tensors_pass<T, 0, CLIP>;
+  }
+}
+
 template <bool CLIP>
-void launch_tensors(const Table& t, int dtype, unsigned blocks, const NormSpace& ws, unsigned first, float* norm,
-                    float max_norm, cudaStream_t s) {
-  const unsigned all = first + blocks;
-  if (dtype == ZERO_FP16) tensors_pass<__half, CLIP><<<blocks, kThreads, 0, s>>>(t, ws, first, all, norm, max_norm);
-  else if (dtype == ZERO_BF16)
-    tensors_pass<__nv_bfloat16, CLIP><<<blocks, kThreads, 0, s>>>(t, ws, first, all, norm, max_norm);
-  else tensors_pass<float, CLIP><<<blocks, kThreads, 0, s>>>(t, ws, first, all, norm, max_norm);
+TensorsFn pick_tensors(int dtype, int W) {
+  if (dtype == ZERO_FP16) return pick_tensors_w<__half, CLIP>(W);
+  return dtype == ZERO_BF16 ? pick_tensors_w<__nv_bfloat16, CLIP>(W) : pick_tensors_w<float, CLIP>(W);
 }
 
 }  // namespace
@@ -464,9 +543,10 @@ cudaError_t launch_mean_norm(int W, int grad_dtype, const void* const* grads, in
   a.ws = norm_space(workspace);
   a.norm = norm;
   const MeanNormFn fn = grad_dtype == kF16 ? pick_mean_norm<__half>(W) : pick_mean_norm<__nv_bfloat16>(W);
-  fn<<<pass_blocks(n_pad / 8 / kThreads + 1, kMaxBlocks), kThreads, 0, stream>>>(a);
+  const int64_t resident = static_cast<int64_t>(sm_count()) * 5;
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>({n_pad / 8 / kThreads + 1, resident, kMaxBlocks}));
   ++*launches;
-  return cudaGetLastError();
+  return launch_chained(fn, dim3(static_cast<unsigned>(blocks)), kThreads, 0, stream, a);
 }
 
 cudaError_t launch_clipped_update(const FusedLaunch& f, const float* mean, const float* norm, float max_norm,
@@ -489,10 +569,9 @@ cudaError_t launch_clipped_update(const FusedLaunch& f, const float* mean, const
   const int64_t per_seg = ceil_div(static_cast<int64_t>(sm_count()) * 2, f.nseg);
   const int64_t bx = std::max<int64_t>(1, std::min<int64_t>(per_seg, longest / 8 / kThreads + 1));
   const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>(f.nseg));
-  if (f.work_dtype == kF16) clipped_update<__half><<<grid, kThreads, 0, stream>>>(a);
-  else clipped_update<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
   ++*launches;
-  return cudaGetLastError();
+  return launch_chained(f.work_dtype == kF16 ? clipped_update<__half> : clipped_update<__nv_bfloat16>, grid, kThreads, 0,
+                        stream, a);
 }
 
 }  // namespace zero
@@ -515,9 +594,9 @@ extern "C" int zero_grad_norm(int W, int64_t n_tensors, const int64_t* numels, i
   return for_tables(W, n_tensors, numels, grads, nullptr, [&](const Table& t, bool last) -> int {
     const unsigned blocks = pass_blocks(t.chunks, kMaxBlocks / launches);
     if (first + blocks > kMaxBlocks) return fail(ZERO_E_ARG, "too many elements");
-    launch_tensors<false>(t, dtype, blocks, ws, first, last ? norm : nullptr, 0.f, s);
+    ZERO_CUDA(launch_chained(pick_tensors<false>(dtype, W), dim3(blocks), kThreads, 0, s, t, ws, first, first + blocks,
+                             last ? norm : nullptr, 0.f));
     first += blocks;
-    ZERO_CUDA(cudaGetLastError());
     return ZERO_OK;
   });
 }
@@ -535,9 +614,8 @@ extern "C" int zero_grad_clip(int W, int64_t n_tensors, const int64_t* numels, i
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return for_tables(W, n_tensors, numels, grads, out, [&](const Table& t, bool) -> int {
     if (t.tensors == 0) return ZERO_OK;
-    launch_tensors<true>(t, dtype, pass_blocks(t.chunks, INT32_MAX), NormSpace{nullptr, nullptr}, 0,
-                         const_cast<float*>(norm), limit, s);
-    ZERO_CUDA(cudaGetLastError());
+    ZERO_CUDA(launch_chained(pick_tensors<true>(dtype, W), dim3(pass_blocks(t.chunks, INT32_MAX)), kThreads, 0, s, t,
+                             NormSpace{nullptr, nullptr}, 0u, 0u, const_cast<float*>(norm), limit));
     return ZERO_OK;
   });
 }

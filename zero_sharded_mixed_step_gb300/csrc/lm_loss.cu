@@ -27,7 +27,9 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
+#include "launch.cuh"
 #include "step_math.cuh"
 #include "umma.cuh"
 #include "zero_context.h"
@@ -50,8 +52,14 @@ constexpr int kTileK = 64;           // 128 bytes of a 16-bit operand: one swizz
 constexpr int kStages = 6;
 constexpr int kOperandBytes = 128 * kTileK * 2;      // one operand's half tile in one CTA
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kThreads = 192;        // warp 0 loads, warp 1 issues the products, warps 2-5 are the epilogue
+// warp 0 loads (and warp 3 takes B from it where B is not K-major), warp 1 issues the products, warp 2 hands out
+// the tiles, warps 4-11 are the epilogue: two for each quarter of the TMEM
+// lanes, taking turns over the columns
+constexpr int kThreads = 384;
+constexpr int kEpilogueWarps = 8;
+constexpr int kQueue = 4;            // tiles handed out ahead
 constexpr int kGemmSmem = kStages * kStageBytes + 1024;
+constexpr int kMaxJobs = 3;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -61,31 +69,39 @@ enum Kind : int { kStats = 0, kProbs = 1, kDHidden = 2, kDTable = 3 };
 // What fp16 scales D by (see above); bf16 has fp32's range.
 template <typename T>
 __host__ __device__ constexpr float d_scale() {
-  return sizeof(T) == 2 && std::is_same<T, __half>::value ? 16384.f : 1.f;
+  return std::is_same<T, __half>::value ? 16384.f : 1.f;
 }
 
-struct GemmArgs {
-  CUtensorMap a, b;
+// One matrix product of a launch, cut into tiles of kTileM x bn (x splits of K).
+struct Job {
+  int kind;
+  int tiles;                 // m_tiles * n_tiles * splits
   int m_tiles, n_tiles, splits, kb_total;
   int M, N;                  // rows and columns of the product that exist
   int bn;                    // columns of a tile, a multiple of 32
   int b_boxes;               // boxes of an MN-major B half tile
-  int b_half;                // columns of B that each CTA of the pair holds: bn / 2
   uint32_t stage_tx;         // bytes that land per stage, both CTAs together
   int b_row0;                // first row of the table that B starts from (kStats, kProbs: N; kDHidden: K)
-  int tokens;
   int vocab0;                // vocabulary index of column 0 (kProbs)
-  int vocab;
-  const void* targets;
-  int id_bytes;
-  const float* lse;
-  float2* part;              // kStats: [row][n tile] maximum and sum, in powers of 2
-  float* target_logit;
   void* out16;               // kProbs: D; kDTable: the table's gradient
   int64_t out_stride;
   float* acc;                // kDHidden: [split][row][N]
   int add;                   // kDHidden: add to acc; kDTable: add to the gradient
+  int wide;                  // kDTable: rows allow 32-byte stores
   float scale;
+};
+
+struct GemmArgs {
+  CUtensorMap a[kMaxJobs], b[kMaxJobs];
+  Job job[kMaxJobs];         // the longest tiles first
+  int jobs;
+  unsigned int* next;        // tiles handed out beyond one per pair (0 at the launch)
+  int vocab;
+  const void* targets;
+  int id_bytes;
+  const float* lse;
+  float2* part;              // kStats: [row][n tile][half of its columns] maximum and sum, in powers of 2
+  float* target_logit;
 };
 
 // The target of token i, or -1 where it has none.
@@ -100,29 +116,110 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// One fp32 row of a tile of the accumulator, 32 columns at a time.
-template <typename F>
-__device__ __forceinline__ void for_columns(uint32_t tmem, int bn, F f) {
-  float v[32];
-  for (int c = 0; c < bn; c += 32) {
-    tmem_ld32(tmem + c, v);
-    tmem_ld_wait();
-    f(c, v);
+__device__ __forceinline__ void st_32B_words(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
+// A tile of a launch: which job, where, which blocks of K.  job < 0: no more.
+struct alignas(16) Tile {
+  int job, mt, nt, split, k0, k1, unused[2];
+};
+
+__device__ __forceinline__ Tile locate(const GemmArgs& g, int t) {
+  Tile x{};
+  while (x.job < g.jobs && t >= g.job[x.job].tiles) t -= g.job[x.job++].tiles;
+  if (x.job == g.jobs) {
+    x.job = -1;
+    return x;
+  }
+  const Job& j = g.job[x.job];
+  const unsigned m_tiles = j.m_tiles, rest = static_cast<unsigned>(t) / m_tiles;
+  x.mt = t - static_cast<int>(rest * m_tiles);
+  x.nt = static_cast<int>(rest);
+  x.k1 = j.kb_total;
+  if (j.splits > 1) {   // at most 2^18 blocks of K and 64 splits
+    x.split = static_cast<int>(rest / static_cast<unsigned>(j.n_tiles));
+    x.nt = static_cast<int>(rest) - x.split * j.n_tiles;
+    x.k0 = static_cast<int>(static_cast<unsigned>(j.kb_total * x.split) / static_cast<unsigned>(j.splits));
+    x.k1 = static_cast<int>(static_cast<unsigned>(j.kb_total * (x.split + 1)) / static_cast<unsigned>(j.splits));
+  }
+  return x;
+}
+
+// What the epilogue needs to know of its row, read before the tile is complete.
+struct RowInfo {
+  int target;      // -1: none
+  float lse;
+};
+
+template <bool GRAD>
+__device__ __forceinline__ RowInfo row_info(const GemmArgs& g, const Job& j, int row) {
+  RowInfo r{-1, 0.f};
+  if ((GRAD && j.kind != kProbs) || row >= j.M) return r;
+  r.target = load_target(g.targets, g.id_bytes, row, g.vocab);
+  if (GRAD) r.lse = g.lse[row];
+  return r;
+}
+
+// This thread's row of the accumulator, 32 columns at a time from column
+// `first` in steps of 64 (the quarter's other warp takes those between); the
+// next columns are on their way while f works on these.  `release` runs as
+// soon as the last columns are in registers.
+template <typename F, typename R>
+__device__ __forceinline__ void for_columns(uint32_t tmem, int first, int bn, F f, R release) {
+  if (first >= bn) {
+    release();
+    return;
+  }
+  float va[32], vb[32];
+  int c = first;
+  tmem_ld32(tmem + c, va);
+  tmem_ld_wait(va);
+  for (;;) {
+    if (c + 64 < bn) tmem_ld32(tmem + c + 64, vb);
+    else release();
+    f(c, va);
+    c += 64;
+    if (c >= bn) return;
+    tmem_ld_wait(vb);
+    if (c + 64 < bn) tmem_ld32(tmem + c + 64, va);
+    else release();
+    f(c, vb);
+    c += 64;
+    if (c >= bn) return;
+    tmem_ld_wait(va);
   }
 }
 
-template <typename T, int KIND>
-__device__ __forceinline__ void epilogue(const GemmArgs& g, uint32_t tmem, int row, int mt, int nt, int split) {
-  const int n0 = nt * g.bn;
-  const bool row_ok = row < g.M;
-  if constexpr (KIND == kStats) {
-    const int target = row_ok ? load_target(g.targets, g.id_bytes, row, g.vocab) - n0 : -1;
+// The same without loads ahead, for the epilogues whose tiles take long anyway
+// and which read what they add to.
+template <typename F, typename R>
+__device__ __forceinline__ void for_columns_plain(uint32_t tmem, int first, int bn, F f, R release) {
+#pragma unroll 1
+  for (int c = first; c < bn; c += 64) {
+    float v[32];
+    tmem_ld32(tmem + c, v);
+    tmem_ld_wait(v);
+    f(c, v);
+  }
+  release();
+}
+
+template <typename T, bool GRAD, typename R>
+__device__ __forceinline__ void epilogue(const GemmArgs& g, const Job& j, const Tile& x, const RowInfo& info,
+                                         uint32_t tmem, int row, int half, R release) {
+  const int n0 = x.nt * j.bn;
+  const bool row_ok = row < j.M;
+  if (!GRAD) {
+    const int target = info.target - n0;
     float top = -INFINITY, sum = 0.f;
-    for_columns(tmem, g.bn, [&](int c, float (&v)[32]) {
-      if (n0 + c + 32 > g.N) {
+    for_columns(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+      if (n0 + c + 32 > j.N) {
 #pragma unroll
         for (int k = 0; k < 32; ++k)
-          if (n0 + c + k >= g.N) v[k] = -INFINITY;
+          if (n0 + c + k >= j.N) v[k] = -INFINITY;
       }
       if (target >= c && target < c + 32) {
 #pragma unroll
@@ -146,68 +243,100 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, uint32_t tmem, int r
         s1 += exp2_fast(fmaf(v[k + 1], kLog2e, -ref));
       }
       sum += s0 + s1;
-    });
-    if (row_ok) g.part[static_cast<int64_t>(row) * g.n_tiles + nt] = make_float2(top, sum);
-  } else if constexpr (KIND == kProbs) {
-    const int target = row_ok ? load_target(g.targets, g.id_bytes, row, g.vocab) : -1;
-    const int local = target - g.vocab0 - n0;
-    const float ref = row_ok ? g.lse[row] * kLog2e : 0.f;
-    T* out = static_cast<T*>(g.out16) + static_cast<int64_t>(row) * g.out_stride + n0;
-    for_columns(tmem, g.bn, [&](int c, float (&v)[32]) {
+    }, release);
+    if (row_ok) g.part[(static_cast<int64_t>(row) * j.n_tiles + x.nt) * 2 + half] = make_float2(top, sum);
+    return;
+  }
+  if (j.kind == kProbs) {
+    const int local = info.target - j.vocab0 - n0;
+    // a token without target: exp2(-inf) = 0 in every column
+    const float ref = info.target >= 0 ? info.lse * kLog2e : INFINITY;
+    T* out = static_cast<T*>(j.out16) + static_cast<int64_t>(row) * j.out_stride + n0;
+    for_columns(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        float p = exp2_fast(fmaf(v[k], kLog2e, -ref));
-        if (local == c + k) p -= 1.f;
-        v[k] = target >= 0 && n0 + c + k < g.N ? p * d_scale<T>() : 0.f;
+      for (int k = 0; k < 32; ++k) v[k] = exp2_fast(fmaf(v[k], kLog2e, -ref)) * d_scale<T>();
+      if (local >= c && local < c + 32) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (local == c + k) v[k] -= d_scale<T>();
       }
       if (row_ok) {
 #pragma unroll
-        for (int k = 0; k < 32; k += 8) {
-          float w[8];
+        for (int k = 0; k < 32; k += 16) {
+          float lo[8], hi[8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) w[q] = v[k + q];
-          dev::st_16B(out + c + k, Fmt<T>::pack8(w));
+          for (int q = 0; q < 8; ++q) {
+            lo[q] = v[k + q];
+            hi[q] = v[k + 8 + q];
+          }
+          st_32B_words(out + c + k, Fmt<T>::pack8(lo), Fmt<T>::pack8(hi));
         }
       }
-    });
-  } else if constexpr (KIND == kDHidden) {
-    float* out = g.acc + (static_cast<int64_t>(split) * g.M + row) * g.N + n0;
-    for_columns(tmem, g.bn, [&](int c, float (&v)[32]) {
+    }, release);
+  } else if (j.kind == kDHidden) {
+    float* out = j.acc + (static_cast<int64_t>(x.split) * j.M + row) * j.N + n0;
+    for_columns_plain(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+      float w[4][8];
+      if (j.add) {
 #pragma unroll
-      for (int k = 0; k < 32; k += 8) {
-        if (!row_ok || n0 + c + k >= g.N) continue;
-        float w[8];
-        if (g.add) dev::ld_32B(out + c + k, w);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) w[q] = g.add ? w[q] + v[k + q] : v[k + q];
-        dev::st_32B(out + c + k, w);
+        for (int k = 0; k < 4; ++k)
+          if (row_ok && n0 + c + 8 * k < j.N) dev::ld_32B(out + c + 8 * k, w[k]);
       }
-    });
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (!row_ok || n0 + c + 8 * k >= j.N) continue;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) w[k][q] = j.add ? w[k][q] + v[8 * k + q] : v[8 * k + q];
+        dev::st_32B(out + c + 8 * k, w[k]);
+      }
+    }, release);
   } else {
-    T* out = static_cast<T*>(g.out16) + static_cast<int64_t>(row) * g.out_stride + n0;
-    for_columns(tmem, g.bn, [&](int c, float (&v)[32]) {
+    T* out = static_cast<T*>(j.out16) + static_cast<int64_t>(row) * j.out_stride + n0;
+    for_columns_plain(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+uint4 old[4];
+      if (j.add) {
 #pragma unroll
-      for (int k = 0; k < 32; k += 8) {
-        if (!row_ok || n0 + c + k >= g.N) continue;
-        float w[8];
-        if (g.add) Fmt<T>::unpack8(dev::ld_16B(out + c + k), w);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) w[q] = g.add ? fmaf(v[k + q], g.scale, w[q]) : v[k + q] * g.scale;
-        dev::st_16B(out + c + k, Fmt<T>::pack8(w));
+        for (int k = 0; k < 4; ++k)
+          if (row_ok && n0 + c + 8 * k < j.N) old[k] = dev::ld_16B(out + c + 8 * k);
       }
-    });
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        uint4 packed[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int at = c + 8 * (k + h);
+          if (!row_ok || n0 + at >= j.N) continue;
+          float w[8];
+          if (j.add) Fmt<T>::unpack8(old[k + h], w);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float p = v[8 * (k + h) + q];
+            w[q] = j.add ? fmaf(p, j.scale, w[q]) : p * j.scale;
+          }
+          packed[h] = Fmt<T>::pack8(w);
+          if (!j.wide) dev::st_16B(out + at, packed[h]);
+        }
+        if (j.wide && row_ok && n0 + c + 8 * k < j.N) st_32B_words(out + c + 8 * k, packed[0], packed[1]);
+      }
+    }, release);
   }
 }
 
 // The persistent product kernel: pairs of CTAs, each pair one 256-row tile at
 // a time, operands through a ring of TMA stages, two accumulators in TMEM so
-// that one tile's epilogue runs beside the next one's products.
-template <typename T, int KIND>
+// that one tile's epilogue runs beside the next one's products.  One thread of
+// the pair hands out its tiles through a short queue in shared memory, worked
+// out, so that no role waits for a division or a counter between two tiles.
+// The loss's tiles are all alike and are dealt out in turn.  The gradient's
+// differ: beyond its first tile a pair takes the next one from a counter, in
+// the order of the jobs, the longest tiles first, so that the short ones fill
+// the gaps at the end.
+template <typename T, bool GRAD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm(const __grid_constant__ GemmArgs g) {
-  constexpr bool kAMn = KIND == kDTable;                        // A = D^T: rows of vocabulary are contiguous in D
-  constexpr bool kBMn = KIND == kDTable || KIND == kDHidden;    // B = h or T with K the row index
   extern __shared__ unsigned char raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 2 * kQueue + 5];
+  __shared__ Tile queue[kQueue];
+  __shared__ Job jobs[kMaxJobs];
   __shared__ uint32_t tmem_slot;
   __shared__ int failed;
   const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
@@ -217,11 +346,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm
   auto done = [&](int a) { return bar0 + 8 * (2 * kStages + a); };        // accumulator a is complete
   auto taken = [&](int a) { return bar0 + 8 * (2 * kStages + 2 + a); };   // accumulator a has been read
   const uint32_t drained = bar0 + 8 * (2 * kStages + 4);
+  auto told = [&](int q) { return bar0 + 8 * (2 * kStages + 5 + q); };             // queue[q] holds a tile
+  auto heard = [&](int q) { return bar0 + 8 * (2 * kStages + 5 + kQueue + q); };   // everyone has read it
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int total = g.m_tiles * g.n_tiles * g.splits;
 
+  allow_next();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       bar_init(full(s), 1);
@@ -229,81 +360,129 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm
     }
     for (int a = 0; a < 2; ++a) {
       bar_init(done(a), 1);
-      bar_init(taken(a), 8);
+      bar_init(taken(a), 2 * kEpilogueWarps);
+    }
+    for (int q = 0; q < kQueue; ++q) {
+      bar_init(told(q), 1);
+      bar_init(heard(q), 5 + 2 * kEpilogueWarps);   // in both CTAs two loaders and the epilogue, and the issuer
     }
     bar_init(drained, 1);
     failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    tma_prefetch_map(&g.a);
-    tma_prefetch_map(&g.b);
+    for (int k = 0; k < g.jobs; ++k) {
+      tma_prefetch_map(&g.a[k]);
+      tma_prefetch_map(&g.b[k]);
+    }
   }
   if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 512);
+  if (warp == 2 && lane < g.jobs) jobs[lane] = g.job[lane];
   __syncthreads();
   fence_before();
   cluster_sync();
   fence_after();
   const uint32_t tmem = tmem_slot;
+  await_previous();
 
-  int issued = 0;      // stages loaded by this CTA (warp 0)
+  // The i-th tile of this pair, read by one lane of each consuming warp.
   bool ok = true;
-  if (warp == 0) {
+  auto tile_of = [&](int i) {
+    Tile x{};
+    const int q = i % kQueue;
+    ok = bar_wait<true>(told(q), (i / kQueue) & 1);
+    x.job = -1;
+    if (!ok) return x;
+    x = queue[q];
+    asm volatile("" ::: "memory");
+    bar_arrive(in_cta(heard(q), 0));
+    return x;
+  };
+
+  int issued = 0;      // stages loaded by this thread
+  if (warp == 0 || warp == 3) {
     if (lane == 0) {
-      for (int t = pair; t < total && ok; t += pairs) {
-        const int mt = t % g.m_tiles, rest = t / g.m_tiles, nt = rest % g.n_tiles, sp = rest / g.n_tiles;
-        const int k0 = static_cast<int>(static_cast<int64_t>(g.kb_total) * sp / g.splits);
-        const int k1 = static_cast<int>(static_cast<int64_t>(g.kb_total) * (sp + 1) / g.splits);
-        const int am = mt * kTileM + static_cast<int>(rank) * 128;
-        const int bn = nt * g.bn + static_cast<int>(rank) * g.b_half;
-        for (int kb = k0; kb < k1; ++kb, ++issued) {
+      for (int i = 0;; ++i) {
+        const Tile x = tile_of(i);
+        if (!ok || x.job < 0) break;
+        const Job& j = jobs[x.job];
+        const CUtensorMap *ma = &g.a[x.job], *mb = &g.b[x.job];
+        const int kind = GRAD ? j.kind : static_cast<int>(kStats);
+        const int am = x.mt * kTileM + static_cast<int>(rank) * 128;
+        const int bn = x.nt * j.bn + static_cast<int>(rank) * (j.bn / 2);
+        // an MN-major operand comes as boxes of 64 columns, with K the row index
+        const bool a_mn = kind == kDTable, b_mn = kind >= kDHidden;
+        // one thread loads both operands where each is one box; four boxes a stage are too many for it
+        const bool both = !b_mn, load_a = warp == 0, load_b = both ? warp == 0 : warp == 3;
+        if (both && warp == 3) {
+          issued += x.k1 - x.k0;
+          continue;
+        }
+        const int row0 = b_mn ? (kind == kDHidden ? j.b_row0 : 0) : bn + j.b_row0;
+        const int boxes = j.b_boxes;
+        const uint32_t tx = j.stage_tx;
+        for (int kb = x.k0; kb < x.k1; ++kb, ++issued) {
           const int s = issued % kStages;
-          if (!(ok = bar_wait(empty(s), ((issued / kStages) & 1) ^ 1))) break;
-          if (rank == 0) bar_expect(full(s), g.stage_tx);
+          ok = bar_wait(empty(s), ((issued / kStages) & 1) ^ 1);
+          if (!ok) break;
+          if (load_a && rank == 0) bar_expect(full(s), tx);
           const uint32_t bar = in_cta(full(s), 0);
           const uint32_t sa = ring + s * kStageBytes, sb = sa + kOperandBytes;
           const int k = kb * kTileK;
-          if (kAMn) {
-            tma_load(sa, &g.a, am, k, bar);
-            tma_load(sa + 8192, &g.a, am + 64, k, bar);
-          } else {
-            tma_load(sa, &g.a, k, am, bar);
+          if (load_a) {
+            if (a_mn) {
+              tma_load(sa, ma, am, k, bar);
+              tma_load(sa + 8192, ma, am + 64, k, bar);
+            } else {
+              tma_load(sa, ma, k, am, bar);
+            }
           }
-          if (kBMn) {
-            const int row = k + (KIND == kDHidden ? g.b_row0 : 0);
-            for (int j = 0; j < g.b_boxes; ++j) tma_load(sb + j * 8192, &g.b, bn + 64 * j, row, bar);
-          } else {
-            tma_load(sb, &g.b, k, bn + g.b_row0, bar);
+          if (load_b) {
+            if (b_mn) {
+              tma_load(sb, mb, bn, row0 + k, bar);
+              if (boxes > 1) tma_load(sb + 8192, mb, bn + 64, row0 + k, bar);
+            } else {
+              tma_load(sb, mb, k, row0, bar);
+            }
           }
         }
+        if (!ok) break;
       }
       if (!ok) failed = 1;
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
-      const uint32_t idesc = instr_desc(std::is_same<T, __nv_bfloat16>::value, kAMn, kBMn, kTileM, g.bn);
-      int stage = 0, tile = 0;
-      for (int t = pair; t < total && ok; t += pairs, ++tile) {
-        const int sp = t / g.m_tiles / g.n_tiles;
-        const int k0 = static_cast<int>(static_cast<int64_t>(g.kb_total) * sp / g.splits);
-        const int k1 = static_cast<int>(static_cast<int64_t>(g.kb_total) * (sp + 1) / g.splits);
-        const int a = tile & 1;
-        if (!(ok = bar_wait(taken(a), ((tile >> 1) & 1) ^ 1))) break;
+      int stage = 0;
+      Tile x = tile_of(0);
+      for (int i = 0; ok && x.job >= 0; ++i) {
+        const Job& j = jobs[x.job];
+        const bool a_mn = GRAD && j.kind == kDTable;      // A = D^T: rows of vocabulary are contiguous in D
+        const bool b_mn = GRAD && j.kind >= kDHidden;     // B = h or T with K the row index
+        const uint32_t idesc = instr_desc(std::is_same<T, __nv_bfloat16>::value, a_mn, b_mn, kTileM, j.bn);
+        // 16 values of K further: 32 bytes within a K-major row, 16 rows of an MN-major tile
+        const uint64_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+        const int a = i & 1;
+        Tile next = x;
+        ok = bar_wait(taken(a), ((i >> 1) & 1) ^ 1);
+        if (!ok) break;
         fence_after();
         const uint32_t d = tmem + a * kTileN;
-        for (int kb = k0; kb < k1; ++kb, ++stage) {
+        for (int kb = x.k0; kb < x.k1; ++kb, ++stage) {
           const int s = stage % kStages;
-          if (!(ok = bar_wait(full(s), (stage / kStages) & 1))) break;
+          ok = bar_wait(full(s), (stage / kStages) & 1);
+          if (!ok) break;
           fence_after();
           const uint32_t sa = ring + s * kStageBytes, sb = sa + kOperandBytes;
-          const uint64_t da = operand_desc(sa, kAMn ? 8192 : 0), db = operand_desc(sb, kBMn ? 8192 : 0);
+          const uint64_t da = operand_desc(sa, a_mn ? 8192 : 0), db = operand_desc(sb, b_mn ? 8192 : 0);
 #pragma unroll
-          for (int q = 0; q < kTileK / 16; ++q) {
-            // 16 values of K further: 32 bytes within a K-major row, 16 rows of an MN-major tile
-            const uint64_t ka = (kAMn ? 2048 : 32) * q >> 4, kb16 = (kBMn ? 2048 : 32) * q >> 4;
-            mma(d, da + ka, db + kb16, idesc, kb > k0 || q > 0);
-          }
+          for (int q = 0; q < kTileK / 16; ++q) mma(d, da + q * a_step, db + q * b_step, idesc, kb > x.k0 || q > 0);
           mma_commit(empty(s));
+          if (kb == min(x.k0 + 3, x.k1 - 1)) {   // while the products already issued run
+            next = tile_of(i + 1);
+            if (!ok) break;
+          }
         }
-        if (ok) mma_commit(done(a));
+        if (!ok) break;
+        mma_commit(done(a));
+        x = next;
       }
       if (!ok) {
         // leave no product in flight behind
@@ -312,23 +491,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm
         bar_wait(drained, 0);
       }
     }
-  } else {
-    int tile = 0;
-    const int quad = warp & 3;
-    for (int t = pair; t < total; t += pairs, ++tile) {
-      const int mt = t % g.m_tiles, rest = t / g.m_tiles, nt = rest % g.n_tiles, sp = rest / g.n_tiles;
-      const int a = tile & 1;
-      if (!__all_sync(0xffffffffu, bar_wait(done(a), (tile >> 1) & 1))) {
-        if (lane == 0) failed = 1;
-        break;
+  } else if (warp == 2) {
+    if (rank == 0 && lane == 0) {
+      for (int i = 0;; ++i) {
+        const int q = i % kQueue;
+        ok = bar_wait(heard(q), ((i / kQueue) & 1) ^ 1);
+        if (!ok) break;
+        const int t = GRAD ? (i == 0 ? pair : pairs + static_cast<int>(atomicAdd(g.next, 1u))) : pair + i * pairs;
+        const Tile x = locate(g, t);
+        for (uint32_t r = 0; r < 2; ++r) {
+          const uint32_t at = in_cta(smem_addr(&queue[q]), r);
+          st_cluster(at, x.job, x.mt, x.nt, x.split);
+          st_cluster(at + 16, x.k0, x.k1, 0, 0);
+          bar_arrive_written(in_cta(told(q), r));
+        }
+        if (x.job < 0) break;
       }
-      fence_after();
-      epilogue<T, KIND>(g, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21),
-                        mt * kTileM + static_cast<int>(rank) * 128 + quad * 32 + lane, mt, nt, sp);
-      fence_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive_cluster(in_cta(taken(a), 0));
+      if (!ok) failed = 1;
     }
+  } else if (warp >= 4) {
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    for (int i = 0;; ++i) {
+      const int q = i % kQueue, a = i & 1;
+      ok = __all_sync(0xffffffffu, bar_wait<true>(told(q), (i / kQueue) & 1));
+      if (!ok) break;
+      const Tile x = queue[q];
+      __syncwarp();
+      if (lane == 0) bar_arrive(in_cta(heard(q), 0));
+      if (x.job < 0) break;
+      const Job& j = jobs[x.job];
+      const int row = x.mt * kTileM + static_cast<int>(rank) * 128 + quad * 32 + lane;
+      const RowInfo info = row_info<GRAD>(g, j, row);
+      ok = __all_sync(0xffffffffu, bar_wait(done(a), (i >> 1) & 1));
+      if (!ok) break;
+      fence_after();
+      epilogue<T, GRAD>(g, j, x, info, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21), row, half, [&] {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(in_cta(taken(a), 0));
+      });
+    }
+    if (!ok && lane == 0) failed = 1;
   }
   __syncthreads();
   if (failed) {
@@ -336,7 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm
       atomicAdd(&g_lm_timeouts, 1u);
       // the copies in flight land on the leader's barriers: both CTAs stay until they have
       if (rank == 0)
-        for (int j = max(0, issued - kStages); j < issued; ++j) bar_wait(full(j % kStages), (j / kStages) & 1);
+        for (int k = max(0, issued - kStages); k < issued; ++k) bar_wait(full(k % kStages), (k / kStages) & 1);
     }
     __syncthreads();
   }
@@ -354,6 +557,8 @@ constexpr int kSmallThreads = 256;
 __global__ void __launch_bounds__(kSmallThreads) lm_combine(const float2* part, int tiles, const float* target_logit,
                                                             const void* targets, int id_bytes, int vocab, int tokens,
                                                             float* loss, float* lse) {
+  allow_next();
+  await_previous();
   const int row = (blockIdx.x * kSmallThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
   if (row >= tokens) return;
   const float2* p = part + static_cast<int64_t>(row) * tiles;
@@ -382,10 +587,15 @@ __global__ void __launch_bounds__(kSmallThreads) lm_combine(const float2* part, 
 
 // The hidden vectors with the rows of tokens without target set to 0: such a
 // row times D's zeros must add nothing to the table's gradient even where it
-// holds an infinity or a NaN.
+// holds an infinity or a NaN.  Also sets the products' tile counters to 0.
 __global__ void __launch_bounds__(kSmallThreads) lm_masked_hidden(const uint16_t* hidden, int64_t stride, int width8,
                                                                   const void* targets, int id_bytes, int vocab,
-                                                                  int tokens, uint16_t* out) {
+                                                                  int tokens, uint16_t* out, unsigned int* counters,
+                                                                  int n_counters) {
+  allow_next();
+  await_previous();
+  if (blockIdx.x == 0)
+    for (int k = threadIdx.x; k < n_counters; k += kSmallThreads) counters[k] = 0;
   const int64_t total = static_cast<int64_t>(tokens) * width8;
   for (int64_t e = static_cast<int64_t>(blockIdx.x) * kSmallThreads + threadIdx.x; e < total;
        e += static_cast<int64_t>(gridDim.x) * kSmallThreads) {
@@ -400,6 +610,8 @@ __global__ void __launch_bounds__(kSmallThreads) lm_masked_hidden(const uint16_t
 template <typename T>
 __global__ void __launch_bounds__(kSmallThreads) lm_finish_dhidden(const float* acc, int splits, int64_t tokens,
                                                                    int width8, float scale, T* out, int64_t stride) {
+  allow_next();
+  await_previous();
   const int64_t total = tokens * width8;
   for (int64_t e = static_cast<int64_t>(blockIdx.x) * kSmallThreads + threadIdx.x; e < total;
        e += static_cast<int64_t>(gridDim.x) * kSmallThreads) {
@@ -457,17 +669,14 @@ int make_map(CUtensorMap* map, int dtype, const void* base, int64_t rows, int64_
   return r == CUDA_SUCCESS ? ZERO_OK : fail(ZERO_E_CUDA, "encoding a tensor map failed (%d)", static_cast<int>(r));
 }
 
-using GemmFn = void (*)(const GemmArgs);
-
-template <int KIND>
+template <bool GRAD>
 int launch_gemm(const GemmArgs& g, int dtype, cudaStream_t s) {
-  const GemmFn fn = dtype == ZERO_FP16 ? static_cast<GemmFn>(lm_gemm<__half, KIND>)
-                                       : static_cast<GemmFn>(lm_gemm<__nv_bfloat16, KIND>);
+  const auto fn = dtype == ZERO_FP16 ? lm_gemm<__half, GRAD> : lm_gemm<__nv_bfloat16, GRAD>;
   ZERO_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem));
-  const int64_t tiles = static_cast<int64_t>(g.m_tiles) * g.n_tiles * g.splits;
+  int64_t tiles = 0;
+  for (int k = 0; k < g.jobs; ++k) tiles += g.job[k].tiles;
   const int pairs = static_cast<int>(std::min<int64_t>(std::max(1, sm_count() / 2), tiles));
-  fn<<<2 * pairs, kThreads, kGemmSmem, s>>>(g);
-  ZERO_CUDA(cudaGetLastError());
+  ZERO_CUDA(launch_chained(fn, dim3(2 * pairs), kThreads, kGemmSmem, s, g));
   return ZERO_OK;
 }
 
@@ -497,9 +706,12 @@ int tile_width(int64_t width) {
   return best;
 }
 
-constexpr int64_t kPieceBytes = int64_t(64) << 20;   // of D: stays in L2 between its three uses
+// Bytes of D at a time.  8192 tokens x 50257 x 768 took 2.73 ms with 32 MB, 1.99
+// with 64, 1.94 with 128, 1.95 with 256 and 1.91 with 512 (two launches in all).
+constexpr int64_t kPieceBytes = int64_t(128) << 20;
 constexpr int64_t kMinPiece = 2048;
 constexpr int kMaxSplits = 64;
+constexpr int kMinLossTile = 96;
 
 GradPlan plan_grad(int64_t tokens, int64_t vocab, int64_t width) {
   GradPlan p;
@@ -512,23 +724,47 @@ GradPlan plan_grad(int64_t tokens, int64_t vocab, int64_t width) {
   return p;
 }
 
+// Byte offsets of the workspace's parts: the masked hidden vectors, D of two
+// pieces (one is formed while the other is used), dh's fp32 sums, and a tile
+// counter for each launch.
 struct GradSpace {
-  int64_t hidden, probs, acc, total;   // byte offsets of the parts
+  int64_t hidden, probs[2], acc, counters, total;
 };
 
-GradSpace grad_space(int64_t tokens, int64_t width, const GradPlan& p) {
+GradSpace grad_space(int64_t tokens, int64_t vocab, int64_t width, const GradPlan& p) {
+  const int64_t pieces = ceil_div(vocab, p.piece);
   GradSpace s;
   s.hidden = 0;
-  s.probs = round_up(tokens * width * 2, 256);
-  s.acc = s.probs + round_up(tokens * p.piece * 2, 256);
-  s.total = s.acc + round_up(p.splits * tokens * width * 4, 256);
+  s.probs[0] = round_up(tokens * width * 2, 256);
+  s.probs[1] = s.probs[0] + round_up(tokens * p.piece * 2, 256);
+  s.acc = s.probs[1] + (pieces > 1 ? s.probs[1] - s.probs[0] : 0);
+  s.counters = s.acc + round_up(p.splits * tokens * width * 4, 256);
+  s.total = s.counters + round_up((pieces + 1) * 4, 256);
   return s;
 }
 
-int64_t loss_tiles(int64_t vocab) { return ceil_div(vocab, kTileN); }
+// Columns of a tile of the loss.  Many tokens: the widest.  A few tokens (one
+// row of tiles): the time is that of reading the table, and the width is the
+// one whose last round of tiles over the pairs of SMs wastes least.
+int loss_tile(int64_t tokens, int64_t vocab) {
+  if (tokens > kTileM) return kTileN;
+  const int64_t pairs = std::max(1, sm_count() / 2);
+  int best = kTileN;
+  int64_t cost = INT64_MAX;
+  for (int bn = kTileN; bn >= kMinLossTile; bn -= 32) {
+    const int64_t c = ceil_div(ceil_div(vocab, bn), pairs) * (bn + 8);
+    if (c < cost) {
+      cost = c;
+      best = bn;
+    }
+  }
+  return best;
+}
 
 int64_t loss_space(int64_t tokens, int64_t vocab) {
-  return round_up(tokens * loss_tiles(vocab) * 8, 256) + round_up(tokens * 4, 256);
+  // room for a row of the narrowest tiles, which few tokens may get
+  const int64_t parts = std::max(tokens * ceil_div(vocab, kTileN), std::min<int64_t>(tokens, kTileM) * ceil_div(vocab, kMinLossTile));
+  return round_up(parts * 16, 256) + round_up(tokens * 4, 256);
 }
 
 constexpr int64_t kMaxTokens = int64_t(1) << 24, kMaxVocab = int64_t(1) << 24, kMaxWidth = int64_t(1) << 16;
@@ -576,9 +812,10 @@ extern "C" int64_t zero_lm_workspace_bytes(int64_t tokens, int64_t vocab, int64_
   if (!with_grad) return bytes;
   // any smaller count of tokens has to fit too: its sums may be split more often, and its pieces be wider
   const int64_t wide = round_up(vocab, 256);
-  const int64_t probs = std::max(std::min(tokens * wide * 2, kPieceBytes), tokens * std::min(kMinPiece, wide) * 2);
+  const int64_t probs = 2 * std::max(std::min(tokens * wide * 2, kPieceBytes), tokens * std::min(kMinPiece, wide) * 2);
   const int64_t sums = std::max(tokens, std::min<int64_t>(tokens * kMaxSplits, 76 * kTileM)) * (round_up(width, 256)) * 4;
-  return std::max(bytes, round_up(tokens * width * 2, 256) + round_up(probs, 256) + round_up(sums, 256));
+  const int64_t counters = (ceil_div(vocab, std::min(kMinPiece, wide)) + 1) * 4;
+  return std::max(bytes, round_up(tokens * width * 2, 256) + round_up(probs, 512) + round_up(sums, 256) + round_up(counters, 256));
 }
 
 extern "C" int zero_lm_loss(int64_t tokens, int64_t vocab, int64_t width, int dtype, const void* hidden,
@@ -598,25 +835,28 @@ extern "C" int zero_lm_loss(int64_t tokens, int64_t vocab, int64_t width, int dt
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   GemmArgs g;
   std::memset(&g, 0, sizeof g);
-  if ((rc = make_map(&g.a, dtype, hidden, tokens, width, hidden_stride, 128))) return rc;
-  if ((rc = make_map(&g.b, dtype, table, vocab, width, table_stride, kTileN / 2))) return rc;
-  g.m_tiles = static_cast<int>(ceil_div(tokens, kTileM));
-  g.n_tiles = static_cast<int>(loss_tiles(vocab));
-  g.splits = 1;
-  g.kb_total = static_cast<int>(ceil_div(width, kTileK));
-  g.M = g.tokens = static_cast<int>(tokens);
-  g.N = g.vocab = static_cast<int>(vocab);
-  g.bn = kTileN;
-  g.b_half = kTileN / 2;
-  g.stage_tx = 2 * kStageBytes;
+  Job& j = g.job[0];
+  j.kind = kStats;
+  j.bn = loss_tile(tokens, vocab);
+  j.m_tiles = static_cast<int>(ceil_div(tokens, kTileM));
+  j.n_tiles = static_cast<int>(ceil_div(vocab, j.bn));
+  j.splits = 1;
+  j.tiles = j.m_tiles * j.n_tiles;
+  j.kb_total = static_cast<int>(ceil_div(width, kTileK));
+  j.M = static_cast<int>(tokens);
+  j.N = static_cast<int>(vocab);
+  j.stage_tx = 2 * (kOperandBytes + j.bn / 2 * kTileK * 2);
+  g.jobs = 1;
+  g.vocab = static_cast<int>(vocab);
   g.targets = targets;
   g.id_bytes = id_bytes;
   g.part = static_cast<float2*>(workspace);
-  g.target_logit = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(tokens * g.n_tiles * 8, 256));
-  if ((rc = launch_gemm<kStats>(g, dtype, s))) return rc;
-  lm_combine<<<static_cast<unsigned>(ceil_div(tokens * 32, kSmallThreads)), kSmallThreads, 0, s>>>(
-      g.part, g.n_tiles, g.target_logit, targets, id_bytes, g.vocab, g.tokens, loss, lse);
-  ZERO_CUDA(cudaGetLastError());
+  g.target_logit = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(tokens * j.n_tiles * 16, 256));
+  if ((rc = make_map(&g.a[0], dtype, hidden, tokens, width, hidden_stride, 128))) return rc;
+  if ((rc = make_map(&g.b[0], dtype, table, vocab, width, table_stride, j.bn / 2))) return rc;
+  if ((rc = launch_gemm<false>(g, dtype, s))) return rc;
+  ZERO_CUDA(launch_chained(lm_combine, dim3(static_cast<unsigned>(ceil_div(tokens * 32, kSmallThreads))), kSmallThreads, 0,
+                           s, g.part, 2 * j.n_tiles, g.target_logit, targets, id_bytes, g.vocab, j.M, loss, lse));
   return ZERO_OK;
 }
 
@@ -641,94 +881,99 @@ extern "C" int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, i
     return ZERO_OK;
   }
   const GradPlan p = plan_grad(tokens, vocab, width);
-  const GradSpace sp = grad_space(tokens, width, p);
+  const GradSpace sp = grad_space(tokens, vocab, width, p);
   if (workspace_bytes < sp.total)
     return fail(ZERO_E_ARG, "workspace of %lld bytes: %lld are needed", (long long)workspace_bytes,
                 (long long)sp.total);
   char* ws = static_cast<char*>(workspace);
   uint16_t* masked = reinterpret_cast<uint16_t*>(ws + sp.hidden);
-  void* probs = ws + sp.probs;
   float* acc = reinterpret_cast<float*>(ws + sp.acc);
+  unsigned int* counters = reinterpret_cast<unsigned int*>(ws + sp.counters);
   const int width8 = static_cast<int>(width / 8);
-  lm_masked_hidden<<<small_grid(tokens * width8), kSmallThreads, 0, s>>>(
-      static_cast<const uint16_t*>(hidden), hidden_stride, width8, targets, id_bytes, static_cast<int>(vocab),
-      static_cast<int>(tokens), masked);
-  ZERO_CUDA(cudaGetLastError());
-
-  GemmArgs g;
-  std::memset(&g, 0, sizeof g);
-  g.tokens = static_cast<int>(tokens);
-  g.vocab = static_cast<int>(vocab);
-  g.targets = targets;
-  g.id_bytes = id_bytes;
-  g.lse = lse;
+  const int64_t pieces = ceil_div(vocab, p.piece), items = tokens * width8;
+  ZERO_CUDA(launch_chained(lm_masked_hidden, dim3(small_grid(items)), kSmallThreads, 0, s,
+                           static_cast<const uint16_t*>(hidden), hidden_stride, width8, targets, id_bytes,
+                           static_cast<int>(vocab), static_cast<int>(tokens), masked, counters,
+                           static_cast<int>(pieces + 1)));
   const float unscale = static_cast<float>(scale) / (dtype == ZERO_FP16 ? d_scale<__half>() : d_scale<__nv_bfloat16>());
-  for (int64_t v0 = 0; v0 < vocab; v0 += p.piece) {
-    const int64_t w = std::min(p.piece, vocab - v0);
-    // D of the piece
-    GemmArgs a = g;
-    if ((rc = make_map(&a.a, dtype, masked, tokens, width, width, 128))) return rc;
-    if ((rc = make_map(&a.b, dtype, table, vocab, width, table_stride, kTileN / 2))) return rc;
-    a.m_tiles = static_cast<int>(ceil_div(tokens, kTileM));
-    a.n_tiles = static_cast<int>(ceil_div(w, kTileN));
-    a.splits = 1;
-    a.kb_total = static_cast<int>(ceil_div(width, kTileK));
-    a.M = g.tokens;
-    a.N = static_cast<int>(w);
-    a.bn = kTileN;
-    a.b_half = kTileN / 2;
-    a.stage_tx = 2 * kStageBytes;
-    a.b_row0 = static_cast<int>(v0);
-    a.vocab0 = static_cast<int>(v0);
-    a.out16 = probs;
-    a.out_stride = p.piece;
-    if ((rc = launch_gemm<kProbs>(a, dtype, s))) return rc;
-    // its share of dh
-    GemmArgs b = g;
-    if ((rc = make_map(&b.a, dtype, probs, tokens, w, p.piece, 128))) return rc;
-    if ((rc = make_map(&b.b, dtype, table, vocab, width, table_stride, 64))) return rc;
-    b.m_tiles = a.m_tiles;
-    b.n_tiles = static_cast<int>(ceil_div(width, p.bn));
-    b.kb_total = static_cast<int>(ceil_div(w, kTileK));
-    b.splits = std::min(p.splits, b.kb_total);
-    b.M = g.tokens;
-    b.N = static_cast<int>(width);
-    b.bn = p.bn;
-    b.b_half = p.bn / 2;
-    b.b_boxes = static_cast<int>(ceil_div(b.b_half, 64));
-    b.stage_tx = 2 * (kOperandBytes + b.b_boxes * 8192);
-    b.b_row0 = static_cast<int>(v0);
-    b.acc = acc;
-    b.add = v0 > 0;
-    if ((rc = launch_gemm<kDHidden>(b, dtype, s))) return rc;
-    // its rows of the table's gradient
-    GemmArgs c = g;
-    if ((rc = make_map(&c.a, dtype, probs, tokens, w, p.piece, 64))) return rc;
-    if ((rc = make_map(&c.b, dtype, masked, tokens, width, width, 64))) return rc;
-    c.m_tiles = static_cast<int>(ceil_div(w, kTileM));
-    c.n_tiles = b.n_tiles;
-    c.splits = 1;
-    c.kb_total = static_cast<int>(ceil_div(tokens, kTileK));
-    c.M = static_cast<int>(w);
-    c.N = static_cast<int>(width);
-    c.bn = p.bn;
-    c.b_half = b.b_half;
-    c.b_boxes = b.b_boxes;
-    c.stage_tx = b.stage_tx;
-    c.out16 = static_cast<uint16_t*>(dtable) + v0 * dtable_stride;
-    c.out_stride = dtable_stride;
-    c.add = accumulate != 0;
-    c.scale = unscale;
-    if ((rc = launch_gemm<kDTable>(c, dtype, s))) return rc;
+
+  // Launch k forms D of piece k and multiplies with D of piece k - 1.
+  for (int64_t k = 0; k <= pieces; ++k) {
+    GemmArgs g;
+    std::memset(&g, 0, sizeof g);
+    g.next = counters + k;
+    g.vocab = static_cast<int>(vocab);
+    g.targets = targets;
+    g.id_bytes = id_bytes;
+    g.lse = lse;
+    if (k > 0) {
+      const int64_t v0 = (k - 1) * p.piece, w = std::min(p.piece, vocab - v0);
+      const void* probs = ws + sp.probs[(k - 1) & 1];
+      // the piece's share of dh, and its rows of the table's gradient: the longer tiles first
+      Job dh{}, dt{};
+      dh.kind = kDHidden;
+      dh.bn = dt.bn = p.bn;
+      dh.b_boxes = dt.b_boxes = static_cast<int>(ceil_div(p.bn / 2, 64));
+      dh.stage_tx = dt.stage_tx = 2 * (kOperandBytes + dh.b_boxes * 8192);
+      dh.n_tiles = dt.n_tiles = static_cast<int>(ceil_div(width, p.bn));
+      dh.N = dt.N = static_cast<int>(width);
+      dh.m_tiles = static_cast<int>(ceil_div(tokens, kTileM));
+      dh.kb_total = static_cast<int>(ceil_div(w, kTileK));
+      dh.splits = std::min(p.splits, dh.kb_total);
+      dh.M = static_cast<int>(tokens);
+      dh.b_row0 = static_cast<int>(v0);
+      dh.acc = acc;
+      dh.add = v0 > 0;
+      dt.kind = kDTable;
+      dt.m_tiles = static_cast<int>(ceil_div(w, kTileM));
+      dt.kb_total = static_cast<int>(ceil_div(tokens, kTileK));
+      dt.splits = 1;
+      dt.M = static_cast<int>(w);
+      dt.out16 = static_cast<uint16_t*>(dtable) + v0 * dtable_stride;
+      dt.out_stride = dtable_stride;
+      dt.add = accumulate != 0;
+      dt.wide = width % 16 == 0 && dtable_stride % 16 == 0 && host::aligned32(dtable);
+      dt.scale = unscale;
+      const bool table_first = dt.kb_total >= dh.kb_total / dh.splits;
+      const int at_h = table_first ? 1 : 0, at_t = 1 - at_h;
+      dh.tiles = dh.m_tiles * dh.n_tiles * dh.splits;
+      dt.tiles = dt.m_tiles * dt.n_tiles;
+      g.job[at_h] = dh;
+      g.job[at_t] = dt;
+      if ((rc = make_map(&g.a[at_h], dtype, probs, tokens, w, p.piece, 128))) return rc;
+      if ((rc = make_map(&g.b[at_h], dtype, table, vocab, width, table_stride, 64))) return rc;
+      if ((rc = make_map(&g.a[at_t], dtype, probs, tokens, w, p.piece, 64))) return rc;
+      if ((rc = make_map(&g.b[at_t], dtype, masked, tokens, width, width, 64))) return rc;
+      g.jobs = 2;
+    }
+    if (k < pieces) {
+      const int64_t v0 = k * p.piece, w = std::min(p.piece, vocab - v0);
+      Job& j = g.job[g.jobs];
+      j.kind = kProbs;
+      j.bn = kTileN;
+      j.m_tiles = static_cast<int>(ceil_div(tokens, kTileM));
+      j.n_tiles = static_cast<int>(ceil_div(w, kTileN));
+      j.splits = 1;
+      j.tiles = j.m_tiles * j.n_tiles;
+      j.kb_total = static_cast<int>(ceil_div(width, kTileK));
+      j.M = static_cast<int>(tokens);
+      j.N = static_cast<int>(w);
+      j.stage_tx = 2 * kStageBytes;
+      j.b_row0 = j.vocab0 = static_cast<int>(v0);
+      j.out16 = ws + sp.probs[k & 1];
+      j.out_stride = p.piece;
+      if ((rc = make_map(&g.a[g.jobs], dtype, masked, tokens, width, width, 128))) return rc;
+      if ((rc = make_map(&g.b[g.jobs], dtype, table, vocab, width, table_stride, kTileN / 2))) return rc;
+      ++g.jobs;
+    }
+    if ((rc = launch_gemm<true>(g, dtype, s))) return rc;
   }
-  const int64_t items = tokens * width8;
   if (dtype == ZERO_FP16)
-    lm_finish_dhidden<__half><<<small_grid(items), kSmallThreads, 0, s>>>(acc, p.splits, tokens, width8, unscale,
-                                                                          static_cast<__half*>(dhidden), dhidden_stride);
+    ZERO_CUDA(launch_chained(lm_finish_dhidden<__half>, dim3(small_grid(items)), kSmallThreads, 0, s, acc, p.splits,
+                             tokens, width8, unscale, static_cast<__half*>(dhidden), dhidden_stride));
   else
-    lm_finish_dhidden<__nv_bfloat16><<<small_grid(items), kSmallThreads, 0, s>>>(
-        acc, p.splits, tokens, width8, unscale, static_cast<__nv_bfloat16*>(dhidden), dhidden_stride);
-  ZERO_CUDA(cudaGetLastError());
+    ZERO_CUDA(launch_chained(lm_finish_dhidden<__nv_bfloat16>, dim3(small_grid(items)), kSmallThreads, 0, s, acc,
+                             p.splits, tokens, width8, unscale, static_cast<__nv_bfloat16*>(dhidden), dhidden_stride));
   return ZERO_OK;
 }
 
