@@ -962,7 +962,7 @@ class GradClip(_Owner):
         flat = [g for rank in grads for g in rank]
         if len(grads) != self.W or list(map(T.numel, flat)) != self._expected:
             raise ValueError(f"grads must be {self.W} lists of tensors of the owner's sizes")
-        if any(g.dtype != self.torch_dtype for g in flat) or not all(map(T.is_contiguous, flat)):
+        if {g.dtype for g in flat} - {self.torch_dtype} or not all(map(T.is_contiguous, flat)):
             raise ValueError(f"gradients must be contiguous and {self.torch_dtype}")
         return _u64_array(map(T.data_ptr, flat))
 

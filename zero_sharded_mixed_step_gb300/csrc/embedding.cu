@@ -114,13 +114,13 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The lanes whose `bits`-bit digit equals this lane's, one vote for each bit
-// (the match instruction takes time with every different value: it made a
-// pass over 32 unequal digits cost 2,500 cycles).  Lanes without a pair match
-// nobody's.
-__device__ __forceinline__ unsigned same_digit(int digit, bool real, int bits) {
+// The lanes whose 8-bit digit equals this lane's, by one vote for each bit
+// (the match instruction takes time with every different value: a pass over
+// 32 unequal digits took 2,500 cycles).  Lanes without a pair match nobody's.
+__device__ __forceinline__ unsigned same_digit(int digit, bool real) {
   unsigned same = __ballot_sync(0xffffffffu, real);
-  for (int b = 0; b < bits; ++b) {
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
     const unsigned one = __ballot_sync(0xffffffffu, (digit >> b) & 1);
     same &= (digit >> b) & 1 ? one : ~one;
   }
@@ -171,16 +171,20 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     };
     for (int d = lane; d < kRadix; d += 32) count[warp][d] = 0;
     __syncwarp();
-    for (int g = g0; g < g1; g += kSortBatch) {
-      int2 x[kSortBatch];
+    // a batch of groups: their pairs, and which lanes share each one's digit
+    int2 x[kSortBatch];
+    unsigned same[kSortBatch];
+    auto load = [&](int g) {
 #pragma unroll
       for (int u = 0; u < kSortBatch; ++u) x[u] = g + u < g1 ? pair_at((g + u) * 32 + lane) : make_int2(-1, 0);
 #pragma unroll
+      for (int u = 0; u < kSortBatch; ++u) same[u] = same_digit((x[u].x >> shift) & mask, x[u].x >= 0);
+    };
+    for (int g = g0; g < g1; g += kSortBatch) {
+      load(g);
+#pragma unroll
       for (int u = 0; u < kSortBatch; ++u) {
-        if (g + u >= g1) break;
-        const int d = (x[u].x >> shift) & mask;
-        const unsigned same = same_digit(d, x[u].x >= 0, a.bits);
-        if (same && (same & ((1u << lane) - 1)) == 0) count[warp][d] += __popc(same);
+        if (same[u] && (same[u] & ((1u << lane) - 1)) == 0) count[warp][(x[u].x >> shift) & mask] += __popc(same[u]);
         __syncwarp();
       }
     }
@@ -223,22 +227,17 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     for (int d = lane; d < kRadix; d += 32) count[warp][d] += digit_base[d];
     __syncwarp();
     for (int g = g0; g < g1; g += kSortBatch) {
-      int2 x[kSortBatch];
-#pragma unroll
-      for (int u = 0; u < kSortBatch; ++u) x[u] = g + u < g1 ? pair_at((g + u) * 32 + lane) : make_int2(-1, 0);
+      if (g1 - g0 > kSortBatch) load(g);   // else the one batch is still there
 #pragma unroll
       for (int u = 0; u < kSortBatch; ++u) {
-        if (g + u >= g1) break;
-        const bool real = x[u].x >= 0;
         const int d = (x[u].x >> shift) & mask;
-        const unsigned same = same_digit(d, real, a.bits);
-        const int ahead = __popc(same & ((1u << lane) - 1));
+        const int ahead = __popc(same[u] & ((1u << lane) - 1));
         int at = 0;
-        if (real) at = count[warp][d] + ahead;
+        if (same[u]) at = count[warp][d] + ahead;
         __syncwarp();
-        if (real && ahead == 0) count[warp][d] += __popc(same);
+        if (same[u] && ahead == 0) count[warp][d] = at + __popc(same[u]);
         __syncwarp();
-        if (real) __stcg(out + at, x[u]);
+        if (same[u]) __stcg(out + at, x[u]);
       }
     }
     // the pairs of this pass, and everyone's reads of cta_count, before the next pass

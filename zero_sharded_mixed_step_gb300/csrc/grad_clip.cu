@@ -7,8 +7,9 @@
 // zero_grad_norm computes norm, zero_grad_clip writes round(coef g), and
 // zero_step_clipped runs the step on coef g: its first pass reads the W
 // gradient vectors once, keeps g in fp32 and sums the squares, its second
-// runs Adam on coef g.  Reading the fp32 mean back costs 8 bytes an element
-// (written and read) where reading the W gradients again would cost 2 W.
+// runs Adam on coef g.  The fp32 mean costs 8 bytes an element (written and
+// read) where reading the W gradients again would cost 2 W, which is faster
+// for 1 and 2 ranks.
 //
 // Squares are summed in fp32 by each thread and in fp64 from there on: within
 // a block, and over the blocks in their order by the last block to finish, so
@@ -36,8 +37,16 @@ using host::ceil_div;
 using host::fail;
 
 constexpr int kThreads = 256;
+// Blocks of the mean pass on each SM: 2 took 918 us for the whole clipped step of
+// 124M elements of 8 ranks, 3 took 927 and 4 took 936.
+constexpr int kMeanBlocksPerSm = 2;
 constexpr int kMaxBlocks = 1024;           // partial sums of one launch
 constexpr double kClipEps = 1e-6;
+// Up to this many ranks the clipped step reads the gradients twice (4 W bytes an
+// element) instead of writing and reading their fp32 mean (2 W + 8).  At 60M
+// elements: 1 rank 312 us, 2 ranks 312, 3 ranks 388 against 381 for 4 through
+// the mean.
+constexpr int kDirectRanks = 2;
 
 // Workspace: the number of blocks that have finished (0 between calls), then
 // a partial sum of squares for each block.
@@ -82,6 +91,12 @@ struct Eight<float> {
   static __device__ __forceinline__ float load1(const float* p) { return *p; }
   static __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 };
+
+__device__ __forceinline__ void ld_32B_words(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
 
 // ---- sums over the blocks ---------------------------------------------------------
 
@@ -171,6 +186,38 @@ __device__ __forceinline__ void sum_ranks8(F rank, int64_t i, int W, float (&sum
   }
 }
 
+// The same for 16 elements, in 32-byte loads where `wide` says that every
+// rank's vector allows them.
+template <typename T, int WC, typename F>
+__device__ __forceinline__ void sum_ranks16(F rank, int64_t i, int W, bool wide, float (&sum)[2][8]) {
+  constexpr int kAtOnce = WC > 0 && WC <= 8 ? WC : 8;
+  for (int w0 = 0; w0 < (WC > 0 ? WC : W); w0 += kAtOnce) {
+    uint4 raw[kAtOnce][2];
+#pragma unroll
+    for (int w = 0; w < kAtOnce; ++w) {
+      if (WC > 0 || w0 + w < W) {
+        if (wide) {
+          ld_32B_words(rank(w0 + w) + i, raw[w][0], raw[w][1]);
+        } else {
+          raw[w][0] = ld_16B(rank(w0 + w) + i);
+          raw[w][1] = ld_16B(rank(w0 + w) + i + 8);
+        }
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < kAtOnce; ++w) {
+      if (WC == 0 && w0 + w >= W) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float f[8];
+        Fmt<T>::unpack8(raw[w][h], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[h][k] = w0 + w == 0 ? f[k] : __fadd_rn(sum[h][k], f[k]);
+      }
+    }
+  }
+}
+
 template <typename T, typename F>
 __device__ __forceinline__ float mean1(F rank, int64_t i, int W, bool pow2, float inv_w) {
   float g = Eight<T>::load1(rank(0) + i);
@@ -225,7 +272,6 @@ template <typename T, int WC, bool CLIP>
 __global__ void __launch_bounds__(kThreads) tensors_pass(const __grid_constant__ Table t, NormSpace ws,
                                                          unsigned int first, unsigned int blocks, float* norm,
                                                          float max_norm) {
-  allow_next();
   await_previous();
   const int W = WC > 0 ? WC : t.W;
   const bool pow2 = (W & (W - 1)) == 0;
@@ -299,37 +345,43 @@ struct MeanNormArgs {
   int W;
   const void* grads[kMaxRanks];
   int64_t n;
-  float* mean;
+  float* mean;               // NULL: the update will read the gradients again
+  int wide;                  // every gradient vector is 32-byte aligned
   float inv_w;
   NormSpace ws;
   float* norm;
 };
 
+// 16 elements of each rank at a time in one 32-byte load (as 8, at twice the
+// threads, the pass ran at 0.94 of this rate).
 template <typename GT, int WC>
 __global__ void __launch_bounds__(kThreads) mean_norm_pass(const __grid_constant__ MeanNormArgs a) {
-  allow_next();
   await_previous();
   const int W = WC > 0 ? WC : a.W;
   const bool pow2 = (W & (W - 1)) == 0;
   auto rank = [&](int w) { return static_cast<const GT*>(a.grads[w]); };
   float squares = 0.f;
-  const int64_t groups = a.n >> 3;
+  const int64_t groups = a.n >> 4;
+  const bool wide = a.wide;
   for (int64_t gi = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; gi < groups;
        gi += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t i = gi << 3;
-    float sum[8];
-    sum_ranks8<GT, WC>(rank, i, W, sum);
+    const int64_t i = gi << 4;
+    float sum[2][8];
+    sum_ranks16<GT, WC>(rank, i, W, wide, sum);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      sum[k] = rank_mean(sum[k], W, a.inv_w, pow2);
-      squares = fmaf(sum[k], sum[k], squares);
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        sum[h][k] = rank_mean(sum[h][k], W, a.inv_w, pow2);
+        squares = fmaf(sum[h][k], sum[h][k], squares);
+      }
+      if (a.mean) st_32B(a.mean + i + 8 * h, sum[h]);
     }
-    st_32B(a.mean + i, sum);
   }
   if (blockIdx.x == 0) {
-    for (int64_t e = (groups << 3) + threadIdx.x; e < a.n; e += kThreads) {
+    for (int64_t e = (groups << 4) + threadIdx.x; e < a.n; e += kThreads) {
       const float g = mean1<GT>(rank, e, W, pow2, a.inv_w);
-      a.mean[e] = g;
+      if (a.mean) a.mean[e] = g;
       squares = fmaf(g, g, squares);
     }
   }
@@ -338,6 +390,7 @@ __global__ void __launch_bounds__(kThreads) mean_norm_pass(const __grid_constant
 
 struct ClippedArgs {
   const float* mean;
+  const void* grads[kDirectRanks];
   float* master;
   float* m;
   float* v;
@@ -347,17 +400,20 @@ struct ClippedArgs {
   float max_norm;
 };
 
-// Adam on coef * mean over a segment; the ZeRO-3 gather of its old 16-bit
-// values (pre_out) as in the fused step.  A norm that is not finite leaves
-// the state as it was.
-template <typename OT>
+// Adam on coef * g over a segment; the ZeRO-3 gather of its old 16-bit values
+// (pre_out) as in the fused step.  g comes from the fp32 mean (WC == 0) or
+// again from the WC ranks' gradients.  A norm that is not finite leaves the
+// state as it was.  The groups run from the segment's end to its start: the
+// end of the mean is what L2 still holds of the pass before.
+template <typename GT, typename OT, int WC>
 __global__ void __launch_bounds__(kThreads) clipped_update(const __grid_constant__ ClippedArgs a) {
-  allow_next();
   await_previous();
+  constexpr bool pow2 = (WC & (WC - 1)) == 0;
   const Seg& seg = a.segs[blockIdx.y];
   const float norm = *a.norm;
   const bool update = isfinite(norm);
   const float coef = update ? clip_coef(norm, a.max_norm) : 0.f;
+  auto rank = [&](int w) { return static_cast<const GT*>(a.grads[w]); };
   OT* out = static_cast<OT*>(seg.out);
   OT* pre = static_cast<OT*>(seg.pre_out);
   if (!update && !pre) return;
@@ -369,15 +425,18 @@ __global__ void __launch_bounds__(kThreads) clipped_update(const __grid_constant
     const int64_t j = e - lo;
     if (pre) pre[j] = out[j];
     if (!update) return;
+    float g;
+    if constexpr (WC > 0) g = mean1<GT>(rank, e, WC, pow2, a.coef.inv_w);
+    else g = a.mean[e];
     float th = a.master[e], m = a.m[e], v = a.v[e];
-    adam_element(__fmul_rn(a.mean[e], coef), th, m, v, a.coef);
+    adam_element(__fmul_rn(g, coef), th, m, v, a.coef);
     a.master[e] = th;
     a.m[e] = m;
     a.v[e] = v;
     Fmt<OT>::store1(out, j, th);
   };
-  for (int64_t g = g0 + static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; g < g1;
-       g += static_cast<int64_t>(gridDim.x) * kThreads) {
+  for (int64_t g = g1 - 1 - (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x); g >= g0;
+       g -= static_cast<int64_t>(gridDim.x) * kThreads) {
     const int64_t i = g << 3, j = i - lo;
     if (pre) {
       if (pre_vec) {
@@ -389,10 +448,27 @@ __global__ void __launch_bounds__(kThreads) clipped_update(const __grid_constant
     }
     if (!update) continue;
     float x[8], th[8], m[8], v[8];
-    ld_32B(a.mean + i, x);
+    typename Eight<GT>::Raw raw[WC > 0 ? WC : 1];
+    if constexpr (WC > 0) {
+#pragma unroll
+      for (int w = 0; w < WC; ++w) raw[w] = Eight<GT>::raw(rank(w) + i);
+    } else {
+      ld_32B(a.mean + i, x);
+    }
     ld_32B(a.master + i, th);
     ld_32B(a.m + i, m);
     ld_32B(a.v + i, v);
+    if constexpr (WC > 0) {
+#pragma unroll
+      for (int w = 0; w < WC; ++w) {
+        float f[8];
+        Eight<GT>::unpack(raw[w], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = w == 0 ? f[k] : __fadd_rn(x[k], f[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = rank_mean(x[k], WC, a.coef.inv_w, pow2);
+    }
 #pragma unroll
     for (int k = 0; k < 8; ++k) adam_element(__fmul_rn(x[k], coef), th[k], m[k], v[k], a.coef);
     st_32B(a.master + i, th);
@@ -410,6 +486,22 @@ __global__ void __launch_bounds__(kThreads) clipped_update(const __grid_constant
     for (int64_t e = lo + threadIdx.x; e < head; e += kThreads) one(e);
     for (int64_t e = tail + threadIdx.x; e < hi; e += kThreads) one(e);
   }
+}
+
+using ClippedFn = void (*)(const ClippedArgs);
+
+template <typename GT, typename OT>
+ClippedFn pick_clipped_w(int direct) {
+  switch (direct) {
+    case 1: return clipped_update<GT, OT, 1>;
+    case 2: return clipped_update<GT, OT, 2>;
+    default: return clipped_update<float, OT, 0>;
+  }
+}
+
+ClippedFn pick_clipped(int gdt, int wdt, int direct) {
+  if (gdt == kF16) return wdt == kF16 ? pick_clipped_w<__half, __half>(direct) : pick_clipped_w<__half, __nv_bfloat16>(direct);
+  return wdt == kF16 ? pick_clipped_w<__nv_bfloat16, __half>(direct) : pick_clipped_w<__nv_bfloat16, __nv_bfloat16>(direct);
 }
 
 using MeanNormFn = void (*)(const MeanNormArgs);
@@ -538,13 +630,15 @@ cudaError_t launch_mean_norm(int W, int grad_dtype, const void* const* grads, in
   a.W = W;
   for (int w = 0; w < W; ++w) a.grads[w] = grads[w];
   a.n = n_pad;
-  a.mean = clip_mean(workspace);
+  a.mean = W <= kDirectRanks ? nullptr : clip_mean(workspace);
+  a.wide = 1;
+  for (int w = 0; w < W; ++w) a.wide = a.wide && host::aligned32(grads[w]);
   a.inv_w = static_cast<float>(1.0 / W);
   a.ws = norm_space(workspace);
   a.norm = norm;
   const MeanNormFn fn = grad_dtype == kF16 ? pick_mean_norm<__half>(W) : pick_mean_norm<__nv_bfloat16>(W);
-  const int64_t resident = static_cast<int64_t>(sm_count()) * 5;
-  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>({n_pad / 8 / kThreads + 1, resident, kMaxBlocks}));
+  const int64_t resident = static_cast<int64_t>(sm_count()) * kMeanBlocksPerSm;
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>({n_pad / 16 / kThreads + 1, resident, kMaxBlocks}));
   ++*launches;
   return launch_chained(fn, dim3(static_cast<unsigned>(blocks)), kThreads, 0, stream, a);
 }
@@ -554,7 +648,9 @@ cudaError_t launch_clipped_update(const FusedLaunch& f, const float* mean, const
   if (f.nseg <= 0) return cudaSuccess;
   ClippedArgs a;
   std::memset(&a, 0, sizeof a);
+  const int direct = f.W <= kDirectRanks ? f.W : 0;
   a.mean = mean;
+  for (int w = 0; w < direct; ++w) a.grads[w] = f.grads[w];
   a.master = f.master;
   a.m = f.m;
   a.v = f.v;
@@ -570,8 +666,7 @@ cudaError_t launch_clipped_update(const FusedLaunch& f, const float* mean, const
   const int64_t bx = std::max<int64_t>(1, std::min<int64_t>(per_seg, longest / 8 / kThreads + 1));
   const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>(f.nseg));
   ++*launches;
-  return launch_chained(f.work_dtype == kF16 ? clipped_update<__half> : clipped_update<__nv_bfloat16>, grid, kThreads, 0,
-                        stream, a);
+  return launch_chained(pick_clipped(f.grad_dtype, f.work_dtype, direct), grid, kThreads, 0, stream, a);
 }
 
 }  // namespace zero
