@@ -178,7 +178,8 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
 #pragma unroll
       for (int u = 0; u < kSortBatch; ++u) x[u] = g + u < g1 ? pair_at((g + u) * 32 + lane) : make_int2(-1, 0);
 #pragma unroll
-      for (int u = 0; u < kSortBatch; ++u) same[u] = same_digit((x[u].x >> shift) & mask, x[u].x >= 0);
+      for (int u = 0; u < kSortBatch; ++u)
+        same[u] = g + u < g1 ? same_digit((x[u].x >> shift) & mask, x[u].x >= 0) : 0u;
     };
     for (int g = g0; g < g1; g += kSortBatch) {
       load(g);
@@ -247,13 +248,16 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
 
 // ---- summing the runs ---------------------------------------------------------------
 //
-// One CTA per chunk of sorted pairs, a thread per 8 columns.  Runs that lie
-// inside the chunk are written at once; the part of a run that goes on from
-// the chunk before (head) or into the chunk after (tail) is left in workspace
-// in fp32, the run is noted, and embed_join adds its parts in order.
+// One CTA per chunk of sorted pairs, a thread per 8 columns.  A run of at most
+// a chunk's length belongs to the chunk it begins in, whole, even where it
+// ends in the next one, and is written at once.  A longer run is cut at the
+// chunks: its part of each is left in workspace in fp32 (head: it goes on from
+// the chunk before; tail: it begins here and goes on), the run is noted, and
+// embed_join adds its parts in order.
 
 constexpr int kMinChunk = 8, kMaxChunk = 64;
-constexpr int kRunBatch = 8;          // rows whose loads a thread has in flight
+constexpr int kAddBatch = 4;          // (with 8, two CTAs fewer fit an SM)
+
 
 struct RunArgs {
   const int2* pairs;
@@ -281,54 +285,72 @@ template <typename T, bool ADD>
 __global__ void __launch_bounds__(256) embed_runs(const RunArgs a) {
   allow_next();
   await_previous();
-  __shared__ int key[kMaxChunk + 2];   // the chunk's, with one before and one after (-1: none)
-  __shared__ int val[kMaxChunk];
-  const int first = blockIdx.x * a.chunk, count = min(a.chunk, a.tokens - first);
-  for (int k = threadIdx.x; k < count + 2; k += blockDim.x) {
-    const int i = first + k - 1;
-    const int2 x = i >= 0 && i < a.tokens ? a.pairs[i] : make_int2(-1, 0);
+  // pairs first - chunk - 1 .. first + 2 chunk (ids -1 and -2 outside the list)
+  __shared__ int key[3 * kMaxChunk + 2];
+  __shared__ int val[3 * kMaxChunk + 2];
+  __shared__ int edge[4];
+  const int c = a.chunk, first = blockIdx.x * c, last = min(first + c, a.tokens) - 1, low = first - c - 1;
+  for (int k = threadIdx.x; k < 3 * c + 2; k += blockDim.x) {
+    const int i = low + k;
+    const int2 x = i < 0 ? make_int2(-1, 0) : i < a.tokens ? a.pairs[i] : make_int2(-2, 0);
     key[k] = x.x;
-    if (k >= 1 && k <= count) val[k - 1] = x.y;
+    val[k] = x.y;
+  }
+  // where the first pair's run begins and ends, and the last pair's; far
+  // enough away where the window does not show it
+  if (threadIdx.x < 4) edge[threadIdx.x] = threadIdx.x % 2 == 0 ? low : first + 2 * c + 1;
+  __syncthreads();
+  for (int k = threadIdx.x + 1; k < 3 * c + 2; k += blockDim.x) {
+    if (key[k] == key[k - 1]) continue;
+    const int i = low + k;   // a run begins at i, and one ends
+    if (i <= first) atomicMax(&edge[0], i);
+    else atomicMin(&edge[1], i);
+    if (i <= last) atomicMax(&edge[2], i);
+    else atomicMin(&edge[3], i);
   }
   __syncthreads();
-  const int last_key = key[count];
-  // begins here and goes on: the last key continues, and its run did not come from before
-  if (threadIdx.x == 0 && last_key < a.vocab && key[count + 1] == last_key && key[0] != last_key)
-    a.runs[1 + atomicAdd(a.runs, 1)] = blockIdx.x;
+  const bool long0 = edge[1] - edge[0] > c, long1 = edge[3] - edge[2] > c;
+  const bool began_before = edge[0] < first, begins_here = edge[2] >= first;
+  const int begin = began_before && !long0 ? min(edge[1], last + 1) : first;
+  const int end = begins_here && !long1 ? edge[3] : last + 1;
+  const bool continues = long1 && edge[3] > last + 1;     // the last pair's run, into the next chunk
+  const bool head_first = began_before && long0;
+  if (threadIdx.x == 0 && begins_here && continues && key[last - low] < a.vocab) a.runs[1 + atomicAdd(a.runs, 1)] = blockIdx.x;
   const T* dout = static_cast<const T*>(a.dout);
   const int64_t width = static_cast<int64_t>(a.width8) * 8;
   float* head = a.parts + static_cast<int64_t>(blockIdx.x) * 2 * width;
+  constexpr int kRunBatch = ADD ? kAddBatch : 8;   // rows whose loads a thread has in flight
   for (int c8 = threadIdx.x; c8 < a.width8; c8 += blockDim.x) {
-    const int64_t c = static_cast<int64_t>(c8) * 8;
+    const int64_t col = static_cast<int64_t>(c8) * 8;
     float sum[8];
-    bool from_before = key[1] == key[0];   // the run that is being summed began in an earlier chunk
+    bool from_before = head_first;
 #pragma unroll
     for (int q = 0; q < 8; ++q) sum[q] = 0.f;
-    for (int k0 = 0; k0 < count; k0 += kRunBatch) {
+    for (int k0 = begin - low; k0 < end - low; k0 += kRunBatch) {
       uint4 x[kRunBatch], old[ADD ? kRunBatch : 1];
 #pragma unroll
       for (int k = 0; k < kRunBatch; ++k) {
         x[k] = make_uint4(0, 0, 0, 0);
         if (ADD) old[k] = x[k];
-        if (k0 + k < count && key[k0 + k + 1] < a.vocab) {
-          x[k] = dev::ld_16B(dout + val[k0 + k] * a.dout_stride + c);
-          if (ADD && key[k0 + k + 2] != key[k0 + k + 1])
-            old[k] = dev::ld_16B(static_cast<const T*>(a.dtable) + key[k0 + k + 1] * a.dtable_stride + c);
+        if (k0 + k < end - low && key[k0 + k] < a.vocab) {
+          x[k] = dev::ld_16B(dout + val[k0 + k] * a.dout_stride + col);
+          if (ADD && key[k0 + k + 1] != key[k0 + k])
+            old[k] = dev::ld_16B(static_cast<const T*>(a.dtable) + key[k0 + k] * a.dtable_stride + col);
         }
       }
 #pragma unroll
       for (int k = 0; k < kRunBatch; ++k) {
-        if (k0 + k >= count) break;
+        if (k0 + k >= end - low) break;
         float f[8];
         Fmt<T>::unpack8(x[k], f);
 #pragma unroll
         for (int q = 0; q < 8; ++q) sum[q] += f[q];
-        const int id = key[k0 + k + 1];
-        const bool goes_on = key[k0 + k + 2] == id;
-        if (k0 + k == count - 1 || !goes_on) {
-          if (from_before) dev::st_32B(head + c, sum);
-          else if (goes_on) dev::st_32B(head + width + c, sum);
-          else if (id < a.vocab) write_row<T, ADD>(a, id, c, sum, old[ADD ? k : 0]);
+        const int id = key[k0 + k];
+        const bool at_end = k0 + k == end - low - 1;
+        if (at_end || key[k0 + k + 1] != id) {
+          if (from_before) dev::st_32B(head + col, sum);
+          else if (at_end && continues) dev::st_32B(head + width + col, sum);
+          else if (id < a.vocab) write_row<T, ADD>(a, id, col, sum, old[ADD ? k : 0]);
           from_before = false;
 #pragma unroll
           for (int q = 0; q < 8; ++q) sum[q] = 0.f;
@@ -338,7 +360,7 @@ __global__ void __launch_bounds__(256) embed_runs(const RunArgs a) {
   }
 }
 
-// The runs that go past the chunk they begin in.  An item is one run and 256
+// The long runs.  An item is one run and 256
 // columns; kJoinSlices groups of 32 threads each add a stretch of the run's
 // parts, and the first adds the stretches, in order.
 constexpr int kJoinSlices = 8;
@@ -397,11 +419,12 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join(const RunArgs a) {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 24, kMaxVocab = int64_t(1) << 24, kMaxWidth = int64_t(1) << 16;
 
-// Sorted pairs per chunk: 600 to 1200 chunks where the tokens allow it (4 to 8
-// CTAs for each SM), a power of two.
+// Sorted pairs per chunk, a power of two: 608 to 1215 chunks where the tokens
+// allow it (4 to 8 for each SM).
+constexpr int kChunks = 608;
 int chunk_of(int64_t tokens) {
   int c = kMinChunk;
-  while (c < kMaxChunk && tokens / (2 * c) >= 608) c *= 2;
+  while (c < kMaxChunk && tokens / (2 * c) >= kChunks) c *= 2;
   return c;
 }
 
@@ -434,7 +457,7 @@ int64_t pairs_bytes(int64_t tokens) { return round_up(tokens * 8, 256); }
 
 // Most chunks that any count up to `tokens` is cut into.
 int64_t most_chunks(int64_t tokens) {
-  return std::min(ceil_div(tokens, kMinChunk), std::max<int64_t>(1217, ceil_div(tokens, kMaxChunk)));
+  return std::min(ceil_div(tokens, kMinChunk), std::max<int64_t>(2 * kChunks + 1, ceil_div(tokens, kMaxChunk)));
 }
 
 int64_t runs_bytes(int64_t tokens) { return round_up((most_chunks(tokens) + 1) * 4, 256); }
