@@ -772,20 +772,29 @@ def _on(stream):
     return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
 
 
+def _stream_getter():
+    import torch
+    # a tenth of a microsecond where torch.cuda.current_stream takes three
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _current_stream(index):
     """The handle of the device's current stream."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)      # a tenth of a microsecond instead of three
-    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+    global _current_stream
+    _current_stream = _stream_getter()
+    return _current_stream(index)
 
 
 def _rows(x, what, rows, width, dtype):
     """(address, row stride) of a matrix of 16-bit rows; raises ValueError where it is none."""
-    if x.dim() != 2 or x.dtype != dtype or x.shape[1] != width or (rows is not None and x.shape[0] != rows) or \
-            not x.is_cuda or (width > 1 and x.stride(1) != 1):
-        raise ValueError(f"{what} must be a CUDA tensor of {'any number of' if rows is None else rows} rows of {width} "
-                         f"adjacent {dtype} values, not {x.dtype} {tuple(x.shape)} with strides {x.stride()}")
-    return x.data_ptr(), (x.stride(0) if x.shape[0] > 1 else width)
+    shape = x.shape
+    if len(shape) == 2 and shape[0] == rows and shape[1] == width and x.dtype is dtype and x.is_cuda:
+        stride, step = x.stride()
+        if step == 1 or width == 1:
+            return x.data_ptr(), (stride if rows > 1 else width)
+    raise ValueError(f"{what} must be a CUDA tensor of {rows} rows of {width} adjacent {dtype} values, not {x.dtype} "
+                     f"{tuple(shape)} with strides {x.stride()}")
 
 
 def _ids(x, what):
@@ -808,7 +817,19 @@ class _Owner:
         self.stream = stream
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device() if torch.cuda.is_available() else 0)
+        self._index, self._new, self._fp32 = self.device.index, torch.empty, torch.float32
         self._alloc = alloc or (lambda numel, dt: torch.zeros(numel, dtype=dt, device=self.device))
+
+    def _bind(self, name):
+        """The C entry point, raising like its wrapper: the owners' calls are
+        short enough for the wrapper's own conversions to count."""
+        fn = getattr(lib(), name)
+
+        def call(*args):
+            rc = fn(*args)
+            if rc < 0:
+                raise ZeroError(rc, name, lib().zero_last_error().decode())
+        return call
 
     def _workspace(self, nbytes):
         with _on(self.stream):
@@ -818,14 +839,14 @@ class _Owner:
 
     def _raw_stream(self):
         if self.stream is None:
-            return _current_stream(self.device.index) or None
+            return _current_stream(self._index) or None
         return self.stream.cuda_stream or None
 
     def _empty(self, shape, dtype):
         if self.stream is None:
-            return self.torch.empty(shape, dtype=dtype, device=self.device)
+            return self._new(shape, dtype=dtype, device=self.device)
         with _on(self.stream):
-            return self.torch.empty(shape, dtype=dtype, device=self.device)
+            return self._new(shape, dtype=dtype, device=self.device)
 
     def _check_tokens(self, count):
         if count > self.max_tokens:
@@ -845,6 +866,7 @@ class LmLoss(_Owner):
         self.vocab, self.width, self.max_tokens = int(vocab), int(width), int(max_tokens)
         self.with_grad = bool(with_grad)
         self._workspace(zero_lm_workspace_bytes(self.max_tokens, self.vocab, self.width, self.with_grad))
+        self._loss, self._grad = self._bind("zero_lm_loss"), self._bind("zero_lm_loss_grad")
 
     def loss(self, hidden, table, targets, loss=None, lse=None):
         """(loss, lse) of each token, fp32; loss is 0 where the target lies outside the vocabulary."""
@@ -853,10 +875,10 @@ class LmLoss(_Owner):
         h, hs = _rows(hidden, "hidden", tokens, self.width, self.torch_dtype)
         t, ts = _rows(table, "table", self.vocab, self.width, self.torch_dtype)
         ids, id_bytes = _ids(targets, "targets")
-        loss = self._vector(loss, tokens)
-        lse = self._vector(lse, tokens)
-        zero_lm_loss(tokens, self.vocab, self.width, self.dtype, h, hs, t, ts, ids, id_bytes, loss.data_ptr(),
-                     lse.data_ptr(), self._ws, self.workspace_bytes, self._raw_stream())
+        loss = self._empty(tokens, self._fp32) if loss is None else self._vector(loss, tokens)
+        lse = self._empty(tokens, self._fp32) if lse is None else self._vector(lse, tokens)
+        self._loss(tokens, self.vocab, self.width, self.dtype, h, hs, t, ts, ids, id_bytes, loss.data_ptr(),
+                   lse.data_ptr(), self._ws, self.workspace_bytes, self._raw_stream())
         return loss, lse
 
     def grad(self, hidden, table, targets, lse, scale, dhidden=None, dtable=None, accumulate=False):
@@ -870,21 +892,23 @@ class LmLoss(_Owner):
         h, hs = _rows(hidden, "hidden", tokens, self.width, self.torch_dtype)
         t, ts = _rows(table, "table", self.vocab, self.width, self.torch_dtype)
         ids, id_bytes = _ids(targets, "targets")
-        lse = self._vector(lse, tokens)
+        self._vector(lse, tokens)
         if dhidden is None:
             dhidden = self._empty((tokens, self.width), self.torch_dtype)
+            dh, dhs = dhidden.data_ptr(), self.width
+        else:
+            dh, dhs = _rows(dhidden, "dhidden", tokens, self.width, self.torch_dtype)
         if dtable is None:
             dtable = self._empty((self.vocab, self.width), self.torch_dtype)
-        dh, dhs = _rows(dhidden, "dhidden", tokens, self.width, self.torch_dtype)
-        dt, dts = _rows(dtable, "dtable", self.vocab, self.width, self.torch_dtype)
-        zero_lm_loss_grad(tokens, self.vocab, self.width, self.dtype, h, hs, t, ts, ids, id_bytes, lse.data_ptr(),
-                          scale, dh, dhs, dt, dts, accumulate, self._ws, self.workspace_bytes, self._raw_stream())
+            dt, dts = dtable.data_ptr(), self.width
+        else:
+            dt, dts = _rows(dtable, "dtable", self.vocab, self.width, self.torch_dtype)
+        self._grad(tokens, self.vocab, self.width, self.dtype, h, hs, t, ts, ids, id_bytes, lse.data_ptr(), scale, dh,
+                   dhs, dt, dts, 1 if accumulate else 0, self._ws, self.workspace_bytes, self._raw_stream())
         return dhidden, dtable
 
     def _vector(self, x, tokens):
-        if x is None:
-            return self._empty(tokens, self.torch.float32)
-        if x.dtype != self.torch.float32 or x.numel() != tokens or not x.is_contiguous() or not x.is_cuda:
+        if x.dtype != self._fp32 or x.numel() != tokens or not x.is_contiguous() or not x.is_cuda:
             raise ValueError(f"loss and lse must be contiguous CUDA tensors of {tokens} fp32 values")
         return x
 
@@ -903,6 +927,7 @@ class Embedding(_Owner):
         self.vocab, self.width, self.max_tokens = int(vocab), int(width), int(max_tokens)
         self.scale = float(scale)
         self._workspace(zero_embedding_workspace_bytes(self.max_tokens, self.width))
+        self._lookup, self._grad = self._bind("zero_embedding"), self._bind("zero_embedding_grad")
 
     def forward(self, tokens, table, out=None):
         """scale * table[tokens], one row per id (0 for an id outside the table)."""
@@ -911,9 +936,11 @@ class Embedding(_Owner):
         ids, id_bytes = _ids(tokens, "tokens")
         if out is None:
             out = self._empty((count, self.width), self.torch_dtype)
-        o, os_ = _rows(out, "out", count, self.width, self.torch_dtype)
-        zero_embedding(count, self.vocab, self.width, self.dtype, ids, id_bytes, t, ts, self.scale, o, os_,
-                       self._raw_stream())
+            o, os_ = out.data_ptr(), self.width
+        else:
+            o, os_ = _rows(out, "out", count, self.width, self.torch_dtype)
+        self._lookup(count, self.vocab, self.width, self.dtype, ids, id_bytes, t, ts, self.scale, o, os_,
+                     self._raw_stream())
         return out
 
     def grad(self, tokens, dout, dtable=None, accumulate=False):
@@ -926,9 +953,11 @@ class Embedding(_Owner):
         d, ds = _rows(dout, "dout", count, self.width, self.torch_dtype)
         if dtable is None:
             dtable = self._empty((self.vocab, self.width), self.torch_dtype)
-        t, ts = _rows(dtable, "dtable", self.vocab, self.width, self.torch_dtype)
-        zero_embedding_grad(count, self.vocab, self.width, self.dtype, ids, id_bytes, d, ds, self.scale, t, ts,
-                            accumulate, self._ws, self.workspace_bytes, self._raw_stream())
+            t, ts = dtable.data_ptr(), self.width
+        else:
+            t, ts = _rows(dtable, "dtable", self.vocab, self.width, self.torch_dtype)
+        self._grad(count, self.vocab, self.width, self.dtype, ids, id_bytes, d, ds, self.scale, t, ts,
+                   1 if accumulate else 0, self._ws, self.workspace_bytes, self._raw_stream())
         return dtable
 
 
@@ -956,6 +985,7 @@ class GradClip(_Owner):
             at += k
         self._offsets = offsets
         self._workspace(zero_grad_norm_workspace_bytes())
+        self._c_norm, self._c_clip = self._bind("zero_grad_norm"), self._bind("zero_grad_clip")
 
     def _pointers(self, grads):
         T = self.torch.Tensor
@@ -968,8 +998,8 @@ class GradClip(_Owner):
 
     def _norm(self, ptrs_at, stream):
         norm = self._empty(1, self.torch.float32)
-        _check("zero_grad_norm", lib().zero_grad_norm(self.W, len(self.numels), self._sizes_at, self.dtype, ptrs_at,
-                                                      norm.data_ptr(), self._ws, self.workspace_bytes, stream))
+        self._c_norm(self.W, len(self.numels), self._sizes_at, self.dtype, ptrs_at, norm.data_ptr(), self._ws,
+                     self.workspace_bytes, stream)
         return norm
 
     def _clip(self, ptrs_at, norm, max_norm, out, stream):
@@ -979,8 +1009,8 @@ class GradClip(_Owner):
             raise ValueError(f"out must be {self.n} contiguous values of {self.torch_dtype}")
         base = out.data_ptr()
         outs, outs_at = _u64_array([base + o for o in self._offsets])
-        _check("zero_grad_clip", lib().zero_grad_clip(self.W, len(self.numels), self._sizes_at, self.dtype, ptrs_at,
-                                                      norm.data_ptr(), max_norm, outs_at, stream))
+        self._c_clip(self.W, len(self.numels), self._sizes_at, self.dtype, ptrs_at, norm.data_ptr(), max_norm, outs_at,
+                     stream)
         return out
 
     def norm(self, grads):
