@@ -821,6 +821,16 @@ int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, int dtype, c
  */
 int zero_lm_status(void* stream);
 
+/*
+ * Testing the bounded waits: in the calling thread's next LM call the first
+ * tile's first block of operands never arrives.  The waits for it run out
+ * after about a second, the CTAs count a device error, wait (bounded) for the
+ * copies they did issue and return; what the call writes is not valid, and
+ * zero_lm_status then returns ZERO_E_STATE.  Nothing faults or hangs, and
+ * later calls are not affected.
+ */
+int zero_lm_inject_stall(void);
+
 /* Message for the calling thread's last error ("" if none). */
 const char* zero_last_error(void);
 

@@ -256,3 +256,34 @@ def test_owner_refusals():
         zs.LmLoss(40, 12, "fp16")
     with pytest.raises(zs.ZeroError):
         op.loss(torch.empty(20, 20, dtype=torch.float16, device="cuda")[:, :16], t, tg)   # rows of 40 bytes
+
+
+def test_more_tokens_than_one_slab():
+    """The loss goes over the tokens in slabs of 32768."""
+    h, t, tg = make(33_000, 70, 16, "bf16", seed=8)
+    *_, dh, dt, want = check(h, t, tg, scale=1 / 33_000)
+    assert ref.rel_norm(dh, want["dhidden"]) <= 2 * ref.HALF_ULP[h.dtype]
+
+
+@pytest.mark.parametrize("which", ["loss", "grad"])
+def test_a_lost_copy_is_reported(which):
+    """A block of operands that never arrives: the waits run out, the status
+    says so, and the next call works."""
+    h, t, tg = make(400, 3000, 640, "bf16")
+    op = zs.LmLoss(3000, 640, "bf16", max_tokens=400)
+    loss, lse = op.loss(h, t, tg)
+    grads = [x.clone() for x in op.grad(h, t, tg, lse, 1.0)]
+    op.status()
+    zs.zero_lm_inject_stall()
+    if which == "loss":
+        op.loss(h, t, tg)
+    else:
+        op.grad(h, t, tg, lse, 1.0)
+    with pytest.raises(zs.ZeroError) as e:
+        op.status()
+    assert e.value.code == zs.ZERO_E_STATE
+    op.status()                                   # reported once
+    loss2, lse2 = op.loss(h, t, tg)
+    assert torch.equal(loss2, loss) and torch.equal(lse2, lse)
+    assert all(torch.equal(x, y) for x, y in zip(op.grad(h, t, tg, lse, 1.0), grads))
+    op.status()

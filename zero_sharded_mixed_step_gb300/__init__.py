@@ -97,6 +97,7 @@ SIGNATURES = {
     "zero_lm_loss": (_I, [_L, _L, _L, _I, _P, _L, _P, _L, _P, _I, _P, _P, _P, _L, _P]),
     "zero_lm_loss_grad": (_I, [_L, _L, _L, _I, _P, _L, _P, _L, _P, _I, _P, _D, _P, _L, _P, _L, _I, _P, _L, _P]),
     "zero_lm_status": (_I, [_P]),
+    "zero_lm_inject_stall": (_I, []),
     "zero_last_error": (ctypes.c_char_p, []),
 }
 
@@ -494,6 +495,11 @@ def zero_lm_loss_grad(tokens, vocab, width, dtype, hidden, hidden_stride, table,
 def zero_lm_status(stream=None) -> None:
     """Wait for the stream; raises ZeroError if a bounded device wait of the LM kernels gave up."""
     _check("zero_lm_status", lib().zero_lm_status(_stream(stream)))
+
+
+def zero_lm_inject_stall() -> None:
+    """Testing: this thread's next LM call loses a block of operands, and its waits run out."""
+    _check("zero_lm_inject_stall", lib().zero_lm_inject_stall())
 
 
 # ---- convenience owners ---------------------------------------------------------

@@ -95,6 +95,7 @@ struct GemmArgs {
   CUtensorMap a[kMaxJobs], b[kMaxJobs];
   Job job[kMaxJobs];         // the longest tiles first
   int jobs;
+  int stall;                 // testing the bounded waits: the first pair's first block of K never arrives
   unsigned int* next;        // tiles handed out beyond one per pair (0 at the launch)
   int vocab;
   const void* targets;
@@ -427,7 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm
           const uint32_t bar = in_cta(full(s), 0);
           const uint32_t sa = ring + s * kStageBytes, sb = sa + kOperandBytes;
           const int k = kb * kTileK;
-          if (load_a) {
+          if (load_a && !(g.stall && pair == 0 && issued == 0)) {
             if (a_mn) {
               tma_load(sa, ma, am, k, bar);
               tma_load(sa + 8192, ma, am + 64, k, bar);
@@ -669,8 +670,12 @@ int make_map(CUtensorMap* map, int dtype, const void* base, int64_t rows, int64_
   return r == CUDA_SUCCESS ? ZERO_OK : fail(ZERO_E_CUDA, "encoding a tensor map failed (%d)", static_cast<int>(r));
 }
 
+thread_local bool g_stall_next = false;
+
 template <bool GRAD>
-int launch_gemm(const GemmArgs& g, int dtype, cudaStream_t s) {
+int launch_gemm(GemmArgs& g, int dtype, cudaStream_t s) {
+  g.stall = g_stall_next;
+  g_stall_next = false;
   const auto fn = dtype == ZERO_FP16 ? lm_gemm<__half, GRAD> : lm_gemm<__nv_bfloat16, GRAD>;
   ZERO_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem));
   int64_t tiles = 0;
@@ -709,14 +714,23 @@ int tile_width(int64_t width) {
 // Bytes of D at a time.  8192 tokens x 50257 x 768 took 2.73 ms with 32 MB, 1.99
 // with 64, 1.94 with 128, 1.95 with 256 and 1.91 with 512 (two launches in all).
 constexpr int64_t kPieceBytes = int64_t(128) << 20;
-constexpr int64_t kMinPiece = 2048;
+// At least so many rows of the vocabulary at a time (the table's gradient is
+// complete over the tokens, so its tiles take 256), while D of them stays
+// below kMostPieceBytes.
+constexpr int64_t kMinPiece = 2048, kLeastPiece = 256;
+constexpr int64_t kMostPieceBytes = int64_t(1) << 30;
 constexpr int kMaxSplits = 64;
 constexpr int kMinLossTile = 96;
 
+int64_t piece_rows(int64_t tokens) {
+  const int64_t row = 2 * std::max<int64_t>(tokens, 1);   // bytes of D per row of the vocabulary
+  const int64_t least = std::max(kLeastPiece, std::min(kMinPiece, kMostPieceBytes / row / 256 * 256));
+  return std::max(least, kPieceBytes / row / 256 * 256);
+}
+
 GradPlan plan_grad(int64_t tokens, int64_t vocab, int64_t width) {
   GradPlan p;
-  const int64_t by_bytes = kPieceBytes / (2 * std::max<int64_t>(tokens, 1)) / 256 * 256;
-  p.piece = std::min(round_up(vocab, 256), std::max(kMinPiece, by_bytes));
+  p.piece = std::min(round_up(vocab, 256), piece_rows(tokens));
   p.bn = tile_width(width);
   const int64_t tiles = ceil_div(tokens, kTileM) * ceil_div(width, p.bn);
   const int64_t kb = ceil_div(std::min(p.piece, vocab), kTileK);
@@ -761,7 +775,12 @@ int loss_tile(int64_t tokens, int64_t vocab) {
   return best;
 }
 
+// The loss goes over the tokens in slabs: its partial sums take 16 bytes for
+// each token and 256 columns, which must not grow with the batch.
+constexpr int64_t kSlab = 32768;
+
 int64_t loss_space(int64_t tokens, int64_t vocab) {
+  tokens = std::min(tokens, kSlab);
   // room for a row of the narrowest tiles, which few tokens may get
   const int64_t parts = std::max(tokens * ceil_div(vocab, kTileN), std::min<int64_t>(tokens, kTileM) * ceil_div(vocab, kMinLossTile));
   return round_up(parts * 16, 256) + round_up(tokens * 4, 256);
@@ -810,11 +829,14 @@ extern "C" int64_t zero_lm_workspace_bytes(int64_t tokens, int64_t vocab, int64_
   if (rc) return rc;
   int64_t bytes = std::max<int64_t>(256, loss_space(tokens, vocab));
   if (!with_grad) return bytes;
-  // any smaller count of tokens has to fit too: its sums may be split more often, and its pieces be wider
+  // any smaller count of tokens has to fit too: its pieces may be wider and its sums split more often.  With
+  // fewer tokens D of a piece takes at most kPieceBytes, or less than kMinPiece rows of all the tokens would
   const int64_t wide = round_up(vocab, 256);
-  const int64_t probs = 2 * std::max(std::min(tokens * wide * 2, kPieceBytes), tokens * std::min(kMinPiece, wide) * 2);
-  const int64_t sums = std::max(tokens, std::min<int64_t>(tokens * kMaxSplits, 76 * kTileM)) * (round_up(width, 256)) * 4;
-  const int64_t counters = (ceil_div(vocab, std::min(kMinPiece, wide)) + 1) * 4;
+  const int64_t piece = std::max(std::min(tokens * std::min(wide, kMinPiece) * 2, std::max(kMostPieceBytes, tokens * kLeastPiece * 2)),
+                                 std::min(tokens * wide * 2, kPieceBytes));
+  const int64_t probs = 2 * piece;
+  const int64_t sums = std::max(tokens, std::min<int64_t>(tokens * kMaxSplits, 76 * kTileM)) * round_up(width, 256) * 4;
+  const int64_t counters = (ceil_div(vocab, kLeastPiece) + 1) * 4;
   return std::max(bytes, round_up(tokens * width * 2, 256) + round_up(probs, 512) + round_up(sums, 256) + round_up(counters, 256));
 }
 
@@ -833,30 +855,36 @@ extern "C" int zero_lm_loss(int64_t tokens, int64_t vocab, int64_t width, int dt
     return fail(ZERO_E_ARG, "workspace of %lld bytes: %lld are needed", (long long)workspace_bytes,
                 (long long)loss_space(tokens, vocab));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  GemmArgs g;
-  std::memset(&g, 0, sizeof g);
-  Job& j = g.job[0];
-  j.kind = kStats;
-  j.bn = loss_tile(tokens, vocab);
-  j.m_tiles = static_cast<int>(ceil_div(tokens, kTileM));
-  j.n_tiles = static_cast<int>(ceil_div(vocab, j.bn));
-  j.splits = 1;
-  j.tiles = j.m_tiles * j.n_tiles;
-  j.kb_total = static_cast<int>(ceil_div(width, kTileK));
-  j.M = static_cast<int>(tokens);
-  j.N = static_cast<int>(vocab);
-  j.stage_tx = 2 * (kOperandBytes + j.bn / 2 * kTileK * 2);
-  g.jobs = 1;
-  g.vocab = static_cast<int>(vocab);
-  g.targets = targets;
-  g.id_bytes = id_bytes;
-  g.part = static_cast<float2*>(workspace);
-  g.target_logit = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(tokens * j.n_tiles * 16, 256));
-  if ((rc = make_map(&g.a[0], dtype, hidden, tokens, width, hidden_stride, 128))) return rc;
-  if ((rc = make_map(&g.b[0], dtype, table, vocab, width, table_stride, j.bn / 2))) return rc;
-  if ((rc = launch_gemm<false>(g, dtype, s))) return rc;
-  ZERO_CUDA(launch_chained(lm_combine, dim3(static_cast<unsigned>(ceil_div(tokens * 32, kSmallThreads))), kSmallThreads, 0,
-                           s, g.part, 2 * j.n_tiles, g.target_logit, targets, id_bytes, g.vocab, j.M, loss, lse));
+  for (int64_t t0 = 0; t0 < tokens; t0 += kSlab) {
+    const int64_t count = std::min(kSlab, tokens - t0);
+    const void* slab_targets = static_cast<const char*>(targets) + t0 * id_bytes;
+    GemmArgs g;
+    std::memset(&g, 0, sizeof g);
+    Job& j = g.job[0];
+    j.kind = kStats;
+    j.bn = loss_tile(count, vocab);
+    j.m_tiles = static_cast<int>(ceil_div(count, kTileM));
+    j.n_tiles = static_cast<int>(ceil_div(vocab, j.bn));
+    j.splits = 1;
+    j.tiles = j.m_tiles * j.n_tiles;
+    j.kb_total = static_cast<int>(ceil_div(width, kTileK));
+    j.M = static_cast<int>(count);
+    j.N = static_cast<int>(vocab);
+    j.stage_tx = 2 * (kOperandBytes + j.bn / 2 * kTileK * 2);
+    g.jobs = 1;
+    g.vocab = static_cast<int>(vocab);
+    g.targets = slab_targets;
+    g.id_bytes = id_bytes;
+    g.part = static_cast<float2*>(workspace);
+    g.target_logit = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(count * j.n_tiles * 16, 256));
+    const uint16_t* rows = static_cast<const uint16_t*>(hidden) + t0 * hidden_stride;
+    if ((rc = make_map(&g.a[0], dtype, rows, count, width, hidden_stride, 128))) return rc;
+    if ((rc = make_map(&g.b[0], dtype, table, vocab, width, table_stride, j.bn / 2))) return rc;
+    if ((rc = launch_gemm<false>(g, dtype, s))) return rc;
+    const dim3 grid(static_cast<unsigned>(ceil_div(count * 32, kSmallThreads)));
+    ZERO_CUDA(launch_chained(lm_combine, grid, kSmallThreads, 0, s, g.part, 2 * j.n_tiles, g.target_logit, slab_targets,
+                             id_bytes, g.vocab, j.M, loss + t0, lse + t0));
+  }
   return ZERO_OK;
 }
 
@@ -986,4 +1014,9 @@ extern "C" int zero_lm_status(void* stream) {
   const unsigned int zero_count = 0;
   ZERO_CUDA(cudaMemcpyToSymbol(g_lm_timeouts, &zero_count, sizeof zero_count));
   return fail(ZERO_E_STATE, "%u bounded device waits gave up; the losses or gradients they belonged to are incomplete", n);
+}
+
+extern "C" int zero_lm_inject_stall(void) {
+  g_stall_next = true;
+  return ZERO_OK;
 }
