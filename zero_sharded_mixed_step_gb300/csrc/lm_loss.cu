@@ -696,14 +696,17 @@ struct GradPlan {
   int splits;           // of the vocabulary within kDHidden
 };
 
-// Tile width for `width` columns: the multiple of 32 that wastes least, counting
-// what a tile costs besides its columns as 32 more.
+// Tile width for `width` columns of a gradient.  A block of K costs a pair
+// 2 bn cycles of products, or the time its operands take from L2: about 600
+// cycles for the 256 rows and 256 columns of the largest tile, in proportion
+// to what is loaded (whole boxes of 64 columns for each CTA).
 int tile_width(int64_t width) {
   int best = kTileN;
   int64_t cost = INT64_MAX;
   for (int bn = kTileN; bn >= 32; bn -= 32) {
-    const int64_t c = ceil_div(width, bn) * (bn + 32);
-    if (c < cost) {
+    const int64_t loaded = kTileM + 2 * round_up(bn / 2, 64);
+    const int64_t c = ceil_div(width, bn) * std::max<int64_t>(2 * bn, loaded * 600 / 512);
+    if (c <= cost) {
       cost = c;
       best = bn;
     }
