@@ -824,7 +824,7 @@ class _Owner:
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device() if torch.cuda.is_available() else 0)
         self._index, self._new, self._fp32 = self.device.index, torch.empty, torch.float32
-        self._alloc = alloc or (lambda numel, dt: torch.zeros(numel, dtype=dt, device=self.device))
+        self._alloc = alloc
 
     def _bind(self, name):
         """The C entry point, raising like its wrapper: the owners' calls are
@@ -837,9 +837,15 @@ class _Owner:
                 raise ZeroError(rc, name, lib().zero_last_error().decode())
         return call
 
-    def _workspace(self, nbytes):
+    def _workspace(self, nbytes, zero=False):
+        """The workspace; set to 0 only where the calls ask for it."""
+        torch = self.torch
         with _on(self.stream):
-            self.workspace = self._alloc(max(256, nbytes), self.torch.uint8)
+            if self._alloc is not None:
+                self.workspace = self._alloc(max(256, nbytes), torch.uint8)
+            else:
+                self.workspace = (torch.zeros if zero else torch.empty)(max(256, nbytes), dtype=torch.uint8,
+                                                                        device=self.device)
         self.workspace_bytes = self.workspace.numel()
         self._ws = self.workspace.data_ptr()
 
@@ -990,7 +996,7 @@ class GradClip(_Owner):
             offsets.append(at * self._item)
             at += k
         self._offsets = offsets
-        self._workspace(zero_grad_norm_workspace_bytes())
+        self._workspace(zero_grad_norm_workspace_bytes(), zero=True)
         self._c_norm, self._c_clip = self._bind("zero_grad_norm"), self._bind("zero_grad_clip")
 
     def _pointers(self, grads):

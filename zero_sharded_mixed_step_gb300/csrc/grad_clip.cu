@@ -144,18 +144,21 @@ __device__ __forceinline__ float clip_coef(float norm, float max_norm) {
 //
 // The tensors' sizes and addresses travel as the kernel's parameters, so a
 // call needs no copy to the device; a list that does not fit one launch takes
-// several.  Work is cut into chunks of kChunk elements of one tensor.
+// several.  Work is cut into chunks of kChunk elements of one tensor.  There
+// are two sizes of parameters: the large one costs the host 13 us more a
+// launch, whatever it holds.
 
 constexpr int kChunk = 8192;
-constexpr int kTableBytes = 28 * 1024;     // a launch's parameters may hold 32,764 bytes
+constexpr int kSmallTable = 9 * 1024, kLargeTable = 28 * 1024;   // a launch's parameters may hold 32,764 bytes
 
+template <int BYTES>
 struct Table {
   int tensors, W;
   unsigned int chunks;
   int want_out;
   // follows: chunk_start[tensors + 1], then per tensor its element count,
   // W gradient addresses and, with want_out, an output address
-  alignas(8) unsigned char data[kTableBytes];
+  alignas(8) unsigned char data[BYTES];
 
   __host__ __device__ int64_t words() const { return 1 + W + want_out; }
   __host__ __device__ const unsigned int* starts() const { return reinterpret_cast<const unsigned int*>(data); }
@@ -268,8 +271,8 @@ __device__ __forceinline__ void store_shifted(T* out, int shift, const float (&v
 // alike relative to a group of 8 elements are read a group at a time; the
 // output may lie anywhere.  The clipping pass walks the chunks backwards:
 // what the norm's pass read last is what L2 still holds.
-template <typename T, int WC, bool CLIP>
-__global__ void __launch_bounds__(kThreads) tensors_pass(const __grid_constant__ Table t, NormSpace ws,
+template <typename T, int WC, bool CLIP, int BYTES>
+__global__ void __launch_bounds__(kThreads) tensors_pass(const __grid_constant__ Table<BYTES> t, NormSpace ws,
                                                          unsigned int first, unsigned int blocks, float* norm,
                                                          float max_norm) {
   await_previous();
@@ -542,13 +545,16 @@ int check_tensors(int W, int64_t n_tensors, const int64_t* numels, int dtype, co
   return ZERO_OK;
 }
 
-// Fill launches from the list and call `launch(table, last)` for each.
-template <typename F>
-int for_tables(int W, int64_t n_tensors, const int64_t* numels, const void* const* grads, void* const* out, F launch) {
-  static thread_local Table t;
-  static thread_local int64_t pick[kTableBytes / 16];   // the tensors of one launch
-  const int64_t words = 1 + W + (out ? 1 : 0);
-  const int64_t most = (kTableBytes - 16) / (8 * words + 4);
+// Tensors that a table of `bytes` holds.
+int64_t table_tensors(int bytes, int W, bool out) { return (bytes - 16) / (8 * (1 + W + (out ? 1 : 0)) + 4); }
+
+// Fill tables from the list and call launch(table, last) for each.
+template <int BYTES, typename F>
+int for_tables_of(int W, int64_t n_tensors, const int64_t* numels, const void* const* grads, void* const* out,
+                  F launch) {
+  static thread_local Table<BYTES> t;
+  static thread_local int64_t pick[BYTES / 16];   // the tensors of one launch
+  const int64_t most = table_tensors(BYTES, W, out != nullptr);
   int64_t k = 0;
   do {
     int64_t chunks = 0;
@@ -584,6 +590,13 @@ int for_tables(int W, int64_t n_tensors, const int64_t* numels, const void* cons
   return ZERO_OK;
 }
 
+template <typename F>
+int for_tables(int W, int64_t n_tensors, const int64_t* numels, const void* const* grads, void* const* out, F launch) {
+  return n_tensors <= table_tensors(kSmallTable, W, out != nullptr)
+             ? for_tables_of<kSmallTable>(W, n_tensors, numels, grads, out, launch)
+             : for_tables_of<kLargeTable>(W, n_tensors, numels, grads, out, launch);
+}
+
 unsigned pass_blocks(int64_t chunks, int64_t most) {
   return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>({chunks, static_cast<int64_t>(sm_count()) * 4, most})));
 }
@@ -598,23 +611,32 @@ int check_norm_args(const float* norm, const void* workspace, int64_t workspace_
   return ZERO_OK;
 }
 
-using TensorsFn = void (*)(const Table, NormSpace, unsigned int, unsigned int, float*, float);
+// One launch over a list that fits its table.
+template <typename T, int WC, bool CLIP, int BYTES>
+cudaError_t launch_table(const Table<BYTES>& t, unsigned blocks, const NormSpace& ws, unsigned first, float* norm,
+                         float max_norm, cudaStream_t s) {
+  return launch_chained(tensors_pass<T, WC, CLIP, BYTES>, dim3(blocks), kThreads, 0, s, t, ws, first, first + blocks,
+                        norm, max_norm);
+}
 
-template <typename T, bool CLIP>
-TensorsFn pick_tensors_w(int W) {
-  switch (W) {
-    case 1: return tensors_pass<T, 1, CLIP>;
-    case 2: return tensors_pass<T, 2, CLIP>;
-    case 4: return tensors_pass<T, 4, CLIP>;
-    case 8: return tensors_pass<T, 8, CLIP>;
-    default: return tensors_pass<T, 0, CLIP>;
+template <typename T, bool CLIP, int BYTES>
+cudaError_t launch_tensors_w(const Table<BYTES>& t, unsigned blocks, const NormSpace& ws, unsigned first, float* norm,
+                             float max_norm, cudaStream_t s) {
+  switch (t.W) {
+    case 1: return launch_table<T, 1, CLIP>(t, blocks, ws, first, norm, max_norm, s);
+    case 2: return launch_table<T, 2, CLIP>(t, blocks, ws, first, norm, max_norm, s);
+    case 4: return launch_table<T, 4, CLIP>(t, blocks, ws, first, norm, max_norm, s);
+    case 8: return launch_table<T, 8, CLIP>(t, blocks, ws, first, norm, max_norm, s);
+    default: return launch_table<T, 0, CLIP>(t, blocks, ws, first, norm, max_norm, s);
   }
 }
 
-template <bool CLIP>
-TensorsFn pick_tensors(int dtype, int W) {
-  if (dtype == ZERO_FP16) return pick_tensors_w<__half, CLIP>(W);
-  return dtype == ZERO_BF16 ? pick_tensors_w<__nv_bfloat16, CLIP>(W) : pick_tensors_w<float, CLIP>(W);
+template <bool CLIP, int BYTES>
+cudaError_t launch_tensors(const Table<BYTES>& t, int dtype, unsigned blocks, const NormSpace& ws, unsigned first,
+                           float* norm, float max_norm, cudaStream_t s) {
+  if (dtype == ZERO_FP16) return launch_tensors_w<__half, CLIP>(t, blocks, ws, first, norm, max_norm, s);
+  if (dtype == ZERO_BF16) return launch_tensors_w<__nv_bfloat16, CLIP>(t, blocks, ws, first, norm, max_norm, s);
+  return launch_tensors_w<float, CLIP>(t, blocks, ws, first, norm, max_norm, s);
 }
 
 }  // namespace
@@ -682,15 +704,13 @@ extern "C" int zero_grad_norm(int W, int64_t n_tensors, const int64_t* numels, i
   const NormSpace ws = norm_space(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // every launch leaves its blocks' sums in slots of its own; the last one adds them up
-  const int64_t words = 1 + W, most = (kTableBytes - 16) / (8 * words + 4);
-  const int64_t launches = std::max<int64_t>(1, ceil_div(n_tensors, most));
+  const int64_t launches = std::max<int64_t>(1, ceil_div(n_tensors, table_tensors(kLargeTable, W, false)));
   if (launches > kMaxBlocks) return fail(ZERO_E_ARG, "too many tensors (%lld)", (long long)n_tensors);
   unsigned first = 0;
-  return for_tables(W, n_tensors, numels, grads, nullptr, [&](const Table& t, bool last) -> int {
+  return for_tables(W, n_tensors, numels, grads, nullptr, [&](const auto& t, bool last) -> int {
     const unsigned blocks = pass_blocks(t.chunks, kMaxBlocks / launches);
     if (first + blocks > kMaxBlocks) return fail(ZERO_E_ARG, "too many elements");
-    ZERO_CUDA(launch_chained(pick_tensors<false>(dtype, W), dim3(blocks), kThreads, 0, s, t, ws, first, first + blocks,
-                             last ? norm : nullptr, 0.f));
+    ZERO_CUDA(launch_tensors<false>(t, dtype, blocks, ws, first, last ? norm : nullptr, 0.f, s));
     first += blocks;
     return ZERO_OK;
   });
@@ -707,10 +727,10 @@ extern "C" int zero_grad_clip(int W, int64_t n_tensors, const int64_t* numels, i
   if (!(limit > 0) || !std::isfinite(limit)) return fail(ZERO_E_ARG, "max_norm %g is not a positive finite fp32 value", max_norm);
   if (n_tensors == 0) return ZERO_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return for_tables(W, n_tensors, numels, grads, out, [&](const Table& t, bool) -> int {
+  return for_tables(W, n_tensors, numels, grads, out, [&](const auto& t, bool) -> int {
     if (t.tensors == 0) return ZERO_OK;
-    ZERO_CUDA(launch_chained(pick_tensors<true>(dtype, W), dim3(pass_blocks(t.chunks, INT32_MAX)), kThreads, 0, s, t,
-                             NormSpace{nullptr, nullptr}, 0u, 0u, const_cast<float*>(norm), limit));
+    ZERO_CUDA(launch_tensors<true>(t, dtype, pass_blocks(t.chunks, INT32_MAX), NormSpace{nullptr, nullptr}, 0u,
+                                   const_cast<float*>(norm), limit, s));
     return ZERO_OK;
   });
 }
