@@ -733,7 +733,9 @@ int64_t piece_rows(int64_t tokens) {
 
 GradPlan plan_grad(int64_t tokens, int64_t vocab, int64_t width) {
   GradPlan p;
-  p.piece = std::min(round_up(vocab, 256), piece_rows(tokens));
+  // pieces of one size: a short last one has too few tiles for the SMs and the longest ones all the same
+  const int64_t pieces = ceil_div(vocab, piece_rows(tokens));
+  p.piece = round_up(ceil_div(vocab, pieces), 256);
   p.bn = tile_width(width);
   const int64_t tiles = ceil_div(tokens, kTileM) * ceil_div(width, p.bn);
   const int64_t kb = ceil_div(std::min(p.piece, vocab), kTileK);
