@@ -93,7 +93,7 @@ struct Job {
 
 struct GemmArgs {
   CUtensorMap a[kMaxJobs], b[kMaxJobs];
-  Job job[kMaxJobs];         // the longest tiles first
+  Job job[kMaxJobs];         // the longest tiles first, and kProbs last (see the loads)
   int jobs;
   int stall;                 // testing the bounded waits: the first pair's first block of K never arrives
   unsigned int* next;        // tiles handed out beyond one per pair (0 at the launch)
@@ -325,13 +325,11 @@ uint4 old[4];
 
 // The persistent product kernel: pairs of CTAs, each pair one 256-row tile at
 // a time, operands through a ring of TMA stages, two accumulators in TMEM so
-// that one tile's epilogue runs beside the next one's products.  One thread of
-// the pair hands out its tiles through a short queue in shared memory, worked
-// out, so that no role waits for a division or a counter between two tiles.
-// The loss's tiles are all alike and are dealt out in turn.  The gradient's
-// differ: beyond its first tile a pair takes the next one from a counter, in
-// the order of the jobs, the longest tiles first, so that the short ones fill
-// the gaps at the end.
+// that one tile's epilogue runs beside the next one's products.  The loss's
+// tiles are all alike and are dealt out in turn.  The gradient's differ: one
+// thread of the pair takes them from a counter, in the order of the jobs, the
+// longest tiles first, so that the short ones fill the gaps at the end, and
+// hands them to the roles of both CTAs through a short queue in shared memory.
 template <typename T, bool GRAD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm(const __grid_constant__ GemmArgs g) {
   extern __shared__ unsigned char raw[];
@@ -384,108 +382,126 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm
   const uint32_t tmem = tmem_slot;
   await_previous();
 
-  // The i-th tile of this pair, read by one lane of each consuming warp.
+  // Every role runs as a whole warp with uniform control flow, one elected
+  // lane issuing: what the loads and products take then sits in uniform
+  // registers, and the issuing keeps up with the products (from a single
+  // lane's branch, the products ran 10% slower).
+  const bool lead = elect_one();
   bool ok = true;
+  auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity)) != 0; };
+  // The i-th tile of this pair.  The one who hands out the gradient's runs in
+  // the leader, so only the other CTA has to acquire from the cluster.
   auto tile_of = [&](int i) {
+    if (!GRAD) return locate(g, pair + i * pairs);
     Tile x{};
-    const int q = i % kQueue;
-    ok = bar_wait<true>(told(q), (i / kQueue) & 1);
     x.job = -1;
+    const int q = i % kQueue;
+    const uint32_t parity = (i / kQueue) & 1;
+    ok = __all_sync(0xffffffffu, rank == 0 ? bar_wait(told(q), parity) : bar_wait<true>(told(q), parity)) != 0;
     if (!ok) return x;
     x = queue[q];
-    asm volatile("" ::: "memory");
-    bar_arrive(in_cta(heard(q), 0));
+    __syncwarp();
+    if (lead) bar_arrive(in_cta(heard(q), 0));
     return x;
   };
 
-  int issued = 0;      // stages loaded by this thread
-  if (warp == 0 || warp == 3) {
-    if (lane == 0) {
-      for (int i = 0;; ++i) {
-        const Tile x = tile_of(i);
-        if (!ok || x.job < 0) break;
-        const Job& j = jobs[x.job];
-        const CUtensorMap *ma = &g.a[x.job], *mb = &g.b[x.job];
-        const int kind = GRAD ? j.kind : static_cast<int>(kStats);
-        const int am = x.mt * kTileM + static_cast<int>(rank) * 128;
-        const int bn = x.nt * j.bn + static_cast<int>(rank) * (j.bn / 2);
-        // an MN-major operand comes as boxes of 64 columns, with K the row index
-        const bool a_mn = kind == kDTable, b_mn = kind >= kDHidden;
-        // one thread loads both operands where each is one box; four boxes a stage are too many for it
-        const bool both = !b_mn, load_a = warp == 0, load_b = both ? warp == 0 : warp == 3;
-        if (both && warp == 3) {
-          issued += x.k1 - x.k0;
-          continue;
-        }
-        const int row0 = b_mn ? (kind == kDHidden ? j.b_row0 : 0) : bn + j.b_row0;
-        const int boxes = j.b_boxes;
-        const uint32_t tx = j.stage_tx;
-        for (int kb = x.k0; kb < x.k1; ++kb, ++issued) {
-          const int s = issued % kStages;
-          ok = bar_wait(empty(s), ((issued / kStages) & 1) ^ 1);
+  int issued = 0;      // stages loaded by this warp
+  if (warp == 0 || (GRAD && warp == 3)) {
+    int s = 0;
+    uint32_t phase = 1;
+    for (int i = 0;; ++i) {
+      const Tile x = tile_of(i);
+      if (!ok || x.job < 0) break;
+      const Job& j = jobs[x.job];
+      const CUtensorMap *ma = &g.a[x.job], *mb = &g.b[x.job];
+      const int kind = GRAD ? j.kind : static_cast<int>(kStats);
+      const int am = x.mt * kTileM + static_cast<int>(rank) * 128;
+      const int bn = x.nt * j.bn + static_cast<int>(rank) * (j.bn / 2);
+      // an MN-major operand comes as boxes of 64 columns, with K the row index
+      const bool a_mn = kind == kDTable, b_mn = kind >= kDHidden;
+      // One warp loads both operands where each is one box; four boxes a stage are too many for it.  The second
+      // warp does not wait where it does not load, so it must not load again after that: products with an MN-major
+      // B come first among a launch's jobs.
+      const bool load_a = warp == 0, load_b = (warp == 0) != b_mn;
+      const int row0 = b_mn ? (kind == kDHidden ? j.b_row0 : 0) : bn + j.b_row0;
+      const bool two = j.b_boxes > 1, expect = load_a && rank == 0;
+      const uint32_t tx = j.stage_tx;
+      for (int kb = x.k0; kb < x.k1; ++kb, ++issued) {
+        if (load_a || load_b) {
+          ok = wait_all(empty(s), phase);
           if (!ok) break;
-          if (load_a && rank == 0) bar_expect(full(s), tx);
           const uint32_t bar = in_cta(full(s), 0);
           const uint32_t sa = ring + s * kStageBytes, sb = sa + kOperandBytes;
           const int k = kb * kTileK;
-          if (load_a && !(g.stall && pair == 0 && issued == 0)) {
-            if (a_mn) {
-              tma_load(sa, ma, am, k, bar);
-              tma_load(sa + 8192, ma, am + 64, k, bar);
-            } else {
-              tma_load(sa, ma, k, am, bar);
+          if (lead) {
+            if (expect) bar_expect(full(s), tx);
+            if (load_a && !(g.stall && pair == 0 && issued == 0)) {
+              if (a_mn) {
+                tma_load(sa, ma, am, k, bar);
+                tma_load(sa + 8192, ma, am + 64, k, bar);
+              } else {
+                tma_load(sa, ma, k, am, bar);
+              }
+            }
+            if (load_b) {
+              if (b_mn) {
+                tma_load(sb, mb, bn, row0 + k, bar);
+                if (two) tma_load(sb + 8192, mb, bn + 64, row0 + k, bar);
+              } else {
+                tma_load(sb, mb, k, row0, bar);
+              }
             }
           }
-          if (load_b) {
-            if (b_mn) {
-              tma_load(sb, mb, bn, row0 + k, bar);
-              if (boxes > 1) tma_load(sb + 8192, mb, bn + 64, row0 + k, bar);
-            } else {
-              tma_load(sb, mb, k, row0, bar);
-            }
-          }
+          __syncwarp();
         }
-        if (!ok) break;
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1;
+        }
       }
-      if (!ok) failed = 1;
+      if (!ok) break;
     }
+    if (!ok && lead) failed = 1;
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
-      int stage = 0;
-      Tile x = tile_of(0);
-      for (int i = 0; ok && x.job >= 0; ++i) {
+    if (rank == 0) {
+      int s = 0;
+      uint32_t phase = 0;
+      for (int i = 0;; ++i) {
+        const Tile x = tile_of(i);
+        if (!ok || x.job < 0) break;
         const Job& j = jobs[x.job];
         const bool a_mn = GRAD && j.kind == kDTable;      // A = D^T: rows of vocabulary are contiguous in D
         const bool b_mn = GRAD && j.kind >= kDHidden;     // B = h or T with K the row index
         const uint32_t idesc = instr_desc(std::is_same<T, __nv_bfloat16>::value, a_mn, b_mn, kTileM, j.bn);
         // 16 values of K further: 32 bytes within a K-major row, 16 rows of an MN-major tile
         const uint64_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+        const uint64_t a0 = operand_desc(ring, a_mn ? 8192 : 0), b0 = operand_desc(ring + kOperandBytes, b_mn ? 8192 : 0);
         const int a = i & 1;
-        Tile next = x;
-        ok = bar_wait(taken(a), ((i >> 1) & 1) ^ 1);
+        ok = wait_all(taken(a), ((i >> 1) & 1) ^ 1);
         if (!ok) break;
         fence_after();
         const uint32_t d = tmem + a * kTileN;
-        for (int kb = x.k0; kb < x.k1; ++kb, ++stage) {
-          const int s = stage % kStages;
-          ok = bar_wait(full(s), (stage / kStages) & 1);
+        for (int kb = x.k0; kb < x.k1; ++kb) {
+          ok = wait_all(full(s), phase);
           if (!ok) break;
           fence_after();
-          const uint32_t sa = ring + s * kStageBytes, sb = sa + kOperandBytes;
-          const uint64_t da = operand_desc(sa, a_mn ? 8192 : 0), db = operand_desc(sb, b_mn ? 8192 : 0);
+          const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
+          if (lead) {
 #pragma unroll
-          for (int q = 0; q < kTileK / 16; ++q) mma(d, da + q * a_step, db + q * b_step, idesc, kb > x.k0 || q > 0);
-          mma_commit(empty(s));
-          if (kb == min(x.k0 + 3, x.k1 - 1)) {   // while the products already issued run
-            next = tile_of(i + 1);
-            if (!ok) break;
+            for (int q = 0; q < kTileK / 16; ++q) mma(d, da + q * a_step, db + q * b_step, idesc, kb > x.k0 || q > 0);
+            mma_commit(empty(s));
+          }
+          __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
           }
         }
         if (!ok) break;
-        mma_commit(done(a));
-        x = next;
+        if (lead) mma_commit(done(a));
+        __syncwarp();
       }
-      if (!ok) {
+      if (!ok && lead) {
         // leave no product in flight behind
         failed = 1;
         mma_commit(drained);
@@ -493,12 +509,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm
       }
     }
   } else if (warp == 2) {
-    if (rank == 0 && lane == 0) {
+    if (GRAD && rank == 0 && lead) {
       for (int i = 0;; ++i) {
         const int q = i % kQueue;
         ok = bar_wait(heard(q), ((i / kQueue) & 1) ^ 1);
         if (!ok) break;
-        const int t = GRAD ? (i == 0 ? pair : pairs + static_cast<int>(atomicAdd(g.next, 1u))) : pair + i * pairs;
+        const int t = i == 0 ? pair : pairs + static_cast<int>(atomicAdd(g.next, 1u));
         const Tile x = locate(g, t);
         for (uint32_t r = 0; r < 2; ++r) {
           const uint32_t at = in_cta(smem_addr(&queue[q]), r);
@@ -513,17 +529,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm
   } else if (warp >= 4) {
     const int quad = warp & 3, half = (warp - 4) >> 2;
     for (int i = 0;; ++i) {
-      const int q = i % kQueue, a = i & 1;
-      ok = __all_sync(0xffffffffu, bar_wait<true>(told(q), (i / kQueue) & 1));
-      if (!ok) break;
-      const Tile x = queue[q];
-      __syncwarp();
-      if (lane == 0) bar_arrive(in_cta(heard(q), 0));
-      if (x.job < 0) break;
+      const int a = i & 1;
+      const Tile x = tile_of(i);
+      if (!ok || x.job < 0) break;
       const Job& j = jobs[x.job];
       const int row = x.mt * kTileM + static_cast<int>(rank) * 128 + quad * 32 + lane;
       const RowInfo info = row_info<GRAD>(g, j, row);
-      ok = __all_sync(0xffffffffu, bar_wait(done(a), (i >> 1) & 1));
+      ok = wait_all(done(a), (i >> 1) & 1);
       if (!ok) break;
       fence_after();
       epilogue<T, GRAD>(g, j, x, info, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21), row, half, [&] {
