@@ -759,7 +759,7 @@ int64_t zero_embedding_workspace_bytes(int64_t tokens, int64_t width);
 
 /*
  * The table's gradient: dtable[v] = scale * sum of dout[i] over the i with
- * ids[i] = v, summed in fp32 in the order of i and rounded once.  With
+ * ids[i] = v, summed in fp32 in an order fixed by the ids and rounded once.  With
  * accumulate = 0 every row of dtable is written (0 where no id names it);
  * with 1 the sum is added, in fp32, to the rows that ids name, and the others
  * are left alone (a tied table: on top of zero_lm_loss_grad's).  Ids outside

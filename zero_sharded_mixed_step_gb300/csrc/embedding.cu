@@ -6,8 +6,16 @@
 // Both move bytes and do next to no arithmetic.  The lookup reads and writes
 // one row per token.  The gradient sorts the (token, position) pairs, stably,
 // so that the rows of one token stand together in the order of their
-// positions; it then sums each run in fp32 in that order, which makes the
-// result the same every time, and writes each table row once.
+// positions; it then sums each run in fp32, in an order fixed by the ids (long
+// runs in stretches), which makes the result the same every time, and writes
+// each table row once.
+//
+// What bounds them.  This device writes at most about 4 TB/s, half of what it
+// copies: the lookup of 32768 rows of 1600 writes 105 MB in 25.3 us (4.1
+// TB/s), and an untouched 50257 x 768 gradient alone takes 22.6 us to fill
+// with zeros, the same as a memset, of 32.9 us for 8192 tokens.  65535 tokens
+// onto a 50257 x 1600 gradient take 94 us: 27 for the sort (latencies, 8 SMs),
+// 58 for the runs (283 MB from and to DRAM, 4.7 TB/s) and 10 for the long ones.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -11,6 +11,13 @@
 // read) where reading the W gradients again would cost 2 W, which is faster
 // for 1 and 2 ranks.
 //
+// What bounds them: HBM.  The clipped step of 124M elements of 8 ranks moves 2 W
+// + 4 bytes an element in its first pass (2.49 GB in 358 us, 6.95 TB/s) and 30
+// in its second (3.73 GB in 548 us, 6.8 TB/s), 912 to 918 us in all; the same
+// bytes at the measured copy rate take 917.  The norm and the clipped mean of
+// 148 tensors of 4 ranks, 20M elements, take 34 + 36 us on the device (160 and
+// 200 MB); a Python caller spends 190 us on 592 tensor objects.
+//
 // Squares are summed in fp32 by each thread and in fp64 from there on: within
 // a block, and over the blocks in their order by the last block to finish, so
 // the norm does not depend on the order in which blocks run.
