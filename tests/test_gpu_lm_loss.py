@@ -287,3 +287,34 @@ def test_a_lost_copy_is_reported(which):
     assert torch.equal(loss2, loss) and torch.equal(lse2, lse)
     assert all(torch.equal(x, y) for x, y in zip(op.grad(h, t, tg, lse, 1.0), grads))
     op.status()
+
+
+def test_calls_in_a_cuda_graph():
+    """Loss and gradients captured once and replayed on new contents."""
+    N, V, d = 300, 5000, 256
+    h, t, tg = make(N, V, d, "bf16", seed=21)
+    op = zs.LmLoss(V, d, "bf16", max_tokens=N)
+    emb = zs.Embedding(V, d, "bf16", max_tokens=N)
+    ids = tg.clamp(min=0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def run():
+        loss, lse = op.loss(h, t, tg)
+        dh, dt = op.grad(h, t, tg, lse, 1.0 / N)
+        return loss, dh, emb.grad(ids, dh, dt, accumulate=True), emb.forward(ids, t)
+
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        outs = run()
+    for seed in (22, 23):
+        h2, t2, tg2 = make(N, V, d, "bf16", seed=seed)
+        h.copy_(h2), t.copy_(t2), tg.copy_(tg2), ids.copy_(tg2.clamp(min=0))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in outs]
+        assert all(torch.equal(x, y) for x, y in zip(got, run()))

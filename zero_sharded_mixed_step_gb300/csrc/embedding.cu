@@ -428,7 +428,9 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join(const RunArgs a) {
 constexpr int64_t kMaxTokens = int64_t(1) << 24, kMaxVocab = int64_t(1) << 24, kMaxWidth = int64_t(1) << 16;
 
 // Sorted pairs per chunk, a power of two: 608 to 1215 chunks where the tokens
-// allow it (4 to 8 for each SM).
+// allow it (4 to 8 for each SM).  65535 tokens onto 50257 x 1600 took 94 us so
+// and with 304, 100 with 1216 and 112 with 2432; 8192 tokens x 768 took 35 us
+// with 304 and 33 with the others.
 constexpr int kChunks = 608;
 int chunk_of(int64_t tokens) {
   int c = kMinChunk;
