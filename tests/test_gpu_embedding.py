@@ -122,3 +122,19 @@ def test_refusals():
         emb.grad(torch.cat([ids, ids]), torch.cat([rows, rows]))
     with pytest.raises(zs.ZeroError):
         zs.Embedding(40, 20, "fp16")
+
+
+@pytest.mark.parametrize("kind", ["words", "uniform", "one", "outside"])
+@pytest.mark.parametrize("N", [1, 700, 3000])
+def test_rows_that_no_id_names_are_zero_in_a_large_table(N, kind):
+    """A table of 61 MB: part of its rows is filled beside the sort, the rest beside the sums."""
+    V, d = 59_999, 512
+    ids, rows, table = draw(N, V, d, "bf16", seed=N, kind=kind)
+    ids[-1] = V - 1
+    emb = zs.Embedding(V, d, "bf16", max_tokens=N)
+    wide = torch.full((V, d + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+    total, bound = ref.embedding_grad_reference(ids, rows, 1.0, V)
+    got = emb.grad(ids, rows, torch.full((V, d), 5.0, dtype=torch.bfloat16, device="cuda"))
+    ref.assert_within(got, total, bound, "dtable")
+    emb.grad(ids, rows, wide[:, :d])
+    assert torch.equal(wide[:, :d], got) and (wide[:, d:] == 3).all()

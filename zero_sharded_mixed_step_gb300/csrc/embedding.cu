@@ -12,8 +12,8 @@
 //
 // What bounds them.  This device writes at most about 4 TB/s, half of what it
 // copies: the lookup of 32768 rows of 1600 writes 105 MB in 25.3 us (4.1
-// TB/s), and an untouched 50257 x 768 gradient alone takes 22.6 us to fill
-// with zeros, the same as a memset, of 32.9 us for 8192 tokens.  65535 tokens
+// TB/s), and a 50257 x 768 gradient alone takes 22.6 us to fill with zeros, by
+// a memset too, of 28.6 us for 8192 tokens.  65535 tokens
 // onto a 50257 x 1600 gradient take 94 us: 27 for the sort (latencies, 8 SMs),
 // 58 for the runs (283 MB from and to DRAM, 4.7 TB/s) and 10 for the long ones.
 
@@ -97,8 +97,10 @@ __global__ void __launch_bounds__(kLookupThreads) embed_lookup(const void* ids, 
 // their barrier is hardware, so nothing spins, and each pass exchanges its
 // digit counts through the cluster's shared memory.  Token i belongs to a
 // fixed warp, in order, and a pass places the pairs of (digit, warp, order in
-// the warp) one after another.  The launch's other clusters meanwhile set the
-// gradient's rows to 0: the sort waits on latencies, the fill on bandwidth.
+// the warp) one after another.  The launch's other clusters meanwhile set
+// rows of the gradient to 0: the sort waits on latencies, the fill on
+// bandwidth.  Rows beyond what the sort's time covers are left to the next
+// launch, which knows the ids and fills only those without any.
 
 constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 1024;
@@ -277,7 +279,42 @@ struct RunArgs {
   float* parts;                // [chunk][head, tail][width]
   int* runs;                   // how many runs go past their chunk, and after it the chunks where they begin
   float scale;
+  int fill_first, fills;       // rows from here on are still to be set to 0 where no id names them, by so many blocks
 };
+
+constexpr int kFillRows = 64;        // rows of a filling block
+
+// Set to 0 the rows [r0, r0 + kFillRows) that no sorted pair names.
+template <typename T>
+__device__ void fill_unnamed(const RunArgs& a, int r0) {
+  __shared__ int named[kFillRows];
+  __shared__ int start;
+  const int r1 = min(r0 + kFillRows, a.vocab), lane = threadIdx.x & 31;
+  for (int k = threadIdx.x; k < kFillRows; k += blockDim.x) named[k] = 0;
+  if (threadIdx.x < 32) {
+    // the first pair with an id of r0 or more: 32 probes at a time
+    int lo = 0, hi = a.tokens;
+    while (lo < hi) {
+      const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step - 1;
+      const int below = __popc(__ballot_sync(0xffffffffu, at < hi && a.pairs[at].x < r0));
+      hi = min(hi, lo + (below + 1) * step - 1);
+      lo = min(hi, lo + below * step);
+    }
+    if (lane == 0) start = lo;
+  }
+  __syncthreads();
+  for (int64_t base = start;; base += blockDim.x) {
+    const int64_t i = base + threadIdx.x;
+    const int id = i < a.tokens ? a.pairs[i].x : a.vocab;
+    if (id < r1) named[id - r0] = 1;
+    if (!__syncthreads_or(threadIdx.x == blockDim.x - 1 && id < r1)) break;
+  }
+  for (int r = r0; r < r1; ++r) {
+    if (named[r - r0]) continue;
+    T* out = static_cast<T*>(a.dtable) + r * a.dtable_stride;
+    for (int c8 = threadIdx.x; c8 < a.width8; c8 += blockDim.x) dev::st_16B(out + c8 * 8, make_uint4(0, 0, 0, 0));
+  }
+}
 
 // scale * sum (+ the old row) to a row of the table's gradient.
 template <typename T, bool ADD>
@@ -293,11 +330,16 @@ template <typename T, bool ADD>
 __global__ void __launch_bounds__(256) embed_runs(const RunArgs a) {
   allow_next();
   await_previous();
+  const int block = static_cast<int>(blockIdx.x) - a.fills;
+  if (!ADD && block < 0) {
+    fill_unnamed<T>(a, a.fill_first + static_cast<int>(blockIdx.x) * kFillRows);
+    return;
+  }
   // pairs first - chunk - 1 .. first + 2 chunk (ids -1 and -2 outside the list)
   __shared__ int key[3 * kMaxChunk + 2];
   __shared__ int val[3 * kMaxChunk + 2];
   __shared__ int edge[4];
-  const int c = a.chunk, first = blockIdx.x * c, last = min(first + c, a.tokens) - 1, low = first - c - 1;
+  const int c = a.chunk, first = block * c, last = min(first + c, a.tokens) - 1, low = first - c - 1;
   for (int k = threadIdx.x; k < 3 * c + 2; k += blockDim.x) {
     const int i = low + k;
     const int2 x = i < 0 ? make_int2(-1, 0) : i < a.tokens ? a.pairs[i] : make_int2(-2, 0);
@@ -323,10 +365,10 @@ __global__ void __launch_bounds__(256) embed_runs(const RunArgs a) {
   const int end = begins_here && !long1 ? edge[3] : last + 1;
   const bool continues = long1 && edge[3] > last + 1;     // the last pair's run, into the next chunk
   const bool head_first = began_before && long0;
-  if (threadIdx.x == 0 && begins_here && continues && key[last - low] < a.vocab) a.runs[1 + atomicAdd(a.runs, 1)] = blockIdx.x;
+  if (threadIdx.x == 0 && begins_here && continues && key[last - low] < a.vocab) a.runs[1 + atomicAdd(a.runs, 1)] = block;
   const T* dout = static_cast<const T*>(a.dout);
   const int64_t width = static_cast<int64_t>(a.width8) * 8;
-  float* head = a.parts + static_cast<int64_t>(blockIdx.x) * 2 * width;
+  float* head = a.parts + static_cast<int64_t>(block) * 2 * width;
   constexpr int kRunBatch = ADD ? kAddBatch : 8;   // rows whose loads a thread has in flight
   for (int c8 = threadIdx.x; c8 < a.width8; c8 += blockDim.x) {
     const int64_t col = static_cast<int64_t>(c8) * 8;
@@ -494,7 +536,7 @@ int lookup(int64_t tokens, int64_t vocab, int64_t width, const void* ids, int id
 template <typename T, bool ADD>
 int sum_runs(const RunArgs& a, cudaStream_t s) {
   const int threads = static_cast<int>(std::min<int64_t>(256, round_up(a.width8, 32)));
-  ZERO_CUDA(launch_chained(embed_runs<T, ADD>, dim3(a.chunks), threads, 0, s, a));
+  ZERO_CUDA(launch_chained(embed_runs<T, ADD>, dim3(static_cast<unsigned>(a.chunks + a.fills)), threads, 0, s, a));
   if (a.chunks > 1) {
     const int64_t most = static_cast<int64_t>(a.chunks - 1) * ceil_div(a.width8, 32);
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(8 * sm_count(), most)));
@@ -562,19 +604,23 @@ extern "C" int zero_embedding_grad(int64_t tokens, int64_t vocab, int64_t width,
   for (int k = 0; k < 2; ++k) sa.pairs[k] = reinterpret_cast<int2*>(ws + k * pb);
   sa.runs = reinterpret_cast<int*>(ws + 2 * pb);
   unsigned grid = kSortCtas;
+  int64_t fill_now = 0;
   if (!accumulate) {
-    sa.fill = static_cast<char*>(dtable);
+    // What is written while the ids are sorted: 30 MB and 1 KB for each id.  8192 tokens x 768 onto 50257 rows (77
+    // MB) take 32.9 us with all rows filled there, 28.6 so, 29.4 with 20 MB, 29.6 with 40 and 31.0 with 50.
+    fill_now = std::min(vocab, ceil_div(30'000'000 + tokens * 1000, width * 2));
     if (dtable_stride == width) {   // one stretch, in rows of 64 KB
-      sa.fill_words = vocab * (width / 8);
+      sa.fill_words = fill_now * (width / 8);
       sa.row16 = 4096;
       sa.fill_rows = ceil_div(sa.fill_words, sa.row16);
       sa.fill_stride = sa.row16 * 16;
     } else {
       sa.row16 = width / 8;
-      sa.fill_rows = vocab;
-      sa.fill_words = vocab * sa.row16;
+      sa.fill_rows = fill_now;
+      sa.fill_words = fill_now * sa.row16;
       sa.fill_stride = dtable_stride * 2;
     }
+    sa.fill = static_cast<char*>(dtable);
     const int64_t clusters = std::min<int64_t>(sm_count() / kSortCtas - 1, ceil_div(sa.fill_rows, kSortCtas));
     grid += kSortCtas * static_cast<unsigned>(std::max<int64_t>(1, clusters));
   }
@@ -593,6 +639,8 @@ extern "C" int zero_embedding_grad(int64_t tokens, int64_t vocab, int64_t width,
   ra.runs = sa.runs;
   ra.parts = reinterpret_cast<float*>(ws + 2 * pb + runs_bytes(tokens));
   ra.scale = static_cast<float>(scale);
+  ra.fill_first = static_cast<int>(fill_now);
+  ra.fills = accumulate ? 0 : static_cast<int>(ceil_div(vocab - fill_now, kFillRows));
   if (accumulate) return dtype == ZERO_FP16 ? sum_runs<__half, true>(ra, s) : sum_runs<__nv_bfloat16, true>(ra, s);
   return dtype == ZERO_FP16 ? sum_runs<__half, false>(ra, s) : sum_runs<__nv_bfloat16, false>(ra, s);
 }

@@ -755,8 +755,8 @@ int tile_width(int64_t width) {
   return best;
 }
 
-// Bytes of D at a time.  8192 tokens x 50257 x 768 took 2.73 ms with 32 MB, 1.99
-// with 64, 1.94 with 128, 1.95 with 256 and 1.91 with 512 (two launches in all).
+// Bytes of D at a time.  8192 tokens x 50257 x 768 take 1.66 ms with 64 MB, 1.61
+// with 96 and 128, 1.60 with 192, 1.62 with 256 and 1.65 with 448 (two pieces).
 constexpr int64_t kPieceBytes = int64_t(128) << 20;
 // At least so many rows of the vocabulary at a time (the table's gradient is
 // complete over the tokens, so its tiles take 256), while D of them stays
