@@ -46,7 +46,7 @@ def check(h, t, tg, scale=1.0, op=None, what=""):
     return loss, lse, dh, dt, want
 
 
-SIZES = [(1, 1, 8), (1, 2, 8), (2, 31, 16), (3, 257, 72), (127, 255, 64), (128, 256, 64), (129, 1031, 264),
+SIZES = [(1, 1, 8), (1, 2, 8), (2, 31, 16), (3, 257, 72), (31, 1000, 136), (32, 513, 64), (33, 513, 64), (127, 255, 64), (128, 256, 64), (129, 1031, 264),
          (255, 511, 136), (257, 2048, 128), (300, 4099, 520), (64, 5000, 1600), (1, 50257, 768), (515, 777, 2056)]
 
 

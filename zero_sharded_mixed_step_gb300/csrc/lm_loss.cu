@@ -11,7 +11,8 @@
 // through one persistent tensor-core kernel, lm_gemm, with an epilogue each:
 //   kStats    keeps the maximum and the sum of exponentials of each row over
 //             the tile's columns, and the target's logit; lm_combine joins
-//             them over the vocabulary;
+//             them over the vocabulary (kFew: the same with the operands
+//             exchanged, for a few tokens);
 //   kProbs    forms D of one piece of the vocabulary, 16-bit, in workspace;
 //   kDHidden  D T over the piece, added to fp32 sums in workspace;
 //   kDTable   D^T h of the piece's rows, complete over the tokens, rounded
@@ -75,7 +76,7 @@ constexpr int kMaxJobs = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-enum Kind : int { kStats = 0, kProbs = 1, kDHidden = 2, kDTable = 3 };
+enum Kind : int { kFew = -1, kStats = 0, kProbs = 1, kDHidden = 2, kDTable = 3 };
 
 // What fp16 scales D by (see above); bf16 has fp32's range.
 template <typename T>
@@ -112,7 +113,8 @@ struct GemmArgs {
   const void* targets;
   int id_bytes;
   const float* lse;
-  float2* part;              // kStats: [row][n tile][half of its columns] maximum and sum, in powers of 2
+  float2* part;              // maximum and sum, in powers of 2: kStats [row][n tile][half of its columns],
+                             // kFew [token][32 rows of the vocabulary]
   float* target_logit;
 };
 
@@ -160,6 +162,22 @@ __device__ __forceinline__ Tile locate(const GemmArgs& g, int t) {
   return x;
 }
 
+// 32 values of each lane, joined over the lanes by op; lane l receives the
+// l-th.  Each step exchanges half of what is left: 31 exchanges in all.
+template <typename Op>
+__device__ __forceinline__ float join_lanes(float (&x)[32], int lane, Op op) {
+#pragma unroll
+  for (int w = 16; w > 0; w /= 2) {
+    const bool up = (lane & w) != 0;
+#pragma unroll
+    for (int k = 0; k < w; ++k) {
+      const float give = up ? x[k] : x[k + w], keep = up ? x[k + w] : x[k];
+      x[k] = op(keep, __shfl_xor_sync(0xffffffffu, give, w));
+    }
+  }
+  return x[0];
+}
+
 // What the epilogue needs to know of its row, read before the tile is complete.
 struct RowInfo {
   int target;      // -1: none
@@ -169,7 +187,7 @@ struct RowInfo {
 template <bool GRAD>
 __device__ __forceinline__ RowInfo row_info(const GemmArgs& g, const Job& j, int row) {
   RowInfo r{-1, 0.f};
-  if ((GRAD && j.kind != kProbs) || row >= j.M) return r;
+  if ((GRAD ? j.kind != kProbs : j.kind != kStats) || row >= j.M) return r;
   r.target = load_target(g.targets, g.id_bytes, row, g.vocab);
   if (GRAD) r.lse = g.lse[row];
   return r;
@@ -224,6 +242,28 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const Job& j, const 
                                          uint32_t tmem, int row, int half, R release) {
   const int n0 = x.nt * j.bn;
   const bool row_ok = row < j.M;
+  if (!GRAD && j.kind == kFew) {
+    // a thread holds one row of the vocabulary, its columns are the tokens
+    const int lane = threadIdx.x & 31;
+    for_columns(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+      const int token = n0 + c + lane;
+      const int target = token < j.N ? load_target(g.targets, g.id_bytes, token, g.vocab) : -1;
+      float m[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        if (__shfl_sync(0xffffffffu, target, k) == row) g.target_logit[n0 + c + k] = v[k];
+        v[k] = row_ok ? v[k] * kLog2e : -INFINITY;
+        m[k] = v[k];
+      }
+      const float top = join_lanes(m, lane, [](float a, float b) { return fmaxf(a, b); });
+      const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = exp2_fast(v[k] - __shfl_sync(0xffffffffu, ref, k));
+      const float sum = join_lanes(v, lane, [](float a, float b) { return a + b; });
+      if (token < j.N) g.part[static_cast<int64_t>(token) * (j.m_tiles * 8) + row / 32] = make_float2(top, sum);
+    }, release);
+    return;
+  }
   if (!GRAD) {
     const int target = info.target - n0;
     float top = -INFINITY, sum = 0.f;
@@ -425,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm
       if (!ok || x.job < 0) break;
       const Job& j = jobs[x.job];
       const CUtensorMap *ma = &g.a[x.job], *mb = &g.b[x.job];
-      const int kind = GRAD ? j.kind : static_cast<int>(kStats);
+      const int kind = GRAD ? j.kind : static_cast<int>(kStats);   // kFew loads alike
       const int am = x.mt * kTileM + static_cast<int>(rank) * 128;
       const int bn = x.nt * j.bn + static_cast<int>(rank) * (j.bn / 2);
       // an MN-major operand comes as boxes of 64 columns, with K the row index
@@ -764,7 +804,6 @@ constexpr int64_t kPieceBytes = int64_t(128) << 20;
 constexpr int64_t kMinPiece = 2048, kLeastPiece = 256;
 constexpr int64_t kMostPieceBytes = int64_t(1) << 30;
 constexpr int kMaxSplits = 64;
-constexpr int kMinLossTile = 96;
 
 int64_t piece_rows(int64_t tokens) {
   const int64_t row = 2 * std::max<int64_t>(tokens, 1);   // bytes of D per row of the vocabulary
@@ -806,24 +845,12 @@ GradSpace grad_space(int64_t tokens, int64_t vocab, int64_t width, const GradPla
   return s;
 }
 
-// Columns of a tile of the loss.  Many tokens: the widest.  A few tokens (one
-// row of tiles): the time is that of reading the table, and the width is the
-// one whose last round of tiles over the pairs of SMs wastes least (200 tokens
-// x 32000 x 1024: 18.8 us against 19.7 with the widest; 16 x 50257 x 768: the
-// same).
-int loss_tile(int64_t tokens, int64_t vocab) {
-  if (tokens > kTileM) return kTileN;
-  int best = kTileN;
-  int64_t cost = INT64_MAX;
-  for (int bn = kTileN; bn >= kMinLossTile; bn -= 32) {
-    const int64_t c = ceil_div(ceil_div(vocab, bn), kPairs) * (bn + 8);
-    if (c < cost) {
-      cost = c;
-      best = bn;
-    }
-  }
-  return best;
-}
+// Up to so many tokens the loss's operands change places: the vocabulary takes
+// the 256 rows of a tile and the tokens its columns, so that the products take
+// no time for rows that are not there.  16 tokens x 50257 x 768 take 20.5 us so
+// and 23.5 with the tokens as rows, x 32000 x 2048 28 and 40; from 64 tokens on
+// the joining of the columns over the lanes takes longer: 24.9 and 22.0.
+constexpr int64_t kFewTokens = 32;
 
 // The loss goes over the tokens in slabs: its partial sums take 16 bytes for
 // each token and 256 columns, which must not grow with the batch.
@@ -831,8 +858,8 @@ constexpr int64_t kSlab = 32768;
 
 int64_t loss_space(int64_t tokens, int64_t vocab) {
   tokens = std::min(tokens, kSlab);
-  // room for a row of the narrowest tiles, which few tokens may get
-  const int64_t parts = std::max(tokens * ceil_div(vocab, kTileN), std::min<int64_t>(tokens, kTileM) * ceil_div(vocab, kMinLossTile));
+  const int64_t tiles = ceil_div(vocab, kTileN);
+  const int64_t parts = std::max(tokens * tiles, std::min(tokens, kFewTokens) * tiles * 4);
   return round_up(parts * 16, 256) + round_up(tokens * 4, 256);
 }
 
@@ -911,29 +938,33 @@ extern "C" int zero_lm_loss(int64_t tokens, int64_t vocab, int64_t width, int dt
     GemmArgs g;
     std::memset(&g, 0, sizeof g);
     Job& j = g.job[0];
-    j.kind = kStats;
-    j.bn = loss_tile(count, vocab);
-    j.m_tiles = static_cast<int>(ceil_div(count, kTileM));
-    j.n_tiles = static_cast<int>(ceil_div(vocab, j.bn));
+    // rows and columns of the product: tokens and vocabulary, or for a few tokens the other way round
+    const bool few = count <= kFewTokens;
+    j.kind = few ? kFew : kStats;
+    j.M = static_cast<int>(few ? vocab : count);
+    j.N = static_cast<int>(few ? count : vocab);
+    j.bn = few ? static_cast<int>(round_up(count, 32)) : kTileN;
+    j.m_tiles = static_cast<int>(ceil_div(j.M, kTileM));
+    j.n_tiles = static_cast<int>(ceil_div(j.N, j.bn));
     j.splits = 1;
     j.tiles = j.m_tiles * j.n_tiles;
     j.kb_total = static_cast<int>(ceil_div(width, kTileK));
-    j.M = static_cast<int>(count);
-    j.N = static_cast<int>(vocab);
     j.stage_tx = 2 * (kOperandBytes + j.bn / 2 * kTileK * 2);
+    const int parts = few ? j.m_tiles * 8 : j.n_tiles * 2;   // of a token
     g.jobs = 1;
     g.vocab = static_cast<int>(vocab);
     g.targets = slab_targets;
     g.id_bytes = id_bytes;
     g.part = static_cast<float2*>(workspace);
-    g.target_logit = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(count * j.n_tiles * 16, 256));
+    g.target_logit = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(count * parts * 8, 256));
     const uint16_t* rows = static_cast<const uint16_t*>(hidden) + t0 * hidden_stride;
-    if ((rc = make_map(&g.a[0], dtype, rows, count, width, hidden_stride, 128))) return rc;
-    if ((rc = make_map(&g.b[0], dtype, table, vocab, width, table_stride, j.bn / 2))) return rc;
+    CUtensorMap *of_tokens = few ? &g.b[0] : &g.a[0], *of_vocab = few ? &g.a[0] : &g.b[0];
+    if ((rc = make_map(of_tokens, dtype, rows, count, width, hidden_stride, few ? j.bn / 2 : 128))) return rc;
+    if ((rc = make_map(of_vocab, dtype, table, vocab, width, table_stride, few ? 128 : j.bn / 2))) return rc;
     if ((rc = launch_gemm<false>(g, dtype, s))) return rc;
     const dim3 grid(static_cast<unsigned>(ceil_div(count * 32, kSmallThreads)));
-    ZERO_CUDA(launch_chained(lm_combine, grid, kSmallThreads, 0, s, g.part, 2 * j.n_tiles, g.target_logit, slab_targets,
-                             id_bytes, g.vocab, j.M, loss + t0, lse + t0));
+    ZERO_CUDA(launch_chained(lm_combine, grid, kSmallThreads, 0, s, g.part, parts, g.target_logit, slab_targets, id_bytes,
+                             g.vocab, static_cast<int>(count), loss + t0, lse + t0));
   }
   return ZERO_OK;
 }
