@@ -617,22 +617,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm
 
 constexpr int kSmallThreads = 256;
 
-// One warp per token: joins the tiles' maxima and sums, writes lse and loss.
+// A maximum and a sum joined with another pair: sums of exponentials relative
+// to their maxima.
+__device__ __forceinline__ void join_pair(float& top, float& sum, float top2, float sum2) {
+  const float m = fmaxf(top, top2), ref = m == -INFINITY ? 0.f : m;
+  sum = sum * exp2_fast(top - ref) + sum2 * exp2_fast(top2 - ref);
+  top = m;
+}
+
+// Joins the tiles' maxima and sums of each token and writes lse and loss: TEAM
+// threads a token, a warp for many tokens, a block for kFew's few, whose parts
+// are more (16 tokens of 1,576 parts: 8 us with a warp each).
+template <int TEAM>
 __global__ void __launch_bounds__(kSmallThreads) lm_combine(const float2* part, int tiles, const float* target_logit,
                                                             const void* targets, int id_bytes, int vocab, int tokens,
                                                             float* loss, float* lse) {
+  __shared__ float2 of_warp[kSmallThreads / 32];
   allow_next();
   await_previous();
-  const int row = (blockIdx.x * kSmallThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  if (row >= tokens) return;
+  const int row = (blockIdx.x * kSmallThreads + threadIdx.x) / TEAM, at = threadIdx.x % TEAM;
+  if (row >= tokens) return;   // whole teams
   const float2* p = part + static_cast<int64_t>(row) * tiles;
   float top = -INFINITY, sum = 0.f;
-  for (int k0 = lane; k0 < tiles; k0 += 32 * 4) {
+  for (int k0 = at; k0 < tiles; k0 += TEAM * 4) {
     float2 x[4];
     float m = top;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      x[k] = k0 + 32 * k < tiles ? p[k0 + 32 * k] : make_float2(-INFINITY, 0.f);
+      x[k] = k0 + TEAM * k < tiles ? p[k0 + TEAM * k] : make_float2(-INFINITY, 0.f);
       m = fmaxf(m, x[k].x);
     }
     const float ref = m == -INFINITY ? 0.f : m;
@@ -644,12 +656,15 @@ __global__ void __launch_bounds__(kSmallThreads) lm_combine(const float2* part, 
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float t2 = __shfl_xor_sync(0xffffffffu, top, o), s2 = __shfl_xor_sync(0xffffffffu, sum, o);
-    const float m = fmaxf(top, t2);
-    const float ref = m == -INFINITY ? 0.f : m;
-    sum = sum * exp2_fast(top - ref) + s2 * exp2_fast(t2 - ref);
-    top = m;
+    join_pair(top, sum, t2, s2);
   }
-  if (lane == 0) {
+  if (TEAM > 32) {
+    if (at % 32 == 0) of_warp[at / 32] = make_float2(top, sum);
+    __syncthreads();
+    if (at == 0)
+      for (int k = 1; k < TEAM / 32; ++k) join_pair(top, sum, of_warp[k].x, of_warp[k].y);
+  }
+  if (at == 0) {
     const float l = fmaf(top, kLn2, logf(sum));
     lse[row] = l;
     loss[row] = load_target(targets, id_bytes, row, vocab) >= 0 ? l - target_logit[row] : 0.f;
@@ -962,9 +977,11 @@ extern "C" int zero_lm_loss(int64_t tokens, int64_t vocab, int64_t width, int dt
     if ((rc = make_map(of_tokens, dtype, rows, count, width, hidden_stride, few ? j.bn / 2 : 128))) return rc;
     if ((rc = make_map(of_vocab, dtype, table, vocab, width, table_stride, few ? 128 : j.bn / 2))) return rc;
     if ((rc = launch_gemm<false>(g, dtype, s))) return rc;
-    const dim3 grid(static_cast<unsigned>(ceil_div(count * 32, kSmallThreads)));
-    ZERO_CUDA(launch_chained(lm_combine, grid, kSmallThreads, 0, s, g.part, parts, g.target_logit, slab_targets, id_bytes,
-                             g.vocab, static_cast<int>(count), loss + t0, lse + t0));
+    const int team = few ? kSmallThreads : 32;
+    const dim3 grid(static_cast<unsigned>(ceil_div(count * team, kSmallThreads)));
+    ZERO_CUDA(launch_chained(few ? lm_combine<kSmallThreads> : lm_combine<32>, grid, kSmallThreads, 0, s, g.part, parts,
+                             g.target_logit, slab_targets, id_bytes, g.vocab, static_cast<int>(count), loss + t0,
+                             lse + t0));
   }
   return ZERO_OK;
 }
