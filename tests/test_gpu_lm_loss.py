@@ -50,8 +50,12 @@ SIZES = [(1, 1, 8), (1, 2, 8), (2, 31, 16), (3, 257, 72), (31, 1000, 136), (32, 
          (255, 511, 136), (257, 2048, 128), (300, 4099, 520), (64, 5000, 1600), (1, 50257, 768), (515, 777, 2056)]
 
 
+# each width of tile that a few tokens as columns take, and the counts around its changes
+FEW = [(48, 4099, 64), (64, 257, 72), (65, 1000, 136), (95, 255, 64), (96, 513, 264), (97, 513, 264)]
+
+
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
-@pytest.mark.parametrize("N,V,d", SIZES)
+@pytest.mark.parametrize("N,V,d", SIZES + FEW)
 def test_loss_and_gradients(N, V, d, dtype):
     h, t, tg = make(N, V, d, dtype, seed=N + V + d, t_sigma=min(0.3, 2 / d ** 0.5))
     loss, lse, dh, dt, want = check(h, t, tg, scale=2048.0 / N if dtype == "fp16" else 1.0 / N, what=f"{N}x{V}x{d}")

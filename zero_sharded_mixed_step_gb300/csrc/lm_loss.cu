@@ -862,10 +862,12 @@ GradSpace grad_space(int64_t tokens, int64_t vocab, int64_t width, const GradPla
 
 // Up to so many tokens the loss's operands change places: the vocabulary takes
 // the 256 rows of a tile and the tokens its columns, so that the products take
-// no time for rows that are not there.  16 tokens x 50257 x 768 take 20.5 us so
-// and 23.5 with the tokens as rows, x 32000 x 2048 28 and 40; from 64 tokens on
-// the joining of the columns over the lanes takes longer: 24.9 and 22.0.
-constexpr int64_t kFewTokens = 32;
+// no time for rows that are not there.  Exchanged and with the tokens as rows,
+// us: 16 tokens x 50257 x 768 19.5 and 24.5, 64 tokens 20.2 and 25.6, 96 tokens
+// 22.0 and 22.5; x 32000 x 2048 28.1 and 35.7 for 16, 30.8 and 31.1 for 96.  At
+// 128 tokens the joining of the columns over the lanes takes what the products
+// save: 22.8 and 22.6, 31.6 and 31.3.
+constexpr int64_t kFewTokens = 96;
 
 // The loss goes over the tokens in slabs: its partial sums take 16 bytes for
 // each token and 256 columns, which must not grow with the batch.
