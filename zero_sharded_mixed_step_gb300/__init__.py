@@ -792,22 +792,23 @@ def _current_stream(index):
     return _current_stream(index)
 
 
-def _rows(x, what, rows, width, dtype):
+def _rows(x, what, rows, width, dtype, device):
     """(address, row stride) of a matrix of 16-bit rows; raises ValueError where it is none."""
     shape = x.shape
-    if len(shape) == 2 and shape[0] == rows and shape[1] == width and x.dtype is dtype and x.is_cuda:
+    if len(shape) == 2 and shape[0] == rows and shape[1] == width and x.dtype is dtype and x.device == device:
         stride, step = x.stride()
         if step == 1 or width == 1:
             return x.data_ptr(), (stride if rows > 1 else width)
-    raise ValueError(f"{what} must be a CUDA tensor of {rows} rows of {width} adjacent {dtype} values, not {x.dtype} "
-                     f"{tuple(shape)} with strides {x.stride()}")
+    raise ValueError(f"{what} must be a tensor on {device} of {rows} rows of {width} adjacent {dtype} values, not "
+                     f"{x.dtype} {tuple(shape)} with strides {x.stride()} on {x.device}")
 
 
-def _ids(x, what):
+def _ids(x, what, device):
     """(address, bytes per id) of a contiguous vector of ids."""
     size = x.element_size()
-    if size < 4 or x.is_floating_point() or x.is_complex() or not x.is_contiguous() or not x.is_cuda:
-        raise ValueError(f"{what} must be a contiguous CUDA tensor of int32 or int64 ids, not {x.dtype}")
+    if size < 4 or x.is_floating_point() or x.is_complex() or not x.is_contiguous() or x.device != device:
+        raise ValueError(f"{what} must be a contiguous tensor of int32 or int64 ids on {device}, not {x.dtype} on "
+                         f"{x.device}")
     return x.data_ptr(), size
 
 
@@ -884,9 +885,9 @@ class LmLoss(_Owner):
         """(loss, lse) of each token, fp32; loss is 0 where the target lies outside the vocabulary."""
         tokens = targets.numel()
         self._check_tokens(tokens)
-        h, hs = _rows(hidden, "hidden", tokens, self.width, self.torch_dtype)
-        t, ts = _rows(table, "table", self.vocab, self.width, self.torch_dtype)
-        ids, id_bytes = _ids(targets, "targets")
+        h, hs = _rows(hidden, "hidden", tokens, self.width, self.torch_dtype, self.device)
+        t, ts = _rows(table, "table", self.vocab, self.width, self.torch_dtype, self.device)
+        ids, id_bytes = _ids(targets, "targets", self.device)
         loss = self._empty(tokens, self._fp32) if loss is None else self._vector(loss, tokens)
         lse = self._empty(tokens, self._fp32) if lse is None else self._vector(lse, tokens)
         self._loss(tokens, self.vocab, self.width, self.dtype, h, hs, t, ts, ids, id_bytes, loss.data_ptr(),
@@ -901,27 +902,27 @@ class LmLoss(_Owner):
             raise ValueError("accumulate needs the dtable to add to")
         tokens = targets.numel()
         self._check_tokens(tokens)
-        h, hs = _rows(hidden, "hidden", tokens, self.width, self.torch_dtype)
-        t, ts = _rows(table, "table", self.vocab, self.width, self.torch_dtype)
-        ids, id_bytes = _ids(targets, "targets")
+        h, hs = _rows(hidden, "hidden", tokens, self.width, self.torch_dtype, self.device)
+        t, ts = _rows(table, "table", self.vocab, self.width, self.torch_dtype, self.device)
+        ids, id_bytes = _ids(targets, "targets", self.device)
         self._vector(lse, tokens)
         if dhidden is None:
             dhidden = self._empty((tokens, self.width), self.torch_dtype)
             dh, dhs = dhidden.data_ptr(), self.width
         else:
-            dh, dhs = _rows(dhidden, "dhidden", tokens, self.width, self.torch_dtype)
+            dh, dhs = _rows(dhidden, "dhidden", tokens, self.width, self.torch_dtype, self.device)
         if dtable is None:
             dtable = self._empty((self.vocab, self.width), self.torch_dtype)
             dt, dts = dtable.data_ptr(), self.width
         else:
-            dt, dts = _rows(dtable, "dtable", self.vocab, self.width, self.torch_dtype)
+            dt, dts = _rows(dtable, "dtable", self.vocab, self.width, self.torch_dtype, self.device)
         self._grad(tokens, self.vocab, self.width, self.dtype, h, hs, t, ts, ids, id_bytes, lse.data_ptr(), scale, dh,
                    dhs, dt, dts, 1 if accumulate else 0, self._ws, self.workspace_bytes, self._raw_stream())
         return dhidden, dtable
 
     def _vector(self, x, tokens):
-        if x.dtype != self._fp32 or x.numel() != tokens or not x.is_contiguous() or not x.is_cuda:
-            raise ValueError(f"loss and lse must be contiguous CUDA tensors of {tokens} fp32 values")
+        if x.dtype != self._fp32 or x.numel() != tokens or not x.is_contiguous() or x.device != self.device:
+            raise ValueError(f"loss and lse must be contiguous tensors of {tokens} fp32 values on {self.device}")
         return x
 
     def status(self):
@@ -944,13 +945,13 @@ class Embedding(_Owner):
     def forward(self, tokens, table, out=None):
         """scale * table[tokens], one row per id (0 for an id outside the table)."""
         count = tokens.numel()
-        t, ts = _rows(table, "table", self.vocab, self.width, self.torch_dtype)
-        ids, id_bytes = _ids(tokens, "tokens")
+        t, ts = _rows(table, "table", self.vocab, self.width, self.torch_dtype, self.device)
+        ids, id_bytes = _ids(tokens, "tokens", self.device)
         if out is None:
             out = self._empty((count, self.width), self.torch_dtype)
             o, os_ = out.data_ptr(), self.width
         else:
-            o, os_ = _rows(out, "out", count, self.width, self.torch_dtype)
+            o, os_ = _rows(out, "out", count, self.width, self.torch_dtype, self.device)
         self._lookup(count, self.vocab, self.width, self.dtype, ids, id_bytes, t, ts, self.scale, o, os_,
                      self._raw_stream())
         return out
@@ -961,13 +962,13 @@ class Embedding(_Owner):
             raise ValueError("accumulate needs the dtable to add to")
         count = tokens.numel()
         self._check_tokens(count)
-        ids, id_bytes = _ids(tokens, "tokens")
-        d, ds = _rows(dout, "dout", count, self.width, self.torch_dtype)
+        ids, id_bytes = _ids(tokens, "tokens", self.device)
+        d, ds = _rows(dout, "dout", count, self.width, self.torch_dtype, self.device)
         if dtable is None:
             dtable = self._empty((self.vocab, self.width), self.torch_dtype)
             t, ts = dtable.data_ptr(), self.width
         else:
-            t, ts = _rows(dtable, "dtable", self.vocab, self.width, self.torch_dtype)
+            t, ts = _rows(dtable, "dtable", self.vocab, self.width, self.torch_dtype, self.device)
         self._grad(count, self.vocab, self.width, self.dtype, ids, id_bytes, d, ds, self.scale, t, ts,
                    1 if accumulate else 0, self._ws, self.workspace_bytes, self._raw_stream())
         return dtable
@@ -1000,12 +1001,15 @@ class GradClip(_Owner):
         self._c_norm, self._c_clip = self._bind("zero_grad_norm"), self._bind("zero_grad_clip")
 
     def _pointers(self, grads):
-        T = self.torch.Tensor
+        T, count = self.torch.Tensor, len(self.numels)
         flat = [g for rank in grads for g in rank]
-        if len(grads) != self.W or list(map(T.numel, flat)) != self._expected:
+        if (len(grads) != self.W or any(len(rank) != count for rank in grads)
+                or list(map(T.numel, flat)) != self._expected):
             raise ValueError(f"grads must be {self.W} lists of tensors of the owner's sizes")
-        if {g.dtype for g in flat} - {self.torch_dtype} or not all(map(T.is_contiguous, flat)):
-            raise ValueError(f"gradients must be contiguous and {self.torch_dtype}")
+        # get_device: the index where the tensor is on a GPU (comparing devices takes three times as long)
+        if ({g.dtype for g in flat} - {self.torch_dtype} or set(map(T.get_device, flat)) - {self._index}
+                or not all(map(T.is_contiguous, flat))):
+            raise ValueError(f"gradients must be contiguous, {self.torch_dtype} and on {self.device}")
         return _u64_array(map(T.data_ptr, flat))
 
     def _norm(self, ptrs_at, stream):
@@ -1014,11 +1018,15 @@ class GradClip(_Owner):
                      self.workspace_bytes, stream)
         return norm
 
-    def _clip(self, ptrs_at, norm, max_norm, out, stream):
+    def _out(self, out):
         if out is None:
-            out = self._empty(self.n, self.torch_dtype)
-        if out.numel() != self.n or out.dtype != self.torch_dtype or not out.is_contiguous():
-            raise ValueError(f"out must be {self.n} contiguous values of {self.torch_dtype}")
+            return self._empty(self.n, self.torch_dtype)
+        if (out.numel() != self.n or out.dtype != self.torch_dtype or not out.is_contiguous()
+                or out.device != self.device):
+            raise ValueError(f"out must be {self.n} contiguous values of {self.torch_dtype} on {self.device}")
+        return out
+
+    def _clip(self, ptrs_at, norm, max_norm, out, stream):
         base = out.data_ptr()
         outs, outs_at = _u64_array([base + o for o in self._offsets])
         self._c_clip(self.W, len(self.numels), self._sizes_at, self.dtype, ptrs_at, norm.data_ptr(), max_norm, outs_at,
@@ -1032,12 +1040,15 @@ class GradClip(_Owner):
 
     def clip(self, grads, norm, max_norm, out=None):
         """The flat mean gradient times min(1, max_norm / (norm + 1e-6))."""
+        if norm.dtype != self._fp32 or norm.numel() != 1 or norm.device != self.device:
+            raise ValueError(f"norm must be one fp32 value on {self.device}, not {norm.dtype} {tuple(norm.shape)} on "
+                             f"{norm.device}")
         ptrs, at = self._pointers(grads)
-        return self._clip(at, norm, max_norm, out, self._raw_stream())
+        return self._clip(at, norm, max_norm, self._out(out), self._raw_stream())
 
     def norm_and_clip(self, grads, max_norm, out=None):
         """(norm, flat clipped mean gradient)."""
         ptrs, at = self._pointers(grads)
-        stream = self._raw_stream()
+        out, stream = self._out(out), self._raw_stream()
         norm = self._norm(at, stream)
         return norm, self._clip(at, norm, max_norm, out, stream)
