@@ -73,3 +73,59 @@ def test_matrices_ids_and_vectors_off_the_device_are_refused(zlib, device):
         emb.grad(ids, h)
     with pytest.raises(ValueError, match="cuda:0"):
         zs._ids(ids, "tokens", op.device)
+
+
+class Devices:
+    """Stands for the current device and for torch.cuda.device()."""
+
+    def __init__(self, current):
+        self.current, self.entered = current, []
+
+    def get(self):
+        return self.current
+
+    def device(self, index):
+        import contextlib
+
+        @contextlib.contextmanager
+        def scope():
+            before, self.current = self.current, index
+            self.entered.append(index)
+            yield
+            self.current = before
+        return scope()
+
+
+def test_calls_run_under_the_owners_device(zlib, monkeypatch):
+    """The C entry points launch on the current device: it has to be the owner's at the call."""
+    devices, seen = Devices(0), []
+
+    class Library:
+        @staticmethod
+        def zero_lm_loss(*args):
+            seen.append(devices.current)
+            return 0
+
+        zero_lm_loss_grad = zero_lm_status = zero_lm_workspace_status = zero_lm_loss
+
+        @staticmethod
+        def zero_lm_workspace_bytes(*args):
+            return 256
+
+    monkeypatch.setattr(zs, "lib", lambda: Library)
+    monkeypatch.setattr(zs, "_current_device", devices.get)
+    monkeypatch.setattr(torch.cuda, "device", devices.device)
+    here = zs.LmLoss(40, 16, "fp16", max_tokens=8, device="cuda:0", alloc=on_host)
+    there = zs.LmLoss(40, 16, "fp16", max_tokens=8, device="cuda:1", alloc=on_host)
+    here._loss(), there._loss(), there._grad(), here._grad()
+    assert seen == [0, 1, 1, 0] and devices.current == 0 and devices.entered == [1, 1]
+
+
+def test_errors_under_another_device_are_raised(zlib, monkeypatch):
+    devices = Devices(1)
+    monkeypatch.setattr(zs, "_current_device", devices.get)
+    monkeypatch.setattr(torch.cuda, "device", devices.device)
+    op = zs.LmLoss(40, 16, "fp16", max_tokens=8, device="cuda:0", alloc=on_host)
+    with pytest.raises(zs.ZeroError):
+        op._loss(-1, 40, 16, zs.ZERO_FP16, None, 16, None, 16, None, 8, None, None, None, 0, None)
+    assert devices.entered == [0] and devices.current == 1

@@ -792,6 +792,15 @@ def _current_stream(index):
     return _current_stream(index)
 
 
+def _current_device():
+    """The index of the current device."""
+    global _current_device
+    import torch
+    # without torch.cuda.current_device's check that CUDA is there
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _current_device()
+
+
 def _rows(x, what, rows, width, dtype, device):
     """(address, row stride) of a matrix of 16-bit rows; raises ValueError where it is none."""
     shape = x.shape
@@ -828,12 +837,16 @@ class _Owner:
         self._alloc = alloc
 
     def _bind(self, name):
-        """The C entry point, raising like its wrapper: the owners' calls are
-        short enough for the wrapper's own conversions to count."""
-        fn = getattr(lib(), name)
+        """The C entry point under the owner's device, raising like its wrapper:
+        the owners' calls are short enough for the wrapper's own conversions to count."""
+        fn, index, torch = getattr(lib(), name), self._index, self.torch
 
         def call(*args):
-            rc = fn(*args)
+            if _current_device() == index:
+                rc = fn(*args)
+            else:
+                with torch.cuda.device(index):
+                    rc = fn(*args)
             if rc < 0:
                 raise ZeroError(rc, name, lib().zero_last_error().decode())
         return call
@@ -880,6 +893,7 @@ class LmLoss(_Owner):
         self.with_grad = bool(with_grad)
         self._workspace(zero_lm_workspace_bytes(self.max_tokens, self.vocab, self.width, self.with_grad))
         self._loss, self._grad = self._bind("zero_lm_loss"), self._bind("zero_lm_loss_grad")
+        self._status = self._bind("zero_lm_status")
 
     def loss(self, hidden, table, targets, loss=None, lse=None):
         """(loss, lse) of each token, fp32; loss is 0 where the target lies outside the vocabulary."""
@@ -927,7 +941,7 @@ class LmLoss(_Owner):
 
     def status(self):
         """Wait for the work enqueued so far; raises ZeroError if a device wait gave up."""
-        zero_lm_status(self._raw_stream())
+        self._status(self._raw_stream())
 
 
 class Embedding(_Owner):
