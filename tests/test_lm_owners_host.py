@@ -129,3 +129,9 @@ def test_errors_under_another_device_are_raised(zlib, monkeypatch):
     with pytest.raises(zs.ZeroError):
         op._loss(-1, 40, 16, zs.ZERO_FP16, None, 16, None, 16, None, 8, None, None, None, 0, None)
     assert devices.entered == [0] and devices.current == 1
+
+
+def test_the_norms_workspace_is_zero_whatever_alloc_returns(zlib):
+    """Its count of finished blocks has to start at 0."""
+    op = clip_owner([4, 5])
+    assert op.workspace.numel() == zs.zero_grad_norm_workspace_bytes() and (op.workspace == 0).all()

@@ -852,14 +852,15 @@ class _Owner:
         return call
 
     def _workspace(self, nbytes, zero=False):
-        """The workspace; set to 0 only where the calls ask for it."""
+        """The workspace, from ``alloc`` or PyTorch with any contents; set to 0 only where the calls ask for it."""
         torch = self.torch
         with _on(self.stream):
             if self._alloc is not None:
                 self.workspace = self._alloc(max(256, nbytes), torch.uint8)
             else:
-                self.workspace = (torch.zeros if zero else torch.empty)(max(256, nbytes), dtype=torch.uint8,
-                                                                        device=self.device)
+                self.workspace = torch.empty(max(256, nbytes), dtype=torch.uint8, device=self.device)
+            if zero:
+                self.workspace.zero_()
         self.workspace_bytes = self.workspace.numel()
         self._ws = self.workspace.data_ptr()
 
