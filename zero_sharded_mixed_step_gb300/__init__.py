@@ -863,11 +863,30 @@ class _Owner:
                 self.workspace.zero_()
         self.workspace_bytes = self.workspace.numel()
         self._ws = self.workspace.data_ptr()
+        # where the workspace was used last: its fill, so far
+        self._used = torch.cuda.current_stream(self.device) if self.stream is None and self.workspace.is_cuda else None
+        self._used_raw = self._used.cuda_stream if self._used else None
 
     def _raw_stream(self):
-        if self.stream is None:
-            return _current_stream(self._index) or None
-        return self.stream.cuda_stream or None
+        if self.stream is not None:
+            return self.stream.cuda_stream or None
+        raw = _current_stream(self._index)
+        if raw != self._used_raw:
+            self._change_stream(raw)
+        return raw or None
+
+    def _change_stream(self, raw):
+        """The workspace goes to another stream: after the work of the one that had it, and the allocator must not
+        hand it out again before this one's.  A capture begins with everything before it done and its replays are
+        ordered by the caller, so nothing is recorded there."""
+        torch = self.torch
+        with torch.cuda.device(self._index):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        here = torch.cuda.current_stream(self.device)
+        here.wait_stream(self._used)
+        self.workspace.record_stream(here)
+        self._used, self._used_raw = here, raw
 
     def _empty(self, shape, dtype):
         if self.stream is None:
@@ -885,7 +904,9 @@ class LmLoss(_Owner):
     gradients, for up to ``max_tokens`` tokens a call (zero_lm_loss,
     zero_lm_loss_grad).  The owner holds the workspace: calls that may overlap
     on the GPU need an owner each.  Work goes to ``stream``, or to the stream
-    that is current at the call."""
+    that is current at the call; a call on another stream than the last one's
+    waits for that one (a captured call does not: what a graph's replays may
+    overlap is the caller's to order)."""
 
     def __init__(self, vocab, width, dtype="fp16", max_tokens=8192, with_grad=True, device="cuda", stream=None,
                  alloc=None):
