@@ -117,3 +117,41 @@ def test_a_capture_on_another_stream_than_the_calls_before():
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip((loss, lse, dh, dt), want + grads))
     assert torch.equal(op.loss(h, t, tg)[0], loss)
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_the_clipped_steps_workspace_belongs_to_the_steps_stream(as_handle):
+    """Made in the order of the step's stream, however that is given, while another one is current."""
+    n, W = 50_000, 4
+    theta0 = torch.randn(n, device="cuda") * 0.02
+    side = torch.cuda.Stream()
+    a = zs.ZeroStep(zs.ZERO_SCHEME_Z2, W, [n], "bf16", theta0=theta0)
+    grads = a.new_grad_buffers()
+    for k, x in enumerate(grads):
+        x.copy_(torch.randn(a.n_pad, device="cuda") * 0.01 * (k + 1))
+    torch.cuda.synchronize()
+    b = zs.ZeroStep(zs.ZERO_SCHEME_Z2, W, [n], "bf16", theta0=theta0, stream=side.cuda_stream if as_handle else side)
+    torch.cuda.synchronize()
+    a.step(grads, LR, B1, B2, EPS, 1, max_norm=0.1)
+    nbytes = zs.zero_step_clipped_workspace_bytes(b.ctx)
+    dirty = torch.full((nbytes,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del dirty
+    torch.cuda._sleep(DELAY)            # on the current stream, which the step does not use
+    b.step(grads, LR, B1, B2, EPS, 1, max_norm=0.1)
+    b.sync()
+    got = b.grad_norm.clone()
+    torch.cuda.synchronize()
+    assert torch.equal(got, a.grad_norm) and torch.equal(b.master, a.master) and torch.equal(b.p16, a.p16)
+    a.close(), b.close()
+
+
+def test_owners_take_a_stream_by_its_handle():
+    side = torch.cuda.Stream()
+    h = torch.randn(40, 64, device="cuda").half()
+    t, tg = torch.randn(90, 64, device="cuda").half(), torch.arange(40, device="cuda")
+    want = zs.LmLoss(90, 64, "fp16", max_tokens=40).loss(h, t, tg)
+    torch.cuda.synchronize()
+    got = zs.LmLoss(90, 64, "fp16", max_tokens=40, stream=side.cuda_stream).loss(h, t, tg)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -593,7 +593,7 @@ class ZeroStep:
             return
         if self._clip_space is None:
             nbytes = zero_step_clipped_workspace_bytes(self.ctx)
-            with _on(self.stream):
+            with _on(self.stream, self.device):
                 self._clip_space = self._alloc(nbytes, self.torch.uint8)
                 self.grad_norm = self._alloc(1, self.torch.float32)
         zero_step_clipped(self.ctx, self.scheme, self.W, self.n, grads, lr, beta1, beta2, eps, t, max_norm,
@@ -770,12 +770,17 @@ class ZeroOffload:
 
 # ---- operators of a language model around the step ----------------------------------
 
-def _on(stream):
-    """Allocate in the order of ``stream`` (None: the current one)."""
+def _on(stream, device):
+    """Allocate in the order of ``stream``, a stream or its handle (None: the current one)."""
     import contextlib
 
     import torch
-    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _stream_getter():
@@ -854,7 +859,7 @@ class _Owner:
     def _workspace(self, nbytes, zero=False):
         """The workspace, from ``alloc`` or PyTorch with any contents; set to 0 only where the calls ask for it."""
         torch = self.torch
-        with _on(self.stream):
+        with _on(self.stream, self.device):
             if self._alloc is not None:
                 self.workspace = self._alloc(max(256, nbytes), torch.uint8)
             else:
@@ -869,7 +874,7 @@ class _Owner:
 
     def _raw_stream(self):
         if self.stream is not None:
-            return self.stream.cuda_stream or None
+            return _stream(self.stream)
         raw = _current_stream(self._index)
         if raw != self._used_raw:
             self._change_stream(raw)
@@ -891,7 +896,7 @@ class _Owner:
     def _empty(self, shape, dtype):
         if self.stream is None:
             return self._new(shape, dtype=dtype, device=self.device)
-        with _on(self.stream):
+        with _on(self.stream, self.device):
             return self._new(shape, dtype=dtype, device=self.device)
 
     def _check_tokens(self, count):
