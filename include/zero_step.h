@@ -822,8 +822,9 @@ int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, int dtype, c
 int zero_lm_status(void* stream);
 
 /*
- * Testing the bounded waits: in the calling thread's next LM call the first
- * tile's first block of operands never arrives.  The waits for it run out
+ * Testing the bounded waits: in the calling thread's next LM call (refused
+ * and empty ones count, and lose nothing) the first tile's first block of
+ * operands never arrives.  The waits for it run out
  * after about a second, the CTAs count a device error, wait (bounded) for the
  * copies they did issue and return; what the call writes is not valid, and
  * zero_lm_status then returns ZERO_E_STATE.  Nothing faults or hangs, and

@@ -38,6 +38,7 @@
 #include <cstdint>
 #include <cstring>
 #include <type_traits>
+#include <utility>
 
 #include "launch.cuh"
 #include "step_math.cuh"
@@ -765,10 +766,13 @@ int make_map(CUtensorMap* map, int dtype, const void* base, int64_t rows, int64_
 
 thread_local bool g_stall_next = false;
 
+// Whether this call, the thread's next one, was to lose a block of operands.
+bool take_stall() { return std::exchange(g_stall_next, false); }
+
+// Launch the products; `stall` is handed to the first launch of a call alone.
 template <bool GRAD>
-int launch_gemm(GemmArgs& g, int dtype, cudaStream_t s) {
-  g.stall = g_stall_next;
-  g_stall_next = false;
+int launch_gemm(GemmArgs& g, int dtype, cudaStream_t s, bool& stall) {
+  g.stall = std::exchange(stall, false);
   const auto fn = dtype == ZERO_FP16 ? lm_gemm<__half, GRAD> : lm_gemm<__nv_bfloat16, GRAD>;
   ZERO_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem));
   int64_t tiles = 0;
@@ -938,6 +942,7 @@ extern "C" int zero_lm_loss(int64_t tokens, int64_t vocab, int64_t width, int dt
                             int64_t hidden_stride, const void* table, int64_t table_stride, const void* targets,
                             int id_bytes, float* loss, float* lse, void* workspace, int64_t workspace_bytes,
                             void* stream) {
+  bool stall = take_stall();
   int rc = check_common(tokens, vocab, width, dtype, hidden, hidden_stride, table, table_stride, targets, id_bytes,
                         workspace);
   if (rc) return rc;
@@ -978,7 +983,7 @@ extern "C" int zero_lm_loss(int64_t tokens, int64_t vocab, int64_t width, int dt
     CUtensorMap *of_tokens = few ? &g.b[0] : &g.a[0], *of_vocab = few ? &g.a[0] : &g.b[0];
     if ((rc = make_map(of_tokens, dtype, rows, count, width, hidden_stride, few ? j.bn / 2 : 128))) return rc;
     if ((rc = make_map(of_vocab, dtype, table, vocab, width, table_stride, few ? 128 : j.bn / 2))) return rc;
-    if ((rc = launch_gemm<false>(g, dtype, s))) return rc;
+    if ((rc = launch_gemm<false>(g, dtype, s, stall))) return rc;
     const int team = few ? kSmallThreads : 32;
     const dim3 grid(static_cast<unsigned>(ceil_div(count * team, kSmallThreads)));
     ZERO_CUDA(launch_chained(few ? lm_combine<kSmallThreads> : lm_combine<32>, grid, kSmallThreads, 0, s, g.part, parts,
@@ -993,6 +998,7 @@ extern "C" int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, i
                                  int id_bytes, const float* lse, double scale, void* dhidden, int64_t dhidden_stride,
                                  void* dtable, int64_t dtable_stride, int accumulate, void* workspace,
                                  int64_t workspace_bytes, void* stream) {
+  bool stall = take_stall();
   int rc = check_common(tokens, vocab, width, dtype, hidden, hidden_stride, table, table_stride, targets, id_bytes,
                         workspace);
   if (rc) return rc;
@@ -1094,7 +1100,7 @@ extern "C" int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, i
       if ((rc = make_map(&g.b[g.jobs], dtype, table, vocab, width, table_stride, kTileN / 2))) return rc;
       ++g.jobs;
     }
-    if ((rc = launch_gemm<true>(g, dtype, s))) return rc;
+    if ((rc = launch_gemm<true>(g, dtype, s, stall))) return rc;
   }
   if (dtype == ZERO_FP16)
     ZERO_CUDA(launch_chained(lm_finish_dhidden<__half>, dim3(small_grid(items)), kSmallThreads, 0, s, acc, p.splits,
