@@ -790,7 +790,8 @@ int64_t zero_lm_workspace_bytes(int64_t tokens, int64_t vocab, int64_t width, in
  *              least width, a multiple of 8); rows start on 16-byte boundaries.
  *   targets    device, int32 (id_bytes 4) or int64 (8).
  *   loss, lse  device, `tokens` fp32 values each.
- *   workspace  device, 256-byte aligned, any contents.
+ *   workspace  device, 256-byte aligned, any contents; its first 4 bytes count
+ *              waits that gave up (zero_lm_workspace_status).
  * Products are accumulated, and the sums of exponentials kept, in fp32.
  * Enqueues on `stream` (NULL: legacy default) and returns.
  */
@@ -815,9 +816,19 @@ int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, int dtype, c
                       int64_t dtable_stride, int accumulate, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
- * Wait for `stream` and report the LM kernels' bounded device waits (each
- * about a second): ZERO_E_STATE if any gave up on the current device since
- * the last call, so that what it belonged to is incomplete; else ZERO_OK.
+ * Wait for `stream` and report the bounded device waits (each about a second)
+ * of the LM calls made with `workspace`: ZERO_E_STATE if any gave up since the
+ * last report, so that what it belonged to is incomplete; else ZERO_OK.  The
+ * workspace's first 4 bytes hold the count: set them to 0 before the first
+ * call if this is to be asked.  `stream` is the calls' (all of them have run
+ * when this returns).
+ */
+int zero_lm_workspace_status(void* workspace, void* stream);
+
+/*
+ * The same over every LM call on the current device: wait for `stream`, and
+ * ZERO_E_STATE if any wait gave up since the last zero_lm_status.  Whose it
+ * was, zero_lm_workspace_status says; neither takes a report from the other.
  */
 int zero_lm_status(void* stream);
 
@@ -827,7 +838,7 @@ int zero_lm_status(void* stream);
  * operands never arrives.  The waits for it run out
  * after about a second, the CTAs count a device error, wait (bounded) for the
  * copies they did issue and return; what the call writes is not valid, and
- * zero_lm_status then returns ZERO_E_STATE.  Nothing faults or hangs, and
+ * zero_lm_workspace_status and zero_lm_status then return ZERO_E_STATE.  Nothing faults or hangs, and
  * later calls are not affected.
  */
 int zero_lm_inject_stall(void);

@@ -138,3 +138,32 @@ def test_rows_that_no_id_names_are_zero_in_a_large_table(N, kind):
     ref.assert_within(got, total, bound, "dtable")
     emb.grad(ids, rows, wide[:, :d])
     assert torch.equal(wide[:, :d], got) and (wide[:, d:] == 3).all()
+
+
+def _gradient_time(ids, rows, V):
+    """Median device time of the table's gradient, in us."""
+    emb = zs.Embedding(V, rows.shape[1], "bf16", max_tokens=len(ids))
+    table = torch.empty(V, rows.shape[1], dtype=torch.bfloat16, device="cuda")
+    times = []
+    for _ in range(13):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda._sleep(200_000)        # the call is queued whole before it runs
+        a.record()
+        emb.grad(ids, rows, table)
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b) * 1e3)
+    return sorted(times[3:])[5]
+
+
+@pytest.mark.parametrize("N,V,d,share", [(65_535, 1 << 20, 64, 1), (47_000, 50_257, 768, 1), (8192, 50_257, 768, 2)])
+def test_a_frequent_id_costs_the_same_wherever_it_stands(N, V, d, share):
+    """One token in `share` has one id, as padding has: the first of the table, or the last."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    ids = torch.randint(0, V, (N,), device="cuda", generator=gen)
+    rows = torch.randn(N, d, device="cuda", generator=gen).bfloat16()
+    us = []
+    for frequent in (0, V - 1):
+        ids[::share] = frequent
+        us.append(_gradient_time(ids, rows, V))
+    assert us[1] <= 1.3 * us[0] + 3, us

@@ -290,3 +290,18 @@ def test_refusals():
                   tensors([10, 20], 1, "bf16"), [[ok[0][0], torch.zeros(40, dtype=torch.float16, device="cuda")[::2]]]):
         with pytest.raises(ValueError):
             op.norm(wrong)
+
+
+@pytest.mark.parametrize("scheme,units", [(zs.ZERO_SCHEME_Z2, [300_007]), (zs.ZERO_SCHEME_Z3, [4096, 70_001, 5])])
+def test_timing_shows_the_norm_pass(scheme, units):
+    s = zs.ZeroStep(scheme, 4, units, "bf16", theta0=torch.randn(sum(units), device="cuda"))
+    zs.zero_enable_timing(s.ctx, True)
+    for t in (1, 2, 3):
+        s.step(ranks(s, 4, "bf16", 1e-2, t), LR, B1, B2, EPS, t, max_norm=1.0)
+    s.step(ranks(s, 4, "bf16", 1e-2, 4), LR, B1, B2, EPS, 4)
+    ms, n = zs.zero_read_timing(s.ctx, zs.ZERO_KERNEL_NORM)
+    assert n == 3 and ms > 0
+    ms, n = zs.zero_read_timing(s.ctx, zs.ZERO_KERNEL_FUSED)
+    assert n == 4 * len(units) and ms > 0
+    assert zs.zero_read_timing(s.ctx, zs.ZERO_KERNEL_NORM) == (0.0, 0)
+    s.close()

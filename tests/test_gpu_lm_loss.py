@@ -1,6 +1,8 @@
 """The cross entropy over a large vocabulary and its gradients against a plain
 64-bit form, inside bounds derived from the kernels' arithmetic."""
 
+import math
+
 import pytest
 import torch
 
@@ -322,3 +324,61 @@ def test_calls_in_a_cuda_graph():
         torch.cuda.synchronize()
         got = [x.clone() for x in outs]
         assert all(torch.equal(x, y) for x, y in zip(got, run()))
+
+
+@pytest.mark.parametrize("N", [96, 200])
+def test_large_logits_lose_nothing_to_the_change_of_base(N):
+    """Two equal logits l, exact in fp32: lse = l + log 2.  Exponents are formed
+    in base 2 and back: the two constants' product is within 1.2e-8 of 1, the
+    result is rounded once (half a unit in its last place), and the two
+    exponentials and the logarithm are good to 1e-6.  A rounding of l log2(e)
+    by itself would show here."""
+    a = torch.linspace(17, 32, N, device="cuda").half()
+    h, t = torch.zeros(N, 8, device="cuda").half(), torch.zeros(2, 8, device="cuda").half()
+    h[:, 0], t[:, 0] = a, 31.78125
+    want = a.double() * 31.78125 + math.log(2)
+    ulp = 2.0 ** (torch.floor(torch.log2(want)) - 23)
+    loss, lse = zs.LmLoss(2, 8, "fp16", max_tokens=N).loss(h, t, torch.zeros(N, dtype=torch.int64, device="cuda"))
+    ref.assert_within(lse, want, ulp / 2 + want * 1.2e-8 + 1e-6, "lse")
+    # the subtraction of the logit is exact (within a factor of 2 of lse)
+    ref.assert_within(loss, torch.full_like(want, math.log(2)), ulp / 2 + want * 1.2e-8 + 1e-6, "loss")
+
+
+def test_four_pieces_of_the_vocabulary():
+    """Enough pieces that both buffers of D are used again and dh is added to
+    more than once; the last piece is shorter than the others."""
+    h, t, tg = make(9000, 25_001, 16, "bf16", seed=4, t_sigma=0.3)
+    *_, dh, dt, want = check(h, t, tg, scale=1 / 9000)
+    assert ref.rel_norm(dh, want["dhidden"]) <= 2 * ref.HALF_ULP[h.dtype]
+    assert ref.rel_norm(dt, want["dtable"]) <= 2 * ref.HALF_ULP[h.dtype]
+
+
+@pytest.mark.parametrize("tail", [1, 96, 97])
+def test_a_short_last_slab(tail):
+    """After a slab of 32768 tokens, one small enough for exchanged operands (and one just not)."""
+    h, t, tg = make(32_768 + tail, 300, 24, "fp16", seed=tail)
+    op = zs.LmLoss(300, 24, "fp16", max_tokens=len(tg), with_grad=False)
+    loss, lse = op.loss(h, t, tg)
+    op.status()
+    want = ref.lm_reference(h, t, tg)
+    valid = ref.valid_mask(tg, 300)
+    ref.assert_within(loss, want["loss"], want["loss_bound"], "loss")
+    ref.assert_within(lse[valid], want["lse"][valid], want["lse_bound"][valid], "lse")
+    last = zs.LmLoss(300, 24, "fp16", max_tokens=tail).loss(h[-tail:].contiguous(), t, tg[-tail:].contiguous())
+    assert torch.equal(loss[-tail:], last[0]) and torch.equal(lse[-tail:], last[1])
+
+
+@pytest.mark.parametrize("N,V,d", [(133, 517, 72), (5000, 20_011, 72), (40, 3000, 64)])
+def test_a_table_gradient_added_in_fp16(N, V, d):
+    """D carries a factor of 2^14 in fp16, which has to be undone before the old value is added."""
+    h, t, tg = make(N, V, d, "fp16", seed=N)
+    scale = 2048.0 / N
+    op = zs.LmLoss(V, d, "fp16", max_tokens=N)
+    lse = op.loss(h, t, tg)[1]
+    want = ref.lm_reference(h, t, tg, scale)
+    old = torch.randn(V, d, device="cuda").half()
+    dh, got = op.grad(h, t, tg, lse, scale, dtable=old.clone(), accumulate=True)
+    total = want["dtable"] + old.double()
+    bound = want["dtable_bound"] + total.abs() * ref.HALF_ULP[h.dtype] + old.double().abs() * 2.0 ** -23
+    ref.assert_within(got, total, bound, "accumulated dtable")
+    ref.assert_within(dh, want["dhidden"], want["dhidden_bound"], "dhidden")

@@ -27,6 +27,45 @@ def make(tokens=N, seed=0):
     return h, t, tg
 
 
+def failed(op):
+    with pytest.raises(zs.ZeroError) as e:
+        op.status()
+    return e.value.code == zs.ZERO_E_STATE
+
+
+@pytest.mark.parametrize("which", ["loss", "grad"])
+def test_an_owner_learns_of_its_own_failures_only(which):
+    h, t, tg = make()
+    a, b = (zs.LmLoss(V, D, "bf16", max_tokens=N) for _ in range(2))
+    lse = a.loss(h, t, tg)[1]
+    a.status()
+    zs.zero_lm_inject_stall()
+    if which == "loss":
+        a.loss(h, t, tg)
+    else:
+        a.grad(h, t, tg, lse, 1.0)
+    b.loss(h, t, tg)
+    b.status()                        # not b's failure, and not b's to report
+    assert failed(a)
+    a.status(), b.status()
+
+
+def test_the_device_count_is_reported_once_beside_the_owners():
+    h, t, tg = make()
+    op = zs.LmLoss(V, D, "bf16", max_tokens=N)
+    try:
+        zs.zero_lm_status()           # what other tests left
+    except zs.ZeroError:
+        pass
+    zs.zero_lm_inject_stall()
+    op.loss(h, t, tg)
+    with pytest.raises(zs.ZeroError) as e:
+        zs.zero_lm_status()
+    assert e.value.code == zs.ZERO_E_STATE
+    zs.zero_lm_status()
+    assert failed(op)
+
+
 @pytest.mark.parametrize("first", ["refused", "empty", "empty gradient"])
 def test_an_injected_stall_is_spent_by_the_next_call(first):
     h, t, tg = make()

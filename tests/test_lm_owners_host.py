@@ -106,7 +106,7 @@ def test_calls_run_under_the_owners_device(zlib, monkeypatch):
             seen.append(devices.current)
             return 0
 
-        zero_lm_loss_grad = zero_lm_status = zero_lm_workspace_status = zero_lm_loss
+        zero_lm_loss_grad = zero_lm_workspace_status = zero_lm_loss
 
         @staticmethod
         def zero_lm_workspace_bytes(*args):
@@ -135,3 +135,15 @@ def test_the_norms_workspace_is_zero_whatever_alloc_returns(zlib):
     """Its count of finished blocks has to start at 0."""
     op = clip_owner([4, 5])
     assert op.workspace.numel() == zs.zero_grad_norm_workspace_bytes() and (op.workspace == 0).all()
+
+
+def test_the_loss_owners_count_of_failures_starts_at_zero(zlib):
+    op = zs.LmLoss(40, 16, "fp16", max_tokens=8, device="cuda:0", alloc=on_host)
+    assert (op.workspace[:4] == 0).all()
+
+
+def test_workspace_status_refusals(zlib):
+    for workspace, want in ((None, zs.ZERO_E_ARG), (0x7F0000000080, zs.ZERO_E_ALIGN)):
+        with pytest.raises(zs.ZeroError) as e:
+            zs.zero_lm_workspace_status(workspace)
+        assert e.value.code == want

@@ -96,6 +96,7 @@ SIGNATURES = {
     "zero_lm_workspace_bytes": (_L, [_L, _L, _L, _I]),
     "zero_lm_loss": (_I, [_L, _L, _L, _I, _P, _L, _P, _L, _P, _I, _P, _P, _P, _L, _P]),
     "zero_lm_loss_grad": (_I, [_L, _L, _L, _I, _P, _L, _P, _L, _P, _I, _P, _D, _P, _L, _P, _L, _I, _P, _L, _P]),
+    "zero_lm_workspace_status": (_I, [_P, _P]),
     "zero_lm_status": (_I, [_P]),
     "zero_lm_inject_stall": (_I, []),
     "zero_last_error": (ctypes.c_char_p, []),
@@ -492,8 +493,13 @@ def zero_lm_loss_grad(tokens, vocab, width, dtype, hidden, hidden_stride, table,
         1 if accumulate else 0, _addr(workspace), workspace_bytes, _stream(stream)))
 
 
+def zero_lm_workspace_status(workspace, stream=None) -> None:
+    """Wait for the stream; raises ZeroError if a bounded device wait of a call with this workspace gave up."""
+    _check("zero_lm_workspace_status", lib().zero_lm_workspace_status(_addr(workspace), _stream(stream)))
+
+
 def zero_lm_status(stream=None) -> None:
-    """Wait for the stream; raises ZeroError if a bounded device wait of the LM kernels gave up."""
+    """Wait for the stream; raises ZeroError if a bounded device wait of any LM call on the device gave up."""
     _check("zero_lm_status", lib().zero_lm_status(_stream(stream)))
 
 
@@ -856,8 +862,8 @@ class _Owner:
                 raise ZeroError(rc, name, lib().zero_last_error().decode())
         return call
 
-    def _workspace(self, nbytes, zero=False):
-        """The workspace, from ``alloc`` or PyTorch with any contents; set to 0 only where the calls ask for it."""
+    def _workspace(self, nbytes, zero=0):
+        """The workspace, from ``alloc`` or PyTorch with any contents; its first ``zero`` bytes are set to 0."""
         torch = self.torch
         with _on(self.stream, self.device):
             if self._alloc is not None:
@@ -865,7 +871,7 @@ class _Owner:
             else:
                 self.workspace = torch.empty(max(256, nbytes), dtype=torch.uint8, device=self.device)
             if zero:
-                self.workspace.zero_()
+                self.workspace[:zero].zero_()
         self.workspace_bytes = self.workspace.numel()
         self._ws = self.workspace.data_ptr()
         # where the workspace was used last: its fill, so far
@@ -918,9 +924,9 @@ class LmLoss(_Owner):
         self._setup(dtype, device, stream, alloc)
         self.vocab, self.width, self.max_tokens = int(vocab), int(width), int(max_tokens)
         self.with_grad = bool(with_grad)
-        self._workspace(zero_lm_workspace_bytes(self.max_tokens, self.vocab, self.width, self.with_grad))
+        self._workspace(zero_lm_workspace_bytes(self.max_tokens, self.vocab, self.width, self.with_grad), zero=4)
         self._loss, self._grad = self._bind("zero_lm_loss"), self._bind("zero_lm_loss_grad")
-        self._status = self._bind("zero_lm_status")
+        self._status = self._bind("zero_lm_workspace_status")
 
     def loss(self, hidden, table, targets, loss=None, lse=None):
         """(loss, lse) of each token, fp32; loss is 0 where the target lies outside the vocabulary."""
@@ -967,8 +973,8 @@ class LmLoss(_Owner):
         return x
 
     def status(self):
-        """Wait for the work enqueued so far; raises ZeroError if a device wait gave up."""
-        self._status(self._raw_stream())
+        """Wait for the owner's calls so far; raises ZeroError if a device wait of theirs gave up."""
+        self._status(self._ws, self._raw_stream())
 
 
 class Embedding(_Owner):
@@ -1038,7 +1044,8 @@ class GradClip(_Owner):
             offsets.append(at * self._item)
             at += k
         self._offsets = offsets
-        self._workspace(zero_grad_norm_workspace_bytes(), zero=True)
+        nbytes = zero_grad_norm_workspace_bytes()
+        self._workspace(nbytes, zero=nbytes)
         self._c_norm, self._c_clip = self._bind("zero_grad_norm"), self._bind("zero_grad_clip")
 
     def _pointers(self, grads):

@@ -37,6 +37,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
 #include <type_traits>
 #include <utility>
 
@@ -49,7 +50,7 @@
 
 namespace zero {
 
-// Bounded device-side waits of lm_gemm that gave up.
+// Bounded device-side waits of lm_gemm that gave up, over all calls; never set back (see zero_lm_status).
 __device__ unsigned int g_lm_timeouts;
 
 namespace {
@@ -110,6 +111,7 @@ struct GemmArgs {
   int jobs;
   int stall;                 // testing the bounded waits: the first pair's first block of K never arrives
   unsigned int* next;        // tiles handed out beyond one per pair (0 at the launch)
+  unsigned int* failures;    // the workspace's count of waits that gave up
   int vocab;
   const void* targets;
   int id_bytes;
@@ -602,6 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm
   if (failed) {
     if (threadIdx.x == 0) {
       atomicAdd(&g_lm_timeouts, 1u);
+      atomicAdd(g.failures, 1u);
       // the copies in flight land on the leader's barriers: both CTAs stay until they have
       if (rank == 0)
         for (int k = max(0, issued - kStages); k < issued; ++k) bar_wait(full(k % kStages), (k / kStages) & 1);
@@ -845,6 +848,10 @@ GradPlan plan_grad(int64_t tokens, int64_t vocab, int64_t width) {
   return p;
 }
 
+// The workspace begins with its count of waits that gave up, which the calls
+// add to and zero_lm_workspace_status reads and clears.
+constexpr int64_t kStatusBytes = 256;
+
 // Byte offsets of the workspace's parts: the masked hidden vectors, D of two
 // pieces (one is formed while the other is used), dh's fp32 sums, and a tile
 // counter for each launch.
@@ -855,8 +862,8 @@ struct GradSpace {
 GradSpace grad_space(int64_t tokens, int64_t vocab, int64_t width, const GradPlan& p) {
   const int64_t pieces = ceil_div(vocab, p.piece);
   GradSpace s;
-  s.hidden = 0;
-  s.probs[0] = round_up(tokens * width * 2, 256);
+  s.hidden = kStatusBytes;
+  s.probs[0] = s.hidden + round_up(tokens * width * 2, 256);
   s.probs[1] = s.probs[0] + round_up(tokens * p.piece * 2, 256);
   s.acc = s.probs[1] + (pieces > 1 ? s.probs[1] - s.probs[0] : 0);
   s.counters = s.acc + round_up(p.splits * tokens * width * 4, 256);
@@ -881,7 +888,7 @@ int64_t loss_space(int64_t tokens, int64_t vocab) {
   tokens = std::min(tokens, kSlab);
   const int64_t tiles = ceil_div(vocab, kTileN);
   const int64_t parts = std::max(tokens * tiles, std::min(tokens, kFewTokens) * tiles * 4);
-  return round_up(parts * 16, 256) + round_up(tokens * 4, 256);
+  return kStatusBytes + round_up(parts * 16, 256) + round_up(tokens * 4, 256);
 }
 
 constexpr int64_t kMaxTokens = int64_t(1) << 24, kMaxVocab = int64_t(1) << 24, kMaxWidth = int64_t(1) << 16;
@@ -935,7 +942,8 @@ extern "C" int64_t zero_lm_workspace_bytes(int64_t tokens, int64_t vocab, int64_
   const int64_t probs = 2 * piece;
   const int64_t sums = std::max(tokens, std::min<int64_t>(tokens * kMaxSplits, kPairs * kTileM)) * round_up(width, 256) * 4;
   const int64_t counters = (ceil_div(vocab, kLeastPiece) + 1) * 4;
-  return std::max(bytes, round_up(tokens * width * 2, 256) + round_up(probs, 512) + round_up(sums, 256) + round_up(counters, 256));
+  return std::max(bytes, kStatusBytes + round_up(tokens * width * 2, 256) + round_up(probs, 512) + round_up(sums, 256) +
+                             round_up(counters, 256));
 }
 
 extern "C" int zero_lm_loss(int64_t tokens, int64_t vocab, int64_t width, int dtype, const void* hidden,
@@ -977,8 +985,10 @@ extern "C" int zero_lm_loss(int64_t tokens, int64_t vocab, int64_t width, int dt
     g.vocab = static_cast<int>(vocab);
     g.targets = slab_targets;
     g.id_bytes = id_bytes;
-    g.part = static_cast<float2*>(workspace);
-    g.target_logit = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(count * parts * 8, 256));
+    g.failures = static_cast<unsigned int*>(workspace);
+    char* space = static_cast<char*>(workspace) + kStatusBytes;
+    g.part = reinterpret_cast<float2*>(space);
+    g.target_logit = reinterpret_cast<float*>(space + round_up(count * parts * 8, 256));
     const uint16_t* rows = static_cast<const uint16_t*>(hidden) + t0 * hidden_stride;
     CUtensorMap *of_tokens = few ? &g.b[0] : &g.a[0], *of_vocab = few ? &g.a[0] : &g.b[0];
     if ((rc = make_map(of_tokens, dtype, rows, count, width, hidden_stride, few ? j.bn / 2 : 128))) return rc;
@@ -1036,6 +1046,7 @@ extern "C" int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, i
     GemmArgs g;
     std::memset(&g, 0, sizeof g);
     g.next = counters + k;
+    g.failures = static_cast<unsigned int*>(workspace);
     g.vocab = static_cast<int>(vocab);
     g.targets = targets;
     g.id_bytes = id_bytes;
@@ -1111,15 +1122,34 @@ extern "C" int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, i
   return ZERO_OK;
 }
 
-extern "C" int zero_lm_status(void* stream) {
+extern "C" int zero_lm_workspace_status(void* workspace, void* stream) {
+  if (workspace == nullptr) return fail(ZERO_E_ARG, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(ZERO_E_ALIGN, "workspace must be 256-byte aligned");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned int n = 0;
+  ZERO_CUDA(cudaMemcpyAsync(&n, workspace, sizeof n, cudaMemcpyDeviceToHost, s));
   ZERO_CUDA(cudaStreamSynchronize(s));
-  ZERO_CUDA(cudaMemcpyFromSymbol(&n, g_lm_timeouts, sizeof n));
   if (n == 0) return ZERO_OK;
-  const unsigned int zero_count = 0;
-  ZERO_CUDA(cudaMemcpyToSymbol(g_lm_timeouts, &zero_count, sizeof zero_count));
+  ZERO_CUDA(cudaMemsetAsync(workspace, 0, sizeof n, s));
   return fail(ZERO_E_STATE, "%u bounded device waits gave up; the losses or gradients they belonged to are incomplete", n);
+}
+
+extern "C" int zero_lm_status(void* stream) {
+  // The device's count only grows: what one call reports cannot be lost to another's clearing of it.
+  constexpr int kDevices = 64;
+  static std::mutex mutex;
+  static unsigned int seen[kDevices];
+  int device = 0;
+  ZERO_CUDA(cudaGetDevice(&device));
+  if (device >= kDevices) return fail(ZERO_E_ARG, "device %d: %d are supported", device, kDevices);
+  ZERO_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
+  std::lock_guard<std::mutex> lock(mutex);
+  unsigned int n = 0;
+  ZERO_CUDA(cudaMemcpyFromSymbol(&n, g_lm_timeouts, sizeof n));
+  const unsigned int fresh = n - seen[device];
+  seen[device] = n;
+  if (fresh == 0) return ZERO_OK;
+  return fail(ZERO_E_STATE, "%u bounded device waits gave up on the device; what they belonged to is incomplete", fresh);
 }
 
 extern "C" int zero_lm_inject_stall(void) {
