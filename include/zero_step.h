@@ -818,7 +818,9 @@ int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, int dtype, c
 /*
  * Wait for `stream` and report the bounded device waits (each about a second)
  * of the LM calls made with `workspace`: ZERO_E_STATE if any gave up since the
- * last report, so that what it belonged to is incomplete; else ZERO_OK.  The
+ * last report, so that what it belonged to is incomplete; else ZERO_OK.  What a
+ * call could not compute is NaN: the losses (of tokens with a target) and lse
+ * that lack a part, or both gradients whole.  The
  * workspace's first 4 bytes hold the count: set them to 0 before the first
  * call if this is to be asked.  `stream` is the calls' (all of them have run
  * when this returns).
@@ -837,7 +839,7 @@ int zero_lm_status(void* stream);
  * and empty ones count, and lose nothing) the first tile's first block of
  * operands never arrives.  The waits for it run out
  * after about a second, the CTAs count a device error, wait (bounded) for the
- * copies they did issue and return; what the call writes is not valid, and
+ * copies they did issue and return; what the call could not compute is NaN, and
  * zero_lm_workspace_status and zero_lm_status then return ZERO_E_STATE.  Nothing faults or hangs, and
  * later calls are not affected.
  */

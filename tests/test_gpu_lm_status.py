@@ -66,6 +66,42 @@ def test_the_device_count_is_reported_once_beside_the_owners():
     assert failed(op)
 
 
+@pytest.mark.parametrize("tokens", [N, 40])
+def test_what_a_failed_loss_could_not_compute_is_nan(tokens):
+    """Every loss is either the right one or a NaN: never what an earlier call left in the workspace."""
+    h, t, tg = make(tokens)
+    op = zs.LmLoss(V, D, "bf16", max_tokens=N)
+    loss, lse = op.loss(h, t, tg)
+    h2, t2, _ = make(tokens, seed=1)
+    op.loss(h2, t2, tg)
+    zs.zero_lm_inject_stall()
+    got, got_lse = op.loss(h, t, tg)
+    assert failed(op)
+    assert torch.isnan(got_lse).any()
+    for x, y in ((got, loss), (got_lse, lse)):
+        assert ((x == y) | torch.isnan(x)).all()
+    again = op.loss(h, t, tg)         # and nothing of it is left
+    assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_failed_gradients_are_nan(accumulate):
+    h, t, tg = make()
+    op = zs.LmLoss(V, D, "bf16", max_tokens=N)
+    lse = op.loss(h, t, tg)[1]
+    wide = torch.zeros(V, D + 8, dtype=torch.bfloat16, device="cuda")
+    want = [x.clone() for x in op.grad(h, t, tg, lse, 1.0, dtable=wide[:, :D], accumulate=accumulate)]
+    wide.zero_()
+    zs.zero_lm_inject_stall()
+    dh, dt = op.grad(h, t, tg, lse, 1.0, dtable=wide[:, :D], accumulate=accumulate)
+    assert failed(op)
+    assert torch.isnan(dh).all() and torch.isnan(dt).all() and (wide[:, D:] == 0).all()
+    wide.zero_()
+    again = op.grad(h, t, tg, lse, 1.0, dtable=wide[:, :D], accumulate=accumulate)
+    op.status()
+    assert all(torch.equal(x, y) for x, y in zip(again, want))
+
+
 @pytest.mark.parametrize("first", ["refused", "empty", "empty gradient"])
 def test_an_injected_stall_is_spent_by_the_next_call(first):
     h, t, tg = make()

@@ -112,6 +112,7 @@ struct GemmArgs {
   int stall;                 // testing the bounded waits: the first pair's first block of K never arrives
   unsigned int* next;        // tiles handed out beyond one per pair (0 at the launch)
   unsigned int* failures;    // the workspace's count of waits that gave up
+  unsigned int* lost;        // gradient: set where tiles of this call were not computed
   int vocab;
   const void* targets;
   int id_bytes;
@@ -377,6 +378,20 @@ uint4 old[4];
   }
 }
 
+// The loss's partial sums of a tile whose products never came: no number, so
+// that the losses that lack it are none either.
+__device__ __forceinline__ void spoil_parts(const GemmArgs& g, const Job& j, const Tile& x, int row, int half) {
+  const float2 none = make_float2(-INFINITY, NAN);
+  if (j.kind == kStats) {
+    if (row < j.M) g.part[(static_cast<int64_t>(row) * j.n_tiles + x.nt) * 2 + half] = none;
+    return;
+  }
+  for (int c = half * 32; c < j.bn; c += 64) {
+    const int token = x.nt * j.bn + c + static_cast<int>(threadIdx.x & 31);
+    if (token < j.N) g.part[static_cast<int64_t>(token) * (j.m_tiles * 8) + row / 32] = none;
+  }
+}
+
 // The persistent product kernel: pairs of CTAs, each pair one 256-row tile at
 // a time, operands through a ring of TMA stages, two accumulators in TMEM so
 // that one tile's epilogue runs beside the next one's products.  The loss's
@@ -582,12 +597,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm
     }
   } else if (warp >= 4) {
     const int quad = warp & 3, half = (warp - 4) >> 2;
-    for (int i = 0;; ++i) {
+    auto row_of = [&](const Tile& x) { return x.mt * kTileM + static_cast<int>(rank) * 128 + quad * 32 + lane; };
+    int i = 0;
+    for (;; ++i) {
       const int a = i & 1;
       const Tile x = tile_of(i);
       if (!ok || x.job < 0) break;
       const Job& j = jobs[x.job];
-      const int row = x.mt * kTileM + static_cast<int>(rank) * 128 + quad * 32 + lane;
+      const int row = row_of(x);
       const RowInfo info = row_info<GRAD>(g, j, row);
       ok = wait_all(done(a), (i >> 1) & 1);
       if (!ok) break;
@@ -598,13 +615,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm
         if (lane == 0) bar_arrive(in_cta(taken(a), 0));
       });
     }
-    if (!ok && lane == 0) failed = 1;
+    if (!ok) {
+      if (lane == 0) failed = 1;
+      if (!GRAD) {
+        // this tile and the pair's others
+        for (;; ++i) {
+          const Tile x = tile_of(i);
+          if (x.job < 0) break;
+          spoil_parts(g, jobs[x.job], x, row_of(x), half);
+        }
+      }
+    }
   }
   __syncthreads();
   if (failed) {
     if (threadIdx.x == 0) {
       atomicAdd(&g_lm_timeouts, 1u);
       atomicAdd(g.failures, 1u);
+      if (GRAD) *g.lost = 1;
       // the copies in flight land on the leader's barriers: both CTAs stay until they have
       if (rank == 0)
         for (int k = max(0, issued - kStages); k < issued; ++k) bar_wait(full(k % kStages), (k / kStages) & 1);
@@ -677,7 +705,8 @@ __global__ void __launch_bounds__(kSmallThreads) lm_combine(const float2* part, 
 
 // The hidden vectors with the rows of tokens without target set to 0: such a
 // row times D's zeros must add nothing to the table's gradient even where it
-// holds an infinity or a NaN.  Also sets the products' tile counters to 0.
+// holds an infinity or a NaN.  Also sets the products' tile counters, and the
+// word after them that says whether a tile was lost, to 0.
 __global__ void __launch_bounds__(kSmallThreads) lm_masked_hidden(const uint16_t* hidden, int64_t stride, int width8,
                                                                   const void* targets, int id_bytes, int vocab,
                                                                   int tokens, uint16_t* out, unsigned int* counters,
@@ -697,14 +726,18 @@ __global__ void __launch_bounds__(kSmallThreads) lm_masked_hidden(const uint16_t
 }
 
 // dh = scale * the sum of the splits' fp32 sums, in the splits' order, so many
-// loads at a time (one by one, 38 splits of 30 tokens took 12 us).
+// loads at a time (one by one, 38 splits of 30 tokens took 12 us).  Where tiles
+// were lost it is not known which: both gradients become NaN.
 constexpr int kFinishBatch = 8;
 
 template <typename T>
 __global__ void __launch_bounds__(kSmallThreads) lm_finish_dhidden(const float* acc, int splits, int64_t tokens,
-                                                                   int width8, float scale, T* out, int64_t stride) {
+                                                                   int width8, float scale, T* out, int64_t stride,
+                                                                   const unsigned int* lost, T* dtable, int64_t vocab,
+                                                                   int64_t dtable_stride) {
   allow_next();
   await_previous();
+  const bool spoiled = *lost != 0;
   const int64_t total = tokens * width8;
   for (int64_t e = static_cast<int64_t>(blockIdx.x) * kSmallThreads + threadIdx.x; e < total;
        e += static_cast<int64_t>(gridDim.x) * kSmallThreads) {
@@ -723,9 +756,14 @@ __global__ void __launch_bounds__(kSmallThreads) lm_finish_dhidden(const float* 
         }
     }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s[q] *= scale;
+    for (int q = 0; q < 8; ++q) s[q] = spoiled ? NAN : s[q] * scale;
     dev::st_16B(out + row * stride + c * 8, Fmt<T>::pack8(s));
   }
+  if (!spoiled) return;
+  const float none[8] = {NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN};
+  for (int64_t row = blockIdx.x; row < vocab; row += gridDim.x)
+    for (int c = threadIdx.x; c < width8; c += kSmallThreads)
+      dev::st_16B(dtable + row * dtable_stride + c * 8, Fmt<T>::pack8(none));
 }
 
 // ---- host -------------------------------------------------------------------------
@@ -854,7 +892,7 @@ constexpr int64_t kStatusBytes = 256;
 
 // Byte offsets of the workspace's parts: the masked hidden vectors, D of two
 // pieces (one is formed while the other is used), dh's fp32 sums, and a tile
-// counter for each launch.
+// counter for each launch with a word for lost tiles after them.
 struct GradSpace {
   int64_t hidden, probs[2], acc, counters, total;
 };
@@ -867,7 +905,7 @@ GradSpace grad_space(int64_t tokens, int64_t vocab, int64_t width, const GradPla
   s.probs[1] = s.probs[0] + round_up(tokens * p.piece * 2, 256);
   s.acc = s.probs[1] + (pieces > 1 ? s.probs[1] - s.probs[0] : 0);
   s.counters = s.acc + round_up(p.splits * tokens * width * 4, 256);
-  s.total = s.counters + round_up((pieces + 1) * 4, 256);
+  s.total = s.counters + round_up((pieces + 2) * 4, 256);
   return s;
 }
 
@@ -941,7 +979,7 @@ extern "C" int64_t zero_lm_workspace_bytes(int64_t tokens, int64_t vocab, int64_
                                  std::min(tokens * wide * 2, kPieceBytes));
   const int64_t probs = 2 * piece;
   const int64_t sums = std::max(tokens, std::min<int64_t>(tokens * kMaxSplits, kPairs * kTileM)) * round_up(width, 256) * 4;
-  const int64_t counters = (ceil_div(vocab, kLeastPiece) + 1) * 4;
+  const int64_t counters = (ceil_div(vocab, kLeastPiece) + 2) * 4;
   return std::max(bytes, kStatusBytes + round_up(tokens * width * 2, 256) + round_up(probs, 512) + round_up(sums, 256) +
                              round_up(counters, 256));
 }
@@ -1035,10 +1073,11 @@ extern "C" int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, i
   unsigned int* counters = reinterpret_cast<unsigned int*>(ws + sp.counters);
   const int width8 = static_cast<int>(width / 8);
   const int64_t pieces = ceil_div(vocab, p.piece), items = tokens * width8;
+  unsigned int* lost = counters + pieces + 1;
   ZERO_CUDA(launch_chained(lm_masked_hidden, dim3(small_grid(items)), kSmallThreads, 0, s,
                            static_cast<const uint16_t*>(hidden), hidden_stride, width8, targets, id_bytes,
                            static_cast<int>(vocab), static_cast<int>(tokens), masked, counters,
-                           static_cast<int>(pieces + 1)));
+                           static_cast<int>(pieces + 2)));
   const float unscale = static_cast<float>(scale) / (dtype == ZERO_FP16 ? d_scale<__half>() : d_scale<__nv_bfloat16>());
 
   // Launch k forms D of piece k and multiplies with D of piece k - 1.
@@ -1046,6 +1085,7 @@ extern "C" int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, i
     GemmArgs g;
     std::memset(&g, 0, sizeof g);
     g.next = counters + k;
+    g.lost = lost;
     g.failures = static_cast<unsigned int*>(workspace);
     g.vocab = static_cast<int>(vocab);
     g.targets = targets;
@@ -1115,10 +1155,12 @@ extern "C" int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, i
   }
   if (dtype == ZERO_FP16)
     ZERO_CUDA(launch_chained(lm_finish_dhidden<__half>, dim3(small_grid(items)), kSmallThreads, 0, s, acc, p.splits,
-                             tokens, width8, unscale, static_cast<__half*>(dhidden), dhidden_stride));
+                             tokens, width8, unscale, static_cast<__half*>(dhidden), dhidden_stride, lost,
+                             static_cast<__half*>(dtable), vocab, dtable_stride));
   else
     ZERO_CUDA(launch_chained(lm_finish_dhidden<__nv_bfloat16>, dim3(small_grid(items)), kSmallThreads, 0, s, acc,
-                             p.splits, tokens, width8, unscale, static_cast<__nv_bfloat16*>(dhidden), dhidden_stride));
+                             p.splits, tokens, width8, unscale, static_cast<__nv_bfloat16*>(dhidden), dhidden_stride, lost,
+                             static_cast<__nv_bfloat16*>(dtable), vocab, dtable_stride));
   return ZERO_OK;
 }
 
