@@ -400,9 +400,11 @@ int64_t zero_stat(const zero_ctx* ctx, int which);
 int zero_sync(zero_ctx* ctx, int timeout_ms);
 
 /* ---- timing of the context's own kernels ---------------------------------- */
-#define ZERO_KERNEL_FUSED   0  /* the fused reduce-scatter + Adam + recast pass */
+#define ZERO_KERNEL_FUSED   0  /* the fused reduce-scatter + Adam + recast pass;
+                                * of a clipped step, its update pass            */
 #define ZERO_KERNEL_GATHER  1  /* ZeRO-3 unit gathers                           */
 #define ZERO_KERNEL_CAST    2  /* working-copy casts                            */
+#define ZERO_KERNEL_NORM    3  /* a clipped step's mean and norm pass           */
 
 /*
  * Per-launch timing on (1) or off (0).  While on, every kernel the context

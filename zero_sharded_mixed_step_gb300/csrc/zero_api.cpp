@@ -306,11 +306,14 @@ int poison_unit(zero_ctx* c, int64_t u, void* buf, cudaStream_t s) {
 
 // The mean and norm pass of a clipped step, on the update stream.
 int launch_norm(zero_ctx* c, const void* const* grads) {
+  Bracket br{c, ZERO_KERNEL_NORM, c->su};
+  const int rc = br.open();
+  if (rc) return rc;
   const cudaError_t e = zero::launch_mean_norm(c->W, c->gdt, grads, c->L.n_pad, c->clip->workspace, c->clip->norm,
                                                c->su, &c->launches);
   if (e != cudaSuccess) return cuda_fail(e, "gradient norm launch");
   touch(c, c->su);
-  return ZERO_OK;
+  return br.close();
 }
 
 // ZeRO-3 step: forward gathers in unit order, backward gathers in reverse
@@ -1025,7 +1028,7 @@ int zero_enable_timing(zero_ctx* c, int on) {
 
 int zero_read_timing(zero_ctx* c, int kernel, double* total_ms, int64_t* launches) {
   if (c == nullptr) return fail(ZERO_E_ARG, "ctx is NULL");
-  if (kernel < ZERO_KERNEL_FUSED || kernel > ZERO_KERNEL_CAST) return fail(ZERO_E_ARG, "unknown kernel %d", kernel);
+  if (kernel < ZERO_KERNEL_FUSED || kernel > ZERO_KERNEL_NORM) return fail(ZERO_E_ARG, "unknown kernel %d", kernel);
   double sum = 0.0;
   int64_t count = 0;
   auto& list = c->timed[kernel];

@@ -118,7 +118,7 @@ struct zero_ctx {
   std::map<int64_t, int64_t> covered;
   int64_t covered_elems = 0;
   std::vector<cudaEvent_t> event_pool;
-  std::vector<std::pair<cudaEvent_t, cudaEvent_t>> timed[3];
+  std::vector<std::pair<cudaEvent_t, cudaEvent_t>> timed[ZERO_KERNEL_NORM + 1];
   // ZeRO-3 steps replayed from a CUDA graph (zero_set_graph): the captured
   // step, its fused-kernel nodes with their launch arguments, and what one
   // step adds to the counters
