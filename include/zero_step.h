@@ -713,14 +713,15 @@ int zero_grad_clip(int W, int64_t n_tensors, const int64_t* numels, int dtype, c
                    const float* norm, double max_norm, void* const* out, void* stream);
 
 /* Device bytes of the workspace zero_step_clipped needs for this context: the
- * fp32 mean gradient (4 n_pad) and the norm's partial sums. */
+ * norm's partial sums and, with 3 ranks or more, the fp32 mean gradient (4 n_pad). */
 int64_t zero_step_clipped_workspace_bytes(const zero_ctx* ctx);
 
 /*
  * zero_step with the mean gradient clipped by its global norm: Adam runs on
  * g * min(1, max_norm / (norm + 1e-6)).  One pass over the W gradient vectors
  * leaves g, in fp32, in the workspace and the norm in *norm; the update reads
- * g from there.  Arguments as for zero_step, and
+ * g from there (with 1 and 2 ranks from the gradients again, which is less).
+ * The gradients must not change until the step has run.  Arguments as for zero_step, and
  *   max_norm   a positive finite fp32 value.
  *   norm       one fp32 value of device memory: the norm before clipping.
  *   workspace  device, 256-byte aligned, zero_step_clipped_workspace_bytes

@@ -305,3 +305,20 @@ def test_timing_shows_the_norm_pass(scheme, units):
     assert n == 4 * len(units) and ms > 0
     assert zs.zero_read_timing(s.ctx, zs.ZERO_KERNEL_NORM) == (0.0, 0)
     s.close()
+
+
+@pytest.mark.parametrize("W", [1, 2])
+def test_few_ranks_step_without_a_mean(W):
+    """Their workspace has no room for one; guards lie around all of it."""
+    n = 100_003
+    arena = Arena(96 << 20, "cuda")
+    theta0 = torch.randn(n, device="cuda") * 0.02
+    a = zs.ZeroStep(zs.ZERO_SCHEME_Z2, W, [n], "fp16", theta0=theta0, alloc=arena)
+    b = zs.ZeroStep(zs.ZERO_SCHEME_Z2, W, [n], "fp16", theta0=theta0)
+    for t in (1, 2):
+        grads = ranks(a, W, "fp16", 1e-2, t)
+        a.step(grads, LR, B1, B2, EPS, t, max_norm=0.1)
+        b.step(grads, LR, B1, B2, EPS, t, max_norm=0.1)
+    assert all(torch.equal(x, y) for x, y in zip(state(a), state(b))) and torch.equal(a.grad_norm, b.grad_norm)
+    arena.check()
+    a.close(), b.close()

@@ -147,3 +147,14 @@ def test_workspace_status_refusals(zlib):
         with pytest.raises(zs.ZeroError) as e:
             zs.zero_lm_workspace_status(workspace)
         assert e.value.code == want
+
+
+@pytest.mark.parametrize("W,keeps_mean", [(1, False), (2, False), (3, True), (8, True)])
+def test_the_clipped_steps_workspace_holds_a_mean_only_where_one_is_written(zlib, W, keeps_mean):
+    """With 1 and 2 ranks the update reads the gradients again."""
+    n, norm = 1_000_003, zs.zero_grad_norm_workspace_bytes()
+    fake = 0x7F0000000000
+    ctx = zs.zero_init(zs.ZERO_SCHEME_Z1, W, n, [n], 0, 0, fake, fake + (1 << 30), fake + (2 << 30), fake + (3 << 30))
+    nbytes = zs.zero_step_clipped_workspace_bytes(ctx)
+    assert (nbytes >= norm + 4 * n) if keeps_mean else (nbytes == norm)
+    zs.zero_destroy(ctx)

@@ -648,7 +648,9 @@ cudaError_t launch_tensors(const Table<BYTES>& t, int dtype, unsigned blocks, co
 
 }  // namespace
 
-int64_t clip_workspace_bytes(int64_t n_pad) { return kNormBytes + host::round_up(n_pad * 4, 256); }
+int64_t clip_workspace_bytes(int W, int64_t n_pad) {
+  return kNormBytes + (W <= kDirectRanks ? 0 : host::round_up(n_pad * 4, 256));
+}
 
 float* clip_mean(void* workspace) { return reinterpret_cast<float*>(static_cast<char*>(workspace) + kNormBytes); }
 

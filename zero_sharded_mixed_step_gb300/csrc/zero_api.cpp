@@ -835,7 +835,7 @@ int zero_step(zero_ctx* c, int scheme, int W, int64_t n, const void* const* grad
 
 int64_t zero_step_clipped_workspace_bytes(const zero_ctx* c) {
   if (c == nullptr) return fail(ZERO_E_ARG, "ctx is NULL");
-  return zero::clip_workspace_bytes(c->L.n_pad);
+  return zero::clip_workspace_bytes(c->W, c->L.n_pad);
 }
 
 int zero_step_clipped(zero_ctx* c, int scheme, int W, int64_t n, const void* const* grads, double lr, double beta1,
@@ -848,9 +848,9 @@ int zero_step_clipped(zero_ctx* c, int scheme, int W, int64_t n, const void* con
   if (norm == nullptr || workspace == nullptr) return fail(ZERO_E_ARG, "norm and workspace are required");
   if (reinterpret_cast<uintptr_t>(norm) % 4) return fail(ZERO_E_ALIGN, "norm must be 4-byte aligned");
   if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(ZERO_E_ALIGN, "workspace must be 256-byte aligned");
-  if (workspace_bytes < zero::clip_workspace_bytes(c->L.n_pad))
+  if (workspace_bytes < zero::clip_workspace_bytes(c->W, c->L.n_pad))
     return fail(ZERO_E_ARG, "workspace of %lld bytes: %lld are needed", (long long)workspace_bytes,
-                (long long)zero::clip_workspace_bytes(c->L.n_pad));
+                (long long)zero::clip_workspace_bytes(c->W, c->L.n_pad));
   const Clip clip = {workspace, norm, limit};
   return run_step(c, scheme, W, n, grads, lr, beta1, beta2, eps, t, &clip);
 }

@@ -77,8 +77,9 @@ cudaError_t launch_rank_mean(const MeanLaunch& a, cudaStream_t stream, int64_t* 
 // The clipped step (grad_clip.cu): the rank-ordered fp32 mean of the W ranks'
 // gradients over the flat vector, kept in the workspace, and its global norm;
 // then the fused launch's segments updated from that mean, scaled by
-// min(1, max_norm / (norm + 1e-6)).
-int64_t clip_workspace_bytes(int64_t n_pad);
+// min(1, max_norm / (norm + 1e-6)).  With 1 and 2 ranks no mean is kept: the
+// update reads the gradients again.
+int64_t clip_workspace_bytes(int W, int64_t n_pad);
 float* clip_mean(void* workspace);
 cudaError_t launch_mean_norm(int W, int grad_dtype, const void* const* grads, int64_t n_pad, void* workspace,
                              float* norm, cudaStream_t stream, int64_t* launches);
