@@ -693,7 +693,8 @@ int64_t zero_grad_norm_workspace_bytes(void);
  *   stream     cudaStream_t (NULL: the legacy default stream).
  * Squares are summed in fp32 within a thread and in fp64 beyond, in an order
  * that depends on the sizes alone.  A NaN or an infinity anywhere makes the
- * norm NaN or infinite, as does a sum of squares beyond fp32's range.
+ * norm NaN or infinite, as does a thread's sum of squares beyond fp32's range;
+ * elements below about 1e-19, whose squares are subnormal, lose precision in it.
  * Enqueues and returns.  ZERO_E_ARG / ZERO_E_ALIGN / ZERO_E_CUDA.
  */
 int zero_grad_norm(int W, int64_t n_tensors, const int64_t* numels, int dtype, const void* const* grads, float* norm,
@@ -721,7 +722,7 @@ int64_t zero_step_clipped_workspace_bytes(const zero_ctx* ctx);
  * g * min(1, max_norm / (norm + 1e-6)).  One pass over the W gradient vectors
  * leaves g, in fp32, in the workspace and the norm in *norm; the update reads
  * g from there (with 1 and 2 ranks from the gradients again, which is less).
- * The gradients must not change until the step has run.  Arguments as for zero_step, and
+ * Arguments as for zero_step, and
  *   max_norm   a positive finite fp32 value.
  *   norm       one fp32 value of device memory: the norm before clipping.
  *   workspace  device, 256-byte aligned, zero_step_clipped_workspace_bytes
@@ -731,8 +732,11 @@ int64_t zero_step_clipped_workspace_bytes(const zero_ctx* ctx);
  * same, and *norm says so.  ZeRO-3 with a unit hook: the backward pass gathers
  * each unit and calls the hook without updating it; the norm and the updates
  * follow, so that gradients which the hook's work makes are complete.  Clipped
- * steps run as ordinary launches under zero_set_graph.  Where the norm is
- * below max_norm the result is that of zero_step, bit for bit.
+ * steps run as ordinary launches under zero_set_graph.  Where norm + 1e-6 (in
+ * fp32) is at most max_norm the factor is 1 and the result that of zero_step,
+ * bit for bit.  zero_step alone has this form: the steps by buckets, from host
+ * memory, on literal replicas, of a static ZeRO-3 and with the optimizer on
+ * the host do not clip.
  */
 int zero_step_clipped(zero_ctx* ctx, int scheme, int W, int64_t n, const void* const* grads, double lr, double beta1,
                       double beta2, double eps, int64_t t, double max_norm, float* norm, void* workspace,

@@ -322,3 +322,21 @@ def test_few_ranks_step_without_a_mean(W):
     assert all(torch.equal(x, y) for x, y in zip(state(a), state(b))) and torch.equal(a.grad_norm, b.grad_norm)
     arena.check()
     a.close(), b.close()
+
+
+def test_a_norm_just_below_the_limit():
+    """The factor is limit / (norm + 1e-6): 1 from norm + 1e-6 <= limit on, below 1 for a limit equal to the norm."""
+    theta0 = torch.randn(1000, device="cuda") * 0.02
+    a, b = (zs.ZeroStep(zs.ZERO_SCHEME_Z2, 4, [1000], "bf16", theta0=theta0) for _ in range(2))
+    grads = ranks(a, 4, "bf16", 1e-5, 1)
+    a.step(grads, LR, B1, B2, EPS, 1)
+    b.step(grads, LR, B1, B2, EPS, 1, max_norm=1e9)
+    norm = np.float32(b.grad_norm.item())
+    for limit, same in ((np.float32(norm + np.float32(1e-6)), True), (norm, False)):
+        c = zs.ZeroStep(zs.ZERO_SCHEME_Z2, 4, [1000], "bf16", theta0=theta0)
+        c.step(grads, LR, B1, B2, EPS, 1, max_norm=float(limit))
+        assert torch.equal(c.m, a.m) == same
+        factor = 1.0 if same else float(limit) / (float(norm) + 1e-6)
+        assert torch.allclose(c.m.double(), a.m.double() * factor, rtol=1e-6, atol=0)
+        c.close()
+    a.close(), b.close()

@@ -349,7 +349,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const Job& j, const 
   } else {
     T* out = static_cast<T*>(j.out16) + static_cast<int64_t>(row) * j.out_stride + n0;
     for_columns_plain(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
-uint4 old[4];
+      uint4 old[4];
       if (j.add) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -911,11 +911,15 @@ GradSpace grad_space(int64_t tokens, int64_t vocab, int64_t width, const GradPla
 
 // Up to so many tokens the loss's operands change places: the vocabulary takes
 // the 256 rows of a tile and the tokens its columns, so that the products take
-// no time for rows that are not there.  Exchanged and with the tokens as rows,
-// us: 16 tokens x 50257 x 768 19.5 and 24.5, 64 tokens 20.2 and 25.6, 96 tokens
-// 22.0 and 22.5; x 32000 x 2048 28.1 and 35.7 for 16, 30.8 and 31.1 for 96.  At
-// 128 tokens the joining of the columns over the lanes takes what the products
-// save: 22.8 and 22.6, 31.6 and 31.3.
+// no time for rows that are not there; joining the columns over the lanes takes
+// time for each 32 tokens instead, whatever the width.  Exchanged and with the
+// tokens as rows, us, the same tables call after call (bf16):
+//            50257 x 768  50257 x 1600  32000 x 2048  50257 x 128  8000 x 256
+//   64       15.3  22.5   32.7  35.7    28.6  30.7    11.3  13.3   7.2  8.0
+//   96       18.3  20.1   34.3  35.9    30.4  30.8    15.5  13.6   9.0  8.1
+//   128      19.3  20.2   34.7  36.0    30.9  31.0    16.5  13.6   9.0  8.1
+// Models of usual widths gain a little up to 128 tokens, the narrowest lose
+// from about 96 on; one limit for all widths lies between.
 constexpr int64_t kFewTokens = 96;
 
 // The loss goes over the tokens in slabs: its partial sums take 16 bytes for

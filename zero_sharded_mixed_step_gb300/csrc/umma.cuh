@@ -11,7 +11,9 @@
 namespace zero {
 namespace umma {
 
-constexpr long long kWaitCycles = 1LL << 31;   // about a second; a real wait is microseconds
+// About a second.  A wait lasts microseconds, and with 2^24 tokens, whose tiles
+// of the table's gradient take 0.07 s each, some tenths of a second.
+constexpr long long kWaitCycles = 1LL << 31;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
