@@ -725,12 +725,14 @@ __global__ void __launch_bounds__(kSmallThreads) lm_masked_hidden(const uint16_t
   }
 }
 
-// dh = scale * the sum of the splits' fp32 sums, in the splits' order, so many
-// loads at a time (one by one, 38 splits of 30 tokens took 12 us).  Where tiles
-// were lost it is not known which: both gradients become NaN.
+// dh = scale * the sum of the splits' fp32 sums, in the splits' order, BATCH
+// loads at a time: several splits, of few tokens, kFinishBatch (one by one, 38
+// splits of 30 tokens took 12 us), one split one, for the registers that a
+// batch takes leave too few threads (8192 x 768 by batches: 14.8 us).  Where
+// tiles were lost it is not known which: both gradients become NaN.
 constexpr int kFinishBatch = 8;
 
-template <typename T>
+template <typename T, int BATCH>
 __global__ void __launch_bounds__(kSmallThreads) lm_finish_dhidden(const float* acc, int splits, int64_t tokens,
                                                                    int width8, float scale, T* out, int64_t stride,
                                                                    const unsigned int* lost, T* dtable, int64_t vocab,
@@ -743,13 +745,13 @@ __global__ void __launch_bounds__(kSmallThreads) lm_finish_dhidden(const float* 
        e += static_cast<int64_t>(gridDim.x) * kSmallThreads) {
     const int64_t row = e / width8, c = e - row * width8;
     float s[8] = {};
-    for (int k0 = 0; k0 < splits; k0 += kFinishBatch) {
-      float x[kFinishBatch][8];
+    for (int k0 = 0; k0 < splits; k0 += BATCH) {
+      float x[BATCH][8];
 #pragma unroll
-      for (int k = 0; k < kFinishBatch; ++k)
+      for (int k = 0; k < BATCH; ++k)
         if (k0 + k < splits) dev::ld_32B(acc + ((k0 + k) * total + e) * 8, x[k]);
 #pragma unroll
-      for (int k = 0; k < kFinishBatch; ++k)
+      for (int k = 0; k < BATCH; ++k)
         if (k0 + k < splits) {
 #pragma unroll
           for (int q = 0; q < 8; ++q) s[q] += x[k][q];
@@ -1157,14 +1159,14 @@ extern "C" int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, i
     }
     if ((rc = launch_gemm<true>(g, dtype, s, stall))) return rc;
   }
-  if (dtype == ZERO_FP16)
-    ZERO_CUDA(launch_chained(lm_finish_dhidden<__half>, dim3(small_grid(items)), kSmallThreads, 0, s, acc, p.splits,
-                             tokens, width8, unscale, static_cast<__half*>(dhidden), dhidden_stride, lost,
-                             static_cast<__half*>(dtable), vocab, dtable_stride));
-  else
-    ZERO_CUDA(launch_chained(lm_finish_dhidden<__nv_bfloat16>, dim3(small_grid(items)), kSmallThreads, 0, s, acc,
-                             p.splits, tokens, width8, unscale, static_cast<__nv_bfloat16*>(dhidden), dhidden_stride, lost,
-                             static_cast<__nv_bfloat16*>(dtable), vocab, dtable_stride));
+  const auto finish = [&](auto* dh, auto* dt) {
+    using T = std::remove_pointer_t<decltype(dh)>;
+    const auto fn = p.splits > 1 ? lm_finish_dhidden<T, kFinishBatch> : lm_finish_dhidden<T, 1>;
+    return launch_chained(fn, dim3(small_grid(items)), kSmallThreads, 0, s, acc, p.splits, tokens, width8, unscale, dh,
+                          dhidden_stride, lost, dt, vocab, dtable_stride);
+  };
+  ZERO_CUDA(dtype == ZERO_FP16 ? finish(static_cast<__half*>(dhidden), static_cast<__half*>(dtable))
+                               : finish(static_cast<__nv_bfloat16*>(dhidden), static_cast<__nv_bfloat16*>(dtable)));
   return ZERO_OK;
 }
 
