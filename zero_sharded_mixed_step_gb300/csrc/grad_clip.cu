@@ -16,7 +16,7 @@
 // in its second (3.73 GB in 548 us, 6.8 TB/s), 912 to 918 us in all; the same
 // bytes at the measured copy rate take 917.  The norm and the clipped mean of
 // 148 tensors of 4 ranks, 20M elements, take 34 + 36 us on the device (160 and
-// 200 MB); a Python caller spends 190 us on 592 tensor objects.
+// 200 MB); a Python caller spends 220 us on 592 tensor objects.
 //
 // Squares are summed in fp32 by each thread and in fp64 from there on: within
 // a block, and over the blocks in their order by the last block to finish, so

@@ -29,7 +29,7 @@
 // of the tensor pipe's cycles (307 us) and the gradient's launches at 0.81 to
 // 0.84 (D is written at 0.7 TB/s beside them); loss and gradient together take
 // 1.43 ms, 1.77 PFLOP/s over the four products.  Called without a pause the
-// power limit brings the clock to about 1.45 GHz and the pair to 1.59 to 1.66 ms.
+// power limit brings the clock to about 1.45 GHz and the pair to 1.6 to 1.7 ms.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
