@@ -10,7 +10,7 @@ from tests import lm_reference as ref
 
 pytestmark = pytest.mark.gpu
 
-DELAY = 40_000_000          # cycles of a sleeping kernel: some 20 ms, longer than the host takes over a test
+DELAY = 200_000_000         # cycles of a sleeping kernel: some 0.1 s, longer than the host takes over a test
 LR, B1, B2, EPS = 1e-3, 0.9, 0.95, 1e-8
 
 
@@ -65,6 +65,29 @@ def test_a_call_follows_the_last_one_on_another_stream():
     torch.cuda.synchronize()
     for x, y in zip(got, want):
         assert all(torch.equal(p, q) for p, q in zip(x, y))
+
+
+def test_calls_without_the_workspace_wait_for_none():
+    """The lookup and the clipping do not use it: they run beside a gradient or a norm on another stream."""
+    h, t = torch.randn(64, 64, device="cuda").half(), torch.randn(100, 64, device="cuda").half()
+    ids, g = torch.zeros(64, dtype=torch.int64, device="cuda"), [torch.ones(100, device="cuda").half()]
+    emb, clip = zs.Embedding(100, 64, "fp16", max_tokens=64), zs.GradClip([100], 1, "fp16")
+    norm = clip.norm([g])
+    emb.grad(ids, h), emb.forward(ids, t), clip.clip([g], norm, 1.0)      # kernels loaded
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    held, free = torch.cuda.Event(), torch.cuda.Event()
+    with torch.cuda.stream(a):
+        torch.cuda._sleep(DELAY)
+        emb.grad(ids, h), clip.norm([g])
+        held.record()
+    with torch.cuda.stream(b):
+        y, out = emb.forward(ids, t), clip.clip([g], norm, 1.0)
+        free.record()
+    free.synchronize()
+    beside = not held.query()
+    torch.cuda.synchronize()
+    assert beside and torch.equal(y, t[ids]) and torch.allclose(out, (g[0].float() / 10).half())
 
 
 @pytest.mark.parametrize("make", [lambda: zs.GradClip([100], 1, "fp16"),

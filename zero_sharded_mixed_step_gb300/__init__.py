@@ -878,11 +878,12 @@ class _Owner:
         self._used = torch.cuda.current_stream(self.device) if self.stream is None and self.workspace.is_cuda else None
         self._used_raw = self._used.cuda_stream if self._used else None
 
-    def _raw_stream(self):
+    def _raw_stream(self, workspace=True):
+        """The handle of the stream for a call, which uses the workspace or not."""
         if self.stream is not None:
             return _stream(self.stream)
         raw = _current_stream(self._index)
-        if raw != self._used_raw:
+        if workspace and raw != self._used_raw:
             self._change_stream(raw)
         return raw or None
 
@@ -1000,7 +1001,7 @@ class Embedding(_Owner):
         else:
             o, os_ = _rows(out, "out", count, self.width, self.torch_dtype, self.device)
         self._lookup(count, self.vocab, self.width, self.dtype, ids, id_bytes, t, ts, self.scale, o, os_,
-                     self._raw_stream())
+                     self._raw_stream(workspace=False))
         return out
 
     def grad(self, tokens, dout, dtable=None, accumulate=False):
@@ -1092,7 +1093,7 @@ class GradClip(_Owner):
             raise ValueError(f"norm must be one fp32 value on {self.device}, not {norm.dtype} {tuple(norm.shape)} on "
                              f"{norm.device}")
         ptrs, at = self._pointers(grads)
-        return self._clip(at, norm, max_norm, self._out(out), self._raw_stream())
+        return self._clip(at, norm, max_norm, self._out(out), self._raw_stream(workspace=False))
 
     def norm_and_clip(self, grads, max_norm, out=None):
         """(norm, flat clipped mean gradient)."""
