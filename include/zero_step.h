@@ -822,6 +822,54 @@ int zero_lm_loss_grad(int64_t tokens, int64_t vocab, int64_t width, int dtype, c
                       const float* lse, double scale, void* dhidden, int64_t dhidden_stride, void* dtable,
                       int64_t dtable_stride, int accumulate, void* workspace, int64_t workspace_bytes, void* stream);
 
+/* Device bytes of the workspace that zero_lm_logprobs with up to `top`
+ * alternatives (with_grad = 0), or both it and zero_lm_logprobs_grad (1), need
+ * for up to `tokens` tokens. */
+int64_t zero_lm_logprobs_workspace_bytes(int64_t tokens, int64_t vocab, int64_t width, int top, int with_grad);
+
+/*
+ * Log probabilities of given tokens, the entropy of each distribution and its
+ * likeliest alternatives: with z = scale * hidden table^T (never stored whole),
+ *   lse[i] = log sum_v exp z[i, v],   logp[i] = z[i, targets[i]] - lse[i],
+ *   entropy[i] = -sum_v p[i, v] log p[i, v],   p = exp(z - lse),
+ * and the `top` largest z[i, v] - lse[i] as top_logp[i, 0..top) with their v as
+ * top_ids[i, 0..top), in falling order, of equal logits the lower v first.
+ * logp is 0 where the target is outside [0, vocab); the token's other results
+ * are written all the same.  Logits of -infinity and NaN are not listed: where
+ * fewer than `top` others are there, the rest of the ids are -1 and their values
+ * -infinity (NaN where lse is NaN or -infinity).
+ *   scale      positive and finite in fp32: 1 / temperature.
+ *   top        0..16 and at most vocab; 0: top_logp and top_ids may be NULL.
+ *   logp, entropy, lse  device, `tokens` fp32 values each.
+ *   top_logp, top_ids   device, tokens x top fp32 and int32 values.
+ * Other arguments as for zero_lm_loss.  Products are accumulated, and all sums
+ * kept, in fp32; the same inputs give the same bits every time.
+ */
+int zero_lm_logprobs(int64_t tokens, int64_t vocab, int64_t width, int dtype, const void* hidden, int64_t hidden_stride,
+                     const void* table, int64_t table_stride, const void* targets, int id_bytes, double scale, int top,
+                     float* logp, float* entropy, float* lse, float* top_logp, int32_t* top_ids, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+
+/*
+ * The gradients of a loss through logp and entropy: with a = dlogp, b = dentropy
+ * (the loss's derivatives for each token) and
+ *   D = a ([v = target] - p) - b p (log p + entropy)
+ *   dhidden = scale D table,   dtable = scale D^T hidden (+ dtable).
+ * The rows of tokens without target, and of tokens whose a and b are both 0, are
+ * 0 whatever their hidden vectors hold.  lse and entropy as zero_lm_logprobs
+ * wrote them with the same scale; dentropy may be NULL (no term of it; entropy
+ * may then be NULL too).  D is rounded to `dtype` for the two products, in fp16
+ * scaled by one power of two for all tokens: what a weight more than about 2^14
+ * below the largest one adds loses precision.
+ * Other arguments as for zero_lm_loss_grad.
+ */
+int zero_lm_logprobs_grad(int64_t tokens, int64_t vocab, int64_t width, int dtype, const void* hidden,
+                          int64_t hidden_stride, const void* table, int64_t table_stride, const void* targets,
+                          int id_bytes, double scale, const float* lse, const float* dlogp, const float* entropy,
+                          const float* dentropy, void* dhidden, int64_t dhidden_stride, void* dtable,
+                          int64_t dtable_stride, int accumulate, void* workspace, int64_t workspace_bytes,
+                          void* stream);
+
 /*
  * Wait for `stream` and report the bounded device waits (each about a second)
  * of the LM calls made with `workspace`: ZERO_E_STATE if any gave up since the

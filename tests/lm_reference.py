@@ -97,3 +97,54 @@ def clip_reference(grads, W, max_norm):
     norm = float(torch.linalg.vector_norm(mean))
     coef = min(1.0, max_norm / (norm + 1e-6)) if math.isfinite(norm) else 1.0
     return norm, mean * coef
+
+
+def logprobs_reference(hidden, table, targets, scale=1.0, dlogp=None, dentropy=None):
+    """dict of the 64-bit logp, entropy, lse and bounds for them; with dlogp also dhidden and dtable and theirs.
+    ``logits`` are the plain ones, ``z_bound`` the error of a scaled logit."""
+    dtype, u = hidden.dtype, HALF_ULP[hidden.dtype]
+    vocab, d = table.shape
+    valid = valid_mask(targets, vocab)
+    h, t = hidden.double(), table.double()
+    if dlogp is not None:
+        a = torch.where(valid, dlogp.double(), 0.0)
+        b = torch.where(valid, dentropy.double(), 0.0) if dentropy is not None else torch.zeros_like(a)
+        active = (a != 0) | (b != 0)
+        h = torch.where(active[:, None], h, 0.0)
+    logits = h @ t.T
+    z = logits * scale
+    lse = torch.logsumexp(z, 1)
+    logs = z - lse[:, None]
+    p = torch.exp(logs)
+    plogp = torch.where(p > 0, p * logs, 0.0)
+    entropy = -plogp.sum(1)
+    at = torch.where(valid, targets, 0).long()[:, None]
+    out = dict(logits=logits, lse=lse, logs=logs, entropy=entropy, logp=torch.where(valid, logs.gather(1, at)[:, 0], 0.0))
+    top = z.abs().amax(1)
+    # a scaled logit: the product's truncations, and its product with scale log2(e), whose factor was rounded once
+    z_bound = (d / 16 + 5) * 2.0 ** -23 * scale * (h.abs() @ t.abs().T).amax(1) + (top + 1) * 2.0 ** -22
+    # sums of exponentials: 2^-22 each; a thread adds at most 16 and the chunks of 64 columns one after another
+    rel_sum = z_bound + 2.0 ** -22 + (vocab / 64 + 100) * 2.0 ** -24
+    out["z_bound"] = z_bound
+    out["lse_bound"] = z_bound + rel_sum + (lse.abs() + 1) * 2.0 ** -22
+    out["logp_bound"] = torch.where(valid, out["lse_bound"] + z_bound + (out["logp"].abs() + 1) * 2.0 ** -22, 0.0)
+    # d entropy = -sum p (log p + entropy) dz, of which sum p |log p + entropy| is at most twice the entropy
+    out["entropy_bound"] = (2 * entropy + 2) * 2 * rel_sum + (entropy + 1) * 2.0 ** -22
+    if dlogp is None:
+        return out
+    onehot = torch.zeros_like(z).scatter_(1, at, active.double()[:, None])
+    inner = logs + entropy[:, None]
+    D = a[:, None] * (onehot - p * active[:, None]) - torch.where(active[:, None] & (p > 0), b[:, None] * p * inner, 0.0)
+    size = a.abs()[:, None] * (p + onehot) + torch.where(p > 0, b.abs()[:, None] * p * (logs.abs() + entropy[:, None]), 0.0)
+    rel_p = (z_bound + out["lse_bound"] + 2.0 ** -21)[:, None]
+    Derr = size * (rel_p + 3 * 2.0 ** -23) + b.abs()[:, None] * p * (rel_p + out["entropy_bound"][:, None]) + D.abs() * u
+    largest = (a.abs() + b.abs() * (entropy + 0.37)).max() if len(a) else 0.0
+    # fp16: the weights are scaled so that the largest bound comes to 2^13 or more
+    Derr = Derr + (TINY16[dtype] * largest * 2.0 ** -13 if dtype == torch.float16 else TINY16[dtype]) * active[:, None]
+    N = h.shape[0]
+    out["dhidden"], out["dtable"] = scale * D @ t, scale * D.T @ h
+    out["dhidden_bound"] = scale * (Derr @ t.abs() + (vocab / 16 + 64) * 2.0 ** -23 * (size @ t.abs())) * (1 + u) + \
+        out["dhidden"].abs() * u + TINY16[dtype]
+    out["dtable_bound"] = scale * (Derr.T @ h.abs() + (N / 16 + 64) * 2.0 ** -23 * (size.T @ h.abs())) * (1 + u) + \
+        out["dtable"].abs() * u + TINY16[dtype]
+    return out

@@ -96,6 +96,10 @@ SIGNATURES = {
     "zero_lm_workspace_bytes": (_L, [_L, _L, _L, _I]),
     "zero_lm_loss": (_I, [_L, _L, _L, _I, _P, _L, _P, _L, _P, _I, _P, _P, _P, _L, _P]),
     "zero_lm_loss_grad": (_I, [_L, _L, _L, _I, _P, _L, _P, _L, _P, _I, _P, _D, _P, _L, _P, _L, _I, _P, _L, _P]),
+    "zero_lm_logprobs_workspace_bytes": (_L, [_L, _L, _L, _I, _I]),
+    "zero_lm_logprobs": (_I, [_L, _L, _L, _I, _P, _L, _P, _L, _P, _I, _D, _I, _P, _P, _P, _P, _P, _P, _L, _P]),
+    "zero_lm_logprobs_grad": (_I, [_L, _L, _L, _I, _P, _L, _P, _L, _P, _I, _D, _P, _P, _P, _P, _P, _L, _P, _L, _I, _P,
+                                   _L, _P]),
     "zero_lm_workspace_status": (_I, [_P, _P]),
     "zero_lm_status": (_I, [_P]),
     "zero_lm_inject_stall": (_I, []),
@@ -491,6 +495,28 @@ def zero_lm_loss_grad(tokens, vocab, width, dtype, hidden, hidden_stride, table,
         tokens, vocab, width, dtype, _addr(hidden), hidden_stride, _addr(table), table_stride, _addr(targets),
         id_bytes, _addr(lse), scale, _addr(dhidden), dhidden_stride, _addr(dtable), dtable_stride,
         1 if accumulate else 0, _addr(workspace), workspace_bytes, _stream(stream)))
+
+
+def zero_lm_logprobs_workspace_bytes(tokens: int, vocab: int, width: int, top: int = 0, with_grad: bool = True) -> int:
+    return _check("zero_lm_logprobs_workspace_bytes", lib().zero_lm_logprobs_workspace_bytes(
+        tokens, vocab, width, top, 1 if with_grad else 0))
+
+
+def zero_lm_logprobs(tokens, vocab, width, dtype, hidden, hidden_stride, table, table_stride, targets, id_bytes, scale,
+                     top, logp, entropy, lse, top_logp, top_ids, workspace, workspace_bytes, stream=None) -> None:
+    _check("zero_lm_logprobs", lib().zero_lm_logprobs(
+        tokens, vocab, width, dtype, _addr(hidden), hidden_stride, _addr(table), table_stride, _addr(targets), id_bytes,
+        scale, top, _addr(logp), _addr(entropy), _addr(lse), _addr(top_logp), _addr(top_ids), _addr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def zero_lm_logprobs_grad(tokens, vocab, width, dtype, hidden, hidden_stride, table, table_stride, targets, id_bytes,
+                          scale, lse, dlogp, entropy, dentropy, dhidden, dhidden_stride, dtable, dtable_stride,
+                          accumulate, workspace, workspace_bytes, stream=None) -> None:
+    _check("zero_lm_logprobs_grad", lib().zero_lm_logprobs_grad(
+        tokens, vocab, width, dtype, _addr(hidden), hidden_stride, _addr(table), table_stride, _addr(targets), id_bytes,
+        scale, _addr(lse), _addr(dlogp), _addr(entropy), _addr(dentropy), _addr(dhidden), dhidden_stride, _addr(dtable),
+        dtable_stride, accumulate, _addr(workspace), workspace_bytes, _stream(stream)))
 
 
 def zero_lm_workspace_status(workspace, stream=None) -> None:
@@ -971,6 +997,78 @@ class LmLoss(_Owner):
     def _vector(self, x, tokens):
         if x.dtype != self._fp32 or x.numel() != tokens or not x.is_contiguous() or x.device != self.device:
             raise ValueError(f"loss and lse must be contiguous tensors of {tokens} fp32 values on {self.device}")
+        return x
+
+    def status(self):
+        """Wait for the owner's calls so far; raises ZeroError if a device wait of theirs gave up."""
+        self._status(self._ws, self._raw_stream())
+
+
+class LmLogprobs(_Owner):
+    """Log probabilities of given tokens under a head of ``vocab`` rows of
+    ``width`` values, with the entropy of each distribution and its ``top``
+    likeliest alternatives (0..16), and their gradients, for up to
+    ``max_tokens`` tokens a call (zero_lm_logprobs, zero_lm_logprobs_grad).
+    ``scale`` multiplies the logits: 1 / temperature.  Workspace and stream as
+    for :class:`LmLoss`."""
+
+    def __init__(self, vocab, width, dtype="fp16", max_tokens=8192, scale=1.0, top=0, with_grad=True, device="cuda",
+                 stream=None, alloc=None):
+        self._setup(dtype, device, stream, alloc)
+        self.vocab, self.width, self.max_tokens = int(vocab), int(width), int(max_tokens)
+        self.scale, self.top, self.with_grad = float(scale), int(top), bool(with_grad)
+        self._workspace(zero_lm_logprobs_workspace_bytes(self.max_tokens, self.vocab, self.width, self.top,
+                                                         self.with_grad), zero=4)
+        self._logprobs, self._grad = self._bind("zero_lm_logprobs"), self._bind("zero_lm_logprobs_grad")
+        self._status = self._bind("zero_lm_workspace_status")
+
+    def _operands(self, hidden, table, targets):
+        tokens = targets.numel()
+        self._check_tokens(tokens)
+        h, hs = _rows(hidden, "hidden", tokens, self.width, self.torch_dtype, self.device)
+        t, ts = _rows(table, "table", self.vocab, self.width, self.torch_dtype, self.device)
+        ids, id_bytes = _ids(targets, "targets", self.device)
+        return tokens, (tokens, self.vocab, self.width, self.dtype, h, hs, t, ts, ids, id_bytes, self.scale)
+
+    def logprobs(self, hidden, table, targets):
+        """(logp, entropy, lse) of each token, fp32; with ``top`` also the alternatives' log probabilities and ids
+        (tokens x top, fp32 and int32, the likeliest first).  logp is 0 where the target lies outside the vocabulary."""
+        tokens, operands = self._operands(hidden, table, targets)
+        logp, entropy, lse = (self._empty(tokens, self._fp32) for _ in range(3))
+        outs, top_logp, top_ids = (logp, entropy, lse), None, None
+        if self.top:
+            values, ids = (self._empty((tokens, self.top), t) for t in (self._fp32, self.torch.int32))
+            outs, top_logp, top_ids = outs + (values, ids), values.data_ptr(), ids.data_ptr()
+        self._logprobs(*operands, self.top, logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top_logp, top_ids,
+                       self._ws, self.workspace_bytes, self._raw_stream())
+        return outs
+
+    def grad(self, hidden, table, targets, lse, dlogp, entropy=None, dentropy=None, dhidden=None, dtable=None,
+             accumulate=False):
+        """(dhidden, dtable) from the gradients of the tokens' logp and, with ``dentropy``, of their entropy; lse and
+        entropy as :meth:`logprobs` returned them.  With ``accumulate`` added onto the given dtable."""
+        if not self.with_grad:
+            raise ValueError("this owner was made without room for the gradient (with_grad=False)")
+        if accumulate and dtable is None:
+            raise ValueError("accumulate needs the dtable to add to")
+        if dentropy is not None and entropy is None:
+            raise ValueError("dentropy needs the entropy")
+        tokens, operands = self._operands(hidden, table, targets)
+        given = [None if x is None else self._vector(x, what, tokens).data_ptr()
+                 for x, what in ((lse, "lse"), (dlogp, "dlogp"), (entropy, "entropy"), (dentropy, "dentropy"))]
+        if dhidden is None:
+            dhidden = self._empty((tokens, self.width), self.torch_dtype)
+        if dtable is None:
+            dtable = self._empty((self.vocab, self.width), self.torch_dtype)
+        dh, dhs = _rows(dhidden, "dhidden", tokens, self.width, self.torch_dtype, self.device)
+        dt, dts = _rows(dtable, "dtable", self.vocab, self.width, self.torch_dtype, self.device)
+        self._grad(*operands, *given, dh, dhs, dt, dts, 1 if accumulate else 0, self._ws, self.workspace_bytes,
+                   self._raw_stream())
+        return dhidden, dtable
+
+    def _vector(self, x, what, tokens):
+        if x.dtype != self._fp32 or x.numel() != tokens or not x.is_contiguous() or x.device != self.device:
+            raise ValueError(f"{what} must be a contiguous tensor of {tokens} fp32 values on {self.device}")
         return x
 
     def status(self):

@@ -125,6 +125,9 @@ cudaError_t reset_device_errors(int slot, cudaStream_t stream);
 // Read a counter slot (synchronous; call after the work has finished).
 cudaError_t read_device_errors(int slot, unsigned int* out);
 
+// Bounded waits of the log probabilities' kernels that gave up on the current device (synchronous).
+cudaError_t logprobs_timeouts(unsigned int* out);
+
 // Streaming multiprocessors of the current device.
 int sm_count();
 
