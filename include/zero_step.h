@@ -870,9 +870,82 @@ int zero_lm_logprobs_grad(int64_t tokens, int64_t vocab, int64_t width, int dtyp
                           int64_t dtable_stride, int accumulate, void* workspace, int64_t workspace_bytes,
                           void* stream);
 
+/* ---- orthogonalised updates of matrices ------------------------------------------------ */
+
+/* Device bytes of the workspace zero_orthogonalize needs for these matrices
+ * (about 4 times their fp32 size). */
+int64_t zero_orthogonalize_workspace_bytes(int64_t n_matrices, const int64_t* rows, const int64_t* cols);
+
+/*
+ * Newton-Schulz orthogonalisation of many matrices: X_0 = G / |G|_F, then for
+ * each step's (a, b, c), over the shorter side,
+ *   A = X X^T,   X <- a X + (b A + c A A) X,
+ * which maps every singular value s to a s + b s^3 + c s^5 and leaves the
+ * singular vectors alone.
+ *   n_matrices, rows, cols  0..65536 matrices with sides of 1..32768.
+ *   dtype      ZERO_FP16, ZERO_BF16 or ZERO_FP32, of every input and output.
+ *   in, out    host arrays of device pointers, aligned to their element;
+ *              in_strides, out_strides the elements from one row to the next
+ *              (at least cols), NULL for contiguous rows.  Matrices that start on
+ *              boundaries of 8 elements with columns and strides of multiples of
+ *              8 are read and written faster.  out[i] may be in[i] with the same
+ *              stride; otherwise no output may overlap an input or another output.
+ *   steps, coefficients  1..32 steps, 3 doubles each, at most 64 in size.  Singular
+ *              values must stay below 4 on the way (fp16's range).
+ *   fine_steps the first so many steps carry every operand as a sum of two fp16
+ *              values (22 bits), the others as one (11 bits); -1 chooses: all for
+ *              ZERO_FP32, else all but the last two.  With Muon's coefficients
+ *              the result is about 1e-3 off so (2-norm), 1e-2 with 0 where few
+ *              singular values stand above the rest, 1e-6 with all.
+ *   workspace  device, 256-byte aligned, any contents; its first 4 bytes count
+ *              waits that gave up (zero_lm_workspace_status).
+ * A matrix of norm 0 gives 0, one whose norm is not finite NaN.  The norm's squares
+ * are summed in fp32 within a thread and in fp64 beyond; products accumulate in
+ * fp32; the result is rounded once.  The same inputs give the same bits every
+ * time.  Enqueues on `stream` and returns.  ZERO_E_ARG / ZERO_E_ALIGN / ZERO_E_CUDA.
+ */
+int zero_orthogonalize(int64_t n_matrices, const int64_t* rows, const int64_t* cols, int dtype, const void* const* in,
+                       const int64_t* in_strides, void* const* out, const int64_t* out_strides, int steps,
+                       const double* coefficients, int fine_steps, void* workspace, int64_t workspace_bytes,
+                       void* stream);
+
+/* Device bytes of the workspace zero_muon_step needs: zero_orthogonalize's and,
+ * with 3 ranks or more, the fp32 mean gradients. */
+int64_t zero_muon_workspace_bytes(int W, int64_t n_matrices, const int64_t* rows, const int64_t* cols);
+
+/*
+ * One optimizer step on matrices whose direction is their orthogonalised
+ * momentum (Muon), for W ranks: for each matrix i
+ *   g = (G_0 + ... + G_{W-1}) / W        (ranks in order, fp32)
+ *   M <- mu M + g,   U = g + mu M (nesterov) or M
+ *   theta <- theta (1 - lr weight_decay) - lr scales[i] X(U),
+ * X as zero_orthogonalize computes it (of the fp32 U), and p16 is theta's
+ * round-to-nearest-even copy.  Matrices alone: vectors and embeddings take
+ * their own zero_step.
+ *   grads      host array of W * n_matrices device pointers, rank after rank:
+ *              grads[w * n_matrices + i], rows[i] x cols[i] contiguous values of
+ *              grad_dtype (ZERO_FP16 or ZERO_BF16).
+ *   master, momentum, p16  host arrays of n_matrices device pointers, contiguous;
+ *              p16 in work_dtype.  Aligned to their element; faster where all of a
+ *              matrix's allow accesses of 8 elements and its columns are a
+ *              multiple of 8.  No two buffers may overlap.
+ *   lr, weight_decay, scales  lr and lr * scales[i] finite in fp32; scales NULL: 1.
+ *   mu         0 <= mu < 1.
+ *   steps, coefficients, fine_steps, workspace  as for zero_orthogonalize.
+ * A matrix whose U has a norm that is not finite (an overflow in fp16 gradients)
+ * keeps its master, momentum and p16 as they were; one of norm 0 decays alone.
+ * The caller keeps the step counter, if any.  A device wait that gave up
+ * (zero_lm_workspace_status) can leave the matrices partly updated: restore them
+ * from a saved copy.
+ */
+int zero_muon_step(int W, int64_t n_matrices, const int64_t* rows, const int64_t* cols, int grad_dtype, int work_dtype,
+                   const void* const* grads, float* const* master, float* const* momentum, void* const* p16, double lr,
+                   double mu, int nesterov, double weight_decay, const double* scales, int steps,
+                   const double* coefficients, int fine_steps, void* workspace, int64_t workspace_bytes, void* stream);
+
 /*
  * Wait for `stream` and report the bounded device waits (each about a second)
- * of the LM calls made with `workspace`: ZERO_E_STATE if any gave up since the
+ * of the LM and matrix calls made with `workspace`: ZERO_E_STATE if any gave up since the
  * last report, so that what it belonged to is incomplete; else ZERO_OK.  What a
  * call could not compute is NaN: the losses (of tokens with a target) and lse
  * that lack a part, or both gradients whole.  The
@@ -883,14 +956,14 @@ int zero_lm_logprobs_grad(int64_t tokens, int64_t vocab, int64_t width, int dtyp
 int zero_lm_workspace_status(void* workspace, void* stream);
 
 /*
- * The same over every LM call on the current device: wait for `stream`, and
+ * The same over every LM and matrix call on the current device: wait for `stream`, and
  * ZERO_E_STATE if any wait gave up since the last zero_lm_status.  Whose it
  * was, zero_lm_workspace_status says; neither takes a report from the other.
  */
 int zero_lm_status(void* stream);
 
 /*
- * Testing the bounded waits: in the calling thread's next LM call (refused
+ * Testing the bounded waits: in the calling thread's next LM or matrix call (refused
  * and empty ones count, and lose nothing) the first tile's first block of
  * operands never arrives.  The waits for it run out
  * after about a second, the CTAs count a device error, wait (bounded) for the

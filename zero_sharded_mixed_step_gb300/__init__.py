@@ -35,6 +35,10 @@ ZERO_MAX_RANKS = 64
 ZERO_KERNEL_FUSED, ZERO_KERNEL_GATHER, ZERO_KERNEL_CAST, ZERO_KERNEL_NORM = 0, 1, 2, 3
 ZERO_DEBUG_POISON_RELEASED = 1
 
+# (a, b, c) of each Newton-Schulz step as Muon's authors published them: they take singular values from about 1e-2
+# up to between 0.7 and 1.2 in five steps
+MUON_COEFFICIENTS = ((3.4445, -4.7750, 2.0315),) * 5
+
 ERROR_NAMES = {ZERO_E_ARG: "ZERO_E_ARG", ZERO_E_ALIGN: "ZERO_E_ALIGN", ZERO_E_CUDA: "ZERO_E_CUDA",
                ZERO_E_RANK: "ZERO_E_RANK", ZERO_E_TIMEOUT: "ZERO_E_TIMEOUT", ZERO_E_STATE: "ZERO_E_STATE",
                ZERO_E_NOMEM: "ZERO_E_NOMEM"}
@@ -100,6 +104,10 @@ SIGNATURES = {
     "zero_lm_logprobs": (_I, [_L, _L, _L, _I, _P, _L, _P, _L, _P, _I, _D, _I, _P, _P, _P, _P, _P, _P, _L, _P]),
     "zero_lm_logprobs_grad": (_I, [_L, _L, _L, _I, _P, _L, _P, _L, _P, _I, _D, _P, _P, _P, _P, _P, _L, _P, _L, _I, _P,
                                    _L, _P]),
+    "zero_orthogonalize_workspace_bytes": (_L, [_L, _P, _P]),
+    "zero_orthogonalize": (_I, [_L, _P, _P, _I, _P, _P, _P, _P, _I, _P, _I, _P, _L, _P]),
+    "zero_muon_workspace_bytes": (_L, [_I, _L, _P, _P]),
+    "zero_muon_step": (_I, [_I, _L, _P, _P, _I, _I, _P, _P, _P, _P, _D, _D, _I, _D, _P, _I, _P, _I, _P, _L, _P]),
     "zero_lm_workspace_status": (_I, [_P, _P]),
     "zero_lm_status": (_I, [_P]),
     "zero_lm_inject_stall": (_I, []),
@@ -517,6 +525,63 @@ def zero_lm_logprobs_grad(tokens, vocab, width, dtype, hidden, hidden_stride, ta
         tokens, vocab, width, dtype, _addr(hidden), hidden_stride, _addr(table), table_stride, _addr(targets), id_bytes,
         scale, _addr(lse), _addr(dlogp), _addr(entropy), _addr(dentropy), _addr(dhidden), dhidden_stride, _addr(dtable),
         dtable_stride, accumulate, _addr(workspace), workspace_bytes, _stream(stream)))
+
+
+def _c_array(code, values):
+    """The values as a C array of the given type code and its address."""
+    a = array.array(code, values)
+    return a, a.buffer_info()[0]
+
+
+def _shape_arrays(shapes):
+    rows, rows_at = _c_array("q", [r for r, _ in shapes])
+    cols, cols_at = _c_array("q", [c for _, c in shapes])
+    return (rows, cols), rows_at, cols_at
+
+
+def _steps_of(coefficients):
+    """(number of steps, array, address) of rows (a, b, c)."""
+    rows = [tuple(map(float, row)) for row in coefficients]
+    if any(len(row) != 3 for row in rows):
+        raise ValueError("coefficients must be rows (a, b, c), one for each step")
+    a, at = _c_array("d", [x for row in rows for x in row])
+    return len(rows), a, at
+
+
+def zero_orthogonalize_workspace_bytes(shapes) -> int:
+    keep, rows, cols = _shape_arrays(shapes)
+    return _check("zero_orthogonalize_workspace_bytes", lib().zero_orthogonalize_workspace_bytes(len(shapes), rows, cols))
+
+
+def zero_orthogonalize(shapes, dtype, matrices, in_strides, out, out_strides, coefficients, fine_steps, workspace,
+                       workspace_bytes, stream=None) -> None:
+    """``in_strides`` and ``out_strides`` may be None (contiguous rows)."""
+    keep, rows, cols = _shape_arrays(shapes)
+    ins, ins_at = _u64_array([_addr(x) or 0 for x in matrices])
+    outs, outs_at = _u64_array([_addr(x) or 0 for x in out])
+    si, si_at = (None, None) if in_strides is None else _c_array("q", in_strides)
+    so, so_at = (None, None) if out_strides is None else _c_array("q", out_strides)
+    steps, co, co_at = _steps_of(coefficients)
+    _check("zero_orthogonalize", lib().zero_orthogonalize(
+        len(shapes), rows, cols, dtype, ins_at, si_at, outs_at, so_at, steps, co_at, fine_steps, _addr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def zero_muon_workspace_bytes(W, shapes) -> int:
+    keep, rows, cols = _shape_arrays(shapes)
+    return _check("zero_muon_workspace_bytes", lib().zero_muon_workspace_bytes(W, len(shapes), rows, cols))
+
+
+def zero_muon_step(W, shapes, grad_dtype, work_dtype, grads, master, momentum, p16, lr, mu, nesterov, weight_decay,
+                   scales, coefficients, fine_steps, workspace, workspace_bytes, stream=None) -> None:
+    """``grads``: W lists of matrices; ``scales`` may be None (1 for every matrix)."""
+    keep, rows, cols = _shape_arrays(shapes)
+    lists = [_u64_array([_addr(x) or 0 for x in xs]) for xs in ([g for rank in grads for g in rank], master, momentum, p16)]
+    sc, sc_at = (None, None) if scales is None else _c_array("d", scales)
+    steps, co, co_at = _steps_of(coefficients)
+    _check("zero_muon_step", lib().zero_muon_step(
+        W, len(shapes), rows, cols, grad_dtype, work_dtype, *(at for _, at in lists), lr, mu, 1 if nesterov else 0,
+        weight_decay, sc_at, steps, co_at, fine_steps, _addr(workspace), workspace_bytes, _stream(stream)))
 
 
 def zero_lm_workspace_status(workspace, stream=None) -> None:
@@ -1199,3 +1264,130 @@ class GradClip(_Owner):
         out, stream = self._out(out), self._raw_stream()
         norm = self._norm(at, stream)
         return norm, self._clip(at, norm, max_norm, out, stream)
+
+
+def _starts(shapes):
+    """Where each matrix starts in a flat vector, on boundaries of 8 values, and the vector's length."""
+    at, starts = 0, []
+    for r, c in shapes:
+        starts.append(at)
+        at += -(-r * c // 8) * 8
+    return starts, at
+
+
+class _Matrices(_Owner):
+    """What the owners over a list of matrices share."""
+
+    def _setup_matrices(self, shapes, coefficients, fine_steps):
+        self.shapes = [(int(r), int(c)) for r, c in shapes]
+        self.starts, self.n = _starts(self.shapes)
+        self._keep, self._rows_at, self._cols_at = _shape_arrays(self.shapes)
+        self.steps, self._co, self._co_at = _steps_of(coefficients)
+        self.fine_steps = -1 if fine_steps is None else int(fine_steps)
+
+    def views(self, flat):
+        """The matrices in a flat vector laid out like the owner's."""
+        return [flat[at:at + r * c].view(r, c) for (r, c), at in zip(self.shapes, self.starts)]
+
+    def status(self):
+        """Wait for the owner's calls so far; raises ZeroError if a device wait of theirs gave up."""
+        self._status(self._ws, self._raw_stream())
+
+
+class Orthogonalize(_Matrices):
+    """Newton-Schulz orthogonalisation of matrices of the given (rows, cols),
+    all of one dtype: "fp16", "bf16" or "fp32" (zero_orthogonalize).
+    ``coefficients`` holds (a, b, c) for each step; ``fine_steps`` of them carry
+    their operands in two 16-bit parts (None: all but the last two, for fp32
+    all).  Workspace and stream as for :class:`LmLoss`."""
+
+    def __init__(self, shapes, dtype="bf16", coefficients=MUON_COEFFICIENTS, fine_steps=None, device="cuda",
+                 stream=None, alloc=None):
+        import torch
+        fp32 = dtype in ("fp32", ZERO_FP32)
+        self._setup("fp16" if fp32 else dtype, device, stream, alloc)
+        if fp32:
+            self.dtype, self.torch_dtype = ZERO_FP32, torch.float32
+        self._setup_matrices(shapes, coefficients, fine_steps)
+        self._workspace(zero_orthogonalize_workspace_bytes(self.shapes), zero=4)
+        self._call, self._status = self._bind("zero_orthogonalize"), self._bind("zero_lm_workspace_status")
+
+    def _addresses(self, matrices, what):
+        if len(matrices) != len(self.shapes):
+            raise ValueError(f"{what}: {len(matrices)} matrices, this owner was made for {len(self.shapes)}")
+        both = [_rows(x, what, r, c, self.torch_dtype, self.device) for x, (r, c) in zip(matrices, self.shapes)]
+        return _u64_array([a for a, _ in both]), _u64_array([s for _, s in both])
+
+    def forward(self, matrices, out=None):
+        """The orthogonalised matrices, written to ``out`` (which may be the matrices themselves) or to new memory."""
+        (ins, ins_at), (si, si_at) = self._addresses(matrices, "matrices")
+        if out is None:
+            out = self.views(self._empty(self.n, self.torch_dtype))
+        (outs, outs_at), (so, so_at) = self._addresses(out, "out")
+        self._call(len(self.shapes), self._rows_at, self._cols_at, self.dtype, ins_at, si_at, outs_at, so_at,
+                   self.steps, self._co_at, self.fine_steps, self._ws, self.workspace_bytes, self._raw_stream())
+        return out
+
+
+class MuonStep(_Matrices):
+    """The step of W ranks on matrices of the given (rows, cols) that takes its
+    direction from the orthogonalised momentum (zero_muon_step).  ``master``,
+    ``momentum`` (fp32) and ``p16`` are flat vectors, matrix after matrix, each
+    starting on a boundary of 8 values (``views`` cuts them up); ``theta0``, a
+    list of matrices, seeds the master and the 16-bit copy.  ``scales``
+    multiplies the learning rate of each matrix (None: 1).  What a ZeRO step
+    trains beside them (embeddings, vectors) has a :class:`ZeroStep` of its own.
+    ``alloc`` as for :class:`ZeroStep`; workspace and stream as for
+    :class:`LmLoss`."""
+
+    def __init__(self, shapes, W=1, grad_dtype="fp16", work_dtype=None, theta0=None, coefficients=MUON_COEFFICIENTS,
+                 fine_steps=None, scales=None, device="cuda", stream=None, alloc=None):
+        import torch
+        self._setup(grad_dtype, device, stream, alloc)
+        self.W = int(W)
+        self.wdt = _DT[work_dtype if work_dtype is not None else grad_dtype]
+        self._setup_matrices(shapes, coefficients, fine_steps)
+        if scales is not None and len(scales) != len(self.shapes):
+            raise ValueError(f"scales must hold one factor for each of the {len(self.shapes)} matrices")
+        self.scales = None if scales is None else [float(x) for x in scales]
+        self._sc, self._sc_at = (None, None) if scales is None else _c_array("d", self.scales)
+        self._workspace(zero_muon_workspace_bytes(self.W, self.shapes), zero=4)
+        new = alloc or (lambda numel, dtype: torch.zeros(numel, dtype=dtype, device=self.device))
+        work = {ZERO_FP16: torch.float16, ZERO_BF16: torch.bfloat16}[self.wdt]
+        with _on(self.stream, self.device):
+            self.master, self.momentum = new(self.n, torch.float32), new(self.n, torch.float32)
+            self.p16 = new(self.n, work)
+            if theta0 is not None:
+                for to, x in zip(self.views(self.master), theta0):
+                    to.copy_(torch.as_tensor(x))
+                self.p16.copy_(self.master)
+        self._new_state = new
+        self._state = [_u64_array([x.data_ptr() + at * x.element_size() for at in self.starts])
+                       for x in (self.master, self.momentum, self.p16)]
+        self._call, self._status = self._bind("zero_muon_step"), self._bind("zero_lm_workspace_status")
+
+    def new_grad_buffers(self):
+        """W lists of matrices for the ranks' gradients, each list in one flat vector."""
+        with _on(self.stream, self.device):
+            return [self.views(self._new_state(self.n, self.torch_dtype)) for _ in range(self.W)]
+
+    def _change_stream(self, raw):
+        super()._change_stream(raw)
+        if self._used_raw == raw:
+            for x in (self.master, self.momentum, self.p16):
+                x.record_stream(self._used)
+
+    def step(self, grads, lr, mu=0.95, weight_decay=0.0, nesterov=True):
+        """One step; ``grads`` is W lists of contiguous matrices."""
+        T = self.torch.Tensor
+        flat = [g for rank in grads for g in rank]
+        if (len(grads) != self.W or any(len(rank) != len(self.shapes) for rank in grads)
+                or [tuple(g.shape) for g in flat] != self.shapes * self.W):
+            raise ValueError(f"grads must be {self.W} lists of matrices of the owner's shapes")
+        if ({g.dtype for g in flat} - {self.torch_dtype}
+                or any(g.device != self.device for g in flat) or not all(map(T.is_contiguous, flat))):
+            raise ValueError(f"gradients must be contiguous, {self.torch_dtype} and on {self.device}")
+        ptrs, at = _u64_array(map(T.data_ptr, flat))
+        self._call(self.W, len(self.shapes), self._rows_at, self._cols_at, self.dtype, self.wdt, at,
+                   *(a for _, a in self._state), lr, mu, 1 if nesterov else 0, weight_decay, self._sc_at, self.steps,
+                   self._co_at, self.fine_steps, self._ws, self.workspace_bytes, self._raw_stream())

@@ -17,15 +17,13 @@
 
 #include "launch.cuh"
 #include "step_math.cuh"
+#include "tensor_map.h"
 #include "umma.cuh"
 #include "zero_context.h"
 #include "zero_internal.h"
 #include "zero_step.h"
 
 namespace zero {
-
-// Whether the calling thread's next call is to lose a block of operands.
-inline thread_local bool g_stall_next = false;
 
 namespace {
 
@@ -228,50 +226,6 @@ __device__ __forceinline__ RowInfo row_info(const GemmArgs& g, const Job& j, int
     }
   }
   return r;
-}
-
-// This thread's row of the accumulator, 32 columns at a time from column
-// `first` in steps of 64 (the quarter's other warp takes those between); the
-// next columns are on their way while f works on these.  `release` runs as
-// soon as the last columns are in registers.
-template <typename F, typename R>
-__device__ __forceinline__ void for_columns(uint32_t tmem, int first, int bn, F f, R release) {
-  if (first >= bn) {
-    release();
-    return;
-  }
-  float va[32], vb[32];
-  int c = first;
-  tmem_ld32(tmem + c, va);
-  tmem_ld_wait(va);
-  for (;;) {
-    if (c + 64 < bn) tmem_ld32(tmem + c + 64, vb);
-    else release();
-    f(c, va);
-    c += 64;
-    if (c >= bn) return;
-    tmem_ld_wait(vb);
-    if (c + 64 < bn) tmem_ld32(tmem + c + 64, va);
-    else release();
-    f(c, vb);
-    c += 64;
-    if (c >= bn) return;
-    tmem_ld_wait(va);
-  }
-}
-
-// The same without loads ahead, for the epilogues whose tiles take long anyway
-// and which read what they add to.
-template <typename F, typename R>
-__device__ __forceinline__ void for_columns_plain(uint32_t tmem, int first, int bn, F f, R release) {
-#pragma unroll 1
-  for (int c = first; c < bn; c += 64) {
-    float v[32];
-    tmem_ld32(tmem + c, v);
-    tmem_ld_wait(v);
-    f(c, v);
-  }
-  release();
 }
 
 // A row's running sums over the columns that a thread has seen: the maximum of
@@ -971,25 +925,10 @@ __global__ void __launch_bounds__(kSmallThreads) lm_finish_dhidden(const float* 
 
 using host::ceil_div;
 using host::cuda_fail;
+using host::encoder;
+using host::EncodeFn;
 using host::fail;
 using host::round_up;
-
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder (looked up once; nullptr if there is none).
-EncodeFn encoder() {
-  static EncodeFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult st;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &st) != cudaSuccess ||
-        st != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeFn>(p);
-  }();
-  return fn;
-}
 
 // A matrix of `rows` x `cols` 16-bit values with a row stride, in boxes of
 // box_rows x 64 under the 128-byte swizzle; what lies outside reads as 0.

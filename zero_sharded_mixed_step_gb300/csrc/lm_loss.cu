@@ -211,10 +211,11 @@ extern "C" int zero_lm_status(void* stream) {
   if (device >= kDevices) return fail(ZERO_E_ARG, "device %d: %d are supported", device, kDevices);
   ZERO_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
   std::lock_guard<std::mutex> lock(mutex);
-  unsigned int n = 0, of_logprobs = 0;
+  unsigned int n = 0, of_logprobs = 0, of_ns = 0;
   ZERO_CUDA(cudaMemcpyFromSymbol(&n, g_lm_timeouts, sizeof n));
   ZERO_CUDA(logprobs_timeouts(&of_logprobs));
-  n += of_logprobs;
+  ZERO_CUDA(ns_timeouts(&of_ns));
+  n += of_logprobs + of_ns;
   const unsigned int fresh = n - seen[device];
   seen[device] = n;
   if (fresh == 0) return ZERO_OK;

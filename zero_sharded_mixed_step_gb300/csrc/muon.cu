@@ -1,0 +1,1251 @@
+// Orthogonalising a matrix by Newton-Schulz products, and the optimizer step
+// that takes its direction from it (Muon).
+//
+//   X_0 = G / |G|_F, taken over its shorter side (m x n, m <= n)
+//   A = X X^T,   P = a I + b A + c A^2,   X <- P X      for each step's (a, b, c)
+//
+// Every step maps the singular values by s -> a s + b s^3 + c s^5; the usual
+// coefficients bring them near 1.  The step is, for each matrix of many,
+//   g = (G_0 + ... + G_{W-1}) / W,   M <- mu M + g,   U = g + mu M or M,
+//   theta <- theta (1 - lr wd) - lr s X(U),   16-bit copy <- theta
+//
+// A step of the recurrence is three launches, each over every matrix of the
+// call; matrices of one shape (or its transpose) lie one after another in the
+// workspace, X as m x n always, so that a 3-D tensor map loads any of them.
+// All products run on one persistent tensor-core kernel, ns_gemm, pairs of
+// CTAs on tiles of 256 rows, in fp16 with fp32 sums:
+//   kGram   A, of which the lower half is computed and mirrored
+//   kPoly   A A likewise, with P formed in its epilogue
+//   kApply  P X; of the last step its epilogue writes the caller's matrix or
+//           updates the master and the 16-bit copy in place.
+// Precision.  A singular value far below 1 grows by `a` (3.4) a step, and with
+// it the noise that rounding X, A and P to 16 bits leaves in its direction:
+// with fp16 operands throughout, a matrix whose largest singular values stand
+// 20 times above the rest comes out 1.4e-2 off (2-norm), with bf16 11e-2.  So
+// in the first `fine` steps every operand is a sum of two fp16 parts (22 bits)
+// and a product three products of parts; the last steps, after which little
+// growth is left, take one part.  Two such steps leave an error of about 1e-3.
+// X and A are stored times 2^12, P times 2^9: entries of fp16's normal range.
+// The first X is the input times a power of two, the rest of 1 / |G| (between
+// 1/2 and 1) being applied in the epilogues: a 16-bit input is then exact in
+// one part.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <type_traits>
+#include <utility>
+#include <vector>
+
+#include "launch.cuh"
+#include "step_math.cuh"
+#include "tensor_map.h"
+#include "umma.cuh"
+#include "zero_context.h"
+#include "zero_internal.h"
+#include "zero_step.h"
+
+namespace zero {
+namespace {
+
+using namespace umma;
+using dev::Fmt;
+using host::ceil_div;
+using host::cuda_fail;
+using host::fail;
+using host::round_up;
+
+// Bounded device-side waits of ns_gemm that gave up, over all calls; never set back (see zero_lm_status).
+__device__ unsigned int g_ns_timeouts;
+
+constexpr int kTileM = 256;          // rows of a tile: 128 in each CTA of the pair
+constexpr int kTileN = 256;          // most columns of a tile
+constexpr int kTileK = 64;
+constexpr int kSlotBytes = 128 * kTileK * 2;     // one part of one operand's half tile in one CTA
+constexpr int kSlots = 12;
+constexpr int kMostStages = 6;
+constexpr int kThreads = 384;        // warp 0 loads, warp 1 issues the products, warps 4-11 are the epilogue
+constexpr int kEpilogueWarps = 8;
+constexpr int kGemmSmem = kSlots * kSlotBytes + 1024;
+constexpr int kMaxGroups = 12;       // shapes of one launch
+constexpr int64_t kPairs = 76;       // pairs of CTAs among GB300's 152 SMs
+
+// How the workspace holds X, A and P: times powers of two.
+constexpr float kScaleX = 4096.f, kScaleA = 4096.f, kScaleP = 512.f;
+
+enum Kind : int { kGram, kPoly, kApply, kLastF16, kLastBF16, kLastF32, kUpdateF16, kUpdateBF16 };
+
+__host__ __device__ constexpr bool symmetric(int kind) { return kind <= kPoly; }
+__host__ __device__ constexpr bool applies(int kind) { return kind >= kApply; }
+
+// One matrix of a call, in device memory.
+struct Entry {
+  int rows, cols;              // the caller's
+  int transposed;              // X is its transpose
+  int wide;                    // the caller's rows allow accesses of 8 values
+  const void* in;              // zero_orthogonalize
+  void* out;
+  int64_t in_stride, out_stride;
+  float* master;               // zero_muon_step
+  float* momentum;
+  void* p16;
+  float* mean;                 // the ranks' mean gradient in workspace, or NULL
+  float step, keep;            // lr s and 1 - lr wd
+  unsigned tile0;              // first of its tiles in the elementwise passes
+  int unused;
+  uint16_t* x;                 // its first X: the high part, the low part x_part further
+  int64_t x_part;
+  int64_t ld;                  // of X
+};
+
+// What the passes leave for the products: 2^12 over the stored X's norm, and
+// whether the input's norm is finite.
+struct Norm {
+  float unit;
+  int finite;
+};
+
+struct Job {
+  int matrices, first;         // of the group: how many, the first one's entry
+  int m_tiles, n_tiles, per_matrix, tiles;
+  int M, N, kb, bn;
+  int b_boxes;                 // boxes of an MN-major B half tile
+  int parts_a, parts_b;
+  uint32_t stage_tx;           // bytes that land per stage, both CTAs together
+  int use_unit;                // powers of the first X's rest of the norm to apply
+  int two_out;                 // write a low part too
+  uint16_t* out;
+  int64_t out_ld, out_matrix, out_part;
+  const uint16_t* add;         // kPoly: A, laid out like the output
+  int add_two;
+  float a, b, c;
+};
+
+struct GemmArgs {
+  CUtensorMap map_a[kMaxGroups], map_b[kMaxGroups];
+  Job job[kMaxGroups];
+  int jobs;
+  int stall;                   // testing the bounded waits: the first pair's first block of K never arrives
+  const Entry* entries;
+  const Norm* norms;
+  unsigned int* failures;      // the workspace's count of waits that gave up
+  unsigned int* lost;          // set where tiles of this call were not computed
+};
+
+struct Tile {
+  int job, matrix, mt, nt;
+};
+
+// Tiles of a row of tiles that hold something on or below the diagonal.
+__host__ __device__ inline int tiles_of_row(int mt, int bn, int n_tiles) {
+  const int reach = (mt + 1) * (kTileM / bn);
+  return reach < n_tiles ? reach : n_tiles;
+}
+
+template <int KIND>
+__device__ __forceinline__ Tile locate(const GemmArgs& g, int t) {
+  Tile x{0, 0, 0, 0};
+  while (x.job < g.jobs && t >= g.job[x.job].tiles) t -= g.job[x.job++].tiles;
+  if (x.job == g.jobs) {
+    x.job = -1;
+    return x;
+  }
+  const Job& j = g.job[x.job];
+  x.matrix = static_cast<int>(static_cast<unsigned>(t) / static_cast<unsigned>(j.per_matrix));
+  t -= x.matrix * j.per_matrix;
+  if (symmetric(KIND)) {
+    for (;;) {
+      const int n = tiles_of_row(x.mt, j.bn, j.n_tiles);
+      if (t < n) break;
+      t -= n;
+      ++x.mt;
+    }
+    x.nt = t;
+  } else {
+    x.nt = static_cast<int>(static_cast<unsigned>(t) / static_cast<unsigned>(j.m_tiles));
+    x.mt = t - x.nt * j.m_tiles;
+  }
+  return x;
+}
+
+// ---- the epilogues -------------------------------------------------------------------
+
+// x as fp16 and what that leaves, as fp16.
+__device__ __forceinline__ void split(float x, __half& hi, __half& lo) {
+  hi = __float2half_rn(x);
+  lo = __float2half_rn(x - __half2float(hi));
+}
+
+__device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo) {
+  hi = Fmt<__half>::pack8(v);
+  float h[8], rest[8];
+  Fmt<__half>::unpack8(hi, h);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) rest[k] = v[k] - h[k];
+  lo = Fmt<__half>::pack8(rest);
+}
+
+// 32 columns from col0 of this thread's row, as they are.
+__device__ __forceinline__ void store_row(const Job& j, uint16_t* out, int row, int col0, const float (&v)[32]) {
+  uint16_t* p = out + row * j.out_ld + col0;
+#pragma unroll
+  for (int k = 0; k < 32; k += 8) {
+    if (col0 + k >= j.N) break;
+    float w[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) w[q] = v[k + q];
+    uint4 hi, lo;
+    split8(w, hi, lo);
+    dev::st_16B(p + k, hi);
+    if (j.two_out) dev::st_16B(p + j.out_part + k, lo);
+  }
+}
+
+// The same of a symmetric matrix: what is on or below the diagonal, and its
+// mirror image, where the lanes' rows are neighbours.
+__device__ __forceinline__ void store_symmetric(const Job& j, uint16_t* out, int row, int col0, const float (&v)[32]) {
+  const int row0 = row - static_cast<int>(threadIdx.x & 31);
+  if (col0 > row0 + 31) return;
+  const bool row_ok = row < j.M;
+  const bool below = col0 + 31 < row0;      // the whole block
+  if (below && row_ok) store_row(j, out, row, col0, v);
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const int col = col0 + k;
+    if (!row_ok || col > row || col >= j.N) continue;
+    __half hi, lo;
+    split(v[k], hi, lo);
+    uint16_t* mirror = out + col * j.out_ld + row;
+    *mirror = __half_as_ushort(hi);
+    if (j.two_out) mirror[j.out_part] = __half_as_ushort(lo);
+    if (!below) {
+      uint16_t* p = out + row * j.out_ld + col;
+      *p = __half_as_ushort(hi);
+      if (j.two_out) p[j.out_part] = __half_as_ushort(lo);
+    }
+  }
+}
+
+// One element of the last product, at (row, col) of X, to the caller.
+template <int KIND>
+__device__ __forceinline__ void write_one(const Entry& e, int64_t at, float x) {
+  if (KIND == kLastF16) Fmt<__half>::store1(e.out, at, x);
+  if (KIND == kLastBF16) Fmt<__nv_bfloat16>::store1(e.out, at, x);
+  if (KIND == kLastF32) static_cast<float*>(e.out)[at] = x;
+  if (KIND >= kUpdateF16) {
+    const float theta = fmaf(-e.step, x, e.keep * e.master[at]);
+    e.master[at] = theta;
+    if (KIND == kUpdateF16) Fmt<__half>::store1(e.p16, at, theta);
+    else Fmt<__nv_bfloat16>::store1(e.p16, at, theta);
+  }
+}
+
+// 8 of them, on boundaries of 8.
+template <int KIND>
+__device__ __forceinline__ void write_8(const Entry& e, int64_t at, const float (&x)[8]) {
+  if (KIND == kLastF16) dev::st_16B(static_cast<uint16_t*>(e.out) + at, Fmt<__half>::pack8(x));
+  if (KIND == kLastBF16) dev::st_16B(static_cast<uint16_t*>(e.out) + at, Fmt<__nv_bfloat16>::pack8(x));
+  if (KIND == kLastF32) dev::st_32B(static_cast<float*>(e.out) + at, x);
+  if (KIND >= kUpdateF16) {
+    float theta[8];
+    dev::ld_32B(e.master + at, theta);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) theta[k] = fmaf(-e.step, x[k], e.keep * theta[k]);
+    dev::st_32B(e.master + at, theta);
+    dev::st_16B(static_cast<uint16_t*>(e.p16) + at,
+                KIND == kUpdateF16 ? Fmt<__half>::pack8(theta) : Fmt<__nv_bfloat16>::pack8(theta));
+  }
+}
+
+template <int KIND, typename R>
+__device__ __forceinline__ void epilogue(const GemmArgs& g, const Job& j, const Tile& x, uint32_t tmem, int row,
+                                         int half, bool lost, R release) {
+  const int n0 = x.nt * j.bn;
+  const bool row_ok = row < j.M;
+  const int which = j.first + x.matrix;
+  const float unit = j.use_unit ? g.norms[which].unit : 1.f;
+  if (KIND == kGram) {
+    uint16_t* out = j.out + x.matrix * j.out_matrix;
+    const float scale = unit * unit * (kScaleA / (kScaleX * kScaleX));
+    for_columns_plain(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] *= scale;
+      store_symmetric(j, out, row, n0 + c, v);
+    }, release);
+  } else if (KIND == kPoly) {
+    uint16_t* out = j.out + x.matrix * j.out_matrix;
+    const uint16_t* add = j.add + x.matrix * j.out_matrix + row * j.out_ld;
+    const float square = j.c * (kScaleP / (kScaleA * kScaleA)), once = j.b * (kScaleP / kScaleA);
+    const int row0 = row - static_cast<int>(threadIdx.x & 31);
+    for_columns_plain(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+      const int col0 = n0 + c;
+      if (col0 > row0 + 31) return;
+#pragma unroll
+      for (int k = 0; k < 32; k += 8) {
+        float hi[8] = {}, lo[8] = {};
+        if (row_ok && col0 + k < j.N) {
+          Fmt<__half>::unpack8(dev::ld_16B(add + col0 + k), hi);
+          if (j.add_two) Fmt<__half>::unpack8(dev::ld_16B(add + j.out_part + col0 + k), lo);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          v[k + q] = fmaf(once, hi[q] + lo[q], square * v[k + q]);
+          if (row == col0 + k + q) v[k + q] += j.a * kScaleP;
+        }
+      }
+      store_symmetric(j, out, row, col0, v);
+    }, release);
+  } else if (KIND == kApply) {
+    uint16_t* out = j.out + x.matrix * j.out_matrix;
+    const float scale = unit / kScaleP;
+    for_columns_plain(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] *= scale;
+      if (row_ok) store_row(j, out, row, n0 + c, v);
+    }, release);
+  } else {
+    const Entry& e = g.entries[which];
+    const bool finite = g.norms[which].finite && !lost;
+    const bool update = KIND >= kUpdateF16;
+    const float scale = finite ? unit / (kScaleP * kScaleX) : NAN;
+    const bool transposed = e.transposed, wide = e.wide;
+    const int64_t stride = update ? e.cols : e.out_stride;
+    for_columns_plain(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+      const int col0 = n0 + c;
+      // a norm that is not finite leaves the state as it was
+      if (!row_ok || (update && !finite)) return;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] *= scale;
+      if (!transposed && wide) {
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) {
+          if (col0 + k >= j.N) break;
+          float w[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) w[q] = v[k + q];
+          write_8<KIND>(e, row * stride + col0 + k, w);
+        }
+        return;
+      }
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        if (col0 + k >= j.N) break;
+        write_one<KIND>(e, transposed ? (col0 + k) * stride + row : row * stride + col0 + k, v[k]);
+      }
+    }, release);
+  }
+}
+
+// The persistent product kernel: pairs of CTAs, each pair one tile at a time,
+// operands through a ring of TMA stages of one or two parts each, two
+// accumulators in TMEM so that one tile's epilogue runs beside the next one's
+// products.  Tiles are dealt out in turn.
+template <int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm(const __grid_constant__ GemmArgs g) {
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kMostStages + 5];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int failed;
+  const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
+  const uint32_t bar0 = smem_addr(bars);
+  auto full = [&](int s) { return bar0 + 8 * s; };
+  auto empty = [&](int s) { return bar0 + 8 * (kMostStages + s); };
+  auto done = [&](int a) { return bar0 + 8 * (2 * kMostStages + a); };        // accumulator a is complete
+  auto taken = [&](int a) { return bar0 + 8 * (2 * kMostStages + 2 + a); };   // accumulator a has been read
+  const uint32_t drained = bar0 + 8 * (2 * kMostStages + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  // every job of a launch has operands of as many parts
+  const int parts_a = g.job[0].parts_a, parts_b = g.job[0].parts_b;
+  const int stages = kSlots / (parts_a + parts_b);
+  const uint32_t stage_bytes = (parts_a + parts_b) * kSlotBytes;
+
+  allow_next();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMostStages; ++s) {
+      bar_init(full(s), 1);
+      bar_init(empty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      bar_init(done(a), 1);
+      bar_init(taken(a), 2 * kEpilogueWarps);
+    }
+    bar_init(drained, 1);
+    failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int k = 0; k < g.jobs; ++k) {
+      tma_prefetch_map(&g.map_a[k]);
+      tma_prefetch_map(&g.map_b[k]);
+    }
+  }
+  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 512);
+  __syncthreads();
+  fence_before();
+  cluster_sync();
+  fence_after();
+  const uint32_t tmem = tmem_slot;
+  await_previous();
+
+  const bool lead = elect_one();
+  bool ok = true;
+  auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity)) != 0; };
+
+  int issued = 0;      // stages loaded by this warp
+  if (warp == 0) {
+    int s = 0;
+    uint32_t phase = 1;
+    for (int t = pair; ok; t += pairs) {
+      const Tile x = locate<KIND>(g, t);
+      if (x.job < 0) break;
+      const Job& j = g.job[x.job];
+      const CUtensorMap *ma = &g.map_a[x.job], *mb = &g.map_b[x.job];
+      const int am = x.mt * kTileM + static_cast<int>(rank) * 128;
+      const int bn = x.nt * j.bn + static_cast<int>(rank) * (j.bn / 2);
+      const int boxes = applies(KIND) ? j.b_boxes : 1;
+      for (int kb = 0; kb < j.kb; ++kb, ++issued) {
+        ok = wait_all(empty(s), phase);
+        if (!ok) break;
+        const uint32_t bar = in_cta(full(s), 0);
+        const uint32_t sa = ring + s * stage_bytes, sb = sa + parts_a * kSlotBytes;
+        const int k = kb * kTileK;
+        if (lead) {
+          if (rank == 0) bar_expect(full(s), j.stage_tx);
+          if (!(g.stall && pair == 0 && issued == 0)) {
+            for (int p = 0; p < parts_a; ++p)
+              tma_load3(sa + p * kSlotBytes, ma, k, am, p * j.matrices + x.matrix, bar);
+          }
+          for (int p = 0; p < parts_b; ++p) {
+            const uint32_t to = sb + p * kSlotBytes;
+            const int z = p * j.matrices + x.matrix;
+            if (applies(KIND)) {
+              // K is the row index of X: boxes of 64 columns
+              tma_load3(to, mb, bn, k, z, bar);
+              if (boxes > 1) tma_load3(to + 8192, mb, bn + 64, k, z, bar);
+            } else {
+              tma_load3(to, mb, k, bn, z, bar);
+            }
+          }
+        }
+        __syncwarp();
+        if (++s == stages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (!ok && lead) failed = 1;
+  } else if (warp == 1) {
+    if (rank == 0) {
+      int s = 0, i = 0;
+      uint32_t phase = 0;
+      for (int t = pair; ok; t += pairs, ++i) {
+        const Tile x = locate<KIND>(g, t);
+        if (x.job < 0) break;
+        const Job& j = g.job[x.job];
+        constexpr bool b_mn = applies(KIND);
+        const uint32_t idesc = instr_desc(false, false, b_mn, kTileM, j.bn);
+        const uint64_t a_step = 32 >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+        const uint64_t a0 = operand_desc(ring, 0), b0 = operand_desc(ring + parts_a * kSlotBytes, b_mn ? 8192 : 0);
+        constexpr uint64_t kPart = kSlotBytes >> 4;
+        const int a = i & 1;
+        ok = wait_all(taken(a), ((i >> 1) & 1) ^ 1);
+        if (!ok) break;
+        fence_after();
+        const uint32_t d = tmem + a * kTileN;
+        for (int kb = 0; kb < j.kb; ++kb) {
+          ok = wait_all(full(s), phase);
+          if (!ok) break;
+          fence_after();
+          const uint64_t da = a0 + s * (stage_bytes >> 4), db = b0 + s * (stage_bytes >> 4);
+          if (lead) {
+            // of two parts each, the product of the low ones is left out: 2^-22 of the whole
+#pragma unroll
+            for (int q = 0; q < kTileK / 16; ++q) {
+              mma(d, da + q * a_step, db + q * b_step, idesc, kb > 0 || q > 0);
+              if (parts_a > 1) mma(d, da + kPart + q * a_step, db + q * b_step, idesc, true);
+              if (parts_b > 1) mma(d, da + q * a_step, db + kPart + q * b_step, idesc, true);
+            }
+            mma_commit(empty(s));
+          }
+          __syncwarp();
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (lead) mma_commit(done(a));
+        __syncwarp();
+      }
+      if (!ok && lead) {
+        // leave no product in flight behind
+        failed = 1;
+        mma_commit(drained);
+        bar_wait(drained, 0);
+      }
+    }
+  } else if (warp >= 4) {
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const bool lost = KIND > kApply && *g.lost != 0;
+    int i = 0;
+    for (int t = pair;; t += pairs, ++i) {
+      const int a = i & 1;
+      const Tile x = locate<KIND>(g, t);
+      if (x.job < 0) break;
+      const Job& j = g.job[x.job];
+      const int row = x.mt * kTileM + static_cast<int>(rank) * 128 + quad * 32 + lane;
+      ok = ok && wait_all(done(a), (i >> 1) & 1);
+      if (!ok) {
+        if (KIND < kLastF16 || KIND > kLastF32) break;
+        // this tile and the pair's others of the caller's matrices: no number
+        const Entry& e = g.entries[j.first + x.matrix];
+        for (int c = half * 32; c < j.bn && row < j.M; c += 64)
+          for (int col = x.nt * j.bn + c; col < min(x.nt * j.bn + c + 32, j.N); ++col)
+            write_one<KIND>(e, e.transposed ? col * e.out_stride + row : row * e.out_stride + col, NAN);
+        continue;
+      }
+      fence_after();
+      epilogue<KIND>(g, j, x, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21), row, half, lost, [&] {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(in_cta(taken(a), 0));
+      });
+    }
+    if (!ok && lane == 0) failed = 1;
+  }
+  __syncthreads();
+  if (failed) {
+    if (threadIdx.x == 0) {
+      atomicAdd(&g_ns_timeouts, 1u);
+      atomicAdd(g.failures, 1u);
+      *g.lost = 1;
+      // the copies in flight land on the leader's barriers: both CTAs stay until they have
+      if (rank == 0)
+        for (int k = max(0, issued - stages); k < issued; ++k) bar_wait(full(k % stages), (k / stages) & 1);
+    }
+    __syncthreads();
+  }
+  fence_before();
+  cluster_sync();
+  fence_after();
+  if (warp == 1) tmem_free(tmem, 512);
+}
+
+// ---- the passes before the products ------------------------------------------------------
+//
+// Both go over tiles of 32 rows x 256 columns of the caller's matrices.
+
+constexpr int kPassThreads = 256, kPassRows = 32, kPassCols = 256;
+constexpr int kPassBlocksPerSm = 4;
+// Up to this many ranks the second pass reads the gradients again (2 W bytes an
+// element) instead of their fp32 mean, which costs 8.
+constexpr int kDirectRanks = 2;
+
+// The list of matrices on its way to the device: launched once for each
+// kTableBytes of it, since a launch's parameters hold no more.
+template <int BYTES>
+struct TablePart {
+  unsigned char data[BYTES];
+};
+constexpr int kSmallTable = 4 * 1024, kLargeTable = 28 * 1024;
+
+template <int BYTES>
+__global__ void __launch_bounds__(kPassThreads) copy_table(const __grid_constant__ TablePart<BYTES> part, int words,
+                                                           uint64_t* to, unsigned int* lost) {
+  allow_next();
+  await_previous();
+  for (int k = threadIdx.x; k < words; k += kPassThreads) to[k] = reinterpret_cast<const uint64_t*>(part.data)[k];
+  if (threadIdx.x == 0) *lost = 0;
+}
+
+struct PassArgs {
+  const Entry* entries;
+  const uint64_t* grads;       // zero_muon_step: W addresses for each entry
+  int count;
+  unsigned tiles;
+  int W;
+  float mu;
+  int nesterov;
+  int two;                     // the second pass writes low parts
+  double* part;                // a sum of squares for each tile
+  Norm* norms;
+};
+
+// The entry that tile t belongs to.
+__device__ __forceinline__ int entry_of(const Entry* entries, int count, unsigned t) {
+  int lo = 0, hi = count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (entries[mid].tile0 <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ double block_sum(double s) {
+  __shared__ double of_warp[kPassThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) of_warp[threadIdx.x >> 5] = s;
+  __syncthreads();
+  double all = 0.0;
+  for (int k = 0; k < kPassThreads / 32; ++k) all += of_warp[k];
+  return all;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
+  if constexpr (std::is_same<T, float>::value) dev::ld_32B(p, f);
+  else Fmt<T>::unpack8(dev::ld_16B(p), f);
+}
+template <typename T>
+__device__ __forceinline__ float load1(const T* p) {
+  if constexpr (std::is_same<T, float>::value) return *p;
+  else return Fmt<T>::load1(p, 0);
+}
+
+// 8 neighbours' (or, without `wide`, up to 8 neighbours' of which `n` exist)
+// mean over the ranks, in rank order.
+template <typename T>
+__device__ __forceinline__ void rank_mean8(const uint64_t* grads, int W, int64_t at, bool wide, int n, float (&g)[8]) {
+  const bool pow2 = (W & (W - 1)) == 0;
+  const float inv_w = 1.f / W;
+  if (wide) {
+    for (int w0 = 0; w0 < W; w0 += 8) {
+      uint4 raw[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w)
+        if (w0 + w < W) raw[w] = dev::ld_16B(reinterpret_cast<const T*>(grads[w0 + w]) + at);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        if (w0 + w >= W) break;
+        float f[8];
+        Fmt<T>::unpack8(raw[w], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] = w0 + w == 0 ? f[k] : __fadd_rn(g[k], f[k]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      g[k] = 0.f;
+      for (int w = 0; w < W && k < n; ++w) {
+        const float f = Fmt<T>::load1(reinterpret_cast<const T*>(grads[w]), at + k);
+        g[k] = w == 0 ? f : __fadd_rn(g[k], f);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) g[k] = dev::rank_mean(g[k], W, inv_w, pow2);
+}
+
+// 8 values of an fp32 vector; those that do not exist read as 0.
+__device__ __forceinline__ void load_some(const float* p, bool wide, int n, float (&f)[8]) {
+  if (wide) {
+    dev::ld_32B(p, f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = k < n ? p[k] : 0.f;
+  }
+}
+__device__ __forceinline__ void store_some(float* p, bool wide, int n, const float (&f)[8]) {
+  if (wide) {
+    dev::st_32B(p, f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) p[k] = f[k];
+  }
+}
+
+// The matrix's values from (row, col) on, 8 of which n exist: the input, or
+// the step's direction U and the new momentum.
+template <typename T, bool MUON>
+__device__ __forceinline__ void direction8(const PassArgs& p, const Entry& e, int which, int row, int col, int n,
+                                           bool first, float (&u)[8], float (&m)[8]) {
+  const bool wide = e.wide;
+  if constexpr (!MUON) {
+    const T* in = static_cast<const T*>(e.in) + row * e.in_stride + col;
+    if (wide) {
+      load8(in, u);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = k < n ? load1(in + k) : 0.f;
+    }
+  } else {
+    const int64_t at = static_cast<int64_t>(row) * e.cols + col;
+    float g[8];
+    if (first || e.mean == nullptr) rank_mean8<T>(p.grads + static_cast<int64_t>(which) * p.W, p.W, at, wide, n, g);
+    else load_some(e.mean + at, wide, n, g);
+    if (first && e.mean != nullptr) store_some(e.mean + at, wide, n, g);
+    load_some(e.momentum + at, wide, n, m);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      m[k] = __fmaf_rn(p.mu, m[k], g[k]);
+      u[k] = p.nesterov ? __fmaf_rn(p.mu, m[k], g[k]) : m[k];
+    }
+  }
+}
+
+// The first pass: each tile's sum of squares, in fp32 within a thread and in
+// fp64 beyond (and the mean gradient, kept where that pays).
+template <typename T, bool MUON>
+__global__ void __launch_bounds__(kPassThreads) sum_squares(const __grid_constant__ PassArgs p) {
+  allow_next();
+  await_previous();
+  for (unsigned t = blockIdx.x; t < p.tiles; t += gridDim.x) {
+    const int which = entry_of(p.entries, p.count, t);
+    const Entry& e = p.entries[which];
+    const int across = (e.cols + kPassCols - 1) / kPassCols;
+    const int tile = static_cast<int>(t - e.tile0), ty = tile / across;
+    const int col = (tile - ty * across) * kPassCols + static_cast<int>(threadIdx.x & 31) * 8;
+    const int n = e.cols - col;
+    float squares = 0.f;
+    if (n > 0) {
+#pragma unroll
+      for (int r = 0; r < kPassRows / 8; ++r) {
+        const int row = ty * kPassRows + r * 8 + static_cast<int>(threadIdx.x >> 5);
+        if (row >= e.rows) break;
+        float u[8], m[8];
+        direction8<T, MUON>(p, e, which, row, col, n, true, u, m);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < n) squares = fmaf(u[k], u[k], squares);
+      }
+    }
+    const double all = block_sum(squares);
+    if (threadIdx.x == 0) p.part[t] = all;
+  }
+}
+
+// The second pass: X = the matrix times a power of two that brings its norm
+// to [2^12, 2^13), in one or two fp16 parts, transposed where it has more rows
+// than columns; the new momentum, unless the norm is not finite.
+template <typename T, bool MUON>
+__global__ void __launch_bounds__(kPassThreads) make_first(const __grid_constant__ PassArgs p) {
+  __shared__ uint32_t turned[kPassCols * (kPassRows + 1)];
+  allow_next();
+  await_previous();
+  const unsigned t0 = static_cast<unsigned>(static_cast<uint64_t>(p.tiles) * blockIdx.x / gridDim.x);
+  const unsigned t1 = static_cast<unsigned>(static_cast<uint64_t>(p.tiles) * (blockIdx.x + 1) / gridDim.x);
+  int which = -1;
+  float scale = 0.f;
+  bool finite = false;
+  for (unsigned t = t0; t < t1; ++t) {
+    const int now = entry_of(p.entries, p.count, t);
+    const Entry& e = p.entries[now];
+    const int across = (e.cols + kPassCols - 1) / kPassCols;
+    if (now != which) {
+      which = now;
+      const unsigned n = static_cast<unsigned>((e.rows + kPassRows - 1) / kPassRows) * across;
+      double s = 0.0;
+      for (unsigned k = threadIdx.x; k < n; k += kPassThreads) s += p.part[e.tile0 + k];
+      const float norm = static_cast<float>(sqrt(block_sum(s)));
+      finite = isfinite(norm);
+      const int up = norm > 0.f && finite ? min(12 - ilogbf(norm), 126) : 0;
+      scale = finite ? exp2f(static_cast<float>(up)) : 0.f;
+      if (t == e.tile0 && threadIdx.x == 0) p.norms[which] = {norm > 0.f && finite ? kScaleX / (norm * scale) : 0.f, finite};
+    }
+    const int tile = static_cast<int>(t - e.tile0), ty = tile / across, col0 = (tile - ty * across) * kPassCols;
+    const int col = col0 + static_cast<int>(threadIdx.x & 31) * 8, n = e.cols - col;
+    if (e.transposed) __syncthreads();   // the tile before has been written
+#pragma unroll
+    for (int r = 0; r < kPassRows / 8; ++r) {
+      const int in_tile = r * 8 + static_cast<int>(threadIdx.x >> 5), row = ty * kPassRows + in_tile;
+      if (row >= e.rows || n <= 0) break;
+      float u[8], m[8];
+      direction8<T, MUON>(p, e, which, row, col, n, false, u, m);
+      if (MUON && finite) store_some(e.momentum + static_cast<int64_t>(row) * e.cols + col, e.wide, n, m);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = finite ? u[k] * scale : 0.f;
+      uint4 hi, lo;
+      split8(u, hi, lo);
+      if (!e.transposed) {
+        // columns past the last, up to the boundary of 8, are not read again
+        uint16_t* to = e.x + row * e.ld + col;
+        dev::st_16B(to, hi);
+        if (p.two) dev::st_16B(to + e.x_part, lo);
+      } else {
+        const uint16_t *h = reinterpret_cast<const uint16_t*>(&hi), *l = reinterpret_cast<const uint16_t*>(&lo);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          turned[((threadIdx.x & 31) * 8 + k) * (kPassRows + 1) + in_tile] = h[k] | static_cast<uint32_t>(l[k]) << 16;
+      }
+    }
+    if (e.transposed) {
+      __syncthreads();
+      const int row = ty * kPassRows + static_cast<int>(threadIdx.x & 31);
+      for (int c = static_cast<int>(threadIdx.x >> 5); c < min(kPassCols, e.cols - col0); c += kPassThreads / 32) {
+        if (row >= e.rows) break;
+        const uint32_t w = turned[c * (kPassRows + 1) + (threadIdx.x & 31)];
+        uint16_t* to = e.x + (col0 + c) * e.ld + row;
+        *to = static_cast<uint16_t>(w);
+        if (p.two) to[e.x_part] = static_cast<uint16_t>(w >> 16);
+      }
+    }
+  }
+}
+
+// ---- host -------------------------------------------------------------------------------
+
+constexpr int64_t kMaxSide = 32768, kMaxMatrices = 65536;
+constexpr int kMaxSteps = 32;
+constexpr int64_t kStatusBytes = 256;
+
+// The matrices of one shape, or of its transpose.
+struct Group {
+  int64_t m, n;
+  std::vector<int64_t> members;
+  int64_t first;               // of its entries
+  int64_t ldx, lda;
+  int64_t x[2], a, p;          // byte offsets of both X, of A and of P: high parts, then low parts
+  int64_t x_part() const { return static_cast<int64_t>(members.size()) * m * ldx; }
+  int64_t a_part() const { return static_cast<int64_t>(members.size()) * m * lda; }
+};
+
+// How a call's matrices are laid out in the workspace.
+struct Plan {
+  std::vector<Group> groups;
+  int64_t count = 0, tiles = 0;
+  int64_t table, table_words, norms, part, mean, total;
+};
+
+int64_t pass_tiles(int64_t rows, int64_t cols) { return ceil_div(rows, kPassRows) * ceil_div(cols, kPassCols); }
+
+int make_plan(Plan& plan, int64_t n_matrices, const int64_t* rows, const int64_t* cols, int W, bool muon) {
+  if (n_matrices < 0 || n_matrices > kMaxMatrices)
+    return fail(ZERO_E_ARG, "n_matrices=%lld outside [0, %lld]", (long long)n_matrices, (long long)kMaxMatrices);
+  if (n_matrices > 0 && (!rows || !cols)) return fail(ZERO_E_ARG, "rows and cols are required");
+  int64_t numel = 0;
+  for (int64_t i = 0; i < n_matrices; ++i) {
+    if (rows[i] < 1 || rows[i] > kMaxSide || cols[i] < 1 || cols[i] > kMaxSide)
+      return fail(ZERO_E_ARG, "matrix %lld: %lld x %lld, sides outside [1, %lld]", (long long)i, (long long)rows[i],
+                  (long long)cols[i], (long long)kMaxSide);
+    const int64_t m = std::min(rows[i], cols[i]), n = std::max(rows[i], cols[i]);
+    auto it = std::find_if(plan.groups.begin(), plan.groups.end(), [&](const Group& g) { return g.m == m && g.n == n; });
+    if (it == plan.groups.end()) {
+      plan.groups.emplace_back();
+      it = plan.groups.end() - 1;
+      it->m = m;
+      it->n = n;
+    }
+    it->members.push_back(i);
+    plan.tiles += pass_tiles(rows[i], cols[i]);
+    numel += round_up(rows[i] * cols[i], 8);
+  }
+  if (plan.tiles > INT32_MAX) return fail(ZERO_E_ARG, "too many elements");
+  // the longest products first
+  std::sort(plan.groups.begin(), plan.groups.end(),
+            [](const Group& a, const Group& b) { return a.n != b.n ? a.n > b.n : a.m > b.m; });
+  plan.count = n_matrices;
+  plan.table = kStatusBytes;
+  plan.table_words = n_matrices * (static_cast<int64_t>(sizeof(Entry)) / 8 + (muon ? W : 0));
+  plan.norms = plan.table + round_up(plan.table_words * 8, 256);
+  plan.part = plan.norms + round_up(n_matrices * static_cast<int64_t>(sizeof(Norm)), 256);
+  plan.mean = plan.part + round_up(plan.tiles * 8, 256);
+  int64_t at = plan.mean + (muon && W > kDirectRanks ? round_up(numel * 4, 256) : 0);
+  int64_t first = 0;
+  for (Group& g : plan.groups) {
+    g.first = first;
+    first += static_cast<int64_t>(g.members.size());
+    g.ldx = round_up(g.n, 8);
+    g.lda = round_up(g.m, 8);
+    for (int64_t* to : {&g.x[0], &g.x[1]}) {
+      *to = at;
+      at += round_up(g.x_part() * 4, 256);
+    }
+    for (int64_t* to : {&g.a, &g.p}) {
+      *to = at;
+      at += round_up(g.a_part() * 4, 256);
+    }
+  }
+  plan.total = std::max<int64_t>(at, 512);
+  return ZERO_OK;
+}
+
+// A stack of `depth` row-major fp16 matrices, in boxes of box_rows x 64 under the
+// 128-byte swizzle; what lies outside a matrix reads as 0.
+int make_map3(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int64_t depth, int box_rows) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(depth)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * rows * 2};
+  const cuuint32_t box[3] = {kTileK, static_cast<cuuint32_t>(box_rows), 1}, ones[3] = {1, 1, 1};
+  const host::EncodeFn fn = host::encoder();
+  if (!fn) return fail(ZERO_E_CUDA, "the driver offers no tensor-map encoder");
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, ones,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ZERO_OK : fail(ZERO_E_CUDA, "encoding a tensor map failed (%d)", static_cast<int>(r));
+}
+
+// Cuts one group's product into tiles.
+void cut(Job& j, int kind, int64_t M, int64_t N, int64_t K, int matrices, int parts_a, int parts_b, int bn) {
+  j.matrices = matrices;
+  j.M = static_cast<int>(M);
+  j.N = static_cast<int>(N);
+  j.kb = static_cast<int>(ceil_div(K, kTileK));
+  j.bn = bn;
+  j.m_tiles = static_cast<int>(ceil_div(M, kTileM));
+  j.n_tiles = static_cast<int>(ceil_div(N, bn));
+  if (symmetric(kind)) {
+    j.per_matrix = 0;
+    for (int mt = 0; mt < j.m_tiles; ++mt) j.per_matrix += tiles_of_row(mt, bn, j.n_tiles);
+  } else {
+    j.per_matrix = j.m_tiles * j.n_tiles;
+  }
+  j.tiles = j.per_matrix * matrices;
+  j.parts_a = parts_a;
+  j.parts_b = parts_b;
+  j.b_boxes = static_cast<int>(ceil_div(bn / 2, 64));
+  const int b_bytes = applies(kind) ? j.b_boxes * 8192 : bn / 2 * kTileK * 2;
+  j.stage_tx = static_cast<uint32_t>(2 * (parts_a * kSlotBytes + parts_b * b_bytes));
+}
+
+// The width of the tiles of one group's product, a divisor of 256.  A block of K
+// takes 2 bn cycles for each product of parts, or the time its operands take to
+// load; a tile has some 2000 cycles besides.
+int width_of(int kind, int64_t M, int64_t N, int64_t K, int matrices, int parts_a, int parts_b) {
+  const int products = parts_a + parts_b - 1;
+  int best = kTileN;
+  int64_t least = INT64_MAX;
+  for (int bn = kTileN; bn >= 32; bn /= 2) {
+    Job j;
+    cut(j, kind, M, N, K, matrices, parts_a, parts_b, bn);
+    const int64_t block = std::max<int64_t>(2 * bn * products, j.stage_tx / 128);
+    const int64_t cost = ceil_div(j.tiles, kPairs) * (j.kb * block + 2000);
+    if (cost < least) {
+      least = cost;
+      best = bn;
+    }
+  }
+  return best;
+}
+
+template <int KIND>
+int launch_products(GemmArgs& g, cudaStream_t s, bool& stall) {
+  g.stall = std::exchange(stall, false);
+  ZERO_CUDA(cudaFuncSetAttribute(ns_gemm<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem));
+  int64_t tiles = 0;
+  for (int k = 0; k < g.jobs; ++k) tiles += g.job[k].tiles;
+  const int pairs = static_cast<int>(std::min({std::max<int64_t>(1, sm_count() / 2), kPairs, tiles}));
+  ZERO_CUDA(launch_chained(ns_gemm<KIND>, dim3(2 * pairs), kThreads, kGemmSmem, s, g));
+  return ZERO_OK;
+}
+
+int launch_kind(int kind, GemmArgs& g, cudaStream_t s, bool& stall) {
+  switch (kind) {
+    case kGram: return launch_products<kGram>(g, s, stall);
+    case kPoly: return launch_products<kPoly>(g, s, stall);
+    case kApply: return launch_products<kApply>(g, s, stall);
+    case kLastF16: return launch_products<kLastF16>(g, s, stall);
+    case kLastBF16: return launch_products<kLastBF16>(g, s, stall);
+    case kLastF32: return launch_products<kLastF32>(g, s, stall);
+    case kUpdateF16: return launch_products<kUpdateF16>(g, s, stall);
+    default: return launch_products<kUpdateBF16>(g, s, stall);
+  }
+}
+
+struct Recurrence {
+  int steps, fine;
+  const double* coefficients;
+  int first_parts;             // of the first X
+  int last;                    // Kind of the last product
+};
+
+// The steps, over the groups from `from` on, as many as a launch takes.
+int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, char* ws, cudaStream_t s, bool& stall) {
+  for (int step = 0; step < r.steps; ++step) {
+    const int parts = step < r.fine ? 2 : 1, x_parts = step == 0 ? std::min(parts, r.first_parts) : parts;
+    const int next_parts = step + 1 < r.fine ? 2 : 1;
+    const bool last = step + 1 == r.steps;
+    for (int kind : {static_cast<int>(kGram), static_cast<int>(kPoly), last ? r.last : static_cast<int>(kApply)}) {
+      GemmArgs g;
+      std::memset(&g, 0, sizeof g);
+      g.entries = reinterpret_cast<const Entry*>(ws + plan.table);
+      g.norms = reinterpret_cast<const Norm*>(ws + plan.norms);
+      g.failures = reinterpret_cast<unsigned int*>(ws);
+      g.lost = reinterpret_cast<unsigned int*>(ws) + 1;
+      for (size_t i = from; i < to; ++i) {
+        const Group& group = plan.groups[i];
+        const int c = static_cast<int>(group.members.size()), k = g.jobs++;
+        const int64_t m = group.m, n = group.n;
+        Job& j = g.job[k];
+        const int pa = applies(kind) || kind == kPoly ? parts : x_parts, pb = kind == kPoly ? parts : x_parts;
+        const int64_t N = applies(kind) ? n : m, K = kind == kGram ? n : m;
+        cut(j, kind, m, N, K, c, pa, pb, width_of(kind, m, N, K, c, pa, pb));
+        j.first = static_cast<int>(group.first);
+        j.use_unit = step == 0 && kind != kPoly;
+        j.a = static_cast<float>(r.coefficients[3 * step]);
+        j.b = static_cast<float>(r.coefficients[3 * step + 1]);
+        j.c = static_cast<float>(r.coefficients[3 * step + 2]);
+        char *x = ws + group.x[step & 1], *a = ws + group.a, *p = ws + group.p;
+        int rc;
+        if (kind == kGram) {
+          j.out = reinterpret_cast<uint16_t*>(a);
+          if ((rc = make_map3(&g.map_a[k], x, m, n, group.ldx, 2 * c, 128))) return rc;
+          if ((rc = make_map3(&g.map_b[k], x, m, n, group.ldx, 2 * c, j.bn / 2))) return rc;
+        } else if (kind == kPoly) {
+          j.out = reinterpret_cast<uint16_t*>(p);
+          j.add = reinterpret_cast<const uint16_t*>(a);
+          j.add_two = parts > 1;
+          if ((rc = make_map3(&g.map_a[k], a, m, m, group.lda, 2 * c, 128))) return rc;
+          if ((rc = make_map3(&g.map_b[k], a, m, m, group.lda, 2 * c, j.bn / 2))) return rc;
+        } else {
+          j.out = reinterpret_cast<uint16_t*>(ws + group.x[(step & 1) ^ 1]);
+          if ((rc = make_map3(&g.map_a[k], p, m, m, group.lda, 2 * c, 128))) return rc;
+          if ((rc = make_map3(&g.map_b[k], x, m, n, group.ldx, 2 * c, 64))) return rc;
+        }
+        j.two_out = (applies(kind) ? next_parts : parts) > 1;
+        j.out_ld = applies(kind) ? group.ldx : group.lda;
+        j.out_matrix = m * j.out_ld;
+        j.out_part = c * j.out_matrix;
+      }
+      const int rc = launch_kind(kind, g, s, stall);
+      if (rc) return rc;
+    }
+  }
+  return ZERO_OK;
+}
+
+template <int BYTES>
+int send_table_of(const std::vector<uint64_t>& words, char* to, unsigned int* lost, cudaStream_t s) {
+  static thread_local TablePart<BYTES> part;
+  constexpr size_t kWords = BYTES / 8;
+  for (size_t at = 0; at < words.size(); at += kWords) {
+    const size_t count = std::min(kWords, words.size() - at);
+    std::memcpy(part.data, words.data() + at, count * 8);
+    ZERO_CUDA(launch_chained(copy_table<BYTES>, dim3(1), kPassThreads, 0, s, part, static_cast<int>(count),
+                             reinterpret_cast<uint64_t*>(to) + at, lost));
+  }
+  return ZERO_OK;
+}
+
+int send_table(const std::vector<uint64_t>& words, char* to, unsigned int* lost, cudaStream_t s) {
+  return words.size() * 8 <= kSmallTable ? send_table_of<kSmallTable>(words, to, lost, s)
+                                         : send_table_of<kLargeTable>(words, to, lost, s);
+}
+
+template <typename T, bool MUON>
+int launch_passes(const PassArgs& p, cudaStream_t s) {
+  const int64_t most = static_cast<int64_t>(sm_count()) * kPassBlocksPerSm;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(p.tiles, most)));
+  ZERO_CUDA(launch_chained(sum_squares<T, MUON>, grid, kPassThreads, 0, s, p));
+  ZERO_CUDA(launch_chained(make_first<T, MUON>, grid, kPassThreads, 0, s, p));
+  return ZERO_OK;
+}
+
+// Every group, kMaxGroups of them at a time.
+int run_all(const Plan& plan, const Recurrence& r, char* ws, cudaStream_t s, bool& stall) {
+  for (size_t from = 0; from < plan.groups.size(); from += kMaxGroups) {
+    const int rc = run_groups(plan, from, std::min(plan.groups.size(), from + kMaxGroups), r, ws, s, stall);
+    if (rc) return rc;
+  }
+  return ZERO_OK;
+}
+
+int check_recurrence(int steps, const double* coefficients, int fine) {
+  if (steps < 1 || steps > kMaxSteps) return fail(ZERO_E_ARG, "steps=%d outside [1, %d]", steps, kMaxSteps);
+  if (!coefficients) return fail(ZERO_E_ARG, "coefficients is NULL");
+  for (int k = 0; k < 3 * steps; ++k)
+    if (!(std::fabs(coefficients[k]) <= 64.0))
+      return fail(ZERO_E_ARG, "coefficient %d is %g: at most 64 in size is supported", k, coefficients[k]);
+  if (fine < -1 || fine > steps) return fail(ZERO_E_ARG, "fine_steps=%d outside [-1, %d]", fine, steps);
+  return ZERO_OK;
+}
+
+int check_workspace(const void* workspace, int64_t bytes, int64_t needed) {
+  if (workspace == nullptr) return fail(ZERO_E_ARG, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(ZERO_E_ALIGN, "workspace must be 256-byte aligned");
+  if (bytes < needed)
+    return fail(ZERO_E_ARG, "workspace of %lld bytes: %lld are needed", (long long)bytes, (long long)needed);
+  return ZERO_OK;
+}
+
+// The steps that carry two parts where the caller leaves it open: all but the
+// last two, for fp32 results all.
+int fine_steps(int fine, int steps, bool all) { return fine >= 0 ? fine : all ? steps : std::max(0, steps - 2); }
+
+// Fills an entry's place in the workspace.
+void place(Entry& e, const Group& g, int64_t member, char* ws) {
+  e.transposed = e.rows > e.cols;
+  e.ld = g.ldx;
+  e.x = reinterpret_cast<uint16_t*>(ws + g.x[0]) + member * g.m * g.ldx;
+  e.x_part = g.x_part();
+}
+
+}  // namespace
+
+cudaError_t ns_timeouts(unsigned int* out) { return cudaMemcpyFromSymbol(out, g_ns_timeouts, sizeof *out); }
+
+}  // namespace zero
+
+using namespace zero;
+
+extern "C" int64_t zero_orthogonalize_workspace_bytes(int64_t n_matrices, const int64_t* rows, const int64_t* cols) {
+  Plan plan;
+  const int rc = make_plan(plan, n_matrices, rows, cols, 0, false);
+  return rc ? rc : plan.total;
+}
+
+extern "C" int zero_orthogonalize(int64_t n_matrices, const int64_t* rows, const int64_t* cols, int dtype,
+                                  const void* const* in, const int64_t* in_strides, void* const* out,
+                                  const int64_t* out_strides, int steps, const double* coefficients, int fine,
+                                  void* workspace, int64_t workspace_bytes, void* stream) {
+  bool stall = std::exchange(g_stall_next, false);
+  Plan plan;
+  int rc = make_plan(plan, n_matrices, rows, cols, 0, false);
+  if (rc || (rc = check_recurrence(steps, coefficients, fine))) return rc;
+  if (dtype != ZERO_FP16 && dtype != ZERO_BF16 && dtype != ZERO_FP32)
+    return fail(ZERO_E_ARG, "the format must be ZERO_FP16, ZERO_BF16 or ZERO_FP32");
+  if (n_matrices > 0 && (!in || !out)) return fail(ZERO_E_ARG, "in and out are required");
+  const int item = dtype == ZERO_FP32 ? 4 : 2;
+  for (int64_t i = 0; i < n_matrices; ++i) {
+    const int64_t si = in_strides ? in_strides[i] : cols[i], so = out_strides ? out_strides[i] : cols[i];
+    if (!in[i] || !out[i]) return fail(ZERO_E_ARG, "matrix %lld: a NULL pointer", (long long)i);
+    if (reinterpret_cast<uintptr_t>(in[i]) % item || reinterpret_cast<uintptr_t>(out[i]) % item)
+      return fail(ZERO_E_ALIGN, "matrix %lld: not aligned to its elements", (long long)i);
+    if (si < cols[i] || so < cols[i] || si > (int64_t(1) << 32) || so > (int64_t(1) << 32))
+      return fail(ZERO_E_ARG, "matrix %lld: a row stride is below its columns or too large", (long long)i);
+  }
+  if (n_matrices == 0) return ZERO_OK;
+  if ((rc = check_workspace(workspace, workspace_bytes, plan.total))) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  constexpr size_t kEntryWords = sizeof(Entry) / 8;
+  std::vector<uint64_t> words(plan.table_words);
+  unsigned tile = 0;
+  for (const Group& g : plan.groups)
+    for (size_t k = 0; k < g.members.size(); ++k) {
+      const int64_t i = g.members[k];
+      Entry e;
+      std::memset(&e, 0, sizeof e);
+      e.rows = static_cast<int>(rows[i]);
+      e.cols = static_cast<int>(cols[i]);
+      e.in = in[i];
+      e.out = out[i];
+      e.in_stride = in_strides ? in_strides[i] : cols[i];
+      e.out_stride = out_strides ? out_strides[i] : cols[i];
+      const uintptr_t both = reinterpret_cast<uintptr_t>(e.in) | reinterpret_cast<uintptr_t>(e.out);
+      e.wide = both % (8 * item) == 0 && (e.cols | e.in_stride | e.out_stride) % 8 == 0;
+      e.tile0 = tile;
+      tile += static_cast<unsigned>(pass_tiles(rows[i], cols[i]));
+      place(e, g, static_cast<int64_t>(k), ws);
+      std::memcpy(&words[(g.first + k) * kEntryWords], &e, sizeof e);
+    }
+  unsigned int* lost = reinterpret_cast<unsigned int*>(ws) + 1;
+  if ((rc = send_table(words, ws + plan.table, lost, s))) return rc;
+  Recurrence r = {steps, fine_steps(fine, steps, dtype == ZERO_FP32), coefficients, dtype == ZERO_FP32 ? 2 : 1,
+                  dtype == ZERO_FP16 ? kLastF16 : dtype == ZERO_BF16 ? kLastBF16 : kLastF32};
+  PassArgs p;
+  std::memset(&p, 0, sizeof p);
+  p.entries = reinterpret_cast<const Entry*>(ws + plan.table);
+  p.count = static_cast<int>(n_matrices);
+  p.tiles = tile;
+  p.two = r.first_parts > 1 && r.fine > 0;
+  p.part = reinterpret_cast<double*>(ws + plan.part);
+  p.norms = reinterpret_cast<Norm*>(ws + plan.norms);
+  rc = dtype == ZERO_FP16   ? launch_passes<__half, false>(p, s)
+       : dtype == ZERO_BF16 ? launch_passes<__nv_bfloat16, false>(p, s)
+                            : launch_passes<float, false>(p, s);
+  return rc ? rc : run_all(plan, r, ws, s, stall);
+}
+
+extern "C" int64_t zero_muon_workspace_bytes(int W, int64_t n_matrices, const int64_t* rows, const int64_t* cols) {
+  if (W < 1 || W > ZERO_MAX_RANKS) return fail(ZERO_E_ARG, "W=%d outside [1, %d]", W, ZERO_MAX_RANKS);
+  Plan plan;
+  const int rc = make_plan(plan, n_matrices, rows, cols, W, true);
+  return rc ? rc : plan.total;
+}
+
+extern "C" int zero_muon_step(int W, int64_t n_matrices, const int64_t* rows, const int64_t* cols, int grad_dtype,
+                              int work_dtype, const void* const* grads, float* const* master, float* const* momentum,
+                              void* const* p16, double lr, double mu, int nesterov, double weight_decay,
+                              const double* scales, int steps, const double* coefficients, int fine, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
+  bool stall = std::exchange(g_stall_next, false);
+  if (W < 1 || W > ZERO_MAX_RANKS) return fail(ZERO_E_ARG, "W=%d outside [1, %d]", W, ZERO_MAX_RANKS);
+  Plan plan;
+  int rc = make_plan(plan, n_matrices, rows, cols, W, true);
+  if (rc || (rc = check_recurrence(steps, coefficients, fine))) return rc;
+  if (!host::valid_dtype(grad_dtype) || !host::valid_dtype(work_dtype))
+    return fail(ZERO_E_ARG, "the 16-bit formats must be ZERO_FP16 or ZERO_BF16");
+  if (!std::isfinite(static_cast<float>(lr))) return fail(ZERO_E_ARG, "lr %g is not a finite fp32 value", lr);
+  if (!(mu >= 0.0 && mu < 1.0)) return fail(ZERO_E_ARG, "mu %g outside [0, 1)", mu);
+  if (!std::isfinite(static_cast<float>(1.0 - lr * weight_decay)))
+    return fail(ZERO_E_ARG, "weight_decay %g: 1 - lr * weight_decay is not a finite fp32 value", weight_decay);
+  if (n_matrices > 0 && (!grads || !master || !momentum || !p16))
+    return fail(ZERO_E_ARG, "grads, master, momentum and p16 are required");
+  for (int64_t i = 0; i < n_matrices; ++i) {
+    if (!master[i] || !momentum[i] || !p16[i]) return fail(ZERO_E_ARG, "matrix %lld: a NULL pointer", (long long)i);
+    if (reinterpret_cast<uintptr_t>(master[i]) % 4 || reinterpret_cast<uintptr_t>(momentum[i]) % 4 ||
+        reinterpret_cast<uintptr_t>(p16[i]) % 2)
+      return fail(ZERO_E_ALIGN, "matrix %lld: not aligned to its elements", (long long)i);
+    if (scales && !std::isfinite(static_cast<float>(lr * scales[i])))
+      return fail(ZERO_E_ARG, "scales[%lld] %g: lr * scale is not a finite fp32 value", (long long)i, scales[i]);
+    for (int w = 0; w < W; ++w) {
+      const void* g = grads[w * n_matrices + i];
+      if (!g) return fail(ZERO_E_ARG, "matrix %lld: rank %d's gradient is NULL", (long long)i, w);
+      if (reinterpret_cast<uintptr_t>(g) % 2)
+        return fail(ZERO_E_ALIGN, "matrix %lld: rank %d's gradient is not aligned to its elements", (long long)i, w);
+    }
+  }
+  if (n_matrices == 0) return ZERO_OK;
+  if ((rc = check_workspace(workspace, workspace_bytes, plan.total))) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  constexpr size_t kEntryWords = sizeof(Entry) / 8;
+  std::vector<uint64_t> words(plan.table_words);
+  uint64_t* ranks = words.data() + n_matrices * kEntryWords;
+  unsigned tile = 0;
+  int64_t mean_at = plan.mean;
+  for (const Group& g : plan.groups)
+    for (size_t k = 0; k < g.members.size(); ++k) {
+      const int64_t i = g.members[k], to = g.first + static_cast<int64_t>(k);
+      Entry e;
+      std::memset(&e, 0, sizeof e);
+      e.rows = static_cast<int>(rows[i]);
+      e.cols = static_cast<int>(cols[i]);
+      e.master = master[i];
+      e.momentum = momentum[i];
+      e.p16 = p16[i];
+      if (W > kDirectRanks) {
+        e.mean = reinterpret_cast<float*>(ws + mean_at);
+        mean_at += round_up(rows[i] * cols[i], 8) * 4;
+      }
+      e.step = static_cast<float>(lr * (scales ? scales[i] : 1.0));
+      e.keep = static_cast<float>(1.0 - lr * weight_decay);
+      uintptr_t fp32 = reinterpret_cast<uintptr_t>(e.master) | reinterpret_cast<uintptr_t>(e.momentum);
+      uintptr_t b16 = reinterpret_cast<uintptr_t>(e.p16);
+      for (int w = 0; w < W; ++w) {
+        ranks[to * W + w] = reinterpret_cast<uint64_t>(grads[w * n_matrices + i]);
+        b16 |= reinterpret_cast<uintptr_t>(grads[w * n_matrices + i]);
+      }
+      e.wide = fp32 % 32 == 0 && b16 % 16 == 0 && e.cols % 8 == 0;
+      e.tile0 = tile;
+      tile += static_cast<unsigned>(pass_tiles(rows[i], cols[i]));
+      place(e, g, static_cast<int64_t>(k), ws);
+      std::memcpy(&words[to * kEntryWords], &e, sizeof e);
+    }
+  unsigned int* lost = reinterpret_cast<unsigned int*>(ws) + 1;
+  if ((rc = send_table(words, ws + plan.table, lost, s))) return rc;
+  Recurrence r = {steps, fine_steps(fine, steps, false), coefficients, 2, work_dtype == ZERO_FP16 ? kUpdateF16 : kUpdateBF16};
+  PassArgs p;
+  std::memset(&p, 0, sizeof p);
+  p.entries = reinterpret_cast<const Entry*>(ws + plan.table);
+  p.grads = reinterpret_cast<const uint64_t*>(ws + plan.table) + n_matrices * kEntryWords;
+  p.count = static_cast<int>(n_matrices);
+  p.tiles = tile;
+  p.W = W;
+  p.mu = static_cast<float>(mu);
+  p.nesterov = nesterov != 0;
+  p.two = r.fine > 0;
+  p.part = reinterpret_cast<double*>(ws + plan.part);
+  p.norms = reinterpret_cast<Norm*>(ws + plan.norms);
+  rc = grad_dtype == ZERO_FP16 ? launch_passes<__half, true>(p, s) : launch_passes<__nv_bfloat16, true>(p, s);
+  return rc ? rc : run_all(plan, r, ws, s, stall);
+}

@@ -106,6 +106,16 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// The same of a 3-D tensor map.
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                          uint32_t leader_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(leader_bar)
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -147,6 +157,52 @@ __device__ __forceinline__ void tmem_ld_wait(float (&v)[32]) {
                  "+f"(v[30]), "+f"(v[31])
                :
                : "memory");
+}
+
+// ---- an accumulator's columns, for an epilogue of two warps a quarter of its lanes ------
+
+// This thread's row of an accumulator, 32 columns at a time from column
+// `first` in steps of 64 (the quarter's other warp takes those between); the
+// next columns are on their way while f works on these.  `release` runs as
+// soon as the last columns are in registers.
+template <typename F, typename R>
+__device__ __forceinline__ void for_columns(uint32_t tmem, int first, int bn, F f, R release) {
+  if (first >= bn) {
+    release();
+    return;
+  }
+  float va[32], vb[32];
+  int c = first;
+  tmem_ld32(tmem + c, va);
+  tmem_ld_wait(va);
+  for (;;) {
+    if (c + 64 < bn) tmem_ld32(tmem + c + 64, vb);
+    else release();
+    f(c, va);
+    c += 64;
+    if (c >= bn) return;
+    tmem_ld_wait(vb);
+    if (c + 64 < bn) tmem_ld32(tmem + c + 64, va);
+    else release();
+    f(c, vb);
+    c += 64;
+    if (c >= bn) return;
+    tmem_ld_wait(va);
+  }
+}
+
+// The same without loads ahead, for the epilogues whose tiles take long anyway
+// and which read what they add to.
+template <typename F, typename R>
+__device__ __forceinline__ void for_columns_plain(uint32_t tmem, int first, int bn, F f, R release) {
+#pragma unroll 1
+  for (int c = first; c < bn; c += 64) {
+    float v[32];
+    tmem_ld32(tmem + c, v);
+    tmem_ld_wait(v);
+    f(c, v);
+  }
+  release();
 }
 
 // ---- matrix instructions -------------------------------------------------------------

@@ -127,6 +127,11 @@ cudaError_t read_device_errors(int slot, unsigned int* out);
 
 // Bounded waits of the log probabilities' kernels that gave up on the current device (synchronous).
 cudaError_t logprobs_timeouts(unsigned int* out);
+// The same of the orthogonalisation's.
+cudaError_t ns_timeouts(unsigned int* out);
+
+// Whether the calling thread's next call of these operators is to lose a block of operands (zero_lm_inject_stall).
+inline thread_local bool g_stall_next = false;
 
 // Streaming multiprocessors of the current device.
 int sm_count();
