@@ -70,7 +70,8 @@ constexpr int kSlots = 12;
 constexpr int kMostStages = 6;
 constexpr int kThreads = 384;        // warp 0 loads, warp 1 issues the products, warps 4-11 are the epilogue
 constexpr int kEpilogueWarps = 8;
-constexpr int kGemmSmem = kSlots * kSlotBytes + 1024;
+constexpr int kStashBytes = 4096;    // of an epilogue warp: two blocks of 32 x 32 on their way out
+constexpr int kGemmSmem = kSlots * kSlotBytes + kEpilogueWarps * kStashBytes + 1024;
 constexpr int kMaxGroups = 12;       // shapes of one launch
 constexpr int64_t kPairs = 76;       // pairs of CTAs among GB300's 152 SMs
 
@@ -118,7 +119,6 @@ struct Job {
   uint32_t stage_tx;           // bytes that land per stage, both CTAs together
   int use_unit;                // powers of the first X's rest of the norm to apply
   int two_out;                 // write a low part too
-  uint16_t* out;
   int64_t out_ld, out_matrix, out_part;
   const uint16_t* add;         // kPoly: A, laid out like the output
   int add_two;
@@ -126,7 +126,7 @@ struct Job {
 };
 
 struct GemmArgs {
-  CUtensorMap map_a[kMaxGroups], map_b[kMaxGroups];
+  CUtensorMap map_a[kMaxGroups], map_b[kMaxGroups], map_out[kMaxGroups];
   Job job[kMaxGroups];
   int jobs;
   int stall;                   // testing the bounded waits: the first pair's first block of K never arrives
@@ -174,12 +174,6 @@ __device__ __forceinline__ Tile locate(const GemmArgs& g, int t) {
 
 // ---- the epilogues -------------------------------------------------------------------
 
-// x as fp16 and what that leaves, as fp16.
-__device__ __forceinline__ void split(float x, __half& hi, __half& lo) {
-  hi = __float2half_rn(x);
-  lo = __float2half_rn(x - __half2float(hi));
-}
-
 __device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo) {
   hi = Fmt<__half>::pack8(v);
   float h[8], rest[8];
@@ -189,153 +183,208 @@ __device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo
   lo = Fmt<__half>::pack8(rest);
 }
 
-// 32 columns from col0 of this thread's row, as they are.
-__device__ __forceinline__ void store_row(const Job& j, uint16_t* out, int row, int col0, const float (&v)[32]) {
-  uint16_t* p = out + row * j.out_ld + col0;
+// Blocks of 32 x 32 values go to memory through this warp's part of shared
+// memory and a TMA store each, rows of 64 bytes in the 64-byte swizzle: from
+// registers a block's mirror image would take 32 stores of 64 bytes.
+__device__ __forceinline__ void put_block(uint32_t at, int lane, const uint4 (&w)[4]) {
 #pragma unroll
-  for (int k = 0; k < 32; k += 8) {
-    if (col0 + k >= j.N) break;
-    float w[8];
+  for (int k = 0; k < 4; ++k)
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)), "r"(w[k].x),
+                 "r"(w[k].y), "r"(w[k].z), "r"(w[k].w)
+                 : "memory");
+}
+
+// The same with rows and columns exchanged: lanes are columns.
+__device__ __forceinline__ void put_turned(uint32_t at, int lane, const uint4 (&w)[4]) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) w[q] = v[k + q];
-    uint4 hi, lo;
-    split8(w, hi, lo);
-    dev::st_16B(p + k, hi);
-    if (j.two_out) dev::st_16B(p + j.out_part + k, lo);
+  for (int k = 0; k < 32; ++k) {
+    const uint32_t pair = (&w[k / 8].x)[k / 2 % 4];
+    const uint16_t one = static_cast<uint16_t>(k & 1 ? pair >> 16 : pair);
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + k * 64 + (((lane >> 3) ^ ((k >> 1) & 3)) << 4) + (lane & 7) * 2),
+                 "h"(one)
+                 : "memory");
   }
 }
 
-// The same of a symmetric matrix: what is on or below the diagonal, and its
-// mirror image, where the lanes' rows are neighbours.
-__device__ __forceinline__ void store_symmetric(const Job& j, uint16_t* out, int row, int col0, const float (&v)[32]) {
-  const int row0 = row - static_cast<int>(threadIdx.x & 31);
-  if (col0 > row0 + 31) return;
-  const bool row_ok = row < j.M;
-  const bool below = col0 + 31 < row0;      // the whole block
-  if (below && row_ok) store_row(j, out, row, col0, v);
+// The warp's block of 32 rows from row0 and 32 columns from col0, v holding
+// this lane's row, in one or two parts; with `mirror` its mirror image too.
+__device__ __forceinline__ void store_block(const Job& j, const CUtensorMap* map, uint32_t stash, int matrix, int row0,
+                                            int col0, const float (&v)[32], bool mirror) {
+  const int lane = threadIdx.x & 31;
+  if (row0 >= j.M || col0 >= j.N) return;
+  uint4 hi[4], lo[4];
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    const int col = col0 + k;
-    if (!row_ok || col > row || col >= j.N) continue;
-    __half hi, lo;
-    split(v[k], hi, lo);
-    uint16_t* mirror = out + col * j.out_ld + row;
-    *mirror = __half_as_ushort(hi);
-    if (j.two_out) mirror[j.out_part] = __half_as_ushort(lo);
-    if (!below) {
-      uint16_t* p = out + row * j.out_ld + col;
-      *p = __half_as_ushort(hi);
-      if (j.two_out) p[j.out_part] = __half_as_ushort(lo);
+  for (int k = 0; k < 4; ++k) {
+    float w[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) w[q] = v[8 * k + q];
+    split8(w, hi[k], lo[k]);
+  }
+  // two blocks at a time: both parts, or the block and its image
+  const int low = j.matrices + matrix;
+  for (int image = 0; image < (j.two_out && mirror ? 2 : 1); ++image) {
+    if (lane == 0) store_wait_read();
+    __syncwarp();
+    if (image == 0) put_block(stash, lane, hi);
+    else put_turned(stash, lane, hi);
+    if (j.two_out) {
+      if (image == 0) put_block(stash + 2048, lane, lo);
+      else put_turned(stash + 2048, lane, lo);
+    } else if (mirror) {
+      put_turned(stash + 2048, lane, hi);
+    }
+    fence_async();
+    __syncwarp();
+    if (lane == 0) {
+      const int x = image == 0 ? col0 : row0, y = image == 0 ? row0 : col0;
+      tma_store3(map, stash, x, y, matrix);
+      if (j.two_out) tma_store3(map, stash + 2048, x, y, low);
+      else if (mirror) tma_store3(map, stash + 2048, row0, col0, matrix);
+      store_commit();
     }
   }
 }
 
-// One element of the last product, at (row, col) of X, to the caller.
-template <int KIND>
-__device__ __forceinline__ void write_one(const Entry& e, int64_t at, float x) {
-  if (KIND == kLastF16) Fmt<__half>::store1(e.out, at, x);
-  if (KIND == kLastBF16) Fmt<__nv_bfloat16>::store1(e.out, at, x);
-  if (KIND == kLastF32) static_cast<float*>(e.out)[at] = x;
-  if (KIND >= kUpdateF16) {
-    const float theta = fmaf(-e.step, x, e.keep * e.master[at]);
-    e.master[at] = theta;
-    if (KIND == kUpdateF16) Fmt<__half>::store1(e.p16, at, theta);
-    else Fmt<__nv_bfloat16>::store1(e.p16, at, theta);
-  }
+__device__ __forceinline__ void st_32B_words(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
 }
 
-// 8 of them, on boundaries of 8.
+__device__ __forceinline__ void ld_32B_words(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
+
+// The caller's 16-bit type of a last product.
 template <int KIND>
-__device__ __forceinline__ void write_8(const Entry& e, int64_t at, const float (&x)[8]) {
-  if (KIND == kLastF16) dev::st_16B(static_cast<uint16_t*>(e.out) + at, Fmt<__half>::pack8(x));
-  if (KIND == kLastBF16) dev::st_16B(static_cast<uint16_t*>(e.out) + at, Fmt<__nv_bfloat16>::pack8(x));
-  if (KIND == kLastF32) dev::st_32B(static_cast<float*>(e.out) + at, x);
-  if (KIND >= kUpdateF16) {
-    float theta[8];
-    dev::ld_32B(e.master + at, theta);
+using Out16 = std::conditional_t<KIND == kLastF16 || KIND == kUpdateF16, __half, __nv_bfloat16>;
+
+// 32 columns of the last product, from col0 of this thread's row of X, to the
+// caller: the result, or the master's update and its 16-bit copy.  All reads
+// come before the writes, so that they wait for memory once.
+template <int KIND>
+__device__ __forceinline__ void write_columns(const Job& j, const Entry& e, int row, int col0, float (&v)[32]) {
+  constexpr bool kUpdate = KIND >= kUpdateF16;
+  const bool wide = e.wide && !e.transposed;
+  const int64_t stride = kUpdate ? e.cols : e.out_stride;
+  const int64_t first = e.transposed ? col0 * stride + row : row * stride + col0, apart = e.transposed ? stride : 1;
+  const int n = min(32, j.N - col0);
+  if (kUpdate) {
+    float theta[32];
+    if (wide) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) theta[k] = fmaf(-e.step, x[k], e.keep * theta[k]);
-    dev::st_32B(e.master + at, theta);
-    dev::st_16B(static_cast<uint16_t*>(e.p16) + at,
-                KIND == kUpdateF16 ? Fmt<__half>::pack8(theta) : Fmt<__nv_bfloat16>::pack8(theta));
+      for (int k = 0; k < 32; k += 8) {
+        float w[8] = {};
+        if (k < n) dev::ld_32B(e.master + first + k, w);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) theta[k + q] = w[q];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) theta[k] = k < n ? e.master[first + k * apart] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = fmaf(-e.step, v[k], e.keep * theta[k]);
+  }
+  if (wide) {
+    // multiples of 8 columns exist
+#pragma unroll
+    for (int k = 0; k < 32; k += 16) {
+      float a[8], b[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        a[q] = v[k + q];
+        b[q] = v[k + 8 + q];
+      }
+      if (kUpdate || KIND == kLastF32) {
+        float* to = (kUpdate ? e.master : static_cast<float*>(e.out)) + first + k;
+        if (k < n) dev::st_32B(to, a);
+        if (k + 8 < n) dev::st_32B(to + 8, b);
+      }
+      if (KIND != kLastF32) {
+        uint16_t* to = static_cast<uint16_t*>(kUpdate ? e.p16 : e.out) + first + k;
+        const uint4 lo = Fmt<Out16<KIND>>::pack8(a), hi = Fmt<Out16<KIND>>::pack8(b);
+        if (k + 8 < n && (reinterpret_cast<uintptr_t>(to) & 31) == 0) {
+          st_32B_words(to, lo, hi);
+        } else {
+          if (k < n) dev::st_16B(to, lo);
+          if (k + 8 < n) dev::st_16B(to + 8, hi);
+        }
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    if (k >= n) break;
+    const int64_t at = first + k * apart;
+    if (kUpdate || KIND == kLastF32) (kUpdate ? e.master : static_cast<float*>(e.out))[at] = v[k];
+    if (KIND != kLastF32) Fmt<Out16<KIND>>::store1(kUpdate ? e.p16 : e.out, at, v[k]);
   }
 }
 
 template <int KIND, typename R>
-__device__ __forceinline__ void epilogue(const GemmArgs& g, const Job& j, const Tile& x, uint32_t tmem, int row,
-                                         int half, bool lost, R release) {
-  const int n0 = x.nt * j.bn;
+__device__ __forceinline__ void epilogue(const GemmArgs& g, const Job& j, const Tile& x, uint32_t tmem, uint32_t stash,
+                                         int row, int half, bool lost, R release) {
+  const int n0 = x.nt * j.bn, row0 = row - static_cast<int>(threadIdx.x & 31);
   const bool row_ok = row < j.M;
   const int which = j.first + x.matrix;
   const float unit = j.use_unit ? g.norms[which].unit : 1.f;
+  const CUtensorMap* map = &g.map_out[x.job];
   if (KIND == kGram) {
-    uint16_t* out = j.out + x.matrix * j.out_matrix;
     const float scale = unit * unit * (kScaleA / (kScaleX * kScaleX));
-    for_columns_plain(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+    for_columns(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+      if (n0 + c > row0) return;
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= scale;
-      store_symmetric(j, out, row, n0 + c, v);
+      store_block(j, map, stash, x.matrix, row0, n0 + c, v, n0 + c < row0);
     }, release);
   } else if (KIND == kPoly) {
-    uint16_t* out = j.out + x.matrix * j.out_matrix;
     const uint16_t* add = j.add + x.matrix * j.out_matrix + row * j.out_ld;
     const float square = j.c * (kScaleP / (kScaleA * kScaleA)), once = j.b * (kScaleP / kScaleA);
-    const int row0 = row - static_cast<int>(threadIdx.x & 31);
     for_columns_plain(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
       const int col0 = n0 + c;
-      if (col0 > row0 + 31) return;
+      if (col0 > row0) return;
+      // A's rows are padded to 16 values: what is read past the last column is not used
+      uint4 hi[4] = {}, lo[4] = {};
 #pragma unroll
-      for (int k = 0; k < 32; k += 8) {
-        float hi[8] = {}, lo[8] = {};
-        if (row_ok && col0 + k < j.N) {
-          Fmt<__half>::unpack8(dev::ld_16B(add + col0 + k), hi);
-          if (j.add_two) Fmt<__half>::unpack8(dev::ld_16B(add + j.out_part + col0 + k), lo);
-        }
+      for (int k = 0; k < 4; k += 2) {
+        if (!row_ok || col0 + 8 * k >= j.N) continue;
+        ld_32B_words(add + col0 + 8 * k, hi[k], hi[k + 1]);
+        if (j.add_two) ld_32B_words(add + j.out_part + col0 + 8 * k, lo[k], lo[k + 1]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float h[8], l[8];
+        Fmt<__half>::unpack8(hi[k], h);
+        Fmt<__half>::unpack8(lo[k], l);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          v[k + q] = fmaf(once, hi[q] + lo[q], square * v[k + q]);
-          if (row == col0 + k + q) v[k + q] += j.a * kScaleP;
+          v[8 * k + q] = fmaf(once, h[q] + l[q], square * v[8 * k + q]);
+          if (row == col0 + 8 * k + q) v[8 * k + q] += j.a * kScaleP;
         }
       }
-      store_symmetric(j, out, row, col0, v);
+      store_block(j, map, stash, x.matrix, row0, col0, v, col0 < row0);
     }, release);
   } else if (KIND == kApply) {
-    uint16_t* out = j.out + x.matrix * j.out_matrix;
     const float scale = unit / kScaleP;
-    for_columns_plain(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+    for_columns(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= scale;
-      if (row_ok) store_row(j, out, row, n0 + c, v);
+      store_block(j, map, stash, x.matrix, row0, n0 + c, v, false);
     }, release);
   } else {
     const Entry& e = g.entries[which];
     const bool finite = g.norms[which].finite && !lost;
-    const bool update = KIND >= kUpdateF16;
     const float scale = finite ? unit / (kScaleP * kScaleX) : NAN;
-    const bool transposed = e.transposed, wide = e.wide;
-    const int64_t stride = update ? e.cols : e.out_stride;
     for_columns_plain(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
-      const int col0 = n0 + c;
       // a norm that is not finite leaves the state as it was
-      if (!row_ok || (update && !finite)) return;
+      if (!row_ok || n0 + c >= j.N || (KIND >= kUpdateF16 && !finite)) return;
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= scale;
-      if (!transposed && wide) {
-#pragma unroll
-        for (int k = 0; k < 32; k += 8) {
-          if (col0 + k >= j.N) break;
-          float w[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) w[q] = v[k + q];
-          write_8<KIND>(e, row * stride + col0 + k, w);
-        }
-        return;
-      }
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        if (col0 + k >= j.N) break;
-        write_one<KIND>(e, transposed ? (col0 + k) * stride + row : row * stride + col0 + k, v[k]);
-      }
+      write_columns<KIND>(j, e, row, n0 + c, v);
     }, release);
   }
 }
@@ -492,6 +541,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm
   } else if (warp >= 4) {
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const bool lost = KIND > kApply && *g.lost != 0;
+    const uint32_t stash = ring + kSlots * kSlotBytes + (warp - 4) * kStashBytes;
     int i = 0;
     for (int t = pair;; t += pairs, ++i) {
       const int a = i & 1;
@@ -501,22 +551,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm
       const int row = x.mt * kTileM + static_cast<int>(rank) * 128 + quad * 32 + lane;
       ok = ok && wait_all(done(a), (i >> 1) & 1);
       if (!ok) {
-        if (KIND < kLastF16 || KIND > kLastF32) break;
-        // this tile and the pair's others of the caller's matrices: no number
-        const Entry& e = g.entries[j.first + x.matrix];
-        for (int c = half * 32; c < j.bn && row < j.M; c += 64)
-          for (int col = x.nt * j.bn + c; col < min(x.nt * j.bn + c + 32, j.N); ++col)
-            write_one<KIND>(e, e.transposed ? col * e.out_stride + row : row * e.out_stride + col, NAN);
-        continue;
+        if constexpr (KIND >= kLastF16 && KIND <= kLastF32) {
+          // this tile and the pair's others of the caller's matrices: no number
+          for (int c = half * 32; c < j.bn; c += 64) {
+            float none[32];
+  #pragma unroll
+            for (int k = 0; k < 32; ++k) none[k] = NAN;
+            if (row < j.M && x.nt * j.bn + c < j.N)
+              write_columns<KIND>(j, g.entries[j.first + x.matrix], row, x.nt * j.bn + c, none);
+          }
+          continue;
+        } else {
+          break;
+        }
       }
       fence_after();
-      epilogue<KIND>(g, j, x, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21), row, half, lost, [&] {
+      epilogue<KIND>(g, j, x, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21), stash, row, half, lost, [&] {
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(in_cta(taken(a), 0));
       });
     }
     if (!ok && lane == 0) failed = 1;
+    if (KIND <= kApply && lane == 0) store_wait();
   }
   __syncthreads();
   if (failed) {
@@ -541,7 +598,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm
 // Both go over tiles of 32 rows x 256 columns of the caller's matrices.
 
 constexpr int kPassThreads = 256, kPassRows = 32, kPassCols = 256;
-constexpr int kPassBlocksPerSm = 4;
+constexpr int kPassBlocksPerSm = 8;
 // Up to this many ranks the second pass reads the gradients again (2 W bytes an
 // element) instead of their fp32 mean, which costs 8.
 constexpr int kDirectRanks = 2;
@@ -572,19 +629,32 @@ struct PassArgs {
   float mu;
   int nesterov;
   int two;                     // the second pass writes low parts
-  double* part;                // a sum of squares for each tile
+  double* part;                // sums of squares at [block + entry]
   Norm* norms;
 };
 
-// The entry that tile t belongs to.
+// The entry that tile t belongs to, found by a whole warp: 32 of the entries
+// left are looked at together.
 __device__ __forceinline__ int entry_of(const Entry* entries, int count, unsigned t) {
-  int lo = 0, hi = count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (entries[mid].tile0 <= t) lo = mid;
-    else hi = mid - 1;
+  int first = 0;
+  while (count > 1) {
+    const int apart = (count + 31) / 32, at = static_cast<int>(threadIdx.x & 31) * apart;
+    const bool reached = at < count && entries[first + at].tile0 <= t;
+    const int found = (__popc(__ballot_sync(0xffffffffu, reached)) - 1) * apart;
+    first += found;
+    count = min(apart, count - found);
   }
-  return lo;
+  return first;
+}
+
+// The tiles of one block of a pass: a stretch of all of them.
+__device__ __forceinline__ unsigned stretch(unsigned tiles, unsigned block) {
+  return static_cast<unsigned>(static_cast<uint64_t>(tiles) * block / gridDim.x);
+}
+
+// The first tile past those of entry `which`.
+__device__ __forceinline__ unsigned end_of(const PassArgs& p, int which) {
+  return which + 1 < p.count ? p.entries[which + 1].tile0 : p.tiles;
 }
 
 __device__ __forceinline__ double block_sum(double s) {
@@ -693,34 +763,39 @@ __device__ __forceinline__ void direction8(const PassArgs& p, const Entry& e, in
   }
 }
 
-// The first pass: each tile's sum of squares, in fp32 within a thread and in
-// fp64 beyond (and the mean gradient, kept where that pays).
+// The first pass: sums of squares, in fp32 within a thread and in fp64 beyond
+// (and the mean gradient, kept where that pays).  A block goes over a stretch of
+// the tiles and leaves a sum for each matrix that it meets, at [block + entry].
 template <typename T, bool MUON>
 __global__ void __launch_bounds__(kPassThreads) sum_squares(const __grid_constant__ PassArgs p) {
   allow_next();
   await_previous();
-  for (unsigned t = blockIdx.x; t < p.tiles; t += gridDim.x) {
+  const unsigned t1 = stretch(p.tiles, blockIdx.x + 1);
+  for (unsigned t = stretch(p.tiles, blockIdx.x); t < t1;) {
     const int which = entry_of(p.entries, p.count, t);
     const Entry& e = p.entries[which];
     const int across = (e.cols + kPassCols - 1) / kPassCols;
-    const int tile = static_cast<int>(t - e.tile0), ty = tile / across;
-    const int col = (tile - ty * across) * kPassCols + static_cast<int>(threadIdx.x & 31) * 8;
-    const int n = e.cols - col;
-    float squares = 0.f;
-    if (n > 0) {
+    const unsigned tile0 = e.tile0, end = min(t1, end_of(p, which));
+    double all = 0.0;
+    for (; t < end; ++t) {
+      const int tile = static_cast<int>(t - tile0), ty = tile / across;
+      const int col = (tile - ty * across) * kPassCols + static_cast<int>(threadIdx.x & 31) * 8;
+      const int n = e.cols - col;
+      float squares = 0.f;
 #pragma unroll
       for (int r = 0; r < kPassRows / 8; ++r) {
         const int row = ty * kPassRows + r * 8 + static_cast<int>(threadIdx.x >> 5);
-        if (row >= e.rows) break;
+        if (row >= e.rows || n <= 0) continue;
         float u[8], m[8];
         direction8<T, MUON>(p, e, which, row, col, n, true, u, m);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (k < n) squares = fmaf(u[k], u[k], squares);
       }
+      all += squares;
     }
-    const double all = block_sum(squares);
-    if (threadIdx.x == 0) p.part[t] = all;
+    all = block_sum(all);
+    if (threadIdx.x == 0) p.part[blockIdx.x + which] = all;
   }
 }
 
@@ -732,61 +807,62 @@ __global__ void __launch_bounds__(kPassThreads) make_first(const __grid_constant
   __shared__ uint32_t turned[kPassCols * (kPassRows + 1)];
   allow_next();
   await_previous();
-  const unsigned t0 = static_cast<unsigned>(static_cast<uint64_t>(p.tiles) * blockIdx.x / gridDim.x);
-  const unsigned t1 = static_cast<unsigned>(static_cast<uint64_t>(p.tiles) * (blockIdx.x + 1) / gridDim.x);
-  int which = -1;
-  float scale = 0.f;
-  bool finite = false;
-  for (unsigned t = t0; t < t1; ++t) {
-    const int now = entry_of(p.entries, p.count, t);
-    const Entry& e = p.entries[now];
+  const unsigned t1 = stretch(p.tiles, blockIdx.x + 1);
+  for (unsigned t = stretch(p.tiles, blockIdx.x); t < t1;) {
+    const int which = entry_of(p.entries, p.count, t);
+    const Entry& e = p.entries[which];
     const int across = (e.cols + kPassCols - 1) / kPassCols;
-    if (now != which) {
-      which = now;
-      const unsigned n = static_cast<unsigned>((e.rows + kPassRows - 1) / kPassRows) * across;
-      double s = 0.0;
-      for (unsigned k = threadIdx.x; k < n; k += kPassThreads) s += p.part[e.tile0 + k];
-      const float norm = static_cast<float>(sqrt(block_sum(s)));
-      finite = isfinite(norm);
-      const int up = norm > 0.f && finite ? min(12 - ilogbf(norm), 126) : 0;
-      scale = finite ? exp2f(static_cast<float>(up)) : 0.f;
-      if (t == e.tile0 && threadIdx.x == 0) p.norms[which] = {norm > 0.f && finite ? kScaleX / (norm * scale) : 0.f, finite};
-    }
-    const int tile = static_cast<int>(t - e.tile0), ty = tile / across, col0 = (tile - ty * across) * kPassCols;
-    const int col = col0 + static_cast<int>(threadIdx.x & 31) * 8, n = e.cols - col;
-    if (e.transposed) __syncthreads();   // the tile before has been written
+    const unsigned tile0 = e.tile0, past = end_of(p, which), end = min(t1, past);
+    // the blocks of the first pass, of which there were as many, that met this matrix
+    unsigned first = static_cast<unsigned>(static_cast<uint64_t>(tile0) * gridDim.x / p.tiles);
+    while (stretch(p.tiles, first + 1) <= tile0) ++first;
+    double s = 0.0;
+    for (unsigned b = first + threadIdx.x; b < gridDim.x && stretch(p.tiles, b) < past; b += kPassThreads)
+      if (stretch(p.tiles, b + 1) > stretch(p.tiles, b)) s += p.part[b + which];
+    const float norm = static_cast<float>(sqrt(block_sum(s)));
+    const bool finite = isfinite(norm);
+    const int up = norm > 0.f && finite ? min(12 - ilogbf(norm), 126) : 0;
+    const float scale = finite ? exp2f(static_cast<float>(up)) : 0.f;
+    if (t == tile0 && threadIdx.x == 0)
+      p.norms[which] = {norm > 0.f && finite ? kScaleX / (norm * scale) : 0.f, finite};
+    for (; t < end; ++t) {
+      const int tile = static_cast<int>(t - tile0), ty = tile / across, col0 = (tile - ty * across) * kPassCols;
+      const int col = col0 + static_cast<int>(threadIdx.x & 31) * 8, n = e.cols - col;
+      if (e.transposed) __syncthreads();   // the tile before has been written
 #pragma unroll
-    for (int r = 0; r < kPassRows / 8; ++r) {
-      const int in_tile = r * 8 + static_cast<int>(threadIdx.x >> 5), row = ty * kPassRows + in_tile;
-      if (row >= e.rows || n <= 0) break;
-      float u[8], m[8];
-      direction8<T, MUON>(p, e, which, row, col, n, false, u, m);
-      if (MUON && finite) store_some(e.momentum + static_cast<int64_t>(row) * e.cols + col, e.wide, n, m);
+      for (int r = 0; r < kPassRows / 8; ++r) {
+        const int in_tile = r * 8 + static_cast<int>(threadIdx.x >> 5), row = ty * kPassRows + in_tile;
+        if (row >= e.rows || n <= 0) continue;
+        float u[8], m[8];
+        direction8<T, MUON>(p, e, which, row, col, n, false, u, m);
+        if (MUON && finite) store_some(e.momentum + static_cast<int64_t>(row) * e.cols + col, e.wide, n, m);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = finite ? u[k] * scale : 0.f;
-      uint4 hi, lo;
-      split8(u, hi, lo);
-      if (!e.transposed) {
-        // columns past the last, up to the boundary of 8, are not read again
-        uint16_t* to = e.x + row * e.ld + col;
-        dev::st_16B(to, hi);
-        if (p.two) dev::st_16B(to + e.x_part, lo);
-      } else {
-        const uint16_t *h = reinterpret_cast<const uint16_t*>(&hi), *l = reinterpret_cast<const uint16_t*>(&lo);
+        for (int k = 0; k < 8; ++k) u[k] = finite ? u[k] * scale : 0.f;
+        uint4 hi, lo;
+        split8(u, hi, lo);
+        if (!e.transposed) {
+          // columns past the last, up to the boundary of 8, are not read again
+          uint16_t* to = e.x + row * e.ld + col;
+          dev::st_16B(to, hi);
+          if (p.two) dev::st_16B(to + e.x_part, lo);
+        } else {
+          const uint16_t *h = reinterpret_cast<const uint16_t*>(&hi), *l = reinterpret_cast<const uint16_t*>(&lo);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          turned[((threadIdx.x & 31) * 8 + k) * (kPassRows + 1) + in_tile] = h[k] | static_cast<uint32_t>(l[k]) << 16;
+          for (int k = 0; k < 8; ++k)
+            turned[((threadIdx.x & 31) * 8 + k) * (kPassRows + 1) + in_tile] = h[k] | static_cast<uint32_t>(l[k]) << 16;
+        }
       }
-    }
-    if (e.transposed) {
-      __syncthreads();
-      const int row = ty * kPassRows + static_cast<int>(threadIdx.x & 31);
-      for (int c = static_cast<int>(threadIdx.x >> 5); c < min(kPassCols, e.cols - col0); c += kPassThreads / 32) {
-        if (row >= e.rows) break;
-        const uint32_t w = turned[c * (kPassRows + 1) + (threadIdx.x & 31)];
-        uint16_t* to = e.x + (col0 + c) * e.ld + row;
-        *to = static_cast<uint16_t>(w);
-        if (p.two) to[e.x_part] = static_cast<uint16_t>(w >> 16);
+      if (e.transposed) {
+        __syncthreads();
+        // half a warp writes a column of the tile, two rows a lane; a row past the last one lies in the padding
+        const int pair = static_cast<int>(threadIdx.x & 15) * 2, row = ty * kPassRows + pair;
+        if (row >= e.rows) continue;
+        for (int c = static_cast<int>(threadIdx.x >> 4); c < min(kPassCols, e.cols - col0); c += kPassThreads / 16) {
+          const uint32_t a = turned[c * (kPassRows + 1) + pair], b = turned[c * (kPassRows + 1) + pair + 1];
+          uint16_t* to = e.x + (col0 + c) * e.ld + row;
+          *reinterpret_cast<uint32_t*>(to) = __byte_perm(a, b, 0x5410);
+          if (p.two) *reinterpret_cast<uint32_t*>(to + e.x_part) = __byte_perm(a, b, 0x7632);
+        }
       }
     }
   }
@@ -797,6 +873,7 @@ __global__ void __launch_bounds__(kPassThreads) make_first(const __grid_constant
 constexpr int64_t kMaxSide = 32768, kMaxMatrices = 65536;
 constexpr int kMaxSteps = 32;
 constexpr int64_t kStatusBytes = 256;
+constexpr int64_t kMostPassBlocks = 2 * kPairs * kPassBlocksPerSm;
 
 // The matrices of one shape, or of its transpose.
 struct Group {
@@ -848,14 +925,14 @@ int make_plan(Plan& plan, int64_t n_matrices, const int64_t* rows, const int64_t
   plan.table_words = n_matrices * (static_cast<int64_t>(sizeof(Entry)) / 8 + (muon ? W : 0));
   plan.norms = plan.table + round_up(plan.table_words * 8, 256);
   plan.part = plan.norms + round_up(n_matrices * static_cast<int64_t>(sizeof(Norm)), 256);
-  plan.mean = plan.part + round_up(plan.tiles * 8, 256);
+  plan.mean = plan.part + round_up((kMostPassBlocks + n_matrices) * 8, 256);
   int64_t at = plan.mean + (muon && W > kDirectRanks ? round_up(numel * 4, 256) : 0);
   int64_t first = 0;
   for (Group& g : plan.groups) {
     g.first = first;
     first += static_cast<int64_t>(g.members.size());
-    g.ldx = round_up(g.n, 8);
-    g.lda = round_up(g.m, 8);
+    g.ldx = round_up(g.n, 16);
+    g.lda = round_up(g.m, 16);
     for (int64_t* to : {&g.x[0], &g.x[1]}) {
       *to = at;
       at += round_up(g.x_part() * 4, 256);
@@ -870,16 +947,18 @@ int make_plan(Plan& plan, int64_t n_matrices, const int64_t* rows, const int64_t
 }
 
 // A stack of `depth` row-major fp16 matrices, in boxes of box_rows x 64 under the
-// 128-byte swizzle; what lies outside a matrix reads as 0.
-int make_map3(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int64_t depth, int box_rows) {
+// 128-byte swizzle (out: x 32 under the 64-byte one); what lies outside a matrix
+// reads as 0.
+int make_map3(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int64_t depth, int box_rows,
+              bool out = false) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(depth)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * rows * 2};
-  const cuuint32_t box[3] = {kTileK, static_cast<cuuint32_t>(box_rows), 1}, ones[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {out ? 32u : kTileK, static_cast<cuuint32_t>(box_rows), 1}, ones[3] = {1, 1, 1};
   const host::EncodeFn fn = host::encoder();
   if (!fn) return fail(ZERO_E_CUDA, "the driver offers no tensor-map encoder");
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, ones,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? ZERO_OK : fail(ZERO_E_CUDA, "encoding a tensor map failed (%d)", static_cast<int>(r));
 }
 
@@ -985,18 +1064,16 @@ int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, ch
         j.c = static_cast<float>(r.coefficients[3 * step + 2]);
         char *x = ws + group.x[step & 1], *a = ws + group.a, *p = ws + group.p;
         int rc;
+        char* out = kind == kGram ? a : kind == kPoly ? p : ws + group.x[(step & 1) ^ 1];
         if (kind == kGram) {
-          j.out = reinterpret_cast<uint16_t*>(a);
           if ((rc = make_map3(&g.map_a[k], x, m, n, group.ldx, 2 * c, 128))) return rc;
           if ((rc = make_map3(&g.map_b[k], x, m, n, group.ldx, 2 * c, j.bn / 2))) return rc;
         } else if (kind == kPoly) {
-          j.out = reinterpret_cast<uint16_t*>(p);
           j.add = reinterpret_cast<const uint16_t*>(a);
           j.add_two = parts > 1;
           if ((rc = make_map3(&g.map_a[k], a, m, m, group.lda, 2 * c, 128))) return rc;
           if ((rc = make_map3(&g.map_b[k], a, m, m, group.lda, 2 * c, j.bn / 2))) return rc;
         } else {
-          j.out = reinterpret_cast<uint16_t*>(ws + group.x[(step & 1) ^ 1]);
           if ((rc = make_map3(&g.map_a[k], p, m, m, group.lda, 2 * c, 128))) return rc;
           if ((rc = make_map3(&g.map_b[k], x, m, n, group.ldx, 2 * c, 64))) return rc;
         }
@@ -1004,6 +1081,7 @@ int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, ch
         j.out_ld = applies(kind) ? group.ldx : group.lda;
         j.out_matrix = m * j.out_ld;
         j.out_part = c * j.out_matrix;
+        if ((rc = make_map3(&g.map_out[k], out, m, applies(kind) ? n : m, j.out_ld, 2 * c, 32, true))) return rc;
       }
       const int rc = launch_kind(kind, g, s, stall);
       if (rc) return rc;
@@ -1032,7 +1110,7 @@ int send_table(const std::vector<uint64_t>& words, char* to, unsigned int* lost,
 
 template <typename T, bool MUON>
 int launch_passes(const PassArgs& p, cudaStream_t s) {
-  const int64_t most = static_cast<int64_t>(sm_count()) * kPassBlocksPerSm;
+  const int64_t most = std::min(static_cast<int64_t>(sm_count()) * kPassBlocksPerSm, kMostPassBlocks);
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(p.tiles, most)));
   ZERO_CUDA(launch_chained(sum_squares<T, MUON>, grid, kPassThreads, 0, s, p));
   ZERO_CUDA(launch_chained(make_first<T, MUON>, grid, kPassThreads, 0, s, p));
