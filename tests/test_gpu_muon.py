@@ -57,6 +57,27 @@ def test_orthogonalize(rows, cols, dtype):
     check([gaussian(cols, rows), few_directions(cols, rows)], dtype, what="few directions")
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("rows,cols", [(128, 256), (128, 272), (2048, 128), (64, 2048), (128, 1025), (1999, 17), (5, 700), (2049, 16), (129, 130)])
+def test_around_what_one_cluster_takes(rows, cols, dtype):
+    check([gaussian(rows, cols)], dtype, what="gaussian")
+    check([few_directions(rows, cols)], dtype, what="few directions")
+
+
+def test_mixed_sizes_in_one_call():
+    """Matrices of one CTA, of clusters and beyond in one call, few of each and many."""
+    shapes = [(30, 20), (128, 700), (300, 300), (9, 1500), (64, 64), (260, 140), (700, 128), (1, 1)]
+    matrices = [gaussian(r, c, seed=i) for i, (r, c) in enumerate(shapes)]
+    whole = check(matrices, "bf16")
+    many = check(matrices * 20, "bf16")
+    for i, (x, got) in enumerate(zip(matrices, whole)):
+        # how many CTAs share a matrix goes by the call's other matrices, where SMs are left
+        want = ref.orthogonal(x.bfloat16())
+        tol = ref.tolerance(x.bfloat16(), want, ref.COEFFICIENTS, 3, 1) + ref.HALF_ULP[torch.bfloat16]
+        ref.assert_near(got, want, tol, f"{i}")
+        ref.assert_near(many[i + 8 * 13], want, tol, f"{i} of many")
+
+
 @pytest.mark.parametrize("fine", [0, 1, 3, 5])
 def test_fine_steps(fine):
     for dtype in ("bf16", "fp32"):
@@ -280,8 +301,8 @@ def test_the_same_bits_every_time_and_in_a_graph(what):
     assert torch.equal(op.master, twin.master) and torch.equal(op.momentum, twin.momentum)
 
 
-def test_a_wait_that_runs_out_is_reported():
-    shapes = [(300, 300), (64, 600)]
+@pytest.mark.parametrize("shapes", [[(300, 300), (200, 600)], [(64, 600)], [(64, 64)]])
+def test_a_wait_that_runs_out_is_reported(shapes):
     xs = [gaussian(*s).bfloat16() for s in shapes]
     op, other = zs.Orthogonalize(shapes, "bf16"), zs.Orthogonalize(shapes, "bf16")
     good = op.forward(xs)

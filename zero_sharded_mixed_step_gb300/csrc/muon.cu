@@ -42,6 +42,7 @@
 #include <vector>
 
 #include "launch.cuh"
+#include "ns_common.cuh"
 #include "step_math.cuh"
 #include "tensor_map.h"
 #include "umma.cuh"
@@ -53,6 +54,7 @@ namespace zero {
 namespace {
 
 using namespace umma;
+using namespace ns;
 using dev::Fmt;
 using host::ceil_div;
 using host::cuda_fail;
@@ -75,47 +77,16 @@ constexpr int kGemmSmem = kSlots * kSlotBytes + kEpilogueWarps * kStashBytes + 1
 constexpr int kMaxGroups = 12;       // shapes of one launch
 constexpr int64_t kPairs = 76;       // pairs of CTAs among GB300's 152 SMs
 
-// How the workspace holds X, A and P: times powers of two.
-constexpr float kScaleX = 4096.f, kScaleA = 4096.f, kScaleP = 512.f;
-
-enum Kind : int { kGram, kPoly, kApply, kLastF16, kLastBF16, kLastF32, kUpdateF16, kUpdateBF16 };
+enum Kind : int { kGram, kPoly, kApply, kLast, kUpdate };
 
 __host__ __device__ constexpr bool symmetric(int kind) { return kind <= kPoly; }
 __host__ __device__ constexpr bool applies(int kind) { return kind >= kApply; }
-
-// One matrix of a call, in device memory.
-struct Entry {
-  int rows, cols;              // the caller's
-  int transposed;              // X is its transpose
-  int wide;                    // the caller's rows allow accesses of 8 values
-  const void* in;              // zero_orthogonalize
-  void* out;
-  int64_t in_stride, out_stride;
-  float* master;               // zero_muon_step
-  float* momentum;
-  void* p16;
-  float* mean;                 // the ranks' mean gradient in workspace, or NULL
-  float step, keep;            // lr s and 1 - lr wd
-  unsigned tile0;              // first of its tiles in the elementwise passes
-  int unused;
-  uint16_t* x;                 // its first X: the high part, the low part x_part further
-  int64_t x_part;
-  int64_t ld;                  // of X
-};
-
-// What the passes leave for the products: 2^12 over the stored X's norm, and
-// whether the input's norm is finite.
-struct Norm {
-  float unit;
-  int finite;
-};
 
 struct Job {
   int matrices, first;         // of the group: how many, the first one's entry
   int m_tiles, n_tiles, per_matrix, tiles;
   int M, N, kb, bn;
   int b_boxes;                 // boxes of an MN-major B half tile
-  int parts_a, parts_b;
   uint32_t stage_tx;           // bytes that land per stage, both CTAs together
   int use_unit;                // powers of the first X's rest of the norm to apply
   int two_out;                 // write a low part too
@@ -130,6 +101,7 @@ struct GemmArgs {
   Job job[kMaxGroups];
   int jobs;
   int stall;                   // testing the bounded waits: the first pair's first block of K never arrives
+  int dtype;                   // kLast: of the results; kUpdate: of the 16-bit copies
   const Entry* entries;
   const Norm* norms;
   unsigned int* failures;      // the workspace's count of waits that gave up
@@ -173,15 +145,6 @@ __device__ __forceinline__ Tile locate(const GemmArgs& g, int t) {
 }
 
 // ---- the epilogues -------------------------------------------------------------------
-
-__device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo) {
-  hi = Fmt<__half>::pack8(v);
-  float h[8], rest[8];
-  Fmt<__half>::unpack8(hi, h);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) rest[k] = v[k] - h[k];
-  lo = Fmt<__half>::pack8(rest);
-}
 
 // Blocks of 32 x 32 values go to memory through this warp's part of shared
 // memory and a TMA store each, rows of 64 bytes in the 64-byte swizzle: from
@@ -245,86 +208,6 @@ __device__ __forceinline__ void store_block(const Job& j, const CUtensorMap* map
   }
 }
 
-__device__ __forceinline__ void st_32B_words(void* p, const uint4& a, const uint4& b) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
-               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-               : "memory");
-}
-
-__device__ __forceinline__ void ld_32B_words(const void* p, uint4& a, uint4& b) {
-  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
-               : "l"(p));
-}
-
-// The caller's 16-bit type of a last product.
-template <int KIND>
-using Out16 = std::conditional_t<KIND == kLastF16 || KIND == kUpdateF16, __half, __nv_bfloat16>;
-
-// 32 columns of the last product, from col0 of this thread's row of X, to the
-// caller: the result, or the master's update and its 16-bit copy.  All reads
-// come before the writes, so that they wait for memory once.
-template <int KIND>
-__device__ __forceinline__ void write_columns(const Job& j, const Entry& e, int row, int col0, float (&v)[32]) {
-  constexpr bool kUpdate = KIND >= kUpdateF16;
-  const bool wide = e.wide && !e.transposed;
-  const int64_t stride = kUpdate ? e.cols : e.out_stride;
-  const int64_t first = e.transposed ? col0 * stride + row : row * stride + col0, apart = e.transposed ? stride : 1;
-  const int n = min(32, j.N - col0);
-  if (kUpdate) {
-    float theta[32];
-    if (wide) {
-#pragma unroll
-      for (int k = 0; k < 32; k += 8) {
-        float w[8] = {};
-        if (k < n) dev::ld_32B(e.master + first + k, w);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) theta[k + q] = w[q];
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) theta[k] = k < n ? e.master[first + k * apart] : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] = fmaf(-e.step, v[k], e.keep * theta[k]);
-  }
-  if (wide) {
-    // multiples of 8 columns exist
-#pragma unroll
-    for (int k = 0; k < 32; k += 16) {
-      float a[8], b[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        a[q] = v[k + q];
-        b[q] = v[k + 8 + q];
-      }
-      if (kUpdate || KIND == kLastF32) {
-        float* to = (kUpdate ? e.master : static_cast<float*>(e.out)) + first + k;
-        if (k < n) dev::st_32B(to, a);
-        if (k + 8 < n) dev::st_32B(to + 8, b);
-      }
-      if (KIND != kLastF32) {
-        uint16_t* to = static_cast<uint16_t*>(kUpdate ? e.p16 : e.out) + first + k;
-        const uint4 lo = Fmt<Out16<KIND>>::pack8(a), hi = Fmt<Out16<KIND>>::pack8(b);
-        if (k + 8 < n && (reinterpret_cast<uintptr_t>(to) & 31) == 0) {
-          st_32B_words(to, lo, hi);
-        } else {
-          if (k < n) dev::st_16B(to, lo);
-          if (k + 8 < n) dev::st_16B(to + 8, hi);
-        }
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    if (k >= n) break;
-    const int64_t at = first + k * apart;
-    if (kUpdate || KIND == kLastF32) (kUpdate ? e.master : static_cast<float*>(e.out))[at] = v[k];
-    if (KIND != kLastF32) Fmt<Out16<KIND>>::store1(kUpdate ? e.p16 : e.out, at, v[k]);
-  }
-}
-
 template <int KIND, typename R>
 __device__ __forceinline__ void epilogue(const GemmArgs& g, const Job& j, const Tile& x, uint32_t tmem, uint32_t stash,
                                          int row, int half, bool lost, R release) {
@@ -381,10 +264,10 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const Job& j, const 
     const float scale = finite ? unit / (kScaleP * kScaleX) : NAN;
     for_columns_plain(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
       // a norm that is not finite leaves the state as it was
-      if (!row_ok || n0 + c >= j.N || (KIND >= kUpdateF16 && !finite)) return;
+      if (!row_ok || n0 + c >= j.N || (KIND == kUpdate && !finite)) return;
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= scale;
-      write_columns<KIND>(j, e, row, n0 + c, v);
+      write_columns<KIND == kUpdate>(j.N, e, g.dtype, row, n0 + c, v);
     }, release);
   }
 }
@@ -392,8 +275,10 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const Job& j, const 
 // The persistent product kernel: pairs of CTAs, each pair one tile at a time,
 // operands through a ring of TMA stages of one or two parts each, two
 // accumulators in TMEM so that one tile's epilogue runs beside the next one's
-// products.  Tiles are dealt out in turn.
-template <int KIND>
+// products.  Tiles are dealt out in turn.  PA and PB are the operands' parts:
+// known at run time alone, they kept the loads of one part each from keeping up
+// with the products (4096 x 4096 in five such steps: 1146 us, 911 so).
+template <int KIND, int PA, int PB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm(const __grid_constant__ GemmArgs g) {
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t bars[2 * kMostStages + 5];
@@ -409,10 +294,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  // every job of a launch has operands of as many parts
-  const int parts_a = g.job[0].parts_a, parts_b = g.job[0].parts_b;
-  const int stages = kSlots / (parts_a + parts_b);
-  const uint32_t stage_bytes = (parts_a + parts_b) * kSlotBytes;
+  constexpr int stages = kSlots / (PA + PB);
+  constexpr uint32_t stage_bytes = (PA + PB) * kSlotBytes;
 
   allow_next();
   if (threadIdx.x == 0) {
@@ -460,15 +343,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm
         ok = wait_all(empty(s), phase);
         if (!ok) break;
         const uint32_t bar = in_cta(full(s), 0);
-        const uint32_t sa = ring + s * stage_bytes, sb = sa + parts_a * kSlotBytes;
+        const uint32_t sa = ring + s * stage_bytes, sb = sa + PA * kSlotBytes;
         const int k = kb * kTileK;
         if (lead) {
           if (rank == 0) bar_expect(full(s), j.stage_tx);
           if (!(g.stall && pair == 0 && issued == 0)) {
-            for (int p = 0; p < parts_a; ++p)
+#pragma unroll
+            for (int p = 0; p < PA; ++p)
               tma_load3(sa + p * kSlotBytes, ma, k, am, p * j.matrices + x.matrix, bar);
           }
-          for (int p = 0; p < parts_b; ++p) {
+#pragma unroll
+          for (int p = 0; p < PB; ++p) {
             const uint32_t to = sb + p * kSlotBytes;
             const int z = p * j.matrices + x.matrix;
             if (applies(KIND)) {
@@ -499,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm
         constexpr bool b_mn = applies(KIND);
         const uint32_t idesc = instr_desc(false, false, b_mn, kTileM, j.bn);
         const uint64_t a_step = 32 >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
-        const uint64_t a0 = operand_desc(ring, 0), b0 = operand_desc(ring + parts_a * kSlotBytes, b_mn ? 8192 : 0);
+        const uint64_t a0 = operand_desc(ring, 0), b0 = operand_desc(ring + PA * kSlotBytes, b_mn ? 8192 : 0);
         constexpr uint64_t kPart = kSlotBytes >> 4;
         const int a = i & 1;
         ok = wait_all(taken(a), ((i >> 1) & 1) ^ 1);
@@ -516,8 +401,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm
 #pragma unroll
             for (int q = 0; q < kTileK / 16; ++q) {
               mma(d, da + q * a_step, db + q * b_step, idesc, kb > 0 || q > 0);
-              if (parts_a > 1) mma(d, da + kPart + q * a_step, db + q * b_step, idesc, true);
-              if (parts_b > 1) mma(d, da + q * a_step, db + kPart + q * b_step, idesc, true);
+              if (PA > 1) mma(d, da + kPart + q * a_step, db + q * b_step, idesc, true);
+              if (PB > 1) mma(d, da + q * a_step, db + kPart + q * b_step, idesc, true);
             }
             mma_commit(empty(s));
           }
@@ -551,14 +436,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm
       const int row = x.mt * kTileM + static_cast<int>(rank) * 128 + quad * 32 + lane;
       ok = ok && wait_all(done(a), (i >> 1) & 1);
       if (!ok) {
-        if constexpr (KIND >= kLastF16 && KIND <= kLastF32) {
+        if constexpr (KIND == kLast) {
           // this tile and the pair's others of the caller's matrices: no number
           for (int c = half * 32; c < j.bn; c += 64) {
             float none[32];
   #pragma unroll
             for (int k = 0; k < 32; ++k) none[k] = NAN;
             if (row < j.M && x.nt * j.bn + c < j.N)
-              write_columns<KIND>(j, g.entries[j.first + x.matrix], row, x.nt * j.bn + c, none);
+              write_columns<false>(j.N, g.entries[j.first + x.matrix], g.dtype, row, x.nt * j.bn + c, none);
           }
           continue;
         } else {
@@ -597,19 +482,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm
 //
 // Both go over tiles of 32 rows x 256 columns of the caller's matrices.
 
-constexpr int kPassThreads = 256, kPassRows = 32, kPassCols = 256;
 constexpr int kPassBlocksPerSm = 8;
 // Up to this many ranks the second pass reads the gradients again (2 W bytes an
 // element) instead of their fp32 mean, which costs 8.
 constexpr int kDirectRanks = 2;
-
-// The list of matrices on its way to the device: launched once for each
-// kTableBytes of it, since a launch's parameters hold no more.
-template <int BYTES>
-struct TablePart {
-  unsigned char data[BYTES];
-};
-constexpr int kSmallTable = 4 * 1024, kLargeTable = 28 * 1024;
 
 template <int BYTES>
 __global__ void __launch_bounds__(kPassThreads) copy_table(const __grid_constant__ TablePart<BYTES> part, int words,
@@ -619,19 +495,6 @@ __global__ void __launch_bounds__(kPassThreads) copy_table(const __grid_constant
   for (int k = threadIdx.x; k < words; k += kPassThreads) to[k] = reinterpret_cast<const uint64_t*>(part.data)[k];
   if (threadIdx.x == 0) *lost = 0;
 }
-
-struct PassArgs {
-  const Entry* entries;
-  const uint64_t* grads;       // zero_muon_step: W addresses for each entry
-  int count;
-  unsigned tiles;
-  int W;
-  float mu;
-  int nesterov;
-  int two;                     // the second pass writes low parts
-  double* part;                // sums of squares at [block + entry]
-  Norm* norms;
-};
 
 // The entry that tile t belongs to, found by a whole warp: 32 of the entries
 // left are looked at together.
@@ -655,112 +518,6 @@ __device__ __forceinline__ unsigned stretch(unsigned tiles, unsigned block) {
 // The first tile past those of entry `which`.
 __device__ __forceinline__ unsigned end_of(const PassArgs& p, int which) {
   return which + 1 < p.count ? p.entries[which + 1].tile0 : p.tiles;
-}
-
-__device__ __forceinline__ double block_sum(double s) {
-  __shared__ double of_warp[kPassThreads / 32];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) of_warp[threadIdx.x >> 5] = s;
-  __syncthreads();
-  double all = 0.0;
-  for (int k = 0; k < kPassThreads / 32; ++k) all += of_warp[k];
-  return all;
-}
-
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
-  if constexpr (std::is_same<T, float>::value) dev::ld_32B(p, f);
-  else Fmt<T>::unpack8(dev::ld_16B(p), f);
-}
-template <typename T>
-__device__ __forceinline__ float load1(const T* p) {
-  if constexpr (std::is_same<T, float>::value) return *p;
-  else return Fmt<T>::load1(p, 0);
-}
-
-// 8 neighbours' (or, without `wide`, up to 8 neighbours' of which `n` exist)
-// mean over the ranks, in rank order.
-template <typename T>
-__device__ __forceinline__ void rank_mean8(const uint64_t* grads, int W, int64_t at, bool wide, int n, float (&g)[8]) {
-  const bool pow2 = (W & (W - 1)) == 0;
-  const float inv_w = 1.f / W;
-  if (wide) {
-    for (int w0 = 0; w0 < W; w0 += 8) {
-      uint4 raw[8];
-#pragma unroll
-      for (int w = 0; w < 8; ++w)
-        if (w0 + w < W) raw[w] = dev::ld_16B(reinterpret_cast<const T*>(grads[w0 + w]) + at);
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        if (w0 + w >= W) break;
-        float f[8];
-        Fmt<T>::unpack8(raw[w], f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] = w0 + w == 0 ? f[k] : __fadd_rn(g[k], f[k]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      g[k] = 0.f;
-      for (int w = 0; w < W && k < n; ++w) {
-        const float f = Fmt<T>::load1(reinterpret_cast<const T*>(grads[w]), at + k);
-        g[k] = w == 0 ? f : __fadd_rn(g[k], f);
-      }
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 8; ++k) g[k] = dev::rank_mean(g[k], W, inv_w, pow2);
-}
-
-// 8 values of an fp32 vector; those that do not exist read as 0.
-__device__ __forceinline__ void load_some(const float* p, bool wide, int n, float (&f)[8]) {
-  if (wide) {
-    dev::ld_32B(p, f);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = k < n ? p[k] : 0.f;
-  }
-}
-__device__ __forceinline__ void store_some(float* p, bool wide, int n, const float (&f)[8]) {
-  if (wide) {
-    dev::st_32B(p, f);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < n) p[k] = f[k];
-  }
-}
-
-// The matrix's values from (row, col) on, 8 of which n exist: the input, or
-// the step's direction U and the new momentum.
-template <typename T, bool MUON>
-__device__ __forceinline__ void direction8(const PassArgs& p, const Entry& e, int which, int row, int col, int n,
-                                           bool first, float (&u)[8], float (&m)[8]) {
-  const bool wide = e.wide;
-  if constexpr (!MUON) {
-    const T* in = static_cast<const T*>(e.in) + row * e.in_stride + col;
-    if (wide) {
-      load8(in, u);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = k < n ? load1(in + k) : 0.f;
-    }
-  } else {
-    const int64_t at = static_cast<int64_t>(row) * e.cols + col;
-    float g[8];
-    if (first || e.mean == nullptr) rank_mean8<T>(p.grads + static_cast<int64_t>(which) * p.W, p.W, at, wide, n, g);
-    else load_some(e.mean + at, wide, n, g);
-    if (first && e.mean != nullptr) store_some(e.mean + at, wide, n, g);
-    load_some(e.momentum + at, wide, n, m);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      m[k] = __fmaf_rn(p.mu, m[k], g[k]);
-      u[k] = p.nesterov ? __fmaf_rn(p.mu, m[k], g[k]) : m[k];
-    }
-  }
 }
 
 // The first pass: sums of squares, in fp32 within a thread and in fp64 beyond
@@ -871,7 +628,6 @@ __global__ void __launch_bounds__(kPassThreads) make_first(const __grid_constant
 // ---- host -------------------------------------------------------------------------------
 
 constexpr int64_t kMaxSide = 32768, kMaxMatrices = 65536;
-constexpr int kMaxSteps = 32;
 constexpr int64_t kStatusBytes = 256;
 constexpr int64_t kMostPassBlocks = 2 * kPairs * kPassBlocksPerSm;
 
@@ -889,6 +645,7 @@ struct Group {
 // How a call's matrices are laid out in the workspace.
 struct Plan {
   std::vector<Group> groups;
+  std::vector<int64_t> small;  // the matrices that one cluster of CTAs takes whole
   int64_t count = 0, tiles = 0;
   int64_t table, table_words, norms, part, mean, total;
 };
@@ -904,7 +661,12 @@ int make_plan(Plan& plan, int64_t n_matrices, const int64_t* rows, const int64_t
     if (rows[i] < 1 || rows[i] > kMaxSide || cols[i] < 1 || cols[i] > kMaxSide)
       return fail(ZERO_E_ARG, "matrix %lld: %lld x %lld, sides outside [1, %lld]", (long long)i, (long long)rows[i],
                   (long long)cols[i], (long long)kMaxSide);
+    if (small_fits(rows[i], cols[i])) {
+      plan.small.push_back(i);
+      continue;
+    }
     const int64_t m = std::min(rows[i], cols[i]), n = std::max(rows[i], cols[i]);
+    ++plan.count;
     auto it = std::find_if(plan.groups.begin(), plan.groups.end(), [&](const Group& g) { return g.m == m && g.n == n; });
     if (it == plan.groups.end()) {
       plan.groups.emplace_back();
@@ -920,12 +682,11 @@ int make_plan(Plan& plan, int64_t n_matrices, const int64_t* rows, const int64_t
   // the longest products first
   std::sort(plan.groups.begin(), plan.groups.end(),
             [](const Group& a, const Group& b) { return a.n != b.n ? a.n > b.n : a.m > b.m; });
-  plan.count = n_matrices;
   plan.table = kStatusBytes;
-  plan.table_words = n_matrices * (static_cast<int64_t>(sizeof(Entry)) / 8 + (muon ? W : 0));
+  plan.table_words = plan.count * (static_cast<int64_t>(sizeof(Entry)) / 8 + (muon ? W : 0));
   plan.norms = plan.table + round_up(plan.table_words * 8, 256);
-  plan.part = plan.norms + round_up(n_matrices * static_cast<int64_t>(sizeof(Norm)), 256);
-  plan.mean = plan.part + round_up((kMostPassBlocks + n_matrices) * 8, 256);
+  plan.part = plan.norms + round_up(plan.count * static_cast<int64_t>(sizeof(Norm)), 256);
+  plan.mean = plan.part + round_up((kMostPassBlocks + plan.count) * 8, 256);
   int64_t at = plan.mean + (muon && W > kDirectRanks ? round_up(numel * 4, 256) : 0);
   int64_t first = 0;
   for (Group& g : plan.groups) {
@@ -978,8 +739,6 @@ void cut(Job& j, int kind, int64_t M, int64_t N, int64_t K, int matrices, int pa
     j.per_matrix = j.m_tiles * j.n_tiles;
   }
   j.tiles = j.per_matrix * matrices;
-  j.parts_a = parts_a;
-  j.parts_b = parts_b;
   j.b_boxes = static_cast<int>(ceil_div(bn / 2, 64));
   const int b_bytes = applies(kind) ? j.b_boxes * 8192 : bn / 2 * kTileK * 2;
   j.stage_tx = static_cast<uint32_t>(2 * (parts_a * kSlotBytes + parts_b * b_bytes));
@@ -1005,27 +764,34 @@ int width_of(int kind, int64_t M, int64_t N, int64_t K, int matrices, int parts_
   return best;
 }
 
-template <int KIND>
+template <int KIND, int PA, int PB>
 int launch_products(GemmArgs& g, cudaStream_t s, bool& stall) {
   g.stall = std::exchange(stall, false);
-  ZERO_CUDA(cudaFuncSetAttribute(ns_gemm<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem));
+  const auto fn = ns_gemm<KIND, PA, PB>;
+  ZERO_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem));
   int64_t tiles = 0;
   for (int k = 0; k < g.jobs; ++k) tiles += g.job[k].tiles;
   const int pairs = static_cast<int>(std::min({std::max<int64_t>(1, sm_count() / 2), kPairs, tiles}));
-  ZERO_CUDA(launch_chained(ns_gemm<KIND>, dim3(2 * pairs), kThreads, kGemmSmem, s, g));
+  ZERO_CUDA(launch_chained(fn, dim3(2 * pairs), kThreads, kGemmSmem, s, g));
   return ZERO_OK;
 }
 
-int launch_kind(int kind, GemmArgs& g, cudaStream_t s, bool& stall) {
+template <int KIND>
+int launch_parts(int parts_a, int parts_b, GemmArgs& g, cudaStream_t s, bool& stall) {
+  if (parts_a == 1) return launch_products<KIND, 1, 1>(g, s, stall);
+  if constexpr (KIND == kApply || KIND == kLast) {   // the first X of a 16-bit input
+    if (parts_b == 1) return launch_products<KIND, 2, 1>(g, s, stall);
+  }
+  return launch_products<KIND, 2, 2>(g, s, stall);
+}
+
+int launch_kind(int kind, int parts_a, int parts_b, GemmArgs& g, cudaStream_t s, bool& stall) {
   switch (kind) {
-    case kGram: return launch_products<kGram>(g, s, stall);
-    case kPoly: return launch_products<kPoly>(g, s, stall);
-    case kApply: return launch_products<kApply>(g, s, stall);
-    case kLastF16: return launch_products<kLastF16>(g, s, stall);
-    case kLastBF16: return launch_products<kLastBF16>(g, s, stall);
-    case kLastF32: return launch_products<kLastF32>(g, s, stall);
-    case kUpdateF16: return launch_products<kUpdateF16>(g, s, stall);
-    default: return launch_products<kUpdateBF16>(g, s, stall);
+    case kGram: return launch_parts<kGram>(parts_a, parts_b, g, s, stall);
+    case kPoly: return launch_parts<kPoly>(parts_a, parts_b, g, s, stall);
+    case kApply: return launch_parts<kApply>(parts_a, parts_b, g, s, stall);
+    case kLast: return launch_parts<kLast>(parts_a, parts_b, g, s, stall);
+    default: return launch_parts<kUpdate>(parts_a, parts_b, g, s, stall);
   }
 }
 
@@ -1034,6 +800,7 @@ struct Recurrence {
   const double* coefficients;
   int first_parts;             // of the first X
   int last;                    // Kind of the last product
+  int dtype;                   // of what it writes
 };
 
 // The steps, over the groups from `from` on, as many as a launch takes.
@@ -1043,8 +810,10 @@ int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, ch
     const int next_parts = step + 1 < r.fine ? 2 : 1;
     const bool last = step + 1 == r.steps;
     for (int kind : {static_cast<int>(kGram), static_cast<int>(kPoly), last ? r.last : static_cast<int>(kApply)}) {
+      const int pa = kind == kGram ? x_parts : parts, pb = kind == kPoly ? parts : x_parts;
       GemmArgs g;
       std::memset(&g, 0, sizeof g);
+      g.dtype = r.dtype;
       g.entries = reinterpret_cast<const Entry*>(ws + plan.table);
       g.norms = reinterpret_cast<const Norm*>(ws + plan.norms);
       g.failures = reinterpret_cast<unsigned int*>(ws);
@@ -1054,7 +823,6 @@ int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, ch
         const int c = static_cast<int>(group.members.size()), k = g.jobs++;
         const int64_t m = group.m, n = group.n;
         Job& j = g.job[k];
-        const int pa = applies(kind) || kind == kPoly ? parts : x_parts, pb = kind == kPoly ? parts : x_parts;
         const int64_t N = applies(kind) ? n : m, K = kind == kGram ? n : m;
         cut(j, kind, m, N, K, c, pa, pb, width_of(kind, m, N, K, c, pa, pb));
         j.first = static_cast<int>(group.first);
@@ -1083,7 +851,7 @@ int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, ch
         j.out_part = c * j.out_matrix;
         if ((rc = make_map3(&g.map_out[k], out, m, applies(kind) ? n : m, j.out_ld, 2 * c, 32, true))) return rc;
       }
-      const int rc = launch_kind(kind, g, s, stall);
+      const int rc = launch_kind(kind, pa, pb, g, s, stall);
       if (rc) return rc;
     }
   }
@@ -1150,7 +918,6 @@ int fine_steps(int fine, int steps, bool all) { return fine >= 0 ? fine : all ? 
 
 // Fills an entry's place in the workspace.
 void place(Entry& e, const Group& g, int64_t member, char* ws) {
-  e.transposed = e.rows > e.cols;
   e.ld = g.ldx;
   e.x = reinterpret_cast<uint16_t*>(ws + g.x[0]) + member * g.m * g.ldx;
   e.x_part = g.x_part();
@@ -1158,7 +925,14 @@ void place(Entry& e, const Group& g, int64_t member, char* ws) {
 
 }  // namespace
 
-cudaError_t ns_timeouts(unsigned int* out) { return cudaMemcpyFromSymbol(out, g_ns_timeouts, sizeof *out); }
+cudaError_t ns_timeouts(unsigned int* out) {
+  unsigned int small = 0;
+  const cudaError_t e = ns::small_timeouts(&small);
+  if (e != cudaSuccess) return e;
+  const cudaError_t e2 = cudaMemcpyFromSymbol(out, g_ns_timeouts, sizeof *out);
+  *out += small;
+  return e2;
+}
 
 }  // namespace zero
 
@@ -1194,35 +968,45 @@ extern "C" int zero_orthogonalize(int64_t n_matrices, const int64_t* rows, const
   if ((rc = check_workspace(workspace, workspace_bytes, plan.total))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
+  auto entry = [&](int64_t i) {
+    Entry e;
+    std::memset(&e, 0, sizeof e);
+    e.rows = static_cast<int>(rows[i]);
+    e.cols = static_cast<int>(cols[i]);
+    e.transposed = rows[i] > cols[i];
+    e.in = in[i];
+    e.out = out[i];
+    e.in_stride = in_strides ? in_strides[i] : cols[i];
+    e.out_stride = out_strides ? out_strides[i] : cols[i];
+    const uintptr_t both = reinterpret_cast<uintptr_t>(e.in) | reinterpret_cast<uintptr_t>(e.out);
+    e.wide = both % (8 * item) == 0 && (e.cols | e.in_stride | e.out_stride) % 8 == 0;
+    return e;
+  };
+  Recurrence r = {steps, fine_steps(fine, steps, dtype == ZERO_FP32), coefficients, dtype == ZERO_FP32 ? 2 : 1,
+                  kLast, dtype};
+  std::vector<Entry> small;
+  for (int64_t i : plan.small) small.push_back(entry(i));
+  SmallCall c = {small.data(), nullptr, static_cast<int>(small.size()), false, dtype, dtype, 0, 0.f, 0, steps, r.fine,
+                 r.first_parts, coefficients, static_cast<unsigned int*>(workspace), s};
+  if ((rc = run_small(c, stall))) return rc;
+  if (plan.count == 0) return ZERO_OK;
   constexpr size_t kEntryWords = sizeof(Entry) / 8;
   std::vector<uint64_t> words(plan.table_words);
   unsigned tile = 0;
   for (const Group& g : plan.groups)
     for (size_t k = 0; k < g.members.size(); ++k) {
-      const int64_t i = g.members[k];
-      Entry e;
-      std::memset(&e, 0, sizeof e);
-      e.rows = static_cast<int>(rows[i]);
-      e.cols = static_cast<int>(cols[i]);
-      e.in = in[i];
-      e.out = out[i];
-      e.in_stride = in_strides ? in_strides[i] : cols[i];
-      e.out_stride = out_strides ? out_strides[i] : cols[i];
-      const uintptr_t both = reinterpret_cast<uintptr_t>(e.in) | reinterpret_cast<uintptr_t>(e.out);
-      e.wide = both % (8 * item) == 0 && (e.cols | e.in_stride | e.out_stride) % 8 == 0;
+      Entry e = entry(g.members[k]);
       e.tile0 = tile;
-      tile += static_cast<unsigned>(pass_tiles(rows[i], cols[i]));
+      tile += static_cast<unsigned>(pass_tiles(e.rows, e.cols));
       place(e, g, static_cast<int64_t>(k), ws);
       std::memcpy(&words[(g.first + k) * kEntryWords], &e, sizeof e);
     }
   unsigned int* lost = reinterpret_cast<unsigned int*>(ws) + 1;
   if ((rc = send_table(words, ws + plan.table, lost, s))) return rc;
-  Recurrence r = {steps, fine_steps(fine, steps, dtype == ZERO_FP32), coefficients, dtype == ZERO_FP32 ? 2 : 1,
-                  dtype == ZERO_FP16 ? kLastF16 : dtype == ZERO_BF16 ? kLastBF16 : kLastF32};
   PassArgs p;
   std::memset(&p, 0, sizeof p);
   p.entries = reinterpret_cast<const Entry*>(ws + plan.table);
-  p.count = static_cast<int>(n_matrices);
+  p.count = static_cast<int>(plan.count);
   p.tiles = tile;
   p.two = r.first_parts > 1 && r.fine > 0;
   p.part = reinterpret_cast<double*>(ws + plan.part);
@@ -1276,47 +1060,60 @@ extern "C" int zero_muon_step(int W, int64_t n_matrices, const int64_t* rows, co
   if ((rc = check_workspace(workspace, workspace_bytes, plan.total))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
+  auto entry = [&](int64_t i, uint64_t* ranks) {
+    Entry e;
+    std::memset(&e, 0, sizeof e);
+    e.rows = static_cast<int>(rows[i]);
+    e.cols = static_cast<int>(cols[i]);
+    e.transposed = rows[i] > cols[i];
+    e.master = master[i];
+    e.momentum = momentum[i];
+    e.p16 = p16[i];
+    e.step = static_cast<float>(lr * (scales ? scales[i] : 1.0));
+    e.keep = static_cast<float>(1.0 - lr * weight_decay);
+    const uintptr_t fp32 = reinterpret_cast<uintptr_t>(e.master) | reinterpret_cast<uintptr_t>(e.momentum);
+    uintptr_t b16 = reinterpret_cast<uintptr_t>(e.p16);
+    for (int w = 0; w < W; ++w) {
+      ranks[w] = reinterpret_cast<uint64_t>(grads[w * n_matrices + i]);
+      b16 |= reinterpret_cast<uintptr_t>(grads[w * n_matrices + i]);
+    }
+    e.wide = fp32 % 32 == 0 && b16 % 16 == 0 && e.cols % 8 == 0;
+    return e;
+  };
+  Recurrence r = {steps, fine_steps(fine, steps, false), coefficients, 2, kUpdate, work_dtype};
+  std::vector<Entry> small;
+  std::vector<uint64_t> small_ranks(plan.small.size() * W);
+  for (int64_t i : plan.small) small.push_back(entry(i, &small_ranks[small.size() * W]));
+  SmallCall c = {small.data(), small_ranks.data(), static_cast<int>(small.size()), true, grad_dtype, work_dtype, W,
+                 static_cast<float>(mu), nesterov != 0, steps, r.fine, r.first_parts, coefficients,
+                 static_cast<unsigned int*>(workspace), s};
+  if ((rc = run_small(c, stall))) return rc;
+  if (plan.count == 0) return ZERO_OK;
   constexpr size_t kEntryWords = sizeof(Entry) / 8;
   std::vector<uint64_t> words(plan.table_words);
-  uint64_t* ranks = words.data() + n_matrices * kEntryWords;
+  uint64_t* ranks = words.data() + plan.count * kEntryWords;
   unsigned tile = 0;
   int64_t mean_at = plan.mean;
   for (const Group& g : plan.groups)
     for (size_t k = 0; k < g.members.size(); ++k) {
-      const int64_t i = g.members[k], to = g.first + static_cast<int64_t>(k);
-      Entry e;
-      std::memset(&e, 0, sizeof e);
-      e.rows = static_cast<int>(rows[i]);
-      e.cols = static_cast<int>(cols[i]);
-      e.master = master[i];
-      e.momentum = momentum[i];
-      e.p16 = p16[i];
+      const int64_t to = g.first + static_cast<int64_t>(k);
+      Entry e = entry(g.members[k], ranks + to * W);
       if (W > kDirectRanks) {
         e.mean = reinterpret_cast<float*>(ws + mean_at);
-        mean_at += round_up(rows[i] * cols[i], 8) * 4;
+        mean_at += round_up(static_cast<int64_t>(e.rows) * e.cols, 8) * 4;
       }
-      e.step = static_cast<float>(lr * (scales ? scales[i] : 1.0));
-      e.keep = static_cast<float>(1.0 - lr * weight_decay);
-      uintptr_t fp32 = reinterpret_cast<uintptr_t>(e.master) | reinterpret_cast<uintptr_t>(e.momentum);
-      uintptr_t b16 = reinterpret_cast<uintptr_t>(e.p16);
-      for (int w = 0; w < W; ++w) {
-        ranks[to * W + w] = reinterpret_cast<uint64_t>(grads[w * n_matrices + i]);
-        b16 |= reinterpret_cast<uintptr_t>(grads[w * n_matrices + i]);
-      }
-      e.wide = fp32 % 32 == 0 && b16 % 16 == 0 && e.cols % 8 == 0;
       e.tile0 = tile;
-      tile += static_cast<unsigned>(pass_tiles(rows[i], cols[i]));
+      tile += static_cast<unsigned>(pass_tiles(e.rows, e.cols));
       place(e, g, static_cast<int64_t>(k), ws);
       std::memcpy(&words[to * kEntryWords], &e, sizeof e);
     }
   unsigned int* lost = reinterpret_cast<unsigned int*>(ws) + 1;
   if ((rc = send_table(words, ws + plan.table, lost, s))) return rc;
-  Recurrence r = {steps, fine_steps(fine, steps, false), coefficients, 2, work_dtype == ZERO_FP16 ? kUpdateF16 : kUpdateBF16};
   PassArgs p;
   std::memset(&p, 0, sizeof p);
   p.entries = reinterpret_cast<const Entry*>(ws + plan.table);
-  p.grads = reinterpret_cast<const uint64_t*>(ws + plan.table) + n_matrices * kEntryWords;
-  p.count = static_cast<int>(n_matrices);
+  p.grads = reinterpret_cast<const uint64_t*>(ws + plan.table) + plan.count * kEntryWords;
+  p.count = static_cast<int>(plan.count);
   p.tiles = tile;
   p.W = W;
   p.mu = static_cast<float>(mu);
