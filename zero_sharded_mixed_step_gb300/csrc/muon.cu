@@ -9,15 +9,23 @@
 //   g = (G_0 + ... + G_{W-1}) / W,   M <- mu M + g,   U = g + mu M or M,
 //   theta <- theta (1 - lr wd) - lr s X(U),   16-bit copy <- theta
 //
-// A step of the recurrence is three launches, each over every matrix of the
-// call; matrices of one shape (or its transpose) lie one after another in the
-// workspace, X as m x n always, so that a 3-D tensor map loads any of them.
-// All products run on one persistent tensor-core kernel, ns_gemm, pairs of
-// CTAs on tiles of 256 rows, in fp16 with fp32 sums:
+// Small matrices run in shared memory (muon_small.cu).  The others take three
+// launches: two passes over the input, which find the norm and write X_0, and one
+// persistent tensor-core kernel, ns_run, for all the steps.  Matrices of one
+// shape (or its transpose) lie one after another in the workspace, X as m x n
+// always, so that a 3-D tensor map loads any of them.  The work is a list of
+// tiles of 256 rows, one product after another:
 //   kGram   A, of which the lower half is computed and mirrored
 //   kPoly   A A likewise, with P formed in its epilogue
 //   kApply  P X; of the last step its epilogue writes the caller's matrix or
 //           updates the master and the 16-bit copy in place.
+// Pairs of CTAs take tiles from a counter in the list's order; a tile waits until
+// every tile of its matrix's product before has been written, which another
+// counter for each matrix says.  What a tile waits for has a lower number, so
+// some running pair has it or has done it, and no wait can last for ever.  With
+// several matrices a pair finds tiles that are ready; one product's tail runs
+// beside the next one's start (as 15 launches, 24 matrices of 768 x 768 took 490
+// us: the products' own time is about 226).
 // Precision.  A singular value far below 1 grows by `a` (3.4) a step, and with
 // it the noise that rounding X, A and P to 16 bits leaves in its direction:
 // with fp16 operands throughout, a matrix whose largest singular values stand
@@ -61,55 +69,65 @@ using host::cuda_fail;
 using host::fail;
 using host::round_up;
 
-// Bounded device-side waits of ns_gemm that gave up, over all calls; never set back (see zero_lm_status).
+// Bounded device-side waits of ns_run that gave up, over all calls; never set back (see zero_lm_status).
 __device__ unsigned int g_ns_timeouts;
 
 constexpr int kTileM = 256;          // rows of a tile: 128 in each CTA of the pair
 constexpr int kTileN = 256;          // most columns of a tile
 constexpr int kTileK = 64;
 constexpr int kSlotBytes = 128 * kTileK * 2;     // one part of one operand's half tile in one CTA
-constexpr int kSlots = 12;
-constexpr int kMostStages = 6;
-constexpr int kThreads = 384;        // warp 0 loads, warp 1 issues the products, warps 4-11 are the epilogue
+// A stage of the operands' ring: of two parts, A's and B's parts of one block of
+// K; of one part, A and B of two blocks
+constexpr int kStages = 3, kStageBytes = 4 * kSlotBytes;
+// warp 0 loads A (and in the leader takes the tiles), warp 3 loads B, warp 1
+// issues the products, warps 4-11 are the epilogue
+constexpr int kThreads = 384;
 constexpr int kEpilogueWarps = 8;
+constexpr int kQueue = 4;            // tiles on their way through a pair
 constexpr int kStashBytes = 4096;    // of an epilogue warp: two blocks of 32 x 32 on their way out
-constexpr int kGemmSmem = kSlots * kSlotBytes + kEpilogueWarps * kStashBytes + 1024;
-constexpr int kMaxGroups = 12;       // shapes of one launch
+constexpr int kRunSmem = kStages * kStageBytes + kEpilogueWarps * kStashBytes + 1024;
+constexpr int kFewGroups = 3, kMaxGroups = 12;       // shapes of one launch
 constexpr int64_t kPairs = 76;       // pairs of CTAs among GB300's 152 SMs
 
 enum Kind : int { kGram, kPoly, kApply, kLast, kUpdate };
 
-__host__ __device__ constexpr bool symmetric(int kind) { return kind <= kPoly; }
-__host__ __device__ constexpr bool applies(int kind) { return kind >= kApply; }
-
-struct Job {
-  int matrices, first;         // of the group: how many, the first one's entry
-  int m_tiles, n_tiles, per_matrix, tiles;
-  int M, N, kb, bn;
-  int b_boxes;                 // boxes of an MN-major B half tile
-  uint32_t stage_tx;           // bytes that land per stage, both CTAs together
-  int use_unit;                // powers of the first X's rest of the norm to apply
-  int two_out;                 // write a low part too
-  int64_t out_ld, out_matrix, out_part;
-  const uint16_t* add;         // kPoly: A, laid out like the output
-  int add_two;
-  float a, b, c;
+// The matrices of one shape.
+struct Shape {
+  CUtensorMap x[2], a, p;            // loads in boxes of 128 rows x 64
+  CUtensorMap x64[2], a64;           // of 64 x 64
+  CUtensorMap x_out[2], a_out, p_out;   // stores of 32 x 32
+  int matrices, first;               // how many, the first one's entry
+  int m, n;
+  int bn[3];                         // columns of a tile of each kind: 128 or 256
+  int tiles[3];                      // of one matrix
+  const uint16_t* gram;              // A
+  int64_t ld, apart, part;           // of A: rows, matrices, parts
 };
 
-struct GemmArgs {
-  CUtensorMap map_a[kMaxGroups], map_b[kMaxGroups], map_out[kMaxGroups];
-  Job job[kMaxGroups];
-  int jobs;
-  int stall;                   // testing the bounded waits: the first pair's first block of K never arrives
+template <int GROUPS>
+struct RunArgs {
+  Shape shape[GROUPS];
+  int shapes;
+  int tiles[3];                // of a step, by kind
+  int steps, fine, first_parts;
   int dtype;                   // kLast: of the results; kUpdate: of the 16-bit copies
+  int stall;                   // testing the bounded waits: the first tile's first block of K never arrives
   const Entry* entries;
   const Norm* norms;
+  unsigned int* next;          // tiles taken so far (0 at the launch)
+  unsigned int* exits;         // CTAs that have ended (0)
+  unsigned int* written;       // for each matrix: tiles written, counted by epilogue warp (0)
   unsigned int* failures;      // the workspace's count of waits that gave up
-  unsigned int* lost;          // set where tiles of this call were not computed
+  unsigned int* lost;          // set where tiles of this call were not computed (0)
+  int entries_here;            // of these shapes, from shape[0].first on
+  float coefficients[3 * kMaxSteps];
 };
 
-struct Tile {
-  int job, matrix, mt, nt;
+// What the roles of a pair need to know of a tile.
+struct alignas(16) Tile {
+  int kind;                    // -1: no more
+  int shape, matrix, mt;
+  int nt, step, kb, unused;    // kb: blocks of K
 };
 
 // Tiles of a row of tiles that hold something on or below the diagonal.
@@ -118,31 +136,58 @@ __host__ __device__ inline int tiles_of_row(int mt, int bn, int n_tiles) {
   return reach < n_tiles ? reach : n_tiles;
 }
 
-template <int KIND>
-__device__ __forceinline__ Tile locate(const GemmArgs& g, int t) {
-  Tile x{0, 0, 0, 0};
-  while (x.job < g.jobs && t >= g.job[x.job].tiles) t -= g.job[x.job++].tiles;
-  if (x.job == g.jobs) {
-    x.job = -1;
+// Tile t of the list; `before`: the tiles of its matrix's products before.
+template <int GROUPS>
+__device__ __forceinline__ Tile locate(const RunArgs<GROUPS>& g, unsigned t, unsigned& before) {
+  Tile x = {};
+  const unsigned each = g.tiles[0] + g.tiles[1] + g.tiles[2];
+  x.step = static_cast<int>(t / each);
+  if (x.step >= g.steps) {
+    x.kind = -1;
     return x;
   }
-  const Job& j = g.job[x.job];
-  x.matrix = static_cast<int>(static_cast<unsigned>(t) / static_cast<unsigned>(j.per_matrix));
-  t -= x.matrix * j.per_matrix;
-  if (symmetric(KIND)) {
+  int r = static_cast<int>(t - x.step * each);
+  while (r >= g.tiles[x.kind]) r -= g.tiles[x.kind++];
+  while (r >= g.shape[x.shape].matrices * g.shape[x.shape].tiles[x.kind]) {
+    r -= g.shape[x.shape].matrices * g.shape[x.shape].tiles[x.kind];
+    ++x.shape;
+  }
+  const Shape& h = g.shape[x.shape];
+  x.matrix = static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(h.tiles[x.kind]));
+  r -= x.matrix * h.tiles[x.kind];
+  before = x.step * (h.tiles[0] + h.tiles[1] + h.tiles[2]);
+  for (int k = 0; k < x.kind; ++k) before += h.tiles[k];
+  const int bn = h.bn[x.kind];
+  if (x.kind < kApply) {
+    const int n_tiles = (h.m + bn - 1) / bn;
     for (;;) {
-      const int n = tiles_of_row(x.mt, j.bn, j.n_tiles);
-      if (t < n) break;
-      t -= n;
+      const int n = tiles_of_row(x.mt, bn, n_tiles);
+      if (r < n) break;
+      r -= n;
       ++x.mt;
     }
-    x.nt = t;
+    x.nt = r;
   } else {
-    x.nt = static_cast<int>(static_cast<unsigned>(t) / static_cast<unsigned>(j.m_tiles));
-    x.mt = t - x.nt * j.m_tiles;
+    const unsigned m_tiles = (h.m + kTileM - 1) / kTileM;
+    x.nt = static_cast<int>(static_cast<unsigned>(r) / m_tiles);
+    x.mt = r - x.nt * static_cast<int>(m_tiles);
   }
+  x.kb = ((x.kind == kGram ? h.n : h.m) + kTileK - 1) / kTileK;
   return x;
 }
+
+// The operands' parts in a tile's product.
+struct Parts {
+  int a, b;
+};
+template <int GROUPS>
+__device__ __forceinline__ Parts parts_of(const RunArgs<GROUPS>& g, const Tile& x) {
+  const int parts = x.step < g.fine ? 2 : 1, of_x = x.step == 0 ? min(parts, g.first_parts) : parts;
+  return {x.kind == kGram ? of_x : parts, x.kind == kPoly ? parts : of_x};
+}
+
+// Bytes of a half tile of B for one CTA: rows of K-major, or boxes of 64 columns.
+__device__ __forceinline__ uint32_t b_bytes(const Shape& h, const Tile& x) { return h.bn[x.kind] / 2 * kTileK * 2; }
 
 // ---- the epilogues -------------------------------------------------------------------
 
@@ -169,12 +214,31 @@ __device__ __forceinline__ void put_turned(uint32_t at, int lane, const uint4 (&
   }
 }
 
+// One block on its way: the two places take turns, so that a block is put into
+// one while the other's is read.
+__device__ __forceinline__ void send_block(const CUtensorMap* map, uint32_t stash, int& turn, int x, int y, int z,
+                                           const uint4 (&w)[4], bool turned) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t to = stash + (turn & 1) * 2048;
+  ++turn;
+  if (lane == 0) store_wait_read_but_one();
+  __syncwarp();
+  if (turned) put_turned(to, lane, w);
+  else put_block(to, lane, w);
+  fence_async();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store3(map, to, x, y, z);
+    store_commit();
+  }
+}
+
 // The warp's block of 32 rows from row0 and 32 columns from col0, v holding
 // this lane's row, in one or two parts; with `mirror` its mirror image too.
-__device__ __forceinline__ void store_block(const Job& j, const CUtensorMap* map, uint32_t stash, int matrix, int row0,
-                                            int col0, const float (&v)[32], bool mirror) {
-  const int lane = threadIdx.x & 31;
-  if (row0 >= j.M || col0 >= j.N) return;
+__device__ __forceinline__ void store_block(const Shape& h, int rows, int cols, const CUtensorMap* map, uint32_t stash,
+                                            int& turn, int matrix, int row0, int col0, const float (&v)[32], bool two,
+                                            bool mirror) {
+  if (row0 >= rows || col0 >= cols) return;
   uint4 hi[4], lo[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -183,123 +247,121 @@ __device__ __forceinline__ void store_block(const Job& j, const CUtensorMap* map
     for (int q = 0; q < 8; ++q) w[q] = v[8 * k + q];
     split8(w, hi[k], lo[k]);
   }
-  // two blocks at a time: both parts, or the block and its image
-  const int low = j.matrices + matrix;
-  for (int image = 0; image < (j.two_out && mirror ? 2 : 1); ++image) {
-    if (lane == 0) store_wait_read();
-    __syncwarp();
-    if (image == 0) put_block(stash, lane, hi);
-    else put_turned(stash, lane, hi);
-    if (j.two_out) {
-      if (image == 0) put_block(stash + 2048, lane, lo);
-      else put_turned(stash + 2048, lane, lo);
-    } else if (mirror) {
-      put_turned(stash + 2048, lane, hi);
-    }
-    fence_async();
-    __syncwarp();
-    if (lane == 0) {
-      const int x = image == 0 ? col0 : row0, y = image == 0 ? row0 : col0;
-      tma_store3(map, stash, x, y, matrix);
-      if (j.two_out) tma_store3(map, stash + 2048, x, y, low);
-      else if (mirror) tma_store3(map, stash + 2048, row0, col0, matrix);
-      store_commit();
-    }
+  send_block(map, stash, turn, col0, row0, matrix, hi, false);
+  if (two) send_block(map, stash, turn, col0, row0, h.matrices + matrix, lo, false);
+  if (mirror) {
+    send_block(map, stash, turn, row0, col0, matrix, hi, true);
+    if (two) send_block(map, stash, turn, row0, col0, h.matrices + matrix, lo, true);
   }
 }
 
-template <int KIND, typename R>
-__device__ __forceinline__ void epilogue(const GemmArgs& g, const Job& j, const Tile& x, uint32_t tmem, uint32_t stash,
-                                         int row, int half, bool lost, R release) {
-  const int n0 = x.nt * j.bn, row0 = row - static_cast<int>(threadIdx.x & 31);
-  const bool row_ok = row < j.M;
-  const int which = j.first + x.matrix;
-  const float unit = j.use_unit ? g.norms[which].unit : 1.f;
-  const CUtensorMap* map = &g.map_out[x.job];
-  if (KIND == kGram) {
+// 16 bytes that another SM wrote while this kernel ran: past L1.
+__device__ __forceinline__ uint4 ld_fresh(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.cg.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+  return r;
+}
+
+template <int FINAL, int GROUPS, typename R>
+__device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x, uint32_t tmem, uint32_t stash,
+                                         int& turn, int row, int half, R release) {
+  const Shape& h = g.shape[x.shape];
+  const int bn = h.bn[x.kind], n0 = x.nt * bn, row0 = row - static_cast<int>(threadIdx.x & 31);
+  const int which = h.first + x.matrix;
+  const float unit = x.step == 0 ? g.norms[which].unit : 1.f;     // what the first X lacks of the norm
+  const bool two = x.step < g.fine;
+  if (x.kind == kGram) {
     const float scale = unit * unit * (kScaleA / (kScaleX * kScaleX));
-    for_columns(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+    for_columns(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
       if (n0 + c > row0) return;
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= scale;
-      store_block(j, map, stash, x.matrix, row0, n0 + c, v, n0 + c < row0);
+      store_block(h, h.m, h.m, &h.a_out, stash, turn, x.matrix, row0, n0 + c, v, two, n0 + c < row0);
     }, release);
-  } else if (KIND == kPoly) {
-    const uint16_t* add = j.add + x.matrix * j.out_matrix + row * j.out_ld;
-    const float square = j.c * (kScaleP / (kScaleA * kScaleA)), once = j.b * (kScaleP / kScaleA);
-    for_columns_plain(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+  } else if (x.kind == kPoly) {
+    const uint16_t* add = h.gram + x.matrix * h.apart + row * h.ld;
+    const float a = g.coefficients[3 * x.step] * kScaleP, once = g.coefficients[3 * x.step + 1] * (kScaleP / kScaleA);
+    const float square = g.coefficients[3 * x.step + 2] * (kScaleP / (kScaleA * kScaleA));
+    for_columns_plain(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
       const int col0 = n0 + c;
       if (col0 > row0) return;
       // A's rows are padded to 16 values: what is read past the last column is not used
       uint4 hi[4] = {}, lo[4] = {};
 #pragma unroll
-      for (int k = 0; k < 4; k += 2) {
-        if (!row_ok || col0 + 8 * k >= j.N) continue;
-        ld_32B_words(add + col0 + 8 * k, hi[k], hi[k + 1]);
-        if (j.add_two) ld_32B_words(add + j.out_part + col0 + 8 * k, lo[k], lo[k + 1]);
+      for (int k = 0; k < 4; ++k) {
+        if (row >= h.m || col0 + 8 * k >= h.m) continue;
+        hi[k] = ld_fresh(add + col0 + 8 * k);
+        if (two) lo[k] = ld_fresh(add + h.part + col0 + 8 * k);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float h[8], l[8];
-        Fmt<__half>::unpack8(hi[k], h);
+        float u[8], l[8];
+        Fmt<__half>::unpack8(hi[k], u);
         Fmt<__half>::unpack8(lo[k], l);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          v[8 * k + q] = fmaf(once, h[q] + l[q], square * v[8 * k + q]);
-          if (row == col0 + 8 * k + q) v[8 * k + q] += j.a * kScaleP;
+          v[8 * k + q] = fmaf(once, u[q] + l[q], square * v[8 * k + q]);
+          if (row == col0 + 8 * k + q) v[8 * k + q] += a;
         }
       }
-      store_block(j, map, stash, x.matrix, row0, col0, v, col0 < row0);
+      store_block(h, h.m, h.m, &h.p_out, stash, turn, x.matrix, row0, col0, v, two, col0 < row0);
     }, release);
-  } else if (KIND == kApply) {
+  } else if (x.step + 1 < g.steps) {
     const float scale = unit / kScaleP;
-    for_columns(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+    for_columns(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= scale;
-      store_block(j, map, stash, x.matrix, row0, n0 + c, v, false);
+      store_block(h, h.m, h.n, &h.x_out[(x.step & 1) ^ 1], stash, turn, x.matrix, row0, n0 + c, v, x.step + 1 < g.fine,
+                  false);
     }, release);
   } else {
     const Entry& e = g.entries[which];
-    const bool finite = g.norms[which].finite && !lost;
+    const bool finite = g.norms[which].finite;
     const float scale = finite ? unit / (kScaleP * kScaleX) : NAN;
-    for_columns_plain(tmem, half * 32, j.bn, [&](int c, float (&v)[32]) {
+    for_columns_plain(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
       // a norm that is not finite leaves the state as it was
-      if (!row_ok || n0 + c >= j.N || (KIND == kUpdate && !finite)) return;
+      if (row >= h.m || n0 + c >= h.n || (FINAL == kUpdate && !finite)) return;
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= scale;
-      write_columns<KIND == kUpdate>(j.N, e, g.dtype, row, n0 + c, v);
+      write_columns<FINAL == kUpdate>(h.n, e, g.dtype, row, n0 + c, v);
     }, release);
   }
 }
 
-// The persistent product kernel: pairs of CTAs, each pair one tile at a time,
-// operands through a ring of TMA stages of one or two parts each, two
-// accumulators in TMEM so that one tile's epilogue runs beside the next one's
-// products.  Tiles are dealt out in turn.  PA and PB are the operands' parts:
-// known at run time alone, they kept the loads of one part each from keeping up
-// with the products (4096 x 4096 in five such steps: 1146 us, 911 so).
-template <int KIND, int PA, int PB>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm(const __grid_constant__ GemmArgs g) {
+__device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void add_release(unsigned* p, unsigned v) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// All the steps of the matrices of a launch: see above.  Operands through a ring
+// of TMA stages, two accumulators in TMEM so that one tile's epilogue runs beside
+// the next one's products.
+template <int FINAL, int GROUPS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(const __grid_constant__ RunArgs<GROUPS> g) {
   extern __shared__ unsigned char raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMostStages + 5];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 2 * kQueue + 5];
+  __shared__ Tile queue[kQueue];
   __shared__ uint32_t tmem_slot;
-  __shared__ int failed;
+  __shared__ int failed, last_out;
   const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
   const uint32_t bar0 = smem_addr(bars);
   auto full = [&](int s) { return bar0 + 8 * s; };
-  auto empty = [&](int s) { return bar0 + 8 * (kMostStages + s); };
-  auto done = [&](int a) { return bar0 + 8 * (2 * kMostStages + a); };        // accumulator a is complete
-  auto taken = [&](int a) { return bar0 + 8 * (2 * kMostStages + 2 + a); };   // accumulator a has been read
-  const uint32_t drained = bar0 + 8 * (2 * kMostStages + 4);
+  auto empty = [&](int s) { return bar0 + 8 * (kStages + s); };
+  auto done = [&](int a) { return bar0 + 8 * (2 * kStages + a); };        // accumulator a is complete
+  auto taken = [&](int a) { return bar0 + 8 * (2 * kStages + 2 + a); };   // accumulator a has been read
+  const uint32_t drained = bar0 + 8 * (2 * kStages + 4);
+  auto told = [&](int q) { return bar0 + 8 * (2 * kStages + 5 + q); };             // queue[q] holds a tile
+  auto heard = [&](int q) { return bar0 + 8 * (2 * kStages + 5 + kQueue + q); };   // everyone has read it
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  constexpr int stages = kSlots / (PA + PB);
-  constexpr uint32_t stage_bytes = (PA + PB) * kSlotBytes;
 
   allow_next();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kMostStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       bar_init(full(s), 1);
       bar_init(empty(s), 1);
     }
@@ -307,13 +369,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm
       bar_init(done(a), 1);
       bar_init(taken(a), 2 * kEpilogueWarps);
     }
+    for (int q = 0; q < kQueue; ++q) {
+      bar_init(told(q), 1);
+      bar_init(heard(q), 4 + 2 * kEpilogueWarps);   // the loaders but the leader's first, the issuer, the epilogue
+    }
     bar_init(drained, 1);
     failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    for (int k = 0; k < g.jobs; ++k) {
-      tma_prefetch_map(&g.map_a[k]);
-      tma_prefetch_map(&g.map_b[k]);
-    }
   }
   if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 512);
   __syncthreads();
@@ -326,92 +388,175 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm
   const bool lead = elect_one();
   bool ok = true;
   auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity)) != 0; };
+  // The i-th tile of this pair, from the leader's first warp.
+  auto tile_of = [&](int i) {
+    Tile x{};
+    x.kind = -1;
+    const int q = i % kQueue;
+    ok = __all_sync(0xffffffffu, bar_wait<true>(told(q), (i / kQueue) & 1)) != 0;
+    if (!ok) return x;
+    x = queue[q];
+    __syncwarp();
+    if (lead) bar_arrive(in_cta(heard(q), 0));
+    return x;
+  };
+  // The next tile: taken from the counter, waited for, and told to the others.
+  auto take_tile = [&](int i) {
+    const int q = i % kQueue;
+    Tile x{};
+    x.kind = -1;
+    ok = wait_all(heard(q), ((i / kQueue) & 1) ^ 1);
+    if (!ok) return x;
+    unsigned t = 0, before = 0;
+    if (lead) t = atomicAdd(g.next, 1u);
+    t = __reduce_max_sync(0xffffffffu, lead ? t : 0u);
+    x = locate(g, t, before);
+    if (x.kind >= 0 && before > 0) {
+      const unsigned* p = g.written + g.shape[x.shape].first + x.matrix;
+      const unsigned want = before * 2 * kEpilogueWarps;
+      bool there = true;
+      if (lead) {
+        const long long t0 = clock64();
+        while (there && ld_acquire(p) < want) there = clock64() - t0 <= kWaitCycles;
+      }
+      ok = __all_sync(0xffffffffu, there) != 0;
+      if (!ok) return x;
+    }
+    // what the others wrote through the async proxy is loaded through it
+    fence_all_async();
+    if (lead) {
+      for (uint32_t r = 0; r < 2; ++r) {
+        const uint32_t at = in_cta(smem_addr(&queue[q]), r);
+        st_cluster(at, x.kind, x.shape, x.matrix, x.mt);
+        st_cluster(at + 16, x.nt, x.step, x.kb, 0);
+        bar_arrive_written(in_cta(told(q), r));
+      }
+    }
+    __syncwarp();
+    return x;
+  };
 
   int issued = 0;      // stages loaded by this warp
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     int s = 0;
     uint32_t phase = 1;
-    for (int t = pair; ok; t += pairs) {
-      const Tile x = locate<KIND>(g, t);
-      if (x.job < 0) break;
-      const Job& j = g.job[x.job];
-      const CUtensorMap *ma = &g.map_a[x.job], *mb = &g.map_b[x.job];
+    const bool first = warp == 0;
+    for (int i = 0;; ++i) {
+      const Tile x = first && rank == 0 ? take_tile(i) : tile_of(i);
+      if (!ok || x.kind < 0) break;
+      fence_all_async();
+      const Shape& h = g.shape[x.shape];
+      const Parts parts = parts_of(g, x);
+      const int bn = h.bn[x.kind];
+      const bool b_mn = x.kind == kApply;
+      const CUtensorMap* map;
+      if (first) map = x.kind == kGram ? &h.x[x.step & 1] : x.kind == kPoly ? &h.a : &h.p;
+      else if (bn == kTileN) map = x.kind == kGram ? &h.x[x.step & 1] : x.kind == kPoly ? &h.a : &h.x64[x.step & 1];
+      else map = x.kind == kPoly ? &h.a64 : &h.x64[x.step & 1];
       const int am = x.mt * kTileM + static_cast<int>(rank) * 128;
-      const int bn = x.nt * j.bn + static_cast<int>(rank) * (j.bn / 2);
-      const int boxes = applies(KIND) ? j.b_boxes : 1;
-      for (int kb = 0; kb < j.kb; ++kb, ++issued) {
+      const int b0 = x.nt * bn + static_cast<int>(rank) * (bn / 2);
+      const bool single = parts.a == 1;                 // then B is too: two blocks of K a stage
+      const int z0 = x.matrix, z1 = h.matrices + x.matrix;
+      const bool boxes2 = b_mn && bn == kTileN;
+      const uint32_t block_tx = 2 * (parts.a * kSlotBytes + parts.b * b_bytes(h, x));
+      for (int kb = 0; kb < x.kb; kb += single ? 2 : 1, ++issued) {
         ok = wait_all(empty(s), phase);
         if (!ok) break;
+        const bool both = single && kb + 1 < x.kb;
         const uint32_t bar = in_cta(full(s), 0);
-        const uint32_t sa = ring + s * stage_bytes, sb = sa + PA * kSlotBytes;
+        const uint32_t sa = ring + s * kStageBytes, sb = sa + 2 * kSlotBytes;
         const int k = kb * kTileK;
         if (lead) {
-          if (rank == 0) bar_expect(full(s), j.stage_tx);
-          if (!(g.stall && pair == 0 && issued == 0)) {
-#pragma unroll
-            for (int p = 0; p < PA; ++p)
-              tma_load3(sa + p * kSlotBytes, ma, k, am, p * j.matrices + x.matrix, bar);
-          }
-#pragma unroll
-          for (int p = 0; p < PB; ++p) {
-            const uint32_t to = sb + p * kSlotBytes;
-            const int z = p * j.matrices + x.matrix;
-            if (applies(KIND)) {
-              // K is the row index of X: boxes of 64 columns
-              tma_load3(to, mb, bn, k, z, bar);
-              if (boxes > 1) tma_load3(to + 8192, mb, bn + 64, k, z, bar);
-            } else {
-              tma_load3(to, mb, k, bn, z, bar);
+          if (first) {
+            if (rank == 0) bar_expect(full(s), both ? 2 * block_tx : block_tx);
+            if (!(g.stall && blockIdx.x < 2 && issued == 0)) {
+              tma_load3(sa, map, k, am, z0, bar);
+              if (parts.a > 1) tma_load3(sa + kSlotBytes, map, k, am, z1, bar);
+              if (both) tma_load3(sa + kSlotBytes, map, k + kTileK, am, z0, bar);
             }
+          } else if (b_mn) {
+            // K is the row index of X: boxes of 64 columns
+            tma_load3(sb, map, b0, k, z0, bar);
+            if (boxes2) tma_load3(sb + 8192, map, b0 + 64, k, z0, bar);
+            if (parts.b > 1 || both) {
+              const int k1 = both ? k + kTileK : k, z = both ? z0 : z1;
+              tma_load3(sb + kSlotBytes, map, b0, k1, z, bar);
+              if (boxes2) tma_load3(sb + kSlotBytes + 8192, map, b0 + 64, k1, z, bar);
+            }
+          } else {
+            tma_load3(sb, map, k, b0, z0, bar);
+            if (parts.b > 1) tma_load3(sb + kSlotBytes, map, k, b0, z1, bar);
+            if (both) tma_load3(sb + kSlotBytes, map, k + kTileK, b0, z0, bar);
           }
         }
         __syncwarp();
-        if (++s == stages) {
+        if (++s == kStages) {
           s = 0;
           phase ^= 1;
         }
       }
+      if (!ok) break;
     }
     if (!ok && lead) failed = 1;
   } else if (warp == 1) {
     if (rank == 0) {
-      int s = 0, i = 0;
+      int s = 0;
       uint32_t phase = 0;
-      for (int t = pair; ok; t += pairs, ++i) {
-        const Tile x = locate<KIND>(g, t);
-        if (x.job < 0) break;
-        const Job& j = g.job[x.job];
-        constexpr bool b_mn = applies(KIND);
-        const uint32_t idesc = instr_desc(false, false, b_mn, kTileM, j.bn);
+      for (int i = 0;; ++i) {
+        const Tile x = tile_of(i);
+        if (!ok || x.kind < 0) break;
+        const Parts parts = parts_of(g, x);
+        const bool b_mn = x.kind == kApply;
+        const uint32_t idesc = instr_desc(false, false, b_mn, kTileM, g.shape[x.shape].bn[x.kind]);
         const uint64_t a_step = 32 >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
-        const uint64_t a0 = operand_desc(ring, 0), b0 = operand_desc(ring + PA * kSlotBytes, b_mn ? 8192 : 0);
-        constexpr uint64_t kPart = kSlotBytes >> 4;
+        const uint64_t a0 = operand_desc(ring, 0), b0 = operand_desc(ring + 2 * kSlotBytes, b_mn ? 8192 : 0);
+        constexpr uint64_t kNext = kSlotBytes >> 4;
         const int a = i & 1;
         ok = wait_all(taken(a), ((i >> 1) & 1) ^ 1);
         if (!ok) break;
         fence_after();
         const uint32_t d = tmem + a * kTileN;
-        for (int kb = 0; kb < j.kb; ++kb) {
-          ok = wait_all(full(s), phase);
-          if (!ok) break;
-          fence_after();
-          const uint64_t da = a0 + s * (stage_bytes >> 4), db = b0 + s * (stage_bytes >> 4);
-          if (lead) {
-            // of two parts each, the product of the low ones is left out: 2^-22 of the whole
+        // the tile's blocks of K: PA and PB parts (one each: two blocks a stage), known here for the instructions to
+        // follow one another closely
+        auto run = [&](auto pa, auto pb) {
+          constexpr int PA = decltype(pa)::value, PB = decltype(pb)::value;
+          for (int kb = 0; kb < x.kb; kb += PA == 1 ? 2 : 1) {
+            ok = wait_all(full(s), phase);
+            if (!ok) break;
+            fence_after();
+            const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
+            if (lead) {
+              if (PA == 1) {
 #pragma unroll
-            for (int q = 0; q < kTileK / 16; ++q) {
-              mma(d, da + q * a_step, db + q * b_step, idesc, kb > 0 || q > 0);
-              if (PA > 1) mma(d, da + kPart + q * a_step, db + q * b_step, idesc, true);
-              if (PB > 1) mma(d, da + q * a_step, db + kPart + q * b_step, idesc, true);
+                for (int q = 0; q < kTileK / 16; ++q) mma(d, da + q * a_step, db + q * b_step, idesc, kb > 0 || q > 0);
+                if (kb + 1 < x.kb) {
+#pragma unroll
+                  for (int q = 0; q < kTileK / 16; ++q)
+                    mma(d, da + kNext + q * a_step, db + kNext + q * b_step, idesc, true);
+                }
+              } else {
+                // of two parts each, the product of the low ones is left out: 2^-22 of the whole
+#pragma unroll
+                for (int q = 0; q < kTileK / 16; ++q) {
+                  mma(d, da + q * a_step, db + q * b_step, idesc, kb > 0 || q > 0);
+                  mma(d, da + kNext + q * a_step, db + q * b_step, idesc, true);
+                  if (PB > 1) mma(d, da + q * a_step, db + kNext + q * b_step, idesc, true);
+                }
+              }
+              mma_commit(empty(s));
             }
-            mma_commit(empty(s));
+            __syncwarp();
+            if (++s == kStages) {
+              s = 0;
+              phase ^= 1;
+            }
           }
-          __syncwarp();
-          if (++s == stages) {
-            s = 0;
-            phase ^= 1;
-          }
-        }
+        };
+        using One = std::integral_constant<int, 1>;
+        using Two = std::integral_constant<int, 2>;
+        if (parts.a == 1) run(One{}, One{});
+        else if (parts.b == 1) run(Two{}, One{});
+        else run(Two{}, Two{});
         if (!ok) break;
         if (lead) mma_commit(done(a));
         __syncwarp();
@@ -425,40 +570,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm
     }
   } else if (warp >= 4) {
     const int quad = warp & 3, half = (warp - 4) >> 2;
-    const bool lost = KIND > kApply && *g.lost != 0;
-    const uint32_t stash = ring + kSlots * kSlotBytes + (warp - 4) * kStashBytes;
-    int i = 0;
-    for (int t = pair;; t += pairs, ++i) {
+    const uint32_t stash = ring + kStages * kStageBytes + (warp - 4) * kStashBytes;
+    int turn = 0;
+    for (int i = 0;; ++i) {
       const int a = i & 1;
-      const Tile x = locate<KIND>(g, t);
-      if (x.job < 0) break;
-      const Job& j = g.job[x.job];
+      const Tile x = tile_of(i);
+      if (!ok || x.kind < 0) break;
       const int row = x.mt * kTileM + static_cast<int>(rank) * 128 + quad * 32 + lane;
-      ok = ok && wait_all(done(a), (i >> 1) & 1);
-      if (!ok) {
-        if constexpr (KIND == kLast) {
-          // this tile and the pair's others of the caller's matrices: no number
-          for (int c = half * 32; c < j.bn; c += 64) {
-            float none[32];
-  #pragma unroll
-            for (int k = 0; k < 32; ++k) none[k] = NAN;
-            if (row < j.M && x.nt * j.bn + c < j.N)
-              write_columns<false>(j.N, g.entries[j.first + x.matrix], g.dtype, row, x.nt * j.bn + c, none);
-          }
-          continue;
-        } else {
-          break;
-        }
-      }
+      ok = wait_all(done(a), (i >> 1) & 1);
+      if (!ok) break;
       fence_after();
-      epilogue<KIND>(g, j, x, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21), stash, row, half, lost, [&] {
+      epilogue<FINAL>(g, x, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21), stash, turn, row, half, [&] {
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(in_cta(taken(a), 0));
       });
+      // this warp's share of the tile is in memory
+      __syncwarp();
+      if (lane == 0) {
+        store_wait();
+        fence_all_async();
+        add_release(g.written + g.shape[x.shape].first + x.matrix, 1u);
+      }
     }
     if (!ok && lane == 0) failed = 1;
-    if (KIND <= kApply && lane == 0) store_wait();
+    if (lane == 0) store_wait();
   }
   __syncthreads();
   if (failed) {
@@ -468,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm
       *g.lost = 1;
       // the copies in flight land on the leader's barriers: both CTAs stay until they have
       if (rank == 0)
-        for (int k = max(0, issued - stages); k < issued; ++k) bar_wait(full(k % stages), (k / stages) & 1);
+        for (int k = max(0, issued - kStages); k < issued; ++k) bar_wait(full(k % kStages), (k / kStages) & 1);
     }
     __syncthreads();
   }
@@ -476,6 +612,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_gemm
   cluster_sync();
   fence_after();
   if (warp == 1) tmem_free(tmem, 512);
+  if (FINAL == kUpdate) return;
+  // where tiles were lost it is not known which: the last CTA to end makes every result of the launch no number
+  if (threadIdx.x == 0) {
+    __threadfence();
+    last_out = atomicAdd(g.exits, 1u) == gridDim.x - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!last_out || ld_acquire(g.lost) == 0) return;
+  for (int k = 0; k < g.entries_here; ++k) {
+    const Entry& e = g.entries[g.shape[0].first + k];
+    const int64_t count = static_cast<int64_t>(e.rows) * e.cols;
+    for (int64_t i = threadIdx.x; i < count; i += kThreads) {
+      const int64_t r = i / e.cols, at = r * e.out_stride + (i - r * e.cols);
+      if (g.dtype == ZERO_FP32) static_cast<float*>(e.out)[at] = NAN;
+      else static_cast<uint16_t*>(e.out)[at] = pack1(g.dtype, NAN);
+    }
+  }
 }
 
 // ---- the passes before the products ------------------------------------------------------
@@ -489,11 +643,11 @@ constexpr int kDirectRanks = 2;
 
 template <int BYTES>
 __global__ void __launch_bounds__(kPassThreads) copy_table(const __grid_constant__ TablePart<BYTES> part, int words,
-                                                           uint64_t* to, unsigned int* lost) {
+                                                           uint64_t* to, unsigned int* counters, int n_counters) {
   allow_next();
   await_previous();
   for (int k = threadIdx.x; k < words; k += kPassThreads) to[k] = reinterpret_cast<const uint64_t*>(part.data)[k];
-  if (threadIdx.x == 0) *lost = 0;
+  for (int k = threadIdx.x; k < n_counters; k += kPassThreads) counters[k] = 0;
 }
 
 // The entry that tile t belongs to, found by a whole warp: 32 of the entries
@@ -647,7 +801,10 @@ struct Plan {
   std::vector<Group> groups;
   std::vector<int64_t> small;  // the matrices that one cluster of CTAs takes whole
   int64_t count = 0, tiles = 0;
-  int64_t table, table_words, norms, part, mean, total;
+  int64_t table, table_words, counters, norms, part, mean, total;
+  // tiles lost, then for each launch its tiles taken and CTAs ended, then for each matrix its tiles written
+  int64_t launches() const { return ceil_div(static_cast<int64_t>(groups.size()), kMaxGroups); }
+  int64_t counter_words() const { return 1 + 2 * launches() + count; }
 };
 
 int64_t pass_tiles(int64_t rows, int64_t cols) { return ceil_div(rows, kPassRows) * ceil_div(cols, kPassCols); }
@@ -684,7 +841,8 @@ int make_plan(Plan& plan, int64_t n_matrices, const int64_t* rows, const int64_t
             [](const Group& a, const Group& b) { return a.n != b.n ? a.n > b.n : a.m > b.m; });
   plan.table = kStatusBytes;
   plan.table_words = plan.count * (static_cast<int64_t>(sizeof(Entry)) / 8 + (muon ? W : 0));
-  plan.norms = plan.table + round_up(plan.table_words * 8, 256);
+  plan.counters = plan.table + round_up(plan.table_words * 8, 256);
+  plan.norms = plan.counters + round_up(plan.counter_words() * 4, 256);
   plan.part = plan.norms + round_up(plan.count * static_cast<int64_t>(sizeof(Norm)), 256);
   plan.mean = plan.part + round_up((kMostPassBlocks + plan.count) * 8, 256);
   int64_t at = plan.mean + (muon && W > kDirectRanks ? round_up(numel * 4, 256) : 0);
@@ -723,76 +881,34 @@ int make_map3(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, in
   return r == CUDA_SUCCESS ? ZERO_OK : fail(ZERO_E_CUDA, "encoding a tensor map failed (%d)", static_cast<int>(r));
 }
 
-// Cuts one group's product into tiles.
-void cut(Job& j, int kind, int64_t M, int64_t N, int64_t K, int matrices, int parts_a, int parts_b, int bn) {
-  j.matrices = matrices;
-  j.M = static_cast<int>(M);
-  j.N = static_cast<int>(N);
-  j.kb = static_cast<int>(ceil_div(K, kTileK));
-  j.bn = bn;
-  j.m_tiles = static_cast<int>(ceil_div(M, kTileM));
-  j.n_tiles = static_cast<int>(ceil_div(N, bn));
-  if (symmetric(kind)) {
-    j.per_matrix = 0;
-    for (int mt = 0; mt < j.m_tiles; ++mt) j.per_matrix += tiles_of_row(mt, bn, j.n_tiles);
-  } else {
-    j.per_matrix = j.m_tiles * j.n_tiles;
-  }
-  j.tiles = j.per_matrix * matrices;
-  j.b_boxes = static_cast<int>(ceil_div(bn / 2, 64));
-  const int b_bytes = applies(kind) ? j.b_boxes * 8192 : bn / 2 * kTileK * 2;
-  j.stage_tx = static_cast<uint32_t>(2 * (parts_a * kSlotBytes + parts_b * b_bytes));
+// Tiles of one matrix's product.
+int tiles_of(int kind, int64_t m, int64_t n, int bn) {
+  const int m_tiles = static_cast<int>(ceil_div(m, kTileM)), n_tiles = static_cast<int>(ceil_div(kind == kApply ? n : m, bn));
+  if (kind == kApply) return m_tiles * n_tiles;
+  int t = 0;
+  for (int mt = 0; mt < m_tiles; ++mt) t += tiles_of_row(mt, bn, n_tiles);
+  return t;
 }
 
-// The width of the tiles of one group's product, a divisor of 256.  A block of K
-// takes 2 bn cycles for each product of parts, or the time its operands take to
-// load; a tile has some 2000 cycles besides.
-int width_of(int kind, int64_t M, int64_t N, int64_t K, int matrices, int parts_a, int parts_b) {
-  const int products = parts_a + parts_b - 1;
+// The width of a product's tiles.  A block of K takes 2 bn cycles for each of
+// the products of parts, or the time its operands take to load (64 bytes a
+// cycle); a tile has some 2000 cycles besides, and the tiles of a product that
+// are one more than the pairs take as long as two each.
+int width_of(int kind, int64_t m, int64_t n, int matrices, bool fine) {
+  const int products = fine ? 3 : 1, parts = fine ? 2 : 1;
+  const int64_t kb = ceil_div(kind == kGram ? n : m, kTileK);
   int best = kTileN;
-  int64_t least = INT64_MAX;
-  for (int bn = kTileN; bn >= 32; bn /= 2) {
-    Job j;
-    cut(j, kind, M, N, K, matrices, parts_a, parts_b, bn);
-    const int64_t block = std::max<int64_t>(2 * bn * products, j.stage_tx / 128);
-    const int64_t cost = ceil_div(j.tiles, kPairs) * (j.kb * block + 2000);
-    if (cost < least) {
+  double least = 0;
+  for (int bn : {256, 128}) {
+    const double tiles = static_cast<double>(tiles_of(kind, m, n, bn)) * matrices;
+    const double block = std::max<double>(2 * bn * products, (128 + bn / 2) * kTileK * 2 * parts / 64);
+    const double cost = (kb * block + 2000) * (matrices > 1 ? std::max(1.0, tiles / kPairs) : std::ceil(tiles / kPairs));
+    if (bn == kTileN || cost < least) {
       least = cost;
       best = bn;
     }
   }
   return best;
-}
-
-template <int KIND, int PA, int PB>
-int launch_products(GemmArgs& g, cudaStream_t s, bool& stall) {
-  g.stall = std::exchange(stall, false);
-  const auto fn = ns_gemm<KIND, PA, PB>;
-  ZERO_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem));
-  int64_t tiles = 0;
-  for (int k = 0; k < g.jobs; ++k) tiles += g.job[k].tiles;
-  const int pairs = static_cast<int>(std::min({std::max<int64_t>(1, sm_count() / 2), kPairs, tiles}));
-  ZERO_CUDA(launch_chained(fn, dim3(2 * pairs), kThreads, kGemmSmem, s, g));
-  return ZERO_OK;
-}
-
-template <int KIND>
-int launch_parts(int parts_a, int parts_b, GemmArgs& g, cudaStream_t s, bool& stall) {
-  if (parts_a == 1) return launch_products<KIND, 1, 1>(g, s, stall);
-  if constexpr (KIND == kApply || KIND == kLast) {   // the first X of a 16-bit input
-    if (parts_b == 1) return launch_products<KIND, 2, 1>(g, s, stall);
-  }
-  return launch_products<KIND, 2, 2>(g, s, stall);
-}
-
-int launch_kind(int kind, int parts_a, int parts_b, GemmArgs& g, cudaStream_t s, bool& stall) {
-  switch (kind) {
-    case kGram: return launch_parts<kGram>(parts_a, parts_b, g, s, stall);
-    case kPoly: return launch_parts<kPoly>(parts_a, parts_b, g, s, stall);
-    case kApply: return launch_parts<kApply>(parts_a, parts_b, g, s, stall);
-    case kLast: return launch_parts<kLast>(parts_a, parts_b, g, s, stall);
-    default: return launch_parts<kUpdate>(parts_a, parts_b, g, s, stall);
-  }
 }
 
 struct Recurrence {
@@ -803,77 +919,86 @@ struct Recurrence {
   int dtype;                   // of what it writes
 };
 
-// The steps, over the groups from `from` on, as many as a launch takes.
+// The steps of plan.groups[from, to).
+template <int FINAL, int GROUPS>
 int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, char* ws, cudaStream_t s, bool& stall) {
-  for (int step = 0; step < r.steps; ++step) {
-    const int parts = step < r.fine ? 2 : 1, x_parts = step == 0 ? std::min(parts, r.first_parts) : parts;
-    const int next_parts = step + 1 < r.fine ? 2 : 1;
-    const bool last = step + 1 == r.steps;
-    for (int kind : {static_cast<int>(kGram), static_cast<int>(kPoly), last ? r.last : static_cast<int>(kApply)}) {
-      const int pa = kind == kGram ? x_parts : parts, pb = kind == kPoly ? parts : x_parts;
-      GemmArgs g;
-      std::memset(&g, 0, sizeof g);
-      g.dtype = r.dtype;
-      g.entries = reinterpret_cast<const Entry*>(ws + plan.table);
-      g.norms = reinterpret_cast<const Norm*>(ws + plan.norms);
-      g.failures = reinterpret_cast<unsigned int*>(ws);
-      g.lost = reinterpret_cast<unsigned int*>(ws) + 1;
-      for (size_t i = from; i < to; ++i) {
-        const Group& group = plan.groups[i];
-        const int c = static_cast<int>(group.members.size()), k = g.jobs++;
-        const int64_t m = group.m, n = group.n;
-        Job& j = g.job[k];
-        const int64_t N = applies(kind) ? n : m, K = kind == kGram ? n : m;
-        cut(j, kind, m, N, K, c, pa, pb, width_of(kind, m, N, K, c, pa, pb));
-        j.first = static_cast<int>(group.first);
-        j.use_unit = step == 0 && kind != kPoly;
-        j.a = static_cast<float>(r.coefficients[3 * step]);
-        j.b = static_cast<float>(r.coefficients[3 * step + 1]);
-        j.c = static_cast<float>(r.coefficients[3 * step + 2]);
-        char *x = ws + group.x[step & 1], *a = ws + group.a, *p = ws + group.p;
-        int rc;
-        char* out = kind == kGram ? a : kind == kPoly ? p : ws + group.x[(step & 1) ^ 1];
-        if (kind == kGram) {
-          if ((rc = make_map3(&g.map_a[k], x, m, n, group.ldx, 2 * c, 128))) return rc;
-          if ((rc = make_map3(&g.map_b[k], x, m, n, group.ldx, 2 * c, j.bn / 2))) return rc;
-        } else if (kind == kPoly) {
-          j.add = reinterpret_cast<const uint16_t*>(a);
-          j.add_two = parts > 1;
-          if ((rc = make_map3(&g.map_a[k], a, m, m, group.lda, 2 * c, 128))) return rc;
-          if ((rc = make_map3(&g.map_b[k], a, m, m, group.lda, 2 * c, j.bn / 2))) return rc;
-        } else {
-          if ((rc = make_map3(&g.map_a[k], p, m, m, group.lda, 2 * c, 128))) return rc;
-          if ((rc = make_map3(&g.map_b[k], x, m, n, group.ldx, 2 * c, 64))) return rc;
-        }
-        j.two_out = (applies(kind) ? next_parts : parts) > 1;
-        j.out_ld = applies(kind) ? group.ldx : group.lda;
-        j.out_matrix = m * j.out_ld;
-        j.out_part = c * j.out_matrix;
-        if ((rc = make_map3(&g.map_out[k], out, m, applies(kind) ? n : m, j.out_ld, 2 * c, 32, true))) return rc;
-      }
-      const int rc = launch_kind(kind, pa, pb, g, s, stall);
-      if (rc) return rc;
+  static thread_local RunArgs<GROUPS> g;
+  std::memset(&g, 0, sizeof g);
+  g.steps = r.steps;
+  g.fine = r.fine;
+  g.first_parts = r.first_parts;
+  g.dtype = r.dtype;
+  g.stall = std::exchange(stall, false);
+  g.entries = reinterpret_cast<const Entry*>(ws + plan.table);
+  g.norms = reinterpret_cast<const Norm*>(ws + plan.norms);
+  g.failures = reinterpret_cast<unsigned int*>(ws);
+  unsigned int* counters = reinterpret_cast<unsigned int*>(ws + plan.counters);
+  g.lost = counters;
+  g.next = counters + 1 + 2 * (from / kMaxGroups);
+  g.exits = g.next + 1;
+  g.written = counters + 1 + 2 * plan.launches();
+  for (int k = 0; k < 3 * r.steps; ++k) g.coefficients[k] = static_cast<float>(r.coefficients[k]);
+  for (size_t i = from; i < to; ++i) {
+    const Group& group = plan.groups[i];
+    Shape& h = g.shape[g.shapes++];
+    const int c = static_cast<int>(group.members.size());
+    const int64_t m = group.m, n = group.n;
+    h.matrices = c;
+    h.first = static_cast<int>(group.first);
+    h.m = static_cast<int>(m);
+    h.n = static_cast<int>(n);
+    g.entries_here += c;
+    for (int kind = 0; kind < 3; ++kind) {
+      h.bn[kind] = width_of(kind, m, n, c, r.fine > 0);
+      h.tiles[kind] = tiles_of(kind, m, n, h.bn[kind]);
+      const int64_t all = g.tiles[kind] + static_cast<int64_t>(c) * h.tiles[kind];
+      if (all * 3 * r.steps > INT32_MAX / 2) return fail(ZERO_E_ARG, "too many tiles");
+      g.tiles[kind] = static_cast<int>(all);
     }
+    h.gram = reinterpret_cast<const uint16_t*>(ws + group.a);
+    h.ld = group.lda;
+    h.apart = m * group.lda;
+    h.part = group.a_part();
+    int rc;
+    for (int k = 0; k < 2; ++k) {
+      if ((rc = make_map3(&h.x[k], ws + group.x[k], m, n, group.ldx, 2 * c, 128)) ||
+          (rc = make_map3(&h.x64[k], ws + group.x[k], m, n, group.ldx, 2 * c, 64)) ||
+          (rc = make_map3(&h.x_out[k], ws + group.x[k], m, n, group.ldx, 2 * c, 32, true)))
+        return rc;
+    }
+    if ((rc = make_map3(&h.a, ws + group.a, m, m, group.lda, 2 * c, 128)) ||
+        (rc = make_map3(&h.a64, ws + group.a, m, m, group.lda, 2 * c, 64)) ||
+        (rc = make_map3(&h.a_out, ws + group.a, m, m, group.lda, 2 * c, 32, true)) ||
+        (rc = make_map3(&h.p, ws + group.p, m, m, group.lda, 2 * c, 128)) ||
+        (rc = make_map3(&h.p_out, ws + group.p, m, m, group.lda, 2 * c, 32, true)))
+      return rc;
   }
+  const auto fn = ns_run<FINAL, GROUPS>;
+  ZERO_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRunSmem));
+  const int64_t most = std::max({g.tiles[0], g.tiles[1], g.tiles[2]});
+  const int pairs = static_cast<int>(std::min({std::max<int64_t>(1, sm_count() / 2), kPairs, most}));
+  ZERO_CUDA(launch_chained(fn, dim3(2 * pairs), kThreads, kRunSmem, s, g));
   return ZERO_OK;
 }
 
 template <int BYTES>
-int send_table_of(const std::vector<uint64_t>& words, char* to, unsigned int* lost, cudaStream_t s) {
+int send_table_of(const std::vector<uint64_t>& words, char* to, unsigned int* counters, int n_counters, cudaStream_t s) {
   static thread_local TablePart<BYTES> part;
   constexpr size_t kWords = BYTES / 8;
   for (size_t at = 0; at < words.size(); at += kWords) {
     const size_t count = std::min(kWords, words.size() - at);
     std::memcpy(part.data, words.data() + at, count * 8);
     ZERO_CUDA(launch_chained(copy_table<BYTES>, dim3(1), kPassThreads, 0, s, part, static_cast<int>(count),
-                             reinterpret_cast<uint64_t*>(to) + at, lost));
+                             reinterpret_cast<uint64_t*>(to) + at, counters, n_counters));
   }
   return ZERO_OK;
 }
 
-int send_table(const std::vector<uint64_t>& words, char* to, unsigned int* lost, cudaStream_t s) {
-  return words.size() * 8 <= kSmallTable ? send_table_of<kSmallTable>(words, to, lost, s)
-                                         : send_table_of<kLargeTable>(words, to, lost, s);
+int send_table(const Plan& plan, const std::vector<uint64_t>& words, char* ws, cudaStream_t s) {
+  unsigned int* counters = reinterpret_cast<unsigned int*>(ws + plan.counters);
+  const int n = static_cast<int>(plan.counter_words());
+  return words.size() * 8 <= kSmallTable ? send_table_of<kSmallTable>(words, ws + plan.table, counters, n, s)
+                                         : send_table_of<kLargeTable>(words, ws + plan.table, counters, n, s);
 }
 
 template <typename T, bool MUON>
@@ -887,8 +1012,14 @@ int launch_passes(const PassArgs& p, cudaStream_t s) {
 
 // Every group, kMaxGroups of them at a time.
 int run_all(const Plan& plan, const Recurrence& r, char* ws, cudaStream_t s, bool& stall) {
-  for (size_t from = 0; from < plan.groups.size(); from += kMaxGroups) {
-    const int rc = run_groups(plan, from, std::min(plan.groups.size(), from + kMaxGroups), r, ws, s, stall);
+  const size_t groups = plan.groups.size();
+  for (size_t from = 0; from < groups; from += kMaxGroups) {
+    const size_t to = std::min(groups, from + kMaxGroups);
+    const bool few = to - from <= kFewGroups, update = r.last == kUpdate;
+    const int rc = few ? (update ? run_groups<kUpdate, kFewGroups>(plan, from, to, r, ws, s, stall)
+                                 : run_groups<kLast, kFewGroups>(plan, from, to, r, ws, s, stall))
+                       : (update ? run_groups<kUpdate, kMaxGroups>(plan, from, to, r, ws, s, stall)
+                                 : run_groups<kLast, kMaxGroups>(plan, from, to, r, ws, s, stall));
     if (rc) return rc;
   }
   return ZERO_OK;
@@ -1001,8 +1132,7 @@ extern "C" int zero_orthogonalize(int64_t n_matrices, const int64_t* rows, const
       place(e, g, static_cast<int64_t>(k), ws);
       std::memcpy(&words[(g.first + k) * kEntryWords], &e, sizeof e);
     }
-  unsigned int* lost = reinterpret_cast<unsigned int*>(ws) + 1;
-  if ((rc = send_table(words, ws + plan.table, lost, s))) return rc;
+  if ((rc = send_table(plan, words, ws, s))) return rc;
   PassArgs p;
   std::memset(&p, 0, sizeof p);
   p.entries = reinterpret_cast<const Entry*>(ws + plan.table);
@@ -1107,8 +1237,7 @@ extern "C" int zero_muon_step(int W, int64_t n_matrices, const int64_t* rows, co
       place(e, g, static_cast<int64_t>(k), ws);
       std::memcpy(&words[to * kEntryWords], &e, sizeof e);
     }
-  unsigned int* lost = reinterpret_cast<unsigned int*>(ws) + 1;
-  if ((rc = send_table(words, ws + plan.table, lost, s))) return rc;
+  if ((rc = send_table(plan, words, ws, s))) return rc;
   PassArgs p;
   std::memset(&p, 0, sizeof p);
   p.entries = reinterpret_cast<const Entry*>(ws + plan.table);

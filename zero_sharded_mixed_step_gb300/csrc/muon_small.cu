@@ -115,8 +115,6 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
   return r;
 }
-// Generic writes, to any CTA's shared memory, before what the tensor cores read from there.
-__device__ __forceinline__ void fence_all_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 __device__ __forceinline__ void meet_cluster() {
   __syncwarp();
