@@ -76,15 +76,15 @@ constexpr int kTileM = 256;          // rows of a tile: 128 in each CTA of the p
 constexpr int kTileN = 256;          // most columns of a tile
 constexpr int kTileK = 64;
 constexpr int kSlotBytes = 128 * kTileK * 2;     // one part of one operand's half tile in one CTA
-// A stage of the operands' ring: of two parts, A's and B's parts of one block of
-// K; of one part, A and B of two blocks
-constexpr int kStages = 3, kStageBytes = 4 * kSlotBytes;
+// A stage of the operands' ring: one part of A and of B for one block of K.  A
+// block in two parts takes two stages, the high parts first.
+constexpr int kStages = 6, kStageBytes = 2 * kSlotBytes;
 // warp 0 loads A (and in the leader takes the tiles), warp 3 loads B, warp 1
 // issues the products, warps 4-11 are the epilogue
 constexpr int kThreads = 384;
 constexpr int kEpilogueWarps = 8;
 constexpr int kQueue = 4;            // tiles on their way through a pair
-constexpr int kStashBytes = 4096;    // of an epilogue warp: two blocks of 32 x 32 on their way out
+constexpr int kStashBytes = 4096;    // of an epilogue warp: two mirrored blocks of 32 x 32 on their way out
 constexpr int kRunSmem = kStages * kStageBytes + kEpilogueWarps * kStashBytes + 1024;
 constexpr int kFewGroups = 3, kMaxGroups = 12;       // shapes of one launch
 constexpr int64_t kPairs = 76;       // pairs of CTAs among GB300's 152 SMs
@@ -95,13 +95,14 @@ enum Kind : int { kGram, kPoly, kApply, kLast, kUpdate };
 struct Shape {
   CUtensorMap x[2], a, p;            // loads in boxes of 128 rows x 64
   CUtensorMap x64[2], a64;           // of 64 x 64
-  CUtensorMap x_out[2], a_out, p_out;   // stores of 32 x 32
+  CUtensorMap x32[2], a32;           // of 32 x 64
+  CUtensorMap a_out, p_out;          // stores of 32 x 32
   int matrices, first;               // how many, the first one's entry
   int m, n;
-  int bn[3];                         // columns of a tile of each kind: 128 or 256
+  int bn[3];                         // columns of a tile of each kind: 64, 128 or 256
   int tiles[3];                      // of one matrix
-  const uint16_t* gram;              // A
-  int64_t ld, apart, part;           // of A: rows, matrices, parts
+  uint16_t *x_at[2], *a_at, *p_at;
+  int64_t ldx, lda, apart_x, apart_a, part_x, part_a;    // rows, matrices, parts
 };
 
 template <int GROUPS>
@@ -186,23 +187,17 @@ __device__ __forceinline__ Parts parts_of(const RunArgs<GROUPS>& g, const Tile& 
   return {x.kind == kGram ? of_x : parts, x.kind == kPoly ? parts : of_x};
 }
 
-// Bytes of a half tile of B for one CTA: rows of K-major, or boxes of 64 columns.
-__device__ __forceinline__ uint32_t b_bytes(const Shape& h, const Tile& x) { return h.bn[x.kind] / 2 * kTileK * 2; }
+// Bytes of a half tile of B for one CTA: rows of K-major, or whole boxes of 64 columns.
+__device__ __forceinline__ uint32_t b_bytes(const Shape& h, const Tile& x) {
+  const int half = h.bn[x.kind] / 2;
+  return (x.kind == kApply ? (half + 63) / 64 * 64 : half) * kTileK * 2;
+}
 
 // ---- the epilogues -------------------------------------------------------------------
 
-// Blocks of 32 x 32 values go to memory through this warp's part of shared
-// memory and a TMA store each, rows of 64 bytes in the 64-byte swizzle: from
-// registers a block's mirror image would take 32 stores of 64 bytes.
-__device__ __forceinline__ void put_block(uint32_t at, int lane, const uint4 (&w)[4]) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)), "r"(w[k].x),
-                 "r"(w[k].y), "r"(w[k].z), "r"(w[k].w)
-                 : "memory");
-}
-
-// The same with rows and columns exchanged: lanes are columns.
+// A block's mirror image goes to memory through this warp's part of shared
+// memory and a TMA store, rows of 64 bytes in the 64-byte swizzle: from registers
+// it would take 32 stores of 64 bytes.  Here lanes are columns.
 __device__ __forceinline__ void put_turned(uint32_t at, int lane, const uint4 (&w)[4]) {
 #pragma unroll
   for (int k = 0; k < 32; ++k) {
@@ -214,30 +209,13 @@ __device__ __forceinline__ void put_turned(uint32_t at, int lane, const uint4 (&
   }
 }
 
-// One block on its way: the two places take turns, so that a block is put into
-// one while the other's is read.
-__device__ __forceinline__ void send_block(const CUtensorMap* map, uint32_t stash, int& turn, int x, int y, int z,
-                                           const uint4 (&w)[4], bool turned) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t to = stash + (turn & 1) * 2048;
-  ++turn;
-  if (lane == 0) store_wait_read_but_one();
-  __syncwarp();
-  if (turned) put_turned(to, lane, w);
-  else put_block(to, lane, w);
-  fence_async();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store3(map, to, x, y, z);
-    store_commit();
-  }
-}
-
-// The warp's block of 32 rows from row0 and 32 columns from col0, v holding
-// this lane's row, in one or two parts; with `mirror` its mirror image too.
-__device__ __forceinline__ void store_block(const Shape& h, int rows, int cols, const CUtensorMap* map, uint32_t stash,
-                                            int& turn, int matrix, int row0, int col0, const float (&v)[32], bool two,
-                                            bool mirror) {
+// 32 columns from col0 of this thread's row, v, in one or two parts, rows of
+// multiples of 16 values from a 32-byte boundary; with `map` their warp's block's
+// mirror image too, whose rows begin at col0.
+__device__ __forceinline__ void store_block(uint16_t* out, int64_t ld, int64_t part, int rows, int cols, int row, int col0,
+                                            const float (&v)[32], bool two, const CUtensorMap* map, int z, int z_low,
+                                            uint32_t stash) {
+  const int lane = threadIdx.x & 31, row0 = row - lane;
   if (row0 >= rows || col0 >= cols) return;
   uint4 hi[4], lo[4];
 #pragma unroll
@@ -247,11 +225,26 @@ __device__ __forceinline__ void store_block(const Shape& h, int rows, int cols, 
     for (int q = 0; q < 8; ++q) w[q] = v[8 * k + q];
     split8(w, hi[k], lo[k]);
   }
-  send_block(map, stash, turn, col0, row0, matrix, hi, false);
-  if (two) send_block(map, stash, turn, col0, row0, h.matrices + matrix, lo, false);
-  if (mirror) {
-    send_block(map, stash, turn, row0, col0, matrix, hi, true);
-    if (two) send_block(map, stash, turn, row0, col0, h.matrices + matrix, lo, true);
+  if (row < rows) {
+    uint16_t* to = out + row * ld + col0;
+    st_32B_words(to, hi[0], hi[1]);
+    if (two) st_32B_words(to + part, lo[0], lo[1]);
+    if (col0 + 16 < cols) {
+      st_32B_words(to + 16, hi[2], hi[3]);
+      if (two) st_32B_words(to + part + 16, lo[2], lo[3]);
+    }
+  }
+  if (map == nullptr) return;
+  if (lane == 0) store_wait_read();
+  __syncwarp();
+  put_turned(stash, lane, hi);
+  if (two) put_turned(stash + 2048, lane, lo);
+  fence_async();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store3(map, stash, row0, col0, z);
+    if (two) tma_store3(map, stash + 2048, row0, col0, z_low);
+    store_commit();
   }
 }
 
@@ -262,67 +255,106 @@ __device__ __forceinline__ uint4 ld_fresh(const void* p) {
   return r;
 }
 
+// What the epilogue reads beside the sums for 32 columns of a row, fetched
+// before the sums are there: A's values of both parts (kPoly), or the master's.
+struct Beside {
+  uint4 w[8];
+};
+
+template <int FINAL, int GROUPS>
+__device__ __forceinline__ void fetch(const RunArgs<GROUPS>& g, const Tile& x, int row, int c, Beside& b) {
+  const Shape& h = g.shape[x.shape];
+  const int col0 = x.nt * h.bn[x.kind] + c;
+  if (x.kind == kPoly) {
+    if (row >= h.m || col0 > (row | 31) || col0 >= h.m) return;
+    // A's rows are padded to 16 values: what is read past the last column is not used
+    const uint16_t* a = h.a_at + x.matrix * h.apart_a + row * h.lda + col0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (col0 + 8 * k >= h.m) break;
+      b.w[k] = ld_fresh(a + 8 * k);
+      if (x.step < g.fine) b.w[4 + k] = ld_fresh(a + h.part_a + 8 * k);
+    }
+  } else if (FINAL == kUpdate && x.kind == kApply && x.step + 1 == g.steps) {
+    if (row >= h.m || col0 >= h.n) return;
+    read_master(g.entries[h.first + x.matrix], h.n, row, col0, b.w);
+  }
+}
+
+// This thread's row of an accumulator, 32 columns at a time from `first` in
+// steps of 64; `release` runs when the last ones are in registers.
+template <typename F, typename R>
+__device__ __forceinline__ void each_32(uint32_t tmem, int first, int bn, F f, R release) {
+  if (first >= bn) release();
+#pragma unroll 1
+  for (int c = first; c < bn; c += 64) {
+    float v[32];
+    tmem_ld32(tmem + c, v);
+    tmem_ld_wait(v);
+    if (c + 64 >= bn) release();
+    f(c, v);
+  }
+}
+
 template <int FINAL, int GROUPS, typename R>
 __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x, uint32_t tmem, uint32_t stash,
-                                         int& turn, int row, int half, R release) {
+                                         Beside& b, int row, int half, R release) {
   const Shape& h = g.shape[x.shape];
   const int bn = h.bn[x.kind], n0 = x.nt * bn, row0 = row - static_cast<int>(threadIdx.x & 31);
-  const int which = h.first + x.matrix;
+  const int which = h.first + x.matrix, z = x.matrix, z_low = h.matrices + x.matrix;
   const float unit = x.step == 0 ? g.norms[which].unit : 1.f;     // what the first X lacks of the norm
   const bool two = x.step < g.fine;
   if (x.kind == kGram) {
     const float scale = unit * unit * (kScaleA / (kScaleX * kScaleX));
-    for_columns(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
+    each_32(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
       if (n0 + c > row0) return;
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= scale;
-      store_block(h, h.m, h.m, &h.a_out, stash, turn, x.matrix, row0, n0 + c, v, two, n0 + c < row0);
+      store_block(h.a_at + x.matrix * h.apart_a, h.lda, h.part_a, h.m, h.m, row, n0 + c, v, two,
+                  n0 + c < row0 ? &h.a_out : nullptr, z, z_low, stash);
     }, release);
   } else if (x.kind == kPoly) {
-    const uint16_t* add = h.gram + x.matrix * h.apart + row * h.ld;
     const float a = g.coefficients[3 * x.step] * kScaleP, once = g.coefficients[3 * x.step + 1] * (kScaleP / kScaleA);
     const float square = g.coefficients[3 * x.step + 2] * (kScaleP / (kScaleA * kScaleA));
-    for_columns_plain(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
+    each_32(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
       const int col0 = n0 + c;
       if (col0 > row0) return;
-      // A's rows are padded to 16 values: what is read past the last column is not used
-      uint4 hi[4] = {}, lo[4] = {};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (row >= h.m || col0 + 8 * k >= h.m) continue;
-        hi[k] = ld_fresh(add + col0 + 8 * k);
-        if (two) lo[k] = ld_fresh(add + h.part + col0 + 8 * k);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float u[8], l[8];
-        Fmt<__half>::unpack8(hi[k], u);
-        Fmt<__half>::unpack8(lo[k], l);
+        float u[8], l[8] = {};
+        Fmt<__half>::unpack8(b.w[k], u);
+        if (two) Fmt<__half>::unpack8(b.w[4 + k], l);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           v[8 * k + q] = fmaf(once, u[q] + l[q], square * v[8 * k + q]);
           if (row == col0 + 8 * k + q) v[8 * k + q] += a;
         }
       }
-      store_block(h, h.m, h.m, &h.p_out, stash, turn, x.matrix, row0, col0, v, two, col0 < row0);
+      if (c + 64 < bn) fetch<FINAL>(g, x, row, c + 64, b);
+      store_block(h.p_at + x.matrix * h.apart_a, h.lda, h.part_a, h.m, h.m, row, col0, v, two,
+                  col0 < row0 ? &h.p_out : nullptr, z, z_low, stash);
     }, release);
   } else if (x.step + 1 < g.steps) {
     const float scale = unit / kScaleP;
-    for_columns(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
+    each_32(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= scale;
-      store_block(h, h.m, h.n, &h.x_out[(x.step & 1) ^ 1], stash, turn, x.matrix, row0, n0 + c, v, x.step + 1 < g.fine,
-                  false);
+      store_block(h.x_at[(x.step & 1) ^ 1] + x.matrix * h.apart_x, h.ldx, h.part_x, h.m, h.n, row, n0 + c, v,
+                  x.step + 1 < g.fine, nullptr, 0, 0, stash);
     }, release);
   } else {
     const Entry& e = g.entries[which];
     const bool finite = g.norms[which].finite;
     const float scale = finite ? unit / (kScaleP * kScaleX) : NAN;
-    for_columns_plain(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
+    each_32(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
       // a norm that is not finite leaves the state as it was
       if (row >= h.m || n0 + c >= h.n || (FINAL == kUpdate && !finite)) return;
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= scale;
+      if (FINAL == kUpdate) {
+        step_master(e, b.w, v);
+        if (c + 64 < bn) fetch<FINAL>(g, x, row, c + 64, b);
+      }
       write_columns<FINAL == kUpdate>(h.n, e, g.dtype, row, n0 + c, v);
     }, release);
   }
@@ -401,15 +433,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
     return x;
   };
   // The next tile: taken from the counter, waited for, and told to the others.
+  unsigned taken_early = 0;
+  bool has_early = false;
+  auto take_early = [&] {
+    if (lead) taken_early = atomicAdd(g.next, 1u);
+    has_early = true;
+  };
   auto take_tile = [&](int i) {
     const int q = i % kQueue;
     Tile x{};
     x.kind = -1;
     ok = wait_all(heard(q), ((i / kQueue) & 1) ^ 1);
     if (!ok) return x;
-    unsigned t = 0, before = 0;
-    if (lead) t = atomicAdd(g.next, 1u);
-    t = __reduce_max_sync(0xffffffffu, lead ? t : 0u);
+    unsigned before = 0;
+    if (!has_early) take_early();
+    has_early = false;
+    const unsigned t = __reduce_max_sync(0xffffffffu, lead ? taken_early : 0u);
     x = locate(g, t, before);
     if (x.kind >= 0 && before > 0) {
       const unsigned* p = g.written + g.shape[x.shape].first + x.matrix;
@@ -451,49 +490,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
       const bool b_mn = x.kind == kApply;
       const CUtensorMap* map;
       if (first) map = x.kind == kGram ? &h.x[x.step & 1] : x.kind == kPoly ? &h.a : &h.p;
-      else if (bn == kTileN) map = x.kind == kGram ? &h.x[x.step & 1] : x.kind == kPoly ? &h.a : &h.x64[x.step & 1];
-      else map = x.kind == kPoly ? &h.a64 : &h.x64[x.step & 1];
+      else if (b_mn) map = &h.x64[x.step & 1];
+      else if (x.kind == kGram) map = bn == 256 ? &h.x[x.step & 1] : bn == 128 ? &h.x64[x.step & 1] : &h.x32[x.step & 1];
+      else map = bn == 256 ? &h.a : bn == 128 ? &h.a64 : &h.a32;
       const int am = x.mt * kTileM + static_cast<int>(rank) * 128;
       const int b0 = x.nt * bn + static_cast<int>(rank) * (bn / 2);
-      const bool single = parts.a == 1;                 // then B is too: two blocks of K a stage
-      const int z0 = x.matrix, z1 = h.matrices + x.matrix;
+      const int z = x.matrix;
       const bool boxes2 = b_mn && bn == kTileN;
-      const uint32_t block_tx = 2 * (parts.a * kSlotBytes + parts.b * b_bytes(h, x));
-      for (int kb = 0; kb < x.kb; kb += single ? 2 : 1, ++issued) {
-        ok = wait_all(empty(s), phase);
-        if (!ok) break;
-        const bool both = single && kb + 1 < x.kb;
-        const uint32_t bar = in_cta(full(s), 0);
-        const uint32_t sa = ring + s * kStageBytes, sb = sa + 2 * kSlotBytes;
-        const int k = kb * kTileK;
-        if (lead) {
-          if (first) {
-            if (rank == 0) bar_expect(full(s), both ? 2 * block_tx : block_tx);
-            if (!(g.stall && blockIdx.x < 2 && issued == 0)) {
-              tma_load3(sa, map, k, am, z0, bar);
-              if (parts.a > 1) tma_load3(sa + kSlotBytes, map, k, am, z1, bar);
-              if (both) tma_load3(sa + kSlotBytes, map, k + kTileK, am, z0, bar);
+      const uint32_t of_b = 2 * b_bytes(h, x);
+      for (int kb = 0; kb < x.kb; ++kb) {
+        for (int part = 0; part < parts.a; ++part, ++issued) {
+          // A stage without B is none of the second warp's: it may be used, and emptied, before that warp comes by,
+          // and a wait for a phase that is two back never ends.
+          const bool with_b = part < parts.b;
+          if (first || with_b) ok = wait_all(empty(s), phase);
+          if (!ok) break;
+          const uint32_t bar = in_cta(full(s), 0);
+          const uint32_t sa = ring + s * kStageBytes, sb = sa + kSlotBytes;
+          const int k = kb * kTileK, zp = z + part * h.matrices;
+          if (lead) {
+            if (first) {
+              if (rank == 0) bar_expect(full(s), 2 * kSlotBytes + (with_b ? of_b : 0));
+              if (!(g.stall && blockIdx.x < 2 && issued == 0)) tma_load3(sa, map, k, am, zp, bar);
+            } else if (with_b) {
+              if (b_mn) {
+                // K is the row index of X: boxes of 64 columns
+                tma_load3(sb, map, b0, k, zp, bar);
+                if (boxes2) tma_load3(sb + 8192, map, b0 + 64, k, zp, bar);
+              } else {
+                tma_load3(sb, map, k, b0, zp, bar);
+              }
             }
-          } else if (b_mn) {
-            // K is the row index of X: boxes of 64 columns
-            tma_load3(sb, map, b0, k, z0, bar);
-            if (boxes2) tma_load3(sb + 8192, map, b0 + 64, k, z0, bar);
-            if (parts.b > 1 || both) {
-              const int k1 = both ? k + kTileK : k, z = both ? z0 : z1;
-              tma_load3(sb + kSlotBytes, map, b0, k1, z, bar);
-              if (boxes2) tma_load3(sb + kSlotBytes + 8192, map, b0 + 64, k1, z, bar);
-            }
-          } else {
-            tma_load3(sb, map, k, b0, z0, bar);
-            if (parts.b > 1) tma_load3(sb + kSlotBytes, map, k, b0, z1, bar);
-            if (both) tma_load3(sb + kSlotBytes, map, k + kTileK, b0, z0, bar);
+          }
+          __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
           }
         }
-        __syncwarp();
-        if (++s == kStages) {
-          s = 0;
-          phase ^= 1;
-        }
+        if (!ok) break;
+        // the next tile's number is on its way before the last loads of this one
+        if (first && rank == 0 && !has_early && kb + 4 >= x.kb) take_early();
       }
       if (!ok) break;
     }
@@ -509,40 +546,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
         const bool b_mn = x.kind == kApply;
         const uint32_t idesc = instr_desc(false, false, b_mn, kTileM, g.shape[x.shape].bn[x.kind]);
         const uint64_t a_step = 32 >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
-        const uint64_t a0 = operand_desc(ring, 0), b0 = operand_desc(ring + 2 * kSlotBytes, b_mn ? 8192 : 0);
-        constexpr uint64_t kNext = kSlotBytes >> 4;
+        const uint64_t a0 = operand_desc(ring, 0), b0 = operand_desc(ring + kSlotBytes, b_mn ? 8192 : 0);
         const int a = i & 1;
         ok = wait_all(taken(a), ((i >> 1) & 1) ^ 1);
         if (!ok) break;
         fence_after();
         const uint32_t d = tmem + a * kTileN;
-        // the tile's blocks of K: PA and PB parts (one each: two blocks a stage), known here for the instructions to
-        // follow one another closely
+        // the tile's blocks of K in PA and PB parts, known here for the instructions to follow one another closely
         auto run = [&](auto pa, auto pb) {
           constexpr int PA = decltype(pa)::value, PB = decltype(pb)::value;
-          for (int kb = 0; kb < x.kb; kb += PA == 1 ? 2 : 1) {
+          for (int kb = 0; kb < x.kb; ++kb) {
             ok = wait_all(full(s), phase);
             if (!ok) break;
             fence_after();
+            const int high = s;
             const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
             if (lead) {
-              if (PA == 1) {
 #pragma unroll
-                for (int q = 0; q < kTileK / 16; ++q) mma(d, da + q * a_step, db + q * b_step, idesc, kb > 0 || q > 0);
-                if (kb + 1 < x.kb) {
+              for (int q = 0; q < kTileK / 16; ++q) mma(d, da + q * a_step, db + q * b_step, idesc, kb > 0 || q > 0);
+              if (PA == 1) mma_commit(empty(s));
+            }
+            __syncwarp();
+            if (++s == kStages) {
+              s = 0;
+              phase ^= 1;
+            }
+            if (PA == 1) continue;
+            ok = wait_all(full(s), phase);
+            if (!ok) break;
+            fence_after();
+            const uint64_t la = a0 + s * (kStageBytes >> 4), lb = b0 + s * (kStageBytes >> 4);
+            if (lead) {
+              // of two parts each, the product of the low ones is left out: 2^-22 of the whole
 #pragma unroll
-                  for (int q = 0; q < kTileK / 16; ++q)
-                    mma(d, da + kNext + q * a_step, db + kNext + q * b_step, idesc, true);
-                }
-              } else {
-                // of two parts each, the product of the low ones is left out: 2^-22 of the whole
-#pragma unroll
-                for (int q = 0; q < kTileK / 16; ++q) {
-                  mma(d, da + q * a_step, db + q * b_step, idesc, kb > 0 || q > 0);
-                  mma(d, da + kNext + q * a_step, db + q * b_step, idesc, true);
-                  if (PB > 1) mma(d, da + q * a_step, db + kNext + q * b_step, idesc, true);
-                }
+              for (int q = 0; q < kTileK / 16; ++q) {
+                mma(d, la + q * a_step, db + q * b_step, idesc, true);
+                if (PB > 1) mma(d, da + q * a_step, lb + q * b_step, idesc, true);
               }
+              mma_commit(empty(high));
               mma_commit(empty(s));
             }
             __syncwarp();
@@ -571,16 +612,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
   } else if (warp >= 4) {
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t stash = ring + kStages * kStageBytes + (warp - 4) * kStashBytes;
-    int turn = 0;
+    Beside beside = {};
     for (int i = 0;; ++i) {
       const int a = i & 1;
       const Tile x = tile_of(i);
       if (!ok || x.kind < 0) break;
       const int row = x.mt * kTileM + static_cast<int>(rank) * 128 + quad * 32 + lane;
+      fetch<FINAL>(g, x, row, half * 32, beside);
       ok = wait_all(done(a), (i >> 1) & 1);
       if (!ok) break;
       fence_after();
-      epilogue<FINAL>(g, x, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21), stash, turn, row, half, [&] {
+      epilogue<FINAL>(g, x, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21), stash, beside, row, half, [&] {
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(in_cta(taken(a), 0));
@@ -899,7 +941,7 @@ int width_of(int kind, int64_t m, int64_t n, int matrices, bool fine) {
   const int64_t kb = ceil_div(kind == kGram ? n : m, kTileK);
   int best = kTileN;
   double least = 0;
-  for (int bn : {256, 128}) {
+  for (int bn : {256, 128, 64}) {
     const double tiles = static_cast<double>(tiles_of(kind, m, n, bn)) * matrices;
     const double block = std::max<double>(2 * bn * products, (128 + bn / 2) * kTileK * 2 * parts / 64);
     const double cost = (kb * block + 2000) * (matrices > 1 ? std::max(1.0, tiles / kPairs) : std::ceil(tiles / kPairs));
@@ -955,19 +997,25 @@ int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, ch
       if (all * 3 * r.steps > INT32_MAX / 2) return fail(ZERO_E_ARG, "too many tiles");
       g.tiles[kind] = static_cast<int>(all);
     }
-    h.gram = reinterpret_cast<const uint16_t*>(ws + group.a);
-    h.ld = group.lda;
-    h.apart = m * group.lda;
-    h.part = group.a_part();
+    h.a_at = reinterpret_cast<uint16_t*>(ws + group.a);
+    h.p_at = reinterpret_cast<uint16_t*>(ws + group.p);
+    h.ldx = group.ldx;
+    h.lda = group.lda;
+    h.apart_x = m * group.ldx;
+    h.apart_a = m * group.lda;
+    h.part_x = group.x_part();
+    h.part_a = group.a_part();
     int rc;
     for (int k = 0; k < 2; ++k) {
       if ((rc = make_map3(&h.x[k], ws + group.x[k], m, n, group.ldx, 2 * c, 128)) ||
           (rc = make_map3(&h.x64[k], ws + group.x[k], m, n, group.ldx, 2 * c, 64)) ||
-          (rc = make_map3(&h.x_out[k], ws + group.x[k], m, n, group.ldx, 2 * c, 32, true)))
+          (rc = make_map3(&h.x32[k], ws + group.x[k], m, n, group.ldx, 2 * c, 32)))
         return rc;
+      h.x_at[k] = reinterpret_cast<uint16_t*>(ws + group.x[k]);
     }
     if ((rc = make_map3(&h.a, ws + group.a, m, m, group.lda, 2 * c, 128)) ||
         (rc = make_map3(&h.a64, ws + group.a, m, m, group.lda, 2 * c, 64)) ||
+        (rc = make_map3(&h.a32, ws + group.a, m, m, group.lda, 2 * c, 32)) ||
         (rc = make_map3(&h.a_out, ws + group.a, m, m, group.lda, 2 * c, 32, true)) ||
         (rc = make_map3(&h.p, ws + group.p, m, m, group.lda, 2 * c, 128)) ||
         (rc = make_map3(&h.p_out, ws + group.p, m, m, group.lda, 2 * c, 32, true)))

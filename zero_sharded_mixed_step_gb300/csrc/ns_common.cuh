@@ -81,34 +81,50 @@ __device__ __forceinline__ uint16_t pack1(int dtype, float v) {
   return dtype == ZERO_FP16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// Columns [col0, col0 + 32) of the last product, as far as [0, columns) reaches, of this thread's row of X to the
-// caller: the result, or the master's update and its 16-bit copy.  All reads
-// come before the writes, so that they wait for memory once.
+// Where 32 columns from col0 of a row of X lie with the caller, of `columns` that X has.
+struct Where {
+  bool wide;
+  int64_t first, apart;
+  int n;
+};
+__device__ __forceinline__ Where where(const Entry& e, int64_t stride, int columns, int row, int col0) {
+  return {e.wide && !e.transposed, e.transposed ? col0 * stride + row : row * stride + col0,
+          e.transposed ? stride : 1, min(32, columns - col0)};
+}
+
+// 32 values of the master.  They are read apart from where they are used, all
+// before anything is written, so that they are waited for once or not at all.
+__device__ __forceinline__ void read_master(const Entry& e, int columns, int row, int col0, uint4 (&w)[8]) {
+  const Where at = where(e, e.cols, columns, row, col0);
+  const float* p = e.master + at.first;
+  if (at.wide) {
+#pragma unroll
+    for (int k = 0; k < 8; k += 2)
+      if (4 * k < at.n) ld_32B_words(p + 4 * k, w[k], w[k + 1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (k < at.n) (&w[k / 4].x)[k % 4] = __float_as_uint(p[k * at.apart]);
+  }
+}
+
+// The new master's values from the old ones and the last product's.
+__device__ __forceinline__ void step_master(const Entry& e, const uint4 (&w)[8], float (&v)[32]) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v[k] = fmaf(-e.step, v[k], e.keep * __uint_as_float((&w[k / 4].x)[k % 4]));
+}
+
+// Columns [col0, col0 + 32), as far as [0, columns) reaches, of this thread's row
+// of X to the caller: the last product's, or the new master's and their 16-bit
+// copy.
 template <bool UPDATE>
 __device__ __forceinline__ void write_columns(int columns, const Entry& e, int dtype, int row, int col0,
-                                              float (&v)[32]) {
+                                              const float (&v)[32]) {
   const bool fp32 = !UPDATE && dtype == ZERO_FP32;
-  const bool wide = e.wide && !e.transposed;
-  const int64_t stride = UPDATE ? e.cols : e.out_stride;
-  const int64_t first = e.transposed ? col0 * stride + row : row * stride + col0, apart = e.transposed ? stride : 1;
-  const int n = min(32, columns - col0);
-  if (UPDATE) {
-    float theta[32];
-    if (wide) {
-#pragma unroll
-      for (int k = 0; k < 32; k += 8) {
-        float w[8] = {};
-        if (k < n) dev::ld_32B(e.master + first + k, w);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) theta[k + q] = w[q];
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) theta[k] = k < n ? e.master[first + k * apart] : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] = fmaf(-e.step, v[k], e.keep * theta[k]);
-  }
+  const Where at = where(e, UPDATE ? e.cols : e.out_stride, columns, row, col0);
+  const bool wide = at.wide;
+  const int64_t first = at.first, apart = at.apart;
+  const int n = at.n;
   if (wide) {
     // multiples of 8 columns exist
 #pragma unroll
@@ -140,9 +156,9 @@ __device__ __forceinline__ void write_columns(int columns, const Entry& e, int d
 #pragma unroll
   for (int k = 0; k < 32; ++k) {
     if (k >= n) break;
-    const int64_t at = first + k * apart;
-    if (UPDATE || fp32) (UPDATE ? e.master : static_cast<float*>(e.out))[at] = v[k];
-    if (!fp32) static_cast<uint16_t*>(UPDATE ? e.p16 : e.out)[at] = pack1(dtype, v[k]);
+    const int64_t to = first + k * apart;
+    if (UPDATE || fp32) (UPDATE ? e.master : static_cast<float*>(e.out))[to] = v[k];
+    if (!fp32) static_cast<uint16_t*>(UPDATE ? e.p16 : e.out)[to] = pack1(dtype, v[k]);
   }
 }
 

@@ -129,8 +129,8 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Between the generic and the async proxy, everywhere: what others wrote through one before it is used through the other.
 __device__ __forceinline__ void fence_all_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
-// This thread's stores but the last have read their shared memory, or all are done altogether.
-__device__ __forceinline__ void store_wait_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+// This thread's stores have read their shared memory, or are done altogether.
+__device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
