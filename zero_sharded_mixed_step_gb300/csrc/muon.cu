@@ -80,11 +80,12 @@ constexpr int kSlotBytes = 128 * kTileK * 2;     // one part of one operand's ha
 // block in two parts takes two stages, the high parts first.
 constexpr int kStages = 6, kStageBytes = 2 * kSlotBytes;
 // warp 0 loads A (and in the leader takes the tiles), warp 3 loads B, warp 1
-// issues the products, warps 4-11 are the epilogue
+// issues the products, warps 4-11 are the epilogue, warp 2 says what they have
+// written
 constexpr int kThreads = 384;
 constexpr int kEpilogueWarps = 8;
 constexpr int kQueue = 4;            // tiles on their way through a pair
-constexpr int kStashBytes = 4096;    // of an epilogue warp: two mirrored blocks of 32 x 32 on their way out
+constexpr int kStashBytes = 4096;    // of an epilogue warp: two blocks of 32 x 32 to mirror
 constexpr int kRunSmem = kStages * kStageBytes + kEpilogueWarps * kStashBytes + 1024;
 constexpr int kFewGroups = 3, kMaxGroups = 12;       // shapes of one launch
 constexpr int64_t kPairs = 76;       // pairs of CTAs among GB300's 152 SMs
@@ -96,11 +97,10 @@ struct Shape {
   CUtensorMap x[2], a, p;            // loads in boxes of 128 rows x 64
   CUtensorMap x64[2], a64;           // of 64 x 64
   CUtensorMap x32[2], a32;           // of 32 x 64
-  CUtensorMap a_out, p_out;          // stores of 32 x 32
   int matrices, first;               // how many, the first one's entry
   int m, n;
-  int bn[3];                         // columns of a tile of each kind: 64, 128 or 256
-  int tiles[3];                      // of one matrix
+  int bn[2][3];                      // columns of a tile of each kind: 64, 128 or 256; of one part, of two
+  int tiles[2][3];                   // of one matrix
   uint16_t *x_at[2], *a_at, *p_at;
   int64_t ldx, lda, apart_x, apart_a, part_x, part_a;    // rows, matrices, parts
 };
@@ -109,7 +109,7 @@ template <int GROUPS>
 struct RunArgs {
   Shape shape[GROUPS];
   int shapes;
-  int tiles[3];                // of a step, by kind
+  int tiles[2][3];             // of a step, by kind
   int steps, fine, first_parts;
   int dtype;                   // kLast: of the results; kUpdate: of the 16-bit copies
   int stall;                   // testing the bounded waits: the first tile's first block of K never arrives
@@ -117,7 +117,7 @@ struct RunArgs {
   const Norm* norms;
   unsigned int* next;          // tiles taken so far (0 at the launch)
   unsigned int* exits;         // CTAs that have ended (0)
-  unsigned int* written;       // for each matrix: tiles written, counted by epilogue warp (0)
+  unsigned int* written;       // for each matrix: halves of tiles written (0)
   unsigned int* failures;      // the workspace's count of waits that gave up
   unsigned int* lost;          // set where tiles of this call were not computed (0)
   int entries_here;            // of these shapes, from shape[0].first on
@@ -128,7 +128,7 @@ struct RunArgs {
 struct alignas(16) Tile {
   int kind;                    // -1: no more
   int shape, matrix, mt;
-  int nt, step, kb, unused;    // kb: blocks of K
+  int nt, step, kb, bn;        // kb: blocks of K
 };
 
 // Tiles of a row of tiles that hold something on or below the diagonal.
@@ -141,24 +141,36 @@ __host__ __device__ inline int tiles_of_row(int mt, int bn, int n_tiles) {
 template <int GROUPS>
 __device__ __forceinline__ Tile locate(const RunArgs<GROUPS>& g, unsigned t, unsigned& before) {
   Tile x = {};
-  const unsigned each = g.tiles[0] + g.tiles[1] + g.tiles[2];
-  x.step = static_cast<int>(t / each);
+  // the fine steps first
+  int fine = 1;
+  unsigned each = g.tiles[1][0] + g.tiles[1][1] + g.tiles[1][2];
+  const unsigned in_fine = each * g.fine;
+  if (t >= in_fine) {
+    fine = 0;
+    each = g.tiles[0][0] + g.tiles[0][1] + g.tiles[0][2];
+    t -= in_fine;
+    x.step = g.fine;
+  }
+  const int further = static_cast<int>(t / each);
+  x.step += further;
   if (x.step >= g.steps) {
     x.kind = -1;
     return x;
   }
-  int r = static_cast<int>(t - x.step * each);
-  while (r >= g.tiles[x.kind]) r -= g.tiles[x.kind++];
-  while (r >= g.shape[x.shape].matrices * g.shape[x.shape].tiles[x.kind]) {
-    r -= g.shape[x.shape].matrices * g.shape[x.shape].tiles[x.kind];
+  int r = static_cast<int>(t - further * each);
+  while (r >= g.tiles[fine][x.kind]) r -= g.tiles[fine][x.kind++];
+  while (r >= g.shape[x.shape].matrices * g.shape[x.shape].tiles[fine][x.kind]) {
+    r -= g.shape[x.shape].matrices * g.shape[x.shape].tiles[fine][x.kind];
     ++x.shape;
   }
   const Shape& h = g.shape[x.shape];
-  x.matrix = static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(h.tiles[x.kind]));
-  r -= x.matrix * h.tiles[x.kind];
-  before = x.step * (h.tiles[0] + h.tiles[1] + h.tiles[2]);
-  for (int k = 0; k < x.kind; ++k) before += h.tiles[k];
-  const int bn = h.bn[x.kind];
+  const int* of_kind = h.tiles[fine];
+  x.matrix = static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(of_kind[x.kind]));
+  r -= x.matrix * of_kind[x.kind];
+  before = further * (of_kind[0] + of_kind[1] + of_kind[2]);
+  if (!fine) before += g.fine * (h.tiles[1][0] + h.tiles[1][1] + h.tiles[1][2]);
+  for (int k = 0; k < x.kind; ++k) before += of_kind[k];
+  const int bn = x.bn = h.bn[fine][x.kind];
   if (x.kind < kApply) {
     const int n_tiles = (h.m + bn - 1) / bn;
     for (;;) {
@@ -188,17 +200,18 @@ __device__ __forceinline__ Parts parts_of(const RunArgs<GROUPS>& g, const Tile& 
 }
 
 // Bytes of a half tile of B for one CTA: rows of K-major, or whole boxes of 64 columns.
-__device__ __forceinline__ uint32_t b_bytes(const Shape& h, const Tile& x) {
-  const int half = h.bn[x.kind] / 2;
+__device__ __forceinline__ uint32_t b_bytes(const Tile& x) {
+  const int half = x.bn / 2;
   return (x.kind == kApply ? (half + 63) / 64 * 64 : half) * kTileK * 2;
 }
 
 // ---- the epilogues -------------------------------------------------------------------
 
-// A block's mirror image goes to memory through this warp's part of shared
-// memory and a TMA store, rows of 64 bytes in the 64-byte swizzle: from registers
-// it would take 32 stores of 64 bytes.  Here lanes are columns.
-__device__ __forceinline__ void put_turned(uint32_t at, int lane, const uint4 (&w)[4]) {
+// A block's mirror image goes to memory by way of this warp's part of shared
+// memory, rows of 64 bytes in the 64-byte swizzle: from registers it would take
+// 32 stores of 64 bytes.  Lanes are columns of it, then rows.
+__device__ __forceinline__ void turn(uint32_t at, int lane, uint4 (&w)[4]) {
+  __syncwarp();
 #pragma unroll
   for (int k = 0; k < 32; ++k) {
     const uint32_t pair = (&w[k / 8].x)[k / 2 % 4];
@@ -207,14 +220,26 @@ __device__ __forceinline__ void put_turned(uint32_t at, int lane, const uint4 (&
                  "h"(one)
                  : "memory");
   }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[k].x), "=r"(w[k].y), "=r"(w[k].z), "=r"(w[k].w)
+                 : "r"(at + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4))
+                 : "memory");
 }
 
-// 32 columns from col0 of this thread's row, v, in one or two parts, rows of
-// multiples of 16 values from a 32-byte boundary; with `map` their warp's block's
-// mirror image too, whose rows begin at col0.
+// 32 values of a row, of which those below `cols` from col0 on count, in rows of
+// multiples of 16 values from a 32-byte boundary.
+__device__ __forceinline__ void store_row(uint16_t* to, int col0, int cols, const uint4 (&w)[4]) {
+  st_32B_words(to, w[0], w[1]);
+  if (col0 + 16 < cols) st_32B_words(to + 16, w[2], w[3]);
+}
+
+// 32 columns from col0 of this thread's row, v, in one or two parts; with
+// `mirror` their warp's block's mirror image too.
 __device__ __forceinline__ void store_block(uint16_t* out, int64_t ld, int64_t part, int rows, int cols, int row, int col0,
-                                            const float (&v)[32], bool two, const CUtensorMap* map, int z, int z_low,
-                                            uint32_t stash) {
+                                            const float (&v)[32], bool two, bool mirror, uint32_t stash) {
   const int lane = threadIdx.x & 31, row0 = row - lane;
   if (row0 >= rows || col0 >= cols) return;
   uint4 hi[4], lo[4];
@@ -227,24 +252,16 @@ __device__ __forceinline__ void store_block(uint16_t* out, int64_t ld, int64_t p
   }
   if (row < rows) {
     uint16_t* to = out + row * ld + col0;
-    st_32B_words(to, hi[0], hi[1]);
-    if (two) st_32B_words(to + part, lo[0], lo[1]);
-    if (col0 + 16 < cols) {
-      st_32B_words(to + 16, hi[2], hi[3]);
-      if (two) st_32B_words(to + part + 16, lo[2], lo[3]);
-    }
+    store_row(to, col0, cols, hi);
+    if (two) store_row(to + part, col0, cols, lo);
   }
-  if (map == nullptr) return;
-  if (lane == 0) store_wait_read();
-  __syncwarp();
-  put_turned(stash, lane, hi);
-  if (two) put_turned(stash + 2048, lane, lo);
-  fence_async();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store3(map, stash, row0, col0, z);
-    if (two) tma_store3(map, stash + 2048, row0, col0, z_low);
-    store_commit();
+  if (!mirror) return;
+  uint16_t* to = out + (col0 + lane) * ld + row0;
+  turn(stash, lane, hi);
+  if (col0 + lane < cols) store_row(to, row0, rows, hi);
+  if (two) {
+    turn(stash + 2048, lane, lo);
+    if (col0 + lane < cols) store_row(to + part, row0, rows, lo);
   }
 }
 
@@ -264,7 +281,7 @@ struct Beside {
 template <int FINAL, int GROUPS>
 __device__ __forceinline__ void fetch(const RunArgs<GROUPS>& g, const Tile& x, int row, int c, Beside& b) {
   const Shape& h = g.shape[x.shape];
-  const int col0 = x.nt * h.bn[x.kind] + c;
+  const int col0 = x.nt * x.bn + c;
   if (x.kind == kPoly) {
     if (row >= h.m || col0 > (row | 31) || col0 >= h.m) return;
     // A's rows are padded to 16 values: what is read past the last column is not used
@@ -300,8 +317,8 @@ template <int FINAL, int GROUPS, typename R>
 __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x, uint32_t tmem, uint32_t stash,
                                          Beside& b, int row, int half, R release) {
   const Shape& h = g.shape[x.shape];
-  const int bn = h.bn[x.kind], n0 = x.nt * bn, row0 = row - static_cast<int>(threadIdx.x & 31);
-  const int which = h.first + x.matrix, z = x.matrix, z_low = h.matrices + x.matrix;
+  const int bn = x.bn, n0 = x.nt * bn, row0 = row - static_cast<int>(threadIdx.x & 31);
+  const int which = h.first + x.matrix;
   const float unit = x.step == 0 ? g.norms[which].unit : 1.f;     // what the first X lacks of the norm
   const bool two = x.step < g.fine;
   if (x.kind == kGram) {
@@ -310,8 +327,8 @@ __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x
       if (n0 + c > row0) return;
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= scale;
-      store_block(h.a_at + x.matrix * h.apart_a, h.lda, h.part_a, h.m, h.m, row, n0 + c, v, two,
-                  n0 + c < row0 ? &h.a_out : nullptr, z, z_low, stash);
+      store_block(h.a_at + x.matrix * h.apart_a, h.lda, h.part_a, h.m, h.m, row, n0 + c, v, two, n0 + c < row0,
+                  stash);
     }, release);
   } else if (x.kind == kPoly) {
     const float a = g.coefficients[3 * x.step] * kScaleP, once = g.coefficients[3 * x.step + 1] * (kScaleP / kScaleA);
@@ -331,8 +348,7 @@ __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x
         }
       }
       if (c + 64 < bn) fetch<FINAL>(g, x, row, c + 64, b);
-      store_block(h.p_at + x.matrix * h.apart_a, h.lda, h.part_a, h.m, h.m, row, col0, v, two,
-                  col0 < row0 ? &h.p_out : nullptr, z, z_low, stash);
+      store_block(h.p_at + x.matrix * h.apart_a, h.lda, h.part_a, h.m, h.m, row, col0, v, two, col0 < row0, stash);
     }, release);
   } else if (x.step + 1 < g.steps) {
     const float scale = unit / kScaleP;
@@ -340,7 +356,7 @@ __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= scale;
       store_block(h.x_at[(x.step & 1) ^ 1] + x.matrix * h.apart_x, h.ldx, h.part_x, h.m, h.n, row, n0 + c, v,
-                  x.step + 1 < g.fine, nullptr, 0, 0, stash);
+                  x.step + 1 < g.fine, false, stash);
     }, release);
   } else {
     const Entry& e = g.entries[which];
@@ -375,7 +391,7 @@ __device__ __forceinline__ void add_release(unsigned* p, unsigned v) {
 template <int FINAL, int GROUPS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(const __grid_constant__ RunArgs<GROUPS> g) {
   extern __shared__ unsigned char raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kStages + 2 * kQueue + 5];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 3 * kQueue + 5];
   __shared__ Tile queue[kQueue];
   __shared__ uint32_t tmem_slot;
   __shared__ int failed, last_out;
@@ -388,6 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
   const uint32_t drained = bar0 + 8 * (2 * kStages + 4);
   auto told = [&](int q) { return bar0 + 8 * (2 * kStages + 5 + q); };             // queue[q] holds a tile
   auto heard = [&](int q) { return bar0 + 8 * (2 * kStages + 5 + kQueue + q); };   // everyone has read it
+  auto stored = [&](int q) { return bar0 + 8 * (2 * kStages + 5 + 2 * kQueue + q); };  // this CTA's half of the tile is
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
 
@@ -403,7 +420,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
     }
     for (int q = 0; q < kQueue; ++q) {
       bar_init(told(q), 1);
-      bar_init(heard(q), 4 + 2 * kEpilogueWarps);   // the loaders but the leader's first, the issuer, the epilogue
+      bar_init(heard(q), 6 + 2 * kEpilogueWarps);   // the loaders but the leader's first, the issuer, warps 2, the epilogue
+      bar_init(stored(q), kEpilogueWarps);
     }
     bar_init(drained, 1);
     failed = 0;
@@ -433,26 +451,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
     return x;
   };
   // The next tile: taken from the counter, waited for, and told to the others.
-  unsigned taken_early = 0;
-  bool has_early = false;
-  auto take_early = [&] {
-    if (lead) taken_early = atomicAdd(g.next, 1u);
-    has_early = true;
-  };
   auto take_tile = [&](int i) {
     const int q = i % kQueue;
     Tile x{};
     x.kind = -1;
     ok = wait_all(heard(q), ((i / kQueue) & 1) ^ 1);
     if (!ok) return x;
-    unsigned before = 0;
-    if (!has_early) take_early();
-    has_early = false;
-    const unsigned t = __reduce_max_sync(0xffffffffu, lead ? taken_early : 0u);
+    unsigned t = 0, before = 0;
+    if (lead) t = atomicAdd(g.next, 1u);
+    t = __reduce_max_sync(0xffffffffu, t);
     x = locate(g, t, before);
     if (x.kind >= 0 && before > 0) {
       const unsigned* p = g.written + g.shape[x.shape].first + x.matrix;
-      const unsigned want = before * 2 * kEpilogueWarps;
+      const unsigned want = before * 2;
       bool there = true;
       if (lead) {
         const long long t0 = clock64();
@@ -461,13 +472,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
       ok = __all_sync(0xffffffffu, there) != 0;
       if (!ok) return x;
     }
-    // what the others wrote through the async proxy is loaded through it
+    // what the others' threads wrote is loaded through the async proxy
     fence_all_async();
     if (lead) {
       for (uint32_t r = 0; r < 2; ++r) {
         const uint32_t at = in_cta(smem_addr(&queue[q]), r);
         st_cluster(at, x.kind, x.shape, x.matrix, x.mt);
-        st_cluster(at + 16, x.nt, x.step, x.kb, 0);
+        st_cluster(at + 16, x.nt, x.step, x.kb, x.bn);
         bar_arrive_written(in_cta(told(q), r));
       }
     }
@@ -486,7 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
       fence_all_async();
       const Shape& h = g.shape[x.shape];
       const Parts parts = parts_of(g, x);
-      const int bn = h.bn[x.kind];
+      const int bn = x.bn;
       const bool b_mn = x.kind == kApply;
       const CUtensorMap* map;
       if (first) map = x.kind == kGram ? &h.x[x.step & 1] : x.kind == kPoly ? &h.a : &h.p;
@@ -497,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
       const int b0 = x.nt * bn + static_cast<int>(rank) * (bn / 2);
       const int z = x.matrix;
       const bool boxes2 = b_mn && bn == kTileN;
-      const uint32_t of_b = 2 * b_bytes(h, x);
+      const uint32_t of_b = 2 * b_bytes(x);
       for (int kb = 0; kb < x.kb; ++kb) {
         for (int part = 0; part < parts.a; ++part, ++issued) {
           // A stage without B is none of the second warp's: it may be used, and emptied, before that warp comes by,
@@ -529,8 +540,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
           }
         }
         if (!ok) break;
-        // the next tile's number is on its way before the last loads of this one
-        if (first && rank == 0 && !has_early && kb + 4 >= x.kb) take_early();
       }
       if (!ok) break;
     }
@@ -544,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
         if (!ok || x.kind < 0) break;
         const Parts parts = parts_of(g, x);
         const bool b_mn = x.kind == kApply;
-        const uint32_t idesc = instr_desc(false, false, b_mn, kTileM, g.shape[x.shape].bn[x.kind]);
+        const uint32_t idesc = instr_desc(false, false, b_mn, kTileM, x.bn);
         const uint64_t a_step = 32 >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
         const uint64_t a0 = operand_desc(ring, 0), b0 = operand_desc(ring + kSlotBytes, b_mn ? 8192 : 0);
         const int a = i & 1;
@@ -609,6 +618,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
         bar_wait(drained, 0);
       }
     }
+  } else if (warp == 2) {
+    // A tile's stores are on their way when the epilogue is done with it; saying so takes until they have arrived.
+    for (int i = 0;; ++i) {
+      const Tile x = tile_of(i);
+      if (!ok || x.kind < 0) break;
+      ok = wait_all(stored(i % kQueue), (i / kQueue) & 1);
+      if (!ok) break;
+      if (lead) {
+        fence_all_async();
+        add_release(g.written + g.shape[x.shape].first + x.matrix, 1u);
+      }
+      __syncwarp();
+    }
+    if (!ok && lead) failed = 1;
   } else if (warp >= 4) {
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t stash = ring + kStages * kStageBytes + (warp - 4) * kStashBytes;
@@ -627,16 +650,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
         __syncwarp();
         if (lane == 0) bar_arrive(in_cta(taken(a), 0));
       });
-      // this warp's share of the tile is in memory
       __syncwarp();
-      if (lane == 0) {
-        store_wait();
-        fence_all_async();
-        add_release(g.written + g.shape[x.shape].first + x.matrix, 1u);
-      }
+      // Warps may be a tile or two apart, not as many as there are barriers: of two tiles' products, at most, some warp
+      // has not read the sums.
+      if (lane == 0) bar_arrive_own(stored(i % kQueue));
     }
     if (!ok && lane == 0) failed = 1;
-    if (lane == 0) store_wait();
   }
   __syncthreads();
   if (failed) {
@@ -908,18 +927,16 @@ int make_plan(Plan& plan, int64_t n_matrices, const int64_t* rows, const int64_t
 }
 
 // A stack of `depth` row-major fp16 matrices, in boxes of box_rows x 64 under the
-// 128-byte swizzle (out: x 32 under the 64-byte one); what lies outside a matrix
-// reads as 0.
-int make_map3(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int64_t depth, int box_rows,
-              bool out = false) {
+// 128-byte swizzle; what lies outside a matrix reads as 0.
+int make_map3(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int64_t depth, int box_rows) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(depth)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * rows * 2};
-  const cuuint32_t box[3] = {out ? 32u : kTileK, static_cast<cuuint32_t>(box_rows), 1}, ones[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {kTileK, static_cast<cuuint32_t>(box_rows), 1}, ones[3] = {1, 1, 1};
   const host::EncodeFn fn = host::encoder();
   if (!fn) return fail(ZERO_E_CUDA, "the driver offers no tensor-map encoder");
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, ones,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? ZERO_OK : fail(ZERO_E_CUDA, "encoding a tensor map failed (%d)", static_cast<int>(r));
 }
 
@@ -933,7 +950,7 @@ int tiles_of(int kind, int64_t m, int64_t n, int bn) {
 }
 
 // The width of a product's tiles.  A block of K takes 2 bn cycles for each of
-// the products of parts, or the time its operands take to load (64 bytes a
+// the products of parts, or the time its operands take to load (48 bytes a
 // cycle); a tile has some 2000 cycles besides, and the tiles of a product that
 // are one more than the pairs take as long as two each.
 int width_of(int kind, int64_t m, int64_t n, int matrices, bool fine) {
@@ -943,7 +960,7 @@ int width_of(int kind, int64_t m, int64_t n, int matrices, bool fine) {
   double least = 0;
   for (int bn : {256, 128, 64}) {
     const double tiles = static_cast<double>(tiles_of(kind, m, n, bn)) * matrices;
-    const double block = std::max<double>(2 * bn * products, (128 + bn / 2) * kTileK * 2 * parts / 64);
+    const double block = std::max<double>(2 * bn * products, (128 + bn / 2) * kTileK * 2 * parts / 48.0);
     const double cost = (kb * block + 2000) * (matrices > 1 ? std::max(1.0, tiles / kPairs) : std::ceil(tiles / kPairs));
     if (bn == kTileN || cost < least) {
       least = cost;
@@ -990,13 +1007,14 @@ int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, ch
     h.m = static_cast<int>(m);
     h.n = static_cast<int>(n);
     g.entries_here += c;
-    for (int kind = 0; kind < 3; ++kind) {
-      h.bn[kind] = width_of(kind, m, n, c, r.fine > 0);
-      h.tiles[kind] = tiles_of(kind, m, n, h.bn[kind]);
-      const int64_t all = g.tiles[kind] + static_cast<int64_t>(c) * h.tiles[kind];
-      if (all * 3 * r.steps > INT32_MAX / 2) return fail(ZERO_E_ARG, "too many tiles");
-      g.tiles[kind] = static_cast<int>(all);
-    }
+    for (int fine = 0; fine < 2; ++fine)
+      for (int kind = 0; kind < 3; ++kind) {
+        h.bn[fine][kind] = width_of(kind, m, n, c, fine);
+        h.tiles[fine][kind] = tiles_of(kind, m, n, h.bn[fine][kind]);
+        const int64_t all = g.tiles[fine][kind] + static_cast<int64_t>(c) * h.tiles[fine][kind];
+        if (all * 3 * r.steps > INT32_MAX / 2) return fail(ZERO_E_ARG, "too many tiles");
+        g.tiles[fine][kind] = static_cast<int>(all);
+      }
     h.a_at = reinterpret_cast<uint16_t*>(ws + group.a);
     h.p_at = reinterpret_cast<uint16_t*>(ws + group.p);
     h.ldx = group.ldx;
@@ -1016,15 +1034,14 @@ int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, ch
     if ((rc = make_map3(&h.a, ws + group.a, m, m, group.lda, 2 * c, 128)) ||
         (rc = make_map3(&h.a64, ws + group.a, m, m, group.lda, 2 * c, 64)) ||
         (rc = make_map3(&h.a32, ws + group.a, m, m, group.lda, 2 * c, 32)) ||
-        (rc = make_map3(&h.a_out, ws + group.a, m, m, group.lda, 2 * c, 32, true)) ||
-        (rc = make_map3(&h.p, ws + group.p, m, m, group.lda, 2 * c, 128)) ||
-        (rc = make_map3(&h.p_out, ws + group.p, m, m, group.lda, 2 * c, 32, true)))
+        (rc = make_map3(&h.p, ws + group.p, m, m, group.lda, 2 * c, 128)))
       return rc;
   }
   const auto fn = ns_run<FINAL, GROUPS>;
   ZERO_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRunSmem));
-  const int64_t most = std::max({g.tiles[0], g.tiles[1], g.tiles[2]});
-  const int pairs = static_cast<int>(std::min({std::max<int64_t>(1, sm_count() / 2), kPairs, most}));
+  int most = 1;
+  for (const auto& of : g.tiles) most = std::max({most, of[0], of[1], of[2]});
+  const int pairs = static_cast<int>(std::min({std::max<int64_t>(1, sm_count() / 2), kPairs, static_cast<int64_t>(most)}));
   ZERO_CUDA(launch_chained(fn, dim3(2 * pairs), kThreads, kRunSmem, s, g));
   return ZERO_OK;
 }
