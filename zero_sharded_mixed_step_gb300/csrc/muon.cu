@@ -15,7 +15,8 @@
 // shape (or its transpose) lie one after another in the workspace, X as m x n
 // always, so that a 3-D tensor map loads any of them.  The work is a list of
 // tiles of 256 rows, one product after another:
-//   kGram   A, of which the lower half is computed and mirrored
+//   kGram   A, the blocks of 256 x 256 on and below the diagonal; what lies
+//           above is read from there, rows and columns exchanged
 //   kPoly   A A likewise, with P formed in its epilogue
 //   kApply  P X; of the last step its epilogue writes the caller's matrix or
 //           updates the master and the 16-bit copy in place.
@@ -78,15 +79,14 @@ constexpr int kTileK = 64;
 constexpr int kSlotBytes = 128 * kTileK * 2;     // one part of one operand's half tile in one CTA
 // A stage of the operands' ring: one part of A and of B for one block of K.  A
 // block in two parts takes two stages, the high parts first.
-constexpr int kStages = 6, kStageBytes = 2 * kSlotBytes;
-// warp 0 loads A (and in the leader takes the tiles), warp 3 loads B, warp 1
-// issues the products, warps 4-11 are the epilogue, warp 2 says what they have
-// written
-constexpr int kThreads = 384;
+constexpr int kStages = 7, kStageBytes = 2 * kSlotBytes;
+// warp 0 loads A, warp 3 loads B, warp 1 issues the products, warps 4-11 are the
+// epilogue, warp 2 says what they have written, and in the leader warp 12 takes
+// the tiles
+constexpr int kThreads = 416;
 constexpr int kEpilogueWarps = 8;
 constexpr int kQueue = 4;            // tiles on their way through a pair
-constexpr int kStashBytes = 4096;    // of an epilogue warp: two blocks of 32 x 32 to mirror
-constexpr int kRunSmem = kStages * kStageBytes + kEpilogueWarps * kStashBytes + 1024;
+constexpr int kRunSmem = kStages * kStageBytes + 1024;
 constexpr int kFewGroups = 3, kMaxGroups = 12;       // shapes of one launch
 constexpr int64_t kPairs = 76;       // pairs of CTAs among GB300's 152 SMs
 
@@ -95,7 +95,7 @@ enum Kind : int { kGram, kPoly, kApply, kLast, kUpdate };
 // The matrices of one shape.
 struct Shape {
   CUtensorMap x[2], a, p;            // loads in boxes of 128 rows x 64
-  CUtensorMap x64[2], a64;           // of 64 x 64
+  CUtensorMap x64[2], a64, p64;      // of 64 x 64
   CUtensorMap x32[2], a32;           // of 32 x 64
   int matrices, first;               // how many, the first one's entry
   int m, n;
@@ -199,35 +199,22 @@ __device__ __forceinline__ Parts parts_of(const RunArgs<GROUPS>& g, const Tile& 
   return {x.kind == kGram ? of_x : parts, x.kind == kPoly ? parts : of_x};
 }
 
-// Bytes of a half tile of B for one CTA: rows of K-major, or whole boxes of 64 columns.
-__device__ __forceinline__ uint32_t b_bytes(const Tile& x) {
+// Of A and P the blocks above the diagonal are not there: block kb of K of the
+// operand whose rows begin at `row` is read with rows and columns exchanged
+// where its columns lie in a later block of 256 than its rows.
+__device__ __forceinline__ bool exchanged(int row, int kb) { return kb * kTileK / kTileM > row / kTileM; }
+
+// Whether block kb of K of a tile's B has K as its row index, and the bytes of B's
+// half tile for one CTA: rows of K-major, or whole boxes of 64 columns.
+__device__ __forceinline__ bool b_is_mn(const Tile& x, int kb) {
+  return x.kind == kApply || (x.kind == kPoly && exchanged(x.nt * x.bn, kb));
+}
+__device__ __forceinline__ uint32_t b_bytes(const Tile& x, int kb) {
   const int half = x.bn / 2;
-  return (x.kind == kApply ? (half + 63) / 64 * 64 : half) * kTileK * 2;
+  return (b_is_mn(x, kb) ? (half + 63) / 64 * 64 : half) * kTileK * 2;
 }
 
 // ---- the epilogues -------------------------------------------------------------------
-
-// A block's mirror image goes to memory by way of this warp's part of shared
-// memory, rows of 64 bytes in the 64-byte swizzle: from registers it would take
-// 32 stores of 64 bytes.  Lanes are columns of it, then rows.
-__device__ __forceinline__ void turn(uint32_t at, int lane, uint4 (&w)[4]) {
-  __syncwarp();
-#pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    const uint32_t pair = (&w[k / 8].x)[k / 2 % 4];
-    const uint16_t one = static_cast<uint16_t>(k & 1 ? pair >> 16 : pair);
-    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + k * 64 + (((lane >> 3) ^ ((k >> 1) & 3)) << 4) + (lane & 7) * 2),
-                 "h"(one)
-                 : "memory");
-  }
-  __syncwarp();
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(w[k].x), "=r"(w[k].y), "=r"(w[k].z), "=r"(w[k].w)
-                 : "r"(at + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4))
-                 : "memory");
-}
 
 // 32 values of a row, of which those below `cols` from col0 on count, in rows of
 // multiples of 16 values from a 32-byte boundary.
@@ -236,12 +223,10 @@ __device__ __forceinline__ void store_row(uint16_t* to, int col0, int cols, cons
   if (col0 + 16 < cols) st_32B_words(to + 16, w[2], w[3]);
 }
 
-// 32 columns from col0 of this thread's row, v, in one or two parts; with
-// `mirror` their warp's block's mirror image too.
+// 32 columns from col0 of this thread's row, v, in one or two parts.
 __device__ __forceinline__ void store_block(uint16_t* out, int64_t ld, int64_t part, int rows, int cols, int row, int col0,
-                                            const float (&v)[32], bool two, bool mirror, uint32_t stash) {
-  const int lane = threadIdx.x & 31, row0 = row - lane;
-  if (row0 >= rows || col0 >= cols) return;
+                                            const float (&v)[32], bool two) {
+  if (row >= rows || col0 >= cols) return;
   uint4 hi[4], lo[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -250,19 +235,9 @@ __device__ __forceinline__ void store_block(uint16_t* out, int64_t ld, int64_t p
     for (int q = 0; q < 8; ++q) w[q] = v[8 * k + q];
     split8(w, hi[k], lo[k]);
   }
-  if (row < rows) {
-    uint16_t* to = out + row * ld + col0;
-    store_row(to, col0, cols, hi);
-    if (two) store_row(to + part, col0, cols, lo);
-  }
-  if (!mirror) return;
-  uint16_t* to = out + (col0 + lane) * ld + row0;
-  turn(stash, lane, hi);
-  if (col0 + lane < cols) store_row(to, row0, rows, hi);
-  if (two) {
-    turn(stash + 2048, lane, lo);
-    if (col0 + lane < cols) store_row(to + part, row0, rows, lo);
-  }
+  uint16_t* to = out + row * ld + col0;
+  store_row(to, col0, cols, hi);
+  if (two) store_row(to + part, col0, cols, lo);
 }
 
 // 16 bytes that another SM wrote while this kernel ran: past L1.
@@ -283,7 +258,7 @@ __device__ __forceinline__ void fetch(const RunArgs<GROUPS>& g, const Tile& x, i
   const Shape& h = g.shape[x.shape];
   const int col0 = x.nt * x.bn + c;
   if (x.kind == kPoly) {
-    if (row >= h.m || col0 > (row | 31) || col0 >= h.m) return;
+    if (row >= h.m || col0 >= h.m) return;
     // A's rows are padded to 16 values: what is read past the last column is not used
     const uint16_t* a = h.a_at + x.matrix * h.apart_a + row * h.lda + col0;
 #pragma unroll
@@ -314,28 +289,25 @@ __device__ __forceinline__ void each_32(uint32_t tmem, int first, int bn, F f, R
 }
 
 template <int FINAL, int GROUPS, typename R>
-__device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x, uint32_t tmem, uint32_t stash,
-                                         Beside& b, int row, int half, R release) {
+__device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x, uint32_t tmem, Beside& b, int row,
+                                         int half, R release) {
   const Shape& h = g.shape[x.shape];
-  const int bn = x.bn, n0 = x.nt * bn, row0 = row - static_cast<int>(threadIdx.x & 31);
+  const int bn = x.bn, n0 = x.nt * bn;
   const int which = h.first + x.matrix;
   const float unit = x.step == 0 ? g.norms[which].unit : 1.f;     // what the first X lacks of the norm
   const bool two = x.step < g.fine;
   if (x.kind == kGram) {
     const float scale = unit * unit * (kScaleA / (kScaleX * kScaleX));
     each_32(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
-      if (n0 + c > row0) return;
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= scale;
-      store_block(h.a_at + x.matrix * h.apart_a, h.lda, h.part_a, h.m, h.m, row, n0 + c, v, two, n0 + c < row0,
-                  stash);
+      store_block(h.a_at + x.matrix * h.apart_a, h.lda, h.part_a, h.m, h.m, row, n0 + c, v, two);
     }, release);
   } else if (x.kind == kPoly) {
     const float a = g.coefficients[3 * x.step] * kScaleP, once = g.coefficients[3 * x.step + 1] * (kScaleP / kScaleA);
     const float square = g.coefficients[3 * x.step + 2] * (kScaleP / (kScaleA * kScaleA));
     each_32(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
       const int col0 = n0 + c;
-      if (col0 > row0) return;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         float u[8], l[8] = {};
@@ -348,7 +320,7 @@ __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x
         }
       }
       if (c + 64 < bn) fetch<FINAL>(g, x, row, c + 64, b);
-      store_block(h.p_at + x.matrix * h.apart_a, h.lda, h.part_a, h.m, h.m, row, col0, v, two, col0 < row0, stash);
+      store_block(h.p_at + x.matrix * h.apart_a, h.lda, h.part_a, h.m, h.m, row, col0, v, two);
     }, release);
   } else if (x.step + 1 < g.steps) {
     const float scale = unit / kScaleP;
@@ -356,7 +328,7 @@ __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] *= scale;
       store_block(h.x_at[(x.step & 1) ^ 1] + x.matrix * h.apart_x, h.ldx, h.part_x, h.m, h.n, row, n0 + c, v,
-                  x.step + 1 < g.fine, false, stash);
+                  x.step + 1 < g.fine);
     }, release);
   } else {
     const Entry& e = g.entries[which];
@@ -391,7 +363,7 @@ __device__ __forceinline__ void add_release(unsigned* p, unsigned v) {
 template <int FINAL, int GROUPS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(const __grid_constant__ RunArgs<GROUPS> g) {
   extern __shared__ unsigned char raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kStages + 3 * kQueue + 5];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 3 * kQueue + 6];
   __shared__ Tile queue[kQueue];
   __shared__ uint32_t tmem_slot;
   __shared__ int failed, last_out;
@@ -405,6 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
   auto told = [&](int q) { return bar0 + 8 * (2 * kStages + 5 + q); };             // queue[q] holds a tile
   auto heard = [&](int q) { return bar0 + 8 * (2 * kStages + 5 + kQueue + q); };   // everyone has read it
   auto stored = [&](int q) { return bar0 + 8 * (2 * kStages + 5 + 2 * kQueue + q); };  // this CTA's half of the tile is
+  const uint32_t began = bar0 + 8 * (2 * kStages + 5 + 3 * kQueue);                    // the leader loads the next tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
 
@@ -418,9 +391,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
       bar_init(done(a), 1);
       bar_init(taken(a), 2 * kEpilogueWarps);
     }
+    bar_init(began, 1);
     for (int q = 0; q < kQueue; ++q) {
       bar_init(told(q), 1);
-      bar_init(heard(q), 6 + 2 * kEpilogueWarps);   // the loaders but the leader's first, the issuer, warps 2, the epilogue
+      bar_init(heard(q), 7 + 2 * kEpilogueWarps);   // the loaders, the issuer, the warps 2, the epilogue
       bar_init(stored(q), kEpilogueWarps);
     }
     bar_init(drained, 1);
@@ -438,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
   const bool lead = elect_one();
   bool ok = true;
   auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity)) != 0; };
-  // The i-th tile of this pair, from the leader's first warp.
+  // The i-th tile of this pair, from the leader's last warp.
   auto tile_of = [&](int i) {
     Tile x{};
     x.kind = -1;
@@ -450,87 +424,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
     if (lead) bar_arrive(in_cta(heard(q), 0));
     return x;
   };
-  // The next tile: taken from the counter, waited for, and told to the others.
-  auto take_tile = [&](int i) {
-    const int q = i % kQueue;
-    Tile x{};
-    x.kind = -1;
-    ok = wait_all(heard(q), ((i / kQueue) & 1) ^ 1);
-    if (!ok) return x;
-    unsigned t = 0, before = 0;
-    if (lead) t = atomicAdd(g.next, 1u);
-    t = __reduce_max_sync(0xffffffffu, t);
-    x = locate(g, t, before);
-    if (x.kind >= 0 && before > 0) {
-      const unsigned* p = g.written + g.shape[x.shape].first + x.matrix;
-      const unsigned want = before * 2;
-      bool there = true;
-      if (lead) {
-        const long long t0 = clock64();
-        while (there && ld_acquire(p) < want) there = clock64() - t0 <= kWaitCycles;
-      }
-      ok = __all_sync(0xffffffffu, there) != 0;
-      if (!ok) return x;
-    }
-    // what the others' threads wrote is loaded through the async proxy
-    fence_all_async();
-    if (lead) {
-      for (uint32_t r = 0; r < 2; ++r) {
-        const uint32_t at = in_cta(smem_addr(&queue[q]), r);
-        st_cluster(at, x.kind, x.shape, x.matrix, x.mt);
-        st_cluster(at + 16, x.nt, x.step, x.kb, x.bn);
-        bar_arrive_written(in_cta(told(q), r));
-      }
-    }
-    __syncwarp();
-    return x;
-  };
 
   int issued = 0;      // stages loaded by this warp
   if (warp == 0 || warp == 3) {
     int s = 0;
     uint32_t phase = 1;
-    const bool first = warp == 0;
+    const bool first = warp == 0, stall = g.stall && blockIdx.x < 2;
     for (int i = 0;; ++i) {
-      const Tile x = first && rank == 0 ? take_tile(i) : tile_of(i);
+      const Tile x = tile_of(i);
       if (!ok || x.kind < 0) break;
+      if (first && rank == 0 && lead) bar_arrive_own(began);
       fence_all_async();
       const Shape& h = g.shape[x.shape];
       const Parts parts = parts_of(g, x);
-      const int bn = x.bn;
-      const bool b_mn = x.kind == kApply;
-      const CUtensorMap* map;
-      if (first) map = x.kind == kGram ? &h.x[x.step & 1] : x.kind == kPoly ? &h.a : &h.p;
-      else if (b_mn) map = &h.x64[x.step & 1];
-      else if (x.kind == kGram) map = bn == 256 ? &h.x[x.step & 1] : bn == 128 ? &h.x64[x.step & 1] : &h.x32[x.step & 1];
-      else map = bn == 256 ? &h.a : bn == 128 ? &h.a64 : &h.a32;
-      const int am = x.mt * kTileM + static_cast<int>(rank) * 128;
-      const int b0 = x.nt * bn + static_cast<int>(rank) * (bn / 2);
-      const int z = x.matrix;
-      const bool boxes2 = b_mn && bn == kTileN;
-      const uint32_t of_b = 2 * b_bytes(x);
-      for (int kb = 0; kb < x.kb; ++kb) {
+      const int bn = x.bn, depth = h.matrices, blocks = x.kb;
+      const CUtensorMap *map, *map64;     // K-major, and boxes of 64 columns with K as the row index
+      if (first) {
+        map = x.kind == kGram ? &h.x[x.step & 1] : x.kind == kPoly ? &h.a : &h.p;
+        map64 = x.kind == kPoly ? &h.a64 : &h.p64;
+      } else {
+        if (x.kind == kGram) map = bn == 256 ? &h.x[x.step & 1] : bn == 128 ? &h.x64[x.step & 1] : &h.x32[x.step & 1];
+        else map = bn == 256 ? &h.a : bn == 128 ? &h.a64 : &h.a32;
+        map64 = x.kind == kPoly ? &h.a64 : &h.x64[x.step & 1];
+      }
+      // this CTA's rows (or columns) of the operand
+      const int at = first ? x.mt * kTileM + static_cast<int>(rank) * 128 : x.nt * bn + static_cast<int>(rank) * (bn / 2);
+      const bool second_box = first || bn == kTileN, counts = first && rank == 0;
+      for (int kb = 0; kb < blocks; ++kb) {
+        const bool mn = first ? x.kind != kGram && exchanged(x.mt * kTileM, kb) : b_is_mn(x, kb);
+        const uint32_t of_b = 2 * b_bytes(x, kb);
+        const int k = kb * kTileK;
         for (int part = 0; part < parts.a; ++part, ++issued) {
           // A stage without B is none of the second warp's: it may be used, and emptied, before that warp comes by,
           // and a wait for a phase that is two back never ends.
           const bool with_b = part < parts.b;
           if (first || with_b) ok = wait_all(empty(s), phase);
           if (!ok) break;
-          const uint32_t bar = in_cta(full(s), 0);
-          const uint32_t sa = ring + s * kStageBytes, sb = sa + kSlotBytes;
-          const int k = kb * kTileK, zp = z + part * h.matrices;
-          if (lead) {
-            if (first) {
-              if (rank == 0) bar_expect(full(s), 2 * kSlotBytes + (with_b ? of_b : 0));
-              if (!(g.stall && blockIdx.x < 2 && issued == 0)) tma_load3(sa, map, k, am, zp, bar);
-            } else if (with_b) {
-              if (b_mn) {
-                // K is the row index of X: boxes of 64 columns
-                tma_load3(sb, map, b0, k, zp, bar);
-                if (boxes2) tma_load3(sb + 8192, map, b0 + 64, k, zp, bar);
-              } else {
-                tma_load3(sb, map, k, b0, zp, bar);
-              }
+          if (lead && (first || with_b)) {
+            const uint32_t bar = in_cta(full(s), 0), to = ring + s * kStageBytes + (first ? 0 : kSlotBytes);
+            const int z = x.matrix + part * depth;
+            if (counts) bar_expect(full(s), 2 * kSlotBytes + (with_b ? of_b : 0));
+            if (first && stall && issued == 0) {
+            } else if (mn) {
+              tma_load3(to, map64, at, k, z, bar);
+              if (second_box) tma_load3(to + 8192, map64, at + 64, k, z, bar);
+            } else {
+              tma_load3(to, map, k, at, z, bar);
             }
           }
           __syncwarp();
@@ -552,27 +491,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
         const Tile x = tile_of(i);
         if (!ok || x.kind < 0) break;
         const Parts parts = parts_of(g, x);
-        const bool b_mn = x.kind == kApply;
-        const uint32_t idesc = instr_desc(false, false, b_mn, kTileM, x.bn);
-        const uint64_t a_step = 32 >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
-        const uint64_t a0 = operand_desc(ring, 0), b0 = operand_desc(ring + kSlotBytes, b_mn ? 8192 : 0);
-        const int a = i & 1;
+        const uint32_t idesc = instr_desc(false, false, false, kTileM, x.bn);
+        const int a = i & 1, blocks = x.kb, a_row = x.mt * kTileM;
         ok = wait_all(taken(a), ((i >> 1) & 1) ^ 1);
         if (!ok) break;
         fence_after();
         const uint32_t d = tmem + a * kTileN;
+        // 16 values of K further: 32 bytes within a K-major row, 16 rows of an MN-major tile
+        const uint64_t a_k = operand_desc(ring, 0), a_mn = operand_desc(ring, 8192);
+        const uint64_t b_k = operand_desc(ring + kSlotBytes, 0), b_mn = operand_desc(ring + kSlotBytes, 8192);
         // the tile's blocks of K in PA and PB parts, known here for the instructions to follow one another closely
         auto run = [&](auto pa, auto pb) {
           constexpr int PA = decltype(pa)::value, PB = decltype(pb)::value;
-          for (int kb = 0; kb < x.kb; ++kb) {
+          for (int kb = 0; kb < blocks; ++kb) {
+            const bool of_a = x.kind != kGram && exchanged(a_row, kb), of_b = b_is_mn(x, kb);
+            const uint64_t a_step = of_a ? 128 : 2, b_step = of_b ? 128 : 2;
+            const uint32_t id = idesc | (of_a ? 1u << 15 : 0u) | (of_b ? 1u << 16 : 0u);
             ok = wait_all(full(s), phase);
             if (!ok) break;
             fence_after();
             const int high = s;
-            const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
+            const uint64_t da = (of_a ? a_mn : a_k) + s * (kStageBytes >> 4), db = (of_b ? b_mn : b_k) + s * (kStageBytes >> 4);
             if (lead) {
 #pragma unroll
-              for (int q = 0; q < kTileK / 16; ++q) mma(d, da + q * a_step, db + q * b_step, idesc, kb > 0 || q > 0);
+              for (int q = 0; q < kTileK / 16; ++q) mma(d, da + q * a_step, db + q * b_step, id, kb > 0 || q > 0);
               if (PA == 1) mma_commit(empty(s));
             }
             __syncwarp();
@@ -584,13 +526,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
             ok = wait_all(full(s), phase);
             if (!ok) break;
             fence_after();
-            const uint64_t la = a0 + s * (kStageBytes >> 4), lb = b0 + s * (kStageBytes >> 4);
+            const uint64_t la = (of_a ? a_mn : a_k) + s * (kStageBytes >> 4), lb = (of_b ? b_mn : b_k) + s * (kStageBytes >> 4);
             if (lead) {
               // of two parts each, the product of the low ones is left out: 2^-22 of the whole
 #pragma unroll
               for (int q = 0; q < kTileK / 16; ++q) {
-                mma(d, la + q * a_step, db + q * b_step, idesc, true);
-                if (PB > 1) mma(d, da + q * a_step, lb + q * b_step, idesc, true);
+                mma(d, la + q * a_step, db + q * b_step, id, true);
+                if (PB > 1) mma(d, da + q * a_step, lb + q * b_step, id, true);
               }
               mma_commit(empty(high));
               mma_commit(empty(s));
@@ -632,9 +574,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
       __syncwarp();
     }
     if (!ok && lead) failed = 1;
+  } else if (warp == 12) {
+    // Takes the next tile when the leader begins to load the one before, waits for what it needs, and tells the roles.
+    for (int i = 0; rank == 0; ++i) {
+      const int q = i % kQueue;
+      ok = wait_all(heard(q), ((i / kQueue) & 1) ^ 1);
+      if (ok && i > 0) ok = wait_all(began, (i - 1) & 1);
+      if (!ok) break;
+      unsigned t = 0, before = 0;
+      if (lead) t = atomicAdd(g.next, 1u);
+      t = __reduce_max_sync(0xffffffffu, t);
+      const Tile x = locate(g, t, before);
+      if (x.kind >= 0 && before > 0) {
+        const unsigned* p = g.written + g.shape[x.shape].first + x.matrix;
+        const unsigned want = before * 2;
+        bool there = true;
+        if (lead) {
+          const long long t0 = clock64();
+          while (there && ld_acquire(p) < want) there = clock64() - t0 <= kWaitCycles;
+        }
+        ok = __all_sync(0xffffffffu, there) != 0;
+        if (!ok) break;
+      }
+      // what the others' threads wrote is loaded through the async proxy
+      if (lead) {
+        fence_all_async();
+        for (uint32_t r = 0; r < 2; ++r) {
+          const uint32_t at = in_cta(smem_addr(&queue[q]), r);
+          st_cluster(at, x.kind, x.shape, x.matrix, x.mt);
+          st_cluster(at + 16, x.nt, x.step, x.kb, x.bn);
+          bar_arrive_written(in_cta(told(q), r));
+        }
+      }
+      __syncwarp();
+      if (x.kind < 0) break;
+    }
+    if (!ok && lead) failed = 1;
   } else if (warp >= 4) {
     const int quad = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t stash = ring + kStages * kStageBytes + (warp - 4) * kStashBytes;
     Beside beside = {};
     for (int i = 0;; ++i) {
       const int a = i & 1;
@@ -645,7 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
       ok = wait_all(done(a), (i >> 1) & 1);
       if (!ok) break;
       fence_after();
-      epilogue<FINAL>(g, x, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21), stash, beside, row, half, [&] {
+      epilogue<FINAL>(g, x, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21), beside, row, half, [&] {
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(in_cta(taken(a), 0));
@@ -1034,7 +1011,8 @@ int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, ch
     if ((rc = make_map3(&h.a, ws + group.a, m, m, group.lda, 2 * c, 128)) ||
         (rc = make_map3(&h.a64, ws + group.a, m, m, group.lda, 2 * c, 64)) ||
         (rc = make_map3(&h.a32, ws + group.a, m, m, group.lda, 2 * c, 32)) ||
-        (rc = make_map3(&h.p, ws + group.p, m, m, group.lda, 2 * c, 128)))
+        (rc = make_map3(&h.p, ws + group.p, m, m, group.lda, 2 * c, 128)) ||
+        (rc = make_map3(&h.p64, ws + group.p, m, m, group.lda, 2 * c, 64)))
       return rc;
   }
   const auto fn = ns_run<FINAL, GROUPS>;
