@@ -894,8 +894,8 @@ int64_t zero_orthogonalize_workspace_bytes(int64_t n_matrices, const int64_t* ro
  *              values must stay below 4 on the way (fp16's range).
  *   fine_steps the first so many steps carry every operand as a sum of two fp16
  *              values (22 bits), the others as one (11 bits); -1 chooses: all for
- *              ZERO_FP32, else all but the last two.  With Muon's coefficients
- *              the result is about 1e-3 off so (2-norm), 1e-2 with 0 where few
+ *              ZERO_FP32, else all but the last three.  With Muon's coefficients
+ *              the result is 1e-3 to 2e-3 off so (2-norm), 1e-2 with 0 where few
  *              singular values stand above the rest, 1e-6 with all.
  *   workspace  device, 256-byte aligned, any contents; its first 4 bytes count
  *              waits that gave up (zero_lm_workspace_status).

@@ -1298,7 +1298,7 @@ class Orthogonalize(_Matrices):
     """Newton-Schulz orthogonalisation of matrices of the given (rows, cols),
     all of one dtype: "fp16", "bf16" or "fp32" (zero_orthogonalize).
     ``coefficients`` holds (a, b, c) for each step; ``fine_steps`` of them carry
-    their operands in two 16-bit parts (None: all but the last two, for fp32
+    their operands in two 16-bit parts (None: all but the last three, for fp32
     all).  Workspace and stream as for :class:`LmLoss`."""
 
     def __init__(self, shapes, dtype="bf16", coefficients=MUON_COEFFICIENTS, fine_steps=None, device="cuda",

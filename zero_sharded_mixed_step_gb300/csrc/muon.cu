@@ -33,7 +33,10 @@
 // 20 times above the rest comes out 1.4e-2 off (2-norm), with bf16 11e-2.  So
 // in the first `fine` steps every operand is a sum of two fp16 parts (22 bits)
 // and a product three products of parts; the last steps, after which little
-// growth is left, take one part.  Two such steps leave an error of about 1e-3.
+// growth is left, take one part.  Three such steps leave an error of about 1e-3,
+// 2e-3 where few singular values stand far above the rest, which is what a bf16
+// result's own rounding comes to (two such steps 1e-3 at most, at 1.1 times the
+// time).
 // X and A are stored times 2^12, P times 2^9: entries of fp16's normal range.
 // The first X is the input times a power of two, the rest of 1 / |G| (between
 // 1/2 and 1) being applied in the epilogues: a 16-bit input is then exact in
@@ -80,11 +83,14 @@ constexpr int kSlotBytes = 128 * kTileK * 2;     // one part of one operand's ha
 // A stage of the operands' ring: one part of A and of B for one block of K.  A
 // block in two parts takes two stages, the high parts first.
 constexpr int kStages = 7, kStageBytes = 2 * kSlotBytes;
-// warp 0 loads A, warp 3 loads B, warp 1 issues the products, warps 4-11 are the
-// epilogue, warp 2 says what they have written, and in the leader warp 12 takes
-// the tiles
-constexpr int kThreads = 416;
-constexpr int kEpilogueWarps = 8;
+// warp 0 loads A, warp 3 loads B, warp 1 issues the products, warps 4-19 are the
+// epilogue, four for each quarter of the TMEM lanes taking 16 columns in turn
+// (two for each, 32 columns at a time, took twice as long for a tile, which the
+// next product waits for), warp 2 says what they have written, and in the leader
+// warp 20 takes the tiles
+constexpr int kThreads = 672;
+constexpr int kEpilogueWarps = 16, kTakerWarp = 20;
+constexpr int kCols = 16;            // of a row that an epilogue thread holds at a time
 constexpr int kQueue = 4;            // tiles on their way through a pair
 constexpr int kRunSmem = kStages * kStageBytes + 1024;
 constexpr int kFewGroups = 3, kMaxGroups = 12;       // shapes of one launch
@@ -216,28 +222,22 @@ __device__ __forceinline__ uint32_t b_bytes(const Tile& x, int kb) {
 
 // ---- the epilogues -------------------------------------------------------------------
 
-// 32 values of a row, of which those below `cols` from col0 on count, in rows of
+// 16 columns from col0 of this thread's row, v, in one or two parts, in rows of
 // multiples of 16 values from a 32-byte boundary.
-__device__ __forceinline__ void store_row(uint16_t* to, int col0, int cols, const uint4 (&w)[4]) {
-  st_32B_words(to, w[0], w[1]);
-  if (col0 + 16 < cols) st_32B_words(to + 16, w[2], w[3]);
-}
-
-// 32 columns from col0 of this thread's row, v, in one or two parts.
 __device__ __forceinline__ void store_block(uint16_t* out, int64_t ld, int64_t part, int rows, int cols, int row, int col0,
-                                            const float (&v)[32], bool two) {
+                                            const float (&v)[kCols], bool two) {
   if (row >= rows || col0 >= cols) return;
-  uint4 hi[4], lo[4];
+  uint4 hi[2], lo[2];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < 2; ++k) {
     float w[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) w[q] = v[8 * k + q];
     split8(w, hi[k], lo[k]);
   }
   uint16_t* to = out + row * ld + col0;
-  store_row(to, col0, cols, hi);
-  if (two) store_row(to + part, col0, cols, lo);
+  st_32B_words(to, hi[0], hi[1]);
+  if (two) st_32B_words(to + part, lo[0], lo[1]);
 }
 
 // 16 bytes that another SM wrote while this kernel ran: past L1.
@@ -247,10 +247,10 @@ __device__ __forceinline__ uint4 ld_fresh(const void* p) {
   return r;
 }
 
-// What the epilogue reads beside the sums for 32 columns of a row, fetched
+// What the epilogue reads beside the sums for 16 columns of a row, fetched
 // before the sums are there: A's values of both parts (kPoly), or the master's.
 struct Beside {
-  uint4 w[8];
+  uint4 w[4];
 };
 
 template <int FINAL, int GROUPS>
@@ -262,26 +262,24 @@ __device__ __forceinline__ void fetch(const RunArgs<GROUPS>& g, const Tile& x, i
     // A's rows are padded to 16 values: what is read past the last column is not used
     const uint16_t* a = h.a_at + x.matrix * h.apart_a + row * h.lda + col0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (col0 + 8 * k >= h.m) break;
+    for (int k = 0; k < 2; ++k) {
       b.w[k] = ld_fresh(a + 8 * k);
-      if (x.step < g.fine) b.w[4 + k] = ld_fresh(a + h.part_a + 8 * k);
+      if (x.step < g.fine) b.w[2 + k] = ld_fresh(a + h.part_a + 8 * k);
     }
   } else if (FINAL == kUpdate && x.kind == kApply && x.step + 1 == g.steps) {
     if (row >= h.m || col0 >= h.n) return;
-    read_master(g.entries[h.first + x.matrix], h.n, row, col0, b.w);
+    read_master<kCols>(g.entries[h.first + x.matrix], h.n, row, col0, b.w);
   }
 }
 
-// This thread's row of an accumulator, 32 columns at a time from `first` in
+// This thread's row of an accumulator, 16 columns at a time from `first` in
 // steps of 64; `release` runs when the last ones are in registers.
 template <typename F, typename R>
-__device__ __forceinline__ void each_32(uint32_t tmem, int first, int bn, F f, R release) {
-  if (first >= bn) release();
+__device__ __forceinline__ void each_16(uint32_t tmem, int first, int bn, F f, R release) {
 #pragma unroll 1
   for (int c = first; c < bn; c += 64) {
-    float v[32];
-    tmem_ld32(tmem + c, v);
+    float v[kCols];
+    tmem_ld16(tmem + c, v);
     tmem_ld_wait(v);
     if (c + 64 >= bn) release();
     f(c, v);
@@ -290,7 +288,7 @@ __device__ __forceinline__ void each_32(uint32_t tmem, int first, int bn, F f, R
 
 template <int FINAL, int GROUPS, typename R>
 __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x, uint32_t tmem, Beside& b, int row,
-                                         int half, R release) {
+                                         int share, R release) {
   const Shape& h = g.shape[x.shape];
   const int bn = x.bn, n0 = x.nt * bn;
   const int which = h.first + x.matrix;
@@ -298,21 +296,21 @@ __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x
   const bool two = x.step < g.fine;
   if (x.kind == kGram) {
     const float scale = unit * unit * (kScaleA / (kScaleX * kScaleX));
-    each_32(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
+    each_16(tmem, share * kCols, bn, [&](int c, float (&v)[kCols]) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) v[k] *= scale;
+      for (int k = 0; k < kCols; ++k) v[k] *= scale;
       store_block(h.a_at + x.matrix * h.apart_a, h.lda, h.part_a, h.m, h.m, row, n0 + c, v, two);
     }, release);
   } else if (x.kind == kPoly) {
     const float a = g.coefficients[3 * x.step] * kScaleP, once = g.coefficients[3 * x.step + 1] * (kScaleP / kScaleA);
     const float square = g.coefficients[3 * x.step + 2] * (kScaleP / (kScaleA * kScaleA));
-    each_32(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
+    each_16(tmem, share * kCols, bn, [&](int c, float (&v)[kCols]) {
       const int col0 = n0 + c;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
         float u[8], l[8] = {};
         Fmt<__half>::unpack8(b.w[k], u);
-        if (two) Fmt<__half>::unpack8(b.w[4 + k], l);
+        if (two) Fmt<__half>::unpack8(b.w[2 + k], l);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           v[8 * k + q] = fmaf(once, u[q] + l[q], square * v[8 * k + q]);
@@ -324,9 +322,9 @@ __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x
     }, release);
   } else if (x.step + 1 < g.steps) {
     const float scale = unit / kScaleP;
-    each_32(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
+    each_16(tmem, share * kCols, bn, [&](int c, float (&v)[kCols]) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) v[k] *= scale;
+      for (int k = 0; k < kCols; ++k) v[k] *= scale;
       store_block(h.x_at[(x.step & 1) ^ 1] + x.matrix * h.apart_x, h.ldx, h.part_x, h.m, h.n, row, n0 + c, v,
                   x.step + 1 < g.fine);
     }, release);
@@ -334,13 +332,13 @@ __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x
     const Entry& e = g.entries[which];
     const bool finite = g.norms[which].finite;
     const float scale = finite ? unit / (kScaleP * kScaleX) : NAN;
-    each_32(tmem, half * 32, bn, [&](int c, float (&v)[32]) {
+    each_16(tmem, share * kCols, bn, [&](int c, float (&v)[kCols]) {
       // a norm that is not finite leaves the state as it was
       if (row >= h.m || n0 + c >= h.n || (FINAL == kUpdate && !finite)) return;
 #pragma unroll
-      for (int k = 0; k < 32; ++k) v[k] *= scale;
+      for (int k = 0; k < kCols; ++k) v[k] *= scale;
       if (FINAL == kUpdate) {
-        step_master(e, b.w, v);
+        step_master<kCols>(e, b.w, v);
         if (c + 64 < bn) fetch<FINAL>(g, x, row, c + 64, b);
       }
       write_columns<FINAL == kUpdate>(h.n, e, g.dtype, row, n0 + c, v);
@@ -434,6 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
       const Tile x = tile_of(i);
       if (!ok || x.kind < 0) break;
       if (first && rank == 0 && lead) bar_arrive_own(began);
+      // what other CTAs' threads wrote is loaded through the async proxy
       fence_all_async();
       const Shape& h = g.shape[x.shape];
       const Parts parts = parts_of(g, x);
@@ -568,13 +567,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
       ok = wait_all(stored(i % kQueue), (i / kQueue) & 1);
       if (!ok) break;
       if (lead) {
-        fence_all_async();
         add_release(g.written + g.shape[x.shape].first + x.matrix, 1u);
       }
       __syncwarp();
     }
     if (!ok && lead) failed = 1;
-  } else if (warp == 12) {
+  } else if (warp == kTakerWarp) {
     // Takes the next tile when the leader begins to load the one before, waits for what it needs, and tells the roles.
     for (int i = 0; rank == 0; ++i) {
       const int q = i % kQueue;
@@ -596,9 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
         ok = __all_sync(0xffffffffu, there) != 0;
         if (!ok) break;
       }
-      // what the others' threads wrote is loaded through the async proxy
       if (lead) {
-        fence_all_async();
         for (uint32_t r = 0; r < 2; ++r) {
           const uint32_t at = in_cta(smem_addr(&queue[q]), r);
           st_cluster(at, x.kind, x.shape, x.matrix, x.mt);
@@ -611,18 +607,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
     }
     if (!ok && lead) failed = 1;
   } else if (warp >= 4) {
-    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const int quad = warp & 3, share = (warp - 4) >> 2;
     Beside beside = {};
     for (int i = 0;; ++i) {
       const int a = i & 1;
       const Tile x = tile_of(i);
       if (!ok || x.kind < 0) break;
       const int row = x.mt * kTileM + static_cast<int>(rank) * 128 + quad * 32 + lane;
-      fetch<FINAL>(g, x, row, half * 32, beside);
+      fetch<FINAL>(g, x, row, share * kCols, beside);
       ok = wait_all(done(a), (i >> 1) & 1);
       if (!ok) break;
       fence_after();
-      epilogue<FINAL>(g, x, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21), beside, row, half, [&] {
+      epilogue<FINAL>(g, x, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21), beside, row, share, [&] {
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(in_cta(taken(a), 0));
@@ -1087,8 +1083,8 @@ int check_workspace(const void* workspace, int64_t bytes, int64_t needed) {
 }
 
 // The steps that carry two parts where the caller leaves it open: all but the
-// last two, for fp32 results all.
-int fine_steps(int fine, int steps, bool all) { return fine >= 0 ? fine : all ? steps : std::max(0, steps - 2); }
+// last three, for fp32 results all.
+int fine_steps(int fine, int steps, bool all) { return fine >= 0 ? fine : all ? steps : std::max(0, steps - 3); }
 
 // Fills an entry's place in the workspace.
 void place(Entry& e, const Group& g, int64_t member, char* ws) {

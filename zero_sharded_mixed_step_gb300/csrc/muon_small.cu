@@ -408,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
       for (int k = 0; k < 32; ++k) v[k] *= out;
       if (MUON) {
         uint4 theta[8];
-        read_master(e, c0 + nl, row, c0 + c, theta);
-        step_master(e, theta, v);
+        read_master<32>(e, c0 + nl, row, c0 + c, theta);
+        step_master<32>(e, theta, v);
       }
       write_columns<MUON>(c0 + nl, e, g.out_dtype, row, c0 + c, v);
     }

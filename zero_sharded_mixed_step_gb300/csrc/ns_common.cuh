@@ -81,54 +81,54 @@ __device__ __forceinline__ uint16_t pack1(int dtype, float v) {
   return dtype == ZERO_FP16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// Where 32 columns from col0 of a row of X lie with the caller, of `columns` that X has.
+// Where N columns from col0 of a row of X lie with the caller, of `columns` that X has.
 struct Where {
   bool wide;
   int64_t first, apart;
   int n;
 };
+template <int N>
 __device__ __forceinline__ Where where(const Entry& e, int64_t stride, int columns, int row, int col0) {
   return {e.wide && !e.transposed, e.transposed ? col0 * stride + row : row * stride + col0,
-          e.transposed ? stride : 1, min(32, columns - col0)};
+          e.transposed ? stride : 1, min(N, columns - col0)};
 }
 
-// 32 values of the master.  They are read apart from where they are used, all
+// N values of the master.  They are read apart from where they are used, all
 // before anything is written, so that they are waited for once or not at all.
-__device__ __forceinline__ void read_master(const Entry& e, int columns, int row, int col0, uint4 (&w)[8]) {
-  const Where at = where(e, e.cols, columns, row, col0);
+template <int N>
+__device__ __forceinline__ void read_master(const Entry& e, int columns, int row, int col0, uint4 (&w)[N / 4]) {
+  const Where at = where<N>(e, e.cols, columns, row, col0);
   const float* p = e.master + at.first;
   if (at.wide) {
 #pragma unroll
-    for (int k = 0; k < 8; k += 2)
+    for (int k = 0; k < N / 4; k += 2)
       if (4 * k < at.n) ld_32B_words(p + 4 * k, w[k], w[k + 1]);
   } else {
 #pragma unroll
-    for (int k = 0; k < 32; ++k)
+    for (int k = 0; k < N; ++k)
       if (k < at.n) (&w[k / 4].x)[k % 4] = __float_as_uint(p[k * at.apart]);
   }
 }
 
 // The new master's values from the old ones and the last product's.
-__device__ __forceinline__ void step_master(const Entry& e, const uint4 (&w)[8], float (&v)[32]) {
+template <int N>
+__device__ __forceinline__ void step_master(const Entry& e, const uint4 (&w)[N / 4], float (&v)[N]) {
 #pragma unroll
-  for (int k = 0; k < 32; ++k) v[k] = fmaf(-e.step, v[k], e.keep * __uint_as_float((&w[k / 4].x)[k % 4]));
+  for (int k = 0; k < N; ++k) v[k] = fmaf(-e.step, v[k], e.keep * __uint_as_float((&w[k / 4].x)[k % 4]));
 }
 
-// Columns [col0, col0 + 32), as far as [0, columns) reaches, of this thread's row
+// Columns [col0, col0 + N), as far as [0, columns) reaches, of this thread's row
 // of X to the caller: the last product's, or the new master's and their 16-bit
 // copy.
-template <bool UPDATE>
+template <bool UPDATE, int N>
 __device__ __forceinline__ void write_columns(int columns, const Entry& e, int dtype, int row, int col0,
-                                              const float (&v)[32]) {
+                                              const float (&v)[N]) {
   const bool fp32 = !UPDATE && dtype == ZERO_FP32;
-  const Where at = where(e, UPDATE ? e.cols : e.out_stride, columns, row, col0);
-  const bool wide = at.wide;
-  const int64_t first = at.first, apart = at.apart;
-  const int n = at.n;
-  if (wide) {
+  const Where at = where<N>(e, UPDATE ? e.cols : e.out_stride, columns, row, col0);
+  if (at.wide) {
     // multiples of 8 columns exist
 #pragma unroll
-    for (int k = 0; k < 32; k += 16) {
+    for (int k = 0; k < N; k += 16) {
       float a[8], b[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
@@ -136,27 +136,27 @@ __device__ __forceinline__ void write_columns(int columns, const Entry& e, int d
         b[q] = v[k + 8 + q];
       }
       if (UPDATE || fp32) {
-        float* to = (UPDATE ? e.master : static_cast<float*>(e.out)) + first + k;
-        if (k < n) dev::st_32B(to, a);
-        if (k + 8 < n) dev::st_32B(to + 8, b);
+        float* to = (UPDATE ? e.master : static_cast<float*>(e.out)) + at.first + k;
+        if (k < at.n) dev::st_32B(to, a);
+        if (k + 8 < at.n) dev::st_32B(to + 8, b);
       }
       if (!fp32) {
-        uint16_t* to = static_cast<uint16_t*>(UPDATE ? e.p16 : e.out) + first + k;
+        uint16_t* to = static_cast<uint16_t*>(UPDATE ? e.p16 : e.out) + at.first + k;
         const uint4 lo = pack8(dtype, a), hi = pack8(dtype, b);
-        if (k + 8 < n && (reinterpret_cast<uintptr_t>(to) & 31) == 0) {
+        if (k + 8 < at.n && (reinterpret_cast<uintptr_t>(to) & 31) == 0) {
           st_32B_words(to, lo, hi);
         } else {
-          if (k < n) dev::st_16B(to, lo);
-          if (k + 8 < n) dev::st_16B(to + 8, hi);
+          if (k < at.n) dev::st_16B(to, lo);
+          if (k + 8 < at.n) dev::st_16B(to + 8, hi);
         }
       }
     }
     return;
   }
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    if (k >= n) break;
-    const int64_t to = first + k * apart;
+  for (int k = 0; k < N; ++k) {
+    if (k >= at.n) break;
+    const int64_t to = at.first + k * at.apart;
     if (UPDATE || fp32) (UPDATE ? e.master : static_cast<float*>(e.out))[to] = v[k];
     if (!fp32) static_cast<uint16_t*>(UPDATE ? e.p16 : e.out)[to] = pack1(dtype, v[k]);
   }
