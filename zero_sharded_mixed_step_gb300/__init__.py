@@ -1099,7 +1099,7 @@ class LmLogprobs(_Owner):
         """(logp, entropy, lse) of each token, fp32; with ``top`` also the alternatives' log probabilities and ids
         (tokens x top, fp32 and int32, the likeliest first).  logp is 0 where the target lies outside the vocabulary."""
         tokens, operands = self._operands(hidden, table, targets)
-        logp, entropy, lse = (self._empty(tokens, self._fp32) for _ in range(3))
+        logp, entropy, lse = self._empty((3, tokens), self._fp32).unbind()
         outs, top_logp, top_ids = (logp, entropy, lse), None, None
         if self.top:
             values, ids = (self._empty((tokens, self.top), t) for t in (self._fp32, self.torch.int32))

@@ -311,10 +311,11 @@ __device__ __forceinline__ void scan_logprobs(const GemmArgs& g, const Job& j, c
         stash[k * 32 + lane] = v[k];
         some |= (v[k] > st.best[K - 1] ? 1u : 0u) << k;
       }
-      // a lane reads what it wrote itself
-      for (unsigned all = __reduce_or_sync(0xffffffffu, some); all != 0; all &= all - 1) {
-        const int k = __ffs(static_cast<int>(all)) - 1;
-        st.insert(stash[k * 32 + lane], n0 + c + k);
+      // each lane its own columns, from left to right; it reads what it wrote itself
+      while (__any_sync(0xffffffffu, some != 0)) {
+        const int k = __ffs(static_cast<int>(some)) - 1;
+        if (some != 0) st.insert(stash[k * 32 + lane], n0 + c + k);
+        some &= some - 1;
       }
     }
     const float ref = reference(st.top, scale2);
@@ -829,6 +830,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) lm_gemm
 
 constexpr int kSmallThreads = 256;
 
+// The largest bound of |D| over the tokens first, first + step, ... of a weighted
+// gradient, as the bits of a float: |a| + |b| (entropy + 1/e) for the weights a
+// and b, since |p log p| <= 1/e.  Weights that are not finite leave no bound; their
+// D is none either.
+__device__ __forceinline__ unsigned int largest_weight(const void* targets, int id_bytes, int vocab, int tokens,
+                                                       const float* dlogp, const float* dentropy, const float* entropy,
+                                                       int64_t first, int64_t step) {
+  float most = 0.f;
+  for (int64_t i = first; i < tokens; i += step) {
+    if (load_target(targets, id_bytes, i, vocab) < 0) continue;
+    const float b = dentropy ? dentropy[i] : 0.f;
+    const float bound = fabsf(dlogp[i]) + (b == 0.f ? 0.f : fabsf(b) * (fabsf(entropy[i]) + 0.36788f));
+    if (isfinite(bound)) most = fmaxf(most, bound);
+  }
+  return __float_as_uint(most);
+}
+
 // The hidden vectors with the rows of tokens without target set to 0: such a
 // row times D's zeros must add nothing to the table's gradient even where it
 // holds an infinity or a NaN.  WEIGHTED: a token whose weights are 0 counts as one
@@ -839,11 +857,24 @@ __global__ void __launch_bounds__(kSmallThreads) lm_masked_hidden(const uint16_t
                                                                   const void* targets, int id_bytes, int vocab,
                                                                   int tokens, uint16_t* out, unsigned int* counters,
                                                                   int n_counters, const float* dlogp,
-                                                                  const float* dentropy) {
+                                                                  const float* dentropy, const float* entropy,
+                                                                  unsigned int* largest) {
   allow_next();
   await_previous();
   if (blockIdx.x == 0)
-    for (int k = threadIdx.x; k < n_counters; k += kSmallThreads) counters[k] = 0;
+    for (int k = threadIdx.x; k < n_counters; k += kSmallThreads)
+      if (!WEIGHTED || counters + k != largest) counters[k] = 0;
+  if (WEIGHTED && largest != nullptr && blockIdx.x == gridDim.x - 1) {
+    // few tokens: the largest bound of D too, by one block
+    __shared__ unsigned int most;
+    if (threadIdx.x == 0) most = 0;
+    __syncthreads();
+    const unsigned int mine = __reduce_max_sync(
+        0xffffffffu, largest_weight(targets, id_bytes, vocab, tokens, dlogp, dentropy, entropy, threadIdx.x, kSmallThreads));
+    if ((threadIdx.x & 31) == 0) atomicMax(&most, mine);
+    __syncthreads();
+    if (threadIdx.x == 0) *largest = most;
+  }
   const int64_t total = static_cast<int64_t>(tokens) * width8;
   for (int64_t e = static_cast<int64_t>(blockIdx.x) * kSmallThreads + threadIdx.x; e < total;
        e += static_cast<int64_t>(gridDim.x) * kSmallThreads) {
@@ -855,27 +886,21 @@ __global__ void __launch_bounds__(kSmallThreads) lm_masked_hidden(const uint16_t
   }
 }
 
-// The largest bound of |D| over the tokens of a weighted gradient, as the bits of
-// a float: |a| + |b| (entropy + 1/e) for the weights a and b, since
-// |p log p| <= 1/e.  Weights that are not finite leave no bound; their D is none
-// either.
+// The same by a launch of its own, for many tokens; `largest` is 0 before.
 __global__ void __launch_bounds__(kSmallThreads) lm_largest_weight(const void* targets, int id_bytes, int vocab,
                                                                    int tokens, const float* dlogp,
                                                                    const float* dentropy, const float* entropy,
                                                                    unsigned int* largest) {
   allow_next();
   await_previous();
-  float most = 0.f;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSmallThreads + threadIdx.x; i < tokens;
-       i += static_cast<int64_t>(gridDim.x) * kSmallThreads) {
-    if (load_target(targets, id_bytes, i, vocab) < 0) continue;
-    const float b = dentropy ? dentropy[i] : 0.f;
-    const float bound = fabsf(dlogp[i]) + (b == 0.f ? 0.f : fabsf(b) * (fabsf(entropy[i]) + 0.36788f));
-    if (isfinite(bound)) most = fmaxf(most, bound);
-  }
-  const unsigned int of_warp = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+  const unsigned int of_warp = __reduce_max_sync(
+      0xffffffffu, largest_weight(targets, id_bytes, vocab, tokens, dlogp, dentropy, entropy,
+                                  static_cast<int64_t>(blockIdx.x) * kSmallThreads + threadIdx.x,
+                                  static_cast<int64_t>(gridDim.x) * kSmallThreads));
   if ((threadIdx.x & 31) == 0 && of_warp != 0) atomicMax(largest, of_warp);
 }
+// Up to so many tokens it is found beside the hidden vectors' copy, which saves a launch (4 us of 51).
+constexpr int64_t kFewWeights = 4096;
 
 // dh = scale * the sum of the splits' fp32 sums, in the splits' order, BATCH
 // loads at a time: several splits, of few tokens, kFinishBatch (one by one, 38
@@ -1172,15 +1197,15 @@ int run_grad(const GradCall& c, bool& stall) {
   const int width8 = static_cast<int>(width / 8);
   const int64_t pieces = ceil_div(vocab, p.piece), items = tokens * width8;
   unsigned int* lost = counters + pieces + 1;
+  unsigned int* largest = kOwnWeights && dtype == ZERO_FP16 ? lost + 1 : nullptr;
+  const bool few_weights = tokens <= kFewWeights;
   ZERO_CUDA(launch_chained(lm_masked_hidden<kOwnWeights>, dim3(small_grid(items)), kSmallThreads, 0, s,
                            static_cast<const uint16_t*>(hidden), hidden_stride, width8, targets, id_bytes,
                            static_cast<int>(vocab), static_cast<int>(tokens), masked, counters,
-                           static_cast<int>(pieces + kWords), dlogp, dentropy));
-  unsigned int* largest = nullptr;
+                           static_cast<int>(pieces + kWords), dlogp, dentropy, entropy, few_weights ? largest : nullptr));
   float unscale = static_cast<float>(c.scale);
   if (kOwnWeights) {
-    if (dtype == ZERO_FP16) {
-      largest = lost + 1;
+    if (largest != nullptr && !few_weights) {
       ZERO_CUDA(launch_chained(lm_largest_weight, dim3(small_grid(tokens)), kSmallThreads, 0, s, targets, id_bytes,
                                static_cast<int>(vocab), static_cast<int>(tokens), dlogp, dentropy, entropy, largest));
     }

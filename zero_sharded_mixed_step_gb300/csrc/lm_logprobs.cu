@@ -38,58 +38,66 @@ __device__ __forceinline__ bool before(float a, int at_a, float b, int at_b) {
   return a > b || (a == b && static_cast<unsigned>(at_a) < static_cast<unsigned>(at_b));
 }
 
-// The first of the 32 lanes' (v, at).
+// The first of the 32 lanes' (v, at): two reductions of whole numbers in the
+// floats' order (which -0 and 0 share).
 __device__ __forceinline__ void first_of_warp(float& v, int& at) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float w = __shfl_xor_sync(0xffffffffu, v, o);
-    const int at_w = __shfl_xor_sync(0xffffffffu, at, o);
-    if (before(w, at_w, v, at)) {
-      v = w;
-      at = at_w;
-    }
-  }
+  const int bits = __float_as_int(v + 0.f);
+  const unsigned key = static_cast<unsigned>(bits) ^ (bits < 0 ? 0xffffffffu : 0x80000000u);
+  const unsigned most = __reduce_max_sync(0xffffffffu, key);
+  at = static_cast<int>(__reduce_min_sync(0xffffffffu, key == most ? static_cast<unsigned>(at) : 0xffffffffu));
+  v = __uint_as_float(most ^ (most & 0x80000000u ? 0x80000000u : 0xffffffffu));
 }
 
-// The `count` first of the candidates of a warp, in order: lane r receives the
-// r-th.  get(c, v, at) gives this lane's c-th of n candidates; where two lanes
-// hold the same (v, at), it is none (at = -1).
-template <typename F>
-__device__ __forceinline__ void select_first(int count, int n, F get, float& out_v, int& out_at) {
-  const int lane = threadIdx.x & 31;
-  out_v = -INFINITY;
-  out_at = -1;
-  float last_v = 0.f, v = -INFINITY;
-  int last_at = -1, at = -1;
-  bool any = false, look = true;
-  for (int r = 0; r < count; ++r) {
-    if (look) {
-      v = -INFINITY;
-      at = -1;
-      for (int c = 0; c < n; ++c) {
-        float x;
-        int at_x;
-        get(c, x, at_x);
-        if ((!any || before(last_v, last_at, x, at_x)) && before(x, at_x, v, at)) {
-          v = x;
-          at = at_x;
+// A list of the K first of what it is offered, in order; -infinity and NaN never are.
+template <int K>
+struct List {
+  float v[K];
+  int at[K];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      v[k] = -INFINITY;
+      at[k] = -1;
+    }
+  }
+  // in any order of places
+  __device__ __forceinline__ void offer(float x, int x_at) {
+    if (!before(x, x_at, v[K - 1], at[K - 1])) return;
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+      if (!before(x, x_at, v[k], at[k])) continue;
+      const bool further = k > 0 && before(x, x_at, v[k > 0 ? k - 1 : 0], at[k > 0 ? k - 1 : 0]);
+      v[k] = further ? v[k > 0 ? k - 1 : 0] : x;
+      at[k] = further ? at[k > 0 ? k - 1 : 0] : x_at;
+    }
+  }
+  // The first `count` of the lanes' lists, in order: lane r receives the r-th.  The lists are used up.
+  __device__ __forceinline__ void first_of_lanes(int count, float& out_v, int& out_at) {
+    const int lane = threadIdx.x & 31;
+    out_v = -INFINITY;
+    out_at = -1;
+    for (int r = 0; r < count; ++r) {
+      float w = v[0];
+      int w_at = at[0];
+      first_of_warp(w, w_at);
+      if (w_at < 0) break;
+      if (lane == r) {
+        out_v = w;
+        out_at = w_at;
+      }
+      if (at[0] == w_at) {
+#pragma unroll
+        for (int k = 0; k + 1 < K; ++k) {
+          v[k] = v[k + 1];
+          at[k] = at[k + 1];
         }
+        v[K - 1] = -INFINITY;
+        at[K - 1] = -1;
       }
     }
-    float w = v;
-    int at_w = at;
-    first_of_warp(w, at_w);
-    if (at_w < 0) break;
-    if (lane == r) {
-      out_v = w;
-      out_at = at_w;
-    }
-    look = at_w == at;
-    any = true;
-    last_v = w;
-    last_at = at_w;
   }
-}
+};
 
 // The sums of one token, joined with others of it.
 struct Sums {
@@ -176,50 +184,74 @@ __global__ void __launch_bounds__(kSmallThreads) join_stretches(const __grid_con
   x.join_warp(g.scale2);
   if (lane == 0) write_token(g, row, x);
   if constexpr (K > 0) {
-    float v;
-    int at;
-    const int candidates = parts * K, n = (candidates - lane + 31) / 32;
-    select_first(g.top, n, [&](int c, float& y, int& at_y) {
-      const int e = lane + 32 * c;
-      const int2 b = g.best[place(e / K) * K + e % K];
-      y = __int_as_float(b.x);
-      at_y = b.y;
-    }, v, at);
+    // a stretch's list is in order: a lane takes one at a time
+    float v = -INFINITY;
+    int at = -1;
+    for (int q0 = 0; q0 < parts; q0 += 32) {
+      List<K> list;
+      list.clear();
+      if (q0 + lane < parts) {
+        const int2* from = g.best + place(q0 + lane) * K;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const int2 b = from[k];
+          list.v[k] = __int_as_float(b.x);
+          list.at[k] = b.y;
+        }
+      }
+      float w;
+      int w_at;
+      list.first_of_lanes(g.top, w, w_at);
+      if (q0 > 0) {
+        // what there was before in the lower lanes, these in the upper ones
+        List<1> one;
+        const float there = __shfl_sync(0xffffffffu, w, lane & 15);
+        const int there_at = __shfl_sync(0xffffffffu, w_at, lane & 15);
+        one.v[0] = lane < 16 ? v : there;
+        one.at[0] = lane < 16 ? at : there_at;
+        one.first_of_lanes(g.top, w, w_at);
+      }
+      v = w;
+      at = w_at;
+    }
     write_top(g, row, x, v, at);
   }
 }
 
 // The same of kFew's groups of 32 rows, which are many: a block a token.
-template <bool TOP>
+// K: the length of its lists, 0 without alternatives.
+template <int K>
 __global__ void __launch_bounds__(kSmallThreads) join_groups(const __grid_constant__ Combine g) {
-  __shared__ Sums of_warp[kSmallThreads / 32];
-  __shared__ float group_max[kSmallThreads / 32][kMostTop];
-  __shared__ int group_at[kSmallThreads / 32][kMostTop];
+  constexpr int kWarps = kSmallThreads / 32, kList = K > 0 ? K : 1;
+  __shared__ Sums of_warp[kWarps];
+  __shared__ float group_max[kWarps][kList];
+  __shared__ int group_at[kWarps][kList];
   allow_next();
   await_previous();
   const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float4* p = g.sums + static_cast<int64_t>(row) * g.n_tiles;
   Sums x = {-INFINITY, 0.f, 0.f};
-  for (int k0 = threadIdx.x; k0 < g.n_tiles; k0 += 4 * kSmallThreads) {
-    float4 y[4];
+  // the groups with the largest maxima hold the largest logits: of this thread's groups first
+  List<kList> list;
+  list.clear();
+  for (int k0 = threadIdx.x; k0 < g.n_tiles; k0 += 8 * kSmallThreads) {
+    float4 y[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 8; ++k)
       y[k] = k0 + kSmallThreads * k < g.n_tiles ? p[k0 + kSmallThreads * k] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x.join(y[k].x, y[k].y, y[k].z, g.scale2);
+    for (int k = 0; k < 8; ++k) {
+      x.join(y[k].x, y[k].y, y[k].z, g.scale2);
+      if (K > 0 && y[k].x != -INFINITY) list.offer(y[k].x, k0 + kSmallThreads * k);
+    }
   }
   x.join_warp(g.scale2);
   if (lane == 0) of_warp[warp] = x;
-  if (TOP) {
-    // the groups with the largest maxima, which hold the largest logits: of this warp's groups first
+  if constexpr (K > 0) {
     float v;
     int at;
-    const int mine = g.n_tiles - static_cast<int>(threadIdx.x);
-    select_first(g.top, (mine + kSmallThreads - 1) / kSmallThreads, [&](int c, float& y, int& at_y) {
-      at_y = static_cast<int>(threadIdx.x) + c * kSmallThreads;
-      y = p[at_y].x;
-    }, v, at);
-    if (lane < kMostTop) {
+    list.first_of_lanes(g.top, v, at);
+    if (lane < K) {
       group_max[warp][lane] = v;
       group_at[warp][lane] = at;
     }
@@ -227,48 +259,32 @@ __global__ void __launch_bounds__(kSmallThreads) join_groups(const __grid_consta
   __syncthreads();
   if (warp > 0) return;
   x = of_warp[0];
-  for (int k = 1; k < kSmallThreads / 32; ++k) x.join(of_warp[k].top, of_warp[k].sum, of_warp[k].tilt, g.scale2);
+  for (int k = 1; k < kWarps; ++k) x.join(of_warp[k].top, of_warp[k].sum, of_warp[k].tilt, g.scale2);
   if (lane == 0) write_token(g, row, x);
-  if (TOP) {
+  if constexpr (K > 0) {
     float v;
     int at;
-    select_first(g.top, kSmallThreads / 32 * kMostTop / 32, [&](int c, float& y, int& at_y) {
-      const int e = lane + 32 * c;
-      y = group_max[e / kMostTop][e % kMostTop];
-      at_y = group_at[e / kMostTop][e % kMostTop];
-    }, v, at);
-    // then the logits of those groups, 32 each
-    float logit[kMostTop];
-    int place[kMostTop];
 #pragma unroll
-    for (int k = 0; k < kMostTop; ++k) {
+    for (int k = 0; k < K; ++k) {
+      list.v[k] = lane < kWarps ? group_max[lane % kWarps][k] : -INFINITY;
+      list.at[k] = lane < kWarps ? group_at[lane % kWarps][k] : -1;
+    }
+    list.first_of_lanes(g.top, v, at);
+    // then the logits of those groups, 32 each
+    float logit[K];
+    int place[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
       const int group = __shfl_sync(0xffffffffu, at, k);
       place[k] = group * 32 + lane;
       logit[k] = group >= 0 ? g.logits[row * g.logit_stride + place[k]] : -INFINITY;
-      if (logit[k] == -INFINITY || isnan(logit[k])) place[k] = -1;
     }
-    float best_v = -INFINITY, last_v = 0.f;
-    int best_at = -1, last_at = -1;
-    for (int r = 0; r < g.top; ++r) {
-      float w = -INFINITY;
-      int at_w = -1;
+    list.clear();
 #pragma unroll
-      for (int k = 0; k < kMostTop; ++k)
-        if (place[k] >= 0 && (r == 0 || before(last_v, last_at, logit[k], place[k])) &&
-            before(logit[k], place[k], w, at_w)) {
-          w = logit[k];
-          at_w = place[k];
-        }
-      first_of_warp(w, at_w);
-      if (at_w < 0) break;
-      if (lane == r) {
-        best_v = w;
-        best_at = at_w;
-      }
-      last_v = w;
-      last_at = at_w;
-    }
-    write_top(g, row, x, best_v, best_at);
+    for (int k = 0; k < K; ++k)
+      if (logit[k] > -INFINITY) list.offer(logit[k], place[k]);
+    list.first_of_lanes(g.top, v, at);
+    write_top(g, row, x, v, at);
   }
 }
 
@@ -399,7 +415,7 @@ extern "C" int zero_lm_logprobs(int64_t tokens, int64_t vocab, int64_t width, in
                  static_cast<int>(count), pairs_for(sp.tiles), sp.tiles, sp.few ? sp.m_tiles * 8 : sp.n_tiles, top,
                  g.scale2, logp + i0, lse + i0, entropy + i0, top > 0 ? top_logp + i0 * top : nullptr,
                  top > 0 ? top_ids + i0 * top : nullptr};
-    const auto fn = sp.few ? (top > 0 ? join_groups<true> : join_groups<false>)
+    const auto fn = sp.few ? (list_length(top) == 0 ? join_groups<0> : list_length(top) == 8 ? join_groups<8> : join_groups<16>)
                            : (list == 0 ? join_stretches<0> : list == 8 ? join_stretches<8> : join_stretches<16>);
     const int64_t team = sp.few ? kSmallThreads : 32;
     const dim3 grid(static_cast<unsigned>(ceil_div(count * team, kSmallThreads)));
