@@ -1099,10 +1099,10 @@ class LmLogprobs(_Owner):
         """(logp, entropy, lse) of each token, fp32; with ``top`` also the alternatives' log probabilities and ids
         (tokens x top, fp32 and int32, the likeliest first).  logp is 0 where the target lies outside the vocabulary."""
         tokens, operands = self._operands(hidden, table, targets)
-        logp, entropy, lse = self._empty((3, tokens), self._fp32).unbind()
+        logp, entropy, lse = self._empty(tokens, self._fp32), self._empty(tokens, self._fp32), self._empty(tokens, self._fp32)
         outs, top_logp, top_ids = (logp, entropy, lse), None, None
         if self.top:
-            values, ids = (self._empty((tokens, self.top), t) for t in (self._fp32, self.torch.int32))
+            values, ids = self._empty((tokens, self.top), self._fp32), self._empty((tokens, self.top), self.torch.int32)
             outs, top_logp, top_ids = outs + (values, ids), values.data_ptr(), ids.data_ptr()
         self._logprobs(*operands, self.top, logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top_logp, top_ids,
                        self._ws, self.workspace_bytes, self._raw_stream())
@@ -1322,7 +1322,7 @@ class Orthogonalize(_Matrices):
         """The orthogonalised matrices, written to ``out`` (which may be the matrices themselves) or to new memory."""
         (ins, ins_at), (si, si_at) = self._addresses(matrices, "matrices")
         if out is None:
-            out = self.views(self._empty(self.n, self.torch_dtype))
+            out = [self._empty(s, self.torch_dtype) for s in self.shapes]
         (outs, outs_at), (so, so_at) = self._addresses(out, "out")
         self._call(len(self.shapes), self._rows_at, self._cols_at, self.dtype, ins_at, si_at, outs_at, so_at,
                    self.steps, self._co_at, self.fine_steps, self._ws, self.workspace_bytes, self._raw_stream())
