@@ -604,6 +604,12 @@ def zero_lm_inject_stall() -> None:
 _DT = {"fp16": ZERO_FP16, "bf16": ZERO_BF16, ZERO_FP16: ZERO_FP16, ZERO_BF16: ZERO_BF16}
 
 
+def _zeros_on(device):
+    """The owners' allocator; it holds no owner, whose buffers are then freed with it and not by the next collection."""
+    import torch
+    return lambda numel, dtype: torch.zeros(numel, dtype=dtype, device=device)
+
+
 class ZeroStep:
     """Buffers for one configuration, allocated with PyTorch on ``device``,
     plus the library context that uses them.
@@ -629,7 +635,7 @@ class ZeroStep:
         self.device = torch.device(device)
         t16 = {ZERO_FP16: torch.float16, ZERO_BF16: torch.bfloat16}
         self.grad_torch_dtype, self.work_torch_dtype = t16[self.gdt], t16[self.wdt]
-        self._alloc = alloc or (lambda numel, dtype: torch.zeros(numel, dtype=dtype, device=self.device))
+        self._alloc = alloc or _zeros_on(self.device)
         f32, w16 = torch.float32, self.work_torch_dtype
         self.master = self._alloc(self.n_pad, f32)
         self.m = self._alloc(self.n_pad, f32)
@@ -753,7 +759,7 @@ class DpReplicas:
             if need > free:
                 raise MemoryError(f"{self.W} replicas of {self.n_pad} parameters need {need} bytes of device "
                                   f"memory; {free} are free")
-        self._alloc = alloc or (lambda numel, dtype: torch.zeros(numel, dtype=dtype, device=self.device))
+        self._alloc = alloc or _zeros_on(self.device)
         self.master = [self._alloc(self.n_pad, torch.float32) for _ in range(self.W)]
         self.m = [self._alloc(self.n_pad, torch.float32) for _ in range(self.W)]
         self.v = [self._alloc(self.n_pad, torch.float32) for _ in range(self.W)]
@@ -828,7 +834,7 @@ class ZeroOffload:
         self.master, self.m, self.v, self.host_grad, self.host_p16 = views
         if theta0 is not None:
             self.master[: self.n].copy_(torch.as_tensor(theta0, dtype=torch.float32).cpu())
-        self._alloc = alloc or (lambda numel, dtype: torch.zeros(numel, dtype=dtype, device=self.device))
+        self._alloc = alloc or _zeros_on(self.device)
         self.p16 = self._alloc(self.n_pad, self.work_torch_dtype)
         self.staging_bytes = zero_offload_staging_bytes(chunk_elems)
         self.staging = self._alloc(self.staging_bytes, torch.uint8)
@@ -1352,7 +1358,7 @@ class MuonStep(_Matrices):
         self.scales = None if scales is None else [float(x) for x in scales]
         self._sc, self._sc_at = (None, None) if scales is None else _c_array("d", self.scales)
         self._workspace(zero_muon_workspace_bytes(self.W, self.shapes), zero=4)
-        new = alloc or (lambda numel, dtype: torch.zeros(numel, dtype=dtype, device=self.device))
+        new = alloc or _zeros_on(self.device)
         work = {ZERO_FP16: torch.float16, ZERO_BF16: torch.bfloat16}[self.wdt]
         with _on(self.stream, self.device):
             self.master, self.momentum = new(self.n, torch.float32), new(self.n, torch.float32)
