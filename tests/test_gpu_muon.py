@@ -199,7 +199,8 @@ def check_step(op, grads, lr, mu, nesterov, decay, what=""):
         assert not v[~used].any()          # the padding between the matrices
 
 
-STEP_SHAPES = [[(1, 1), (5, 3)], [(64, 96), (96, 64), (64, 64)], [(100, 37), (33, 130), (7, 7)], [(300, 200), (256, 512)]]
+STEP_SHAPES = [[(1, 1), (5, 3)], [(64, 96), (96, 64), (64, 64)], [(100, 37), (33, 130), (7, 7)], [(300, 200), (256, 512)],
+               [(301, 203), (203, 301), (150, 1001)], [(520, 264), (30, 9), (131, 700)]]
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
