@@ -36,8 +36,12 @@
  * It also holds the operators that stand next to the step in a language
  * model's training: the global gradient norm and clipping (zero_grad_norm,
  * zero_grad_clip, zero_step_clipped), the embedding lookup and its gradient
- * (zero_embedding, zero_embedding_grad), and the cross entropy over a large
- * vocabulary with its gradients (zero_lm_loss, zero_lm_loss_grad).
+ * (zero_embedding, zero_embedding_grad), the cross entropy over a large
+ * vocabulary with its gradients (zero_lm_loss, zero_lm_loss_grad), the log
+ * probabilities of given tokens with entropy, alternatives and gradients
+ * (zero_lm_logprobs, zero_lm_logprobs_grad), and for matrices Newton-Schulz
+ * orthogonalisation and the optimizer step built on it (zero_orthogonalize,
+ * zero_muon_step).
  *
  * Layout.  n real parameters are split into units (one unit for data
  * parallel, ZeRO-1 and ZeRO-2; the caller's units, e.g. one per transformer
@@ -96,7 +100,7 @@ extern "C" {
 /* ---- 16-bit formats ---------------------------------------------------- */
 #define ZERO_FP16       0
 #define ZERO_BF16       1
-#define ZERO_FP32       2   /* zero_grad_norm and zero_grad_clip only            */
+#define ZERO_FP32       2   /* zero_grad_norm, zero_grad_clip, zero_orthogonalize */
 
 /* ---- accounting kinds --------------------------------------------------- */
 #define ZERO_RESIDENT   0
