@@ -711,7 +711,8 @@ __device__ __forceinline__ unsigned end_of(const PassArgs& p, int which) {
 // The first pass: sums of squares, in fp32 within a thread and in fp64 beyond
 // (and the mean gradient, kept where that pays).  A block goes over a stretch of
 // the tiles and leaves a sum for each matrix that it meets, at [block + entry].
-template <typename T, bool MUON>
+// WC > 0: so many ranks, known at compile time; 0: any number.
+template <typename T, bool MUON, int WC>
 __global__ void __launch_bounds__(kPassThreads) sum_squares(const __grid_constant__ PassArgs p) {
   allow_next();
   await_previous();
@@ -727,9 +728,47 @@ __global__ void __launch_bounds__(kPassThreads) sum_squares(const __grid_constan
       const int col = (tile - ty * across) * kPassCols + static_cast<int>(threadIdx.x & 31) * 8;
       const int n = e.cols - col;
       float squares = 0.f;
+      const int first_row = ty * kPassRows + static_cast<int>(threadIdx.x >> 5);
+      if (MUON && WC > 0 && e.wide) {
+        // two rows' loads at a time, before the first store; of 8 ranks one row's (two take 176 registers, and 139 us
+        // for 28M elements where one takes 120)
+        constexpr int kAtOnce = WC >= 8 ? 1 : 2;
+        const uint64_t* ranks = p.grads + static_cast<int64_t>(which) * p.W;
+#pragma unroll
+        for (int r = 0; r < kPassRows / 8; r += kAtOnce) {
+          uint4 raw[kAtOnce][WC > 0 ? WC : 1];
+          float m[kAtOnce][8];
+          bool here[kAtOnce];
+          int64_t at[kAtOnce];
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+            const int row = first_row + (r + j) * 8;
+            here[j] = row < e.rows && n > 0;
+            at[j] = static_cast<int64_t>(row) * e.cols + col;
+            if (!here[j]) continue;
+#pragma unroll
+            for (int w = 0; w < WC; ++w) raw[j][w] = dev::ld_16B(reinterpret_cast<const T*>(ranks[w]) + at[j]);
+            dev::ld_32B(e.momentum + at[j], m[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+            if (!here[j]) continue;
+            float g[8];
+            if constexpr (!std::is_same<T, float>::value) mean_of<T, (WC > 0 ? WC : 1)>(raw[j], g);
+            if (e.mean != nullptr) dev::st_32B(e.mean + at[j], g);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float now = __fmaf_rn(p.mu, m[j][k], g[k]), u = p.nesterov ? __fmaf_rn(p.mu, now, g[k]) : now;
+              squares = fmaf(u, u, squares);
+            }
+          }
+        }
+        all += squares;
+        continue;
+      }
 #pragma unroll
       for (int r = 0; r < kPassRows / 8; ++r) {
-        const int row = ty * kPassRows + r * 8 + static_cast<int>(threadIdx.x >> 5);
+        const int row = first_row + r * 8;
         if (row >= e.rows || n <= 0) continue;
         float u[8], m[8];
         direction8<T, MUON>(p, e, which, row, col, n, true, u, m);
@@ -741,6 +780,27 @@ __global__ void __launch_bounds__(kPassThreads) sum_squares(const __grid_constan
     }
     all = block_sum(all);
     if (threadIdx.x == 0) p.part[blockIdx.x + which] = all;
+  }
+}
+
+// A row's values on their way to X: times the power of two, in their parts, to
+// their place or to be turned.
+__device__ __forceinline__ void to_first(const PassArgs& p, const Entry& e, int row, int col, int in_tile, float scale,
+                                         float (&u)[8], uint32_t* turned) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) u[k] = scale != 0.f ? u[k] * scale : 0.f;
+  uint4 hi, lo;
+  split8(u, hi, lo);
+  if (!e.transposed) {
+    // columns past the last, up to the boundary of 8, are not read again
+    uint16_t* to = e.x + row * e.ld + col;
+    dev::st_16B(to, hi);
+    if (p.two) dev::st_16B(to + e.x_part, lo);
+  } else {
+    const uint16_t *h = reinterpret_cast<const uint16_t*>(&hi), *l = reinterpret_cast<const uint16_t*>(&lo);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      turned[((threadIdx.x & 31) * 8 + k) * (kPassRows + 1) + in_tile] = h[k] | static_cast<uint32_t>(l[k]) << 16;
   }
 }
 
@@ -774,27 +834,44 @@ __global__ void __launch_bounds__(kPassThreads) make_first(const __grid_constant
       const int tile = static_cast<int>(t - tile0), ty = tile / across, col0 = (tile - ty * across) * kPassCols;
       const int col = col0 + static_cast<int>(threadIdx.x & 31) * 8, n = e.cols - col;
       if (e.transposed) __syncthreads();   // the tile before has been written
+      const int warp_row = static_cast<int>(threadIdx.x >> 5), first_row = ty * kPassRows + warp_row;
+      if (MUON && e.mean != nullptr && e.wide) {
+        // two rows' loads at a time, before the first store
 #pragma unroll
-      for (int r = 0; r < kPassRows / 8; ++r) {
-        const int in_tile = r * 8 + static_cast<int>(threadIdx.x >> 5), row = ty * kPassRows + in_tile;
-        if (row >= e.rows || n <= 0) continue;
-        float u[8], m[8];
-        direction8<T, MUON>(p, e, which, row, col, n, false, u, m);
-        if (MUON && finite) store_some(e.momentum + static_cast<int64_t>(row) * e.cols + col, e.wide, n, m);
+        for (int r = 0; r < kPassRows / 8; r += 2) {
+          float g[2][8], m[2][8];
+          bool here[2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) u[k] = finite ? u[k] * scale : 0.f;
-        uint4 hi, lo;
-        split8(u, hi, lo);
-        if (!e.transposed) {
-          // columns past the last, up to the boundary of 8, are not read again
-          uint16_t* to = e.x + row * e.ld + col;
-          dev::st_16B(to, hi);
-          if (p.two) dev::st_16B(to + e.x_part, lo);
-        } else {
-          const uint16_t *h = reinterpret_cast<const uint16_t*>(&hi), *l = reinterpret_cast<const uint16_t*>(&lo);
+          for (int j = 0; j < 2; ++j) {
+            const int row = first_row + (r + j) * 8;
+            const int64_t at = static_cast<int64_t>(row) * e.cols + col;
+            here[j] = row < e.rows && n > 0;
+            if (!here[j]) continue;
+            dev::ld_32B(e.mean + at, g[j]);
+            dev::ld_32B(e.momentum + at, m[j]);
+          }
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            turned[((threadIdx.x & 31) * 8 + k) * (kPassRows + 1) + in_tile] = h[k] | static_cast<uint32_t>(l[k]) << 16;
+          for (int j = 0; j < 2; ++j) {
+            if (!here[j]) continue;
+            const int in_tile = warp_row + (r + j) * 8, row = ty * kPassRows + in_tile;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              m[j][k] = __fmaf_rn(p.mu, m[j][k], g[j][k]);
+              g[j][k] = p.nesterov ? __fmaf_rn(p.mu, m[j][k], g[j][k]) : m[j][k];
+            }
+            if (finite) dev::st_32B(e.momentum + static_cast<int64_t>(row) * e.cols + col, m[j]);
+            to_first(p, e, row, col, in_tile, scale, g[j], turned);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < kPassRows / 8; ++r) {
+          const int in_tile = r * 8 + warp_row, row = ty * kPassRows + in_tile;
+          if (row >= e.rows || n <= 0) continue;
+          float u[8], m[8];
+          direction8<T, MUON>(p, e, which, row, col, n, false, u, m);
+          if (MUON && finite) store_some(e.momentum + static_cast<int64_t>(row) * e.cols + col, e.wide, n, m);
+          to_first(p, e, row, col, in_tile, scale, u, turned);
         }
       }
       if (e.transposed) {
@@ -1044,7 +1121,14 @@ template <typename T, bool MUON>
 int launch_passes(const PassArgs& p, cudaStream_t s) {
   const int64_t most = std::min(static_cast<int64_t>(sm_count()) * kPassBlocksPerSm, kMostPassBlocks);
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(p.tiles, most)));
-  ZERO_CUDA(launch_chained(sum_squares<T, MUON>, grid, kPassThreads, 0, s, p));
+  auto first = sum_squares<T, MUON, 0>;
+  if constexpr (MUON) {
+    if (p.W == 1) first = sum_squares<T, MUON, 1>;
+    if (p.W == 2) first = sum_squares<T, MUON, 2>;
+    if (p.W == 4) first = sum_squares<T, MUON, 4>;
+    if (p.W == 8) first = sum_squares<T, MUON, 8>;
+  }
+  ZERO_CUDA(launch_chained(first, grid, kPassThreads, 0, s, p));
   ZERO_CUDA(launch_chained(make_first<T, MUON>, grid, kPassThreads, 0, s, p));
   return ZERO_OK;
 }

@@ -237,6 +237,20 @@ __device__ __forceinline__ void rank_mean8(const uint64_t* grads, int W, int64_t
   for (int k = 0; k < 8; ++k) g[k] = dev::rank_mean(g[k], W, inv_w, pow2);
 }
 
+// The same of values that have been loaded.
+template <typename T, int WC>
+__device__ __forceinline__ void mean_of(const uint4 (&raw)[WC], float (&g)[8]) {
+#pragma unroll
+  for (int w = 0; w < WC; ++w) {
+    float f[8];
+    Fmt<T>::unpack8(raw[w], f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] = w == 0 ? f[k] : __fadd_rn(g[k], f[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) g[k] = dev::rank_mean(g[k], WC, 1.f / WC, (WC & (WC - 1)) == 0);
+}
+
 // 8 values of an fp32 vector; those that do not exist read as 0.
 __device__ __forceinline__ void load_some(const float* p, bool wide, int n, float (&f)[8]) {
   if (wide) {
