@@ -20,6 +20,9 @@
 //   kPoly   A A likewise, with P formed in its epilogue
 //   kApply  P X; of the last step its epilogue writes the caller's matrix or
 //           updates the master and the 16-bit copy in place.
+//   kMultiply  of wide matrices (n >= 2 m), whose steps go by twos: with P_0 of A
+//           the second A is P_0 A P_0, the second P, P_1, of that, and X <- P_1 P_0 X:
+//           3 n / m + 5 units of work for two steps instead of 6 n / m + 2
 // Pairs of CTAs take tiles from a counter in the list's order; a tile waits until
 // every tile of its matrix's product before has been written, which another
 // counter for each matrix says.  What a tile waits for has a lower number, so
@@ -96,27 +99,40 @@ constexpr int kRunSmem = kStages * kStageBytes + 1024;
 constexpr int kFewGroups = 3, kMaxGroups = 12;       // shapes of one launch
 constexpr int64_t kPairs = 76;       // pairs of CTAs among GB300's 152 SMs
 
-enum Kind : int { kGram, kPoly, kApply, kLast, kUpdate };
+enum Kind : int { kGram, kPoly, kMultiply, kApply };
+enum Final : int { kLast, kUpdate };       // what the last product does
+enum Buffer : int { kX0, kX1, kA, kP, kT, kBuffers };
+constexpr float kScaleT = 2048.f;          // of P A while two steps are joined
+constexpr int kMaxPhases = 7 * kMaxSteps / 2;
+
+// A product of a shape's list.
+struct Phase {
+  int8_t kind, a, b, out;            // its operands' and result's buffers
+  int8_t step, parts_a, parts_b, two;   // kPoly: whose coefficients; the operands' parts; whether a low part is written
+  int8_t units, fine, last, unused;  // powers of what the first X lacks of the norm; two parts in this step; the last
+  float factor;                      // from the sums to what is written
+};
+// What the width of the tiles goes by.
+__host__ __device__ constexpr int class_of(int kind) { return kind == kGram ? 0 : kind == kApply ? 2 : 1; }
 
 // The matrices of one shape.
 struct Shape {
-  CUtensorMap x[2], a, p;            // loads in boxes of 128 rows x 64
-  CUtensorMap x64[2], a64, p64;      // of 64 x 64
-  CUtensorMap x32[2], a32;           // of 32 x 64
+  CUtensorMap box128[kBuffers], box64[kBuffers], box32[kBuffers];   // loads of so many rows x 64
+  uint16_t* at[kBuffers];
   int matrices, first;               // how many, the first one's entry
   int m, n;
-  int bn[2][3];                      // columns of a tile of each kind: 64, 128 or 256; of one part, of two
+  int joined;                        // which list
+  int bn[2][3];                      // columns of a tile by class: 64, 128 or 256; of one part, of two
   int tiles[2][3];                   // of one matrix
-  uint16_t *x_at[2], *a_at, *p_at;
   int64_t ldx, lda, apart_x, apart_a, part_x, part_a;    // rows, matrices, parts
 };
 
 template <int GROUPS>
 struct RunArgs {
   Shape shape[GROUPS];
+  Phase phase[2][kMaxPhases];  // steps one by one, and by twos
+  int phases[2];
   int shapes;
-  int tiles[2][3];             // of a step, by kind
-  int steps, fine, first_parts;
   int dtype;                   // kLast: of the results; kUpdate: of the 16-bit copies
   int stall;                   // testing the bounded waits: the first tile's first block of K never arrives
   const Entry* entries;
@@ -134,7 +150,7 @@ struct RunArgs {
 struct alignas(16) Tile {
   int kind;                    // -1: no more
   int shape, matrix, mt;
-  int nt, step, kb, bn;        // kb: blocks of K
+  int nt, phase, kb, bn;       // kb: blocks of K
 };
 
 // Tiles of a row of tiles that hold something on or below the diagonal.
@@ -143,69 +159,70 @@ __host__ __device__ inline int tiles_of_row(int mt, int bn, int n_tiles) {
   return reach < n_tiles ? reach : n_tiles;
 }
 
-// Tile t of the list; `before`: the tiles of its matrix's products before.
+// Where in the list a pair is: its tiles come in rising order.
+struct Cursor {
+  int phase = 0, shape = 0;
+  unsigned start = 0;          // the first tile of this phase and shape
+};
+
+// Tile t of the list, at or after the cursor.  before[h]: the tiles of one
+// matrix's products before, for each shape up to the cursor.
 template <int GROUPS>
-__device__ __forceinline__ Tile locate(const RunArgs<GROUPS>& g, unsigned t, unsigned& before) {
+__device__ __forceinline__ Tile locate(const RunArgs<GROUPS>& g, unsigned t, Cursor& c, unsigned* before) {
   Tile x = {};
-  // the fine steps first
-  int fine = 1;
-  unsigned each = g.tiles[1][0] + g.tiles[1][1] + g.tiles[1][2];
-  const unsigned in_fine = each * g.fine;
-  if (t >= in_fine) {
-    fine = 0;
-    each = g.tiles[0][0] + g.tiles[0][1] + g.tiles[0][2];
-    t -= in_fine;
-    x.step = g.fine;
-  }
-  const int further = static_cast<int>(t / each);
-  x.step += further;
-  if (x.step >= g.steps) {
+  unsigned each = 0;
+  for (;;) {
+    const Shape& h = g.shape[c.shape];
+    each = 0;
+    if (c.phase < g.phases[h.joined]) {
+      const Phase& f = g.phase[h.joined][c.phase];
+      each = h.tiles[f.fine][class_of(f.kind)];
+    }
+    const unsigned count = each * h.matrices;
+    if (t < c.start + count) break;
+    c.start += count;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) before[c.shape] += each;
+    __syncwarp();
+    if (++c.shape < g.shapes) continue;
+    c.shape = 0;
+    if (++c.phase < max(g.phases[0], g.phases[1])) continue;
     x.kind = -1;
     return x;
   }
-  int r = static_cast<int>(t - further * each);
-  while (r >= g.tiles[fine][x.kind]) r -= g.tiles[fine][x.kind++];
-  while (r >= g.shape[x.shape].matrices * g.shape[x.shape].tiles[fine][x.kind]) {
-    r -= g.shape[x.shape].matrices * g.shape[x.shape].tiles[fine][x.kind];
-    ++x.shape;
-  }
-  const Shape& h = g.shape[x.shape];
-  const int* of_kind = h.tiles[fine];
-  x.matrix = static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(of_kind[x.kind]));
-  r -= x.matrix * of_kind[x.kind];
-  before = further * (of_kind[0] + of_kind[1] + of_kind[2]);
-  if (!fine) before += g.fine * (h.tiles[1][0] + h.tiles[1][1] + h.tiles[1][2]);
-  for (int k = 0; k < x.kind; ++k) before += of_kind[k];
-  const int bn = x.bn = h.bn[fine][x.kind];
-  if (x.kind < kApply) {
+  const Shape& h = g.shape[c.shape];
+  const Phase& f = g.phase[h.joined][c.phase];
+  x.kind = f.kind;
+  x.shape = c.shape;
+  x.phase = c.phase;
+  unsigned r = t - c.start;
+  x.matrix = static_cast<int>(r / each);
+  r -= x.matrix * each;
+  const int bn = x.bn = h.bn[f.fine][class_of(f.kind)];
+  if (f.kind == kApply) {
+    const unsigned m_tiles = (h.m + kTileM - 1) / kTileM;
+    x.nt = static_cast<int>(r / m_tiles);
+    x.mt = static_cast<int>(r - x.nt * m_tiles);
+  } else {
     const int n_tiles = (h.m + bn - 1) / bn;
     for (;;) {
-      const int n = tiles_of_row(x.mt, bn, n_tiles);
+      const unsigned n = tiles_of_row(x.mt, bn, n_tiles);
       if (r < n) break;
       r -= n;
       ++x.mt;
     }
-    x.nt = r;
-  } else {
-    const unsigned m_tiles = (h.m + kTileM - 1) / kTileM;
-    x.nt = static_cast<int>(static_cast<unsigned>(r) / m_tiles);
-    x.mt = r - x.nt * static_cast<int>(m_tiles);
+    x.nt = static_cast<int>(r);
   }
-  x.kb = ((x.kind == kGram ? h.n : h.m) + kTileK - 1) / kTileK;
+  x.kb = ((f.kind == kGram ? h.n : h.m) + kTileK - 1) / kTileK;
   return x;
 }
 
-// The operands' parts in a tile's product.
-struct Parts {
-  int a, b;
-};
 template <int GROUPS>
-__device__ __forceinline__ Parts parts_of(const RunArgs<GROUPS>& g, const Tile& x) {
-  const int parts = x.step < g.fine ? 2 : 1, of_x = x.step == 0 ? min(parts, g.first_parts) : parts;
-  return {x.kind == kGram ? of_x : parts, x.kind == kPoly ? parts : of_x};
+__device__ __forceinline__ const Phase& phase_of(const RunArgs<GROUPS>& g, const Tile& x) {
+  return g.phase[g.shape[x.shape].joined][x.phase];
 }
 
-// Of A and P the blocks above the diagonal are not there: block kb of K of the
+// Of the symmetric matrices the blocks above the diagonal are not there: block kb of K of the
 // operand whose rows begin at `row` is read with rows and columns exchanged
 // where its columns lie in a later block of 256 than its rows.
 __device__ __forceinline__ bool exchanged(int row, int kb) { return kb * kTileK / kTileM > row / kTileM; }
@@ -213,7 +230,7 @@ __device__ __forceinline__ bool exchanged(int row, int kb) { return kb * kTileK 
 // Whether block kb of K of a tile's B has K as its row index, and the bytes of B's
 // half tile for one CTA: rows of K-major, or whole boxes of 64 columns.
 __device__ __forceinline__ bool b_is_mn(const Tile& x, int kb) {
-  return x.kind == kApply || (x.kind == kPoly && exchanged(x.nt * x.bn, kb));
+  return x.kind == kApply || (x.kind != kGram && exchanged(x.nt * x.bn, kb));
 }
 __device__ __forceinline__ uint32_t b_bytes(const Tile& x, int kb) {
   const int half = x.bn / 2;
@@ -257,16 +274,17 @@ template <int FINAL, int GROUPS>
 __device__ __forceinline__ void fetch(const RunArgs<GROUPS>& g, const Tile& x, int row, int c, Beside& b) {
   const Shape& h = g.shape[x.shape];
   const int col0 = x.nt * x.bn + c;
+  const Phase& f = phase_of(g, x);
   if (x.kind == kPoly) {
     if (row >= h.m || col0 >= h.m) return;
     // A's rows are padded to 16 values: what is read past the last column is not used
-    const uint16_t* a = h.a_at + x.matrix * h.apart_a + row * h.lda + col0;
+    const uint16_t* a = h.at[f.a] + x.matrix * h.apart_a + row * h.lda + col0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       b.w[k] = ld_fresh(a + 8 * k);
-      if (x.step < g.fine) b.w[2 + k] = ld_fresh(a + h.part_a + 8 * k);
+      if (f.fine) b.w[2 + k] = ld_fresh(a + h.part_a + 8 * k);
     }
-  } else if (FINAL == kUpdate && x.kind == kApply && x.step + 1 == g.steps) {
+  } else if (FINAL == kUpdate && f.last) {
     if (row >= h.m || col0 >= h.n) return;
     read_master<kCols>(g.entries[h.first + x.matrix], h.n, row, col0, b.w);
   }
@@ -292,25 +310,31 @@ __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x
   const Shape& h = g.shape[x.shape];
   const int bn = x.bn, n0 = x.nt * bn;
   const int which = h.first + x.matrix;
-  const float unit = x.step == 0 ? g.norms[which].unit : 1.f;     // what the first X lacks of the norm
-  const bool two = x.step < g.fine;
-  if (x.kind == kGram) {
-    const float scale = unit * unit * (kScaleA / (kScaleX * kScaleX));
+  const Phase& f = phase_of(g, x);
+  float scale = f.factor;
+  if (f.units > 0) {
+    const float unit = g.norms[which].unit;
+    scale *= f.units > 1 ? unit * unit : unit;
+  }
+  const bool two = f.two;
+  if (x.kind == kGram || x.kind == kMultiply) {
+    uint16_t* out = h.at[f.out] + x.matrix * h.apart_a;
     each_16(tmem, share * kCols, bn, [&](int c, float (&v)[kCols]) {
 #pragma unroll
       for (int k = 0; k < kCols; ++k) v[k] *= scale;
-      store_block(h.a_at + x.matrix * h.apart_a, h.lda, h.part_a, h.m, h.m, row, n0 + c, v, two);
+      store_block(out, h.lda, h.part_a, h.m, h.m, row, n0 + c, v, two);
     }, release);
   } else if (x.kind == kPoly) {
-    const float a = g.coefficients[3 * x.step] * kScaleP, once = g.coefficients[3 * x.step + 1] * (kScaleP / kScaleA);
-    const float square = g.coefficients[3 * x.step + 2] * (kScaleP / (kScaleA * kScaleA));
+    uint16_t* out = h.at[f.out] + x.matrix * h.apart_a;
+    const float a = g.coefficients[3 * f.step] * kScaleP, once = g.coefficients[3 * f.step + 1] * (kScaleP / kScaleA);
+    const float square = g.coefficients[3 * f.step + 2] * (kScaleP / (kScaleA * kScaleA));
     each_16(tmem, share * kCols, bn, [&](int c, float (&v)[kCols]) {
       const int col0 = n0 + c;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float u[8], l[8] = {};
         Fmt<__half>::unpack8(b.w[k], u);
-        if (two) Fmt<__half>::unpack8(b.w[2 + k], l);
+        if (f.fine) Fmt<__half>::unpack8(b.w[2 + k], l);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           v[8 * k + q] = fmaf(once, u[q] + l[q], square * v[8 * k + q]);
@@ -318,20 +342,19 @@ __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x
         }
       }
       if (c + 64 < bn) fetch<FINAL>(g, x, row, c + 64, b);
-      store_block(h.p_at + x.matrix * h.apart_a, h.lda, h.part_a, h.m, h.m, row, col0, v, two);
+      store_block(out, h.lda, h.part_a, h.m, h.m, row, col0, v, two);
     }, release);
-  } else if (x.step + 1 < g.steps) {
-    const float scale = unit / kScaleP;
+  } else if (!f.last) {
+    uint16_t* out = h.at[f.out] + x.matrix * h.apart_x;
     each_16(tmem, share * kCols, bn, [&](int c, float (&v)[kCols]) {
 #pragma unroll
       for (int k = 0; k < kCols; ++k) v[k] *= scale;
-      store_block(h.x_at[(x.step & 1) ^ 1] + x.matrix * h.apart_x, h.ldx, h.part_x, h.m, h.n, row, n0 + c, v,
-                  x.step + 1 < g.fine);
+      store_block(out, h.ldx, h.part_x, h.m, h.n, row, n0 + c, v, two);
     }, release);
   } else {
     const Entry& e = g.entries[which];
     const bool finite = g.norms[which].finite;
-    const float scale = finite ? unit / (kScaleP * kScaleX) : NAN;
+    if (!finite) scale = NAN;
     each_16(tmem, share * kCols, bn, [&](int c, float (&v)[kCols]) {
       // a norm that is not finite leaves the state as it was
       if (row >= h.m || n0 + c >= h.n || (FINAL == kUpdate && !finite)) return;
@@ -364,6 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
   __shared__ __align__(8) uint64_t bars[2 * kStages + 3 * kQueue + 6];
   __shared__ Tile queue[kQueue];
   __shared__ uint32_t tmem_slot;
+  __shared__ unsigned before[GROUPS];
   __shared__ int failed, last_out;
   const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
   const uint32_t bar0 = smem_addr(bars);
@@ -435,17 +459,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
       // what other CTAs' threads wrote is loaded through the async proxy
       fence_all_async();
       const Shape& h = g.shape[x.shape];
-      const Parts parts = parts_of(g, x);
-      const int bn = x.bn, depth = h.matrices, blocks = x.kb;
-      const CUtensorMap *map, *map64;     // K-major, and boxes of 64 columns with K as the row index
-      if (first) {
-        map = x.kind == kGram ? &h.x[x.step & 1] : x.kind == kPoly ? &h.a : &h.p;
-        map64 = x.kind == kPoly ? &h.a64 : &h.p64;
-      } else {
-        if (x.kind == kGram) map = bn == 256 ? &h.x[x.step & 1] : bn == 128 ? &h.x64[x.step & 1] : &h.x32[x.step & 1];
-        else map = bn == 256 ? &h.a : bn == 128 ? &h.a64 : &h.a32;
-        map64 = x.kind == kPoly ? &h.a64 : &h.x64[x.step & 1];
-      }
+      const Phase& f = phase_of(g, x);
+      const int bn = x.bn, depth = h.matrices, blocks = x.kb, parts_a = f.parts_a, parts_b = f.parts_b;
+      // K-major, and boxes of 64 columns with K as the row index
+      const int buffer = first ? f.a : f.b;
+      const CUtensorMap* map = first || bn == 256 ? &h.box128[buffer] : bn == 128 ? &h.box64[buffer] : &h.box32[buffer];
+      const CUtensorMap* map64 = &h.box64[buffer];
       // this CTA's rows (or columns) of the operand
       const int at = first ? x.mt * kTileM + static_cast<int>(rank) * 128 : x.nt * bn + static_cast<int>(rank) * (bn / 2);
       const bool second_box = first || bn == kTileN, counts = first && rank == 0;
@@ -453,10 +472,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
         const bool mn = first ? x.kind != kGram && exchanged(x.mt * kTileM, kb) : b_is_mn(x, kb);
         const uint32_t of_b = 2 * b_bytes(x, kb);
         const int k = kb * kTileK;
-        for (int part = 0; part < parts.a; ++part, ++issued) {
+        for (int part = 0; part < parts_a; ++part, ++issued) {
           // A stage without B is none of the second warp's: it may be used, and emptied, before that warp comes by,
           // and a wait for a phase that is two back never ends.
-          const bool with_b = part < parts.b;
+          const bool with_b = part < parts_b;
           if (first || with_b) ok = wait_all(empty(s), phase);
           if (!ok) break;
           if (lead && (first || with_b)) {
@@ -489,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
       for (int i = 0;; ++i) {
         const Tile x = tile_of(i);
         if (!ok || x.kind < 0) break;
-        const Parts parts = parts_of(g, x);
+        const Phase& f = phase_of(g, x);
         const uint32_t idesc = instr_desc(false, false, false, kTileM, x.bn);
         const int a = i & 1, blocks = x.kb, a_row = x.mt * kTileM;
         ok = wait_all(taken(a), ((i >> 1) & 1) ^ 1);
@@ -545,8 +564,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
         };
         using One = std::integral_constant<int, 1>;
         using Two = std::integral_constant<int, 2>;
-        if (parts.a == 1) run(One{}, One{});
-        else if (parts.b == 1) run(Two{}, One{});
+        if (f.parts_a == 1) run(One{}, One{});
+        else if (f.parts_b == 1) run(Two{}, One{});
         else run(Two{}, Two{});
         if (!ok) break;
         if (lead) mma_commit(done(a));
@@ -574,18 +593,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
     if (!ok && lead) failed = 1;
   } else if (warp == kTakerWarp) {
     // Takes the next tile when the leader begins to load the one before, waits for what it needs, and tells the roles.
+    Cursor cursor;
+    if (lane < GROUPS) before[lane] = 0;
+    __syncwarp();
     for (int i = 0; rank == 0; ++i) {
       const int q = i % kQueue;
       ok = wait_all(heard(q), ((i / kQueue) & 1) ^ 1);
       if (ok && i > 0) ok = wait_all(began, (i - 1) & 1);
       if (!ok) break;
-      unsigned t = 0, before = 0;
+      unsigned t = 0;
       if (lead) t = atomicAdd(g.next, 1u);
       t = __reduce_max_sync(0xffffffffu, t);
-      const Tile x = locate(g, t, before);
-      if (x.kind >= 0 && before > 0) {
+      const Tile x = locate(g, t, cursor, before);
+      if (x.kind >= 0 && before[x.shape] > 0) {
         const unsigned* p = g.written + g.shape[x.shape].first + x.matrix;
-        const unsigned want = before * 2;
+        const unsigned want = before[x.shape] * 2;
         bool there = true;
         if (lead) {
           const long long t0 = clock64();
@@ -598,7 +620,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
         for (uint32_t r = 0; r < 2; ++r) {
           const uint32_t at = in_cta(smem_addr(&queue[q]), r);
           st_cluster(at, x.kind, x.shape, x.matrix, x.mt);
-          st_cluster(at + 16, x.nt, x.step, x.kb, x.bn);
+          st_cluster(at + 16, x.nt, x.phase, x.kb, x.bn);
           bar_arrive_written(in_cta(told(q), r));
         }
       }
@@ -902,7 +924,8 @@ struct Group {
   std::vector<int64_t> members;
   int64_t first;               // of its entries
   int64_t ldx, lda;
-  int64_t x[2], a, p;          // byte offsets of both X, of A and of P: high parts, then low parts
+  int64_t at[kBuffers];        // byte offsets of the buffers: high parts, then low parts
+  bool joined() const { return n >= 2 * m; }   // see kMultiply; T is theirs alone
   int64_t x_part() const { return static_cast<int64_t>(members.size()) * m * ldx; }
   int64_t a_part() const { return static_cast<int64_t>(members.size()) * m * lda; }
 };
@@ -963,13 +986,9 @@ int make_plan(Plan& plan, int64_t n_matrices, const int64_t* rows, const int64_t
     first += static_cast<int64_t>(g.members.size());
     g.ldx = round_up(g.n, 16);
     g.lda = round_up(g.m, 16);
-    for (int64_t* to : {&g.x[0], &g.x[1]}) {
-      *to = at;
-      at += round_up(g.x_part() * 4, 256);
-    }
-    for (int64_t* to : {&g.a, &g.p}) {
-      *to = at;
-      at += round_up(g.a_part() * 4, 256);
+    for (int k = 0; k < kBuffers; ++k) {
+      g.at[k] = at;
+      if (k != kT || g.joined()) at += round_up((k <= kX1 ? g.x_part() : g.a_part()) * 4, 256);
     }
   }
   plan.total = std::max<int64_t>(at, 512);
@@ -990,8 +1009,9 @@ int make_map3(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, in
   return r == CUDA_SUCCESS ? ZERO_OK : fail(ZERO_E_CUDA, "encoding a tensor map failed (%d)", static_cast<int>(r));
 }
 
-// Tiles of one matrix's product.
-int tiles_of(int kind, int64_t m, int64_t n, int bn) {
+// Tiles of one matrix's product of a class.
+int tiles_of(int of, int64_t m, int64_t n, int bn) {
+  const int kind = of == 2 ? kApply : kGram;
   const int m_tiles = static_cast<int>(ceil_div(m, kTileM)), n_tiles = static_cast<int>(ceil_div(kind == kApply ? n : m, bn));
   if (kind == kApply) return m_tiles * n_tiles;
   int t = 0;
@@ -1003,13 +1023,13 @@ int tiles_of(int kind, int64_t m, int64_t n, int bn) {
 // the products of parts, or the time its operands take to load (48 bytes a
 // cycle); a tile has some 2000 cycles besides, and the tiles of a product that
 // are one more than the pairs take as long as two each.
-int width_of(int kind, int64_t m, int64_t n, int matrices, bool fine) {
+int width_of(int of, int64_t m, int64_t n, int matrices, bool fine) {
   const int products = fine ? 3 : 1, parts = fine ? 2 : 1;
-  const int64_t kb = ceil_div(kind == kGram ? n : m, kTileK);
+  const int64_t kb = ceil_div(of == 0 ? n : m, kTileK);
   int best = kTileN;
   double least = 0;
   for (int bn : {256, 128, 64}) {
-    const double tiles = static_cast<double>(tiles_of(kind, m, n, bn)) * matrices;
+    const double tiles = static_cast<double>(tiles_of(of, m, n, bn)) * matrices;
     const double block = std::max<double>(2 * bn * products, (128 + bn / 2) * kTileK * 2 * parts / 48.0);
     const double cost = (kb * block + 2000) * (matrices > 1 ? std::max(1.0, tiles / kPairs) : std::ceil(tiles / kPairs));
     if (bn == kTileN || cost < least) {
@@ -1024,18 +1044,50 @@ struct Recurrence {
   int steps, fine;
   const double* coefficients;
   int first_parts;             // of the first X
-  int last;                    // Kind of the last product
+  int last;                    // Final
   int dtype;                   // of what it writes
 };
+
+// The list of a shape's products, steps one by one or by twos; its length.
+int make_phases(Phase* to, const Recurrence& r, bool joined) {
+  int count = 0, x = kX0;
+  auto add = [&](int kind, int a, int b, int out, int step, bool fine, int parts_a, int parts_b, bool two, int units,
+                 float factor) {
+    const Phase f = {static_cast<int8_t>(kind), static_cast<int8_t>(a), static_cast<int8_t>(b), static_cast<int8_t>(out),
+                     static_cast<int8_t>(step), static_cast<int8_t>(parts_a), static_cast<int8_t>(parts_b),
+                     static_cast<int8_t>(two), static_cast<int8_t>(units), static_cast<int8_t>(fine), 0, 0, factor};
+    to[count++] = f;
+  };
+  for (int s = 0; s < r.steps;) {
+    const bool fine = s < r.fine;
+    const int parts = fine ? 2 : 1, of_x = s == 0 ? std::min(parts, r.first_parts) : parts;
+    // the joined P's entries, up to the product of both a, have to fit fp16
+    const bool two = joined && s + 1 < (fine ? r.fine : r.steps) &&
+                     std::fabs(r.coefficients[3 * s] * r.coefficients[3 * s + 3]) <= 64.0;
+    const int past = s + (two ? 2 : 1);
+    add(kGram, x, x, kA, s, fine, of_x, of_x, fine, s == 0 ? 2 : 0, kScaleA / (kScaleX * kScaleX));
+    add(kPoly, kA, kA, kP, s, fine, parts, parts, fine, 0, 0.f);
+    if (two) {
+      add(kMultiply, kP, kA, kT, s, fine, parts, parts, fine, 0, kScaleT / (kScaleP * kScaleA));
+      add(kMultiply, kT, kP, kA, s, fine, parts, parts, fine, 0, kScaleA / (kScaleT * kScaleP));
+      add(kPoly, kA, kA, kT, s + 1, fine, parts, parts, fine, 0, 0.f);
+      add(kMultiply, kT, kP, kA, s, fine, parts, parts, fine, 0, 1.f / kScaleP);
+    }
+    const bool last = past == r.steps;
+    add(kApply, two ? kA : kP, x, x ^ 1, s, fine, parts, of_x, past < r.fine, s == 0 ? 1 : 0,
+        last ? 1.f / (kScaleP * kScaleX) : 1.f / kScaleP);
+    to[count - 1].last = last;
+    x ^= 1;
+    s = past;
+  }
+  return count;
+}
 
 // The steps of plan.groups[from, to).
 template <int FINAL, int GROUPS>
 int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, char* ws, cudaStream_t s, bool& stall) {
   static thread_local RunArgs<GROUPS> g;
   std::memset(&g, 0, sizeof g);
-  g.steps = r.steps;
-  g.fine = r.fine;
-  g.first_parts = r.first_parts;
   g.dtype = r.dtype;
   g.stall = std::exchange(stall, false);
   g.entries = reinterpret_cast<const Entry*>(ws + plan.table);
@@ -1047,6 +1099,8 @@ int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, ch
   g.exits = g.next + 1;
   g.written = counters + 1 + 2 * plan.launches();
   for (int k = 0; k < 3 * r.steps; ++k) g.coefficients[k] = static_cast<float>(r.coefficients[k]);
+  for (int joined = 0; joined < 2; ++joined) g.phases[joined] = make_phases(g.phase[joined], r, joined);
+  int64_t all = 0, most = 1;
   for (size_t i = from; i < to; ++i) {
     const Group& group = plan.groups[i];
     Shape& h = g.shape[g.shapes++];
@@ -1056,43 +1110,35 @@ int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, ch
     h.first = static_cast<int>(group.first);
     h.m = static_cast<int>(m);
     h.n = static_cast<int>(n);
+    h.joined = group.joined();
     g.entries_here += c;
     for (int fine = 0; fine < 2; ++fine)
-      for (int kind = 0; kind < 3; ++kind) {
-        h.bn[fine][kind] = width_of(kind, m, n, c, fine);
-        h.tiles[fine][kind] = tiles_of(kind, m, n, h.bn[fine][kind]);
-        const int64_t all = g.tiles[fine][kind] + static_cast<int64_t>(c) * h.tiles[fine][kind];
-        if (all * 3 * r.steps > INT32_MAX / 2) return fail(ZERO_E_ARG, "too many tiles");
-        g.tiles[fine][kind] = static_cast<int>(all);
+      for (int of = 0; of < 3; ++of) {
+        h.bn[fine][of] = width_of(of, m, n, c, fine);
+        h.tiles[fine][of] = tiles_of(of, m, n, h.bn[fine][of]);
+        most = std::max(most, static_cast<int64_t>(c) * h.tiles[fine][of]);
+        all += 4 * static_cast<int64_t>(r.steps) * c * h.tiles[fine][of];
       }
-    h.a_at = reinterpret_cast<uint16_t*>(ws + group.a);
-    h.p_at = reinterpret_cast<uint16_t*>(ws + group.p);
     h.ldx = group.ldx;
     h.lda = group.lda;
     h.apart_x = m * group.ldx;
     h.apart_a = m * group.lda;
     h.part_x = group.x_part();
     h.part_a = group.a_part();
-    int rc;
-    for (int k = 0; k < 2; ++k) {
-      if ((rc = make_map3(&h.x[k], ws + group.x[k], m, n, group.ldx, 2 * c, 128)) ||
-          (rc = make_map3(&h.x64[k], ws + group.x[k], m, n, group.ldx, 2 * c, 64)) ||
-          (rc = make_map3(&h.x32[k], ws + group.x[k], m, n, group.ldx, 2 * c, 32)))
-        return rc;
-      h.x_at[k] = reinterpret_cast<uint16_t*>(ws + group.x[k]);
+    for (int k = 0; k < kBuffers; ++k) {
+      if (k == kT && !h.joined) continue;
+      const bool of_x = k <= kX1;
+      char* at = ws + group.at[k];
+      h.at[k] = reinterpret_cast<uint16_t*>(at);
+      CUtensorMap* maps[3] = {&h.box128[k], &h.box64[k], &h.box32[k]};
+      for (int b = 0; b < 3; ++b)
+        if (const int rc = make_map3(maps[b], at, m, of_x ? n : m, of_x ? group.ldx : group.lda, 2 * c, 128 >> b)) return rc;
     }
-    if ((rc = make_map3(&h.a, ws + group.a, m, m, group.lda, 2 * c, 128)) ||
-        (rc = make_map3(&h.a64, ws + group.a, m, m, group.lda, 2 * c, 64)) ||
-        (rc = make_map3(&h.a32, ws + group.a, m, m, group.lda, 2 * c, 32)) ||
-        (rc = make_map3(&h.p, ws + group.p, m, m, group.lda, 2 * c, 128)) ||
-        (rc = make_map3(&h.p64, ws + group.p, m, m, group.lda, 2 * c, 64)))
-      return rc;
   }
+  if (all > INT32_MAX) return fail(ZERO_E_ARG, "too many tiles");
   const auto fn = ns_run<FINAL, GROUPS>;
   ZERO_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRunSmem));
-  int most = 1;
-  for (const auto& of : g.tiles) most = std::max({most, of[0], of[1], of[2]});
-  const int pairs = static_cast<int>(std::min({std::max<int64_t>(1, sm_count() / 2), kPairs, static_cast<int64_t>(most)}));
+  const int pairs = static_cast<int>(std::min({std::max<int64_t>(1, sm_count() / 2), kPairs, most * static_cast<int64_t>(to - from)}));
   ZERO_CUDA(launch_chained(fn, dim3(2 * pairs), kThreads, kRunSmem, s, g));
   return ZERO_OK;
 }
@@ -1173,7 +1219,7 @@ int fine_steps(int fine, int steps, bool all) { return fine >= 0 ? fine : all ? 
 // Fills an entry's place in the workspace.
 void place(Entry& e, const Group& g, int64_t member, char* ws) {
   e.ld = g.ldx;
-  e.x = reinterpret_cast<uint16_t*>(ws + g.x[0]) + member * g.m * g.ldx;
+  e.x = reinterpret_cast<uint16_t*>(ws + g.at[kX0]) + member * g.m * g.ldx;
   e.x_part = g.x_part();
 }
 
