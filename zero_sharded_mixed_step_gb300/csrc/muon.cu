@@ -925,7 +925,9 @@ struct Group {
   int64_t first;               // of its entries
   int64_t ldx, lda;
   int64_t at[kBuffers];        // byte offsets of the buffers: high parts, then low parts
-  bool joined() const { return n >= 2 * m; }   // see kMultiply; T is theirs alone
+  // See kMultiply; T is theirs alone.  By twos and one by one, us: eight of 1024 x 1536 349 and 346, of 1024 x 2048 374
+  // and 397, of 1024 x 4096 510 and 649; one of them 217 and 203, 224 and 215, 257 and 280.
+  bool joined() const { return n >= 2 * m; }
   int64_t x_part() const { return static_cast<int64_t>(members.size()) * m * ldx; }
   int64_t a_part() const { return static_cast<int64_t>(members.size()) * m * lda; }
 };

@@ -47,7 +47,9 @@ using host::round_up;
 // Bounded device-side waits of ns_small that gave up, over all calls; never set back (see zero_lm_status).
 __device__ unsigned int g_small_timeouts;
 
-constexpr int kThreads = kPassThreads;
+// Four warps for each quarter of the TMEM lanes, 16 columns in turn (eight matrices of 128 x 256 take 49.6 us; with
+// two warps of 32 columns 55.7).
+constexpr int kThreads = 512, kCols = 16;
 constexpr int kMostRows = 128, kMostSlice = 256, kMostCtas = 8;
 
 template <int BYTES>
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
     for (int k = 0; k < 8; ++k)
       if (k < count) mine = fmaf(u[k], u[k], mine);
   }
-  double all = block_sum(mine);
+  double all = block_sum<kThreads>(mine);
   if (ctas > 1) {
     if (threadIdx.x == 0) squares_here = all;
     meet_cluster();
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
   const uint32_t tmem = tmem_slot;
 
   // ---- the steps ----
-  const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+  const int quad = warp & 3, share = warp >> 2, row = quad * 32 + lane;
   const uint32_t my_lanes = tmem + (static_cast<uint32_t>(quad) << 21);
   const bool rows_here = quad * 32 < mp;
   bool ok = true, issuer = false;
@@ -245,12 +247,11 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
     if (ok && issuer && report) commit_one(bar);
     if (ok) ok = bar_wait(bar, phase);
     phase ^= 1;
-    ok = __syncthreads_and(ok);
     fence_after();
   };
   // before the next product: what was written to shared memory is seen, what is in TMEM has been read
   auto ready = [&] {
-    fence_all_async();
+    fence_async();
     fence_before();
     __syncthreads();
     fence_after();
@@ -270,10 +271,10 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
       if (b_parts > 1) mma_one(tmem, da, db + (b_low >> 4), idesc, true);
     }
   };
-  // 32 sums of this thread's row, from column c
-  auto load = [&](int c, float (&v)[32]) {
+  // 16 sums of this thread's row, from column c
+  auto load = [&](int c, float (&v)[kCols]) {
     __syncwarp();
-    tmem_ld32(my_lanes + c, v);
+    tmem_ld16(my_lanes + c, v);
     tmem_ld_wait(v);
   };
   // 8 values of a row in one or two parts
@@ -295,11 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
     if (nk > 0) multiply(xs, x_part, x_parts, xs, x_part, x_parts, nk, mp, false);
     finish(!(g.stall && which == 0 && rank == 0 && step == 0));
     if (ctas == 1) {
-      for (int c = half * 32; c < mp && rows_here; c += 64) {
-        float v[32];
+      for (int c = share * kCols; c < mp && rows_here; c += 64) {
+        float v[kCols];
         load(c, v);
 #pragma unroll
-        for (int k = 0; k < 32; k += 8) {
+        for (int k = 0; k < kCols; k += 8) {
           float w[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) w[q] = v[k + q] * gram;
@@ -308,18 +309,19 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
       }
     } else {
       // this CTA's sums in A's place, column after column
-      for (int c = half * 32; c < mp && rows_here; c += 64) {
-        float v[32];
+      for (int c = share * kCols; c < mp && rows_here; c += 64) {
+        float v[kCols];
         load(c, v);
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
+        for (int k = 0; k < kCols; ++k)
           if (row < mp && c + k < mp) st_shared1(as + ((c + k) * mp + row) * 4, nk > 0 ? v[k] : 0.f);
       }
       meet_cluster();
-      // a share of the groups of 8 columns over all the CTAs: at most 128 x 16 / 2 of them, 4 a thread
-      float sum[4][8];
+      // a share of the groups of 8 columns over all the CTAs: at most 128 x 16 / 2 of them, 2 a thread
+      constexpr int kShare = 128 * 16 / 2 / kThreads;
+      float sum[kShare][8];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
+      for (int s = 0; s < kShare; ++s) {
         const int i = s * kThreads + static_cast<int>(threadIdx.x);
 #pragma unroll
         for (int q = 0; q < 8; ++q) sum[s][q] = 0.f;
@@ -333,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
       }
       meet_cluster();
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
+      for (int s = 0; s < kShare; ++s) {
         const int i = s * kThreads + static_cast<int>(threadIdx.x);
         const int g8 = i / mp, r = i - g8 * mp, col = (g8 * ctas + rank) * 8;
         if (col >= mp) continue;
@@ -357,11 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
     finish(true);
     const float pa = g.coefficients[3 * step] * kScaleP, pb = g.coefficients[3 * step + 1] * (kScaleP / kScaleA);
     const float pc = g.coefficients[3 * step + 2] * (kScaleP / (kScaleA * kScaleA));
-    for (int c = half * 32; c < mp && rows_here; c += 64) {
-      float v[32];
+    for (int c = share * kCols; c < mp && rows_here; c += 64) {
+      float v[kCols];
       load(c, v);
 #pragma unroll
-      for (int k = 0; k < 32; k += 8) {
+      for (int k = 0; k < kCols; k += 8) {
         if (row >= mp || c + k >= mp) continue;
         float h[8], l[8] = {}, w[8];
         const uint32_t from = at(as, row, c + k);
@@ -378,11 +380,11 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
     if (nk > 0) multiply(as, a_part, parts, xs, x_part, x_parts, mp, nk, true);
     finish(true);
     if (!last) {
-      for (int c = half * 32; c < nk && rows_here; c += 64) {
-        float v[32];
+      for (int c = share * kCols; c < nk && rows_here; c += 64) {
+        float v[kCols];
         load(c, v);
 #pragma unroll
-        for (int k = 0; k < 32; k += 8) {
+        for (int k = 0; k < kCols; k += 8) {
           float w[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) w[q] = v[k + q] * (rest / kScaleP);
@@ -392,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
       ready();
       continue;
     }
+    ok = __syncthreads_and(ok);
     bool good = ok;
     if (ctas > 1) {
       if (threadIdx.x == 0) ok_here = ok ? 1.f : 0.f;
@@ -399,17 +402,17 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
       for (int k = 0; k < ctas; ++k) good = good && ld_there(in_cta(smem_addr(&ok_here), k)) != 0.f;
     }
     const float out = finite && good ? rest / (kScaleP * kScaleX) : NAN;
-    for (int c = half * 32; c < nk && rows_here; c += 64) {
-      float v[32];
+    for (int c = share * kCols; c < nk && rows_here; c += 64) {
+      float v[kCols];
       load(c, v);
       // a norm that is not finite leaves the state as it was
       if (row >= m || c >= nl || (MUON && !(finite && good))) continue;
 #pragma unroll
-      for (int k = 0; k < 32; ++k) v[k] *= out;
+      for (int k = 0; k < kCols; ++k) v[k] *= out;
       if (MUON) {
-        uint4 theta[8];
-        read_master<32>(e, c0 + nl, row, c0 + c, theta);
-        step_master<32>(e, theta, v);
+        uint4 theta[kCols / 4];
+        read_master<kCols>(e, c0 + nl, row, c0 + c, theta);
+        step_master<kCols>(e, theta, v);
       }
       write_columns<MUON>(c0 + nl, e, g.out_dtype, row, c0 + c, v);
     }

@@ -179,15 +179,16 @@ struct PassArgs {
   Norm* norms;
 };
 
+template <int THREADS = kPassThreads>
 __device__ __forceinline__ double block_sum(double s) {
-  __shared__ double of_warp[kPassThreads / 32];
+  __shared__ double of_warp[THREADS / 32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) of_warp[threadIdx.x >> 5] = s;
   __syncthreads();
   double all = 0.0;
-  for (int k = 0; k < kPassThreads / 32; ++k) all += of_warp[k];
+  for (int k = 0; k < THREADS / 32; ++k) all += of_warp[k];
   return all;
 }
 

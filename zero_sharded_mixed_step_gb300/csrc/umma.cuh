@@ -122,6 +122,8 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, 
 }
 
 // Between the generic and the async proxy, everywhere: what others wrote through one before it is used through the other.
+__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }        // global memory
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }   // this CTA's shared memory
 __device__ __forceinline__ void fence_all_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
