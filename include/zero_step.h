@@ -842,7 +842,7 @@ int64_t zero_lm_logprobs_workspace_bytes(int64_t tokens, int64_t vocab, int64_t 
  * are written all the same.  Logits of -infinity and NaN are not listed: where
  * fewer than `top` others are there, the rest of the ids are -1 and their values
  * -infinity (NaN where lse is NaN or -infinity).
- *   scale      positive and finite in fp32: 1 / temperature.
+ *   scale      positive in fp32 and below 2e38: 1 / temperature.
  *   top        0..16 and at most vocab; 0: top_logp and top_ids may be NULL.
  *   logp, entropy, lse  device, `tokens` fp32 values each.
  *   top_logp, top_ids   device, tokens x top fp32 and int32 values.

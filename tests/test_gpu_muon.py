@@ -349,3 +349,37 @@ def test_streams_take_turns():
         twin.step(grads, 0.01)
     torch.cuda.synchronize()
     assert torch.equal(op.master, twin.master)
+
+
+def test_calls_on_two_streams_at_once():
+    """Small and large matrices, steps and log probabilities beside one another, each by owners of its own."""
+    small = [gaussian(10, 1300, seed=k).bfloat16() for k in range(40)]
+    large = [gaussian(300, 700, seed=k).bfloat16() for k in range(3)]
+    h, t = gaussian(300, 128).bfloat16(), gaussian(5000, 128, 1, 0.1).bfloat16()
+    tg = torch.arange(300, device="cuda")
+    step, grads = make_step([(40, 64), (200, 300)], 3, "bf16")
+    twin, _ = make_step([(40, 64), (200, 300)], 3, "bf16")
+    ops = [zs.Orthogonalize([(10, 1300)] * 40, "bf16"), zs.Orthogonalize([(300, 700)] * 3, "bf16"),
+           zs.LmLogprobs(5000, 128, "bf16", max_tokens=300, top=4)]
+
+    def calls(k):
+        return (ops[0].forward(small), ops[1].forward(large), ops[2].logprobs(h, t, tg))[k]
+
+    want = [calls(k) for k in range(3)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = [[], [], []]
+    for _ in range(10):
+        for k in range(3):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(calls(k))
+        with torch.cuda.stream(streams[3]):
+            step.step(grads, 0.01)
+    torch.cuda.synchronize()
+    for k in range(3):
+        ops[k].status()
+        assert all(torch.equal(x, y) for out in got[k] for x, y in zip(out, want[k]))
+    for _ in range(10):
+        twin.step(grads, 0.01)
+    torch.cuda.synchronize()
+    assert torch.equal(step.master, twin.master)

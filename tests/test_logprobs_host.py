@@ -12,7 +12,7 @@ GRAD = dict({k: v for k, v in FORWARD.items() if k not in ("top", "logp", "entro
                                                           "workspace", "workspace_bytes")},
             lse=fake(5), dlogp=fake(12), entropy=fake(9), dentropy=fake(13), dhidden=fake(7), dhidden_stride=16,
             dtable=fake(8), dtable_stride=16, accumulate=0, workspace=fake(6), workspace_bytes=1 << 20)
-SCALES = [("scale", x, zs.ZERO_E_ARG) for x in (0.0, -1.0, float("nan"), float("inf"), 1e60, 1e-60)]
+SCALES = [("scale", x, zs.ZERO_E_ARG) for x in (0.0, -1.0, float("nan"), float("inf"), 1e60, 3e38, 1e-60)]
 
 
 @pytest.mark.parametrize("name,value,want", COMMON_BAD + SCALES + [

@@ -324,7 +324,8 @@ int check_top(int top, int64_t vocab) {
 
 int check_scale(double scale) {
   const float f = static_cast<float>(scale);
-  return std::isfinite(f) && f > 0.f ? ZERO_OK : fail(ZERO_E_ARG, "scale %g is not a positive finite fp32 value", scale);
+  // the kernels work in powers of 2
+  return std::isfinite(f * kLog2e) && f > 0.f ? ZERO_OK : fail(ZERO_E_ARG, "scale %g is not positive and below 2e38", scale);
 }
 
 int check_floats(const char* what, const void* p) {

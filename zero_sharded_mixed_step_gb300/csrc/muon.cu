@@ -52,6 +52,8 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <map>
+#include <new>
 #include <type_traits>
 #include <utility>
 #include <vector>
@@ -457,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
       if (!ok || x.kind < 0) break;
       if (first && rank == 0 && lead) bar_arrive_own(began);
       // what other CTAs' threads wrote is loaded through the async proxy
-      fence_all_async();
+      fence_async_global();
       const Shape& h = g.shape[x.shape];
       const Phase& f = phase_of(g, x);
       const int bn = x.bn, depth = h.matrices, blocks = x.kb, parts_a = f.parts_a, parts_b = f.parts_b;
@@ -950,6 +952,7 @@ int make_plan(Plan& plan, int64_t n_matrices, const int64_t* rows, const int64_t
     return fail(ZERO_E_ARG, "n_matrices=%lld outside [0, %lld]", (long long)n_matrices, (long long)kMaxMatrices);
   if (n_matrices > 0 && (!rows || !cols)) return fail(ZERO_E_ARG, "rows and cols are required");
   int64_t numel = 0;
+  std::map<std::pair<int64_t, int64_t>, size_t> known;
   for (int64_t i = 0; i < n_matrices; ++i) {
     if (rows[i] < 1 || rows[i] > kMaxSide || cols[i] < 1 || cols[i] > kMaxSide)
       return fail(ZERO_E_ARG, "matrix %lld: %lld x %lld, sides outside [1, %lld]", (long long)i, (long long)rows[i],
@@ -960,14 +963,13 @@ int make_plan(Plan& plan, int64_t n_matrices, const int64_t* rows, const int64_t
     }
     const int64_t m = std::min(rows[i], cols[i]), n = std::max(rows[i], cols[i]);
     ++plan.count;
-    auto it = std::find_if(plan.groups.begin(), plan.groups.end(), [&](const Group& g) { return g.m == m && g.n == n; });
-    if (it == plan.groups.end()) {
+    const auto [it, fresh] = known.try_emplace({m, n}, plan.groups.size());
+    if (fresh) {
       plan.groups.emplace_back();
-      it = plan.groups.end() - 1;
-      it->m = m;
-      it->n = n;
+      plan.groups.back().m = m;
+      plan.groups.back().n = n;
     }
-    it->members.push_back(i);
+    plan.groups[it->second].members.push_back(i);
     plan.tiles += pass_tiles(rows[i], cols[i]);
     numel += round_up(rows[i] * cols[i], 8);
   }
@@ -1225,6 +1227,9 @@ void place(Entry& e, const Group& g, int64_t member, char* ws) {
   e.x_part = g.x_part();
 }
 
+// The lists of matrices are kept on the host while a call is cut up.
+int out_of_memory() { return fail(ZERO_E_NOMEM, "no host memory for the list of matrices"); }
+
 }  // namespace
 
 cudaError_t ns_timeouts(unsigned int* out) {
@@ -1240,16 +1245,18 @@ cudaError_t ns_timeouts(unsigned int* out) {
 
 using namespace zero;
 
-extern "C" int64_t zero_orthogonalize_workspace_bytes(int64_t n_matrices, const int64_t* rows, const int64_t* cols) {
+extern "C" int64_t zero_orthogonalize_workspace_bytes(int64_t n_matrices, const int64_t* rows, const int64_t* cols) try {
   Plan plan;
   const int rc = make_plan(plan, n_matrices, rows, cols, 0, false);
   return rc ? rc : plan.total;
+} catch (const std::bad_alloc&) {
+  return out_of_memory();
 }
 
 extern "C" int zero_orthogonalize(int64_t n_matrices, const int64_t* rows, const int64_t* cols, int dtype,
                                   const void* const* in, const int64_t* in_strides, void* const* out,
                                   const int64_t* out_strides, int steps, const double* coefficients, int fine,
-                                  void* workspace, int64_t workspace_bytes, void* stream) {
+                                  void* workspace, int64_t workspace_bytes, void* stream) try {
   bool stall = std::exchange(g_stall_next, false);
   Plan plan;
   int rc = make_plan(plan, n_matrices, rows, cols, 0, false);
@@ -1316,20 +1323,24 @@ extern "C" int zero_orthogonalize(int64_t n_matrices, const int64_t* rows, const
        : dtype == ZERO_BF16 ? launch_passes<__nv_bfloat16, false>(p, s)
                             : launch_passes<float, false>(p, s);
   return rc ? rc : run_all(plan, r, ws, s, stall);
+} catch (const std::bad_alloc&) {
+  return out_of_memory();
 }
 
-extern "C" int64_t zero_muon_workspace_bytes(int W, int64_t n_matrices, const int64_t* rows, const int64_t* cols) {
+extern "C" int64_t zero_muon_workspace_bytes(int W, int64_t n_matrices, const int64_t* rows, const int64_t* cols) try {
   if (W < 1 || W > ZERO_MAX_RANKS) return fail(ZERO_E_ARG, "W=%d outside [1, %d]", W, ZERO_MAX_RANKS);
   Plan plan;
   const int rc = make_plan(plan, n_matrices, rows, cols, W, true);
   return rc ? rc : plan.total;
+} catch (const std::bad_alloc&) {
+  return out_of_memory();
 }
 
 extern "C" int zero_muon_step(int W, int64_t n_matrices, const int64_t* rows, const int64_t* cols, int grad_dtype,
                               int work_dtype, const void* const* grads, float* const* master, float* const* momentum,
                               void* const* p16, double lr, double mu, int nesterov, double weight_decay,
                               const double* scales, int steps, const double* coefficients, int fine, void* workspace,
-                              int64_t workspace_bytes, void* stream) {
+                              int64_t workspace_bytes, void* stream) try {
   bool stall = std::exchange(g_stall_next, false);
   if (W < 1 || W > ZERO_MAX_RANKS) return fail(ZERO_E_ARG, "W=%d outside [1, %d]", W, ZERO_MAX_RANKS);
   Plan plan;
@@ -1423,4 +1434,6 @@ extern "C" int zero_muon_step(int W, int64_t n_matrices, const int64_t* rows, co
   p.norms = reinterpret_cast<Norm*>(ws + plan.norms);
   rc = grad_dtype == ZERO_FP16 ? launch_passes<__half, true>(p, s) : launch_passes<__nv_bfloat16, true>(p, s);
   return rc ? rc : run_all(plan, r, ws, s, stall);
+} catch (const std::bad_alloc&) {
+  return out_of_memory();
 }

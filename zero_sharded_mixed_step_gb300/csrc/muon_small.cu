@@ -446,8 +446,15 @@ int64_t space_for(const Entry& e, int ctas) {
   return 2 * mp * 128 * (ceil_div(slice, 64) + ceil_div(mp, 64)) + (kMostRows - mp) * 128 + 1024;
 }
 
+// So much shared memory at least: more than half of an SM's, so that no other CTA
+// that takes TMEM, of this launch or of another stream's, shares the SM.  CTAs of
+// two clusters that had TMEM on one SM each and waited for it on the other's would
+// wait for ever.
+constexpr int64_t kAloneBytes = 116 * 1024;
+
 template <typename T, bool MUON, int BYTES>
 int launch_small(SmallArgs<BYTES>& a, int count, int ctas, int64_t space, cudaStream_t s) {
+  space = std::max(space, kAloneBytes);
   const auto fn = ns_small<T, MUON, BYTES>;
   ZERO_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(space)));
   cudaLaunchConfig_t cfg = {};
