@@ -735,7 +735,9 @@ __device__ __forceinline__ unsigned end_of(const PassArgs& p, int which) {
 // The first pass: sums of squares, in fp32 within a thread and in fp64 beyond
 // (and the mean gradient, kept where that pays).  A block goes over a stretch of
 // the tiles and leaves a sum for each matrix that it meets, at [block + entry].
-// WC > 0: so many ranks, known at compile time; 0: any number.
+// WC > 0: so many ranks, known at compile time; 0: any number (8 ranks, whose
+// loads are many anyway, took 120 us so for 28M elements, and 139 to 161 with
+// WC = 8).
 template <typename T, bool MUON, int WC>
 __global__ void __launch_bounds__(kPassThreads) sum_squares(const __grid_constant__ PassArgs p) {
   allow_next();
@@ -754,9 +756,8 @@ __global__ void __launch_bounds__(kPassThreads) sum_squares(const __grid_constan
       float squares = 0.f;
       const int first_row = ty * kPassRows + static_cast<int>(threadIdx.x >> 5);
       if (MUON && WC > 0 && e.wide) {
-        // two rows' loads at a time, before the first store; of 8 ranks one row's (two take 176 registers, and 139 us
-        // for 28M elements where one takes 120)
-        constexpr int kAtOnce = WC >= 8 ? 1 : 2;
+        // two rows' loads at a time, before the first store
+        constexpr int kAtOnce = 2;
         const uint64_t* ranks = p.grads + static_cast<int64_t>(which) * p.W;
 #pragma unroll
         for (int r = 0; r < kPassRows / 8; r += kAtOnce) {
@@ -807,6 +808,8 @@ __global__ void __launch_bounds__(kPassThreads) sum_squares(const __grid_constan
   }
 }
 
+constexpr int kTurnBytes = kPassCols * (kPassRows + 1) * 4;
+
 // A row's values on their way to X: times the power of two, in their parts, to
 // their place or to be turned.
 __device__ __forceinline__ void to_first(const PassArgs& p, const Entry& e, int row, int col, int in_tile, float scale,
@@ -833,7 +836,7 @@ __device__ __forceinline__ void to_first(const PassArgs& p, const Entry& e, int 
 // than columns; the new momentum, unless the norm is not finite.
 template <typename T, bool MUON>
 __global__ void __launch_bounds__(kPassThreads) make_first(const __grid_constant__ PassArgs p) {
-  __shared__ uint32_t turned[kPassCols * (kPassRows + 1)];
+  extern __shared__ uint32_t turned[];      // kTurnBytes, where matrices are turned
   allow_next();
   await_previous();
   const unsigned t1 = stretch(p.tiles, blockIdx.x + 1);
@@ -1176,10 +1179,9 @@ int launch_passes(const PassArgs& p, cudaStream_t s) {
     if (p.W == 1) first = sum_squares<T, MUON, 1>;
     if (p.W == 2) first = sum_squares<T, MUON, 2>;
     if (p.W == 4) first = sum_squares<T, MUON, 4>;
-    if (p.W == 8) first = sum_squares<T, MUON, 8>;
   }
   ZERO_CUDA(launch_chained(first, grid, kPassThreads, 0, s, p));
-  ZERO_CUDA(launch_chained(make_first<T, MUON>, grid, kPassThreads, 0, s, p));
+  ZERO_CUDA(launch_chained(make_first<T, MUON>, grid, kPassThreads, p.turns ? kTurnBytes : 0, s, p));
   return ZERO_OK;
 }
 
@@ -1302,10 +1304,12 @@ extern "C" int zero_orthogonalize(int64_t n_matrices, const int64_t* rows, const
   constexpr size_t kEntryWords = sizeof(Entry) / 8;
   std::vector<uint64_t> words(plan.table_words);
   unsigned tile = 0;
+  bool turns = false;
   for (const Group& g : plan.groups)
     for (size_t k = 0; k < g.members.size(); ++k) {
       Entry e = entry(g.members[k]);
       e.tile0 = tile;
+      turns = turns || e.transposed;
       tile += static_cast<unsigned>(pass_tiles(e.rows, e.cols));
       place(e, g, static_cast<int64_t>(k), ws);
       std::memcpy(&words[(g.first + k) * kEntryWords], &e, sizeof e);
@@ -1316,6 +1320,7 @@ extern "C" int zero_orthogonalize(int64_t n_matrices, const int64_t* rows, const
   p.entries = reinterpret_cast<const Entry*>(ws + plan.table);
   p.count = static_cast<int>(plan.count);
   p.tiles = tile;
+  p.turns = turns;
   p.two = r.first_parts > 1 && r.fine > 0;
   p.part = reinterpret_cast<double*>(ws + plan.part);
   p.norms = reinterpret_cast<Norm*>(ws + plan.norms);
@@ -1405,6 +1410,7 @@ extern "C" int zero_muon_step(int W, int64_t n_matrices, const int64_t* rows, co
   std::vector<uint64_t> words(plan.table_words);
   uint64_t* ranks = words.data() + plan.count * kEntryWords;
   unsigned tile = 0;
+  bool turns = false;
   int64_t mean_at = plan.mean;
   for (const Group& g : plan.groups)
     for (size_t k = 0; k < g.members.size(); ++k) {
@@ -1415,6 +1421,7 @@ extern "C" int zero_muon_step(int W, int64_t n_matrices, const int64_t* rows, co
         mean_at += round_up(static_cast<int64_t>(e.rows) * e.cols, 8) * 4;
       }
       e.tile0 = tile;
+      turns = turns || e.transposed;
       tile += static_cast<unsigned>(pass_tiles(e.rows, e.cols));
       place(e, g, static_cast<int64_t>(k), ws);
       std::memcpy(&words[to * kEntryWords], &e, sizeof e);
@@ -1426,6 +1433,7 @@ extern "C" int zero_muon_step(int W, int64_t n_matrices, const int64_t* rows, co
   p.grads = reinterpret_cast<const uint64_t*>(ws + plan.table) + plan.count * kEntryWords;
   p.count = static_cast<int>(plan.count);
   p.tiles = tile;
+  p.turns = turns;
   p.W = W;
   p.mu = static_cast<float>(mu);
   p.nesterov = nesterov != 0;

@@ -175,6 +175,7 @@ struct PassArgs {
   float mu;
   int nesterov;
   int two;                     // the second pass writes low parts
+  int turns;                   // some matrices are turned
   double* part;                // sums of squares at [block + entry]
   Norm* norms;
 };
