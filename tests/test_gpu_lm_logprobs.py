@@ -93,6 +93,22 @@ def test_alternatives_are_exact_where_the_logits_are(N, top):
     assert torch.equal(got[4].long(), in_order(want["logits"], top))
 
 
+@pytest.mark.parametrize("top", [3, 8, 9, 16])
+@pytest.mark.parametrize("V", [16384, 65536, 65537, 131072, 131073, 300_001])
+def test_alternatives_of_large_vocabularies(V, top):
+    """The largest logits next to one another, far apart, and at every distance that one thread's groups may have."""
+    h, t, tg = make(3, V, 8, "bf16", seed=V, grid=True)
+    h[0] = 1
+    for step in (1, 31, 32, 512, 4096, 8192, 16384, 32768):
+        u = t.clone() / 64
+        at = (torch.arange(40, device="cuda") * step + 5) % V
+        u[at] = torch.arange(40, device="cuda").div(3, rounding_mode="floor")[:, None].to(u.dtype) + 1
+        got, want = check(h, u, tg, top=top, what=f"step {step}")
+        assert torch.equal(got[4].long(), in_order(want["logits"], top)), step
+    got, _ = check(h, torch.zeros_like(t), tg, top=top, what="all equal")
+    assert torch.equal(got[4], torch.arange(top, device="cuda", dtype=torch.int32).expand(3, top))
+
+
 @pytest.mark.parametrize("N", [5, 150])
 def test_fewer_numbers_than_alternatives(N):
     """Logits of -infinity and NaN are not listed."""

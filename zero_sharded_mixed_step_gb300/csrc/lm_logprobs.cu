@@ -218,31 +218,38 @@ __global__ void __launch_bounds__(kSmallThreads) join_stretches(const __grid_con
   }
 }
 
+// Threads of a token's block.  16 tokens x 50257 x 768 with 8 alternatives take 23 us so; 27 with 256 threads, 26 with
+// 1024.
+constexpr int kGroupThreads = 512;
+
 // The same of kFew's groups of 32 rows, which are many: a block a token.
-// K: the length of its lists, 0 without alternatives.
-template <int K>
-__global__ void __launch_bounds__(kSmallThreads) join_groups(const __grid_constant__ Combine g) {
-  constexpr int kWarps = kSmallThreads / 32, kList = K > 0 ? K : 1;
+// K: the length of its lists, 0 without alternatives; L: of a thread's, which
+// sees at most L groups where L < K.
+template <int K, int L>
+__global__ void __launch_bounds__(kGroupThreads) join_groups(const __grid_constant__ Combine g) {
+  constexpr int kWarps = kGroupThreads / 32, kList = K > 0 ? K : 2, kBatch = 4;
   __shared__ Sums of_warp[kWarps];
   __shared__ float group_max[kWarps][kList];
   __shared__ int group_at[kWarps][kList];
+  __shared__ float found[32];
+  __shared__ int found_at[32];
   allow_next();
   await_previous();
   const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float4* p = g.sums + static_cast<int64_t>(row) * g.n_tiles;
   Sums x = {-INFINITY, 0.f, 0.f};
   // the groups with the largest maxima hold the largest logits: of this thread's groups first
-  List<kList> list;
+  List<L> list;
   list.clear();
-  for (int k0 = threadIdx.x; k0 < g.n_tiles; k0 += 8 * kSmallThreads) {
-    float4 y[8];
+  for (int k0 = threadIdx.x; k0 < g.n_tiles; k0 += kBatch * kGroupThreads) {
+    float4 y[kBatch];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      y[k] = k0 + kSmallThreads * k < g.n_tiles ? p[k0 + kSmallThreads * k] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    for (int k = 0; k < kBatch; ++k)
+      y[k] = k0 + kGroupThreads * k < g.n_tiles ? p[k0 + kGroupThreads * k] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kBatch; ++k) {
       x.join(y[k].x, y[k].y, y[k].z, g.scale2);
-      if (K > 0 && y[k].x != -INFINITY) list.offer(y[k].x, k0 + kSmallThreads * k);
+      if (K > 0 && y[k].x != -INFINITY) list.offer(y[k].x, k0 + kGroupThreads * k);
     }
   }
   x.join_warp(g.scale2);
@@ -257,20 +264,29 @@ __global__ void __launch_bounds__(kSmallThreads) join_groups(const __grid_consta
     }
   }
   __syncthreads();
-  if (warp > 0) return;
-  x = of_warp[0];
-  for (int k = 1; k < kWarps; ++k) x.join(of_warp[k].top, of_warp[k].sum, of_warp[k].tilt, g.scale2);
-  if (lane == 0) write_token(g, row, x);
+  // one warp writes the token's results, another one its list
+  if (warp > (K > 0 ? 1 : 0)) return;
+  x = lane < kWarps ? of_warp[lane % kWarps] : Sums{-INFINITY, 0.f, 0.f};
+  x.join_warp(g.scale2);
+  if (warp == (K > 0 ? 1 : 0)) {
+    if (lane == 0) write_token(g, row, x);
+    return;
+  }
   if constexpr (K > 0) {
+    // half of a warp's list to a lane
+    static_assert(kWarps == 16);
+    List<kList / 2> half;
     float v;
     int at;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      list.v[k] = lane < kWarps ? group_max[lane % kWarps][k] : -INFINITY;
-      list.at[k] = lane < kWarps ? group_at[lane % kWarps][k] : -1;
+    for (int k = 0; k < K / 2; ++k) {
+      half.v[k] = group_max[lane / 2][lane % 2 * (K / 2) + k];
+      half.at[k] = group_at[lane / 2][lane % 2 * (K / 2) + k];
     }
-    list.first_of_lanes(g.top, v, at);
-    // then the logits of those groups, 32 each
+    half.first_of_lanes(g.top, v, at);
+    // then the logits of those groups, 32 each.  The maxima are so many logits already: none below the last of them is
+    // listed, which leaves few.
+    const float least = __shfl_sync(0xffffffffu, v, g.top - 1);
     float logit[K];
     int place[K];
 #pragma unroll
@@ -279,11 +295,32 @@ __global__ void __launch_bounds__(kSmallThreads) join_groups(const __grid_consta
       place[k] = group * 32 + lane;
       logit[k] = group >= 0 ? g.logits[row * g.logit_stride + place[k]] : -INFINITY;
     }
-    list.clear();
+    int count = 0;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (logit[k] > -INFINITY) list.offer(logit[k], place[k]);
-    list.first_of_lanes(g.top, v, at);
+    for (int k = 0; k < K; ++k) {
+      const bool kept = logit[k] > -INFINITY && logit[k] >= least;
+      const unsigned mask = __ballot_sync(0xffffffffu, kept);
+      const int to = count + __popc(mask & ((1u << lane) - 1));
+      if (kept && to < 32) {
+        found[to] = logit[k];
+        found_at[to] = place[k];
+      }
+      count += __popc(mask);
+    }
+    __syncwarp();
+    if (count <= 32) {
+      List<1> one;
+      one.clear();
+      if (lane < count) one.offer(found[lane], found_at[lane]);
+      one.first_of_lanes(g.top, v, at);
+    } else {
+      List<K> all;
+      all.clear();
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (logit[k] > -INFINITY) all.offer(logit[k], place[k]);
+      all.first_of_lanes(g.top, v, at);
+    }
     write_top(g, row, x, v, at);
   }
 }
@@ -416,11 +453,15 @@ extern "C" int zero_lm_logprobs(int64_t tokens, int64_t vocab, int64_t width, in
                  static_cast<int>(count), pairs_for(sp.tiles), sp.tiles, sp.few ? sp.m_tiles * 8 : sp.n_tiles, top,
                  g.scale2, logp + i0, lse + i0, entropy + i0, top > 0 ? top_logp + i0 * top : nullptr,
                  top > 0 ? top_ids + i0 * top : nullptr};
-    const auto fn = sp.few ? (list_length(top) == 0 ? join_groups<0> : list_length(top) == 8 ? join_groups<8> : join_groups<16>)
+    const int most = static_cast<int>(ceil_div(c.n_tiles, kGroupThreads));   // groups of a thread
+    const auto fn = sp.few ? (list_length(top) == 0    ? join_groups<0, 1>
+                              : list_length(top) == 8 ? (most <= 4 ? join_groups<8, 4> : join_groups<8, 8>)
+                              : most <= 4             ? join_groups<16, 4>
+                              : most <= 8             ? join_groups<16, 8>
+                                                      : join_groups<16, 16>)
                            : (list == 0 ? join_stretches<0> : list == 8 ? join_stretches<8> : join_stretches<16>);
-    const int64_t team = sp.few ? kSmallThreads : 32;
-    const dim3 grid(static_cast<unsigned>(ceil_div(count * team, kSmallThreads)));
-    ZERO_CUDA(launch_chained(fn, grid, kSmallThreads, 0, s, c));
+    const dim3 grid(static_cast<unsigned>(sp.few ? count : ceil_div(count * 32, kSmallThreads)));
+    ZERO_CUDA(launch_chained(fn, grid, sp.few ? kGroupThreads : kSmallThreads, 0, s, c));
   }
   return ZERO_OK;
 }
