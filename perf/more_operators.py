@@ -165,15 +165,13 @@ def prepare(case, seed):
         s["shapes"] = _shapes(case)
         s["starts"], n = _starts(s["shapes"])
         signal = torch.zeros(n, device="cuda")
-        inside = torch.zeros(n, device="cuda")       # 0 between the matrices, where there is no gradient
         theta = torch.zeros(n, device="cuda")
         momentum = torch.zeros(n, device="cuda")
         for (r, c), at in zip(s["shapes"], s["starts"]):
             signal[at:at + r * c] = _gradient(gen, r, c).flatten()
-            inside[at:at + r * c] = 1.0
             theta[at:at + r * c] = torch.randn(r * c, device="cuda", generator=gen) * 0.02
             momentum[at:at + r * c] = 10 * _gradient(gen, r, c).flatten()
-        s["flat"] = [((signal + _normal(gen, (n,), 1e-3, torch.float32)) * inside).to(dtype) for _ in range(case["W"])]
+        s["flat"] = [(signal + _normal(gen, (n,), 1e-3, torch.float32)).to(dtype) for _ in range(case["W"])]
         s["grads"] = [[g[at:at + r * c].view(r, c) for (r, c), at in zip(s["shapes"], s["starts"])] for g in s["flat"]]
         s["master"], s["momentum"] = theta, momentum
         s["scales"] = [0.2 * math.sqrt(max(r, c)) for r, c in s["shapes"]]
