@@ -193,7 +193,25 @@ def _handle(s):
     step = zs.MuonStep(s["shapes"], case["W"], case["dtype"], coefficients=COEFFICIENTS, scales=s["scales"])
     step.master.copy_(s["master"])
     step.momentum.copy_(s["momentum"])
+    s["gaps"] = _gaps(s, step)
     return step
+
+
+def _gaps(s, step):
+    """What a call for the values between the matrices takes: the gradients' vectors go on there, and so does the
+    momentum.  Each gap is a matrix of one row, whose step has a learning rate of 0; None without gaps."""
+    import zero_sharded_mixed_step_gb300 as zs
+    ends = s["starts"][1:] + [step.n]
+    gaps = [(at + r * c, end) for (r, c), at, end in zip(s["shapes"], s["starts"], ends) if at + r * c < end]
+    if not gaps:
+        return None
+    shapes = [(1, end - at) for at, end in gaps]
+    states = [[x[at:] for at, _ in gaps] for x in (step.master, step.momentum, step.p16)]
+    grads = [[g[at:] for at, _ in gaps] for g in s["flat"]]
+    space = torch.zeros(zs.zero_muon_workspace_bytes(step.W, shapes), dtype=torch.uint8, device="cuda")
+    return lambda: zs.zero_muon_step(step.W, shapes, step.dtype, step.wdt, grads, *states, LR, MU, True, DECAY,
+                                     [0.0] * len(gaps), ((1.0, 0.0, 0.0),), 0, space, space.numel(),
+                                     torch.cuda.current_stream())
 
 
 # ---- the plain forms -----------------------------------------------------------
@@ -289,6 +307,8 @@ def _own(s):
     if op == "orthogonalize":
         return handle.forward(s["matrices"])
     handle.step(s["grads"], LR, MU, weight_decay=DECAY)
+    if s["gaps"] is not None:
+        s["gaps"]()
     return handle.master, handle.momentum, handle.p16
 
 
