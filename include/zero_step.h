@@ -903,10 +903,11 @@ int64_t zero_orthogonalize_workspace_bytes(int64_t n_matrices, const int64_t* ro
  *              singular values stand above the rest, 1e-6 with all.
  *   workspace  device, 256-byte aligned, any contents; its first 4 bytes count
  *              waits that gave up (zero_lm_workspace_status).
- * A matrix of norm 0 gives 0, one whose norm is not finite NaN.  The norm's squares
- * are summed in fp32 within a thread and in fp64 beyond; products accumulate in
- * fp32; the result is rounded once.  The same inputs give the same bits every
- * time.  Enqueues on `stream` and returns.  ZERO_E_ARG / ZERO_E_ALIGN / ZERO_E_CUDA.
+ * A matrix of norm 0 gives 0, one that holds an infinity or a NaN NaN; finite values
+ * of any size have their norm, whose squares are summed in fp32 within a thread, at
+ * scales that hold them, and in fp64 beyond.  Products accumulate in fp32; the
+ * result is rounded once.  The same inputs give the same bits every time.
+ * Enqueues on `stream` and returns.  ZERO_E_ARG / ZERO_E_ALIGN / ZERO_E_CUDA.
  */
 int zero_orthogonalize(int64_t n_matrices, const int64_t* rows, const int64_t* cols, int dtype, const void* const* in,
                        const int64_t* in_strides, void* const* out, const int64_t* out_strides, int steps,
@@ -936,7 +937,7 @@ int64_t zero_muon_workspace_bytes(int W, int64_t n_matrices, const int64_t* rows
  *   lr, weight_decay, scales  lr and lr * scales[i] finite in fp32; scales NULL: 1.
  *   mu         0 <= mu < 1.
  *   steps, coefficients, fine_steps, workspace  as for zero_orthogonalize.
- * A matrix whose U has a norm that is not finite (an overflow in fp16 gradients)
+ * A matrix whose U holds a value that is not finite (an overflow in fp16 gradients)
  * keeps its master, momentum and p16 as they were; one of norm 0 decays alone.
  * The caller keeps the step counter, if any.  A device wait that gave up
  * (zero_lm_workspace_status) can leave the matrices partly updated: restore them

@@ -732,7 +732,7 @@ __device__ __forceinline__ unsigned end_of(const PassArgs& p, int which) {
   return which + 1 < p.count ? p.entries[which + 1].tile0 : p.tiles;
 }
 
-// The first pass: sums of squares, in fp32 within a thread and in fp64 beyond
+// The first pass: sums of squares, in fp32 within a thread (see Squares) and in fp64 beyond
 // (and the mean gradient, kept where that pays).  A block goes over a stretch of
 // the tiles and leaves a sum for each matrix that it meets, at [block + entry].
 // WC > 0: so many ranks, known at compile time; 0: any number (8 ranks, whose
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(kPassThreads) sum_squares(const __grid_constan
       const int tile = static_cast<int>(t - tile0), ty = tile / across;
       const int col = (tile - ty * across) * kPassCols + static_cast<int>(threadIdx.x & 31) * 8;
       const int n = e.cols - col;
-      float squares = 0.f;
+      Squares squares;
       const int first_row = ty * kPassRows + static_cast<int>(threadIdx.x >> 5);
       if (MUON && WC > 0 && e.wide) {
         // two rows' loads at a time, before the first store
@@ -781,14 +781,16 @@ __global__ void __launch_bounds__(kPassThreads) sum_squares(const __grid_constan
             float g[8];
             if constexpr (!std::is_same<T, float>::value) mean_of<T, (WC > 0 ? WC : 1)>(raw[j], g);
             if (e.mean != nullptr) dev::st_32B(e.mean + at[j], g);
+            float u[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const float now = __fmaf_rn(p.mu, m[j][k], g[k]), u = p.nesterov ? __fmaf_rn(p.mu, now, g[k]) : now;
-              squares = fmaf(u, u, squares);
+              const float now = __fmaf_rn(p.mu, m[j][k], g[k]);
+              u[k] = p.nesterov ? __fmaf_rn(p.mu, now, g[k]) : now;
             }
+            squares.add(u, 8);
           }
         }
-        all += squares;
+        all += squares.total();
         continue;
       }
 #pragma unroll
@@ -797,11 +799,9 @@ __global__ void __launch_bounds__(kPassThreads) sum_squares(const __grid_constan
         if (row >= e.rows || n <= 0) continue;
         float u[8], m[8];
         direction8<T, MUON>(p, e, which, row, col, n, true, u, m);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < n) squares = fmaf(u[k], u[k], squares);
+        squares.add(u, n);
       }
-      all += squares;
+      all += squares.total();
     }
     all = block_sum(all);
     if (threadIdx.x == 0) p.part[blockIdx.x + which] = all;
@@ -812,10 +812,10 @@ constexpr int kTurnBytes = kPassCols * (kPassRows + 1) * 4;
 
 // A row's values on their way to X: times the power of two, in their parts, to
 // their place or to be turned.
-__device__ __forceinline__ void to_first(const PassArgs& p, const Entry& e, int row, int col, int in_tile, float scale,
-                                         float (&u)[8], uint32_t* turned) {
+__device__ __forceinline__ void to_first(const PassArgs& p, const Entry& e, int row, int col, int in_tile,
+                                         const First& x0, float (&u)[8], uint32_t* turned) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) u[k] = scale != 0.f ? u[k] * scale : 0.f;
+  for (int k = 0; k < 8; ++k) u[k] = x0(u[k]);
   uint4 hi, lo;
   split8(u, hi, lo);
   if (!e.transposed) {
@@ -851,12 +851,8 @@ __global__ void __launch_bounds__(kPassThreads) make_first(const __grid_constant
     double s = 0.0;
     for (unsigned b = first + threadIdx.x; b < gridDim.x && stretch(p.tiles, b) < past; b += kPassThreads)
       if (stretch(p.tiles, b + 1) > stretch(p.tiles, b)) s += p.part[b + which];
-    const float norm = static_cast<float>(sqrt(block_sum(s)));
-    const bool finite = isfinite(norm);
-    const int up = norm > 0.f && finite ? min(12 - ilogbf(norm), 126) : 0;
-    const float scale = finite ? exp2f(static_cast<float>(up)) : 0.f;
-    if (t == tile0 && threadIdx.x == 0)
-      p.norms[which] = {norm > 0.f && finite ? kScaleX / (norm * scale) : 0.f, finite};
+    const First x0(block_sum(s));
+    if (t == tile0 && threadIdx.x == 0) p.norms[which] = {x0.unit, x0.finite};
     for (; t < end; ++t) {
       const int tile = static_cast<int>(t - tile0), ty = tile / across, col0 = (tile - ty * across) * kPassCols;
       const int col = col0 + static_cast<int>(threadIdx.x & 31) * 8, n = e.cols - col;
@@ -886,8 +882,8 @@ __global__ void __launch_bounds__(kPassThreads) make_first(const __grid_constant
               m[j][k] = __fmaf_rn(p.mu, m[j][k], g[j][k]);
               g[j][k] = p.nesterov ? __fmaf_rn(p.mu, m[j][k], g[j][k]) : m[j][k];
             }
-            if (finite) dev::st_32B(e.momentum + static_cast<int64_t>(row) * e.cols + col, m[j]);
-            to_first(p, e, row, col, in_tile, scale, g[j], turned);
+            if (x0.finite) dev::st_32B(e.momentum + static_cast<int64_t>(row) * e.cols + col, m[j]);
+            to_first(p, e, row, col, in_tile, x0, g[j], turned);
           }
         }
       } else {
@@ -897,8 +893,8 @@ __global__ void __launch_bounds__(kPassThreads) make_first(const __grid_constant
           if (row >= e.rows || n <= 0) continue;
           float u[8], m[8];
           direction8<T, MUON>(p, e, which, row, col, n, false, u, m);
-          if (MUON && finite) store_some(e.momentum + static_cast<int64_t>(row) * e.cols + col, e.wide, n, m);
-          to_first(p, e, row, col, in_tile, scale, u, turned);
+          if (MUON && x0.finite) store_some(e.momentum + static_cast<int64_t>(row) * e.cols + col, e.wide, n, m);
+          to_first(p, e, row, col, in_tile, x0, u, turned);
         }
       }
       if (e.transposed) {

@@ -181,28 +181,23 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
       count = c0 + nl - col;
     }
   };
-  float mine = 0.f;
+  Squares mine;
   for (int i = threadIdx.x; i < items; i += kThreads) {
     int row, col, count;
     item(i, row, col, count);
     float u[8], mom[8];
     direction8<T, MUON>(p, e, which, row, col, count, true, u, mom);
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < count) mine = fmaf(u[k], u[k], mine);
+    mine.add(u, count);
   }
-  double all = block_sum<kThreads>(mine);
+  double all = block_sum<kThreads>(mine.total());
   if (ctas > 1) {
     if (threadIdx.x == 0) squares_here = all;
     meet_cluster();
     all = 0.0;
     for (int k = 0; k < ctas; ++k) all += ld_there64(in_cta(smem_addr(&squares_here), k));
   }
-  const float norm = static_cast<float>(sqrt(all));
-  const bool finite = isfinite(norm);
-  const int up = norm > 0.f && finite ? min(12 - ilogbf(norm), 126) : 0;
-  const float scale = finite ? exp2f(static_cast<float>(up)) : 0.f;
-  const float unit = norm > 0.f && finite ? kScaleX / (norm * scale) : 0.f;
+  const First x0(all);
+  const bool finite = x0.finite;
   for (int i = threadIdx.x; i < items; i += kThreads) {
     int row, col, count;
     item(i, row, col, count);
@@ -210,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
     direction8<T, MUON>(p, e, which, row, col, count, false, u, mom);
     if (MUON && finite) store_some(e.momentum + static_cast<int64_t>(row) * e.cols + col, e.wide, count, mom);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) u[k] = finite && k < count ? u[k] * scale : 0.f;
+    for (int k = 0; k < 8; ++k) u[k] = k < count ? x0(u[k]) : 0.f;
     uint4 hi, lo;
     split8(u, hi, lo);
     if (!turned) {
@@ -289,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
   for (int step = 0; step < g.steps; ++step) {
     const int parts = step < g.fine ? 2 : 1, x_parts = step == 0 ? min(parts, g.first_parts) : parts;
     const bool last = step + 1 == g.steps;
-    const float rest = step == 0 ? unit : 1.f;       // what the first X lacks of the norm
+    const float rest = step == 0 ? x0.unit : 1.f;       // what the first X lacks of the norm
     const float gram = rest * rest * (kScaleA / (kScaleX * kScaleX));
 
     // A = X X^T

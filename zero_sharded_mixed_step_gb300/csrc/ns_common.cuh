@@ -180,6 +180,58 @@ struct PassArgs {
   Norm* norms;
 };
 
+// A thread's sum of squares.  fp32 holds the squares of values between 2^-63 and 2^63 alone: eight neighbours whose
+// largest lies outside [2^-40, 2^55] are summed at a scale of their own (what vanishes beside that one is 2^-69 of it),
+// so that every finite input has the norm it has.  A momentum whose gradients stay 0 gets there in time.
+struct Squares {
+  float here = 0.f, low = 0.f, high = 0.f;      // of values as they are, times 2^100, times 2^-100
+
+  // up to 8 values, n of which exist
+  __device__ __forceinline__ void add(const float (&u)[8], int n) {
+    float most = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) most = fmaxf(most, fabsf(u[k]));
+    if (most >= 0x1p-40f && most <= 0x1p55f) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < n) here = fmaf(u[k], u[k], here);
+      return;
+    }
+    const bool small = most < 0x1p-40f;          // or nothing but NaN
+    const float scale = small ? 0x1p100f : 0x1p-100f;
+    float s = small ? low : high;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) s = fmaf(u[k] * scale, u[k] * scale, s);
+    (small ? low : high) = s;
+  }
+  __device__ __forceinline__ double total() const {
+    double s = here;
+    if (low != 0.f || high != 0.f) s += 0x1p-200 * low + 0x1p200 * high;
+    return s;
+  }
+};
+
+// How the first X is had from an input of the norm that a sum of squares gives: times a power of two, in two factors
+// since fp32 may not hold it, that brings its norm to [2^12, 2^13).
+struct First {
+  float half, rest;            // the factors; 0 where the norm is not finite
+  float unit;                  // 2^12 over the stored X's norm, 0 for a norm of 0
+  bool finite;
+
+  __device__ __forceinline__ explicit First(double squares) {
+    const double norm = sqrt(squares);
+    finite = isfinite(norm);
+    const bool some = finite && norm > 0.0;
+    const int up = some ? 12 - ilogb(norm) : 0;
+    half = finite ? exp2f(static_cast<float>(up / 2)) : 0.f;
+    rest = exp2f(static_cast<float>(up - up / 2));
+    unit = some ? kScaleX / static_cast<float>(scalbn(norm, up)) : 0.f;
+  }
+  __device__ __forceinline__ float operator()(float u) const { return finite ? u * half * rest : 0.f; }
+};
+
 template <int THREADS = kPassThreads>
 __device__ __forceinline__ double block_sum(double s) {
   __shared__ double of_warp[THREADS / 32];
