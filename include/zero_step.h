@@ -897,10 +897,18 @@ int64_t zero_orthogonalize_workspace_bytes(int64_t n_matrices, const int64_t* ro
  *   steps, coefficients  1..32 steps, 3 doubles each, at most 64 in size.  Singular
  *              values must stay below 4 on the way (fp16's range).
  *   fine_steps the first so many steps carry every operand as a sum of two fp16
- *              values (22 bits), the others as one (11 bits); -1 chooses: all for
- *              ZERO_FP32, else all but the last three.  With Muon's coefficients
- *              the result is 1e-3 to 2e-3 off so (2-norm), 1e-2 with 0 where few
- *              singular values stand above the rest, 1e-6 with all.
+ *              values (22 bits), the others as one (11 bits); -1 chooses: all, for
+ *              ZERO_BF16 all but the last.  With Muon's coefficients the result is
+ *              at most so far from 64 bits before its own rounding (Frobenius norm
+ *              of the difference over the result's; own rounding: bf16 1.7e-3, fp16
+ *              2.1e-4), for singular values from all alike to k^-2, exp(-k / 20) and
+ *              few or half of them 100 to 10000 times the rest, and for rank one:
+ *                fine_steps   0      1      2        3      4        5 (of five)
+ *                any          5e-2   4e-2   9e-3     5e-3   1.2e-3   3e-7 L
+ *                rank one     2e-1   4e-2   1.8e-2   5e-3   2e-3     4.5e-7 L
+ *                Gaussian     1.6e-3 1.6e-3 1.6e-3   1e-3   6e-4     8e-8 L
+ *              L being the longer side, over which the sums of products are cut to
+ *              24 bits as they grow.
  *   workspace  device, 256-byte aligned, any contents; its first 4 bytes count
  *              waits that gave up (zero_lm_workspace_status).
  * A matrix of norm 0 gives 0, one that holds an infinity or a NaN NaN; finite values

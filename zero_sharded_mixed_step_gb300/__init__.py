@@ -1304,8 +1304,7 @@ class Orthogonalize(_Matrices):
     """Newton-Schulz orthogonalisation of matrices of the given (rows, cols),
     all of one dtype: "fp16", "bf16" or "fp32" (zero_orthogonalize).
     ``coefficients`` holds (a, b, c) for each step; ``fine_steps`` of them carry
-    their operands in two 16-bit parts (None: all but the last three, for fp32
-    all).  Workspace and stream as for :class:`LmLoss`."""
+    their operands in two 16-bit parts (None: all, for bf16 all but the last).  Workspace and stream as for :class:`LmLoss`."""
 
     def __init__(self, shapes, dtype="bf16", coefficients=MUON_COEFFICIENTS, fine_steps=None, device="cuda",
                  stream=None, alloc=None):

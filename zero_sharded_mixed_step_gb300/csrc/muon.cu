@@ -33,13 +33,14 @@
 // Precision.  A singular value far below 1 grows by `a` (3.4) a step, and with
 // it the noise that rounding X, A and P to 16 bits leaves in its direction:
 // with fp16 operands throughout, a matrix whose largest singular values stand
-// 20 times above the rest comes out 1.4e-2 off (2-norm), with bf16 11e-2.  So
-// in the first `fine` steps every operand is a sum of two fp16 parts (22 bits)
-// and a product three products of parts; the last steps, after which little
-// growth is left, take one part.  Three such steps leave an error of about 1e-3,
-// 2e-3 where few singular values stand far above the rest, which is what a bf16
-// result's own rounding comes to (two such steps 1e-3 at most, at 1.1 times the
-// time).
+// 20 times above the rest comes out 1.4e-2 off (Frobenius norm of the difference
+// over the result's), with bf16 11e-2.  So in the first `fine` steps every
+// operand is a sum of two fp16 parts (22 bits) and a product three products of
+// parts.  A bf16 result takes them in all steps but the last, after which nothing
+// grows: what that one leaves, 3e-4 to 9e-4 over the spectra of zero_step.h,
+// stays below the result's own rounding of 1.7e-3 (two such steps leave up to
+// 4e-3).  fp16 results, whose own rounding is 2.1e-4, fp32 results and the step,
+// which writes an fp32 master, take all steps in two parts.
 // X and A are stored times 2^12, P times 2^9: entries of fp16's normal range.
 // The first X is the input times a power of two, the rest of 1 / |G| (between
 // 1/2 and 1) being applied in the epilogues: a 16-bit input is then exact in
@@ -1214,9 +1215,9 @@ int check_workspace(const void* workspace, int64_t bytes, int64_t needed) {
   return ZERO_OK;
 }
 
-// The steps that carry two parts where the caller leaves it open: all but the
-// last three, for fp32 results all.
-int fine_steps(int fine, int steps, bool all) { return fine >= 0 ? fine : all ? steps : std::max(0, steps - 3); }
+// The steps that carry two parts where the caller leaves it open: all, for bf16
+// results all but the last (see above).
+int fine_steps(int fine, int steps, bool bf16) { return fine >= 0 ? fine : bf16 ? steps - 1 : steps; }
 
 // Fills an entry's place in the workspace.
 void place(Entry& e, const Group& g, int64_t member, char* ws) {
@@ -1289,7 +1290,7 @@ extern "C" int zero_orthogonalize(int64_t n_matrices, const int64_t* rows, const
     e.wide = both % (8 * item) == 0 && (e.cols | e.in_stride | e.out_stride) % 8 == 0;
     return e;
   };
-  Recurrence r = {steps, fine_steps(fine, steps, dtype == ZERO_FP32), coefficients, dtype == ZERO_FP32 ? 2 : 1,
+  Recurrence r = {steps, fine_steps(fine, steps, dtype == ZERO_BF16), coefficients, dtype == ZERO_FP32 ? 2 : 1,
                   kLast, dtype};
   std::vector<Entry> small;
   for (int64_t i : plan.small) small.push_back(entry(i));
