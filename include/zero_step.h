@@ -908,7 +908,8 @@ int64_t zero_orthogonalize_workspace_bytes(int64_t n_matrices, const int64_t* ro
  *                rank one     2e-1   4e-2   1.8e-2   5e-3   2e-3     4.5e-7 L
  *                Gaussian     1.6e-3 1.6e-3 1.6e-3   1e-3   6e-4     8e-8 L
  *              L being the longer side, over which the sums of products are cut to
- *              24 bits as they grow.
+ *              24 bits as they grow.  For ZERO_FP32 they are kept over 64 products
+ *              at a time: 6e-5, 2e-4 and 1e-5 with all steps, whatever the size.
  *   workspace  device, 256-byte aligned, any contents; its first 4 bytes count
  *              waits that gave up (zero_lm_workspace_status).
  * A matrix of norm 0 gives 0, one that holds an infinity or a NaN NaN; finite values

@@ -21,9 +21,14 @@ pytestmark = pytest.mark.gpu
 STATED = (5e-2, 4e-2, 9e-3, 5e-3, 1.2e-3, 3e-7)
 RANK_ONE = (2e-1, 4e-2, 1.8e-2, 5e-3, 2e-3, 4.5e-7)
 GAUSSIAN = (1.6e-3, 1.6e-3, 1.6e-3, 1e-3, 6e-4, 8e-8)
+# fp32 results' sums are cut within 64 products alone, 3e-7, 4.5e-7 and 8e-8 times 64; beside it come operands of 22
+# bits, which leave twice what fp32's 24 do (a plain fp32 form is up to 2e-5, 8e-5 and 2.5e-6 off).
+FP32 = {"rank one": 2e-4, "gaussian": 1e-5}
 
 
-def stated(name, fine, rows, cols):
+def stated(name, fine, rows, cols, dtype=None):
+    if fine == 5 and dtype == "fp32":
+        return FP32.get(name, 6e-5)
     row = {"rank one": RANK_ONE, "gaussian": GAUSSIAN}.get(name, STATED)
     return row[fine] * (max(rows, cols) if fine == 5 else 1)
 
@@ -68,7 +73,7 @@ def test_fine_steps(rows, cols, dtype):
             want = ref.orthogonal(x)
             own = off(want.to(DT[dtype]), want)          # the result's own rounding
             used = fine if fine is not None else 4 if dtype == "bf16" else 5
-            assert off(got, want) <= stated(name, used, rows, cols) + 1.1 * own, (name, fine)
+            assert off(got, want) <= stated(name, used, rows, cols, dtype) + 1.1 * own, (name, fine)
             if fine is None and dtype != "fp32":
                 # by default the steps leave less than the result's own rounding: sqrt(1 + 1) of it together
                 assert off(got, want) <= 1.42 * own, name
@@ -89,3 +94,24 @@ def test_the_steps_update(dtype):
         op.status()
         for name, x, theta in zip(names, u, op.views(op.master)):
             assert off(-theta, ref.orthogonal(x)) <= stated(name, 5, rows, cols), name
+
+
+@pytest.mark.parametrize("rows,cols", [(100, 900), (200, 300), (430, 1321), (1024, 2048), (2300, 700)])
+def test_fp32_results_do_not_lose_with_the_size(rows, cols):
+    """Long sums of one sign, whose cuts would add up: gradients with directions that many tokens share."""
+    x = gaussian(rows, cols) + (gaussian(rows, 32, 1) * 0.3) @ gaussian(32, cols, 2) / 32 ** 0.5
+    got = zs.Orthogonalize([(rows, cols)], "fp32").forward([x])[0]
+    assert off(got, ref.orthogonal(x)) <= FP32["gaussian"]
+
+
+@pytest.mark.parametrize("fine", [1, 2, 3, 4])
+def test_steps_in_two_parts_beside_others(fine):
+    """fp32 results with steps of both kinds: tiles of both follow one another through the same accumulators."""
+    shapes = [(768, 768)] * 11 + [(300, 900)] * 7 + [(520, 264)] * 5
+    xs = [gaussian(*s, seed=k) for k, s in enumerate(shapes)]
+    op = zs.Orthogonalize(shapes, "fp32", fine_steps=fine)
+    want = [ref.orthogonal(x) for x in xs]
+    for _ in range(3):
+        for k, got in enumerate(op.forward(xs)):
+            assert off(got, want[k]) <= GAUSSIAN[fine], (fine, k)
+    op.status()

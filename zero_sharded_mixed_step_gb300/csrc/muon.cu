@@ -101,6 +101,16 @@ constexpr int kQueue = 4;            // tiles on their way through a pair
 constexpr int kRunSmem = kStages * kStageBytes + 1024;
 constexpr int kFewGroups = 3, kMaxGroups = 12;       // shapes of one launch
 constexpr int64_t kPairs = 76;       // pairs of CTAs among GB300's 152 SMs
+// Blocks of K that one accumulator takes in the steps in two parts of an fp32 result.  The tensor core cuts its sums
+// to 24 bits at every instruction, always towards 0: 430 x 1321 came out 2.6e-5 off, growing with the size.  The
+// epilogue adds up the accumulators of a tile, rounding to nearest, in TMEM beside them.  Whole tiles, 4, 2 blocks and
+// 1 leave 24 matrices of 768 x 768 2.8e-5, 1.1e-5, 6.3e-6 and 3.9e-6 off (plain fp32 2.6e-6) in 527, 609, 669 and 757
+// us; 2048 x 2048 takes 443, 479, 498 and 536.
+constexpr int kSegment = 1;
+// Columns of every tile of such a launch at most: an accumulator's neighbour in TMEM takes the sums, which are read
+// while the next tile's first products run.
+constexpr int kSegmentTile = 128, kSumsAt = 128;
+static_assert(kSumsAt >= kSegmentTile && kSumsAt + kSegmentTile <= kTileN);
 
 enum Kind : int { kGram, kPoly, kMultiply, kApply };
 enum Final : int { kLast, kUpdate };       // what the last product does
@@ -138,6 +148,7 @@ struct RunArgs {
   int shapes;
   int dtype;                   // kLast: of the results; kUpdate: of the 16-bit copies
   int stall;                   // testing the bounded waits: the first tile's first block of K never arrives
+  int segment;                 // blocks of K for one accumulator in fine steps; 0: a tile's
   const Entry* entries;
   const Norm* norms;
   unsigned int* next;          // tiles taken so far (0 at the launch)
@@ -220,6 +231,12 @@ __device__ __forceinline__ Tile locate(const RunArgs<GROUPS>& g, unsigned t, Cur
   return x;
 }
 
+// Blocks of K of one accumulator of a tile.
+template <int GROUPS>
+__device__ __forceinline__ int segment_of(const RunArgs<GROUPS>& g, const Phase& f, const Tile& x) {
+  return f.parts_a > 1 && g.segment > 0 ? g.segment : x.kb;
+}
+
 template <int GROUPS>
 __device__ __forceinline__ const Phase& phase_of(const RunArgs<GROUPS>& g, const Tile& x) {
   return g.phase[g.shape[x.shape].joined][x.phase];
@@ -293,22 +310,49 @@ __device__ __forceinline__ void fetch(const RunArgs<GROUPS>& g, const Tile& x, i
   }
 }
 
-// This thread's row of an accumulator, 16 columns at a time from `first` in
-// steps of 64; `release` runs when the last ones are in registers.
+// A tile's columns of this thread's row: the accumulator's, and the sums of
+// those before it, if any.
+struct Sums {
+  uint32_t tmem, before;
+  bool some;                   // there are sums of accumulators before
+
+  __device__ __forceinline__ void load(int c, float (&v)[kCols]) const {
+    tmem_ld16(tmem + c, v);
+    tmem_ld_wait(v);
+    if (!some) return;
+    float w[kCols];
+    tmem_ld16(before + c, w);
+    tmem_ld_wait(w);
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) v[k] += w[k];
+  }
+  // The accumulator joins the sums.
+  __device__ __forceinline__ void keep(int first, int bn) const {
+#pragma unroll 1
+    for (int c = first; c < bn; c += 64) {
+      float v[kCols];
+      load(c, v);
+      tmem_st16(before + c, v);
+    }
+    tmem_st_wait();
+  }
+};
+
+// 16 columns at a time from `first` in steps of 64; `release` runs when the
+// last ones are in registers.
 template <typename F, typename R>
-__device__ __forceinline__ void each_16(uint32_t tmem, int first, int bn, F f, R release) {
+__device__ __forceinline__ void each_16(const Sums& sums, int first, int bn, F f, R release) {
 #pragma unroll 1
   for (int c = first; c < bn; c += 64) {
     float v[kCols];
-    tmem_ld16(tmem + c, v);
-    tmem_ld_wait(v);
+    sums.load(c, v);
     if (c + 64 >= bn) release();
     f(c, v);
   }
 }
 
 template <int FINAL, int GROUPS, typename R>
-__device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x, uint32_t tmem, Beside& b, int row,
+__device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x, const Sums& sums, Beside& b, int row,
                                          int share, R release) {
   const Shape& h = g.shape[x.shape];
   const int bn = x.bn, n0 = x.nt * bn;
@@ -322,7 +366,7 @@ __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x
   const bool two = f.two;
   if (x.kind == kGram || x.kind == kMultiply) {
     uint16_t* out = h.at[f.out] + x.matrix * h.apart_a;
-    each_16(tmem, share * kCols, bn, [&](int c, float (&v)[kCols]) {
+    each_16(sums, share * kCols, bn, [&](int c, float (&v)[kCols]) {
 #pragma unroll
       for (int k = 0; k < kCols; ++k) v[k] *= scale;
       store_block(out, h.lda, h.part_a, h.m, h.m, row, n0 + c, v, two);
@@ -331,7 +375,7 @@ __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x
     uint16_t* out = h.at[f.out] + x.matrix * h.apart_a;
     const float a = g.coefficients[3 * f.step] * kScaleP, once = g.coefficients[3 * f.step + 1] * (kScaleP / kScaleA);
     const float square = g.coefficients[3 * f.step + 2] * (kScaleP / (kScaleA * kScaleA));
-    each_16(tmem, share * kCols, bn, [&](int c, float (&v)[kCols]) {
+    each_16(sums, share * kCols, bn, [&](int c, float (&v)[kCols]) {
       const int col0 = n0 + c;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -349,7 +393,7 @@ __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x
     }, release);
   } else if (!f.last) {
     uint16_t* out = h.at[f.out] + x.matrix * h.apart_x;
-    each_16(tmem, share * kCols, bn, [&](int c, float (&v)[kCols]) {
+    each_16(sums, share * kCols, bn, [&](int c, float (&v)[kCols]) {
 #pragma unroll
       for (int k = 0; k < kCols; ++k) v[k] *= scale;
       store_block(out, h.ldx, h.part_x, h.m, h.n, row, n0 + c, v, two);
@@ -358,7 +402,7 @@ __device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x
     const Entry& e = g.entries[which];
     const bool finite = g.norms[which].finite;
     if (!finite) scale = NAN;
-    each_16(tmem, share * kCols, bn, [&](int c, float (&v)[kCols]) {
+    each_16(sums, share * kCols, bn, [&](int c, float (&v)[kCols]) {
       // a norm that is not finite leaves the state as it was
       if (row >= h.m || n0 + c >= h.n || (FINAL == kUpdate && !finite)) return;
 #pragma unroll
@@ -506,25 +550,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
     if (!ok && lead) failed = 1;
   } else if (warp == 1) {
     if (rank == 0) {
-      int s = 0;
+      int s = 0, turn = 0;     // accumulators begun
       uint32_t phase = 0;
       for (int i = 0;; ++i) {
         const Tile x = tile_of(i);
         if (!ok || x.kind < 0) break;
         const Phase& f = phase_of(g, x);
         const uint32_t idesc = instr_desc(false, false, false, kTileM, x.bn);
-        const int a = i & 1, blocks = x.kb, a_row = x.mt * kTileM;
-        ok = wait_all(taken(a), ((i >> 1) & 1) ^ 1);
+        const int blocks = x.kb, a_row = x.mt * kTileM, segment = segment_of(g, f, x);
+        uint32_t d = 0;
+        int a = 0;
+        auto begin = [&] {
+          a = turn & 1;
+          ok = wait_all(taken(a), ((turn >> 1) & 1) ^ 1);
+          if (!ok) return;
+          fence_after();
+          d = tmem + a * kTileN;
+          ++turn;
+        };
+        begin();
         if (!ok) break;
-        fence_after();
-        const uint32_t d = tmem + a * kTileN;
         // 16 values of K further: 32 bytes within a K-major row, 16 rows of an MN-major tile
         const uint64_t a_k = operand_desc(ring, 0), a_mn = operand_desc(ring, 8192);
         const uint64_t b_k = operand_desc(ring + kSlotBytes, 0), b_mn = operand_desc(ring + kSlotBytes, 8192);
         // the tile's blocks of K in PA and PB parts, known here for the instructions to follow one another closely
         auto run = [&](auto pa, auto pb) {
           constexpr int PA = decltype(pa)::value, PB = decltype(pb)::value;
+          int first = 0;       // block of this accumulator
           for (int kb = 0; kb < blocks; ++kb) {
+            if (PA > 1 && kb == first + segment) {
+              if (lead) mma_commit(done(a));
+              __syncwarp();
+              begin();
+              if (!ok) break;
+              first = kb;
+            }
             const bool of_a = x.kind != kGram && exchanged(a_row, kb), of_b = b_is_mn(x, kb);
             const uint64_t a_step = of_a ? 128 : 2, b_step = of_b ? 128 : 2;
             const uint32_t id = idesc | (of_a ? 1u << 15 : 0u) | (of_b ? 1u << 16 : 0u);
@@ -535,7 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
             const uint64_t da = (of_a ? a_mn : a_k) + s * (kStageBytes >> 4), db = (of_b ? b_mn : b_k) + s * (kStageBytes >> 4);
             if (lead) {
 #pragma unroll
-              for (int q = 0; q < kTileK / 16; ++q) mma(d, da + q * a_step, db + q * b_step, id, kb > 0 || q > 0);
+              for (int q = 0; q < kTileK / 16; ++q) mma(d, da + q * a_step, db + q * b_step, id, kb > first || q > 0);
               if (PA == 1) mma_commit(empty(s));
             }
             __syncwarp();
@@ -633,21 +693,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
     if (!ok && lead) failed = 1;
   } else if (warp >= 4) {
     const int quad = warp & 3, share = (warp - 4) >> 2;
+    const uint32_t my_lanes = tmem + (static_cast<uint32_t>(quad) << 21);
     Beside beside = {};
+    int turn = 0;              // accumulators read
     for (int i = 0;; ++i) {
-      const int a = i & 1;
       const Tile x = tile_of(i);
       if (!ok || x.kind < 0) break;
       const int row = x.mt * kTileM + static_cast<int>(rank) * 128 + quad * 32 + lane;
       fetch<FINAL>(g, x, row, share * kCols, beside);
-      ok = wait_all(done(a), (i >> 1) & 1);
-      if (!ok) break;
-      fence_after();
-      epilogue<FINAL>(g, x, tmem + a * kTileN + (static_cast<uint32_t>(quad) << 21), beside, row, share, [&] {
+      const int segment = segment_of(g, phase_of(g, x), x);
+      Sums sums = {0, my_lanes + kSumsAt, false};
+      int a = 0;
+      auto next = [&] {
+        a = turn & 1;
+        ok = wait_all(done(a), (turn >> 1) & 1);
+        fence_after();
+        sums.tmem = my_lanes + a * kTileN;
+        ++turn;
+      };
+      auto release = [&] {
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(in_cta(taken(a), 0));
-      });
+      };
+      next();
+      for (int k = segment; ok && k < x.kb; k += segment) {
+        sums.keep(share * kCols, x.bn);
+        sums.some = true;
+        release();
+        next();
+      }
+      if (!ok) break;
+      epilogue<FINAL>(g, x, sums, beside, row, share, release);
       __syncwarp();
       // Warps may be a tile or two apart, not as many as there are barriers: of two tiles' products, at most, some warp
       // has not read the sums.
@@ -1027,16 +1104,16 @@ int tiles_of(int of, int64_t m, int64_t n, int bn) {
 // the products of parts, or the time its operands take to load (48 bytes a
 // cycle); a tile has some 2000 cycles besides, and the tiles of a product that
 // are one more than the pairs take as long as two each.
-int width_of(int of, int64_t m, int64_t n, int matrices, bool fine) {
+int width_of(int of, int64_t m, int64_t n, int matrices, bool fine, int most) {
   const int products = fine ? 3 : 1, parts = fine ? 2 : 1;
   const int64_t kb = ceil_div(of == 0 ? n : m, kTileK);
-  int best = kTileN;
+  int best = most;
   double least = 0;
-  for (int bn : {256, 128, 64}) {
+  for (int bn = most; bn >= 64; bn /= 2) {
     const double tiles = static_cast<double>(tiles_of(of, m, n, bn)) * matrices;
     const double block = std::max<double>(2 * bn * products, (128 + bn / 2) * kTileK * 2 * parts / 48.0);
     const double cost = (kb * block + 2000) * (matrices > 1 ? std::max(1.0, tiles / kPairs) : std::ceil(tiles / kPairs));
-    if (bn == kTileN || cost < least) {
+    if (bn == most || cost < least) {
       least = cost;
       best = bn;
     }
@@ -1093,6 +1170,7 @@ int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, ch
   static thread_local RunArgs<GROUPS> g;
   std::memset(&g, 0, sizeof g);
   g.dtype = r.dtype;
+  g.segment = FINAL == kLast && r.dtype == ZERO_FP32 && r.fine > 0 ? kSegment : 0;
   g.stall = std::exchange(stall, false);
   g.entries = reinterpret_cast<const Entry*>(ws + plan.table);
   g.norms = reinterpret_cast<const Norm*>(ws + plan.norms);
@@ -1118,7 +1196,7 @@ int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, ch
     g.entries_here += c;
     for (int fine = 0; fine < 2; ++fine)
       for (int of = 0; of < 3; ++of) {
-        h.bn[fine][of] = width_of(of, m, n, c, fine);
+        h.bn[fine][of] = width_of(of, m, n, c, fine, g.segment > 0 ? kSegmentTile : kTileN);
         h.tiles[fine][of] = tiles_of(of, m, n, h.bn[fine][of]);
         most = std::max(most, static_cast<int64_t>(c) * h.tiles[fine][of]);
         all += 4 * static_cast<int64_t>(r.steps) * c * h.tiles[fine][of];

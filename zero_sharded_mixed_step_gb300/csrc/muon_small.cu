@@ -252,19 +252,29 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
     fence_after();
   };
   // sums over K of products of operands in one or two parts; steps of K of a K-major operand lie 32 bytes apart within
-  // a tile of 64, those of X as P's partner 16 rows
+  // a tile of 64, those of X as P's partner 16 rows.  The products of low parts come first: the tensor core cuts its
+  // sums to 24 bits at every instruction, which costs nothing while they are small.
   auto multiply = [&](uint32_t a, uint32_t a_low, int a_parts, uint32_t b, uint32_t b_low, int b_parts, int K, int N,
                       bool b_mn) {
     if (!ok || !issuer) return;
     const uint32_t idesc = instr_desc(false, false, b_mn, 128, N);
-    for (int k = 0; k < K / 16; ++k) {
-      const uint32_t k_off = (k >> 2) * tile + (k & 3) * 32;
-      const uint64_t da = operand_desc(a + k_off, 0);
-      const uint64_t db = b_mn ? operand_desc(b + k * 2048, tile) : operand_desc(b + k_off, 0);
-      mma_one(tmem, da, db, idesc, k > 0);
-      if (a_parts > 1) mma_one(tmem, da + (a_low >> 4), db, idesc, true);
-      if (b_parts > 1) mma_one(tmem, da, db + (b_low >> 4), idesc, true);
-    }
+    bool some = false;
+    auto each = [&](auto f) {
+      for (int k = 0; k < K / 16; ++k) {
+        const uint32_t k_off = (k >> 2) * tile + (k & 3) * 32;
+        f(operand_desc(a + k_off, 0), b_mn ? operand_desc(b + k * 2048, tile) : operand_desc(b + k_off, 0));
+      }
+    };
+    auto add = [&](uint64_t da, uint64_t db) {
+      mma_one(tmem, da, db, idesc, some);
+      some = true;
+    };
+    if (a_parts > 1 || b_parts > 1)
+      each([&](uint64_t da, uint64_t db) {
+        if (a_parts > 1) add(da + (a_low >> 4), db);
+        if (b_parts > 1) add(da, db + (b_low >> 4));
+      });
+    each(add);
   };
   // 16 sums of this thread's row, from column c
   auto load = [&](int c, float (&v)[kCols]) {
