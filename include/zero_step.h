@@ -915,7 +915,9 @@ int64_t zero_orthogonalize_workspace_bytes(int64_t n_matrices, const int64_t* ro
  * A matrix of norm 0 gives 0, one that holds an infinity or a NaN NaN; finite values
  * of any size have their norm, whose squares are summed in fp32 within a thread, at
  * scales that hold them, and in fp64 beyond.  Products accumulate in fp32; the
- * result is rounded once.  The same inputs give the same bits every time.
+ * result is rounded once.  The same inputs give the same bits every time; the
+ * other matrices of a call change none of a matrix's, but for the order of the
+ * norm's fp64 sum where its smaller side is above 128 or its larger above 2048.
  * Enqueues on `stream` and returns.  ZERO_E_ARG / ZERO_E_ALIGN / ZERO_E_CUDA.
  */
 int zero_orthogonalize(int64_t n_matrices, const int64_t* rows, const int64_t* cols, int dtype, const void* const* in,

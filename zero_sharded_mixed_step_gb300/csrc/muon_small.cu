@@ -66,6 +66,12 @@ struct SmallArgs {
   TablePart<BYTES> table;      // Entry after Entry, then W addresses for each
 };
 
+// The CTAs that a matrix takes.
+__host__ __device__ inline int ctas_for(const Entry& e) {
+  const int n = e.rows > e.cols ? e.rows : e.cols;
+  return (n + kMostSlice - 1) / kMostSlice;
+}
+
 // ---- products by one CTA ------------------------------------------------------------------
 
 __device__ __forceinline__ void alloc_one(uint32_t slot, uint32_t columns) {
@@ -134,9 +140,13 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
   const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
   const uint32_t bar = smem_addr(bars), drained = bar + 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_rank()), ctas = static_cast<int>(cluster_ctas());
-  const int which = static_cast<int>(blockIdx.x) / ctas;
+  const int rank = static_cast<int>(cluster_rank());
+  const int which = static_cast<int>(blockIdx.x) / static_cast<int>(cluster_ctas());
   const Entry& e = reinterpret_cast<const Entry*>(g.table.data)[which];
+  // How a matrix is cut goes by its own shape: its sums are then the same whatever else is in the call.  In a cluster
+  // that is larger the CTAs left over end here; barriers of a cluster wait for those that have not ended.
+  const int ctas = ctas_for(e);
+  if (rank >= ctas) return;
 
   // X is m x n; this CTA has its columns [c0, c0 + nl).  Rows and columns are
   // padded to 16, which is what a matrix instruction takes of K.
@@ -319,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
         load(c, v);
 #pragma unroll
         for (int k = 0; k < kCols; ++k)
-          if (row < mp && c + k < mp) st_shared1(as + ((c + k) * mp + row) * 4, nk > 0 ? v[k] : 0.f);
+          if (row < mp && c + k < mp) st_shared1(as + ((c + k) * mp + row) * 4, v[k]);
       }
       meet_cluster();
       // a share of the groups of 8 columns over all the CTAs: at most 128 x 16 / 2 of them, 2 a thread
@@ -440,14 +450,12 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
 
 // ---- host -------------------------------------------------------------------------
 
-int ctas_for(const Entry& e) { return static_cast<int>(ceil_div(std::max(e.rows, e.cols), kMostSlice)); }
-
-// Bytes of shared memory of a matrix over so many CTAs.  A product takes 128 rows
-// of its first operand whatever there are: what it reads past the last part of
-// A, rows whose sums nobody looks at, is there as well.
-int64_t space_for(const Entry& e, int ctas) {
+// Bytes of shared memory of a matrix in each of its CTAs.  A product takes 128
+// rows of its first operand whatever there are: what it reads past the last part
+// of A, rows whose sums nobody looks at, is there as well.
+int64_t space_for(const Entry& e) {
   const int64_t m = std::min(e.rows, e.cols), n = std::max(e.rows, e.cols);
-  const int64_t mp = round_up(m, 16), slice = round_up(ceil_div(n, ctas), 16);
+  const int64_t mp = round_up(m, 16), slice = round_up(ceil_div(n, ctas_for(e)), 16);
   return 2 * mp * 128 * (ceil_div(slice, 64) + ceil_div(mp, 64)) + (kMostRows - mp) * 128 + 1024;
 }
 
@@ -509,7 +517,7 @@ int run_table(const SmallCall& c, const int* pick, int count, int ctas, bool& st
     a.grads_at = here * static_cast<int>(sizeof(Entry) / 8);
     for (int k = 0; k < here; ++k) {
       const Entry& e = c.entries[pick[from + k]];
-      space = std::max(space, space_for(e, ctas));
+      space = std::max(space, space_for(e));
       std::memcpy(a.table.data + k * sizeof(Entry), &e, sizeof e);
       if (c.W > 0)
         std::memcpy(a.table.data + here * sizeof(Entry) + static_cast<size_t>(k) * 8 * c.W,
@@ -536,7 +544,7 @@ int run_small(const SmallCall& c, bool& stall) {
   std::stable_sort(order.begin(), order.end(),
                    [&](int a, int b) { return ctas_for(c.entries[a]) > ctas_for(c.entries[b]); });
   for (int from = 0; from < c.count;) {
-    // matrices that take as many CTAs go together; where there are SMs for it, so do those that take fewer
+    // matrices that take as many CTAs go together; where there are SMs for it, those that take fewer go with them
     const int ctas = ctas_for(c.entries[order[from]]);
     int to = from;
     while (to < c.count && (ctas_for(c.entries[order[to]]) == ctas || (c.count - from) * ctas <= sm_count())) ++to;
