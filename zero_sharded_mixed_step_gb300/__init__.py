@@ -1354,6 +1354,10 @@ class MuonStep(_Matrices):
         self._setup_matrices(shapes, coefficients, fine_steps)
         if scales is not None and len(scales) != len(self.shapes):
             raise ValueError(f"scales must hold one factor for each of the {len(self.shapes)} matrices")
+        if theta0 is not None:
+            theta0 = [torch.as_tensor(x) for x in theta0]
+            if [tuple(x.shape) for x in theta0] != self.shapes:
+                raise ValueError("theta0 must be a list of matrices of the owner's shapes")
         self.scales = None if scales is None else [float(x) for x in scales]
         self._sc, self._sc_at = (None, None) if scales is None else _c_array("d", self.scales)
         self._workspace(zero_muon_workspace_bytes(self.W, self.shapes), zero=4)
@@ -1364,7 +1368,7 @@ class MuonStep(_Matrices):
             self.p16 = new(self.n, work)
             if theta0 is not None:
                 for to, x in zip(self.views(self.master), theta0):
-                    to.copy_(torch.as_tensor(x))
+                    to.copy_(x)
                 self.p16.copy_(self.master)
         self._new_state = new
         self._state = [_u64_array([x.data_ptr() + at * x.element_size() for at in self.starts])
