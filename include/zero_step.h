@@ -841,7 +841,8 @@ int64_t zero_lm_logprobs_workspace_bytes(int64_t tokens, int64_t vocab, int64_t 
  * logp is 0 where the target is outside [0, vocab); the token's other results
  * are written all the same.  Logits of -infinity and NaN are not listed: where
  * fewer than `top` others are there, the rest of the ids are -1 and their values
- * -infinity (NaN where lse is NaN or -infinity).
+ * -infinity (NaN where lse is NaN or -infinity).  A token with a logit of NaN or
+ * +infinity has NaN for lse, entropy and all its log probabilities.
  *   scale      positive in fp32 and below 2e38: 1 / temperature.
  *   top        0..16 and at most vocab; 0: top_logp and top_ids may be NULL.
  *   logp, entropy, lse  device, `tokens` fp32 values each.
@@ -963,9 +964,14 @@ int zero_muon_step(int W, int64_t n_matrices, const int64_t* rows, const int64_t
  * Wait for `stream` and report the bounded device waits (each about a second)
  * of the LM and matrix calls made with `workspace`: ZERO_E_STATE if any gave up since the
  * last report, so that what it belonged to is incomplete; else ZERO_OK.  What a
- * call could not compute is NaN: the losses (of tokens with a target) and lse
- * that lack a part, or both gradients whole.  The
- * workspace's first 4 bytes hold the count: set them to 0 before the first
+ * call could not compute is NaN:
+ *   the loss and the log probabilities: of the tokens that lack a part the loss or
+ *     logp (0 without a target), lse, entropy and top_logp; their top_ids are -1
+ *     or ids of the vocabulary, not necessarily the likeliest;
+ *   gradients: both, whole;
+ *   zero_orthogonalize: at least the matrices that lack a part, whole;
+ *   zero_muon_step: nothing is marked; the matrices may be partly updated.
+ * The workspace's first 4 bytes hold the count: set them to 0 before the first
  * call if this is to be asked.  `stream` is the calls' (all of them have run
  * when this returns).
  */
