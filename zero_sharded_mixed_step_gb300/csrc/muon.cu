@@ -99,7 +99,7 @@ constexpr int kEpilogueWarps = 16, kTakerWarp = 20;
 constexpr int kCols = 16;            // of a row that an epilogue thread holds at a time
 constexpr int kQueue = 4;            // tiles on their way through a pair
 constexpr int kRunSmem = kStages * kStageBytes + 1024;
-constexpr int kFewGroups = 3, kMaxGroups = 12;       // shapes of one launch
+constexpr int kMaxGroups = 12;       // shapes of one launch, whose parameters hold no more than 32,764 bytes
 constexpr int64_t kPairs = 76;       // pairs of CTAs among GB300's 152 SMs
 // Blocks of K that one accumulator takes in the steps in two parts of an fp32 result.  The tensor core cuts its sums
 // to 24 bits at every instruction, always towards 0: 430 x 1321 came out 2.6e-5 off, growing with the size.  The
@@ -140,9 +140,8 @@ struct Shape {
   int64_t ldx, lda, apart_x, apart_a, part_x, part_a;    // rows, matrices, parts
 };
 
-template <int GROUPS>
 struct RunArgs {
-  Shape shape[GROUPS];
+  Shape shape[kMaxGroups];
   Phase phase[2][kMaxPhases];  // steps one by one, and by twos
   int phases[2];
   int shapes;
@@ -159,6 +158,7 @@ struct RunArgs {
   int entries_here;            // of these shapes, from shape[0].first on
   float coefficients[3 * kMaxSteps];
 };
+static_assert(sizeof(RunArgs) <= 32764);
 
 // What the roles of a pair need to know of a tile.
 struct alignas(16) Tile {
@@ -181,8 +181,7 @@ struct Cursor {
 
 // Tile t of the list, at or after the cursor.  before[h]: the tiles of one
 // matrix's products before, for each shape up to the cursor.
-template <int GROUPS>
-__device__ __forceinline__ Tile locate(const RunArgs<GROUPS>& g, unsigned t, Cursor& c, unsigned* before) {
+__device__ __forceinline__ Tile locate(const RunArgs& g, unsigned t, Cursor& c, unsigned* before) {
   Tile x = {};
   unsigned each = 0;
   for (;;) {
@@ -232,13 +231,11 @@ __device__ __forceinline__ Tile locate(const RunArgs<GROUPS>& g, unsigned t, Cur
 }
 
 // Blocks of K of one accumulator of a tile.
-template <int GROUPS>
-__device__ __forceinline__ int segment_of(const RunArgs<GROUPS>& g, const Phase& f, const Tile& x) {
+__device__ __forceinline__ int segment_of(const RunArgs& g, const Phase& f, const Tile& x) {
   return f.parts_a > 1 && g.segment > 0 ? g.segment : x.kb;
 }
 
-template <int GROUPS>
-__device__ __forceinline__ const Phase& phase_of(const RunArgs<GROUPS>& g, const Tile& x) {
+__device__ __forceinline__ const Phase& phase_of(const RunArgs& g, const Tile& x) {
   return g.phase[g.shape[x.shape].joined][x.phase];
 }
 
@@ -290,8 +287,8 @@ struct Beside {
   uint4 w[4];
 };
 
-template <int FINAL, int GROUPS>
-__device__ __forceinline__ void fetch(const RunArgs<GROUPS>& g, const Tile& x, int row, int c, Beside& b) {
+template <int FINAL>
+__device__ __forceinline__ void fetch(const RunArgs& g, const Tile& x, int row, int c, Beside& b) {
   const Shape& h = g.shape[x.shape];
   const int col0 = x.nt * x.bn + c;
   const Phase& f = phase_of(g, x);
@@ -351,8 +348,8 @@ __device__ __forceinline__ void each_16(const Sums& sums, int first, int bn, F f
   }
 }
 
-template <int FINAL, int GROUPS, typename R>
-__device__ __forceinline__ void epilogue(const RunArgs<GROUPS>& g, const Tile& x, const Sums& sums, Beside& b, int row,
+template <int FINAL, typename R>
+__device__ __forceinline__ void epilogue(const RunArgs& g, const Tile& x, const Sums& sums, Beside& b, int row,
                                          int share, R release) {
   const Shape& h = g.shape[x.shape];
   const int bn = x.bn, n0 = x.nt * bn;
@@ -428,13 +425,13 @@ __device__ __forceinline__ void add_release(unsigned* p, unsigned v) {
 // All the steps of the matrices of a launch: see above.  Operands through a ring
 // of TMA stages, two accumulators in TMEM so that one tile's epilogue runs beside
 // the next one's products.
-template <int FINAL, int GROUPS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(const __grid_constant__ RunArgs<GROUPS> g) {
+template <int FINAL>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(const __grid_constant__ RunArgs g) {
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 3 * kQueue + 6];
   __shared__ Tile queue[kQueue];
   __shared__ uint32_t tmem_slot;
-  __shared__ unsigned before[GROUPS];
+  __shared__ unsigned before[kMaxGroups];
   __shared__ int failed, last_out;
   const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
   const uint32_t bar0 = smem_addr(bars);
@@ -657,7 +654,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ns_run(
   } else if (warp == kTakerWarp) {
     // Takes the next tile when the leader begins to load the one before, waits for what it needs, and tells the roles.
     Cursor cursor;
-    if (lane < GROUPS) before[lane] = 0;
+    if (lane < kMaxGroups) before[lane] = 0;
     __syncwarp();
     for (int i = 0; rank == 0; ++i) {
       const int q = i % kQueue;
@@ -1165,9 +1162,9 @@ int make_phases(Phase* to, const Recurrence& r, bool joined) {
 }
 
 // The steps of plan.groups[from, to).
-template <int FINAL, int GROUPS>
+template <int FINAL>
 int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, char* ws, cudaStream_t s, bool& stall) {
-  static thread_local RunArgs<GROUPS> g;
+  static thread_local RunArgs g;
   std::memset(&g, 0, sizeof g);
   g.dtype = r.dtype;
   g.segment = FINAL == kLast && r.dtype == ZERO_FP32 && r.fine > 0 ? kSegment : 0;
@@ -1218,7 +1215,7 @@ int run_groups(const Plan& plan, size_t from, size_t to, const Recurrence& r, ch
     }
   }
   if (all > INT32_MAX) return fail(ZERO_E_ARG, "too many tiles");
-  const auto fn = ns_run<FINAL, GROUPS>;
+  const auto fn = ns_run<FINAL>;
   ZERO_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRunSmem));
   const int pairs = static_cast<int>(std::min({std::max<int64_t>(1, sm_count() / 2), kPairs, most * static_cast<int64_t>(to - from)}));
   ZERO_CUDA(launch_chained(fn, dim3(2 * pairs), kThreads, kRunSmem, s, g));
@@ -1265,11 +1262,8 @@ int run_all(const Plan& plan, const Recurrence& r, char* ws, cudaStream_t s, boo
   const size_t groups = plan.groups.size();
   for (size_t from = 0; from < groups; from += kMaxGroups) {
     const size_t to = std::min(groups, from + kMaxGroups);
-    const bool few = to - from <= kFewGroups, update = r.last == kUpdate;
-    const int rc = few ? (update ? run_groups<kUpdate, kFewGroups>(plan, from, to, r, ws, s, stall)
-                                 : run_groups<kLast, kFewGroups>(plan, from, to, r, ws, s, stall))
-                       : (update ? run_groups<kUpdate, kMaxGroups>(plan, from, to, r, ws, s, stall)
-                                 : run_groups<kLast, kMaxGroups>(plan, from, to, r, ws, s, stall));
+    const int rc = r.last == kUpdate ? run_groups<kUpdate>(plan, from, to, r, ws, s, stall)
+                                     : run_groups<kLast>(plan, from, to, r, ws, s, stall);
     if (rc) return rc;
   }
   return ZERO_OK;
