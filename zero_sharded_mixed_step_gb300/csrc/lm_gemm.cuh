@@ -899,8 +899,10 @@ __global__ void __launch_bounds__(kSmallThreads) lm_largest_weight(const void* t
                                   static_cast<int64_t>(gridDim.x) * kSmallThreads));
   if ((threadIdx.x & 31) == 0 && of_warp != 0) atomicMax(largest, of_warp);
 }
-// Up to so many tokens it is found beside the hidden vectors' copy, which saves a launch (4 us of 51).
-constexpr int64_t kFewWeights = 4096;
+// Up to so many tokens it is found beside the hidden vectors' copy, by one block, which saves a launch.  Beside it and
+// in a launch of its own, us a gradient: 129 x 2000 x 256 22.6 and 24.7, 1024 26.7 and 26.7, 4096 49.3 and 45.2, 16384
+// 178 and 121; 129 x 8000 x 768 34.9 and 36.7, 1024 51.2 and 51.3, 4096 131 and 119, 16384 526 and 489.
+constexpr int64_t kFewWeights = 1024;
 
 // dh = scale * the sum of the splits' fp32 sums, in the splits' order, BATCH
 // loads at a time: several splits, of few tokens, kFinishBatch (one by one, 38
