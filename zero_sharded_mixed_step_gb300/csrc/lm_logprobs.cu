@@ -15,7 +15,7 @@
 // The forward pass is one product of 2 N V d operations, whose epilogue keeps
 // running sums and a list in each thread's registers while its pair of CTAs
 // moves along a row of tiles (lm_gemm.cuh); the small kernels here join a
-// row's few stretches.  For up to kFewTokens tokens the operands change
+// row's few stretches.  For few tokens (few_tokens) the operands change
 // places as in the loss; the logits then go to the workspace (4 V bytes a
 // token, where alternatives are asked for), and the 32-row groups with the
 // largest maxima are looked through again.
@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(kSmallThreads) join_stretches(const __grid_con
   }
 }
 
-// Threads of a token's block.  16 tokens x 50257 x 768 with 8 alternatives take 23 us so; 27 with 256 threads, 26 with
-// 1024.
+// Threads of a token's block.  16 tokens x 50257 x 768 with 8 alternatives take 23 to 25 us so (in a graph, the same
+// table call after call; 24 with another table each call); 4 us more with 256 threads, 3 with 1024.
 constexpr int kGroupThreads = 512;
 
 // The same of kFew's groups of 32 rows, which are many: a block a token.
@@ -337,9 +337,21 @@ struct Space {
   int64_t sums, best, logits, target_logit, total;
 };
 
-Space space_of(int64_t tokens, int64_t vocab, int top) {
+// Up to so many tokens the operands change places: as for the loss without
+// alternatives, further with them, since with tokens as rows the lists of a few
+// rows fill slowly, in few pairs' epilogues.  Exchanged and with tokens as rows,
+// us, 8 and 16 alternatives (bf16, in a graph):
+//            50257 x 768          50257 x 1600         32000 x 2048         8000 x 256
+//   16       25  27    45   84    41  45    58   94    37  40    51   89    14  16    25  41
+//   96       35  38    45  109    48  51    53  119    42  45    51  115    19  21    26  41
+//   128      37  41    45  110    51  54    55  121    43  47    51  118    19  21    27  41
+// Beyond, the logits that the exchanged form keeps, 4 V bytes a token, would take
+// the workspace of a large batch past its few MB.
+int64_t few_tokens(int top) { return top > 0 ? 128 : kFewTokens; }
+
+Space space_of(int64_t tokens, int64_t vocab, int top, bool few) {
   Space s;
-  s.few = tokens <= kFewTokens;
+  s.few = few;
   s.bn = s.few ? static_cast<int>(round_up(std::max<int64_t>(tokens, 1), 32)) : kTileN;
   s.m_tiles = static_cast<int>(ceil_div(s.few ? vocab : tokens, kTileM));
   s.n_tiles = static_cast<int>(ceil_div(s.few ? tokens : vocab, s.bn));
@@ -351,6 +363,10 @@ Space space_of(int64_t tokens, int64_t vocab, int top) {
   s.target_logit = s.logits + (s.few && top > 0 ? tokens * s.m_tiles * kTileM * 4 : 0);
   s.total = s.target_logit + round_up(tokens * 4, 256);
   return s;
+}
+
+Space space_of(int64_t tokens, int64_t vocab, int top) {
+  return space_of(tokens, vocab, top, tokens <= few_tokens(top));
 }
 
 int check_top(int top, int64_t vocab) {
@@ -381,9 +397,9 @@ extern "C" int64_t zero_lm_logprobs_workspace_bytes(int64_t tokens, int64_t voca
                                                     int with_grad) {
   int rc = check_sizes(tokens, vocab, width);
   if (rc || (rc = check_top(top, vocab))) return rc;
-  // any smaller count of tokens has to fit too: the few tokens' form needs more for each
-  int64_t bytes = std::max(space_of(std::min(tokens, kSlab), vocab, top).total,
-                           space_of(std::min(tokens, kFewTokens), vocab, top).total);
+  // any smaller count of tokens and of alternatives has to fit too: the few tokens' form needs more for each token
+  int64_t bytes = space_of(std::min(tokens, few_tokens(top)), vocab, top, true).total;
+  if (tokens > kFewTokens) bytes = std::max(bytes, space_of(std::min(tokens, kSlab), vocab, top, false).total);
   if (with_grad) bytes = std::max(bytes, grad_bytes(tokens, vocab, width, 3));
   return bytes;
 }
