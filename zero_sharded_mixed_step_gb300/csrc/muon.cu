@@ -28,8 +28,9 @@
 // counter for each matrix says.  What a tile waits for has a lower number, so
 // some running pair has it or has done it, and no wait can last for ever.  With
 // several matrices a pair finds tiles that are ready; one product's tail runs
-// beside the next one's start (as 15 launches, 24 matrices of 768 x 768 took 490
-// us: the products' own time is about 226).
+// beside the next one's start (with two steps in two parts, whose products' own
+// time is about 226 us, 24 matrices of 768 x 768 took 490 us as 15 launches and
+// take 368).
 // Precision.  A singular value far below 1 grows by `a` (3.4) a step, and with
 // it the noise that rounding X, A and P to 16 bits leaves in its direction:
 // with fp16 operands throughout, a matrix whose largest singular values stand
@@ -1001,8 +1002,8 @@ struct Group {
   int64_t first;               // of its entries
   int64_t ldx, lda;
   int64_t at[kBuffers];        // byte offsets of the buffers: high parts, then low parts
-  // See kMultiply; T is theirs alone.  By twos and one by one, us: eight of 1024 x 1536 349 and 346, of 1024 x 2048 374
-  // and 397, of 1024 x 4096 510 and 649; one of them 217 and 203, 224 and 215, 257 and 280.
+  // See kMultiply; T is theirs alone.  By twos and one by one, us (bf16): eight of 1024 x 1536 453 and 454, of 1024 x
+  // 2048 494 and 547, of 1024 x 4096 715 and 999; one of them 241 and 226, 249 and 240, 294 and 330.
   bool joined() const { return n >= 2 * m; }
   int64_t x_part() const { return static_cast<int64_t>(members.size()) * m * ldx; }
   int64_t a_part() const { return static_cast<int64_t>(members.size()) * m * lda; }

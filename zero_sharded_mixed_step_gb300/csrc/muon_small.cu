@@ -47,8 +47,8 @@ using host::round_up;
 // Bounded device-side waits of ns_small that gave up, over all calls; never set back (see zero_lm_status).
 __device__ unsigned int g_small_timeouts;
 
-// Four warps for each quarter of the TMEM lanes, 16 columns in turn (eight matrices of 128 x 256 take 49.6 us; with
-// two warps of 32 columns 55.7).
+// Four warps for each quarter of the TMEM lanes, 16 columns in turn (with two steps of five in two parts eight matrices
+// of 128 x 256 take 49.6 us, with two warps of 32 columns 55.7; by default, with four, 53).
 constexpr int kThreads = 512, kCols = 16;
 constexpr int kMostRows = 128, kMostSlice = 256, kMostCtas = 8;
 
