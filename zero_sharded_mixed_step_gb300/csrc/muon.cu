@@ -829,7 +829,8 @@ __global__ void __launch_bounds__(kPassThreads) sum_squares(const __grid_constan
       const int tile = static_cast<int>(t - tile0), ty = tile / across;
       const int col = (tile - ty * across) * kPassCols + static_cast<int>(threadIdx.x & 31) * 8;
       const int n = e.cols - col;
-      Squares squares;
+      Squares squares;          // of a step's direction
+      float held = 0.f;         // of an input
       const int first_row = ty * kPassRows + static_cast<int>(threadIdx.x >> 5);
       if (MUON && WC > 0 && e.wide) {
         // two rows' loads at a time, before the first store
@@ -866,18 +867,32 @@ __global__ void __launch_bounds__(kPassThreads) sum_squares(const __grid_constan
             squares.add(u, 8);
           }
         }
-        all += squares.total();
-        continue;
-      }
+      } else {
 #pragma unroll
-      for (int r = 0; r < kPassRows / 8; ++r) {
-        const int row = first_row + r * 8;
-        if (row >= e.rows || n <= 0) continue;
-        float u[8], m[8];
-        direction8<T, MUON>(p, e, which, row, col, n, true, u, m);
-        squares.add(u, n);
+        for (int r = 0; r < kPassRows / 8; ++r) {
+          const int row = first_row + r * 8;
+          if (row >= e.rows || n <= 0) continue;
+          float u[8], m[8];
+          direction8<T, MUON>(p, e, which, row, col, n, true, u, m);
+          if (MUON) {
+            squares.add(u, n);
+            continue;
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < n) held = fmaf(u[k], u[k], held);
+        }
+        if (!MUON && !std::is_same<T, __half>::value && !squares_held(held)) {
+          held = 0.f;
+#pragma unroll 1
+          for (int row = first_row; row < min(e.rows, first_row + kPassRows) && n > 0; row += 8) {
+            float u[8], m[8];
+            direction8<T, MUON>(p, e, which, row, col, n, true, u, m);
+            squares.add(u, n);
+          }
+        }
       }
-      all += squares.total();
+      all += MUON || held == 0.f ? squares.total() : held;
     }
     all = block_sum(all);
     if (threadIdx.x == 0) p.part[blockIdx.x + which] = all;

@@ -191,15 +191,30 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small(const __grid_constant__ 
       count = c0 + nl - col;
     }
   };
-  Squares mine;
+  float mine = 0.f;
   for (int i = threadIdx.x; i < items; i += kThreads) {
     int row, col, count;
     item(i, row, col, count);
     float u[8], mom[8];
     direction8<T, MUON>(p, e, which, row, col, count, true, u, mom);
-    mine.add(u, count);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < count) mine = fmaf(u[k], u[k], mine);
   }
-  double all = block_sum<kThreads>(mine.total());
+  double all = mine;
+  if (!squares_held(mine)) {
+    Squares again;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < items; i += kThreads) {
+      int row, col, count;
+      item(i, row, col, count);
+      float u[8], mom[8];
+      direction8<T, MUON>(p, e, which, row, col, count, true, u, mom);
+      again.add(u, count);
+    }
+    all = again.total();
+  }
+  all = block_sum<kThreads>(all);
   if (ctas > 1) {
     if (threadIdx.x == 0) squares_here = all;
     meet_cluster();
