@@ -948,7 +948,8 @@ int64_t zero_muon_workspace_bytes(int W, int64_t n_matrices, const int64_t* rows
  *              multiple of 8.  No two buffers may overlap.
  *   lr, weight_decay, scales  lr and lr * scales[i] finite in fp32; scales NULL: 1.
  *   mu         0 <= mu < 1.
- *   steps, coefficients, fine_steps, workspace  as for zero_orthogonalize.
+ *   steps, coefficients, fine_steps, workspace  as for zero_orthogonalize; a
+ *              fine_steps of -1 chooses all.
  * A matrix whose U holds a value that is not finite (an overflow in fp16 gradients)
  * keeps its master, momentum and p16 as they were; one of norm 0 decays alone.
  * The caller keeps the step counter, if any.  A device wait that gave up

@@ -1340,8 +1340,9 @@ class MuonStep(_Matrices):
     ``momentum`` (fp32) and ``p16`` are flat vectors, matrix after matrix, each
     starting on a boundary of 8 values (``views`` cuts them up); ``theta0``, a
     list of matrices, seeds the master and the 16-bit copy.  ``scales``
-    multiplies the learning rate of each matrix (None: 1).  What a ZeRO step
-    trains beside them (embeddings, vectors) has a :class:`ZeroStep` of its own.
+    multiplies the learning rate of each matrix (None: 1); ``fine_steps`` is as
+    for :class:`Orthogonalize` (None: all).  What a ZeRO step trains beside them
+    (embeddings, vectors) has a :class:`ZeroStep` of its own.
     ``alloc`` as for :class:`ZeroStep`; workspace and stream as for
     :class:`LmLoss`."""
 
